@@ -321,7 +321,9 @@ def _plain_fork(s):
     who = part.nonzero()[:, 0]
     new = _claim(refs, who.shape[0])
     last = table[src[who], full[who].long()].long()
-    s["k_pages"][:, new], s["v_pages"][:, new] = s["k_pages"][:, last], s["v_pages"][:, last]
+    w, r = (torch.arange(ps, device="cuda") < (lens[src] % ps)[who][:, None]).nonzero(as_tuple=True)
+    s["k_pages"][:, new[w], r] = s["k_pages"][:, last[w], r]
+    s["v_pages"][:, new[w], r] = s["v_pages"][:, last[w], r]
     rows[who, full[who].long()] = new.to(rows.dtype)
     refs[new] = 1
     table[dst], lens[dst] = rows, lens[src]
