@@ -73,6 +73,11 @@ typedef enum { SC_F32 = 0, SC_BF16 = 1 } sc_dtype;
 #define SC_DEV_BAD_ACCEPTED 0x4u  /* an accepted length outside [0, D]: that sequence skipped */
 #define SC_DEV_TIMEOUT 0x8u       /* a bounded wait on an asynchronous copy gave up: output incomplete */
 #define SC_DEV_NO_SLOT 0x10u      /* a claim asked for more slots than were free: nothing claimed */
+#define SC_DEV_NO_PAGE 0x40u      /* a call needed more cache pages than were free: nothing changed */
+#define SC_DEV_BAD_PAGE 0x80u     /* a page table entry in use outside [0, n_pages) */
+#define SC_DEV_BAD_LENGTH 0x100u  /* a sequence length outside [0, max_pages * page_size] */
+#define SC_DEV_BAD_TOKEN 0x200u   /* a drafted token outside [0, V): that sequence accepts nothing */
+#define SC_DEV_BAD_PROBS 0x400u   /* no token has any probability: that sequence's next token is -1 */
 #define SC_DEV_OUT_OF_BOUNDS 0x20u /* bounds-checked build only: an access outside the call's
                                       buffers was refused (see shortconv_bounds_checked) */
 
@@ -423,6 +428,154 @@ sc_status shortconv_slots_release(uint32_t *in_use, int n_slots, const int32_t *
 sc_status shortconv_pool_copy(sc_dtype dtype, int H, int K, void *pool, int n_slots,
                               const int32_t *src_slots, const int32_t *dst_slots, int n,
                               void *stream);
+
+/*
+ * Speculative serving around the conv: a paged key/value cache for the hybrid
+ * decoder's attention layers, the attention of a decode or verify step over
+ * it, and the verification of the drafts, whose accepted lengths
+ * shortconv_rollback(_layers) and shortconv_pages_resize take.
+ *
+ * The cache. k_pages and v_pages are pools of n_pages pages of page_size
+ * tokens (a power of two, 8 to 256); a token's row in a page is
+ * token_bytes = Hkv * Dh * element size bytes (a multiple of 16). Token t of
+ * the sequence in slot s (the slot of its conv state) is row t % page_size
+ * of page table[s][t / page_size].
+ *   refs   device int32 [n_pages]            table entries naming the page; 0: free
+ *   table  device int32 [n_slots, max_pages] -1 past the sequence's last page
+ *   lens   device int32 [n_slots]            tokens of the sequence
+ * An empty cache is refs = 0, table = -1, lens = 0. Several sequences may
+ * share a full page; a partly filled last page belongs to one. A model's L
+ * attention layers share the table: their pools are stacked,
+ * [L, n_pages, page_size, Hkv, Dh]; L = 0 (pools NULL) changes the tables
+ * alone. Calls on one cache must be ordered (one stream). Slots listed in a
+ * call must be distinct; a bad slot, length or table entry sets
+ * SC_DEV_BAD_SLOT, SC_DEV_BAD_LENGTH or SC_DEV_BAD_PAGE and skips that
+ * sequence (a bad entry alone, where only it is wrong). Claims take the lowest
+ * free pages, in listed order: results depend on the inputs alone.
+ * n_slots * max_pages, max_pages * page_size and n_pages * page_size stay
+ * below 2^31.
+ *
+ * shortconv_pages_resize: give slot_ids[i] the length new_lens[i]. A shorter
+ * one releases the pages past its end (0 frees the sequence; a rollback of
+ * rejected drafts is a resize to the accepted length); if it ends inside a page
+ * that another sequence shares, the sequence gets a copy of that page's
+ * rows. A longer one claims pages; their contents are whatever they were.
+ * All or nothing: with too few free pages (those released by the call count)
+ * SC_DEV_NO_PAGE is set and no table changes.
+ *
+ * shortconv_pages_fork: dst_slots[i] becomes a branch of src_slots[i]: it
+ * releases its own pages, shares the source's full pages and gets a copy of the
+ * rows of a partly filled last page. A slot that is a destination is no pair's
+ * source (not checked beyond the pair itself). All or nothing, as above.
+ *
+ * shortconv_pages_compact: move the used pages to the front of the pools.
+ * With U pages used, the i-th used page at or past U moves to the i-th free
+ * page before U, table and refs follow, and *n_used (device int32) is U.
+ *
+ * shortconv_pages_append: write the D new tokens of each listed sequence,
+ * already counted in lens: row i*D + j of k and v goes to position
+ * lens - D + j. k_stride and v_stride are bytes between rows (16-byte
+ * multiples, at least token_bytes). One layer's pools.
+ *
+ * workspace: shortconv_pages_workspace_bytes(n_pages, n) bytes, 16-byte
+ * aligned, with n the listed sequences (0 for a compaction; 0 is returned for
+ * invalid sizes), contents ignored on entry.
+ */
+size_t shortconv_pages_workspace_bytes(int n_pages, int n);
+sc_status shortconv_pages_resize(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                                 int n_slots, int max_pages, int page_size,
+                                 const int32_t *slot_ids, const int32_t *new_lens, int n, int L,
+                                 int64_t token_bytes, void *k_pages, void *v_pages,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+sc_status shortconv_pages_fork(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                               int n_slots, int max_pages, int page_size,
+                               const int32_t *src_slots, const int32_t *dst_slots, int n, int L,
+                               int64_t token_bytes, void *k_pages, void *v_pages, void *workspace,
+                               size_t workspace_bytes, void *stream);
+sc_status shortconv_pages_compact(int32_t *refs, int n_pages, int32_t *table, const int32_t *lens,
+                                  int n_slots, int max_pages, int page_size, int L,
+                                  int64_t token_bytes, void *k_pages, void *v_pages,
+                                  int32_t *n_used, void *workspace, size_t workspace_bytes,
+                                  void *stream);
+sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                 int N, int D, int64_t token_bytes, void *k_pages, void *v_pages,
+                                 int n_pages, int page_size, const int32_t *table,
+                                 const int32_t *lens, int n_slots, int max_pages,
+                                 const int32_t *slot_ids, void *stream);
+
+/*
+ * shortconv_prefix_attention: the attention of one decode (D = 1) or verify
+ * (D drafts) step over the paged cache, bf16. Row i*D + j of q is new token j
+ * of the sequence in slot slot_ids[i], at position p = lens - D + j; its keys
+ * are the sequence's tokens 0 .. p (the new ones already appended). Query
+ * head hq reads kv head hq / (Hq / Hkv):
+ *   out = sum_t exp(scale q.k_t) v_t / sum_t exp(scale q.k_t).
+ * A row without keys (p < 0) is zeros. Scores, maxima and sums are held in
+ * fp32, the weights enter the second product in bf16, out is rounded once.
+ * Nothing past lens is looked at: it may hold NaN.
+ *
+ * shared_pages: the caller's word that the first shared_pages table entries
+ * of all listed sequences are equal (branches forked from one prompt); that
+ * part of every row's keys is then read once for the whole batch. 0 is
+ * always right. Every listed sequence must hold at least one entry it shares;
+ * a row that ends inside the shared part sees its own keys alone.
+ *
+ *   Hq, Hkv, Dh   Hq a multiple of Hkv, Hq / Hkv <= 128; Dh 64 or 128
+ *   q             device [N*D, Hq, Dh] bf16, q_stride elements between rows
+ *                 (a multiple of 8, at least Hq * Dh)            read
+ *   k_pages, v_pages  device [n_pages, page_size, Hkv, Dh] bf16  read
+ *   scale         > 0
+ *   out           device [N*D, Hq, Dh] bf16, contiguous          written
+ *   workspace     shortconv_prefix_attention_workspace_bytes(...), 16-byte
+ *                 aligned; 0 is returned for invalid sizes
+ * Device errors: SC_DEV_BAD_SLOT, SC_DEV_BAD_LENGTH, SC_DEV_BAD_PAGE (that
+ * sequence's rows of out, or those of the kv heads that met the page, are not
+ * written), SC_DEV_TIMEOUT.
+ */
+size_t shortconv_prefix_attention_workspace_bytes(int Hq, int Hkv, int Dh, int N, int D,
+                                                  int shared_pages);
+sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, const void *q,
+                                     int64_t q_stride, int N, int D, const void *k_pages,
+                                     const void *v_pages, int n_pages, int page_size,
+                                     const int32_t *table, const int32_t *lens, int n_slots,
+                                     int max_pages, const int32_t *slot_ids, int shared_pages,
+                                     float scale, void *out, void *workspace,
+                                     size_t workspace_bytes, void *stream);
+
+/*
+ * shortconv_draft_accept: verification of drafted tokens against the target's
+ * probabilities, from given random numbers (SGLang PR #31041: the accepted
+ * length that the rollback of section "实现拆解 2" takes). Sequence i
+ * drafted n tokens x_j (n = n_drafts[i], or D when n_drafts is NULL) from
+ * draft distributions q_j; p_j is the target's distribution after j of them.
+ * Draft j is accepted while u_j q_j(x_j) < p_j(x_j), in order;
+ * accepted[i] = a is how many were. The next token is drawn with u_D: from
+ * max(p_a - q_a, 0) if a draft was rejected (from p_a if nothing of it is
+ * left), from p_n otherwise: the lowest token whose inclusive cumulative
+ * weight exceeds floor(W trunc(2^31 u_D) / 2^31), W the sum of all weights. A
+ * probability's weight is trunc(2^40 min(max(p, 0), 1)) (NaN: 0): whole
+ * numbers, so the token does not depend on an order of summation.
+ *
+ *   dtype       of target and draft, SC_F32 or SC_BF16
+ *   target      device [N, D+1, V], rows target_stride elements apart   read
+ *   draft       device [N, D, V], rows draft_stride apart, or NULL: the
+ *               drafts were certain (q_j(x_j) = 1)                      read
+ *   tokens      device int32 [N, D]                                     read
+ *   n_drafts    device int32 [N] or NULL                                read
+ *   uniforms    device fp32 [N, D+1] in [0, 1)                          read
+ *   accepted    device int32 [N]                                        written
+ *   out_tokens  device int32 [N, D+1]: the a accepted drafts, the next
+ *               token, then -1                                          written
+ * 1 <= V <= 2^22, D >= 0 (D = 0 samples one token). Rows need the alignment
+ * of their elements only. Device errors: SC_DEV_BAD_ACCEPTED (n_drafts
+ * outside [0, D]) and SC_DEV_BAD_TOKEN: accepted 0, out_tokens -1;
+ * SC_DEV_BAD_PROBS.
+ */
+sc_status shortconv_draft_accept(sc_dtype dtype, int V, int N, int D, const void *target,
+                                 int64_t target_stride, const void *draft, int64_t draft_stride,
+                                 const int32_t *tokens, const int32_t *n_drafts,
+                                 const float *uniforms, int32_t *accepted, int32_t *out_tokens,
+                                 void *stream);
 
 /*
  * shortconv_check_wait_limit: a health check of the device-side timeout path,

@@ -31,6 +31,9 @@ SC_OK, SC_EINVAL, SC_EUNSUPPORTED, SC_ECUDA, SC_EDEVICE = 0, 1, 2, 3, 4
 SC_F32, SC_BF16 = 0, 1
 DEV_BAD_SLOT, DEV_BAD_SEQLENS, DEV_BAD_ACCEPTED, DEV_TIMEOUT, DEV_NO_SLOT = 0x1, 0x2, 0x4, 0x8, 0x10
 
+DEV_NO_PAGE, DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_BAD_TOKEN, DEV_BAD_PROBS = (
+    0x40, 0x80, 0x100, 0x200, 0x400)
+
 _lock = threading.Lock()
 _lib = None
 
@@ -79,6 +82,23 @@ def lib() -> ctypes.CDLL:
             L.shortconv_slots_claim.argtypes = [p, i32, i32, p, i32, i32, i32, p, p]
             L.shortconv_slots_release.argtypes = [p, i32, p, i32, p]
             L.shortconv_pool_copy.argtypes = [i32, i32, i32, p, i32, p, p, i32, p]
+            sz = ctypes.c_size_t
+            L.shortconv_pages_workspace_bytes.argtypes = [i32, i32]
+            L.shortconv_pages_workspace_bytes.restype = sz
+            L.shortconv_pages_resize.argtypes = [p, i32, p, p, i32, i32, i32, p, p, i32, i32, i64,
+                                                 p, p, p, sz, p]
+            L.shortconv_pages_fork.argtypes = L.shortconv_pages_resize.argtypes
+            L.shortconv_pages_compact.argtypes = [p, i32, p, p, i32, i32, i32, i32, i64, p, p, p,
+                                                  p, sz, p]
+            L.shortconv_pages_append.argtypes = [p, i64, p, i64, i32, i32, i64, p, p, i32, i32, p,
+                                                 p, i32, i32, p, p]
+            L.shortconv_prefix_attention_workspace_bytes.argtypes = [i32] * 6
+            L.shortconv_prefix_attention_workspace_bytes.restype = sz
+            L.shortconv_prefix_attention.argtypes = [i32, i32, i32, i32, p, i64, i32, i32, p, p,
+                                                     i32, i32, p, p, i32, i32, p, i32,
+                                                     ctypes.c_float, p, p, sz, p]
+            L.shortconv_draft_accept.argtypes = [i32, i32, i32, i32, p, i64, p, i64, p, p, p, p, p,
+                                                 p]
             L.shortconv_get_error.argtypes = [p, ctypes.POINTER(ctypes.c_int)]
             L.shortconv_check_wait_limit.argtypes = [p]
             L.shortconv_bounds_checked.argtypes = []
@@ -91,7 +111,9 @@ def lib() -> ctypes.CDLL:
                       "rollback_layers", "backward",
                       "backward_varlen", "in_proj_prefill", "in_proj_decode", "out_proj",
                       "slots_claim",
-                      "slots_release", "pool_copy", "get_error", "check_wait_limit",
+                      "slots_release", "pool_copy", "pages_resize", "pages_fork",
+                      "pages_compact", "pages_append", "prefix_attention", "draft_accept",
+                      "get_error", "check_wait_limit",
                       "bounds_trim_next", "bounds_take_first_bad"):
                 getattr(L, "shortconv_" + f).restype = i32
             _lib = L
@@ -395,6 +417,190 @@ def pool_copy(pool, src_slots, dst_slots, stream=None):
         _dcode(pool), H, K, _dev(pool, "pool", pool.dtype, (n_slots, H, K)), n_slots,
         _dev(src_slots, "src_slots", torch.int32, (n,)),
         _dev(dst_slots, "dst_slots", torch.int32, (n,)), n, _stream(stream, pool.device)))
+
+
+def _rows(t, name, dtype, shape):
+    """Data pointer and row stride (elements) of a CUDA tensor whose rows (the
+    dims after the first) are contiguous and may lie further apart."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    width = 1
+    for d in range(t.dim() - 1, 0, -1):
+        if t.shape[d] != 1 and t.stride(d) != width:
+            raise ValueError(f"{name} must have contiguous rows")
+        width *= t.shape[d]
+    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else width)
+
+
+def _cache(refs, table, lens):
+    n_slots, max_pages = table.shape
+    return (_dev(refs, "refs", torch.int32, (refs.shape[0],)), refs.shape[0],
+            _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (n_slots,)),
+            n_slots, max_pages)
+
+
+def _pools(k_pages, v_pages, n_pages):
+    """(page_size, L, token_bytes, k, v) of [L, n_pages, page_size, Hkv, Dh] or
+    [n_pages, page_size, Hkv, Dh] pools."""
+    shape = tuple(k_pages.shape) if k_pages.dim() == 5 else (1,) + tuple(k_pages.shape)
+    if len(shape) != 5 or shape[1] != n_pages:
+        raise ValueError("k_pages must be [L, n_pages, page_size, Hkv, Dh] or "
+                         "[n_pages, page_size, Hkv, Dh]")
+    _dcode(k_pages)
+    return (shape[2], shape[0], shape[3] * shape[4] * k_pages.element_size(),
+            _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype, k_pages.shape))
+
+
+def _workspace(workspace, need, device):
+    if workspace is None:
+        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or workspace.numel() < need:
+        raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes")
+    return workspace
+
+
+def page_cache(n_slots: int, max_pages: int, n_pages: int, device="cuda"):
+    """``(refs [n_pages], table [n_slots, max_pages], lens [n_slots])`` of an empty cache."""
+    i32 = dict(dtype=torch.int32, device=device)
+    return (torch.zeros((n_pages,), **i32), torch.full((n_slots, max_pages), -1, **i32),
+            torch.zeros((n_slots,), **i32))
+
+
+def pages_workspace_bytes(n_pages: int, n: int) -> int:
+    return int(lib().shortconv_pages_workspace_bytes(n_pages, n))
+
+
+def pages_resize(refs, table, lens, slot_ids, new_lens, k_pages, v_pages, workspace=None,
+                 stream=None):
+    """Give each listed sequence a new length: claims, truncates (a rollback) or frees
+    (0) its pages; in place on ``refs``, ``table``, ``lens`` and, where a shared page
+    has to be copied, on the pools."""
+    n = slot_ids.shape[0]
+    ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
+    ws = _workspace(workspace, pages_workspace_bytes(refs.shape[0], n), refs.device)
+    _raise_on("shortconv_pages_resize", lib().shortconv_pages_resize(
+        *_cache(refs, table, lens), ps, _dev(slot_ids, "slot_ids", torch.int32, (n,)),
+        _dev(new_lens, "new_lens", torch.int32, (n,)), n, L, token_bytes, kp, vp,
+        _dev(ws, "workspace"), ws.numel(), _stream(stream, refs.device)))
+
+
+def pages_fork(refs, table, lens, src_slots, dst_slots, k_pages, v_pages, workspace=None,
+               stream=None):
+    """``dst_slots[i]`` becomes a branch of ``src_slots[i]``: full pages shared, a partly
+    filled last page copied. In place."""
+    n = src_slots.shape[0]
+    ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
+    ws = _workspace(workspace, pages_workspace_bytes(refs.shape[0], n), refs.device)
+    _raise_on("shortconv_pages_fork", lib().shortconv_pages_fork(
+        *_cache(refs, table, lens), ps, _dev(src_slots, "src_slots", torch.int32, (n,)),
+        _dev(dst_slots, "dst_slots", torch.int32, (n,)), n, L, token_bytes, kp, vp,
+        _dev(ws, "workspace"), ws.numel(), _stream(stream, refs.device)))
+
+
+def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=None, stream=None):
+    """Move the used pages to the front of the pools (in place); returns the int32
+    ``n_used [1]``: no page at or past it is in use."""
+    ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
+    if n_used is None:
+        n_used = torch.empty((1,), dtype=torch.int32, device=refs.device)
+    ws = _workspace(workspace, pages_workspace_bytes(refs.shape[0], 0), refs.device)
+    _raise_on("shortconv_pages_compact", lib().shortconv_pages_compact(
+        *_cache(refs, table, lens), ps, L, token_bytes, kp, vp,
+        _dev(n_used, "n_used", torch.int32, (1,)), _dev(ws, "workspace"), ws.numel(),
+        _stream(stream, refs.device)))
+    return n_used
+
+
+def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None):
+    """Write each listed sequence's ``D`` newest tokens, already counted in ``lens``:
+    ``k``, ``v`` ``[N*D, Hkv, Dh]`` (rows may be strided) into one layer's pools."""
+    N = slot_ids.shape[0]
+    n_pages, ps, Hkv, Dh = k_pages.shape
+    dt = k_pages.dtype
+    _dcode(k_pages)
+    es = k_pages.element_size()
+    k_p, k_s = _rows(k, "k", dt, (N * D, Hkv, Dh))
+    v_p, v_s = _rows(v, "v", dt, (N * D, Hkv, Dh))
+    _raise_on("shortconv_pages_append", lib().shortconv_pages_append(
+        k_p, k_s * es, v_p, v_s * es, N, D, Hkv * Dh * es, _dev(k_pages, "k_pages"),
+        _dev(v_pages, "v_pages", dt, k_pages.shape), n_pages, ps,
+        _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (table.shape[0],)),
+        table.shape[0], table.shape[1], _dev(slot_ids, "slot_ids", torch.int32, (N,)),
+        _stream(stream, k_pages.device)))
+
+
+def prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages=0) -> int:
+    return int(lib().shortconv_prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages))
+
+
+def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages=0, scale=None,
+                     out=None, workspace=None, stream=None):
+    """Attention of a decode (``D`` = 1) or verify step over the paged cache (bf16):
+    row ``i*D + j`` of ``q [N*D, Hq, Dh]`` (rows may be strided) is new token j of the
+    sequence in ``slot_ids[i]``. The first ``shared_pages`` pages are the same for all
+    listed sequences and read once. Returns ``out [N*D, Hq, Dh]``."""
+    N = slot_ids.shape[0]
+    n_pages, ps, Hkv, Dh = k_pages.shape
+    Hq = q.shape[1]
+    dt = torch.bfloat16
+    if scale is None:
+        scale = Dh ** -0.5
+    if out is None:
+        out = torch.empty((N * D, Hq, Dh), dtype=dt, device=q.device)
+    q_p, q_s = _rows(q, "q", dt, (N * D, Hq, Dh))
+    ws = _workspace(workspace, prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages),
+                    q.device)
+    _raise_on("shortconv_prefix_attention", lib().shortconv_prefix_attention(
+        _dcode(q), Hq, Hkv, Dh, q_p, q_s, N, D, _dev(k_pages, "k_pages", dt),
+        _dev(v_pages, "v_pages", dt, k_pages.shape), n_pages, ps,
+        _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (table.shape[0],)),
+        table.shape[0], table.shape[1], _dev(slot_ids, "slot_ids", torch.int32, (N,)),
+        shared_pages, scale, _dev(out, "out", dt, (N * D, Hq, Dh)), _dev(ws, "workspace"),
+        ws.numel(), _stream(stream, q.device)))
+    return out
+
+
+def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, out_tokens=None,
+                 stream=None):
+    """Verify drafts against the target: ``target [N, D+1, V]`` and ``draft [N, D, V]``
+    (None: certain drafts) are probabilities (float32 or bfloat16; a last dim sliced
+    from wider rows is fine), ``tokens [N, D]`` int32, ``uniforms [N, D+1]`` float32,
+    ``n_drafts [N]`` int32 or None. Returns int32 ``(accepted [N], out_tokens [N, D+1])``:
+    the accepted drafts, the next token, then -1."""
+    N, D1, V = target.shape
+    D = D1 - 1
+    dt = target.dtype
+
+    def rows(t, name, n):  # [N, n, V] with every row the same distance apart
+        if t.dim() == 3 and n > 1 and N > 1 and t.stride(0) != n * t.stride(1):
+            raise ValueError(f"{name} must have evenly spaced rows")
+        if t.dim() != 3 or tuple(t.shape) != (N, n, V):
+            raise ValueError(f"{name} must have shape {(N, n, V)}, got {tuple(t.shape)}")
+        step = t.stride(1) if n > 1 else t.stride(0)
+        flat = t.as_strided((N * n, V), (step, t.stride(2)))
+        return _rows(flat, name, dt, (N * n, V))
+
+    code = _dcode(target)
+    t_p, t_s = rows(target, "target", D + 1)
+    d_p, d_s = (None, V) if draft is None else rows(draft, "draft", D)
+    if accepted is None:
+        accepted = torch.empty((N,), dtype=torch.int32, device=target.device)
+    if out_tokens is None:
+        out_tokens = torch.empty((N, D + 1), dtype=torch.int32, device=target.device)
+    _raise_on("shortconv_draft_accept", lib().shortconv_draft_accept(
+        code, V, N, D, t_p, t_s, d_p, d_s, _dev(tokens, "tokens", torch.int32, (N, D)),
+        None if n_drafts is None else _dev(n_drafts, "n_drafts", torch.int32, (N,)),
+        _dev(uniforms, "uniforms", torch.float32, (N, D + 1)),
+        _dev(accepted, "accepted", torch.int32, (N,)),
+        _dev(out_tokens, "out_tokens", torch.int32, (N, D + 1)),
+        _stream(stream, target.device)))
+    return accepted, out_tokens
 
 
 def check_wait_limit(stream=None, device=None) -> None:

@@ -139,6 +139,53 @@ sc_status prefill_impl(sc_dtype dtype, int H, int K, const void *bcx, int64_t T,
                                         (cudaStream_t)stream));
 }
 
+
+// The sizes of a page table; token_bytes and L only where pools are given.
+sc_status check_pages(int n_pages, int n_slots, int max_pages, int page_size) {
+    if (n_pages <= 0 || n_slots <= 0 || max_pages <= 0 || page_size <= 0) return SC_EINVAL;
+    if (page_size < 8 || page_size > 256 || (page_size & (page_size - 1)) != 0)
+        return SC_EUNSUPPORTED;
+    if ((int64_t)n_slots * max_pages > INT32_MAX || (int64_t)max_pages * page_size > INT32_MAX ||
+        (int64_t)n_pages * page_size > INT32_MAX)
+        return SC_EUNSUPPORTED;
+    return SC_OK;
+}
+
+struct Buf {
+    const void *p;
+    size_t bytes;
+};
+
+// No output overlaps an input or another output.
+bool disjoint(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+    for (const Buf *o = outs.begin(); o != outs.end(); ++o) {
+        for (const Buf &i : ins)
+            if (overlaps(o->p, o->bytes, i.p, i.bytes)) return false;
+        for (const Buf *q = o + 1; q != outs.end(); ++q)
+            if (overlaps(o->p, o->bytes, q->p, q->bytes)) return false;
+    }
+    return true;
+}
+
+// Arguments that pages_resize, _fork and _compact share; *pool_bytes of one pool.
+sc_status check_page_call(const void *refs, int n_pages, const void *table, const void *lens,
+                          int n_slots, int max_pages, int page_size, int L, int64_t token_bytes,
+                          const void *k, const void *v, const void *ws, size_t ws_bytes,
+                          size_t need, size_t *pool_bytes) {
+    const sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    if (st != SC_OK) return st;
+    if (L < 0 || (L > 0 && token_bytes <= 0)) return SC_EINVAL;
+    if (L > 0 && (token_bytes % 16 != 0 || token_bytes > (1 << 24) || L > (1 << 16)))
+        return SC_EUNSUPPORTED;
+    *pool_bytes = L > 0 ? (size_t)L * n_pages * page_size * token_bytes : 0;
+    if (ws_bytes < need) return SC_EINVAL;
+    if (!ptr_ok(refs, (size_t)n_pages * 4, 4) || !ptr_ok(table, (size_t)n_slots * max_pages * 4, 4) ||
+        !ptr_ok(lens, (size_t)n_slots * 4, 4) || !ptr_ok(k, *pool_bytes, 16) ||
+        !ptr_ok(v, *pool_bytes, 16) || !ptr_ok(ws, need, 16))
+        return SC_EINVAL;
+    return SC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -500,6 +547,220 @@ sc_status shortconv_pool_copy(sc_dtype dtype, int H, int K, void *pool, int n_sl
                       RO(dst_slots, (size_t)n * 4));
     return from_cuda(sc::launch_pool_copy(src_slots, dst_slots, n, state_bytes, pool, n_slots,
                                           (cudaStream_t)stream));
+}
+
+size_t shortconv_pages_workspace_bytes(int n_pages, int n) {
+    if (n_pages <= 0 || n < 0) return 0;
+    return sc::pages_workspace_bytes(n_pages, n);
+}
+
+sc_status shortconv_pages_resize(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                                 int n_slots, int max_pages, int page_size,
+                                 const int32_t *slot_ids, const int32_t *new_lens, int n, int L,
+                                 int64_t token_bytes, void *k_pages, void *v_pages,
+                                 void *workspace, size_t workspace_bytes, void *stream) {
+    if (n < 0 || n > n_slots) return SC_EINVAL;
+    const size_t need = shortconv_pages_workspace_bytes(n_pages, n);
+    size_t n_pool = 0;
+    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
+                                         L, token_bytes, k_pages, v_pages, workspace,
+                                         workspace_bytes, need, &n_pool);
+    if (st != SC_OK) return st;
+    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
+    const size_t n_l = (size_t)n_slots * 4, n_i = (size_t)n * 4;
+    if (!ptr_ok(slot_ids, n_i, 4) || !ptr_ok(new_lens, n_i, 4)) return SC_EINVAL;
+    if (!disjoint({{refs, n_r}, {table, n_t}, {lens, n_l}, {k_pages, n_pool}, {v_pages, n_pool},
+                   {workspace, need}},
+                  {{slot_ids, n_i}, {new_lens, n_i}}))
+        return SC_EINVAL;
+    if (n == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RW(lens, n_l), RO(slot_ids, n_i),
+                      RO(new_lens, n_i), RW(k_pages, n_pool), RW(v_pages, n_pool),
+                      RW(workspace, need));
+    return from_cuda(sc::launch_pages_resize({refs, table, lens, n_pages, n_slots, max_pages, page_size},
+                                             slot_ids, new_lens, n, {k_pages, v_pages, L, token_bytes},
+                                             workspace, sms, (cudaStream_t)stream));
+}
+
+sc_status shortconv_pages_fork(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                               int n_slots, int max_pages, int page_size,
+                               const int32_t *src_slots, const int32_t *dst_slots, int n, int L,
+                               int64_t token_bytes, void *k_pages, void *v_pages, void *workspace,
+                               size_t workspace_bytes, void *stream) {
+    if (n < 0 || n > n_slots) return SC_EINVAL;
+    const size_t need = shortconv_pages_workspace_bytes(n_pages, n);
+    size_t n_pool = 0;
+    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
+                                         L, token_bytes, k_pages, v_pages, workspace,
+                                         workspace_bytes, need, &n_pool);
+    if (st != SC_OK) return st;
+    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
+    const size_t n_l = (size_t)n_slots * 4, n_i = (size_t)n * 4;
+    if (!ptr_ok(src_slots, n_i, 4) || !ptr_ok(dst_slots, n_i, 4)) return SC_EINVAL;
+    if (!disjoint({{refs, n_r}, {table, n_t}, {lens, n_l}, {k_pages, n_pool}, {v_pages, n_pool},
+                   {workspace, need}},
+                  {{src_slots, n_i}, {dst_slots, n_i}}))
+        return SC_EINVAL;
+    if (n == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RW(lens, n_l), RO(src_slots, n_i),
+                      RO(dst_slots, n_i), RW(k_pages, n_pool), RW(v_pages, n_pool),
+                      RW(workspace, need));
+    return from_cuda(sc::launch_pages_fork({refs, table, lens, n_pages, n_slots, max_pages, page_size},
+                                           src_slots, dst_slots, n, {k_pages, v_pages, L, token_bytes},
+                                           workspace, sms, (cudaStream_t)stream));
+}
+
+sc_status shortconv_pages_compact(int32_t *refs, int n_pages, int32_t *table, const int32_t *lens,
+                                  int n_slots, int max_pages, int page_size, int L,
+                                  int64_t token_bytes, void *k_pages, void *v_pages,
+                                  int32_t *n_used, void *workspace, size_t workspace_bytes,
+                                  void *stream) {
+    const size_t need = shortconv_pages_workspace_bytes(n_pages, 0);
+    size_t n_pool = 0;
+    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
+                                         L, token_bytes, k_pages, v_pages, workspace,
+                                         workspace_bytes, need, &n_pool);
+    if (st != SC_OK) return st;
+    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
+    const size_t n_l = (size_t)n_slots * 4;
+    if (!ptr_ok(n_used, 4, 4)) return SC_EINVAL;
+    if (!disjoint({{refs, n_r}, {table, n_t}, {k_pages, n_pool}, {v_pages, n_pool}, {n_used, 4},
+                   {workspace, need}},
+                  {{lens, n_l}}))
+        return SC_EINVAL;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RO(lens, n_l), RW(k_pages, n_pool),
+                      RW(v_pages, n_pool), RW(n_used, 4), RW(workspace, need));
+    return from_cuda(sc::launch_pages_compact(
+        {refs, table, const_cast<int32_t *>(lens), n_pages, n_slots, max_pages, page_size},
+        {k_pages, v_pages, L, token_bytes}, n_used, workspace, sms, (cudaStream_t)stream));
+}
+
+sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                 int N, int D, int64_t token_bytes, void *k_pages, void *v_pages,
+                                 int n_pages, int page_size, const int32_t *table,
+                                 const int32_t *lens, int n_slots, int max_pages,
+                                 const int32_t *slot_ids, void *stream) {
+    const sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    if (st != SC_OK) return st;
+    if (N < 0 || D <= 0 || token_bytes <= 0 || k_stride < token_bytes || v_stride < token_bytes)
+        return SC_EINVAL;
+    if (token_bytes % 16 != 0 || k_stride % 16 != 0 || v_stride % 16 != 0 ||
+        token_bytes > (1 << 24) || k_stride > (1ll << 40) || v_stride > (1ll << 40))
+        return SC_EUNSUPPORTED;
+    if ((int64_t)N * D > INT32_MAX / 2) return SC_EINVAL;
+    const size_t rows = (size_t)N * D;
+    const size_t n_k = rows ? (rows - 1) * k_stride + token_bytes : 0;
+    const size_t n_v = rows ? (rows - 1) * v_stride + token_bytes : 0;
+    const size_t n_pool = (size_t)n_pages * page_size * token_bytes;
+    const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
+    if (!ptr_ok(k, n_k, 16) || !ptr_ok(v, n_v, 16) || !ptr_ok(k_pages, n_pool, 16) ||
+        !ptr_ok(v_pages, n_pool, 16) || !ptr_ok(table, n_t, 4) || !ptr_ok(lens, n_l, 4) ||
+        !ptr_ok(slot_ids, (size_t)N * 4, 4))
+        return SC_EINVAL;
+    if (!disjoint({{k_pages, n_pool}, {v_pages, n_pool}},
+                  {{k, n_k}, {v, n_v}, {table, n_t}, {lens, n_l}, {slot_ids, (size_t)N * 4}}))
+        return SC_EINVAL;
+    if (N == 0) return SC_OK;
+    SC_BOUNDS_INSTALL(kUnitPages, RO(k, n_k), RO(v, n_v), RW(k_pages, n_pool), RW(v_pages, n_pool),
+                      RO(table, n_t), RO(lens, n_l), RO(slot_ids, (size_t)N * 4));
+    return from_cuda(sc::launch_pages_append(
+        {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
+         max_pages, page_size},
+        k, k_stride, v, v_stride, slot_ids, N, D, {k_pages, v_pages, 1, token_bytes},
+        (cudaStream_t)stream));
+}
+
+size_t shortconv_prefix_attention_workspace_bytes(int Hq, int Hkv, int Dh, int N, int D,
+                                                  int shared_pages) {
+    if (Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || (Dh != 64 && Dh != 128) ||
+        N < 0 || D <= 0 || shared_pages < 0 || (int64_t)N * D * Hq > INT32_MAX / 2)
+        return 0;
+    return sc::attention_workspace_bytes({Hq, Hkv, Dh, N, D, shared_pages});
+}
+
+sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, const void *q,
+                                     int64_t q_stride, int N, int D, const void *k_pages,
+                                     const void *v_pages, int n_pages, int page_size,
+                                     const int32_t *table, const int32_t *lens, int n_slots,
+                                     int max_pages, const int32_t *slot_ids, int shared_pages,
+                                     float scale, void *out, void *workspace,
+                                     size_t workspace_bytes, void *stream) {
+    if (dtype != SC_BF16 && dtype != SC_F32) return SC_EUNSUPPORTED;
+    const sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    if (st != SC_OK) return st;
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Dh <= 0 || N < 0 || D <= 0 || shared_pages < 0 ||
+        shared_pages > max_pages || q_stride < (int64_t)Hq * Dh || !(scale > 0.0f))
+        return SC_EINVAL;
+    if (dtype != SC_BF16 || (Dh != 64 && Dh != 128) || Hq / Hkv > 128 || q_stride % 8 != 0 ||
+        q_stride > (1ll << 36) || (int64_t)N * D * Hq > INT32_MAX / 2 ||
+        (int64_t)N * D * Hq * ((int64_t)max_pages * page_size / 64 + 1) > (1ll << 40) ||
+        Hq > (1 << 16) || !(scale < 1e30f))
+        return SC_EUNSUPPORTED;
+    const size_t rows = (size_t)N * D;
+    const size_t n_q = rows ? ((rows - 1) * q_stride + (size_t)Hq * Dh) * 2 : 0;
+    const size_t n_out = rows * Hq * Dh * 2;
+    const size_t n_pool = (size_t)n_pages * page_size * Hkv * Dh * 2;
+    const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
+    const size_t n_i = (size_t)N * 4;
+    const size_t need = sc::attention_workspace_bytes({Hq, Hkv, Dh, N, D, shared_pages});
+    if (workspace_bytes < need) return SC_EINVAL;
+    if (!ptr_ok(q, n_q, 16) || !ptr_ok(k_pages, n_pool, 16) || !ptr_ok(v_pages, n_pool, 16) ||
+        !ptr_ok(table, n_t, 4) || !ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4) ||
+        !ptr_ok(out, n_out, 16) || !ptr_ok(workspace, need, 16))
+        return SC_EINVAL;
+    if (!disjoint({{out, n_out}, {workspace, need}},
+                  {{q, n_q}, {k_pages, n_pool}, {v_pages, n_pool}, {table, n_t}, {lens, n_l},
+                   {slot_ids, n_i}}))
+        return SC_EINVAL;
+    if (N == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitAttention, RO(q, n_q), RO(k_pages, n_pool), RO(v_pages, n_pool),
+                      RO(table, n_t), RO(lens, n_l), RO(slot_ids, n_i), RW(out, n_out),
+                      RW(workspace, need));
+    return from_cuda(sc::launch_prefix_attention(
+        {Hq, Hkv, Dh, N, D, shared_pages}, q, q_stride, k_pages, v_pages,
+        {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
+         max_pages, page_size},
+        slot_ids, scale, out, workspace, sms, (cudaStream_t)stream));
+}
+
+sc_status shortconv_draft_accept(sc_dtype dtype, int V, int N, int D, const void *target,
+                                 int64_t target_stride, const void *draft, int64_t draft_stride,
+                                 const int32_t *tokens, const int32_t *n_drafts,
+                                 const float *uniforms, int32_t *accepted, int32_t *out_tokens,
+                                 void *stream) {
+    if (dtype != SC_BF16 && dtype != SC_F32) return SC_EUNSUPPORTED;
+    if (V <= 0 || N < 0 || D < 0 || target_stride < V || (draft && draft_stride < V))
+        return SC_EINVAL;
+    if (V > (1 << 22) || target_stride > (1ll << 32) || (draft && draft_stride > (1ll << 32)))
+        return SC_EUNSUPPORTED;
+    if ((int64_t)N * (D + 1ll) > INT32_MAX) return SC_EINVAL;
+    const size_t es = elem_size(dtype), nd = (size_t)N * D, nr = (size_t)N * (D + 1);
+    const size_t n_p = nr ? ((nr - 1) * target_stride + V) * es : 0;
+    const size_t n_q = draft && nd ? ((nd - 1) * draft_stride + V) * es : 0;
+    const size_t n_c = n_drafts ? (size_t)N * 4 : 0;
+    if (!ptr_ok(target, n_p, es) || !opt_ok(draft, es) || !ptr_ok(tokens, nd * 4, 4) ||
+        !opt_ok(n_drafts, 4) || !ptr_ok(uniforms, nr * 4, 4) ||
+        !ptr_ok(accepted, (size_t)N * 4, 4) || !ptr_ok(out_tokens, nr * 4, 4))
+        return SC_EINVAL;
+    if (!disjoint({{accepted, (size_t)N * 4}, {out_tokens, nr * 4}},
+                  {{target, n_p}, {draft, n_q}, {tokens, nd * 4}, {n_drafts, n_c},
+                   {uniforms, nr * 4}}))
+        return SC_EINVAL;
+    if (N == 0) return SC_OK;
+    SC_BOUNDS_INSTALL(kUnitDraft, RO(target, n_p), RO(draft, n_q), RO(tokens, nd * 4),
+                      RO(n_drafts, n_c), RO(uniforms, nr * 4), RW(accepted, (size_t)N * 4),
+                      RW(out_tokens, nr * 4));
+    return from_cuda(sc::launch_draft_accept(dtype, V, N, D, target, target_stride, draft,
+                                             draft_stride, tokens, n_drafts, uniforms, accepted,
+                                             out_tokens, (cudaStream_t)stream));
 }
 
 sc_status shortconv_check_wait_limit(void *stream) {

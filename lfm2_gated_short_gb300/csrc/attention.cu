@@ -1,0 +1,684 @@
+// attention.cu -- attention of a serving step over the paged cache (bf16).
+//
+// Row (i, j, hq) is new token j of D of sequence i under query head hq; it
+// sees the sequence's first n = len - D + j + 1 keys of kv head hq / G:
+//   out = sum_t exp(s_t - m) v_t / sum_t exp(s_t - m),  s_t = scale q.k_t.
+// The keys are walked once with a running maximum m and sum l in 32 bits
+// (scores in units of log2, so that one exp2 a score is left); parts of a
+// row's keys join by (m, l).
+//
+// k_own: the D G <= 32 rows of one sequence and kv head are too few for a
+// full tensor-core tile and the call is bound by the keys' bytes, so the
+// rows run on 16-row register MMAs and the work is what streams K and V:
+// every CTA takes an equal share of all 64-key tiles of the call (a share may
+// end inside a sequence), and one producer warp keeps a ring of tiles in
+// flight, one TMA box a page. The four consumer warps take 16 keys each of
+// a tile and keep their own (m, l, O), joined once an item.
+//
+// k_merge joins the parts that CTAs left in the workspace, in a fixed order.
+#include <cuda.h>
+#include <cuda_bf16.h>
+
+#include <atomic>
+#include <mutex>
+
+#include "common.cuh"
+#include "errors.cuh"
+#include "kernels.h"
+#include "launch.h"
+#include "shortconv.h"
+#include "tcgen05.cuh"
+#include "tma.cuh"
+
+namespace sc {
+
+typedef __nv_bfloat16 bf16;
+
+constexpr int kKT = 64;            // keys of a tile
+constexpr int kOwnWarps = 4;       // consumer warps, 16 keys of a tile each
+constexpr int kOwnThreads = 32 * (kOwnWarps + 1);
+constexpr int kMaxCtas = 304;      // two CTAs on each of 152 SMs
+constexpr float kLog2e = 1.4426950408889634f;
+
+struct AttnArgs {
+    const bf16 *q;
+    int64_t q_stride;
+    PageTable pt;
+    const int32_t *slots;
+    int N, D, G, Hkv, Dh;
+    int shared_keys;   // keys whose part the prefix kernel computes
+    float scale_log2;  // scale * log2(e)
+    bf16 *out;
+    int64_t *cum;      // [N + 1] first own tile of each sequence
+    float *own_part;   // [items + CTAs] parts of MR rows: O [MR][Dh], m [MR], l [MR]
+};
+
+// ------------------------------------------------------------ work split
+//
+// The U units (key tiles) of a call lie on a line; CTA c of n takes
+// [c U / n, (c + 1) U / n). The part of item w that CTA c computes goes to
+// slot w + c: along the line each step raises w or c, so slots are distinct.
+
+__host__ __device__ __forceinline__ int64_t share_begin(int64_t c, int64_t U, int64_t n) {
+    return c * U / n;
+}
+__host__ __device__ __forceinline__ int share_of(int64_t u, int64_t U, int64_t n) {
+    return (int)(((u + 1) * n - 1) / U);
+}
+
+// Tokens of sequence i (its D new ones included), or -1 with a bad slot or length.
+__device__ __forceinline__ int seq_len(const AttnArgs &a, int i, int *slot, bool report) {
+    const int s = gld(a.slots + i);
+    *slot = s;
+    if (s < 0 || s >= a.pt.n_slots) {
+        if (report) raise_error(SC_DEV_BAD_SLOT);
+        return -1;
+    }
+    const int len = gld(a.pt.lens + s);
+    if (len < 0 || len > (int64_t)a.pt.max_pages * a.pt.page_size) {
+        if (report) raise_error(SC_DEV_BAD_LENGTH);
+        return -1;
+    }
+    return len;
+}
+
+// Key tiles of a sequence's own part.
+__device__ __forceinline__ int own_tiles(const AttnArgs &a, int len) {
+    return len > a.shared_keys ? (len - a.shared_keys + kKT - 1) / kKT : 0;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+// d += a b for a 16 x 8 x 16 bf16 product, fp32 accumulators.
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A tile row of 64 bf16 is 128 bytes with its 16-byte chunks XOR-swizzled by the
+// row's low 3 bits, as a 128-byte-swizzled TMA box lays it out.
+__device__ __forceinline__ uint32_t swz(int row, int chunk) {
+    return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
+}
+
+template <int DH, int MT>
+struct OwnCfg {
+    static constexpr int MR = 16 * MT;
+    static constexpr int NB = DH / 64;                        // 64-wide column blocks
+    static constexpr uint32_t kBlk = kKT * 128;               // one block of a tile, 8 KB
+    static constexpr uint32_t kStage = 2 * NB * kBlk;         // K and V of a tile
+    static constexpr int kStages = 6;
+    static constexpr int kCtas = DH == 64 ? 2 : 1;            // CTAs of an SM
+    static constexpr uint32_t kQ = MR * 128 * NB;
+    static constexpr int kOs = DH + 4;                        // floats of a joined O row
+    static constexpr uint32_t kJoin = (MR * kOs + 2 * kOwnWarps * MR) * 4;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + kQ + kJoin;
+    static constexpr int kSlot = MR * (DH + 2);               // floats of a part
+};
+
+template <int DH, int MT>
+__global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
+    k_own(AttnArgs a, const __grid_constant__ CUtensorMap mk,
+          const __grid_constant__ CUtensorMap mv) {
+    using C = OwnCfg<DH, MT>;
+    constexpr int ST = C::kStages;
+    extern __shared__ unsigned char raw[];
+    __shared__ uint64_t s_full[ST], s_empty[ST];
+    __shared__ int s_bad[ST];
+    __shared__ int64_t s_scan[kOwnThreads];
+    __shared__ int s_seq;
+    __shared__ int64_t s_seq_unit;
+    const uint32_t raw_a = smem_addr(raw);
+    unsigned char *ring = raw + (((raw_a + 1023u) & ~1023u) - raw_a);
+    const uint32_t ring_a = smem_addr(ring);
+    unsigned char *qs = ring + ST * C::kStage;
+    const uint32_t qs_a = smem_addr(qs);
+    float *join = reinterpret_cast<float *>(qs + C::kQ);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&s_full[s], 1);
+            mbar_init(&s_empty[s], kOwnWarps);
+            s_bad[s] = 0;
+        }
+        mbar_fence_init();
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+        s_seq = a.N;
+        s_seq_unit = 0;
+    }
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+
+    // The units of the call and the sequence that holds this CTA's first one.
+    const int rows = a.D * a.G;
+    const int RT = (rows + C::MR - 1) / C::MR;
+    const int per = RT * a.Hkv;  // items of a sequence
+    int64_t U = 0, u0 = 0, u1 = 0;
+    int n_cta = 1;
+    for (int pass = 0; pass < 2; ++pass) {
+        int64_t base = 0;
+        for (int i0 = 0; i0 < a.N; i0 += kOwnThreads) {
+            const int i = i0 + tid;
+            int slot;
+            int64_t mine = 0;
+            if (i < a.N)
+                mine = (int64_t)per *
+                       own_tiles(a, seq_len(a, i, &slot, pass == 0 && blockIdx.x == 0));
+            s_scan[tid] = mine;
+            __syncthreads();
+            for (int o = 1; o < kOwnThreads; o <<= 1) {
+                const int64_t v = tid >= o ? s_scan[tid - o] : 0;
+                __syncthreads();
+                s_scan[tid] += v;
+                __syncthreads();
+            }
+            const int64_t begin = base + s_scan[tid] - mine;
+            if (pass == 1 && i < a.N) {
+                if (u0 >= begin && u0 < begin + mine) {
+                    s_seq = i;
+                    s_seq_unit = begin;
+                }
+                if (blockIdx.x == 0) gst(a.cum + i, begin);
+            }
+            base += s_scan[kOwnThreads - 1];
+            __syncthreads();
+        }
+        if (pass == 0) {
+            U = base;
+            n_cta = (int)min((int64_t)gridDim.x, max(U, (int64_t)1));
+            u0 = share_begin(blockIdx.x, U, n_cta);
+            u1 = share_begin(blockIdx.x + 1, U, n_cta);
+            if (blockIdx.x == 0 && tid == 0) gst(a.cum + a.N, U);
+            if ((int)blockIdx.x >= n_cta && blockIdx.x > 0) return;
+        }
+    }
+    if (u0 >= u1) return;
+
+    // Walk the CTA's units: f(i, slot, len, rt, h, w, first tile, tiles, T) for each
+    // item piece, in order, until it returns false.
+    auto walk = [&](auto &&f) {
+        int64_t u = u0, begin = s_seq_unit;
+        int i = s_seq;
+        while (u < u1 && i < a.N) {
+            int slot;
+            const int len = seq_len(a, i, &slot, false);
+            const int T = own_tiles(a, len);
+            const int64_t end = begin + (int64_t)T * per;
+            while (u < end && u < u1) {
+                const int it = (int)((u - begin) / T), t0 = (int)((u - begin) % T);
+                const int n = (int)min((int64_t)(T - t0), u1 - u);
+                if (!f(i, slot, len, it / a.Hkv, it % a.Hkv, i * per + it, t0, n, T)) return;
+                u += n;
+            }
+            begin = end;
+            ++i;
+        }
+    };
+
+    if (warp == kOwnWarps) {  // producer
+        const int ps = a.pt.page_size;
+        const int box = min(ps, kKT), nb = kKT / box;  // keys of a box, boxes of a tile
+        uint32_t g = 0;
+        walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
+            const int32_t *row = a.pt.table + (int64_t)slot * a.pt.max_pages;
+            // Lane b holds the page of box b0 + b of the item; one batch ahead is in flight.
+            const int last = (len - 1) / box;
+            auto ids = [&](int b0) {
+                const int b = min(b0 + lane, last);
+                return gld(row + (int64_t)b * box / ps);
+            };
+            int b0 = a.shared_keys / box + t0 * nb;
+            int cur = ids(b0), nxt = ids(b0 + 32);
+            int at = 0;
+            for (int t = 0; t < n; ++t, ++g) {
+                const uint32_t s = g % ST;
+                if (g >= ST && !mbar_wait_bounded(&s_empty[s], (g / ST - 1) & 1u)) {
+                    raise_error(SC_DEV_TIMEOUT);
+                    return false;
+                }
+                const int boxes = min(nb, last + 1 - (b0 + at));
+                int id = __shfl_sync(~0u, cur, (at + lane) & 31);
+                bool bad = lane < boxes && (id < 0 || id >= a.pt.n_pages);
+                if (bad) id = 0;
+                bad = __any_sync(~0u, bad);
+                if (lane == 0) {
+                    if (bad) raise_error(SC_DEV_BAD_PAGE);
+                    s_bad[s] = bad;
+                    mbar_arrive_expect_tx(&s_full[s], (uint32_t)boxes * box * DH * 4);
+                }
+                __syncwarp();
+                if (lane < boxes) {
+                    const int key = id * ps + (int)((int64_t)(b0 + at + lane) * box % ps);
+                    const uint32_t d = ring_a + s * C::kStage + lane * box * 128;
+#pragma unroll
+                    for (int c = 0; c < C::NB; ++c) {
+                        tma_load_3d(d + c * C::kBlk, &mk, &s_full[s], c * 64, h, key);
+                        tma_load_3d(d + (C::NB + c) * C::kBlk, &mv, &s_full[s], c * 64, h, key);
+                    }
+                }
+                at += nb;
+                if (at >= 32) {
+                    at = 0;
+                    b0 += 32;
+                    cur = nxt;
+                    nxt = ids(b0 + 32);
+                }
+            }
+            return true;
+        });
+        // No copy may be in flight when the CTA leaves.
+        for (uint32_t c = g > ST ? g - ST : 0; c < g; ++c)
+            mbar_wait_bounded(&s_full[c % ST], (c / ST) & 1u);
+        return;
+    }
+
+    uint32_t g = 0;
+    bool dead = false;
+    walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
+        // The item's query rows, and the keys that this thread's rows see.
+        const int r0 = rt * C::MR;
+        for (int x = tid; x < C::MR * DH / 8; x += 32 * kOwnWarps) {
+            const int r = x / (DH / 8), ch = x % (DH / 8), rr = r0 + r;
+            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+            if (rr < rows)
+                v = ld_plain(a.q + ((int64_t)i * a.D + rr / a.G) * a.q_stride +
+                             (h * a.G + rr % a.G) * DH + ch * 8);
+            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::MR * 128 + swz(r, ch & 7)) = v;
+        }
+        named_sync(1, 32 * kOwnWarps);
+        uint32_t qf[MT][DH / 16][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                const int ch = kk * 2 + (lane >> 4);
+                ldsm4(qf[mt][kk], qs_a + (ch >> 3) * C::MR * 128 +
+                                      swz(mt * 16 + (lane & 15), ch & 7));
+            }
+        int see[MT][2];
+        float m[MT][2], l[MT][2], o[MT][DH / 8][4];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int rr = r0 + mt * 16 + p * 8 + (lane >> 2);
+                see[mt][p] = rr < rows ? len - a.D + rr / a.G + 1 : 0;
+                m[mt][p] = -INFINITY;
+                l[mt][p] = 0.0f;
+            }
+#pragma unroll
+            for (int d = 0; d < DH / 8; ++d)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.0f;
+        }
+        bool bad = false;
+        for (int t = 0; t < n; ++t, ++g) {
+            const uint32_t s = g % ST;
+            if (!dead && !mbar_wait_bounded(&s_full[s], (g / ST) & 1u)) {
+                raise_error(SC_DEV_TIMEOUT);
+                dead = true;  // no more waits: the rest runs through on what is there
+            }
+            bad |= s_bad[s] != 0;
+            const uint32_t kt = ring_a + s * C::kStage, vt = kt + C::NB * C::kBlk;
+            const int key0 = a.shared_keys + (t0 + t) * kKT + warp * 16;
+            const bool tail = key0 + 16 > len;
+            if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
+                const int from = max(0, len - key0);
+                for (int x = lane; x < (16 - from) * C::NB * 8; x += 32) {
+                    const int r = from + x / (C::NB * 8), ch = x % (C::NB * 8);
+                    *reinterpret_cast<uint4 *>(ring + s * C::kStage + (C::NB + (ch >> 3)) * C::kBlk +
+                                               (warp * 16 + r) * 128 + (ch & 7) * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                __syncwarp();
+            }
+            float sc[MT][2][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[mt][0][e] = sc[mt][1][e] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                uint32_t b[4];
+                const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+                const int ch = kk * 2 + ((lane >> 3) & 1);
+                ldsm4(b, kt + (ch >> 3) * C::kBlk + swz(row, ch & 7));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma16816(sc[mt][0], qf[mt][kk], b[0], b[1]);
+                    mma16816(sc[mt][1], qf[mt][kk], b[2], b[3]);
+                }
+            }
+            uint32_t pf[MT][4];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                float top[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int key = key0 + nt * 8 + (lane & 3) * 2 + (e & 1);
+                        float &x = sc[mt][nt][e];
+                        x = key < see[mt][e >> 1] ? x * a.scale_log2 : -INFINITY;
+                        top[e >> 1] = fmaxf(top[e >> 1], x);
+                    }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
+                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
+                    top[p] = fmaxf(top[p], m[mt][p]);
+                    // A row that has seen no key yet keeps m = -inf and sums of zero.
+                    const float base = top[p] == -INFINITY ? 0.0f : top[p];
+                    const float f = exp2f(m[mt][p] - base);
+                    m[mt][p] = top[p];
+                    l[mt][p] *= f;
+#pragma unroll
+                    for (int d = 0; d < DH / 8; ++d) {
+                        o[mt][d][2 * p] *= f;
+                        o[mt][d][2 * p + 1] *= f;
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const float e0 = exp2f(sc[mt][nt][2 * p] - base);
+                        const float e1 = exp2f(sc[mt][nt][2 * p + 1] - base);
+                        l[mt][p] += e0 + e1;
+                        // P enters the second product as bf16: 2^-9 relative a term.
+                        pf[mt][nt * 2 + p] = pack_bf16(e0, e1);
+                    }
+                }
+            }
+#pragma unroll
+            for (int dd = 0; dd < DH / 16; ++dd) {
+                uint32_t b[4];
+                const int row = warp * 16 + (lane & 15);
+                const int ch = dd * 2 + (lane >> 4);
+                ldsm4_t(b, vt + (ch >> 3) * C::kBlk + swz(row, ch & 7));
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    mma16816(o[mt][2 * dd], pf[mt], b[0], b[1]);
+                    mma16816(o[mt][2 * dd + 1], pf[mt], b[2], b[3]);
+                }
+            }
+            if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_empty[s]);
+        }
+        // Join the four warps: the common maximum, then O and l in turn.
+        float *jm = join + C::MR * C::kOs, *jl = jm + kOwnWarps * C::MR;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                l[mt][p] += __shfl_xor_sync(~0u, l[mt][p], 1);
+                l[mt][p] += __shfl_xor_sync(~0u, l[mt][p], 2);
+                const int r = mt * 16 + p * 8 + (lane >> 2);
+                if ((lane & 3) == 0) jm[warp * C::MR + r] = m[mt][p];
+            }
+        named_sync(1, 32 * kOwnWarps);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int r = mt * 16 + p * 8 + (lane >> 2);
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kOwnWarps; ++k) top = fmaxf(top, jm[k * C::MR + r]);
+                const float f = exp2f(m[mt][p] - (top == -INFINITY ? 0.0f : top));
+                if ((lane & 3) == 0) jl[warp * C::MR + r] = l[mt][p] * f;
+#pragma unroll
+                for (int d = 0; d < DH / 8; ++d) {
+                    o[mt][d][2 * p] *= f;
+                    o[mt][d][2 * p + 1] *= f;
+                }
+            }
+        constexpr int kQuarter = DH / 8 / kOwnWarps;
+#pragma unroll
+        for (int round = 0; round < kOwnWarps; ++round) {
+            const int blk = (warp + round) % kOwnWarps;  // each warp adds another quarter
+#pragma unroll
+            for (int d = 0; d < DH / 8; ++d) {
+                if (d / kQuarter != blk) continue;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        float2 *at = reinterpret_cast<float2 *>(
+                            join + (mt * 16 + p * 8 + (lane >> 2)) * C::kOs + d * 8 +
+                            (lane & 3) * 2);
+                        float2 v = round ? *at : make_float2(0.0f, 0.0f);
+                        v.x += o[mt][d][2 * p];
+                        v.y += o[mt][d][2 * p + 1];
+                        *at = v;
+                    }
+            }
+            named_sync(1, 32 * kOwnWarps);
+        }
+        const bool whole = n == T && a.shared_keys == 0;  // nothing to join with
+        float *part = a.own_part + (int64_t)(w + blockIdx.x) * C::kSlot;
+        for (int x = tid; x < C::MR * DH / 4; x += 32 * kOwnWarps) {
+            const int r = x / (DH / 4), c4 = x % (DH / 4), rr = r0 + r;
+            float4 v = *reinterpret_cast<float4 *>(join + r * C::kOs + c4 * 4);
+            if (rr >= rows) continue;
+            if (whole) {
+                if (bad) continue;
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < kOwnWarps; ++k) sum += jl[k * C::MR + r];
+                const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+                gst(reinterpret_cast<uint2 *>(a.out + (((int64_t)i * a.D + rr / a.G) * a.Hkv + h) *
+                                                          a.G * DH + (rr % a.G) * DH + c4 * 4),
+                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
+            } else {
+                gst(reinterpret_cast<float4 *>(part + r * DH + c4 * 4), v);
+            }
+        }
+        if (!whole && tid < C::MR) {
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < kOwnWarps; ++k) {
+                top = fmaxf(top, jm[k * C::MR + tid]);
+                sum += jl[k * C::MR + tid];
+            }
+            // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
+            gst(part + C::MR * DH + tid, bad ? __int_as_float(0x7FC00000) : top);
+            gst(part + C::MR * DH + C::MR + tid, sum);
+        }
+        named_sync(1, 32 * kOwnWarps);  // join and Q are written again by the next item
+        return true;
+    });
+}
+
+// A row is joined by Dh / 4 lanes, four columns each.
+template <int DH>
+__global__ void __launch_bounds__(256) k_merge(AttnArgs a, int MR, int own_ctas) {
+    pdl_wait();
+    pdl_launch_dependents();
+    constexpr int L = DH / 4;
+    const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
+    const int c4 = threadIdx.x % L;
+    const int Hq = a.Hkv * a.G;
+    if (row >= (int64_t)a.N * a.D * Hq) return;
+    const int i = (int)(row / ((int64_t)a.D * Hq)), j = (int)(row / Hq % a.D);
+    const int hq = (int)(row % Hq), h = hq / a.G, g = hq % a.G;
+    int slot;
+    const int len = seq_len(a, i, &slot, false);
+    if (len < 0) return;
+    const int T = own_tiles(a, len);
+    const int64_t U = gld(a.cum + a.N);
+    const int n_cta = (int)min((int64_t)own_ctas, max(U, (int64_t)1));
+    const int r = j * a.G + g, rt = r / MR, rr = r % MR;
+    const int RT = (a.D * a.G + MR - 1) / MR;
+    const int it = rt * a.Hkv + h;
+    float top = -INFINITY, sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (T > 0) {
+        const int64_t u0 = gld(a.cum + i) + (int64_t)it * T;
+        const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
+        if (c0 == c1 && a.shared_keys == 0) return;  // k_own wrote the row
+        const int64_t w = (int64_t)i * RT * a.Hkv + it;
+        for (int c = c0; c <= c1 && top == top; ++c) {
+            const float *part = a.own_part + (w + c) * ((int64_t)MR * (DH + 2));
+            const float m = gld(part + MR * DH + rr), l = gld(part + MR * DH + MR + rr);
+            const float4 v = gld(reinterpret_cast<const float4 *>(part + rr * DH) + c4);
+            if (m != m) {
+                top = m;
+                break;
+            }
+            const float now = fmaxf(top, m), base = now == -INFINITY ? 0.0f : now;
+            const float f0 = exp2f(top - base), f1 = exp2f(m - base);
+            sum = sum * f0 + l * f1;
+            o.x = o.x * f0 + v.x * f1;
+            o.y = o.y * f0 + v.y * f1;
+            o.z = o.z * f0 + v.z * f1;
+            o.w = o.w * f0 + v.w * f1;
+            top = now;
+        }
+    }
+    if (top != top) return;  // a bad page: the row is not written
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    gst(reinterpret_cast<uint2 *>(a.out + row * DH + c4 * 4),
+        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)));
+}
+
+// ------------------------------------------------------------ host side
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &r) == cudaSuccess &&
+            r == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<EncodeTiledFn>(p);
+    });
+    return fn;
+}
+
+// Pages [n_pages * page_size tokens, Hkv, Dh] in boxes of `keys` tokens of one
+// head, 64 columns, 128-byte swizzle.
+static cudaError_t map_pages(CUtensorMap *m, const void *ptr, const PageTable &pt, int Hkv, int Dh,
+                             int keys) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)Dh, (cuuint64_t)Hkv,
+                                (cuuint64_t)pt.n_pages * pt.page_size};
+    const cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, (cuuint64_t)Hkv * Dh * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)keys};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
+                          strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Rows of an item: 16 hold up to 16 rows of a sequence and kv head, else 32.
+static int own_rows(const AttnShape &s) { return s.D * (s.Hq / s.Hkv) <= 16 ? 16 : 32; }
+
+static size_t own_part_floats(const AttnShape &s) {
+    const int MR = own_rows(s);
+    const size_t items =
+        (size_t)s.N * s.Hkv * (((size_t)s.D * (s.Hq / s.Hkv) + MR - 1) / MR);
+    return (items + kMaxCtas) * MR * (s.Dh + 2);
+}
+static size_t cum_bytes(const AttnShape &s) { return ((size_t)s.N + 2) / 2 * 16; }
+
+size_t attention_workspace_bytes(const AttnShape &s) {
+    return cum_bytes(s) + own_part_floats(s) * 4;
+}
+
+template <int DH, int MT>
+static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
+                              int grid, cudaStream_t stream) {
+    using C = OwnCfg<DH, MT>;
+    auto kern = k_own<DH, MT>;
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (!(done.load() >> (dev & 63) & 1)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)C::kSmem);
+        if (e != cudaSuccess) return e;
+        done.fetch_or(1ull << (dev & 63));
+    }
+    return launch_pdl(kern, dim3((unsigned)grid), dim3(kOwnThreads), C::kSmem, stream, a, mk, mv);
+}
+
+cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
+                                    const void *k_pages, const void *v_pages, const PageTable &pt,
+                                    const int32_t *slots, float scale, void *out,
+                                    void *workspace, int sm_count, cudaStream_t stream) {
+    AttnArgs a;
+    a.q = (const bf16 *)q;
+    a.q_stride = q_stride;
+    a.pt = pt;
+    a.slots = slots;
+    a.N = s.N;
+    a.D = s.D;
+    a.G = s.Hq / s.Hkv;
+    a.Hkv = s.Hkv;
+    a.Dh = s.Dh;
+    a.shared_keys = 0;
+    a.scale_log2 = scale * kLog2e;
+    a.out = (bf16 *)out;
+    a.cum = (int64_t *)workspace;
+    a.own_part = (float *)((char *)workspace + cum_bytes(s));
+    CUtensorMap mk, mv;
+    const int box = pt.page_size < kKT ? pt.page_size : kKT;
+    cudaError_t e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, box);
+    if (e != cudaSuccess) return e;
+    e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, box);
+    if (e != cudaSuccess) return e;
+    const int MR = own_rows(s), ctas = (s.Dh == 64 ? 2 : 1) * sm_count;
+    const int grid = ctas < kMaxCtas ? ctas : kMaxCtas;
+    if (s.Dh == 64)
+        e = MR == 16 ? launch_own<64, 1>(a, mk, mv, grid, stream)
+                     : launch_own<64, 2>(a, mk, mv, grid, stream);
+    else
+        e = MR == 16 ? launch_own<128, 1>(a, mk, mv, grid, stream)
+                     : launch_own<128, 2>(a, mk, mv, grid, stream);
+    if (e != cudaSuccess) return e;
+    const int64_t threads = (int64_t)s.N * s.D * s.Hq * (s.Dh / 4);
+    const dim3 blocks((unsigned)((threads + 255) / 256));
+    return s.Dh == 64 ? launch_pdl(k_merge<64>, blocks, dim3(256), 0, stream, a, MR, grid)
+                      : launch_pdl(k_merge<128>, blocks, dim3(256), 0, stream, a, MR, grid);
+}
+
+cudaError_t take_error_attention(cudaStream_t stream, unsigned int *sum) {
+    return take_error_here(stream, sum);
+}
+
+#ifdef SC_BOUNDS_CHECK
+cudaError_t bounds_install_attention(const BoundsRegion *r, int n, cudaStream_t stream) {
+    return bounds_install_here(r, n, stream);
+}
+cudaError_t bounds_take_attention(cudaStream_t stream, unsigned long long *addr) {
+    return bounds_take_first_bad_here(stream, addr);
+}
+#endif
+
+}  // namespace sc

@@ -934,8 +934,8 @@ cudaError_t launch_backward(int dtype, int H, int K, const void *bcx, int64_t T,
     return backward_K<float>(K, bcx, T, H, w, bias, dy, dbcx, dw, dbias, ws, s);
 }
 
-cudaError_t take_error_backward(cudaStream_t stream, unsigned int *code) {
-    return take_error_here(stream, code);
+cudaError_t take_error_backward(cudaStream_t stream, unsigned int *sum) {
+    return take_error_here(stream, sum);
 }
 
 #ifdef SC_BOUNDS_CHECK

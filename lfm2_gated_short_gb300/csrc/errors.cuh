@@ -10,23 +10,21 @@
 namespace sc {
 
 static __device__ unsigned int g_error_word;   // bit mask of SC_DEV_* codes
-static __device__ unsigned int g_error_taken;  // last value taken by take_error_here
 
 static __device__ __forceinline__ void raise_error(unsigned int code) {
     atomicOr(&g_error_word, code);
 }
 
-static __global__ void k_take_error() { g_error_taken = atomicExch(&g_error_word, 0u); }
+static __global__ void k_take_error(unsigned int *sum) {
+    const unsigned int code = atomicExch(&g_error_word, 0u);
+    if (code) atomicOr(sum, code);
+}
 
-// Take (read and clear) this unit's word, ordered after the stream's work.
-static cudaError_t take_error_here(cudaStream_t stream, unsigned int *code) {
-    k_take_error<<<1, 1, 0, stream>>>();
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-    e = cudaMemcpyFromSymbolAsync(code, g_error_taken, sizeof(unsigned int), 0,
-                                  cudaMemcpyDeviceToHost, stream);
-    if (e != cudaSuccess) return e;
-    return cudaStreamSynchronize(stream);
+// Enqueue: take (read and clear) this unit's word and OR it into *sum (device
+// memory), ordered after the stream's work.
+static cudaError_t take_error_here(cudaStream_t stream, unsigned int *sum) {
+    k_take_error<<<1, 1, 0, stream>>>(sum);
+    return cudaGetLastError();
 }
 
 }  // namespace sc

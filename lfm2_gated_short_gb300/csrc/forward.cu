@@ -11,6 +11,7 @@
 // the K-1 values of u before its tile from the B and x rows just above it.
 #include <algorithm>
 #include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "errors.cuh"
@@ -652,18 +653,28 @@ cudaError_t launch_rollback(int dtype, int H, int K, int L, int N, int D, const 
 
 // ------------------------------------------------------------ error word
 
+// Every unit's word is ORed into one device word, copied once. Host threads
+// take turns: the sum is shared.
+static __device__ unsigned int g_error_sum;
+static __global__ void k_clear_error_sum() { g_error_sum = 0u; }
+
 cudaError_t read_and_clear_error(cudaStream_t stream, unsigned int *code) {
-    unsigned int a = 0, b = 0, c = 0, d = 0;  // forward, backward, slot-pool, projection words
-    cudaError_t e = take_error_here(stream, &a);
+    static std::mutex mu;
+    std::lock_guard<std::mutex> lock(mu);
+    unsigned int *sum = nullptr;
+    cudaError_t e = cudaGetSymbolAddress((void **)&sum, g_error_sum);
     if (e != cudaSuccess) return e;
-    e = take_error_backward(stream, &b);
+    k_clear_error_sum<<<1, 1, 0, stream>>>();
+    e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    e = take_error_slots(stream, &c);
+    for (auto take : {take_error_here, take_error_backward, take_error_slots, take_error_proj,
+                      take_error_pages, take_error_draft, take_error_attention}) {
+        e = take(stream, sum);
+        if (e != cudaSuccess) return e;
+    }
+    e = cudaMemcpyAsync(code, sum, sizeof(unsigned int), cudaMemcpyDeviceToHost, stream);
     if (e != cudaSuccess) return e;
-    e = take_error_proj(stream, &d);
-    if (e != cudaSuccess) return e;
-    *code = a | b | c | d;
-    return cudaSuccess;
+    return cudaStreamSynchronize(stream);
 }
 
 #ifdef SC_BOUNDS_CHECK
@@ -674,19 +685,25 @@ cudaError_t bounds_install(int unit, const BoundsRegion *r, int n, cudaStream_t 
         case kUnitForward: return bounds_install_here(r, n, s);
         case kUnitBackward: return bounds_install_backward(r, n, s);
         case kUnitProj: return bounds_install_proj(r, n, s);
-        default: return bounds_install_slots(r, n, s);
+        case kUnitSlots: return bounds_install_slots(r, n, s);
+        case kUnitPages: return bounds_install_pages(r, n, s);
+        case kUnitDraft: return bounds_install_draft(r, n, s);
+        default: return bounds_install_attention(r, n, s);
     }
 }
 
 cudaError_t bounds_take_first_bad(cudaStream_t s, unsigned long long *addr) {
-    unsigned long long a[4] = {0, 0, 0, 0};
+    unsigned long long a[7] = {0, 0, 0, 0, 0, 0, 0};
     cudaError_t e = bounds_take_first_bad_here(s, &a[0]);
     if (e == cudaSuccess) e = bounds_take_backward(s, &a[1]);
     if (e == cudaSuccess) e = bounds_take_proj(s, &a[2]);
     if (e == cudaSuccess) e = bounds_take_slots(s, &a[3]);
+    if (e == cudaSuccess) e = bounds_take_pages(s, &a[4]);
+    if (e == cudaSuccess) e = bounds_take_draft(s, &a[5]);
+    if (e == cudaSuccess) e = bounds_take_attention(s, &a[6]);
     if (e != cudaSuccess) return e;
     *addr = 0;
-    for (int i = 0; i < 4 && *addr == 0; ++i) *addr = a[i] & ~1ull;  // bit 0 marks "set"
+    for (int i = 0; i < 7 && *addr == 0; ++i) *addr = a[i] & ~1ull;  // bit 0 marks "set"
     return cudaSuccess;
 }
 #endif

@@ -77,10 +77,11 @@ cudaError_t launch_in_proj_decode(int D, int H, int K, const void *hidden, int N
                                   const void *w_in, const void *w, const void *bias,
                                   const int32_t *slot_ids, void *pool, int n_slots, void *y,
                                   int sm_count, cudaStream_t stream);
-cudaError_t take_error_proj(cudaStream_t stream, unsigned int *code);
+cudaError_t take_error_proj(cudaStream_t stream, unsigned int *sum);
 
-// Take (read and clear) the backward translation unit's error word.
-cudaError_t take_error_backward(cudaStream_t stream, unsigned int *code);
+// Enqueue: take (read and clear) a translation unit's error word and OR it into
+// *sum (device memory). Likewise take_error_proj, _slots, _pages, _draft, _attention.
+cudaError_t take_error_backward(cudaStream_t stream, unsigned int *sum);
 
 // Slot pool: claim n_claim free slots (lowest first, all-or-nothing) and
 // zero their states when pool != NULL; release slots; copy states.
@@ -90,9 +91,55 @@ cudaError_t launch_slots_release(uint32_t *in_use, int n_slots, const int32_t *s
                                  cudaStream_t stream);
 cudaError_t launch_pool_copy(const int32_t *src, const int32_t *dst, int n, int64_t state_bytes,
                              void *pool, int n_slots, cudaStream_t stream);
-cudaError_t take_error_slots(cudaStream_t stream, unsigned int *code);
+cudaError_t take_error_slots(cudaStream_t stream, unsigned int *sum);
 // A one-thread kernel whose bounded wait must run out and set SC_DEV_TIMEOUT.
 cudaError_t launch_wait_limit_check(cudaStream_t stream);
+
+// The paged cache (pages.cu). `pools`: L stacked layers of k and v pages of
+// page_size * token_bytes bytes each.
+struct PageTable {
+    int32_t *refs;   // [n_pages] table entries that name the page (0: free)
+    int32_t *table;  // [n_slots, max_pages]
+    int32_t *lens;   // [n_slots]
+    int n_pages, n_slots, max_pages, page_size;
+};
+struct PagePools {
+    void *k, *v;
+    int L;
+    int64_t token_bytes;
+};
+size_t pages_workspace_bytes(int n_pages, int n);
+cudaError_t launch_pages_resize(const PageTable &pt, const int32_t *slots, const int32_t *new_lens,
+                                int n, const PagePools &pools, void *workspace, int sm_count,
+                                cudaStream_t stream);
+cudaError_t launch_pages_fork(const PageTable &pt, const int32_t *src, const int32_t *dst, int n,
+                              const PagePools &pools, void *workspace, int sm_count,
+                              cudaStream_t stream);
+cudaError_t launch_pages_compact(const PageTable &pt, const PagePools &pools, int32_t *n_used,
+                                 void *workspace, int sm_count, cudaStream_t stream);
+cudaError_t launch_pages_append(const PageTable &pt, const void *k, int64_t k_stride,
+                                const void *v, int64_t v_stride, const int32_t *slots, int N,
+                                int D, const PagePools &pools, cudaStream_t stream);
+cudaError_t take_error_pages(cudaStream_t stream, unsigned int *sum);
+
+// Draft acceptance (draft.cu). draft NULL: the drafts were certain.
+cudaError_t launch_draft_accept(int dtype, int V, int N, int D, const void *target,
+                                int64_t target_stride, const void *draft, int64_t draft_stride,
+                                const int32_t *tokens, const int32_t *n_drafts,
+                                const float *uniforms, int32_t *accepted, int32_t *out_tokens,
+                                cudaStream_t stream);
+cudaError_t take_error_draft(cudaStream_t stream, unsigned int *sum);
+
+// Attention over the paged cache (attention.cu), bf16.
+struct AttnShape {
+    int Hq, Hkv, Dh, N, D, shared_pages;
+};
+size_t attention_workspace_bytes(const AttnShape &s);
+cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
+                                    const void *k_pages, const void *v_pages, const PageTable &pt,
+                                    const int32_t *slots, float scale, void *out,
+                                    void *workspace, int sm_count, cudaStream_t stream);
+cudaError_t take_error_attention(cudaStream_t stream, unsigned int *sum);
 
 // Read and clear the device error word of the current device (synchronous
 // with respect to `stream`).
@@ -109,16 +156,30 @@ struct BoundsRegion {
 };
 constexpr int kMaxBoundsRegions = 16;
 #ifdef SC_BOUNDS_CHECK
-enum BoundsUnit { kUnitForward = 0, kUnitBackward = 1, kUnitProj = 2, kUnitSlots = 3 };
+enum BoundsUnit {
+    kUnitForward = 0,
+    kUnitBackward = 1,
+    kUnitProj = 2,
+    kUnitSlots = 3,
+    kUnitPages = 4,
+    kUnitDraft = 5,
+    kUnitAttention = 6
+};
 cudaError_t bounds_install(int unit, const BoundsRegion *r, int n, cudaStream_t stream);
 // The first address any unit refused since the last call (0 when none), cleared.
 cudaError_t bounds_take_first_bad(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_install_backward(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_proj(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_slots(const BoundsRegion *r, int n, cudaStream_t stream);
+cudaError_t bounds_install_pages(const BoundsRegion *r, int n, cudaStream_t stream);
+cudaError_t bounds_install_draft(const BoundsRegion *r, int n, cudaStream_t stream);
+cudaError_t bounds_install_attention(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_take_backward(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_proj(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_slots(cudaStream_t stream, unsigned long long *addr);
+cudaError_t bounds_take_pages(cudaStream_t stream, unsigned long long *addr);
+cudaError_t bounds_take_draft(cudaStream_t stream, unsigned long long *addr);
+cudaError_t bounds_take_attention(cudaStream_t stream, unsigned long long *addr);
 #endif
 
 }  // namespace sc

@@ -1418,8 +1418,8 @@ cudaError_t launch_out_proj(int H, int D, const void *y, int64_t T, const void *
                               stream, kPCluster, ma, mb, mo, H, n_ntiles, (int)n_mtiles);
 }
 
-cudaError_t take_error_proj(cudaStream_t stream, unsigned int *code) {
-    return take_error_here(stream, code);
+cudaError_t take_error_proj(cudaStream_t stream, unsigned int *sum) {
+    return take_error_here(stream, sum);
 }
 
 #ifdef SC_BOUNDS_CHECK

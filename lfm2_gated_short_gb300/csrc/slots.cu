@@ -159,8 +159,8 @@ cudaError_t launch_wait_limit_check(cudaStream_t stream) {
     return launch_pdl(k_wait_limit_check, dim3(1), dim3(1), 0, stream);
 }
 
-cudaError_t take_error_slots(cudaStream_t stream, unsigned int *code) {
-    return take_error_here(stream, code);
+cudaError_t take_error_slots(cudaStream_t stream, unsigned int *sum) {
+    return take_error_here(stream, sum);
 }
 
 #ifdef SC_BOUNDS_CHECK
