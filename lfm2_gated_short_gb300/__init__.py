@@ -16,6 +16,7 @@ dtype; None for none), added to the conv output before the C gate.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -49,6 +50,8 @@ class ShortConvError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """The loaded C library (argument types declared). Raises if it is not built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -137,20 +140,27 @@ def _dcode(t: torch.Tensor) -> int:
 def _dev(t: torch.Tensor, name: str, dtype=None, shape=None) -> int:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:  # torch.Size compares as a tuple
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
 
+# The current stream's handle without building a torch.cuda.Stream object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream, device) -> int:
-    s = stream if stream is not None else torch.cuda.current_stream(device)
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None and device.index is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
 
 
 def _bias(bias, dt, H):
@@ -424,18 +434,18 @@ def _rows(t, name, dtype, shape):
     dims after the first) are contiguous and may lie further apart."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    width = 1
-    for d in range(t.dim() - 1, 0, -1):
-        if t.shape[d] != 1 and t.stride(d) != width:
+    strides, width = t.stride(), 1
+    for n, s in zip(shape[:0:-1], strides[:0:-1]):
+        if n != 1 and s != width:
             raise ValueError(f"{name} must have contiguous rows")
-        width *= t.shape[d]
-    return t.data_ptr(), (t.stride(0) if t.shape[0] > 1 else width)
+        width *= n
+    return t.data_ptr(), (strides[0] if shape[0] > 1 else width)
 
 
 def _cache(refs, table, lens):
@@ -472,6 +482,7 @@ def page_cache(n_slots: int, max_pages: int, n_pages: int, device="cuda"):
             torch.zeros((n_slots,), **i32))
 
 
+@functools.lru_cache(maxsize=1024)
 def pages_workspace_bytes(n_pages: int, n: int) -> int:
     return int(lib().shortconv_pages_workspace_bytes(n_pages, n))
 
@@ -535,6 +546,7 @@ def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None):
         _stream(stream, k_pages.device)))
 
 
+@functools.lru_cache(maxsize=1024)
 def prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages=0) -> int:
     return int(lib().shortconv_prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages))
 
@@ -578,23 +590,27 @@ def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, 
     dt = target.dtype
 
     def rows(t, name, n):  # [N, n, V] with every row the same distance apart
-        if t.dim() == 3 and n > 1 and N > 1 and t.stride(0) != n * t.stride(1):
-            raise ValueError(f"{name} must have evenly spaced rows")
-        if t.dim() != 3 or tuple(t.shape) != (N, n, V):
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+        if t.dtype != dt:
+            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
+        if t.shape != (N, n, V):
             raise ValueError(f"{name} must have shape {(N, n, V)}, got {tuple(t.shape)}")
-        step = t.stride(1) if n > 1 else t.stride(0)
-        flat = t.as_strided((N * n, V), (step, t.stride(2)))
-        return _rows(flat, name, dt, (N * n, V))
+        s0, s1, s2 = t.stride()
+        if (V > 1 and s2 != 1) or (n > 1 and N > 1 and s0 != n * s1):
+            raise ValueError(f"{name} must have contiguous, evenly spaced rows")
+        return t.data_ptr(), max(V, s1 if n > 1 else s0)  # of a single row: any step
 
     code = _dcode(target)
+    tok_p = _dev(tokens, "tokens", torch.int32, (N, D))
     t_p, t_s = rows(target, "target", D + 1)
     d_p, d_s = (None, V) if draft is None else rows(draft, "draft", D)
     if accepted is None:
-        accepted = torch.empty((N,), dtype=torch.int32, device=target.device)
+        accepted = tokens.new_empty((N,))
     if out_tokens is None:
-        out_tokens = torch.empty((N, D + 1), dtype=torch.int32, device=target.device)
+        out_tokens = tokens.new_empty((N, D + 1))
     _raise_on("shortconv_draft_accept", lib().shortconv_draft_accept(
-        code, V, N, D, t_p, t_s, d_p, d_s, _dev(tokens, "tokens", torch.int32, (N, D)),
+        code, V, N, D, t_p, t_s, d_p, d_s, tok_p,
         None if n_drafts is None else _dev(n_drafts, "n_drafts", torch.int32, (N,)),
         _dev(uniforms, "uniforms", torch.float32, (N, D + 1)),
         _dev(accepted, "accepted", torch.int32, (N,)),

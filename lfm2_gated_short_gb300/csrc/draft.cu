@@ -19,11 +19,14 @@
 #include "kernels.h"
 #include "launch.h"
 #include "shortconv.h"
+#include "tcgen05.cuh"
 #include "tma.cuh"
 
 namespace sc {
 
-constexpr int kDraftThreads = 512;
+constexpr int kDraftThreads = 256;
+constexpr int kDraftWarps = kDraftThreads / 32;
+constexpr int kMaxDraftCluster = 8;
 typedef unsigned long long u64;
 
 __device__ __forceinline__ float prob_of(const float *p) { return gld(p); }
@@ -31,9 +34,32 @@ __device__ __forceinline__ float prob_of(const __nv_bfloat16 *p) {
     return __bfloat162float(gld(p));
 }
 
-// trunc(2^40 clamp(p, 0, 1)); fmaxf makes a NaN 0.
-__device__ __forceinline__ u64 weight_of(float p) {
-    return __float2ull_rz(fminf(fmaxf(p, 0.0f), 1.0f) * 1099511627776.0f);
+// trunc(2^40 clamp(p, 0, 1)) = 2^20 hi + lo, hi and lo whole and below 2^20
+// (hi 2^20 for p = 1), as the bit patterns of 2^23 + hi and 2^23 + lo: adding
+// 2^23 rounded towards zero leaves a number's whole part in the low mantissa
+// bits, and what is left of 2^20 p after it is exact. Equal exponents make a
+// difference of patterns the difference of the numbers. A NaN saturates to 0.
+struct Weight {
+    int hi, lo;
+};
+__device__ __forceinline__ Weight weight_of(float saturated) {
+    const float x = saturated * 1048576.0f;
+    const float h = __fadd_rz(x, 8388608.0f);
+    const float l = __fmaf_rz(x - (h - 8388608.0f), 1048576.0f, 8388608.0f);
+    return {__float_as_int(h), __float_as_int(l)};
+}
+// (hi, lo) += max(weight(p) - weight(q), 0): truncation keeps the order of p and q.
+__device__ __forceinline__ void add_rest(float p, float q, int &hi, int &lo) {
+    p = __saturatef(p);
+    q = __saturatef(q);
+    const Weight wp = weight_of(p), wq = weight_of(q);
+    if (p > q) {
+        hi += wp.hi - wq.hi;
+        lo += wp.lo - wq.lo;
+    }
+}
+__device__ __forceinline__ u64 whole_of(int hi, int lo) {
+    return (u64)((long long)hi * 1048576 + lo);
 }
 
 // floor(total m / 2^31) for total < 2^62, m < 2^31.
@@ -41,19 +67,90 @@ __device__ __forceinline__ u64 scaled_mark(u64 total, u64 m) {
     return ((total >> 32) * m << 1) + (((total & 0xFFFFFFFFull) * m) >> 31);
 }
 
+// The kVec = 16 / sizeof(T) probabilities of a row from element t on (a
+// multiple of kVec), zeros past V. A row may start anywhere (an odd V moves every
+// row): the two aligned 16-byte words that hold them are loaded and shifted;
+// a word that reaches outside the row is read by elements.
 template <typename T>
-__global__ void __launch_bounds__(kDraftThreads)
-    k_draft_accept(int V, int D, const T *__restrict__ target, int64_t target_stride,
+struct Row16 {
+    static constexpr int kVec = 16 / sizeof(T);
+    const T *row;
+    int V, mis;  // bytes from the aligned word before the row's start
+
+    __device__ __forceinline__ Row16(const T *p, int v)
+        : row(p), V(v), mis((int)(reinterpret_cast<uintptr_t>(p) & 15)) {}
+
+    // Whether the words of [t, t + n) lie inside the row.
+    __device__ __forceinline__ bool inside(int t, int n) const {
+        return t + n + kVec <= V && (mis == 0 || t > 0);
+    }
+    __device__ __forceinline__ void fetch(int t, uint4 (&w)[2]) const {
+        const char *at = reinterpret_cast<const char *>(row + t) - mis;
+        w[0] = ld_stream(at);
+        if (mis) w[1] = ld_stream(at + 16);
+    }
+    __device__ __forceinline__ void unpack(const uint4 (&v)[2], float (&f)[kVec]) const {
+        uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
+        if (mis & 8) {  // mis is the same for the whole row
+#pragma unroll
+            for (int k = 0; k < 6; ++k) w[k] = w[k + 2];
+        }
+        if (mis & 4) {
+#pragma unroll
+            for (int k = 0; k < 5; ++k) w[k] = w[k + 1];
+        }
+        if (mis & 2) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (sizeof(T) == 4) {
+                f[k] = __uint_as_float(w[k]);
+            } else {
+                f[2 * k] = bf16_lo(w[k]);
+                f[2 * k + 1] = bf16_hi(w[k]);
+            }
+        }
+    }
+    // At the row's ends: element by element, zeros past V.
+    __device__ __forceinline__ void get(int t, float (&f)[kVec]) const {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) f[e] = t + e < V ? prob_of(row + t + e) : 0.0f;
+    }
+};
+
+__device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 up = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += up;
+    }
+    return v;
+}
+
+// A cluster of CTAs shares a sequence's row of V, one run of chunks each; a chunk is
+// one vector a thread. The sums of every (chunk, warp) stay in shared memory,
+// so the row is read once and then only the 32 vectors that hold the token again.
+// `sums` holds chunks * kDraftWarps entries.
+template <typename T>
+__global__ void __launch_bounds__(kDraftThreads, 4)
+    k_draft_accept(int V, int D, int chunks, const T *__restrict__ target, int64_t target_stride,
                    const T *__restrict__ draft, int64_t draft_stride,
                    const int32_t *__restrict__ tokens, const int32_t *__restrict__ n_drafts,
                    const float *__restrict__ uniforms, int32_t *__restrict__ accepted,
                    int32_t *__restrict__ out_tokens) {
-    constexpr int kWarps = kDraftThreads / 32;
-    __shared__ int s_a, s_n, s_pick;
-    __shared__ u64 s_sum[kWarps];
+    using R = Row16<T>;
+    constexpr int kVec = R::kVec;
+    extern __shared__ u64 sums[];
+    __shared__ int s_a, s_n;
+    __shared__ u64 s_warp[kDraftWarps];
+    __shared__ u64 s_total[2][kMaxDraftCluster];  // every CTA's sum, by pass
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t i = blockIdx.x;
+    cluster_arrive();  // every CTA of the cluster runs before one stores to another
+    const int C = (int)cluster_ctas(), rank = (int)cluster_ctarank();
+    const int64_t i = blockIdx.x / C;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const float *u = uniforms + i * (D + 1);
     int32_t *out = out_tokens + i * (D + 1);
@@ -61,22 +158,23 @@ __global__ void __launch_bounds__(kDraftThreads)
     if (warp == 0) {  // the first rejected draft
         int n = n_drafts ? gld(n_drafts + i) : D;
         bool bad = n < 0 || n > D;
-        if (bad && lane == 0) raise_error(SC_DEV_BAD_ACCEPTED);
+        if (bad && lane == 0 && rank == 0) raise_error(SC_DEV_BAD_ACCEPTED);
         int a = bad ? 0 : n;
         for (int j0 = 0; !bad && j0 < n; j0 += 32) {
             const int j = j0 + lane;
             bool ok = true, wrong = false;
             if (j < n) {
                 const int x = gld(tokens + i * D + j);
+                const float r = gld(u + j);
                 wrong = x < 0 || x >= V;
                 if (!wrong) {
                     const double p = prob_of(target + (i * (D + 1) + j) * target_stride + x);
                     const double q = draft ? prob_of(draft + (i * D + j) * draft_stride + x) : 1.0;
-                    ok = (double)gld(u + j) * q < p;
+                    ok = (double)r * q < p;
                 }
             }
             if (__any_sync(~0u, wrong)) {
-                if (lane == 0) raise_error(SC_DEV_BAD_TOKEN);
+                if (lane == 0 && rank == 0) raise_error(SC_DEV_BAD_TOKEN);
                 bad = true;
             }
             const unsigned no = __ballot_sync(~0u, !ok);
@@ -85,73 +183,141 @@ __global__ void __launch_bounds__(kDraftThreads)
         if (lane == 0) {
             s_a = bad ? -1 : a;
             s_n = n;
-            s_pick = -1;
         }
     }
     __syncthreads();
     const int a = s_a;
-    if (a < 0) {  // bad drafts: nothing accepted, no token
-        for (int j = tid; j <= D; j += kDraftThreads) gst(out + j, -1);
-        if (tid == 0) gst(accepted + i, 0);
+    cluster_wait();
+    if (a < 0) {  // bad drafts: nothing accepted, no token (every CTA of the cluster leaves)
+        if (rank == 0) {
+            for (int j = tid; j <= D; j += kDraftThreads) gst(out + j, -1);
+            if (tid == 0) gst(accepted + i, 0);
+        }
         return;
     }
-    const T *p = target + (i * (D + 1) + a) * target_stride;
-    const T *q = draft && a < s_n ? draft + (i * D + a) * draft_stride : nullptr;
+    const float r = gld(u + D);
+    const R p(target + (i * (D + 1) + a) * target_stride, V);
+    const bool with_q = draft && a < s_n;
+    const R q(with_q ? draft + (i * D + a) * draft_stride : p.row, V);
     const int sure = !draft && a < s_n ? gld(tokens + i * D + a) : -1;
     bool rest = a < s_n;
-    auto weight = [&](int t) -> u64 {
-        const u64 wp = weight_of(prob_of(p + t));
-        if (!rest) return wp;
-        const u64 wq = q ? weight_of(prob_of(q + t)) : t == sure ? 1ull << 40 : 0ull;
-        return wp > wq ? wp - wq : 0ull;
-    };
-    // Each warp owns a run of tokens.
-    const int per = ((V + kWarps - 1) / kWarps + 31) / 32 * 32;
-    const int t0 = min(V, warp * per), t1 = min(V, t0 + per);
-    u64 total = 0, before = 0, mine = 0;
+    constexpr int kStep = kDraftThreads * kVec;  // elements of a chunk
+    const int run = chunks * kStep;              // elements of a CTA
+    const int first = rank * run + tid * kVec;      // fits: V <= 2^22 and C <= 8
+    u64 total = 0, before = 0, here = 0;
     for (int pass = 0; pass < 2; ++pass) {  // the rest; the whole of p where nothing is left
-        mine = 0;
-        for (int t = t0 + lane; t < t1; t += 32) mine += weight(t);
+        u64 mine = 0;
+        const bool use_q = rest && with_q;
+        // One chunk's sum over the warp: at most 32 x kVec x 2^20 in hi, as much in lo.
+        auto store = [&](int c, int hi, int lo) {
+            const u64 s = whole_of(__reduce_add_sync(~0u, hi), __reduce_add_sync(~0u, lo));
+            if (lane == 0) sums[c * kDraftWarps + warp] = s;
+            mine += s;
+        };
+        auto values = [&](const float (&fp)[kVec], const float (&fq)[kVec], int t, int &hi, int &lo) {
+            hi = lo = 0;
 #pragma unroll
-        for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(~0u, mine, o);
-        if (lane == 0) s_sum[warp] = mine;
-        __syncthreads();
-        total = before = 0;
-        for (int k = 0; k < kWarps; ++k) {
-            if (k == warp) before = total;
-            total += s_sum[k];
+            for (int e = 0; e < kVec; ++e)
+                add_rest(fp[e], rest && t + e == sure ? 1.0f : fq[e], hi, lo);
+        };
+        constexpr int kAhead = 2;  // chunks loaded before the first is summed
+        for (int c = 0; c < chunks;) {
+            const int t = first + c * kStep, t0 = rank * run + c * kStep;
+            if (c + kAhead <= chunks && p.inside(t0, kAhead * kStep) &&
+                (!use_q || q.inside(t0, kAhead * kStep))) {
+                uint4 wp[kAhead][2], wq[kAhead][2];
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) {
+                    p.fetch(t + x * kStep, wp[x]);
+                    if (use_q) q.fetch(t + x * kStep, wq[x]);
+                }
+#pragma unroll
+                for (int x = 0; x < kAhead; ++x) {
+                    float fp[kVec], fq[kVec] = {};
+                    int hi, lo;
+                    p.unpack(wp[x], fp);
+                    if (use_q) q.unpack(wq[x], fq);
+                    values(fp, fq, t + x * kStep, hi, lo);
+                    store(c + x, hi, lo);
+                }
+                c += kAhead;
+            } else {
+                float fp[kVec], fq[kVec] = {};
+                int hi, lo;
+                p.get(t, fp);
+                if (use_q) q.get(t, fq);
+                values(fp, fq, t, hi, lo);
+                store(c, hi, lo);
+                ++c;
+            }
         }
+        if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
-        if (total > 0 || !rest) break;
+        here = 0;
+#pragma unroll
+        for (int k = 0; k < kDraftWarps; ++k) here += s_warp[k];
+        if (tid < C) st_cluster_u64(cluster_map(smem_addr(&s_total[pass][rank]), tid), here);
+        cluster_sync();
+        total = before = 0;
+        for (int k = 0; k < C; ++k) {
+            if (k == rank) before = total;
+            total += s_total[pass][k];
+        }
+        if (total > 0 || !rest) break;  // the same in every CTA
         rest = false;
     }
-    const float r = gld(u + D);
-    const u64 mark = scaled_mark(total, (u64)__float2ull_rz(fminf(fmaxf(r, 0.0f), 0.99999994f) * 2147483648.0f));
-    if (mark >= before && mark < before + mine) {  // this warp's run holds the token
-        u64 sum = before;
-        for (int c = t0; c < t1; c += 32) {
-            const int t = c + lane;
-            u64 inc = t < t1 ? weight(t) : 0;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const u64 up = __shfl_up_sync(~0u, inc, o);
-                if (lane >= o) inc += up;
-            }
-            const unsigned hit = __ballot_sync(~0u, sum + inc > mark);
-            if (hit) {
-                if (lane == 0) s_pick = c + __ffs(hit) - 1;
-                break;
-            }
-            sum += __shfl_sync(~0u, inc, 31);
+    if (rank == 0) {
+        if (tid == 0) {
+            if (total == 0) raise_error(SC_DEV_BAD_PROBS);
+            gst(accepted + i, a);
         }
+        for (int j = tid; j <= D; j += kDraftThreads)
+            if (j != a || total == 0) gst(out + j, j < a ? gld(tokens + i * D + j) : -1);
     }
-    __syncthreads();
-    if (tid == 0) {
-        if (total == 0) raise_error(SC_DEV_BAD_PROBS);
-        gst(accepted + i, a);
+    const u64 mark = scaled_mark(
+        total, (u64)__float2ull_rz(fminf(fmaxf(r, 0.0f), 0.99999994f) * 2147483648.0f));
+    if (warp != 0 || mark < before || mark >= before + here) return;
+    // This CTA's run holds the token: its (chunk, warp), then the vector.
+    u64 sum = before;
+    int at = -1;
+    for (int k0 = 0; k0 < chunks * kDraftWarps; k0 += 32) {  // kDraftWarps chunks end inside
+        const int k = k0 + lane;
+        const u64 inc = warp_scan(k < chunks * kDraftWarps ? sums[k] : 0, lane);
+        const unsigned hit = __ballot_sync(~0u, sum + inc > mark);
+        if (hit) {
+            const int h = __ffs(hit) - 1;
+            at = k0 + h;
+            const u64 up = __shfl_sync(~0u, inc, h > 0 ? h - 1 : 0);
+            if (h > 0) sum += up;
+            break;
+        }
+        sum += __shfl_sync(~0u, inc, 31);
     }
-    for (int j = tid; j <= D; j += kDraftThreads)
-        gst(out + j, j < a ? gld(tokens + i * D + j) : j == a ? s_pick : -1);
+    if (at < 0) return;  // cannot be: the run's sum holds the mark
+    const int t = rank * run + (at / kDraftWarps * kDraftThreads + at % kDraftWarps * 32 + lane) * kVec;
+    u64 w[kVec], mine = 0;
+    float fp[kVec], fq[kVec] = {};
+    p.get(t, fp);
+    if (rest && with_q) q.get(t, fq);
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+        int hi = 0, lo = 0;
+        add_rest(fp[e], rest && t + e == sure ? 1.0f : fq[e], hi, lo);
+        w[e] = whole_of(hi, lo);
+        mine += w[e];
+    }
+    const u64 inc = warp_scan(mine, lane);
+    const unsigned hit = __ballot_sync(~0u, sum + inc > mark);
+    if (hit && lane == __ffs(hit) - 1) {
+        u64 acc = sum + inc - mine;
+        int pick = t;
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            acc += w[e];
+            if (acc <= mark) pick = t + e + 1;
+        }
+        gst(out + a, pick);
+    }
 }
 
 template <typename T>
@@ -159,9 +325,14 @@ static cudaError_t launch_accept(int V, int N, int D, const void *target, int64_
                                  const void *draft, int64_t draft_stride, const int32_t *tokens,
                                  const int32_t *n_drafts, const float *uniforms, int32_t *accepted,
                                  int32_t *out_tokens, cudaStream_t stream) {
-    return launch_pdl(k_draft_accept<T>, dim3((unsigned)N), dim3(kDraftThreads), 0, stream, V, D,
-                      (const T *)target, target_stride, (const T *)draft, draft_stride, tokens,
-                      n_drafts, uniforms, accepted, out_tokens);
+    constexpr int kChunk = kDraftThreads * (16 / (int)sizeof(T));
+    int C = 1;  // CTAs of a sequence: no more than give each a whole chunk
+    while (C < kMaxDraftCluster && V > C * kChunk) C *= 2;
+    const int chunks = (V + C * kChunk - 1) / (C * kChunk);
+    return launch_pdl_cluster(k_draft_accept<T>, dim3((unsigned)(N * C)), dim3(kDraftThreads),
+                              (size_t)chunks * kDraftWarps * 8, stream, (unsigned)C, V, D, chunks,
+                              (const T *)target, target_stride, (const T *)draft, draft_stride,
+                              tokens, n_drafts, uniforms, accepted, out_tokens);
 }
 
 cudaError_t launch_draft_accept(int dtype, int V, int N, int D, const void *target,
