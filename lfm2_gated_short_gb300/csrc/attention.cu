@@ -38,6 +38,7 @@ constexpr int kKT = 64;            // keys of a tile
 constexpr int kOwnWarps = 4;       // consumer warps, 16 keys of a tile each
 constexpr int kOwnThreads = 32 * (kOwnWarps + 1);
 constexpr int kMaxCtas = 304;      // two CTAs on each of 152 SMs
+constexpr int kMaxPrefixCtas = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct AttnArgs {
@@ -46,7 +47,8 @@ struct AttnArgs {
     PageTable pt;
     const int32_t *slots;
     int N, D, G, Hkv, Dh;
-    int shared_keys;   // keys whose part the prefix kernel computes
+    int shared_keys;   // keys whose part k_prefix computes, if a sequence holds them all
+    const int *leader; // k_prefix's word on that: < 0 when none does (unused without a prefix)
     float scale_log2;  // scale * log2(e)
     bf16 *out;
     int64_t *cum;      // [N + 1] first own tile of each sequence
@@ -164,6 +166,8 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
+
+    if (a.shared_keys > 0 && gld(a.leader) < 0) a.shared_keys = 0;
 
     // The units of the call and the sequence that holds this CTA's first one.
     const int rows = a.D * a.G;
@@ -504,11 +508,19 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
     });
 }
 
-// A row is joined by Dh / 4 lanes, four columns each.
+}  // namespace sc
+
+#include "attention_prefix.cuh"
+
+namespace sc {
+
+// A row is joined by Dh / 4 lanes, four columns each: the prefix's parts, then its own.
 template <int DH>
-__global__ void __launch_bounds__(256) k_merge(AttnArgs a, int MR, int own_ctas) {
+__global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_ctas) {
     pdl_wait();
     pdl_launch_dependents();
+    AttnArgs &a = x.a;
+    if (a.shared_keys > 0 && gld(a.leader) < 0) a.shared_keys = 0;
     constexpr int L = DH / 4;
     const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
     const int c4 = threadIdx.x % L;
@@ -519,36 +531,52 @@ __global__ void __launch_bounds__(256) k_merge(AttnArgs a, int MR, int own_ctas)
     int slot;
     const int len = seq_len(a, i, &slot, false);
     if (len < 0) return;
-    const int T = own_tiles(a, len);
-    const int64_t U = gld(a.cum + a.N);
-    const int n_cta = (int)min((int64_t)own_ctas, max(U, (int64_t)1));
-    const int r = j * a.G + g, rt = r / MR, rr = r % MR;
-    const int RT = (a.D * a.G + MR - 1) / MR;
-    const int it = rt * a.Hkv + h;
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    auto add = [&](const float *part, int rows, int r) {
+        const float m = gld(part + rows * DH + r), l = gld(part + rows * DH + rows + r);
+        const float4 v = gld(reinterpret_cast<const float4 *>(part + r * DH) + c4);
+        if (m != m || top != top) {
+            top = __int_as_float(0x7FC00000);
+            return;
+        }
+        const float now = fmaxf(top, m), base = now == -INFINITY ? 0.0f : now;
+        const float f0 = exp2f(top - base), f1 = exp2f(m - base);
+        sum = sum * f0 + l * f1;
+        o.x = o.x * f0 + v.x * f1;
+        o.y = o.y * f0 + v.y * f1;
+        o.z = o.z * f0 + v.z * f1;
+        o.w = o.w * f0 + v.w * f1;
+        top = now;
+    };
+    if (a.shared_keys > 0) {
+        const int token = i * a.D + j, tile = token / x.tpt, r = token % x.tpt * a.G + g;
+        const int64_t w = (int64_t)(x.split ? tile : tile / 2) * a.Hkv + h;
+        const int c0 = share_of(w * x.T, x.U, x.n_cta);
+        const int c1 = share_of(w * x.T + x.T - 1, x.U, x.n_cta);
+        for (int c = c0; c <= c1; ++c) {
+            const float *part = x.part + ((w + c) * 2) * (int64_t)(kPR * (DH + 2));
+            if (x.split) {
+                add(part, kPR, r);
+                add(part + kPR * (DH + 2), kPR, r);
+            } else {
+                add(part + (tile & 1) * kPR * (DH + 2), kPR, r);
+            }
+        }
+    }
+    const int T = own_tiles(a, len);
     if (T > 0) {
+        const int64_t U = gld(a.cum + a.N);
+        const int n_cta = (int)min((int64_t)own_ctas, max(U, (int64_t)1));
+        const int r = j * a.G + g, rt = r / MR;
+        const int RT = (a.D * a.G + MR - 1) / MR;
+        const int it = rt * a.Hkv + h;
         const int64_t u0 = gld(a.cum + i) + (int64_t)it * T;
         const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
         if (c0 == c1 && a.shared_keys == 0) return;  // k_own wrote the row
         const int64_t w = (int64_t)i * RT * a.Hkv + it;
-        for (int c = c0; c <= c1 && top == top; ++c) {
-            const float *part = a.own_part + (w + c) * ((int64_t)MR * (DH + 2));
-            const float m = gld(part + MR * DH + rr), l = gld(part + MR * DH + MR + rr);
-            const float4 v = gld(reinterpret_cast<const float4 *>(part + rr * DH) + c4);
-            if (m != m) {
-                top = m;
-                break;
-            }
-            const float now = fmaxf(top, m), base = now == -INFINITY ? 0.0f : now;
-            const float f0 = exp2f(top - base), f1 = exp2f(m - base);
-            sum = sum * f0 + l * f1;
-            o.x = o.x * f0 + v.x * f1;
-            o.y = o.y * f0 + v.y * f1;
-            o.z = o.z * f0 + v.z * f1;
-            o.w = o.w * f0 + v.w * f1;
-            top = now;
-        }
+        for (int c = c0; c <= c1; ++c)
+            add(a.own_part + (w + c) * ((int64_t)MR * (DH + 2)), MR, r % MR);
     }
     if (top != top) return;  // a bad page: the row is not written
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
@@ -595,6 +623,25 @@ static cudaError_t map_pages(CUtensorMap *m, const void *ptr, const PageTable &p
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Queries [N*D, Hkv, G, Dh] in boxes of the G heads of `tpt` tokens of one kv
+// head, 64 columns, 128-byte swizzle; tokens past the last read as zeros.
+static cudaError_t map_queries(CUtensorMap *m, const PrefixArgs &x, const AttnShape &s) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const int G = x.a.G;
+    const cuuint64_t dims[4] = {(cuuint64_t)s.Dh, (cuuint64_t)G, (cuuint64_t)s.Hkv,
+                                (cuuint64_t)s.N * s.D};
+    const cuuint64_t strides[3] = {(cuuint64_t)s.Dh * 2, (cuuint64_t)G * s.Dh * 2,
+                                   (cuuint64_t)x.a.q_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)G, 1, (cuuint32_t)x.tpt};
+    const cuuint32_t es[4] = {1, 1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<bf16 *>(x.a.q), dims,
+                          strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 // Rows of an item: 16 hold up to 16 rows of a sequence and kv head, else 32.
 static int own_rows(const AttnShape &s) { return s.D * (s.Hq / s.Hkv) <= 16 ? 16 : 32; }
 
@@ -604,35 +651,74 @@ static size_t own_part_floats(const AttnShape &s) {
         (size_t)s.N * s.Hkv * (((size_t)s.D * (s.Hq / s.Hkv) + MR - 1) / MR);
     return (items + kMaxCtas) * MR * (s.Dh + 2);
 }
-static size_t cum_bytes(const AttnShape &s) { return ((size_t)s.N + 2) / 2 * 16; }
+// [N + 1] first tiles, then k_prefix's leader.
+static size_t cum_bytes(const AttnShape &s) { return ((size_t)s.N + 3) / 2 * 16; }
+
+// The prefix's work: everything but the pointers.
+static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count) {
+    PrefixArgs x = {};
+    const int G = s.Hq / s.Hkv;
+    x.P = s.shared_pages * page_size;
+    x.tpt = kPR / G;
+    x.n_tiles = (s.N * s.D + x.tpt - 1) / x.tpt;
+    x.split = x.n_tiles == 1;
+    const int keys = x.split ? 2 * kPK : kPK;
+    x.T = (x.P + keys - 1) / keys;
+    x.U = (int64_t)s.Hkv * (x.split ? 1 : (x.n_tiles + 1) / 2) * x.T;
+    const int ctas = sm_count < kMaxPrefixCtas ? sm_count : kMaxPrefixCtas;
+    x.n_cta = (int)(x.U < ctas ? x.U : ctas);
+    return x;
+}
+static size_t prefix_part_floats(const AttnShape &s) {
+    if (s.shared_pages == 0) return 0;
+    const PrefixArgs x = prefix_plan(s, 1, kMaxPrefixCtas);
+    const size_t items = (size_t)s.Hkv * (x.split ? 1 : (x.n_tiles + 1) / 2);
+    return 2 * (items + kMaxPrefixCtas) * kPR * (s.Dh + 2);
+}
 
 size_t attention_workspace_bytes(const AttnShape &s) {
-    return cum_bytes(s) + own_part_floats(s) * 4;
+    return cum_bytes(s) + (own_part_floats(s) + prefix_part_floats(s)) * 4;
+}
+
+template <typename F>
+static cudaError_t smem_opt_in(F kern, size_t bytes, std::atomic<unsigned long long> &done) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (done.load() & (1ull << dev))) return cudaSuccess;
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (e == cudaSuccess && dev < 64) done.fetch_or(1ull << dev);
+    return e;
 }
 
 template <int DH, int MT>
 static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                               int grid, cudaStream_t stream) {
     using C = OwnCfg<DH, MT>;
-    auto kern = k_own<DH, MT>;
     static std::atomic<unsigned long long> done{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    const cudaError_t e = smem_opt_in(k_own<DH, MT>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    if (!(done.load() >> (dev & 63) & 1)) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)C::kSmem);
-        if (e != cudaSuccess) return e;
-        done.fetch_or(1ull << (dev & 63));
-    }
-    return launch_pdl(kern, dim3((unsigned)grid), dim3(kOwnThreads), C::kSmem, stream, a, mk, mv);
+    return launch_pdl(k_own<DH, MT>, dim3((unsigned)grid), dim3(kOwnThreads), C::kSmem, stream, a,
+                      mk, mv);
+}
+
+template <int DH>
+static cudaError_t launch_prefix(const PrefixArgs &x, const CUtensorMap &mq, const CUtensorMap &mk,
+                                 const CUtensorMap &mv, cudaStream_t stream) {
+    using C = PfxCfg<DH>;
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = smem_opt_in(k_prefix<DH>, C::kSmem, done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(k_prefix<DH>, dim3((unsigned)x.n_cta), dim3(kPfxThreads), C::kSmem, stream, x,
+                      mq, mk, mv);
 }
 
 cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
                                     const void *k_pages, const void *v_pages, const PageTable &pt,
                                     const int32_t *slots, float scale, void *out,
                                     void *workspace, int sm_count, cudaStream_t stream) {
-    AttnArgs a;
+    PrefixArgs x = prefix_plan(s, pt.page_size, sm_count);
+    AttnArgs &a = x.a;
     a.q = (const bf16 *)q;
     a.q_stride = q_stride;
     a.pt = pt;
@@ -642,14 +728,31 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.G = s.Hq / s.Hkv;
     a.Hkv = s.Hkv;
     a.Dh = s.Dh;
-    a.shared_keys = 0;
+    a.shared_keys = x.P;
     a.scale_log2 = scale * kLog2e;
     a.out = (bf16 *)out;
     a.cum = (int64_t *)workspace;
+    x.leader = (int *)(a.cum + s.N + 1);
+    a.leader = x.leader;
     a.own_part = (float *)((char *)workspace + cum_bytes(s));
+    x.part = a.own_part + own_part_floats(s);
     CUtensorMap mk, mv;
+    cudaError_t e;
+    if (x.P > 0) {
+        CUtensorMap mq;
+        const int box = pt.page_size < kPK ? pt.page_size : kPK;
+        e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, box);
+        if (e != cudaSuccess) return e;
+        e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, box);
+        if (e != cudaSuccess) return e;
+        e = map_queries(&mq, x, s);
+        if (e != cudaSuccess) return e;
+        e = s.Dh == 64 ? launch_prefix<64>(x, mq, mk, mv, stream)
+                       : launch_prefix<128>(x, mq, mk, mv, stream);
+        if (e != cudaSuccess) return e;
+    }
     const int box = pt.page_size < kKT ? pt.page_size : kKT;
-    cudaError_t e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, box);
+    e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, box);
     if (e != cudaSuccess) return e;
     e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, box);
     if (e != cudaSuccess) return e;
@@ -664,8 +767,8 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     if (e != cudaSuccess) return e;
     const int64_t threads = (int64_t)s.N * s.D * s.Hq * (s.Dh / 4);
     const dim3 blocks((unsigned)((threads + 255) / 256));
-    return s.Dh == 64 ? launch_pdl(k_merge<64>, blocks, dim3(256), 0, stream, a, MR, grid)
-                      : launch_pdl(k_merge<128>, blocks, dim3(256), 0, stream, a, MR, grid);
+    return s.Dh == 64 ? launch_pdl(k_merge<64>, blocks, dim3(256), 0, stream, x, MR, grid)
+                      : launch_pdl(k_merge<128>, blocks, dim3(256), 0, stream, x, MR, grid);
 }
 
 cudaError_t take_error_attention(cudaStream_t stream, unsigned int *sum) {

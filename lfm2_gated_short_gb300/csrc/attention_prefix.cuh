@@ -1,0 +1,462 @@
+// attention_prefix.cuh -- the shared prefix's part of attention.cu, on the
+// tcgen05 tensor cores.
+//
+// Every row of the call sees the prefix's keys, so for one kv head the rows
+// of all sequences (N D G of them) are one query matrix against one K and V:
+// tiles of 128 rows by 128 keys, S = Q K^T and O += P V with accumulators in
+// TMEM, P written back to TMEM as the second product's bf16 operand.
+//
+// A CTA runs two streams of tiles, one warpgroup of softmax threads each
+// (thread = row = TMEM lane), so that one stream's exponentials run while the
+// tensor cores work for the other:
+//   more than 128 rows a head: the streams are two row tiles that share every
+//     K and V tile (halves the traffic from L2);
+//   at most 128 rows: the same rows on alternate key tiles.
+// One thread issues all MMAs in the order QK(t+1) after PV(t) of a stream; they
+// execute in that order, so S(t+1) may overwrite P(t)'s columns and S(t+1)
+// ready means PV(t) done. O is rescaled only when a row's maximum rose by more
+// than 2^8 since the last time: weights then stay below 2^8, exact enough in
+// the fp32 sums and bf16's exponent range.
+#pragma once
+
+namespace sc {
+
+constexpr int kPR = 128;                 // rows of a tile
+constexpr int kPK = 128;                 // keys of a tile
+constexpr int kPfxThreads = 320;         // 2 x 4 softmax warps, producer, MMA
+constexpr float kRescaleLog2 = 8.0f;
+
+struct PrefixArgs {
+    AttnArgs a;
+    int P;          // prefix keys
+    int tpt;        // tokens of a row tile: 128 / G
+    int n_tiles;    // row tiles of a kv head
+    int split;      // 1: the two streams take alternate key tiles of one row tile
+    int T;          // units of an item: key tiles, or pairs of them with split
+    int64_t U;      // units of the call
+    int n_cta;
+    float *part;    // [2 (items + CTAs)] parts of 128 rows: O [128][Dh], m [128], l [128]
+    int *leader;    // the listed sequence whose table names the prefix, or -1
+};
+
+template <int DH>
+struct PfxCfg {
+    static constexpr int NB = DH / 64;
+    static constexpr uint32_t kTile = kPK * 128 * NB;  // K, V or Q tile: 16 or 32 KB
+    static constexpr uint32_t kBlk = kPK * 128;        // its 64-column block
+    static constexpr int kSt = DH == 64 ? 5 : 2;       // tiles of the K and of the V ring
+    static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * kSt) * kTile;
+    static constexpr int kSlot = kPR * (DH + 2);
+};
+
+// tcgen05 pieces that only this kernel uses.
+
+// D[tmem] (+)= A[tmem] * B[smem], one 128 x N x 16 step; issued by one thread.
+__device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Descriptor of an MN-major 128-byte-swizzled tile (rows = K, 64 contiguous
+// MN values a row): 64-wide MN blocks lbo bytes apart, groups of 8 rows 1024.
+__device__ __forceinline__ uint64_t sdesc_mn128(uint32_t saddr, uint32_t lbo) {
+    uint64_t d = (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(lbo >> 4) << 16;
+    d |= (uint64_t)(1024 >> 4) << 32;
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+
+// 32 columns of this thread's TMEM lane; valid after tmem_ld_wait().
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(
+            taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// After tmem_ld_wait(): no use of r moves above this point.
+template <int N>
+__device__ __forceinline__ void regs_ready(uint32_t (&r)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+struct PfxBars {
+    uint64_t kfull[8], kempty[8], vfull[8], vempty[8];
+    uint64_t qfull, qempty;
+    uint64_t sfull[2], pready[2], ofull[2], done;
+    uint32_t tmem;
+    int leader;
+    volatile int bad;
+};
+
+template <int DH>
+__global__ void __launch_bounds__(kPfxThreads, 1)
+    k_prefix(PrefixArgs x, const __grid_constant__ CUtensorMap mq,
+             const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+    using C = PfxCfg<DH>;
+    constexpr int ST = C::kSt;
+    const AttnArgs &a = x.a;
+    extern __shared__ unsigned char raw[];
+    __shared__ PfxBars b;
+    const uint32_t raw_a = smem_addr(raw);
+    unsigned char *base = raw + (((raw_a + 1023u) & ~1023u) - raw_a);
+    const uint32_t q_a = smem_addr(base), k_a = q_a + 2 * C::kTile, v_a = k_a + ST * C::kTile;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int s = 0; s < ST; ++s) {
+            mbar_init(&b.kfull[s], 1);
+            mbar_init(&b.kempty[s], 1);
+            mbar_init(&b.vfull[s], 1);
+            mbar_init(&b.vempty[s], 1);
+        }
+        mbar_init(&b.qfull, 1);
+        mbar_init(&b.qempty, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&b.sfull[s], 1);
+            mbar_init(&b.pready[s], 4);
+            mbar_init(&b.ofull[s], 1);
+        }
+        mbar_init(&b.done, 1);
+        b.leader = a.N;
+        b.bad = 0;
+        mbar_fence_init();
+    }
+    if (warp == 8 && lane == 0) {
+        tma_prefetch_map(&mq);
+        tma_prefetch_map(&mk);
+        tma_prefetch_map(&mv);
+    }
+    if (warp == 9) tmem_alloc(&b.tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = b.tmem;
+    pdl_wait();
+    pdl_launch_dependents();
+    // The first listed sequence that holds the whole prefix names its pages.
+    for (int i = tid; i < a.N; i += kPfxThreads) {
+        int slot;
+        if (seq_len(a, i, &slot, false) >= x.P) {
+            atomicMin(&b.leader, i);
+            break;
+        }
+    }
+    __syncthreads();
+    const int leader = b.leader;
+    if (blockIdx.x == 0 && tid == 0) gst(x.leader, leader < a.N ? leader : -1);
+
+    const int64_t u0 = share_begin(blockIdx.x, x.U, x.n_cta);
+    const int64_t u1 = leader < a.N ? share_begin(blockIdx.x + 1, x.U, x.n_cta) : u0;
+    const int per = x.split ? 2 : 1;  // key tiles of a unit
+    // f(head, first row tile, first unit, units, item) for each item piece of the CTA.
+    auto walk = [&](auto &&f) {
+        for (int64_t u = u0; u < u1;) {
+            const int64_t w = u / x.T;
+            const int t0 = (int)(u % x.T), n = (int)min((int64_t)(x.T - t0), u1 - u);
+            if (!f((int)(w % a.Hkv), (int)(w / a.Hkv) * (x.split ? 1 : 2), t0, n, w)) return;
+            u += n;
+        }
+    };
+
+    if (warp == 8) {  // ---------------------------------------------------- producer
+        const int ps = a.pt.page_size;
+        const int box = min(ps, kPK), nb = kPK / box;
+        const int n_box = x.P / box;
+        int slot = 0;
+        if (u0 < u1) seq_len(a, leader, &slot, false);
+        const int32_t *row = a.pt.table + (int64_t)slot * a.pt.max_pages;
+        uint32_t gk = 0, gv = 0, items = 0;
+        bool ok = true;
+        // Tile `kt` of the prefix into the ring; the boxes past the prefix's end
+        // are not read, and V's rows there are zeroed (their weights are 0).
+        auto load = [&](const CUtensorMap *m, uint64_t *full, uint64_t *empty, uint32_t ring,
+                        uint32_t &g, int h, int kt, bool is_v) {
+            const uint32_t s = g % ST;
+            if (g >= ST && !mbar_wait_bounded(&empty[s], (g / ST - 1) & 1u)) {
+                raise_error(SC_DEV_TIMEOUT);
+                return ok = false;
+            }
+            const int boxes = max(0, min(nb, n_box - kt * nb));
+            const uint32_t dst = ring + s * C::kTile;
+            if (is_v && boxes < nb) {
+                unsigned char *at = base + (dst - q_a);
+                for (int r = boxes * box * 8 + lane; r < kPK * 8; r += 32)
+#pragma unroll
+                    for (int c = 0; c < C::NB; ++c)
+                        *reinterpret_cast<uint4 *>(at + c * C::kBlk + r * 16) =
+                            make_uint4(0u, 0u, 0u, 0u);
+                fence_proxy_async_smem();
+            }
+            int id = 0;
+            bool bad = false;
+            if (lane < boxes) {
+                id = gld(row + (int64_t)(kt * nb + lane) * box / ps);
+                bad = id < 0 || id >= a.pt.n_pages;
+                if (bad) id = 0;
+            }
+            bad = __any_sync(~0u, bad);
+            if (lane == 0) {
+                if (bad) {
+                    raise_error(SC_DEV_BAD_PAGE);
+                    b.bad = 1;
+                }
+                mbar_arrive_expect_tx(&full[s], (uint32_t)boxes * box * DH * 2);
+            }
+            __syncwarp();
+            if (lane < boxes) {
+                const int key = id * ps + (int)((int64_t)(kt * nb + lane) * box % ps);
+#pragma unroll
+                for (int c = 0; c < C::NB; ++c)
+                    tma_load_3d(dst + c * C::kBlk + lane * box * 128, m, &full[s], c * 64, h, key);
+            }
+            ++g;
+            return true;
+        };
+        walk([&](int h, int rt, int t0, int n, int64_t) {
+            if (items > 0 && !mbar_wait_bounded(&b.qempty, (items - 1) & 1u)) {
+                raise_error(SC_DEV_TIMEOUT);
+                return ok = false;
+            }
+            ++items;
+            if (lane == 0) {
+                const int tiles = x.split || rt + 1 >= x.n_tiles ? 1 : 2;
+                mbar_arrive_expect_tx(&b.qfull, (uint32_t)tiles * x.tpt * a.G * DH * 2);
+                for (int s = 0; s < tiles; ++s)
+                    for (int c = 0; c < C::NB; ++c)
+                        tma_load_4d(q_a + s * C::kTile + c * C::kBlk, &mq, &b.qfull, c * 64, 0, h,
+                                    (rt + s) * x.tpt);
+            }
+            for (int t = -1; t < n; ++t) {
+                if (t + 1 < n)
+                    for (int k = 0; k < per; ++k)
+                        if (!load(&mk, b.kfull, b.kempty, k_a, gk, h, (t0 + t + 1) * per + k, false))
+                            return false;
+                if (t >= 0)
+                    for (int k = 0; k < per; ++k)
+                        if (!load(&mv, b.vfull, b.vempty, v_a, gv, h, (t0 + t) * per + k, true))
+                            return false;
+            }
+            return true;
+        });
+        // No copy and no MMA's arrival may be in flight when the CTA leaves.
+        if (items > 0) mbar_wait_bounded(&b.qfull, (items - 1) & 1u);
+        for (uint32_t c = gk > ST ? gk - ST : 0; c < gk; ++c)
+            mbar_wait_bounded(&b.kfull[c % ST], (c / ST) & 1u);
+        for (uint32_t c = gv > ST ? gv - ST : 0; c < gv; ++c)
+            mbar_wait_bounded(&b.vfull[c % ST], (c / ST) & 1u);
+    } else if (warp == 9) {  // ------------------------------------------------- MMA issue
+        if (lane == 0) {
+            constexpr uint32_t idq = idesc_bf16_f32(kPR, kPK);
+            constexpr uint32_t idv = idesc_bf16_f32(kPR, DH) | (1u << 16);  // B is MN-major
+            uint32_t gk = 0, gv = 0, items = 0, np[2] = {0, 0};
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                if (mbar_wait_bounded(bar, parity)) return true;
+                raise_error(SC_DEV_TIMEOUT);
+                return false;
+            };
+            // S of stream s = Q K^T with the K tile in ring position g.
+            auto qk = [&](int s, uint32_t g) {
+                if (!wait(&b.kfull[g % ST], (g / ST) & 1u)) return false;
+                tc_fence_after();
+                const uint32_t qt = q_a + (x.split ? 0 : s) * C::kTile;
+                const uint32_t kt = k_a + (g % ST) * C::kTile;
+#pragma unroll
+                for (int j = 0; j < DH / 16; ++j)
+                    mma_bf16(tmem + s * kPK, sdesc_k128(qt + (j / 4) * C::kBlk) + 2 * (j % 4),
+                             sdesc_k128(kt + (j / 4) * C::kBlk) + 2 * (j % 4), idq, j != 0);
+                mma_commit(&b.sfull[s]);
+                return true;
+            };
+            walk([&](int h, int rt, int t0, int n, int64_t) {
+                const int streams = x.split || rt + 1 < x.n_tiles ? 2 : 1;
+                if (!wait(&b.qfull, items & 1u)) return false;
+                ++items;
+                auto free_k = [&](int s, uint32_t g) {  // the tile's last reader is issued
+                    if (x.split || s == streams - 1) mma_commit(&b.kempty[g % ST]);
+                };
+                for (int s = 0; s < streams; ++s) {
+                    const uint32_t g = gk + (x.split ? s : 0);
+                    if (!qk(s, g)) return false;
+                    free_k(s, g);
+                }
+                gk += per;
+                for (int t = 0; t < n; ++t) {
+                    for (int s = 0; s < streams; ++s) {
+                        const uint32_t g = gv + (x.split ? s : 0);
+                        if (!wait(&b.pready[s], np[s] & 1u)) return false;
+                        ++np[s];
+                        if (!wait(&b.vfull[g % ST], (g / ST) & 1u)) return false;
+                        tc_fence_after();
+                        const uint32_t vt = v_a + (g % ST) * C::kTile;
+#pragma unroll
+                        for (int j = 0; j < kPK / 16; ++j)
+                            mma_bf16_ts(tmem + 2 * kPK + s * DH, tmem + s * kPK + j * 8,
+                                        sdesc_mn128(vt + j * 2048, C::kBlk), idv, (t | j) != 0);
+                        if (x.split || s == streams - 1) mma_commit(&b.vempty[g % ST]);
+                        if (t + 1 < n) {
+                            const uint32_t gn = gk + (x.split ? s : 0);
+                            if (!qk(s, gn)) return false;
+                            free_k(s, gn);
+                        } else {
+                            mma_commit(&b.ofull[s]);
+                        }
+                    }
+                    gv += per;
+                    if (t + 1 < n) gk += per;
+                    if (t + 2 == n || n == 1) mma_commit(&b.qempty);  // the item's last S is issued
+                }
+                return true;
+            });
+            mma_commit(&b.done);  // no MMA may still write TMEM when it is freed
+            mbar_wait_bounded(&b.done, 0);
+        }
+        __syncwarp();
+    } else {  // ------------------------------------------------------------- softmax
+        const int s = warp >> 2, r = tid & 127;  // stream, row = TMEM lane
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
+        const uint32_t st = tmem + lane_base + s * kPK, ot = tmem + lane_base + 2 * kPK + s * DH;
+        uint32_t ns = 0, no = 0;
+        bool dead = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            if (!dead && !mbar_wait_bounded(bar, parity)) {
+                raise_error(SC_DEV_TIMEOUT);
+                dead = true;  // no more waits: the rest runs through on what is there
+            }
+            __syncwarp();
+            tc_fence_after();
+        };
+        walk([&](int h, int rt, int t0, int n, int64_t w) {
+            const int tile = x.split ? rt : rt + s;
+            if (tile >= x.n_tiles) return true;  // the second stream has no rows
+            // Keys of the prefix that this thread's row sees.
+            const int64_t token = (int64_t)tile * x.tpt + r / a.G;
+            int limit = 0;
+            if (r < x.tpt * a.G && token < (int64_t)a.N * a.D) {
+                int slot;
+                const int i = (int)(token / a.D), j = (int)(token % a.D);
+                limit = min(x.P, max(0, seq_len(a, i, &slot, false) - a.D + j + 1));
+            }
+            float m = -INFINITY, l = 0.0f;
+            for (int t = 0; t < n; ++t) {
+                const int key0 = ((t0 + t) * per + (x.split ? s : 0)) * kPK;
+                wait(&b.sfull[s], ns & 1u);
+                ++ns;
+                uint32_t v[kPK];
+#pragma unroll
+                for (int c = 0; c < kPK / 32; ++c) tmem_ld32(st + c * 32, v + c * 32);
+                tmem_ld_wait();
+                regs_ready(v);
+                if (key0 + kPK > limit) {
+#pragma unroll
+                    for (int c = 0; c < kPK; ++c)
+                        if (key0 + c >= limit) v[c] = 0xFF800000u;  // -inf
+                }
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int c = 0; c < kPK; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(v[c]));
+                const float now =
+                    fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                const bool rise = now > m + kRescaleLog2 || m == -INFINITY;
+                if (__any_sync(~0u, rise && now > m)) {
+                    const float to = rise ? fmaxf(m, now) : m;
+                    const float f = to == -INFINITY ? 1.0f : ex2(m - to);
+                    m = to;
+                    l *= f;
+                    if (t > 0) {  // S ready: the product before it is done, O is at rest
+#pragma unroll
+                        for (int c = 0; c < DH / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld32(ot + c * 32, o);
+                            tmem_ld_wait();
+                            regs_ready(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st32(ot + c * 32, o);
+                        }
+                    }
+                }
+                const float off = m == -INFINITY ? 0.0f : -m;
+                float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < kPK / 2; ++c) {
+                    const float e0 = ex2(fmaf(__uint_as_float(v[2 * c]), a.scale_log2, off));
+                    const float e1 = ex2(fmaf(__uint_as_float(v[2 * c + 1]), a.scale_log2, off));
+                    sum[0] += e0;
+                    sum[1] += e1;
+                    v[c] = pack_bf16(e0, e1);
+                }
+                l += sum[0] + sum[1];
+                tmem_st32(st, v);
+                tmem_st32(st + 32, v + 32);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&b.pready[s]);
+            }
+            wait(&b.ofull[s], no & 1u);
+            ++no;
+            float *part = x.part + ((w + blockIdx.x) * 2 + s) * C::kSlot;
+#pragma unroll
+            for (int c = 0; c < DH / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld32(ot + c * 32, o);
+                tmem_ld_wait();
+                regs_ready(o);
+#pragma unroll
+                for (int e = 0; e < 32; e += 4)
+                    gst(reinterpret_cast<uint4 *>(part + r * DH + c * 32 + e),
+                        make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]));
+            }
+            // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
+            gst(part + kPR * DH + r, b.bad ? __int_as_float(0x7FC00000) : m);
+            gst(part + kPR * DH + kPR + r, l);
+            tc_fence_before();  // O was read before the next item's first P is announced
+            return true;
+        });
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace sc
