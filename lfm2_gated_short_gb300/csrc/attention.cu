@@ -89,6 +89,42 @@ __device__ __forceinline__ int own_tiles(const AttnArgs &a, int len) {
     return len > a.shared_keys ? (len - a.shared_keys + kKT - 1) / kKT : 0;
 }
 
+// A producer warp's page ids: the table entries of `nb` boxes (of `box` tokens,
+// nb a divisor of 32) a tile, tile after tile. Lane k holds the page of box b0 + k;
+// the next 32 are in flight, so that a tile waits for no table entry.
+struct PageIds {
+    const int32_t *row;
+    int shift, last, b0, at, cur, nxt;  // shift: log2 of the boxes of a page
+
+    // From box b on; boxes past `last_box` repeat it.
+    __device__ __forceinline__ void start(const int32_t *table_row, int boxes_of_page, int b,
+                                          int last_box) {
+        row = table_row;
+        shift = 31 - __clz(boxes_of_page);
+        last = last_box;
+        b0 = b;
+        at = 0;
+        cur = load(b0);
+        nxt = load(b0 + 32);
+    }
+    __device__ __forceinline__ int load(int b) const {
+        return gld(row + (min(b + (int)(threadIdx.x & 31), last) >> shift));
+    }
+    // The tile's first box, and lane k's page of its k-th box.
+    __device__ __forceinline__ int box() const { return b0 + at; }
+    __device__ __forceinline__ int page() const {
+        return __shfl_sync(~0u, cur, (at + threadIdx.x) & 31);
+    }
+    __device__ __forceinline__ void next(int nb) {
+        at += nb;
+        if (at < 32) return;
+        at = 0;
+        b0 += 32;
+        cur = nxt;
+        nxt = load(b0 + 32);
+    }
+};
+
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -240,24 +276,18 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
         const int box = min(ps, kKT), nb = kKT / box;  // keys of a box, boxes of a tile
         uint32_t g = 0;
         walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
-            const int32_t *row = a.pt.table + (int64_t)slot * a.pt.max_pages;
-            // Lane b holds the page of box b0 + b of the item; one batch ahead is in flight.
+            PageIds ids;
             const int last = (len - 1) / box;
-            auto ids = [&](int b0) {
-                const int b = min(b0 + lane, last);
-                return gld(row + (int64_t)b * box / ps);
-            };
-            int b0 = a.shared_keys / box + t0 * nb;
-            int cur = ids(b0), nxt = ids(b0 + 32);
-            int at = 0;
+            ids.start(a.pt.table + (int64_t)slot * a.pt.max_pages, ps / box,
+                      a.shared_keys / box + t0 * nb, last);
             for (int t = 0; t < n; ++t, ++g) {
                 const uint32_t s = g % ST;
                 if (g >= ST && !mbar_wait_bounded(&s_empty[s], (g / ST - 1) & 1u)) {
                     raise_error(SC_DEV_TIMEOUT);
                     return false;
                 }
-                const int boxes = min(nb, last + 1 - (b0 + at));
-                int id = __shfl_sync(~0u, cur, (at + lane) & 31);
+                const int boxes = min(nb, last + 1 - ids.box());
+                int id = ids.page();
                 bool bad = lane < boxes && (id < 0 || id >= a.pt.n_pages);
                 if (bad) id = 0;
                 bad = __any_sync(~0u, bad);
@@ -268,7 +298,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
                 }
                 __syncwarp();
                 if (lane < boxes) {
-                    const int key = id * ps + (int)((int64_t)(b0 + at + lane) * box % ps);
+                    const int key = id * ps + (ids.box() + lane) * box % ps;
                     const uint32_t d = ring_a + s * C::kStage + lane * box * 128;
 #pragma unroll
                     for (int c = 0; c < C::NB; ++c) {
@@ -276,13 +306,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
                         tma_load_3d(d + (C::NB + c) * C::kBlk, &mv, &s_full[s], c * 64, h, key);
                     }
                 }
-                at += nb;
-                if (at >= 32) {
-                    at = 0;
-                    b0 += 32;
-                    cur = nxt;
-                    nxt = ids(b0 + 32);
-                }
+                ids.next(nb);
             }
             return true;
         });

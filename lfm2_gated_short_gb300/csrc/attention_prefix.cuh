@@ -12,9 +12,12 @@
 //   more than 128 rows a head: the streams are two row tiles that share every
 //     K and V tile (halves the traffic from L2);
 //   at most 128 rows: the same rows on alternate key tiles.
-// One thread issues all MMAs in the order QK(t+1) after PV(t) of a stream; they
-// execute in that order, so S(t+1) may overwrite P(t)'s columns and S(t+1)
-// ready means PV(t) done. O is rescaled only when a row's maximum rose by more
+// The streams' tiles are numbered in turn (a0 b0 a1 b1 ..), tile n's S and P in
+// TMEM buffer n % kBufs. One thread issues QK(n) once PV(n - kBufs), the buffer's
+// last reader, is done; another issues PV(n) once P(n) is there (issuing and
+// signalling a tile's two products takes one thread as long as the products).
+// With three buffers (Dh = 64) a stream's next S is ready when its softmax ends; with
+// Dh = 128 O leaves room for two. O is rescaled only when a row's maximum rose by more
 // than 2^8 since the last time: weights then stay below 2^8, exact enough in
 // the fp32 sums and bf16's exponent range.
 #pragma once
@@ -23,7 +26,7 @@ namespace sc {
 
 constexpr int kPR = 128;                 // rows of a tile
 constexpr int kPK = 128;                 // keys of a tile
-constexpr int kPfxThreads = 320;         // 2 x 4 softmax warps, producer, MMA
+constexpr int kPfxThreads = 384;         // 2 x 4 softmax warps; producer, QK, PV, an idle warp
 constexpr float kRescaleLog2 = 8.0f;
 
 struct PrefixArgs {
@@ -45,11 +48,27 @@ struct PfxCfg {
     static constexpr uint32_t kTile = kPK * 128 * NB;  // K, V or Q tile: 16 or 32 KB
     static constexpr uint32_t kBlk = kPK * 128;        // its 64-column block
     static constexpr int kSt = DH == 64 ? 5 : 2;       // tiles of the K and of the V ring
+    static constexpr int kBufs = DH == 64 ? 3 : 2;     // S and P buffers of 128 columns
+    static constexpr int kOCol = kBufs * kPK;          // O of the streams after them
+    static_assert(kOCol + 2 * DH <= 512, "TMEM");
     static constexpr size_t kSmem = 1024 + (size_t)(2 + 2 * kSt) * kTile;
     static constexpr int kSlot = kPR * (DH + 2);
 };
 
 // tcgen05 pieces that only this kernel uses.
+
+// True in one lane of the warp. Behind this branch, unlike behind a comparison of
+// the lane number, the compiler keeps addresses and descriptors in the uniform
+// registers that tcgen05.mma takes: 32 cycles a 128 x 64 x 16 step instead of 45.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(e));
+    return e != 0;
+}
 
 // D[tmem] (+)= A[tmem] * B[smem], one 128 x N x 16 step; issued by one thread.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
@@ -110,16 +129,54 @@ __device__ __forceinline__ void regs_ready(uint32_t (&r)[N]) {
     for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
 }
 
+// Registers of the calling warpgroup's threads from here on. The launch has
+// 384 x 168; 256 x 216 + 128 x 72 is as many. (The checked stores of the
+// bounds-checked build call a function, which needs the launch's own split.)
+template <int N>
+__device__ __forceinline__ void more_regs() {
+#ifndef SC_BOUNDS_CHECK
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+#endif
+}
+template <int N>
+__device__ __forceinline__ void fewer_regs() {
+#ifndef SC_BOUNDS_CHECK
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+#endif
+}
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
+struct RingPos {
+    uint32_t i, phase;
+    __device__ __forceinline__ void next(uint32_t n) {
+        if (++i == n) {
+            i = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 struct PfxBars {
     uint64_t kfull[8], kempty[8], vfull[8], vempty[8];
     uint64_t qfull, qempty;
-    uint64_t sfull[2], pready[2], ofull[2], done;
+    uint64_t sfull[3], pready[3], pvdone[3];  // of the S and P buffers
+    uint64_t done;                            // every MMA of the CTA
     uint32_t tmem;
     int leader;
     volatile int bad;
@@ -147,12 +204,12 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
         }
         mbar_init(&b.qfull, 1);
         mbar_init(&b.qempty, 1);
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < 3; ++s) {
             mbar_init(&b.sfull[s], 1);
             mbar_init(&b.pready[s], 4);
-            mbar_init(&b.ofull[s], 1);
+            mbar_init(&b.pvdone[s], 1);
         }
-        mbar_init(&b.done, 1);
+        mbar_init(&b.done, 2);
         b.leader = a.N;
         b.bad = 0;
         mbar_fence_init();
@@ -194,7 +251,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
         }
     };
 
-    if (warp == 8) {  // ---------------------------------------------------- producer
+    if (warp == 11) {
+        fewer_regs<72>();
+    } else if (warp == 8) {  // --------------------------------------------- producer
+        fewer_regs<72>();
         const int ps = a.pt.page_size;
         const int box = min(ps, kPK), nb = kPK / box;
         const int n_box = x.P / box;
@@ -203,16 +263,16 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
         const int32_t *row = a.pt.table + (int64_t)slot * a.pt.max_pages;
         uint32_t gk = 0, gv = 0, items = 0;
         bool ok = true;
-        // Tile `kt` of the prefix into the ring; the boxes past the prefix's end
+        // The prefix's next tile into the ring; the boxes past the prefix's end
         // are not read, and V's rows there are zeroed (their weights are 0).
         auto load = [&](const CUtensorMap *m, uint64_t *full, uint64_t *empty, uint32_t ring,
-                        uint32_t &g, int h, int kt, bool is_v) {
+                        uint32_t &g, PageIds &ids, int h, bool is_v) {
             const uint32_t s = g % ST;
             if (g >= ST && !mbar_wait_bounded(&empty[s], (g / ST - 1) & 1u)) {
                 raise_error(SC_DEV_TIMEOUT);
                 return ok = false;
             }
-            const int boxes = max(0, min(nb, n_box - kt * nb));
+            const int boxes = max(0, min(nb, n_box - ids.box()));
             const uint32_t dst = ring + s * C::kTile;
             if (is_v && boxes < nb) {
                 unsigned char *at = base + (dst - q_a);
@@ -223,13 +283,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                             make_uint4(0u, 0u, 0u, 0u);
                 fence_proxy_async_smem();
             }
-            int id = 0;
-            bool bad = false;
-            if (lane < boxes) {
-                id = gld(row + (int64_t)(kt * nb + lane) * box / ps);
-                bad = id < 0 || id >= a.pt.n_pages;
-                if (bad) id = 0;
-            }
+            int id = ids.page();
+            bool bad = lane < boxes && (id < 0 || id >= a.pt.n_pages);
+            if (bad) id = 0;
             bad = __any_sync(~0u, bad);
             if (lane == 0) {
                 if (bad) {
@@ -240,14 +296,16 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             }
             __syncwarp();
             if (lane < boxes) {
-                const int key = id * ps + (int)((int64_t)(kt * nb + lane) * box % ps);
+                const int key = id * ps + (ids.box() + lane) * box % ps;
 #pragma unroll
                 for (int c = 0; c < C::NB; ++c)
                     tma_load_3d(dst + c * C::kBlk + lane * box * 128, m, &full[s], c * 64, h, key);
             }
             ++g;
+            ids.next(nb);
             return true;
         };
+        PageIds kids, vids;
         walk([&](int h, int rt, int t0, int n, int64_t) {
             if (items > 0 && !mbar_wait_bounded(&b.qempty, (items - 1) & 1u)) {
                 raise_error(SC_DEV_TIMEOUT);
@@ -262,15 +320,16 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                         tma_load_4d(q_a + s * C::kTile + c * C::kBlk, &mq, &b.qfull, c * 64, 0, h,
                                     (rt + s) * x.tpt);
             }
-            for (int t = -1; t < n; ++t) {
-                if (t + 1 < n)
-                    for (int k = 0; k < per; ++k)
-                        if (!load(&mk, b.kfull, b.kempty, k_a, gk, h, (t0 + t + 1) * per + k, false))
-                            return false;
-                if (t >= 0)
-                    for (int k = 0; k < per; ++k)
-                        if (!load(&mv, b.vfull, b.vempty, v_a, gv, h, (t0 + t) * per + k, true))
-                            return false;
+            // K runs ahead of V as far as QK runs ahead of PV.
+            const int nt = n * per, lead = x.split ? C::kBufs - 1 : 1, b0 = t0 * per * nb;
+            kids.start(row, ps / box, b0, n_box - 1);
+            vids.start(row, ps / box, b0, n_box - 1);
+            for (int t = -lead; t < nt; ++t) {
+                if (t + lead < nt &&
+                    !load(&mk, b.kfull, b.kempty, k_a, gk, kids, h, false))
+                    return false;
+                if (t >= 0 && !load(&mv, b.vfull, b.vempty, v_a, gv, vids, h, true))
+                    return false;
             }
             return true;
         });
@@ -280,69 +339,76 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             mbar_wait_bounded(&b.kfull[c % ST], (c / ST) & 1u);
         for (uint32_t c = gv > ST ? gv - ST : 0; c < gv; ++c)
             mbar_wait_bounded(&b.vfull[c % ST], (c / ST) & 1u);
-    } else if (warp == 9) {  // ------------------------------------------------- MMA issue
-        if (lane == 0) {
+    } else if (warp == 9 || warp == 10) {  // ------------------------------ MMA issue
+        fewer_regs<72>();
+        if (elect_one()) {
             constexpr uint32_t idq = idesc_bf16_f32(kPR, kPK);
             constexpr uint32_t idv = idesc_bf16_f32(kPR, DH) | (1u << 16);  // B is MN-major
-            uint32_t gk = 0, gv = 0, items = 0, np[2] = {0, 0};
+            RingPos ring = {0, 0}, buf = {0, 0};  // of the K (V) tile and of the S and P buffer
+            uint32_t items = 0;
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 if (mbar_wait_bounded(bar, parity)) return true;
                 raise_error(SC_DEV_TIMEOUT);
                 return false;
             };
-            // S of stream s = Q K^T with the K tile in ring position g.
-            auto qk = [&](int s, uint32_t g) {
-                if (!wait(&b.kfull[g % ST], (g / ST) & 1u)) return false;
-                tc_fence_after();
-                const uint32_t qt = q_a + (x.split ? 0 : s) * C::kTile;
-                const uint32_t kt = k_a + (g % ST) * C::kTile;
-#pragma unroll
-                for (int j = 0; j < DH / 16; ++j)
-                    mma_bf16(tmem + s * kPK, sdesc_k128(qt + (j / 4) * C::kBlk) + 2 * (j % 4),
-                             sdesc_k128(kt + (j / 4) * C::kBlk) + 2 * (j % 4), idq, j != 0);
-                mma_commit(&b.sfull[s]);
-                return true;
-            };
-            walk([&](int h, int rt, int t0, int n, int64_t) {
-                const int streams = x.split || rt + 1 < x.n_tiles ? 2 : 1;
-                if (!wait(&b.qfull, items & 1u)) return false;
-                ++items;
-                auto free_k = [&](int s, uint32_t g) {  // the tile's last reader is issued
-                    if (x.split || s == streams - 1) mma_commit(&b.kempty[g % ST]);
-                };
-                for (int s = 0; s < streams; ++s) {
-                    const uint32_t g = gk + (x.split ? s : 0);
-                    if (!qk(s, g)) return false;
-                    free_k(s, g);
-                }
-                gk += per;
-                for (int t = 0; t < n; ++t) {
-                    for (int s = 0; s < streams; ++s) {
-                        const uint32_t g = gv + (x.split ? s : 0);
-                        if (!wait(&b.pready[s], np[s] & 1u)) return false;
-                        ++np[s];
-                        if (!wait(&b.vfull[g % ST], (g / ST) & 1u)) return false;
+            if (warp == 9) {
+                const uint64_t qd = sdesc_k128(q_a), kd = sdesc_k128(k_a);
+                bool fresh = true;  // no buffer has been used yet: nothing to wait for
+                walk([&](int h, int rt, int t0, int n, int64_t) {
+                    const int streams = x.split || rt + 1 < x.n_tiles ? 2 : 1;
+                    const int total = n * streams;
+                    if (!wait(&b.qfull, items & 1u)) return false;
+                    ++items;
+                    for (int m = 0; m < total; ++m) {
+                        const int s = m & (streams - 1);
+                        if ((s == 0 || x.split) && !wait(&b.kfull[ring.i], ring.phase)) return false;
+                        if (!fresh && !wait(&b.pvdone[buf.i], buf.phase ^ 1u)) return false;
                         tc_fence_after();
-                        const uint32_t vt = v_a + (g % ST) * C::kTile;
+                        const uint64_t qt = qd + (s && !x.split ? C::kTile >> 4 : 0);
+                        const uint64_t kt = kd + ring.i * (C::kTile >> 4);
+                        const uint32_t d = tmem + buf.i * kPK;
+#pragma unroll
+                        for (int j = 0; j < DH / 16; ++j) {
+                            const uint32_t off = (j / 4) * (C::kBlk >> 4) + 2 * (j % 4);
+                            mma_bf16(d, qt + off, kt + off, idq, j != 0);
+                        }
+                        mma_commit(&b.sfull[buf.i]);
+                        if (s == streams - 1 || x.split) {  // the K tile's last reader
+                            mma_commit(&b.kempty[ring.i]);
+                            ring.next(ST);
+                        }
+                        buf.next(C::kBufs);
+                        if (buf.i == 0) fresh = false;
+                    }
+                    mma_commit(&b.qempty);
+                    return true;
+                });
+            } else {
+                const uint64_t vd = sdesc_mn128(v_a, C::kBlk);
+                walk([&](int h, int rt, int t0, int n, int64_t) {
+                    const int streams = x.split || rt + 1 < x.n_tiles ? 2 : 1;
+                    const int total = n * streams;
+                    for (int m = 0; m < total; ++m) {
+                        const int s = m & (streams - 1);
+                        if ((s == 0 || x.split) && !wait(&b.vfull[ring.i], ring.phase)) return false;
+                        if (!wait(&b.pready[buf.i], buf.phase)) return false;
+                        tc_fence_after();
+                        const uint64_t vt = vd + ring.i * (C::kTile >> 4);
+                        const uint32_t p = tmem + buf.i * kPK, o = tmem + C::kOCol + s * DH;
 #pragma unroll
                         for (int j = 0; j < kPK / 16; ++j)
-                            mma_bf16_ts(tmem + 2 * kPK + s * DH, tmem + s * kPK + j * 8,
-                                        sdesc_mn128(vt + j * 2048, C::kBlk), idv, (t | j) != 0);
-                        if (x.split || s == streams - 1) mma_commit(&b.vempty[g % ST]);
-                        if (t + 1 < n) {
-                            const uint32_t gn = gk + (x.split ? s : 0);
-                            if (!qk(s, gn)) return false;
-                            free_k(s, gn);
-                        } else {
-                            mma_commit(&b.ofull[s]);
+                            mma_bf16_ts(o, p + j * 8, vt + j * (2048 >> 4), idv,
+                                        m >= streams || j > 0);
+                        mma_commit(&b.pvdone[buf.i]);
+                        if (s == streams - 1 || x.split) {
+                            mma_commit(&b.vempty[ring.i]);
+                            ring.next(ST);
                         }
+                        buf.next(C::kBufs);
                     }
-                    gv += per;
-                    if (t + 1 < n) gk += per;
-                    if (t + 2 == n || n == 1) mma_commit(&b.qempty);  // the item's last S is issued
-                }
-                return true;
-            });
+                    return true;
+                });
+            }
             mma_commit(&b.done);  // no MMA may still write TMEM when it is freed
             mbar_wait_bounded(&b.done, 0);
         }
@@ -350,8 +416,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     } else {  // ------------------------------------------------------------- softmax
         const int s = warp >> 2, r = tid & 127;  // stream, row = TMEM lane
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
-        const uint32_t st = tmem + lane_base + s * kPK, ot = tmem + lane_base + 2 * kPK + s * DH;
-        uint32_t ns = 0, no = 0;
+        const uint32_t ot = tmem + lane_base + C::kOCol + s * DH;
+        uint32_t seq = 0;  // tiles of earlier items, both streams
+        more_regs<216>();
         bool dead = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             if (!dead && !mbar_wait_bounded(bar, parity)) {
@@ -363,6 +430,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
         };
         walk([&](int h, int rt, int t0, int n, int64_t w) {
             const int tile = x.split ? rt : rt + s;
+            const int streams = x.split || rt + 1 < x.n_tiles ? 2 : 1;
+            const uint32_t seq0 = seq;
+            seq += (uint32_t)n * streams;
             if (tile >= x.n_tiles) return true;  // the second stream has no rows
             // Keys of the prefix that this thread's row sees.
             const int64_t token = (int64_t)tile * x.tpt + r / a.G;
@@ -375,8 +445,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             float m = -INFINITY, l = 0.0f;
             for (int t = 0; t < n; ++t) {
                 const int key0 = ((t0 + t) * per + (x.split ? s : 0)) * kPK;
-                wait(&b.sfull[s], ns & 1u);
-                ++ns;
+                const uint32_t at = seq0 + (uint32_t)t * streams + s, buf = at % C::kBufs;
+                const uint32_t st = tmem + lane_base + buf * kPK;
+                wait(&b.sfull[buf], at / C::kBufs & 1u);
                 uint32_t v[kPK];
 #pragma unroll
                 for (int c = 0; c < kPK / 32; ++c) tmem_ld32(st + c * 32, v + c * 32);
@@ -387,18 +458,24 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                     for (int c = 0; c < kPK; ++c)
                         if (key0 + c >= limit) v[c] = 0xFF800000u;  // -inf
                 }
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float top[4];
 #pragma unroll
-                for (int c = 0; c < kPK; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(v[c]));
-                const float now =
-                    fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale_log2;
+                for (int c = 0; c < 4; ++c)
+                    top[c] = max3(__uint_as_float(v[c]), __uint_as_float(v[c + 4]),
+                                  __uint_as_float(v[c + 8]));
+#pragma unroll
+                for (int c = 12; c < kPK; c += 2)
+                    top[c / 2 & 3] = max3(top[c / 2 & 3], __uint_as_float(v[c]),
+                                          __uint_as_float(v[c + 1]));
+                const float now = fmaxf(max3(top[0], top[1], top[2]), top[3]) * a.scale_log2;
                 const bool rise = now > m + kRescaleLog2 || m == -INFINITY;
                 if (__any_sync(~0u, rise && now > m)) {
                     const float to = rise ? fmaxf(m, now) : m;
                     const float f = to == -INFINITY ? 1.0f : ex2(m - to);
                     m = to;
                     l *= f;
-                    if (t > 0) {  // S ready: the product before it is done, O is at rest
+                    if (t > 0) {  // O is at rest after the stream's last product
+                        wait(&b.pvdone[(at - streams) % C::kBufs], (at - streams) / C::kBufs & 1u);
 #pragma unroll
                         for (int c = 0; c < DH / 32; ++c) {
                             uint32_t o[32];
@@ -413,25 +490,31 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                     }
                 }
                 const float off = m == -INFINITY ? 0.0f : -m;
-                float sum[2] = {0.0f, 0.0f};
+                const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2), off2 = f2_make(off, off);
+                f32x2 sum[2] = {0, 0};
 #pragma unroll
                 for (int c = 0; c < kPK / 2; ++c) {
-                    const float e0 = ex2(fmaf(__uint_as_float(v[2 * c]), a.scale_log2, off));
-                    const float e1 = ex2(fmaf(__uint_as_float(v[2 * c + 1]), a.scale_log2, off));
-                    sum[0] += e0;
-                    sum[1] += e1;
+                    float e0, e1;
+                    f2_split(f2_fma(f2_make(__uint_as_float(v[2 * c]), __uint_as_float(v[2 * c + 1])),
+                                    scale2, off2),
+                             e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    sum[c & 1] = f2_add(sum[c & 1], f2_make(e0, e1));
                     v[c] = pack_bf16(e0, e1);
                 }
-                l += sum[0] + sum[1];
+                float s0, s1;
+                f2_split(f2_add(sum[0], sum[1]), s0, s1);
+                l += s0 + s1;
                 tmem_st32(st, v);
                 tmem_st32(st + 32, v + 32);
                 tmem_st_wait();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&b.pready[s]);
+                if (lane == 0) mbar_arrive(&b.pready[buf]);
             }
-            wait(&b.ofull[s], no & 1u);
-            ++no;
+            const uint32_t last = seq0 + (uint32_t)(n - 1) * streams + s;
+            wait(&b.pvdone[last % C::kBufs], last / C::kBufs & 1u);
             float *part = x.part + ((w + blockIdx.x) * 2 + s) * C::kSlot;
 #pragma unroll
             for (int c = 0; c < DH / 32; ++c) {

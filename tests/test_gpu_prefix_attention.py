@@ -114,6 +114,16 @@ def test_many_rows_share_a_prefix(shared):
     check(build(r.integers(641, 900, 70), shared=shared, D=4, G=4, Hkv=2, seed=11))
 
 
+@pytest.mark.parametrize("Dh,ps", [(64, 16), (128, 32)])
+@pytest.mark.parametrize("N,D,G", [(17, 8, 4), (3, 1, 5), (70, 1, 2)])
+def test_long_shared_prefix(Dh, ps, N, D, G):
+    """Many key tiles a CTA: every ring and buffer comes round several times."""
+    r = np.random.default_rng(N)
+    check(build(r.integers(20001, 20300, N), shared=20000 // ps, ps=ps, D=D, G=G, Hkv=1, Dh=Dh,
+                seed=N))
+    check(build(r.integers(3000, 3300, N), shared=3000 // ps, ps=ps, D=D, G=G, Hkv=6, Dh=Dh, seed=N))
+
+
 @pytest.mark.parametrize("Dh,G", [(64, 4), (128, 7)])
 def test_one_long_sequence(Dh, G):
     check(build([20001], ps=64, Hkv=2, G=G, Dh=Dh, seed=12))
