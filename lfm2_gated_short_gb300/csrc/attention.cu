@@ -35,9 +35,8 @@ namespace sc {
 typedef __nv_bfloat16 bf16;
 
 constexpr int kKT = 64;            // keys of a tile
-constexpr int kOwnWarps = 4;       // consumer warps, 16 keys of a tile each
-constexpr int kOwnThreads = 32 * (kOwnWarps + 1);
-constexpr int kMaxCtas = 304;      // two CTAs on each of 152 SMs
+constexpr int kKeyWarps = 4;       // 16 keys of a tile each
+constexpr int kMaxCtas = 456;      // three CTAs on each of 152 SMs
 constexpr int kMaxPrefixCtas = 152;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -65,7 +64,9 @@ __host__ __device__ __forceinline__ int64_t share_begin(int64_t c, int64_t U, in
     return c * U / n;
 }
 __host__ __device__ __forceinline__ int share_of(int64_t u, int64_t U, int64_t n) {
-    return (int)(((u + 1) * n - 1) / U);
+    const int64_t x = (u + 1) * n - 1;
+    if (x <= UINT32_MAX) return (int)((uint32_t)x / (uint32_t)U);  // u < U, n > 0: U is smaller
+    return (int)(x / U);
 }
 
 // Tokens of sequence i (its D new ones included), or -1 with a bad slot or length.
@@ -153,31 +154,43 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
     return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-template <int DH, int MT>
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// RG groups of 16 rows. A CTA's consumer warps are 4 key groups (16 keys of a
+// tile) times RG row groups. Shared memory and registers allow 3 CTAs an SM
+// for 16 rows of 64, 2 for 32 of 64 or 16 of 128, 1 for 32 of 128; either way
+// 160 to 192 KB of tiles are in flight.
+template <int DH, int RG>
 struct OwnCfg {
-    static constexpr int MR = 16 * MT;
+    static constexpr int MR = 16 * RG;
+    static constexpr int kWarps = kKeyWarps * RG;             // consumer warps
+    static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer
     static constexpr int NB = DH / 64;                        // 64-wide column blocks
     static constexpr uint32_t kBlk = kKT * 128;               // one block of a tile, 8 KB
     static constexpr uint32_t kStage = 2 * NB * kBlk;         // K and V of a tile
-    static constexpr int kStages = 6;
-    static constexpr int kCtas = DH == 64 ? 2 : 1;            // CTAs of an SM
+    static constexpr int kCtas = DH == 64 ? (RG == 1 ? 3 : 2) : (RG == 1 ? 2 : 1);
+    static constexpr int kStages = DH == 64 ? (RG == 1 ? 4 : 5) : (RG == 1 ? 3 : 5);
     static constexpr uint32_t kQ = MR * 128 * NB;
     static constexpr int kOs = DH + 4;                        // floats of a joined O row
-    static constexpr uint32_t kJoin = (MR * kOs + 2 * kOwnWarps * MR) * 4;
+    static constexpr uint32_t kJoin = (MR * kOs + 2 * kKeyWarps * MR) * 4;
     static constexpr size_t kSmem = 1024 + kStages * kStage + kQ + kJoin;
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part
 };
 
-template <int DH, int MT>
-__global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
+template <int DH, int RG>
+__global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCtas)
     k_own(AttnArgs a, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
-    using C = OwnCfg<DH, MT>;
-    constexpr int ST = C::kStages;
+    using C = OwnCfg<DH, RG>;
+    constexpr int ST = C::kStages, kThreads = C::kThreads;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t s_full[ST], s_empty[ST];
     __shared__ int s_bad[ST];
-    __shared__ int64_t s_scan[kOwnThreads];
+    __shared__ int64_t s_scan[kThreads];
     __shared__ int s_seq;
     __shared__ int64_t s_seq_unit;
     const uint32_t raw_a = smem_addr(raw);
@@ -190,7 +203,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&s_empty[s], kOwnWarps);
+            mbar_init(&s_empty[s], C::kWarps);
             s_bad[s] = 0;
         }
         mbar_fence_init();
@@ -213,7 +226,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
     int n_cta = 1;
     for (int pass = 0; pass < 2; ++pass) {
         int64_t base = 0;
-        for (int i0 = 0; i0 < a.N; i0 += kOwnThreads) {
+        for (int i0 = 0; i0 < a.N; i0 += kThreads) {
             const int i = i0 + tid;
             int slot;
             int64_t mine = 0;
@@ -222,7 +235,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
                        own_tiles(a, seq_len(a, i, &slot, pass == 0 && blockIdx.x == 0));
             s_scan[tid] = mine;
             __syncthreads();
-            for (int o = 1; o < kOwnThreads; o <<= 1) {
+            for (int o = 1; o < kThreads; o <<= 1) {
                 const int64_t v = tid >= o ? s_scan[tid - o] : 0;
                 __syncthreads();
                 s_scan[tid] += v;
@@ -236,7 +249,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
                 }
                 if (blockIdx.x == 0) gst(a.cum + i, begin);
             }
-            base += s_scan[kOwnThreads - 1];
+            base += s_scan[kThreads - 1];
             __syncthreads();
         }
         if (pass == 0) {
@@ -271,7 +284,7 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
         }
     };
 
-    if (warp == kOwnWarps) {  // producer
+    if (warp == C::kWarps) {  // producer
         const int ps = a.pt.page_size;
         const int box = min(ps, kKT), nb = kKT / box;  // keys of a box, boxes of a tile
         uint32_t g = 0;
@@ -318,10 +331,12 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
 
     uint32_t g = 0;
     bool dead = false;
+    const int kw = warp % kKeyWarps, rg = warp / kKeyWarps;  // key and row group
+    const int group_bar = 2 + rg;                            // barrier of a row group's warps
     walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
-        // The item's query rows, and the keys that this thread's rows see.
+        // The item's query rows, and the keys that this thread's two rows see.
         const int r0 = rt * C::MR;
-        for (int x = tid; x < C::MR * DH / 8; x += 32 * kOwnWarps) {
+        for (int x = tid; x < C::MR * DH / 8; x += 32 * C::kWarps) {
             const int r = x / (DH / 8), ch = x % (DH / 8), rr = r0 + r;
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
             if (rr < rows)
@@ -329,32 +344,27 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
                              (h * a.G + rr % a.G) * DH + ch * 8);
             *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::MR * 128 + swz(r, ch & 7)) = v;
         }
-        named_sync(1, 32 * kOwnWarps);
-        uint32_t qf[MT][DH / 16][4];
+        named_sync(1, 32 * C::kWarps);
+        uint32_t qf[DH / 16][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-                const int ch = kk * 2 + (lane >> 4);
-                ldsm4(qf[mt][kk], qs_a + (ch >> 3) * C::MR * 128 +
-                                      swz(mt * 16 + (lane & 15), ch & 7));
-            }
-        int see[MT][2];
-        float m[MT][2], l[MT][2], o[MT][DH / 8][4];
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int rr = r0 + mt * 16 + p * 8 + (lane >> 2);
-                see[mt][p] = rr < rows ? len - a.D + rr / a.G + 1 : 0;
-                m[mt][p] = -INFINITY;
-                l[mt][p] = 0.0f;
-            }
-#pragma unroll
-            for (int d = 0; d < DH / 8; ++d)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[mt][d][e] = 0.0f;
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            const int ch = kk * 2 + (lane >> 4);
+            ldsm4(qf[kk], qs_a + (ch >> 3) * C::MR * 128 + swz(rg * 16 + (lane & 15), ch & 7));
         }
+        int see[2];
+        float m[2], l[2], o[DH / 8][4];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int rr = r0 + rg * 16 + p * 8 + (lane >> 2);
+            see[p] = rr < rows ? len - a.D + rr / a.G + 1 : 0;
+            m[p] = -INFINITY;
+            l[p] = 0.0f;
+        }
+        const int least = len - a.D + 1;  // keys that every row of the sequence sees
+#pragma unroll
+        for (int d = 0; d < DH / 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
         bool bad = false;
         for (int t = 0; t < n; ++t, ++g) {
             const uint32_t s = g % ST;
@@ -364,150 +374,141 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
             }
             bad |= s_bad[s] != 0;
             const uint32_t kt = ring_a + s * C::kStage, vt = kt + C::NB * C::kBlk;
-            const int key0 = a.shared_keys + (t0 + t) * kKT + warp * 16;
+            const int key0 = a.shared_keys + (t0 + t) * kKT + kw * 16;
             const bool tail = key0 + 16 > len;
             if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
                 const int from = max(0, len - key0);
                 for (int x = lane; x < (16 - from) * C::NB * 8; x += 32) {
                     const int r = from + x / (C::NB * 8), ch = x % (C::NB * 8);
                     *reinterpret_cast<uint4 *>(ring + s * C::kStage + (C::NB + (ch >> 3)) * C::kBlk +
-                                               (warp * 16 + r) * 128 + (ch & 7) * 16) =
+                                               (kw * 16 + r) * 128 + (ch & 7) * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
                 __syncwarp();
             }
-            float sc[MT][2][4];
+            float sc[2][4];
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[mt][0][e] = sc[mt][1][e] = 0.0f;
+            for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.0f;
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk) {
                 uint32_t b[4];
-                const int row = warp * 16 + (lane & 7) + ((lane >> 4) << 3);
+                const int row = kw * 16 + (lane & 7) + ((lane >> 4) << 3);
                 const int ch = kk * 2 + ((lane >> 3) & 1);
                 ldsm4(b, kt + (ch >> 3) * C::kBlk + swz(row, ch & 7));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816(sc[mt][0], qf[mt][kk], b[0], b[1]);
-                    mma16816(sc[mt][1], qf[mt][kk], b[2], b[3]);
-                }
+                mma16816(sc[0], qf[kk], b[0], b[1]);
+                mma16816(sc[1], qf[kk], b[2], b[3]);
             }
-            uint32_t pf[MT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                float top[2] = {-INFINITY, -INFINITY};
+            if (key0 + 16 > least) {  // some row does not see some of these keys
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const int key = key0 + nt * 8 + (lane & 3) * 2 + (e & 1);
-                        float &x = sc[mt][nt][e];
-                        x = key < see[mt][e >> 1] ? x * a.scale_log2 : -INFINITY;
-                        top[e >> 1] = fmaxf(top[e >> 1], x);
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
+                            sc[nt][e] = -INFINITY;
+            }
+            float top[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                top[p] = fmaxf(fmaxf(sc[0][2 * p], sc[0][2 * p + 1]),
+                               fmaxf(sc[1][2 * p], sc[1][2 * p + 1]));
+                top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
+                top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2)) * a.scale_log2;
+            }
+            if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
-                    top[p] = fmaxf(top[p], m[mt][p]);
-                    // A row that has seen no key yet keeps m = -inf and sums of zero.
-                    const float base = top[p] == -INFINITY ? 0.0f : top[p];
-                    const float f = exp2f(m[mt][p] - base);
-                    m[mt][p] = top[p];
-                    l[mt][p] *= f;
+                    const float to = fmaxf(m[p], top[p]);
+                    const float f = to == -INFINITY ? 1.0f : ex2(m[p] - to);
+                    m[p] = to;
+                    l[p] *= f;
 #pragma unroll
                     for (int d = 0; d < DH / 8; ++d) {
-                        o[mt][d][2 * p] *= f;
-                        o[mt][d][2 * p + 1] *= f;
+                        o[d][2 * p] *= f;
+                        o[d][2 * p + 1] *= f;
                     }
+                }
+            }
+            uint32_t pf[4];
 #pragma unroll
-                    for (int nt = 0; nt < 2; ++nt) {
-                        const float e0 = exp2f(sc[mt][nt][2 * p] - base);
-                        const float e1 = exp2f(sc[mt][nt][2 * p + 1] - base);
-                        l[mt][p] += e0 + e1;
-                        // P enters the second product as bf16: 2^-9 relative a term.
-                        pf[mt][nt * 2 + p] = pack_bf16(e0, e1);
-                    }
+            for (int p = 0; p < 2; ++p) {
+                // A row that has seen no key yet keeps m = -inf and sums of zero.
+                const float off = m[p] == -INFINITY ? 0.0f : -m[p];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt) {
+                    const float e0 = ex2(fmaf(sc[nt][2 * p], a.scale_log2, off));
+                    const float e1 = ex2(fmaf(sc[nt][2 * p + 1], a.scale_log2, off));
+                    l[p] += e0 + e1;
+                    // P enters the second product as bf16: 2^-8 relative a term at most.
+                    pf[nt * 2 + p] = pack_bf16(e0, e1);
                 }
             }
 #pragma unroll
             for (int dd = 0; dd < DH / 16; ++dd) {
                 uint32_t b[4];
-                const int row = warp * 16 + (lane & 15);
+                const int row = kw * 16 + (lane & 15);
                 const int ch = dd * 2 + (lane >> 4);
                 ldsm4_t(b, vt + (ch >> 3) * C::kBlk + swz(row, ch & 7));
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    mma16816(o[mt][2 * dd], pf[mt], b[0], b[1]);
-                    mma16816(o[mt][2 * dd + 1], pf[mt], b[2], b[3]);
-                }
+                mma16816(o[2 * dd], pf, b[0], b[1]);
+                mma16816(o[2 * dd + 1], pf, b[2], b[3]);
             }
             if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[s]);
         }
-        // Join the four warps: the common maximum, then O and l in turn.
-        float *jm = join + C::MR * C::kOs, *jl = jm + kOwnWarps * C::MR;
+        // Join the key warps: the common maximum, then O and l in turn.
+        float *jm = join + C::MR * C::kOs, *jl = jm + kKeyWarps * C::MR;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
+        for (int p = 0; p < 2; ++p) {
+            l[p] += __shfl_xor_sync(~0u, l[p], 1);
+            l[p] += __shfl_xor_sync(~0u, l[p], 2);
+            if ((lane & 3) == 0) jm[kw * C::MR + rg * 16 + p * 8 + (lane >> 2)] = m[p];
+        }
+        named_sync(group_bar, 32 * kKeyWarps);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                l[mt][p] += __shfl_xor_sync(~0u, l[mt][p], 1);
-                l[mt][p] += __shfl_xor_sync(~0u, l[mt][p], 2);
-                const int r = mt * 16 + p * 8 + (lane >> 2);
-                if ((lane & 3) == 0) jm[warp * C::MR + r] = m[mt][p];
+        for (int p = 0; p < 2; ++p) {
+            const int r = rg * 16 + p * 8 + (lane >> 2);
+            float top = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kKeyWarps; ++k) top = fmaxf(top, jm[k * C::MR + r]);
+            const float f = ex2(m[p] - (top == -INFINITY ? 0.0f : top));
+            if ((lane & 3) == 0) jl[kw * C::MR + r] = l[p] * f;
+#pragma unroll
+            for (int d = 0; d < DH / 8; ++d) {
+                o[d][2 * p] *= f;
+                o[d][2 * p + 1] *= f;
             }
-        named_sync(1, 32 * kOwnWarps);
+        }
+        constexpr int kQuarter = DH / 8 / kKeyWarps;
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int r = mt * 16 + p * 8 + (lane >> 2);
-                float top = -INFINITY;
-#pragma unroll
-                for (int k = 0; k < kOwnWarps; ++k) top = fmaxf(top, jm[k * C::MR + r]);
-                const float f = exp2f(m[mt][p] - (top == -INFINITY ? 0.0f : top));
-                if ((lane & 3) == 0) jl[warp * C::MR + r] = l[mt][p] * f;
-#pragma unroll
-                for (int d = 0; d < DH / 8; ++d) {
-                    o[mt][d][2 * p] *= f;
-                    o[mt][d][2 * p + 1] *= f;
-                }
-            }
-        constexpr int kQuarter = DH / 8 / kOwnWarps;
-#pragma unroll
-        for (int round = 0; round < kOwnWarps; ++round) {
-            const int blk = (warp + round) % kOwnWarps;  // each warp adds another quarter
+        for (int round = 0; round < kKeyWarps; ++round) {
+            const int blk = (kw + round) % kKeyWarps;  // each warp adds another quarter
 #pragma unroll
             for (int d = 0; d < DH / 8; ++d) {
                 if (d / kQuarter != blk) continue;
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        float2 *at = reinterpret_cast<float2 *>(
-                            join + (mt * 16 + p * 8 + (lane >> 2)) * C::kOs + d * 8 +
-                            (lane & 3) * 2);
-                        float2 v = round ? *at : make_float2(0.0f, 0.0f);
-                        v.x += o[mt][d][2 * p];
-                        v.y += o[mt][d][2 * p + 1];
-                        *at = v;
-                    }
+                for (int p = 0; p < 2; ++p) {
+                    float2 *at = reinterpret_cast<float2 *>(
+                        join + (rg * 16 + p * 8 + (lane >> 2)) * C::kOs + d * 8 + (lane & 3) * 2);
+                    float2 v = round ? *at : make_float2(0.0f, 0.0f);
+                    v.x += o[d][2 * p];
+                    v.y += o[d][2 * p + 1];
+                    *at = v;
+                }
             }
-            named_sync(1, 32 * kOwnWarps);
+            named_sync(group_bar, 32 * kKeyWarps);
         }
         const bool whole = n == T && a.shared_keys == 0;  // nothing to join with
         float *part = a.own_part + (int64_t)(w + blockIdx.x) * C::kSlot;
-        for (int x = tid; x < C::MR * DH / 4; x += 32 * kOwnWarps) {
-            const int r = x / (DH / 4), c4 = x % (DH / 4), rr = r0 + r;
+        const int gt = kw * 32 + lane;  // thread of the row group
+        for (int x = gt; x < 16 * DH / 4; x += 32 * kKeyWarps) {
+            const int r = rg * 16 + x / (DH / 4), c4 = x % (DH / 4), rr = r0 + r;
             float4 v = *reinterpret_cast<float4 *>(join + r * C::kOs + c4 * 4);
             if (rr >= rows) continue;
             if (whole) {
                 if (bad) continue;
                 float sum = 0.0f;
 #pragma unroll
-                for (int k = 0; k < kOwnWarps; ++k) sum += jl[k * C::MR + r];
+                for (int k = 0; k < kKeyWarps; ++k) sum += jl[k * C::MR + r];
                 const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
                 gst(reinterpret_cast<uint2 *>(a.out + (((int64_t)i * a.D + rr / a.G) * a.Hkv + h) *
                                                           a.G * DH + (rr % a.G) * DH + c4 * 4),
@@ -516,18 +517,19 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
                 gst(reinterpret_cast<float4 *>(part + r * DH + c4 * 4), v);
             }
         }
-        if (!whole && tid < C::MR) {
+        if (!whole && gt < 16) {
+            const int r = rg * 16 + gt;
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kOwnWarps; ++k) {
-                top = fmaxf(top, jm[k * C::MR + tid]);
-                sum += jl[k * C::MR + tid];
+            for (int k = 0; k < kKeyWarps; ++k) {
+                top = fmaxf(top, jm[k * C::MR + r]);
+                sum += jl[k * C::MR + r];
             }
             // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
-            gst(part + C::MR * DH + tid, bad ? __int_as_float(0x7FC00000) : top);
-            gst(part + C::MR * DH + C::MR + tid, sum);
+            gst(part + C::MR * DH + r, bad ? __int_as_float(0x7FC00000) : top);
+            gst(part + C::MR * DH + C::MR + r, sum);
         }
-        named_sync(1, 32 * kOwnWarps);  // join and Q are written again by the next item
+        named_sync(1, 32 * C::kWarps);  // join and Q are written again by the next item
         return true;
     });
 }
@@ -538,73 +540,105 @@ __global__ void __launch_bounds__(kOwnThreads, OwnCfg<DH, MT>::kCtas)
 
 namespace sc {
 
-// A row is joined by Dh / 4 lanes, four columns each: the prefix's parts, then its own.
+// A warp joins a row: lane k holds the maximum and sum of part k, then the parts'
+// values are added with Dh / 4 lanes a part, in a fixed order. No load waits for
+// another part's, so the kernel costs a few memory latencies.
 template <int DH>
 __global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_ctas) {
     pdl_wait();
     pdl_launch_dependents();
     AttnArgs &a = x.a;
-    if (a.shared_keys > 0 && gld(a.leader) < 0) a.shared_keys = 0;
-    constexpr int L = DH / 4;
-    const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / L;
-    const int c4 = threadIdx.x % L;
+    constexpr int L = DH / 4, kAtOnce = 32 / L;
+    const int lane = threadIdx.x & 31, c4 = lane % L;
     const int Hq = a.Hkv * a.G;
-    if (row >= (int64_t)a.N * a.D * Hq) return;
-    const int i = (int)(row / ((int64_t)a.D * Hq)), j = (int)(row / Hq % a.D);
-    const int hq = (int)(row % Hq), h = hq / a.G, g = hq % a.G;
+    const int row = (int)((blockIdx.x * (unsigned)blockDim.x + threadIdx.x) >> 5);
+    if (row >= a.N * a.D * Hq) return;
+    const int token = row / Hq, hq = row % Hq, i = token / a.D, j = token % a.D;
+    const int h = hq / a.G, g = hq % a.G;
+    const bool prefix = a.shared_keys > 0 && gld(a.leader) >= 0;
+    const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
     int slot;
-    const int len = seq_len(a, i, &slot, false);
-    if (len < 0) return;
-    float top = -INFINITY, sum = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    auto add = [&](const float *part, int rows, int r) {
-        const float m = gld(part + rows * DH + r), l = gld(part + rows * DH + rows + r);
-        const float4 v = gld(reinterpret_cast<const float4 *>(part + r * DH) + c4);
-        if (m != m || top != top) {
-            top = __int_as_float(0x7FC00000);
-            return;
-        }
-        const float now = fmaxf(top, m), base = now == -INFINITY ? 0.0f : now;
-        const float f0 = exp2f(top - base), f1 = exp2f(m - base);
-        sum = sum * f0 + l * f1;
-        o.x = o.x * f0 + v.x * f1;
-        o.y = o.y * f0 + v.y * f1;
-        o.z = o.z * f0 + v.z * f1;
-        o.w = o.w * f0 + v.w * f1;
-        top = now;
-    };
-    if (a.shared_keys > 0) {
-        const int token = i * a.D + j, tile = token / x.tpt, r = token % x.tpt * a.G + g;
-        const int64_t w = (int64_t)(x.split ? tile : tile / 2) * a.Hkv + h;
+    if (seq_len(a, i, &slot, false) < 0) return;
+
+    // The row's parts: prefix_n from prefix_at on, own_n from own_at on.
+    const float *prefix_at = nullptr, *own_at = nullptr;
+    int prefix_n = 0, own_n = 0, pr = 0, step = 0;
+    constexpr int kPSlot = kPR * (DH + 2);
+    if (prefix) {
+        const int tile = token / x.tpt;
+        pr = token % x.tpt * a.G + g;
+        const int64_t w = (int64_t)(x.split ? tile : tile >> 1) * a.Hkv + h;
         const int c0 = share_of(w * x.T, x.U, x.n_cta);
         const int c1 = share_of(w * x.T + x.T - 1, x.U, x.n_cta);
-        for (int c = c0; c <= c1; ++c) {
-            const float *part = x.part + ((w + c) * 2) * (int64_t)(kPR * (DH + 2));
-            if (x.split) {
-                add(part, kPR, r);
-                add(part + kPR * (DH + 2), kPR, r);
-            } else {
-                add(part + (tile & 1) * kPR * (DH + 2), kPR, r);
+        prefix_at = x.part + ((w + c0) * 2 + (x.split ? 0 : tile & 1)) * kPSlot;
+        step = x.split ? kPSlot : 2 * kPSlot;
+        prefix_n = (c1 - c0 + 1) * (x.split ? 2 : 1);
+    }
+    const int r = j * a.G + g, RT = (a.D * a.G + MR - 1) / MR, per = RT * a.Hkv;
+    const int oslot = MR * (DH + 2), orow = r % MR;
+    if (u_n > u_i) {
+        const int64_t T = (u_n - u_i) / per;
+        const int n_cta = (int)min((int64_t)own_ctas, U);
+        const int it = r / MR * a.Hkv + h;
+        const int64_t u0 = u_i + it * T;
+        const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
+        if (c0 == c1 && !prefix) return;  // k_own wrote the row
+        own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot;
+        own_n = c1 - c0 + 1;
+    }
+    const int parts = prefix_n + own_n;
+    auto row_of = [&](int p) {  // O of part p's row
+        return p < prefix_n ? prefix_at + (int64_t)p * step + pr * DH
+                            : own_at + (int64_t)(p - prefix_n) * oslot + orow * DH;
+    };
+    float top = -INFINITY, sum = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    bool bad = false;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+        float m = -INFINITY, l = 0.0f;
+        if (p0 + lane < parts) {
+            const int p = p0 + lane;
+            const float *ml = p < prefix_n
+                                  ? prefix_at + (int64_t)p * step + kPR * DH + pr
+                                  : own_at + (int64_t)(p - prefix_n) * oslot + MR * DH + orow;
+            m = gld(ml);
+            l = gld(ml + (p < prefix_n ? kPR : MR));
+        }
+        bad |= __any_sync(~0u, m != m);
+        float now = fmaxf(top, m);
+#pragma unroll
+        for (int k = 16; k; k >>= 1) now = fmaxf(now, __shfl_xor_sync(~0u, now, k));
+        const float base = now == -INFINITY ? 0.0f : now;
+        const float f = ex2(m - base), f0 = ex2(top - base);
+        float s = l * f;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
+        sum = sum * f0 + s;
+        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+        top = now;
+        const int here = min(32, parts - p0);
+#pragma unroll 4
+        for (int p = 0; p < here; p += kAtOnce) {
+            const int q = p + lane / L;
+            const float w = __shfl_sync(~0u, f, q & 31);
+            if (q < here) {
+                const float4 v = gld(reinterpret_cast<const float4 *>(row_of(p0 + q)) + c4);
+                o.x = fmaf(w, v.x, o.x);
+                o.y = fmaf(w, v.y, o.y);
+                o.z = fmaf(w, v.z, o.z);
+                o.w = fmaf(w, v.w, o.w);
             }
         }
     }
-    const int T = own_tiles(a, len);
-    if (T > 0) {
-        const int64_t U = gld(a.cum + a.N);
-        const int n_cta = (int)min((int64_t)own_ctas, max(U, (int64_t)1));
-        const int r = j * a.G + g, rt = r / MR;
-        const int RT = (a.D * a.G + MR - 1) / MR;
-        const int it = rt * a.Hkv + h;
-        const int64_t u0 = gld(a.cum + i) + (int64_t)it * T;
-        const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
-        if (c0 == c1 && a.shared_keys == 0) return;  // k_own wrote the row
-        const int64_t w = (int64_t)i * RT * a.Hkv + it;
-        for (int c = c0; c <= c1; ++c)
-            add(a.own_part + (w + c) * ((int64_t)MR * (DH + 2)), MR, r % MR);
+    if constexpr (kAtOnce == 2) {
+        o.x += __shfl_xor_sync(~0u, o.x, 16);
+        o.y += __shfl_xor_sync(~0u, o.y, 16);
+        o.z += __shfl_xor_sync(~0u, o.z, 16);
+        o.w += __shfl_xor_sync(~0u, o.w, 16);
     }
-    if (top != top) return;  // a bad page: the row is not written
+    if (bad || lane >= L) return;  // a bad page: the row is not written
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-    gst(reinterpret_cast<uint2 *>(a.out + row * DH + c4 * 4),
+    gst(reinterpret_cast<uint2 *>(a.out + (int64_t)row * DH + c4 * 4),
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)));
 }
 
@@ -715,14 +749,15 @@ static cudaError_t smem_opt_in(F kern, size_t bytes, std::atomic<unsigned long l
     return e;
 }
 
-template <int DH, int MT>
+template <int DH, int RG>
 static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                              int grid, cudaStream_t stream) {
-    using C = OwnCfg<DH, MT>;
+                              int sm_count, int *grid, cudaStream_t stream) {
+    using C = OwnCfg<DH, RG>;
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = smem_opt_in(k_own<DH, MT>, C::kSmem, done);
+    const cudaError_t e = smem_opt_in(k_own<DH, RG>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    return launch_pdl(k_own<DH, MT>, dim3((unsigned)grid), dim3(kOwnThreads), C::kSmem, stream, a,
+    *grid = C::kCtas * sm_count < kMaxCtas ? C::kCtas * sm_count : kMaxCtas;
+    return launch_pdl(k_own<DH, RG>, dim3((unsigned)*grid), dim3(C::kThreads), C::kSmem, stream, a,
                       mk, mv);
 }
 
@@ -780,17 +815,16 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     if (e != cudaSuccess) return e;
     e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, box);
     if (e != cudaSuccess) return e;
-    const int MR = own_rows(s), ctas = (s.Dh == 64 ? 2 : 1) * sm_count;
-    const int grid = ctas < kMaxCtas ? ctas : kMaxCtas;
+    const int MR = own_rows(s);
+    int grid = 0;
     if (s.Dh == 64)
-        e = MR == 16 ? launch_own<64, 1>(a, mk, mv, grid, stream)
-                     : launch_own<64, 2>(a, mk, mv, grid, stream);
+        e = MR == 16 ? launch_own<64, 1>(a, mk, mv, sm_count, &grid, stream)
+                     : launch_own<64, 2>(a, mk, mv, sm_count, &grid, stream);
     else
-        e = MR == 16 ? launch_own<128, 1>(a, mk, mv, grid, stream)
-                     : launch_own<128, 2>(a, mk, mv, grid, stream);
+        e = MR == 16 ? launch_own<128, 1>(a, mk, mv, sm_count, &grid, stream)
+                     : launch_own<128, 2>(a, mk, mv, sm_count, &grid, stream);
     if (e != cudaSuccess) return e;
-    const int64_t threads = (int64_t)s.N * s.D * s.Hq * (s.Dh / 4);
-    const dim3 blocks((unsigned)((threads + 255) / 256));
+    const dim3 blocks((unsigned)(((int64_t)s.N * s.D * s.Hq + 7) / 8));  // a warp a row
     return s.Dh == 64 ? launch_pdl(k_merge<64>, blocks, dim3(256), 0, stream, x, MR, grid)
                       : launch_pdl(k_merge<128>, blocks, dim3(256), 0, stream, x, MR, grid);
 }

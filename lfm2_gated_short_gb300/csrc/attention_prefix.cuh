@@ -156,12 +156,6 @@ __device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
     return d;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 struct RingPos {
     uint32_t i, phase;
     __device__ __forceinline__ void next(uint32_t n) {
