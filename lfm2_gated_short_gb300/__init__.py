@@ -606,9 +606,9 @@ def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, 
     t_p, t_s = rows(target, "target", D + 1)
     d_p, d_s = (None, V) if draft is None else rows(draft, "draft", D)
     if accepted is None:
-        accepted = tokens.new_empty((N,))
+        accepted = torch.empty((N,), dtype=torch.int32, device=target.device)
     if out_tokens is None:
-        out_tokens = tokens.new_empty((N, D + 1))
+        out_tokens = torch.empty((N, D + 1), dtype=torch.int32, device=target.device)
     _raise_on("shortconv_draft_accept", lib().shortconv_draft_accept(
         code, V, N, D, t_p, t_s, d_p, d_s, tok_p,
         None if n_drafts is None else _dev(n_drafts, "n_drafts", torch.int32, (N,)),

@@ -8,15 +8,16 @@
 // another sequence reads.
 //
 // Claims take the lowest free pages in listed order, so every call's result
-// is a function of its inputs alone. The metadata of a call (a few table
-// rows and the refs array, read once) is worked out by one CTA, which leaves
-// a list of page copies; a second kernel over the whole GPU copies the data
-// of every layer.
+// is a function of its inputs alone. The metadata of a call (the listed table
+// rows, and the refs array read once) is worked out by one CTA or a cluster,
+// which leaves a list of page copies; a second kernel over the whole GPU
+// copies the data of every layer, unless it is little.
 #include "common.cuh"
 #include "errors.cuh"
 #include "kernels.h"
 #include "launch.h"
 #include "shortconv.h"
+#include "tcgen05.cuh"
 #include "tma.cuh"
 
 namespace sc {
@@ -57,8 +58,16 @@ __device__ __forceinline__ void add_refs(const PageTable &pt, int id, int by) {
 __device__ __forceinline__ bool page_ok(const PageTable &pt, int id) {
     return id >= 0 && id < pt.n_pages;
 }
+// page_size is a power of two: its logarithm, and the divisions by it.
+__device__ __forceinline__ int page_log2(const PageTable &pt) { return __ffs(pt.page_size) - 1; }
 __device__ __forceinline__ int pages_of(const PageTable &pt, int len) {
-    return (len + pt.page_size - 1) / pt.page_size;
+    return (len + pt.page_size - 1) >> page_log2(pt);
+}
+__device__ __forceinline__ int full_pages(const PageTable &pt, int len) {
+    return len >> page_log2(pt);
+}
+__device__ __forceinline__ int part_of(const PageTable &pt, int len) {
+    return len & (pt.page_size - 1);
 }
 __device__ __forceinline__ int32_t *table_row(const PageTable &pt, int slot) {
     return pt.table + (int64_t)slot * pt.max_pages;
@@ -104,40 +113,176 @@ __device__ __forceinline__ int block_scan(int v, int *total) {
     return inc - v + (warp > 0 ? s_warp[warp - 1] : 0);
 }
 
+// refs of the 16 pages from p0 + 16 t on, for thread t (pages past the end: in use).
+constexpr int kScanPages = 16;
+__device__ __forceinline__ void load_refs(const PageTable &pt, int p0, int (&r)[kScanPages]) {
+    const int p = p0 + (int)threadIdx.x * kScanPages;
+    if (p + kScanPages <= pt.n_pages && (reinterpret_cast<uintptr_t>(pt.refs) & 15) == 0 &&
+        SC_RD_OK(pt.refs + p, 4 * kScanPages)) {
+#pragma unroll
+        for (int k = 0; k < kScanPages; k += 4) {
+            const int4 v = __ldcg(reinterpret_cast<const int4 *>(pt.refs + p + k));
+            r[k] = v.x, r[k + 1] = v.y, r[k + 2] = v.z, r[k + 3] = v.w;
+        }
+        return;
+    }
+#pragma unroll
+    for (int k = 0; k < kScanPages; ++k) r[k] = p + k < pt.n_pages ? ld_refs(pt.refs + p + k) : 1;
+}
+
 // The `want` lowest free pages into claimed[]; false with fewer free.
 __device__ bool claim_lowest(const PageTable &pt, int want, int32_t *claimed) {
     int found = 0;
-    for (int p0 = 0; p0 < pt.n_pages && found < want; p0 += kMetaThreads) {
-        const int p = p0 + threadIdx.x;
-        const int is_free = p < pt.n_pages && ld_refs(pt.refs + p) <= 0;
-        int here;
-        const int rank = found + block_scan(is_free, &here);
-        if (is_free && rank < want) gst(claimed + rank, p);
+    for (int p0 = 0; p0 < pt.n_pages && found < want; p0 += kMetaThreads * kScanPages) {
+        int r[kScanPages], mine = 0, here;
+        load_refs(pt, p0, r);
+#pragma unroll
+        for (int k = 0; k < kScanPages; ++k) mine += r[k] <= 0;
+        int rank = found + block_scan(mine, &here);
+#pragma unroll
+        for (int k = 0; k < kScanPages; ++k)
+            if (r[k] <= 0) {
+                if (rank < want) gst(claimed + rank, p0 + (int)threadIdx.x * kScanPages + k);
+                ++rank;
+            }
         found += here;
     }
     __syncthreads();  // claimed[] is read by other threads
     return found >= want;
 }
 
-// Release (sign -1) or take back (+1) table entries [from, to) of a slot, one warp.
-__device__ __forceinline__ void count_entries(const PageTable &pt, int slot, int from, int to,
-                                              int sign) {
-    for (int e = from + (int)(threadIdx.x & 31); e < to; e += 32) {
-        const int id = gld(table_row(pt, slot) + e);
-        if (page_ok(pt, id))
-            add_refs(pt, id, sign);
-        else if (sign < 0)
-            raise_error(SC_DEV_BAD_PAGE);
+// Up to kMetaThreads listed sequences in shared memory: entries [lo, hi) of each one's
+// table row are the call's business (lo == hi for one that is skipped).
+struct Rows {
+    int n;
+    int4 q[kMetaThreads];  // slot, lo, hi, and what the call keeps of it
+};
+
+// Threads as (row group, column): a thread walks its group's rows, so that
+// branches of one prompt, next to each other in the list, meet in one thread and
+// their equal page ids become one atomic; the CTAs of the cluster take the
+// columns in turn. f(first row, end row, column) for every column.
+template <typename F>
+__device__ __forceinline__ void for_entries(const Rows &rows, F &&f) {
+    __shared__ int s_width;
+    int width = 0;
+    for (int r = threadIdx.x; r < rows.n; r += kMetaThreads)
+        width = max(width, rows.q[r].z - rows.q[r].y);
+    __syncthreads();
+    if (threadIdx.x == 0) s_width = 0;
+    __syncthreads();
+    width = __reduce_max_sync(~0u, width);
+    if ((threadIdx.x & 31) == 0) atomicMax(&s_width, width);
+    __syncthreads();
+    width = s_width;
+    const int ctas = (int)cluster_ctas(), rank = (int)cluster_ctarank();
+    int shift = 5;  // 2^shift columns a CTA at once
+    while ((1 << shift) * ctas < width && (1 << shift) < kMetaThreads) ++shift;
+    const int groups = kMetaThreads >> shift, col = threadIdx.x & ((1 << shift) - 1);
+    const int per = (rows.n + groups - 1) / groups;
+    const int r0 = min(rows.n, (int)(threadIdx.x >> shift) * per), r1 = min(rows.n, r0 + per);
+    for (int c = (rank << shift) + col; c < width; c += ctas << shift) f(r0, r1, c);
+}
+
+// refs += sign for every listed entry.
+__device__ __forceinline__ void count_entries(const PageTable &pt, const Rows &rows, int sign) {
+    for_entries(rows, [&](int r0, int r1, int c) {
+        int id = -1, run = 0;
+        constexpr int kAhead = 8;  // entries in flight
+        for (int r = r0; r < r1; r += kAhead) {
+            int e[kAhead], in = 0;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int4 q = rows.q[min(r + k, r1 - 1)];
+                const bool live = r + k < r1 && q.y + c < q.z;
+                e[k] = live ? gld(table_row(pt, q.x) + q.y + c) : id;
+                in |= (int)live << k;
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (!(in >> k & 1)) continue;
+                if (e[k] != id) {
+                    if (run) add_refs(pt, id, sign * run);
+                    id = e[k];
+                    run = 0;
+                }
+                if (page_ok(pt, id))
+                    ++run;
+                else if (sign < 0)
+                    raise_error(SC_DEV_BAD_PAGE);
+            }
+        }
+        if (run) add_refs(pt, id, sign * run);
+    });
+}
+
+// Written by one CTA of a cluster and read, after a cluster barrier, by the others.
+template <typename V>
+__device__ __forceinline__ V ld_shared_word(const V *p) {
+    if (!SC_RD_OK(p, sizeof(V))) return V{};
+    return __ldcg(p);
+}
+
+// Copies 0 .. n - 1 in every layer and pool. A unit is up to 4 KB of one page copy,
+// one warp's; `worker` of `workers` warps.
+__device__ __forceinline__ void copy_pages(const PageWork &w, int n, const PageTable &pt,
+                                           const PagePools &pools, int worker, int workers) {
+    constexpr int kWords = 8;  // 16-byte words a lane
+    const int lane = threadIdx.x & 31;
+    const int64_t page_bytes = pt.page_size * pools.token_bytes;
+    const uint32_t chunks = (uint32_t)((page_bytes / 16 + 32 * kWords - 1) / (32 * kWords));
+    const uint32_t per_copy = chunks * 2 * (uint32_t)pools.L;
+    for (int64_t u = worker; u < (int64_t)n * per_copy; u += workers) {
+        const uint32_t ci = u <= UINT32_MAX ? (uint32_t)u / per_copy : (uint32_t)(u / per_copy);
+        const uint32_t rest = (uint32_t)(u - (int64_t)ci * per_copy), lp = rest / chunks;
+        const int4 c = ld_shared_word(reinterpret_cast<const int4 *>(w.copies + ci));
+        char *base =
+            (char *)(lp & 1 ? pools.v : pools.k) + (int64_t)(lp >> 1) * pt.n_pages * page_bytes;
+        const uint4 *from = (const uint4 *)(base + c.x * page_bytes);
+        uint4 *to = (uint4 *)(base + c.y * page_bytes);
+        const int q = (int)(c.z * pools.token_bytes / 16);
+        const int i0 = (int)(rest - lp * chunks) * 32 * kWords + lane;
+        uint4 v[kWords];
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+            if (i0 + 32 * k < q) v[k] = ld_plain(from + i0 + 32 * k);
+#pragma unroll
+        for (int k = 0; k < kWords; ++k)
+            if (i0 + 32 * k < q) st_plain(to + i0 + 32 * k, v[k]);
     }
 }
 
+// The end of a resize or fork: the number of copies for the copy kernel, or the copies
+// themselves, by the cluster's warps, where they are few.
+__device__ __forceinline__ void finish_copies(const PageWork &w, int n, bool enough,
+                                              const PageTable &pt, const PagePools &pools,
+                                              int inline_copy) {
+    const int rank = (int)cluster_ctarank();
+    if (rank == 0 && threadIdx.x == 0) {
+        if (!enough) raise_error(SC_DEV_NO_PAGE);
+        gst(w.n_copies, enough ? n : 0);
+    }
+    cluster_sync();
+    if (inline_copy)
+        copy_pages(w, ld_shared_word(w.n_copies), pt, pools,
+                   rank * (kMetaThreads / 32) + (int)(threadIdx.x >> 5),
+                   (int)cluster_ctas() * (kMetaThreads / 32));
+}
+
+// A cluster works a resize or fork out: entries are spread over its CTAs, what
+// needs an order (claims) or is one item a sequence is CTA 0's. The
+// barriers between the steps are the cluster's. `inline_copy`: the copies are
+// few enough to be made here (else k_pages_copy follows).
 __global__ void __launch_bounds__(kMetaThreads)
     k_pages_resize(PageTable pt, const int32_t *__restrict__ slots,
-                   const int32_t *__restrict__ new_lens, int n, PageWork w) {
+                   const int32_t *__restrict__ new_lens, int n, PageWork w, PagePools pools,
+                   int inline_copy) {
     __shared__ int s_copies;
+    __shared__ Rows rows;
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
+    const bool first = cluster_ctarank() == 0;
     const int64_t cap = (int64_t)pt.max_pages * pt.page_size;
     if (tid == 0) s_copies = 0;
     // Old and new length of listed sequence i; false (reported once) when either is bad.
@@ -152,72 +297,97 @@ __global__ void __launch_bounds__(kMetaThreads)
         return *old >= 0;
     };
     int slot, old, now;
-    for (int i = warp; i < n; i += kMetaThreads / 32)  // released entries
-        if (lengths(i, &slot, &old, &now, lane == 0))
-            count_entries(pt, slot, pages_of(pt, now), pages_of(pt, old), -1);
-    __syncthreads();
-    int want = 0;
-    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {  // claims, in listed order
+    // The sequences from i0 on: released entries, or with `all` the claimed ones too; .w is
+    // the first claim of a growing one, else -1.
+    auto list = [&](int i0, bool all, bool report) {
+        __syncthreads();
+        if (tid == 0) rows.n = min(n - i0, kMetaThreads);
         const int i = i0 + tid;
-        int claims = 0, copy = 0;
-        if (i < n && lengths(i, &slot, &old, &now, false)) {
+        if (i < n) {
+            const bool ok = lengths(i, &slot, &old, &now, report);
             const int need = pages_of(pt, now), have = pages_of(pt, old);
-            if (now < old && now % pt.page_size != 0) {
-                const int id = gld(table_row(pt, slot) + need - 1);
-                copy = page_ok(pt, id) && ld_refs(pt.refs + id) > 1;
-            }
-            claims = copy + max(0, need - have);
+            const bool grows = all && need > have;
+            rows.q[tid] = make_int4(slot, ok ? (grows ? have : need) : 0,
+                                    ok ? (grows ? need : max(need, have)) : 0,
+                                    ok && grows ? ld_shared_word(w.offset + i) : -1);
         }
-        int here;
-        const int at = want + block_scan(claims, &here);
-        if (i < n) gst(w.offset + i, copy ? -1 - at : at);
-        want += here;
+        __syncthreads();
+    };
+    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+        list(i0, false, first);
+        count_entries(pt, rows, -1);
     }
-    const bool enough = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
-    __syncthreads();
-    for (int i = warp; i < n; i += kMetaThreads / 32) {
-        if (!lengths(i, &slot, &old, &now, false)) continue;
-        const int need = pages_of(pt, now), have = pages_of(pt, old);
-        if (!enough) {
-            count_entries(pt, slot, need, have, 1);
+    cluster_sync();
+    if (first) {
+        int want = 0;
+        for (int i0 = 0; i0 < n; i0 += kMetaThreads) {  // claims, in listed order
+            const int i = i0 + tid;
+            int claims = 0, copy = 0;
+            if (i < n && lengths(i, &slot, &old, &now, false)) {
+                const int need = pages_of(pt, now), have = pages_of(pt, old);
+                if (now < old && part_of(pt, now) != 0) {
+                    const int id = gld(table_row(pt, slot) + need - 1);
+                    copy = page_ok(pt, id) && ld_refs(pt.refs + id) > 1;
+                }
+                claims = copy + max(0, need - have);
+            }
+            int here;
+            const int at = want + block_scan(claims, &here);
+            if (i < n) gst(w.offset + i, copy ? -1 - at : at);
+            want += here;
+        }
+        const bool enough = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
+        if (tid == 0) gst(w.n_copies, enough ? 1 : 0);  // until the copies are counted
+    }
+    cluster_sync();
+    const bool enough = ld_shared_word(w.n_copies) != 0;
+    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+        list(i0, enough, false);
+        if (!enough) {  // take the releases back
+            count_entries(pt, rows, 1);
             continue;
         }
-        int32_t *row = table_row(pt, slot);
-        for (int e = need + lane; e < have; e += 32) gst(row + e, -1);
-        int at = gld(w.offset + i);
-        if (at < 0) {
-            at = -1 - at;
-            if (lane == 0) {
-                const int from = gld(row + need - 1), to = gld(w.claimed + at);
+        const int i = i0 + tid;
+        if (first && i < n && lengths(i, &slot, &old, &now, false)) {
+            const int at = gld(w.offset + i);
+            if (at < 0) {
+                int32_t *entry = table_row(pt, slot) + pages_of(pt, now) - 1;
+                const int from = gld(entry), to = gld(w.claimed + (-1 - at));
                 add_refs(pt, from, -1);
                 add_refs(pt, to, 1);
-                gst(row + need - 1, to);
-                gst(w.copies + atomicAdd(&s_copies, 1),
-                    PageCopy{from, to, now % pt.page_size, 0});
+                gst(entry, to);
+                gst(w.copies + atomicAdd(&s_copies, 1), PageCopy{from, to, part_of(pt, now), 0});
             }
-            ++at;
         }
-        for (int e = have + lane; e < need; e += 32) {
-            const int id = gld(w.claimed + at + e - have);
-            add_refs(pt, id, 1);
-            gst(row + e, id);
-        }
-        if (lane == 0) gst(pt.lens + slot, now);
+        for_entries(rows, [&](int r0, int r1, int c) {
+            for (int r = r0; r < r1; ++r) {
+                const int4 q = rows.q[r];
+                if (q.y + c >= q.z) continue;
+                int id = -1;
+                if (q.w >= 0) {
+                    id = ld_shared_word(w.claimed + q.w + c);
+                    add_refs(pt, id, 1);
+                }
+                gst(table_row(pt, q.x) + q.y + c, id);
+            }
+        });
     }
-    __syncthreads();
-    if (tid == 0) {
-        if (!enough) raise_error(SC_DEV_NO_PAGE);
-        gst(w.n_copies, enough ? s_copies : 0);
-    }
+    cluster_sync();  // every CTA has read the old lengths
+    for (int i = tid; first && enough && i < n; i += kMetaThreads)
+        if (lengths(i, &slot, &old, &now, false)) gst(pt.lens + slot, now);
+    finish_copies(w, s_copies, enough, pt, pools, inline_copy);
 }
 
 __global__ void __launch_bounds__(kMetaThreads)
     k_pages_fork(PageTable pt, const int32_t *__restrict__ src, const int32_t *__restrict__ dst,
-                 int n, PageWork w) {
+                 int n, PageWork w, PagePools pools, int inline_copy) {
     __shared__ int s_copies;
+    __shared__ Rows rows;
+    __shared__ int2 s_share[kMetaThreads];  // of a pair: full pages, the page after them (-1: none)
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x;
+    const bool first = cluster_ctarank() == 0;
     if (tid == 0) s_copies = 0;
     auto pair = [&](int i, int *s, int *d, int *ls, int *ld, bool report) {
         *s = gld(src + i);
@@ -231,56 +401,94 @@ __global__ void __launch_bounds__(kMetaThreads)
         return *ls >= 0 && *ld >= 0;
     };
     int s, d, ls, ld;
-    for (int i = warp; i < n; i += kMetaThreads / 32)  // the destinations' old pages
-        if (pair(i, &s, &d, &ls, &ld, lane == 0)) count_entries(pt, d, 0, pages_of(pt, ld), -1);
-    __syncthreads();
-    int want = 0;
-    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+    // The pairs from i0 on: the destination's own entries, or with `share` its whole row
+    // (.w: the source).
+    auto list = [&](int i0, bool share, bool report) {
+        __syncthreads();
+        if (tid == 0) rows.n = min(n - i0, kMetaThreads);
         const int i = i0 + tid;
-        const int claims =
-            i < n && pair(i, &s, &d, &ls, &ld, false) && ls % pt.page_size != 0 ? 1 : 0;
-        int here;
-        const int at = want + block_scan(claims, &here);
-        if (i < n) gst(w.offset + i, at);
-        want += here;
+        if (i < n) {
+            const bool ok = pair(i, &s, &d, &ls, &ld, report);
+            rows.q[tid] = make_int4(d, 0, !ok ? 0 : share ? pt.max_pages : pages_of(pt, ld), s);
+            if (share) {
+                int last = -1;
+                if (ok && part_of(pt, ls)) {
+                    last = ld_shared_word(w.claimed + ld_shared_word(w.offset + i));
+                    if (first) {
+                        const int old = gld(table_row(pt, s) + full_pages(pt, ls));
+                        add_refs(pt, last, 1);
+                        if (page_ok(pt, old))
+                            gst(w.copies + atomicAdd(&s_copies, 1),
+                                PageCopy{old, last, part_of(pt, ls), 0});
+                        else
+                            raise_error(SC_DEV_BAD_PAGE);
+                    }
+                }
+                s_share[tid] = make_int2(full_pages(pt, ls), last);
+            }
+        }
+        __syncthreads();
+    };
+    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+        list(i0, false, first);
+        count_entries(pt, rows, -1);
     }
-    const bool enough = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
-    __syncthreads();
-    for (int i = warp; i < n; i += kMetaThreads / 32) {
-        if (!pair(i, &s, &d, &ls, &ld, false)) continue;
+    cluster_sync();
+    if (first) {
+        int want = 0;
+        for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+            const int i = i0 + tid;
+            const int claims =
+                i < n && pair(i, &s, &d, &ls, &ld, false) && part_of(pt, ls) != 0 ? 1 : 0;
+            int here;
+            const int at = want + block_scan(claims, &here);
+            if (i < n) gst(w.offset + i, at);
+            want += here;
+        }
+        const bool enough = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
+        if (tid == 0) gst(w.n_copies, enough ? 1 : 0);  // until the copies are counted
+    }
+    cluster_sync();
+    const bool enough = ld_shared_word(w.n_copies) != 0;
+    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+        list(i0, enough, false);
         if (!enough) {
-            count_entries(pt, d, 0, pages_of(pt, ld), 1);
+            count_entries(pt, rows, 1);
             continue;
         }
-        const int full = ls / pt.page_size, rows = ls % pt.page_size;
-        const int32_t *from = table_row(pt, s);
-        int32_t *to = table_row(pt, d);
-        for (int e = lane; e < pt.max_pages; e += 32) {
-            int id = -1;
-            if (e < full) {
-                id = gld(from + e);
-                if (page_ok(pt, id))
-                    add_refs(pt, id, 1);
+        for_entries(rows, [&](int r0, int r1, int c) {
+            int from = -1, entry = -1, run = 0;  // of the last source, and its run of shares
+            auto flush = [&]() {
+                if (run == 0) return;
+                if (page_ok(pt, entry))
+                    add_refs(pt, entry, run);
                 else
                     raise_error(SC_DEV_BAD_PAGE);
-            } else if (e == full && rows) {
-                const int old = gld(from + e);
-                id = gld(w.claimed + gld(w.offset + i));
-                add_refs(pt, id, 1);
-                if (page_ok(pt, old))
-                    gst(w.copies + atomicAdd(&s_copies, 1), PageCopy{old, id, rows, 0});
-                else
-                    raise_error(SC_DEV_BAD_PAGE);
+                run = 0;
+            };
+            for (int r = r0; r < r1; ++r) {
+                const int4 q = rows.q[r];
+                const int2 share = s_share[r];
+                if (q.z == 0) continue;
+                int v = c == share.x ? share.y : -1;
+                if (c < share.x) {
+                    if (q.w != from) {
+                        flush();
+                        from = q.w;
+                        entry = gld(table_row(pt, from) + c);
+                    }
+                    ++run;
+                    v = entry;
+                }
+                gst(table_row(pt, q.x) + c, v);
             }
-            gst(to + e, id);
-        }
-        if (lane == 0) gst(pt.lens + d, ls);
+            flush();
+        });
     }
-    __syncthreads();
-    if (tid == 0) {
-        if (!enough) raise_error(SC_DEV_NO_PAGE);
-        gst(w.n_copies, enough ? s_copies : 0);
-    }
+    cluster_sync();  // every CTA has read the old lengths
+    for (int i = tid; first && enough && i < n; i += kMetaThreads)
+        if (pair(i, &s, &d, &ls, &ld, false)) gst(pt.lens + d, ls);
+    finish_copies(w, s_copies, enough, pt, pools, inline_copy);
 }
 
 // U = used pages; the i-th used page >= U moves to the i-th free page < U.
@@ -290,25 +498,41 @@ __global__ void __launch_bounds__(kMetaThreads)
     pdl_wait();
     pdl_launch_dependents();
     const int tid = threadIdx.x;
-    int used = 0, here;
-    for (int p0 = 0; p0 < pt.n_pages; p0 += kMetaThreads) {
-        const int p = p0 + tid;
-        block_scan(p < pt.n_pages && ld_refs(pt.refs + p) > 0, &here);
+    constexpr int kStep = kMetaThreads * kScanPages;
+    int used = 0, here, r[kScanPages];
+    for (int p0 = 0; p0 < pt.n_pages; p0 += kStep) {
+        load_refs(pt, p0, r);
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < kScanPages; ++k)
+            mine += r[k] > 0 && p0 + tid * kScanPages + k < pt.n_pages;
+        block_scan(mine, &here);
         used += here;
     }
     int holes = 0, moved = 0;
-    for (int p0 = 0; p0 < pt.n_pages; p0 += kMetaThreads) {
-        const int p = p0 + tid;
-        const bool in = p < pt.n_pages;
-        const bool busy = in && ld_refs(pt.refs + p) > 0;
-        const int hole = in && p < used && !busy, move = busy && p >= used;
-        const int rh = holes + block_scan(hole, &here);
+    for (int p0 = 0; p0 < pt.n_pages; p0 += kStep) {
+        if (pt.n_pages > kStep) load_refs(pt, p0, r);  // else they are still here
+        const int p = p0 + tid * kScanPages;
+        int hole = 0, move = 0;
+#pragma unroll
+        for (int k = 0; k < kScanPages; ++k) {
+            hole += p + k < used && r[k] <= 0;
+            move += p + k >= used && p + k < pt.n_pages && r[k] > 0;
+        }
+        int rh = holes + block_scan(hole, &here);
         holes += here;
-        const int rm = moved + block_scan(move, &here);
+        int rm = moved + block_scan(move, &here);
         moved += here;
-        if (hole) gst(&w.copies[rh].dst, p);
-        if (move) gst(&w.copies[rm].src, p);
-        if (in && p >= used && !busy) gst(w.claimed + p, -1);  // a table may not name it
+#pragma unroll
+        for (int k = 0; k < kScanPages; ++k) {
+            if (p + k < used && r[k] <= 0) gst(&w.copies[rh++].dst, p + k);
+            if (p + k >= used && p + k < pt.n_pages) {
+                if (r[k] > 0)
+                    gst(&w.copies[rm++].src, p + k);
+                else
+                    gst(w.claimed + p + k, -1);  // a table may not name it
+            }
+        }
     }
     __syncthreads();
     for (int i = tid; i < moved; i += kMetaThreads) {
@@ -322,27 +546,13 @@ __global__ void __launch_bounds__(kMetaThreads)
     }
 }
 
-__device__ __forceinline__ void copy_pages(const PageWork &w, const PageTable &pt,
-                                           const PagePools &pools) {
-    const int n = gld(w.n_copies);
-    const int64_t page_bytes = pt.page_size * pools.token_bytes;
-    for (int64_t u = blockIdx.x; u < (int64_t)n * pools.L * 2; u += gridDim.x) {
-        const PageCopy c = gld(w.copies + u / (2 * pools.L));
-        const int rest = (int)(u % (2 * pools.L));
-        char *base = (char *)(rest & 1 ? pools.v : pools.k) +
-                     (int64_t)(rest >> 1) * pt.n_pages * page_bytes;
-        const uint4 *from = (const uint4 *)(base + c.src * page_bytes);
-        uint4 *to = (uint4 *)(base + c.dst * page_bytes);
-        const int q = (int)(c.rows * pools.token_bytes / 16);
-        for (int i = threadIdx.x; i < q; i += blockDim.x) st_plain(to + i, ld_plain(from + i));
-    }
-}
-
 __global__ void __launch_bounds__(kCopyThreads)
     k_pages_copy(PageTable pt, PagePools pools, PageWork w) {
     pdl_wait();
     pdl_launch_dependents();
-    copy_pages(w, pt, pools);
+    const int warps = kCopyThreads / 32;
+    copy_pages(w, gld(w.n_copies), pt, pools, blockIdx.x * warps + (threadIdx.x >> 5),
+               gridDim.x * warps);
 }
 
 // The moved pages' data, their refs, and every table entry that names one.
@@ -371,7 +581,7 @@ __global__ void __launch_bounds__(kCopyThreads)
                 gst(row + e, to);
         }
     }
-    copy_pages(w, pt, pools);
+    copy_pages(w, n, pt, pools, (int)(tid >> 5), (int)(threads >> 5));
 }
 
 // One warp copies a token's K (or V) row; the token's position is lens - D + j.
@@ -394,7 +604,7 @@ __global__ void __launch_bounds__(kCopyThreads)
         if (lane == 0) raise_error(SC_DEV_BAD_LENGTH);
         return;
     }
-    const int id = gld(table_row(pt, slot) + pos / pt.page_size);
+    const int id = gld(table_row(pt, slot) + full_pages(pt, pos));
     if (!page_ok(pt, id)) {
         if (lane == 0) raise_error(SC_DEV_BAD_PAGE);
         return;
@@ -402,7 +612,7 @@ __global__ void __launch_bounds__(kCopyThreads)
     const bool is_v = unit & 1;
     const uint4 *from = (const uint4 *)(is_v ? v + token * v_stride : k + token * k_stride);
     uint4 *to = (uint4 *)((char *)(is_v ? pools.v : pools.k) +
-                          ((int64_t)id * pt.page_size + pos % pt.page_size) * pools.token_bytes);
+                          ((int64_t)id * pt.page_size + part_of(pt, pos)) * pools.token_bytes);
     for (int64_t q = lane; q < pools.token_bytes / 16; q += 32) st_plain(to + q, ld_plain(from + q));
 }
 
@@ -414,26 +624,44 @@ size_t pages_workspace_bytes(int n_pages, int n) {
     return 16 + copies * sizeof(PageCopy) + ((size_t)n_pages + n) * 4;
 }
 
+// The plan of a resize or fork. One CTA is enough for a few thousand table entries; with
+// more, 8 share them (64 forks of 1025 pages: 46 us with one CTA). Copies of up to 128 KB
+// a CTA (were every listed sequence to need one) cost the cluster less than a second launch.
+struct MetaPlan {
+    unsigned ctas;
+    int inline_copy;
+};
+static MetaPlan meta_plan(const PageTable &pt, const PagePools &pools, int n) {
+    MetaPlan m;
+    m.ctas = (int64_t)n * pt.max_pages > 4096 ? 8 : 1;
+    m.inline_copy = (int64_t)n * pools.L * 2 * pt.page_size * pools.token_bytes <=
+                    (int64_t)m.ctas * (128 << 10);
+    return m;
+}
+
+template <typename F>
+static cudaError_t launch_meta(F kernel, const PageTable &pt, const int32_t *a, const int32_t *b,
+                               int n, const PagePools &pools, void *workspace, int sm_count,
+                               cudaStream_t stream) {
+    const PageWork w = page_work(workspace, pt.n_pages, n);
+    const MetaPlan m = meta_plan(pt, pools, n);
+    const cudaError_t e = launch_pdl_cluster(kernel, dim3(m.ctas), dim3(kMetaThreads), 0, stream,
+                                             m.ctas, pt, a, b, n, w, pools, m.inline_copy);
+    if (e != cudaSuccess || m.inline_copy) return e;
+    return launch_pdl(k_pages_copy, dim3((unsigned)(4 * sm_count)), dim3(kCopyThreads), 0, stream,
+                      pt, pools, w);
+}
+
 cudaError_t launch_pages_resize(const PageTable &pt, const int32_t *slots, const int32_t *new_lens,
                                 int n, const PagePools &pools, void *workspace, int sm_count,
                                 cudaStream_t stream) {
-    const PageWork w = page_work(workspace, pt.n_pages, n);
-    cudaError_t e = launch_pdl(k_pages_resize, dim3(1), dim3(kMetaThreads), 0, stream, pt, slots,
-                               new_lens, n, w);
-    if (e != cudaSuccess || pools.L == 0) return e;
-    return launch_pdl(k_pages_copy, dim3((unsigned)(4 * sm_count)), dim3(kCopyThreads), 0, stream,
-                      pt, pools, w);
+    return launch_meta(k_pages_resize, pt, slots, new_lens, n, pools, workspace, sm_count, stream);
 }
 
 cudaError_t launch_pages_fork(const PageTable &pt, const int32_t *src, const int32_t *dst, int n,
                               const PagePools &pools, void *workspace, int sm_count,
                               cudaStream_t stream) {
-    const PageWork w = page_work(workspace, pt.n_pages, n);
-    cudaError_t e =
-        launch_pdl(k_pages_fork, dim3(1), dim3(kMetaThreads), 0, stream, pt, src, dst, n, w);
-    if (e != cudaSuccess || pools.L == 0) return e;
-    return launch_pdl(k_pages_copy, dim3((unsigned)(4 * sm_count)), dim3(kCopyThreads), 0, stream,
-                      pt, pools, w);
+    return launch_meta(k_pages_fork, pt, src, dst, n, pools, workspace, sm_count, stream);
 }
 
 cudaError_t launch_pages_compact(const PageTable &pt, const PagePools &pools, int32_t *n_used,
