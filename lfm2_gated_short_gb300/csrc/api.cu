@@ -755,12 +755,14 @@ sc_status shortconv_draft_accept(sc_dtype dtype, int V, int N, int D, const void
                    {uniforms, nr * 4}}))
         return SC_EINVAL;
     if (N == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
     SC_BOUNDS_INSTALL(kUnitDraft, RO(target, n_p), RO(draft, n_q), RO(tokens, nd * 4),
                       RO(n_drafts, n_c), RO(uniforms, nr * 4), RW(accepted, (size_t)N * 4),
                       RW(out_tokens, nr * 4));
     return from_cuda(sc::launch_draft_accept(dtype, V, N, D, target, target_stride, draft,
                                              draft_stride, tokens, n_drafts, uniforms, accepted,
-                                             out_tokens, (cudaStream_t)stream));
+                                             out_tokens, sms, (cudaStream_t)stream));
 }
 
 sc_status shortconv_check_wait_limit(void *stream) {

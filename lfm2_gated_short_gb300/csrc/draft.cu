@@ -34,29 +34,38 @@ __device__ __forceinline__ float prob_of(const __nv_bfloat16 *p) {
     return __bfloat162float(gld(p));
 }
 
-// trunc(2^40 clamp(p, 0, 1)) = 2^20 hi + lo, hi and lo whole and below 2^20
-// (hi 2^20 for p = 1), as the bit patterns of 2^23 + hi and 2^23 + lo: adding
-// 2^23 rounded towards zero leaves a number's whole part in the low mantissa
-// bits, and what is left of 2^20 p after it is exact. Equal exponents make a
-// difference of patterns the difference of the numbers. A NaN saturates to 0.
-struct Weight {
-    int hi, lo;
-};
-__device__ __forceinline__ Weight weight_of(float saturated) {
-    const float x = saturated * 1048576.0f;
-    const float h = __fadd_rz(x, 8388608.0f);
-    const float l = __fmaf_rz(x - (h - 8388608.0f), 1048576.0f, 8388608.0f);
-    return {__float_as_int(h), __float_as_int(l)};
+// trunc(2^40 p) = 2^20 hi + lo for 0 <= p <= 1, hi and lo whole and below 2^20 (hi
+// 2^20 for p = 1), as the bit patterns of 2^23 + hi and 2^23 + lo: adding 2^23
+// rounded towards zero leaves a number's whole part in the low mantissa bits,
+// and what is left of 2^20 p after it is exact. Equal exponents make a
+// difference of patterns the difference of the numbers. Two numbers at once.
+__device__ __forceinline__ f32x2 f2_fma_rz(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 d;
+    asm("fma.rz.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
 }
-// (hi, lo) += max(weight(p) - weight(q), 0): truncation keeps the order of p and q.
+struct Weights {
+    f32x2 hi, lo;
+};
+__device__ __forceinline__ Weights weights_of(float p0, float p1) {
+    const f32x2 scale = f2_make(1048576.0f, 1048576.0f), whole = f2_make(8388608.0f, 8388608.0f);
+    const f32x2 p = f2_make(p0, p1);
+    const f32x2 h = f2_fma_rz(p, scale, whole);
+    const f32x2 rest = f2_fma(p, scale, f2_fma(h, f2_make(-1.0f, -1.0f), whole));
+    return {h, f2_fma_rz(rest, scale, whole)};
+}
+// (hi, lo) += max(weight(p) - weight(q), 0) of two elements, all in [0, 1]:
+// truncation keeps the order of p and q, so q is lowered to p where it is larger.
+__device__ __forceinline__ void add_rest(float p0, float p1, float q0, float q1, int &hi, int &lo) {
+    const Weights p = weights_of(p0, p1), q = weights_of(fminf(p0, q0), fminf(p1, q1));
+    hi += (int)p.hi - (int)q.hi;
+    hi += (int)(p.hi >> 32) - (int)(q.hi >> 32);
+    lo += (int)p.lo - (int)q.lo;
+    lo += (int)(p.lo >> 32) - (int)(q.lo >> 32);
+}
+// One element of any value: clamped, a NaN 0.
 __device__ __forceinline__ void add_rest(float p, float q, int &hi, int &lo) {
-    p = __saturatef(p);
-    q = __saturatef(q);
-    const Weight wp = weight_of(p), wq = weight_of(q);
-    if (p > q) {
-        hi += wp.hi - wq.hi;
-        lo += wp.lo - wq.lo;
-    }
+    add_rest(__saturatef(p), 0.0f, __saturatef(q), 0.0f, hi, lo);
 }
 __device__ __forceinline__ u64 whole_of(int hi, int lo) {
     return (u64)((long long)hi * 1048576 + lo);
@@ -89,7 +98,8 @@ struct Row16 {
         w[0] = ld_stream(at);
         if (mis) w[1] = ld_stream(at + 16);
     }
-    __device__ __forceinline__ void unpack(const uint4 (&v)[2], float (&f)[kVec]) const {
+    // The kVec elements as 4 words.
+    __device__ __forceinline__ void align(const uint4 (&v)[2], uint32_t (&out)[4]) const {
         uint32_t w[8] = {v[0].x, v[0].y, v[0].z, v[0].w, v[1].x, v[1].y, v[1].z, v[1].w};
         if (mis & 8) {  // mis is the same for the whole row
 #pragma unroll
@@ -104,6 +114,10 @@ struct Row16 {
             for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(w[k], w[k + 1], 16);
         }
 #pragma unroll
+        for (int k = 0; k < 4; ++k) out[k] = w[k];
+    }
+    static __device__ __forceinline__ void unpack(const uint32_t (&w)[4], float (&f)[kVec]) {
+#pragma unroll
         for (int k = 0; k < 4; ++k) {
             if constexpr (sizeof(T) == 4) {
                 f[k] = __uint_as_float(w[k]);
@@ -111,6 +125,20 @@ struct Row16 {
                 f[2 * k] = bf16_lo(w[k]);
                 f[2 * k + 1] = bf16_hi(w[k]);
             }
+        }
+    }
+    // Whether all elements of p and q are in [0, 1]: as whole numbers, larger bit patterns
+    // are larger numbers, infinity, NaN and everything negative.
+    static __device__ __forceinline__ bool plain(const uint32_t (&p)[4], const uint32_t (&q)[4]) {
+        if constexpr (sizeof(T) == 4) {
+            const uint32_t m = __vimax3_u32(__vimax3_u32(p[0], p[1], p[2]),
+                                            __vimax3_u32(p[3], q[0], q[1]), max(q[2], q[3]));
+            return m <= 0x3F800000u;
+        } else {
+            const uint32_t m = __vimax3_u16x2(__vimax3_u16x2(p[0], p[1], p[2]),
+                                              __vimax3_u16x2(p[3], q[0], q[1]),
+                                              __vmaxu2(q[2], q[3]));
+            return (m & 0xFFFFu) <= 0x3F80u && (m >> 16) <= 0x3F80u;
         }
     }
     // At the row's ends: element by element, zeros past V.
@@ -214,8 +242,7 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
             if (lane == 0) sums[c * kDraftWarps + warp] = s;
             mine += s;
         };
-        auto values = [&](const float (&fp)[kVec], const float (&fq)[kVec], int t, int &hi, int &lo) {
-            hi = lo = 0;
+        auto each = [&](const float (&fp)[kVec], const float (&fq)[kVec], int t, int &hi, int &lo) {
 #pragma unroll
             for (int e = 0; e < kVec; ++e)
                 add_rest(fp[e], rest && t + e == sure ? 1.0f : fq[e], hi, lo);
@@ -233,20 +260,30 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
                 }
 #pragma unroll
                 for (int x = 0; x < kAhead; ++x) {
-                    float fp[kVec], fq[kVec] = {};
-                    int hi, lo;
-                    p.unpack(wp[x], fp);
-                    if (use_q) q.unpack(wq[x], fq);
-                    values(fp, fq, t + x * kStep, hi, lo);
+                    float fp[kVec], fq[kVec];
+                    uint32_t up[4], uq[4] = {0u, 0u, 0u, 0u};
+                    int hi = 0, lo = 0;
+                    p.align(wp[x], up);
+                    if (use_q) q.align(wq[x], uq);
+                    R::unpack(up, fp);
+                    R::unpack(uq, fq);
+                    const int tx = t + x * kStep;
+                    if (R::plain(up, uq) && !(rest && (unsigned)(sure - tx) < kVec)) {
+#pragma unroll
+                        for (int e = 0; e < kVec; e += 2)
+                            add_rest(fp[e], fp[e + 1], fq[e], fq[e + 1], hi, lo);
+                    } else {
+                        each(fp, fq, tx, hi, lo);
+                    }
                     store(c + x, hi, lo);
                 }
                 c += kAhead;
             } else {
                 float fp[kVec], fq[kVec] = {};
-                int hi, lo;
+                int hi = 0, lo = 0;
                 p.get(t, fp);
                 if (use_q) q.get(t, fq);
-                values(fp, fq, t, hi, lo);
+                each(fp, fq, t, hi, lo);
                 store(c, hi, lo);
                 ++c;
             }
@@ -324,10 +361,16 @@ template <typename T>
 static cudaError_t launch_accept(int V, int N, int D, const void *target, int64_t target_stride,
                                  const void *draft, int64_t draft_stride, const int32_t *tokens,
                                  const int32_t *n_drafts, const float *uniforms, int32_t *accepted,
-                                 int32_t *out_tokens, cudaStream_t stream) {
+                                 int32_t *out_tokens, int sm_count, cudaStream_t stream) {
     constexpr int kChunk = kDraftThreads * (16 / (int)sizeof(T));
-    int C = 1;  // CTAs of a sequence: no more than give each a whole chunk
-    while (C < kMaxDraftCluster && V > C * kChunk) C *= 2;
+    // CTAs of a sequence: no more than give each a whole chunk, and all of them on the GPU
+    // at once (4 an SM: finding the rejected draft takes three memory latencies, which
+    // a second wave would pay again: 256 rows of 130051 in bf16 took 54 us with 8
+    // CTAs a row, 37 with 2); but the chunk sums have to fit (512 chunks, 32 KB).
+    int C = 1;
+    while (C < kMaxDraftCluster && V > C * kChunk &&
+           (2ll * N * C <= 4 * sm_count || V > C * kChunk * 512))
+        C *= 2;
     const int chunks = (V + C * kChunk - 1) / (C * kChunk);
     return launch_pdl_cluster(k_draft_accept<T>, dim3((unsigned)(N * C)), dim3(kDraftThreads),
                               (size_t)chunks * kDraftWarps * 8, stream, (unsigned)C, V, D, chunks,
@@ -339,10 +382,10 @@ cudaError_t launch_draft_accept(int dtype, int V, int N, int D, const void *targ
                                 int64_t target_stride, const void *draft, int64_t draft_stride,
                                 const int32_t *tokens, const int32_t *n_drafts,
                                 const float *uniforms, int32_t *accepted, int32_t *out_tokens,
-                                cudaStream_t stream) {
+                                int sm_count, cudaStream_t stream) {
     return (dtype == SC_BF16 ? launch_accept<__nv_bfloat16> : launch_accept<float>)(
         V, N, D, target, target_stride, draft, draft_stride, tokens, n_drafts, uniforms, accepted,
-        out_tokens, stream);
+        out_tokens, sm_count, stream);
 }
 
 cudaError_t take_error_draft(cudaStream_t stream, unsigned int *sum) {

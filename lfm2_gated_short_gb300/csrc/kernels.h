@@ -127,7 +127,7 @@ cudaError_t launch_draft_accept(int dtype, int V, int N, int D, const void *targ
                                 int64_t target_stride, const void *draft, int64_t draft_stride,
                                 const int32_t *tokens, const int32_t *n_drafts,
                                 const float *uniforms, int32_t *accepted, int32_t *out_tokens,
-                                cudaStream_t stream);
+                                int sm_count, cudaStream_t stream);
 cudaError_t take_error_draft(cudaStream_t stream, unsigned int *sum);
 
 // Attention over the paged cache (attention.cu), bf16.
