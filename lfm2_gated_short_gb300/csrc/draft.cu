@@ -14,6 +14,8 @@
 // product of two 32-bit floats in 64 bits, which is exact.
 //
 // Only row a of p and q is read whole: 2 V values a sequence.
+#include <atomic>
+
 #include "common.cuh"
 #include "errors.cuh"
 #include "kernels.h"
@@ -80,23 +82,42 @@ __device__ __forceinline__ u64 scaled_mark(u64 total, u64 m) {
 // multiple of kVec), zeros past V. A row may start anywhere (an odd V moves every
 // row): the two aligned 16-byte words that hold them are loaded and shifted;
 // a word that reaches outside the row is read by elements.
+constexpr int kPer = 2;  // vectors of a lane in a chunk, 32 vectors apart
+
+// Elements are numbered from `skip` before the row's start, where p's row has a 16-byte
+// boundary: every vector of p then is one aligned word, and q's is shifted by
+// the rows' difference only.
 template <typename T>
 struct Row16 {
     static constexpr int kVec = 16 / sizeof(T);
-    const T *row;
-    int V, mis;  // bytes from the aligned word before the row's start
+    const T *row;    // element 0: not read below `lo`
+    int lo, V, mis;  // valid elements [lo, V); bytes that element 0 lies past a boundary
 
-    __device__ __forceinline__ Row16(const T *p, int v)
-        : row(p), V(v), mis((int)(reinterpret_cast<uintptr_t>(p) & 15)) {}
+    __device__ __forceinline__ Row16(const T *p, int v, int skip)
+        : row(p - skip), lo(skip), V(v + skip),
+          mis((int)(reinterpret_cast<uintptr_t>(p - skip) & 15)) {}
 
     // Whether the words of [t, t + n) lie inside the row.
     __device__ __forceinline__ bool inside(int t, int n) const {
-        return t + n + kVec <= V && (mis == 0 || t > 0);
+        return t - mis / (int)sizeof(T) >= lo && t + n + (mis ? kVec : 0) <= V;
     }
-    __device__ __forceinline__ void fetch(int t, uint4 (&w)[2]) const {
-        const char *at = reinterpret_cast<const char *>(row + t) - mis;
-        w[0] = ld_stream(at);
-        if (mis) w[1] = ld_stream(at + 16);
+    // Start copying a warp's words of its chunk from element t on to `dst`, and the one
+    // after them that a row off alignment ends in.
+    __device__ __forceinline__ void copy(int t, uint32_t dst) const {
+        const int lane = threadIdx.x & 31;
+        const char *at = reinterpret_cast<const char *>(row + t) - mis + lane * 16;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) copy16(dst + (lane + 32 * k) * 16, at + 32 * 16 * k);
+        if (mis && lane == 0) copy16(dst + 32 * kPer * 16, at + 32 * kPer * 16);
+    }
+    static __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+        if (!SC_RD_OK(src, 16)) return;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    }
+    // The two words that hold this lane's k-th vector of what copy() brought.
+    __device__ __forceinline__ void take(const uint4 *at, int k, uint4 (&w)[2]) const {
+        w[0] = at[(threadIdx.x & 31) + 32 * k];
+        if (mis) w[1] = at[(threadIdx.x & 31) + 32 * k + 1];
     }
     // The kVec elements as 4 words.
     __device__ __forceinline__ void align(const uint4 (&v)[2], uint32_t (&out)[4]) const {
@@ -141,10 +162,11 @@ struct Row16 {
             return (m & 0xFFFFu) <= 0x3F80u && (m >> 16) <= 0x3F80u;
         }
     }
-    // At the row's ends: element by element, zeros past V.
+    // At the row's ends: element by element, zeros outside.
     __device__ __forceinline__ void get(int t, float (&f)[kVec]) const {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) f[e] = t + e < V ? prob_of(row + t + e) : 0.0f;
+        for (int e = 0; e < kVec; ++e)
+            f[e] = t + e >= lo && t + e < V ? prob_of(row + t + e) : 0.0f;
     }
 };
 
@@ -157,9 +179,15 @@ __device__ __forceinline__ u64 warp_scan(u64 v, int lane) {  // inclusive
     return v;
 }
 
+// A warp's copies in flight: kRing chunks of both rows.
+constexpr int kRing = 3;
+constexpr int kRingWords = 32 * kPer + 1;
+constexpr size_t kRingBytes = (size_t)kDraftWarps * kRing * 2 * kRingWords * 16;
+
 // A cluster of CTAs shares a sequence's row of V, one run of chunks each; a chunk is
-// one vector a thread. The sums of every (chunk, warp) stay in shared memory,
-// so the row is read once and then only the 32 vectors that hold the token again.
+// kPer vectors a thread. Each warp streams its part of the chunks through a ring of its own
+// (4 CTAs an SM: 192 KB in flight, where loads into registers left 50). The sums of every (chunk, warp) stay in shared memory,
+// so the row is read once and then only the 32 kPer vectors that hold the token again.
 // `sums` holds chunks * kDraftWarps entries.
 template <typename T>
 __global__ void __launch_bounds__(kDraftThreads, 4)
@@ -170,7 +198,10 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
                    int32_t *__restrict__ out_tokens) {
     using R = Row16<T>;
     constexpr int kVec = R::kVec;
-    extern __shared__ u64 sums[];
+    extern __shared__ uint4 dyn[];
+    const uint4 *ring = dyn + (threadIdx.x >> 5) * kRing * 2 * kRingWords;  // this warp's
+    const uint32_t ring_a = smem_addr(ring);
+    u64 *sums = reinterpret_cast<u64 *>(dyn + kRingBytes / 16);
     __shared__ int s_a, s_n;
     __shared__ u64 s_warp[kDraftWarps];
     __shared__ u64 s_total[2][kMaxDraftCluster];  // every CTA's sum, by pass
@@ -224,19 +255,20 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
         return;
     }
     const float r = gld(u + D);
-    const R p(target + (i * (D + 1) + a) * target_stride, V);
+    const T *p_row = target + (i * (D + 1) + a) * target_stride;
+    const int skip = (int)(reinterpret_cast<uintptr_t>(p_row) & 15) / (int)sizeof(T);
     const bool with_q = draft && a < s_n;
-    const R q(with_q ? draft + (i * D + a) * draft_stride : p.row, V);
-    const int sure = !draft && a < s_n ? gld(tokens + i * D + a) : -1;
+    const R p(p_row, V, skip);
+    const R q(with_q ? draft + (i * D + a) * draft_stride : p_row, V, skip);
+    const int sure = !draft && a < s_n ? gld(tokens + i * D + a) + skip : -1;
     bool rest = a < s_n;
-    constexpr int kStep = kDraftThreads * kVec;  // elements of a chunk
-    const int run = chunks * kStep;              // elements of a CTA
-    const int first = rank * run + tid * kVec;      // fits: V <= 2^22 and C <= 8
+    constexpr int kWarpStep = 32 * kPer * kVec, kStep = kDraftWarps * kWarpStep;  // of a chunk
+    const int run = chunks * kStep;              // elements of a CTA (V <= 2^22, C <= 8: fits)
     u64 total = 0, before = 0, here = 0;
     for (int pass = 0; pass < 2; ++pass) {  // the rest; the whole of p where nothing is left
         u64 mine = 0;
         const bool use_q = rest && with_q;
-        // One chunk's sum over the warp: at most 32 x kVec x 2^20 in hi, as much in lo.
+        // One chunk's sum over the warp: at most 32 kPer kVec 2^20 = 2^29 in hi, as much in lo.
         auto store = [&](int c, int hi, int lo) {
             const u64 s = whole_of(__reduce_add_sync(~0u, hi), __reduce_add_sync(~0u, lo));
             if (lane == 0) sums[c * kDraftWarps + warp] = s;
@@ -247,47 +279,72 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
             for (int e = 0; e < kVec; ++e)
                 add_rest(fp[e], rest && t + e == sure ? 1.0f : fq[e], hi, lo);
         };
-        constexpr int kAhead = 2;  // chunks loaded before the first is summed
-        for (int c = 0; c < chunks;) {
-            const int t = first + c * kStep, t0 = rank * run + c * kStep;
-            if (c + kAhead <= chunks && p.inside(t0, kAhead * kStep) &&
-                (!use_q || q.inside(t0, kAhead * kStep))) {
-                uint4 wp[kAhead][2], wq[kAhead][2];
-#pragma unroll
-                for (int x = 0; x < kAhead; ++x) {
-                    p.fetch(t + x * kStep, wp[x]);
-                    if (use_q) q.fetch(t + x * kStep, wq[x]);
-                }
-#pragma unroll
-                for (int x = 0; x < kAhead; ++x) {
-                    float fp[kVec], fq[kVec];
-                    uint32_t up[4], uq[4] = {0u, 0u, 0u, 0u};
-                    int hi = 0, lo = 0;
-                    p.align(wp[x], up);
-                    if (use_q) q.align(wq[x], uq);
-                    R::unpack(up, fp);
-                    R::unpack(uq, fq);
-                    const int tx = t + x * kStep;
-                    if (R::plain(up, uq) && !(rest && (unsigned)(sure - tx) < kVec)) {
-#pragma unroll
-                        for (int e = 0; e < kVec; e += 2)
-                            add_rest(fp[e], fp[e + 1], fq[e], fq[e + 1], hi, lo);
-                    } else {
-                        each(fp, fq, tx, hi, lo);
-                    }
-                    store(c + x, hi, lo);
-                }
-                c += kAhead;
-            } else {
+        // This warp's chunks [c0, c1) are whole; the rest, at the row's ends, is read by elements.
+        const int tw = rank * run + warp * kWarpStep;
+        int c0 = 0, c1 = chunks;
+        auto whole = [&](int c) {
+            return p.inside(tw + c * kStep, kWarpStep) &&
+                   (!use_q || q.inside(tw + c * kStep, kWarpStep));
+        };
+        while (c0 < chunks && tw + c0 * kStep < V && !whole(c0)) ++c0;
+        while (c1 > c0 && !whole(c1 - 1)) --c1;
+        for (int c = 0; c < chunks; ++c) {
+            if (c == c0 && c1 > c0) c = c1;
+            if (c == chunks) break;
+            int hi = 0, lo = 0;
+            for (int k = 0; k < kPer; ++k) {
                 float fp[kVec], fq[kVec] = {};
-                int hi = 0, lo = 0;
+                const int t = tw + c * kStep + (lane + 32 * k) * kVec;
                 p.get(t, fp);
                 if (use_q) q.get(t, fq);
                 each(fp, fq, t, hi, lo);
-                store(c, hi, lo);
-                ++c;
             }
+            store(c, hi, lo);
         }
+        int put = 0, take = 0;  // ring slots
+        auto start = [&](int c) {
+            if (c < c1) {
+                const uint32_t dst = ring_a + put * 2 * kRingWords * 16;
+                p.copy(tw + c * kStep, dst);
+                if (use_q) q.copy(tw + c * kStep, dst + kRingWords * 16);
+            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            put = put + 1 == kRing ? 0 : put + 1;
+        };
+        for (int k = 0; k < kRing - 1; ++k) start(c0 + k);
+        for (int c = c0; c < c1; ++c) {
+            start(c + kRing - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+            __syncwarp();
+            const uint4 *at = ring + take * 2 * kRingWords;
+            take = take + 1 == kRing ? 0 : take + 1;
+            int hi = 0, lo = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                float fp[kVec], fq[kVec];
+                uint4 raw[2];
+                uint32_t uq[4] = {0u, 0u, 0u, 0u};
+                const int t = tw + c * kStep + (lane + 32 * k) * kVec;
+                const uint4 pw = at[lane + 32 * k];
+                const uint32_t up[4] = {pw.x, pw.y, pw.z, pw.w};
+                if (use_q) {
+                    q.take(at + kRingWords, k, raw);
+                    q.align(raw, uq);
+                }
+                R::unpack(up, fp);
+                R::unpack(uq, fq);
+                if (R::plain(up, uq) && !(rest && (unsigned)(sure - t) < kVec)) {
+#pragma unroll
+                    for (int e = 0; e < kVec; e += 2)
+                        add_rest(fp[e], fp[e + 1], fq[e], fq[e + 1], hi, lo);
+                } else {
+                    each(fp, fq, t, hi, lo);
+                }
+            }
+            store(c, hi, lo);
+            __syncwarp();  // the words are read before the slot is copied to again
+        }
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
         if (lane == 0) s_warp[warp] = mine;
         __syncthreads();
         here = 0;
@@ -331,29 +388,36 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
         sum += __shfl_sync(~0u, inc, 31);
     }
     if (at < 0) return;  // cannot be: the run's sum holds the mark
-    const int t = rank * run + (at / kDraftWarps * kDraftThreads + at % kDraftWarps * 32 + lane) * kVec;
-    u64 w[kVec], mine = 0;
-    float fp[kVec], fq[kVec] = {};
-    p.get(t, fp);
-    if (rest && with_q) q.get(t, fq);
-#pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-        int hi = 0, lo = 0;
-        add_rest(fp[e], rest && t + e == sure ? 1.0f : fq[e], hi, lo);
-        w[e] = whole_of(hi, lo);
-        mine += w[e];
-    }
-    const u64 inc = warp_scan(mine, lane);
-    const unsigned hit = __ballot_sync(~0u, sum + inc > mark);
-    if (hit && lane == __ffs(hit) - 1) {
-        u64 acc = sum + inc - mine;
-        int pick = t;
+    for (int k = 0; k < kPer; ++k) {
+        const int t = rank * run + at / kDraftWarps * kStep + at % kDraftWarps * kWarpStep +
+                      (lane + 32 * k) * kVec;
+        u64 w[kVec], mine = 0;
+        float fp[kVec], fq[kVec] = {};
+        p.get(t, fp);
+        if (rest && with_q) q.get(t, fq);
 #pragma unroll
         for (int e = 0; e < kVec; ++e) {
-            acc += w[e];
-            if (acc <= mark) pick = t + e + 1;
+            int hi = 0, lo = 0;
+            add_rest(fp[e], rest && t + e == sure ? 1.0f : fq[e], hi, lo);
+            w[e] = whole_of(hi, lo);
+            mine += w[e];
         }
-        gst(out + a, pick);
+        const u64 inc = warp_scan(mine, lane);
+        const unsigned hit = __ballot_sync(~0u, sum + inc > mark);
+        if (hit) {
+            if (lane == __ffs(hit) - 1) {
+                u64 acc = sum + inc - mine;
+                int pick = t;
+#pragma unroll
+                for (int e = 0; e < kVec; ++e) {
+                    acc += w[e];
+                    if (acc <= mark) pick = t + e + 1;
+                }
+                gst(out + a, pick - skip);
+            }
+            return;
+        }
+        sum += __shfl_sync(~0u, inc, 31);
     }
 }
 
@@ -362,18 +426,29 @@ static cudaError_t launch_accept(int V, int N, int D, const void *target, int64_
                                  const void *draft, int64_t draft_stride, const int32_t *tokens,
                                  const int32_t *n_drafts, const float *uniforms, int32_t *accepted,
                                  int32_t *out_tokens, int sm_count, cudaStream_t stream) {
-    constexpr int kChunk = kDraftThreads * (16 / (int)sizeof(T));
+    constexpr int kChunk = kDraftThreads * kPer * (16 / (int)sizeof(T));
     // CTAs of a sequence: no more than give each a whole chunk, and all of them on the GPU
     // at once (4 an SM: finding the rejected draft takes three memory latencies, which
-    // a second wave would pay again: 256 rows of 130051 in bf16 took 54 us with 8
-    // CTAs a row, 37 with 2); but the chunk sums have to fit (512 chunks, 32 KB).
+    // a second wave would pay again); but the chunk sums have to fit (512 chunks, 32 KB).
     int C = 1;
     while (C < kMaxDraftCluster && V > C * kChunk &&
            (2ll * N * C <= 4 * sm_count || V > C * kChunk * 512))
         C *= 2;
-    const int chunks = (V + C * kChunk - 1) / (C * kChunk);
-    return launch_pdl_cluster(k_draft_accept<T>, dim3((unsigned)(N * C)), dim3(kDraftThreads),
-                              (size_t)chunks * kDraftWarps * 8, stream, (unsigned)C, V, D, chunks,
+    // Up to a vector less one before the row (see Row16).
+    const int chunks = (V + 16 / (int)sizeof(T) - 1 + C * kChunk - 1) / (C * kChunk);
+    const size_t smem = kRingBytes + (size_t)chunks * kDraftWarps * 8;
+    static std::atomic<unsigned long long> done{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 64 || !(done.load() & (1ull << dev))) {
+        e = cudaFuncSetAttribute(k_draft_accept<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kRingBytes + 513 * kDraftWarps * 8));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) done.fetch_or(1ull << dev);
+    }
+    return launch_pdl_cluster(k_draft_accept<T>, dim3((unsigned)(N * C)), dim3(kDraftThreads), smem,
+                              stream, (unsigned)C, V, D, chunks,
                               (const T *)target, target_stride, (const T *)draft, draft_stride,
                               tokens, n_drafts, uniforms, accepted, out_tokens);
 }
