@@ -19,6 +19,8 @@
 #include <cuda.h>
 #include <cuda_bf16.h>
 
+#include <limits.h>
+
 #include <atomic>
 #include <mutex>
 
@@ -163,7 +165,7 @@ __device__ __forceinline__ float ex2(float x) {
 // RG groups of 16 rows. A CTA's consumer warps are 4 key groups (16 keys of a
 // tile) times RG row groups. Shared memory and registers allow 3 CTAs an SM
 // for 16 rows of 64, 2 for 32 of 64 or 16 of 128, 1 for 32 of 128; either way
-// 160 to 192 KB of tiles are in flight.
+// 128 to 144 KB of tiles are in flight.
 template <int DH, int RG>
 struct OwnCfg {
     static constexpr int MR = 16 * RG;
@@ -173,10 +175,10 @@ struct OwnCfg {
     static constexpr uint32_t kBlk = kKT * 128;               // one block of a tile, 8 KB
     static constexpr uint32_t kStage = 2 * NB * kBlk;         // K and V of a tile
     static constexpr int kCtas = DH == 64 ? (RG == 1 ? 3 : 2) : (RG == 1 ? 2 : 1);
-    static constexpr int kStages = DH == 64 ? (RG == 1 ? 4 : 5) : (RG == 1 ? 3 : 5);
+    static constexpr int kStages = DH == 64 ? (RG == 1 ? 3 : 4) : (RG == 1 ? 2 : 4);
     static constexpr uint32_t kQ = MR * 128 * NB;
-    static constexpr int kOs = DH + 4;                        // floats of a joined O row
-    static constexpr uint32_t kJoin = (MR * kOs + 2 * kKeyWarps * MR) * 4;
+    static constexpr int kOs = DH + 4;                        // floats of a row to join
+    static constexpr uint32_t kJoin = kKeyWarps * MR * (kOs + 2) * 4;  // O, m, l of each key warp
     static constexpr size_t kSmem = 1024 + kStages * kStage + kQ + kJoin;
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part
 };
@@ -190,8 +192,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t s_full[ST], s_empty[ST];
     __shared__ int s_bad[ST];
-    __shared__ int64_t s_scan[kThreads];
-    __shared__ int s_seq;
+    __shared__ int64_t s_scan[kThreads / 32];
+    __shared__ int s_seq, s_slot, s_len;
     __shared__ int64_t s_seq_unit;
     const uint32_t raw_a = smem_addr(raw);
     unsigned char *ring = raw + (((raw_a + 1023u) & ~1023u) - raw_a);
@@ -210,7 +212,6 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         tma_prefetch_map(&mk);
         tma_prefetch_map(&mv);
         s_seq = a.N;
-        s_seq_unit = 0;
     }
     __syncthreads();
     pdl_wait();
@@ -222,35 +223,42 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     const int rows = a.D * a.G;
     const int RT = (rows + C::MR - 1) / C::MR;
     const int per = RT * a.Hkv;  // items of a sequence
-    int64_t U = 0, u0 = 0, u1 = 0;
-    int n_cta = 1;
+    int64_t U = 0, u0 = 0, u1 = 0, mine = 0;
+    int n_cta = 1, slot = 0, len = -1;
     for (int pass = 0; pass < 2; ++pass) {
         int64_t base = 0;
         for (int i0 = 0; i0 < a.N; i0 += kThreads) {
             const int i = i0 + tid;
-            int slot;
-            int64_t mine = 0;
-            if (i < a.N)
-                mine = (int64_t)per *
-                       own_tiles(a, seq_len(a, i, &slot, pass == 0 && blockIdx.x == 0));
-            s_scan[tid] = mine;
-            __syncthreads();
-            for (int o = 1; o < kThreads; o <<= 1) {
-                const int64_t v = tid >= o ? s_scan[tid - o] : 0;
-                __syncthreads();
-                s_scan[tid] += v;
-                __syncthreads();
+            if (pass == 0 || a.N > kThreads) {  // else this thread's sequence is still here
+                len = i < a.N ? seq_len(a, i, &slot, pass == 0 && blockIdx.x == 0) : -1;
+                mine = (int64_t)per * own_tiles(a, len);
             }
-            const int64_t begin = base + s_scan[tid] - mine;
+            int64_t inc = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t up = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += up;
+            }
+            __syncthreads();
+            if (lane == 31) s_scan[warp] = inc;
+            __syncthreads();
+            int64_t before = base, all = base;
+#pragma unroll
+            for (int k = 0; k < kThreads / 32; ++k) {
+                if (k < warp) before += s_scan[k];
+                all += s_scan[k];
+            }
+            const int64_t begin = before + inc - mine;
             if (pass == 1 && i < a.N) {
                 if (u0 >= begin && u0 < begin + mine) {
                     s_seq = i;
+                    s_slot = slot;
+                    s_len = len;
                     s_seq_unit = begin;
                 }
                 if (blockIdx.x == 0) gst(a.cum + i, begin);
             }
-            base += s_scan[kThreads - 1];
-            __syncthreads();
+            base = all;
         }
         if (pass == 0) {
             U = base;
@@ -261,26 +269,35 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             if ((int)blockIdx.x >= n_cta && blockIdx.x > 0) return;
         }
     }
-    if (u0 >= u1) return;
+    __syncthreads();
+    if (u0 >= u1 || s_seq >= a.N) return;
 
     // Walk the CTA's units: f(i, slot, len, rt, h, w, first tile, tiles, T) for each
     // item piece, in order, until it returns false.
     auto walk = [&](auto &&f) {
-        int64_t u = u0, begin = s_seq_unit;
-        int i = s_seq;
-        while (u < u1 && i < a.N) {
-            int slot;
-            const int len = seq_len(a, i, &slot, false);
-            const int T = own_tiles(a, len);
-            const int64_t end = begin + (int64_t)T * per;
-            while (u < end && u < u1) {
-                const int it = (int)((u - begin) / T), t0 = (int)((u - begin) % T);
-                const int n = (int)min((int64_t)(T - t0), u1 - u);
-                if (!f(i, slot, len, it / a.Hkv, it % a.Hkv, i * per + it, t0, n, T)) return;
-                u += n;
+        int64_t left = u1 - u0;
+        int i = s_seq, slot = s_slot, len = s_len;
+        int T = own_tiles(a, len);
+        int it = (int)((u0 - s_seq_unit) / T), t0 = (int)(u0 - s_seq_unit - (int64_t)it * T);
+        int rt = it / a.Hkv, h = it - rt * a.Hkv;
+        while (true) {
+            for (; it < per; ++it) {
+                const int n = (int)min((int64_t)(T - t0), left);
+                if (!f(i, slot, len, rt, h, i * per + it, t0, n, T)) return;
+                left -= n;
+                if (left <= 0) return;
+                t0 = 0;
+                if (++h == a.Hkv) {
+                    h = 0;
+                    ++rt;
+                }
             }
-            begin = end;
-            ++i;
+            do {  // the next sequence with keys of its own
+                if (++i >= a.N) return;
+                len = seq_len(a, i, &slot, false);
+                T = own_tiles(a, len);
+            } while (T == 0);
+            it = rt = h = 0;
         }
     };
 
@@ -332,16 +349,42 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     uint32_t g = 0;
     bool dead = false;
     const int kw = warp % kKeyWarps, rg = warp / kKeyWarps;  // key and row group
-    const int group_bar = 2 + rg;                            // barrier of a row group's warps
-    walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
-        // The item's query rows, and the keys that this thread's two rows see.
+    // What a thread does with the rows of row tile rt, the same for every item: the
+    // query chunks it loads, the tokens of the two rows it computes, the chunks of
+    // output rows it writes (offset -1: past the item's rows).
+    constexpr int kQn = C::MR * DH / 8 / (32 * C::kWarps);
+    constexpr int kOn = 16 * DH / 4 / (32 * kKeyWarps);
+    const int gt = kw * 32 + lane;  // thread of the row group
+    int rt_now = -1, q_row[kQn], q_off[kQn], row_j[2], o_off[kOn];
+    auto set_rows = [&](int rt) {
+        rt_now = rt;
         const int r0 = rt * C::MR;
-        for (int x = tid; x < C::MR * DH / 8; x += 32 * C::kWarps) {
-            const int r = x / (DH / 8), ch = x % (DH / 8), rr = r0 + r;
+#pragma unroll
+        for (int k = 0; k < kQn; ++k) {
+            const int x = tid + k * 32 * C::kWarps, rr = r0 + x / (DH / 8);
+            q_row[k] = rr < rows ? rr / a.G : -1;
+            q_off[k] = rr % a.G * DH + x % (DH / 8) * 8;
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int rr = r0 + rg * 16 + p * 8 + (lane >> 2);
+            row_j[p] = rr < rows ? rr / a.G : INT_MIN / 2;
+        }
+#pragma unroll
+        for (int k = 0; k < kOn; ++k) {
+            const int x = gt + k * 32 * kKeyWarps, rr = r0 + rg * 16 + x / (DH / 4);
+            o_off[k] = rr < rows ? (rr / a.G * a.Hkv * a.G + rr % a.G) * DH + x % (DH / 4) * 4 : -1;
+        }
+    };
+    walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
+        if (rt != rt_now) set_rows(rt);
+#pragma unroll
+        for (int k = 0; k < kQn; ++k) {
+            const int x = tid + k * 32 * C::kWarps, r = x / (DH / 8), ch = x % (DH / 8);
             uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (rr < rows)
-                v = ld_plain(a.q + ((int64_t)i * a.D + rr / a.G) * a.q_stride +
-                             (h * a.G + rr % a.G) * DH + ch * 8);
+            if (q_row[k] >= 0)
+                v = ld_plain(a.q + ((int64_t)i * a.D + q_row[k]) * a.q_stride + h * a.G * DH +
+                             q_off[k]);
             *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::MR * 128 + swz(r, ch & 7)) = v;
         }
         named_sync(1, 32 * C::kWarps);
@@ -355,8 +398,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         float m[2], l[2], o[DH / 8][4];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
-            const int rr = r0 + rg * 16 + p * 8 + (lane >> 2);
-            see[p] = rr < rows ? len - a.D + rr / a.G + 1 : 0;
+            see[p] = len - a.D + 1 + row_j[p];  // below zero for a row past the item's
             m[p] = -INFINITY;
             l[p] = 0.0f;
         }
@@ -455,81 +497,63 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[s]);
         }
-        // Join the key warps: the common maximum, then O and l in turn.
-        float *jm = join + C::MR * C::kOs, *jl = jm + kKeyWarps * C::MR;
+        // Join the key warps: each leaves its m, l and O, and a thread joins and writes
+        // four columns of a row. (The next join comes after the next item's barrier.)
+        float *jo = join + rg * kKeyWarps * 16 * C::kOs;  // [key warp][16][kOs]
+        float *jm = join + kKeyWarps * C::MR * C::kOs + rg * kKeyWarps * 32;  // [key warp][m 16, l 16]
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
+            const int r = p * 8 + (lane >> 2);
             l[p] += __shfl_xor_sync(~0u, l[p], 1);
             l[p] += __shfl_xor_sync(~0u, l[p], 2);
-            if ((lane & 3) == 0) jm[kw * C::MR + rg * 16 + p * 8 + (lane >> 2)] = m[p];
-        }
-        named_sync(group_bar, 32 * kKeyWarps);
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int r = rg * 16 + p * 8 + (lane >> 2);
-            float top = -INFINITY;
-#pragma unroll
-            for (int k = 0; k < kKeyWarps; ++k) top = fmaxf(top, jm[k * C::MR + r]);
-            const float f = ex2(m[p] - (top == -INFINITY ? 0.0f : top));
-            if ((lane & 3) == 0) jl[kw * C::MR + r] = l[p] * f;
-#pragma unroll
-            for (int d = 0; d < DH / 8; ++d) {
-                o[d][2 * p] *= f;
-                o[d][2 * p + 1] *= f;
+            if ((lane & 3) == 0) {
+                jm[kw * 32 + r] = m[p];
+                jm[kw * 32 + 16 + r] = l[p];
             }
+#pragma unroll
+            for (int d = 0; d < DH / 8; ++d)
+                *reinterpret_cast<float2 *>(jo + (kw * 16 + r) * C::kOs + d * 8 + (lane & 3) * 2) =
+                    make_float2(o[d][2 * p], o[d][2 * p + 1]);
         }
-        constexpr int kQuarter = DH / 8 / kKeyWarps;
-#pragma unroll
-        for (int round = 0; round < kKeyWarps; ++round) {
-            const int blk = (kw + round) % kKeyWarps;  // each warp adds another quarter
-#pragma unroll
-            for (int d = 0; d < DH / 8; ++d) {
-                if (d / kQuarter != blk) continue;
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    float2 *at = reinterpret_cast<float2 *>(
-                        join + (rg * 16 + p * 8 + (lane >> 2)) * C::kOs + d * 8 + (lane & 3) * 2);
-                    float2 v = round ? *at : make_float2(0.0f, 0.0f);
-                    v.x += o[d][2 * p];
-                    v.y += o[d][2 * p + 1];
-                    *at = v;
-                }
-            }
-            named_sync(group_bar, 32 * kKeyWarps);
-        }
+        named_sync(1, 32 * C::kWarps);  // also: every warp has read this item's queries
         const bool whole = n == T && a.shared_keys == 0;  // nothing to join with
         float *part = a.own_part + (int64_t)(w + blockIdx.x) * C::kSlot;
-        const int gt = kw * 32 + lane;  // thread of the row group
-        for (int x = gt; x < 16 * DH / 4; x += 32 * kKeyWarps) {
-            const int r = rg * 16 + x / (DH / 4), c4 = x % (DH / 4), rr = r0 + r;
-            float4 v = *reinterpret_cast<float4 *>(join + r * C::kOs + c4 * 4);
-            if (rr >= rows) continue;
-            if (whole) {
-                if (bad) continue;
-                float sum = 0.0f;
+        bf16 *out = a.out + ((int64_t)i * a.D * a.Hkv + h) * a.G * DH;
 #pragma unroll
-                for (int k = 0; k < kKeyWarps; ++k) sum += jl[k * C::MR + r];
-                const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-                gst(reinterpret_cast<uint2 *>(a.out + (((int64_t)i * a.D + rr / a.G) * a.Hkv + h) *
-                                                          a.G * DH + (rr % a.G) * DH + c4 * 4),
-                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
-            } else {
-                gst(reinterpret_cast<float4 *>(part + r * DH + c4 * 4), v);
-            }
-        }
-        if (!whole && gt < 16) {
-            const int r = rg * 16 + gt;
+        for (int k = 0; k < kOn; ++k) {
+            const int x = gt + k * 32 * kKeyWarps, r = x / (DH / 4), c4 = x % (DH / 4);
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int k = 0; k < kKeyWarps; ++k) {
-                top = fmaxf(top, jm[k * C::MR + r]);
-                sum += jl[k * C::MR + r];
+            for (int q = 0; q < kKeyWarps; ++q) top = fmaxf(top, jm[q * 32 + r]);
+            const float off = top == -INFINITY ? 0.0f : top;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < kKeyWarps; ++q) {
+                const float f = ex2(jm[q * 32 + r] - off);
+                const float4 u =
+                    *reinterpret_cast<float4 *>(jo + (q * 16 + r) * C::kOs + c4 * 4);
+                sum = fmaf(f, jm[q * 32 + 16 + r], sum);
+                v.x = fmaf(f, u.x, v.x);
+                v.y = fmaf(f, u.y, v.y);
+                v.z = fmaf(f, u.z, v.z);
+                v.w = fmaf(f, u.w, v.w);
             }
-            // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
-            gst(part + C::MR * DH + r, bad ? __int_as_float(0x7FC00000) : top);
-            gst(part + C::MR * DH + C::MR + r, sum);
+            if (o_off[k] < 0) continue;
+            if (whole) {
+                if (bad) continue;
+                const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+                gst(reinterpret_cast<uint2 *>(out + o_off[k]),
+                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
+            } else {
+                const int row = rg * 16 + r;
+                gst(reinterpret_cast<float4 *>(part + row * DH + c4 * 4), v);
+                if (c4 == 0) {
+                    // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
+                    gst(part + C::MR * DH + row, bad ? __int_as_float(0x7FC00000) : top);
+                    gst(part + C::MR * DH + C::MR + row, sum);
+                }
+            }
         }
-        named_sync(1, 32 * C::kWarps);  // join and Q are written again by the next item
         return true;
     });
 }
