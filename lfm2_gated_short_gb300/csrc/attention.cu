@@ -41,6 +41,7 @@ constexpr int kKeyWarps = 4;       // 16 keys of a tile each
 constexpr int kMaxCtas = 456;      // three CTAs on each of 152 SMs
 constexpr int kMaxPrefixCtas = 152;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRescaleLog2 = 8.0f;  // a running maximum moves when a score passes it by 2^8
 
 struct AttnArgs {
     const bf16 *q;
@@ -156,6 +157,16 @@ __device__ __forceinline__ uint32_t swz(int row, int chunk) {
     return (uint32_t)(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+    return r;
+}
+__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
+    f32x2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -346,9 +357,14 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         return;
     }
 
-    uint32_t g = 0;
+    uint32_t ring_at = 0, ring_phase = 0;
     bool dead = false;
     const int kw = warp % kKeyWarps, rg = warp / kKeyWarps;  // key and row group
+    // This lane's ldmatrix address in a K and in a V block: a step of 16 columns flips bits 5, 6.
+    const uint32_t k_lane = swz(kw * 16 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    const uint32_t v_lane = swz(kw * 16 + (lane & 15), lane >> 4);
+    const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
+    const float rescale = kRescaleLog2 / a.scale_log2;
     // What a thread does with the rows of row tile rt, the same for every item: the
     // query chunks it loads, the tokens of the two rows it computes, the chunks of
     // output rows it writes (offset -1: past the item's rows).
@@ -394,13 +410,17 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             const int ch = kk * 2 + (lane >> 4);
             ldsm4(qf[kk], qs_a + (ch >> 3) * C::MR * 128 + swz(rg * 16 + (lane & 15), ch & 7));
         }
+        // A row's running maximum m (of the scores before scaling), the score that moves
+        // it, and its offset -m scale; the sums of its weights in pairs.
         int see[2];
-        float m[2], l[2], o[DH / 8][4];
+        float m[2], limit[2], off[2], o[DH / 8][4];
+        f32x2 l2[2];
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             see[p] = len - a.D + 1 + row_j[p];  // below zero for a row past the item's
-            m[p] = -INFINITY;
-            l[p] = 0.0f;
+            m[p] = limit[p] = -INFINITY;
+            off[p] = 0.0f;
+            l2[p] = f2_make(0.0f, 0.0f);
         }
         const int least = len - a.D + 1;  // keys that every row of the sequence sees
 #pragma unroll
@@ -408,23 +428,23 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
         bool bad = false;
-        for (int t = 0; t < n; ++t, ++g) {
-            const uint32_t s = g % ST;
-            if (!dead && !mbar_wait_bounded(&s_full[s], (g / ST) & 1u)) {
+        int key0 = a.shared_keys + t0 * kKT + kw * 16;
+        for (int t = 0; t < n; ++t, key0 += kKT) {
+            if (!dead && !mbar_wait_bounded(&s_full[ring_at], ring_phase)) {
                 raise_error(SC_DEV_TIMEOUT);
                 dead = true;  // no more waits: the rest runs through on what is there
             }
-            bad |= s_bad[s] != 0;
-            const uint32_t kt = ring_a + s * C::kStage, vt = kt + C::NB * C::kBlk;
-            const int key0 = a.shared_keys + (t0 + t) * kKT + kw * 16;
+            bad |= s_bad[ring_at] != 0;
+            const uint32_t stage = ring_a + ring_at * C::kStage;
+            const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
             const bool tail = key0 + 16 > len;
             if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
                 const int from = max(0, len - key0);
                 for (int x = lane; x < (16 - from) * C::NB * 8; x += 32) {
                     const int r = from + x / (C::NB * 8), ch = x % (C::NB * 8);
-                    *reinterpret_cast<uint4 *>(ring + s * C::kStage + (C::NB + (ch >> 3)) * C::kBlk +
-                                               (kw * 16 + r) * 128 + (ch & 7) * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
+                    *reinterpret_cast<uint4 *>(ring + ring_at * C::kStage +
+                                               (C::NB + (ch >> 3)) * C::kBlk + (kw * 16 + r) * 128 +
+                                               (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 __syncwarp();
             }
@@ -434,9 +454,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 #pragma unroll
             for (int kk = 0; kk < DH / 16; ++kk) {
                 uint32_t b[4];
-                const int row = kw * 16 + (lane & 7) + ((lane >> 4) << 3);
-                const int ch = kk * 2 + ((lane >> 3) & 1);
-                ldsm4(b, kt + (ch >> 3) * C::kBlk + swz(row, ch & 7));
+                ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk);
                 mma16816(sc[0], qf[kk], b[0], b[1]);
                 mma16816(sc[1], qf[kk], b[2], b[3]);
             }
@@ -451,18 +469,20 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             float top[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                top[p] = fmaxf(fmaxf(sc[0][2 * p], sc[0][2 * p + 1]),
-                               fmaxf(sc[1][2 * p], sc[1][2 * p + 1]));
+                top[p] = fmaxf(max3(sc[0][2 * p], sc[0][2 * p + 1], sc[1][2 * p]), sc[1][2 * p + 1]);
                 top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-                top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2)) * a.scale_log2;
+                top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
             }
-            if (__any_sync(~0u, top[0] > m[0] || top[1] > m[1])) {
+            // A row that has seen no key yet keeps m = -inf, offset 0 and sums of zero.
+            if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const float to = fmaxf(m[p], top[p]);
-                    const float f = to == -INFINITY ? 1.0f : ex2(m[p] - to);
-                    m[p] = to;
-                    l[p] *= f;
+                    if (!(top[p] > limit[p])) continue;
+                    const float f = ex2((m[p] - top[p]) * a.scale_log2);
+                    m[p] = top[p];
+                    limit[p] = top[p] + rescale;
+                    off[p] = -top[p] * a.scale_log2;
+                    l2[p] = f2_mul(l2[p], f2_make(f, f));
 #pragma unroll
                     for (int d = 0; d < DH / 8; ++d) {
                         o[d][2 * p] *= f;
@@ -473,13 +493,14 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             uint32_t pf[4];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                // A row that has seen no key yet keeps m = -inf and sums of zero.
-                const float off = m[p] == -INFINITY ? 0.0f : -m[p];
+                const f32x2 off2 = f2_make(off[p], off[p]);
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt) {
-                    const float e0 = ex2(fmaf(sc[nt][2 * p], a.scale_log2, off));
-                    const float e1 = ex2(fmaf(sc[nt][2 * p + 1], a.scale_log2, off));
-                    l[p] += e0 + e1;
+                    float e0, e1;
+                    f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    l2[p] = f2_add(l2[p], f2_make(e0, e1));
                     // P enters the second product as bf16: 2^-8 relative a term at most.
                     pf[nt * 2 + p] = pack_bf16(e0, e1);
                 }
@@ -487,15 +508,17 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 #pragma unroll
             for (int dd = 0; dd < DH / 16; ++dd) {
                 uint32_t b[4];
-                const int row = kw * 16 + (lane & 15);
-                const int ch = dd * 2 + (lane >> 4);
-                ldsm4_t(b, vt + (ch >> 3) * C::kBlk + swz(row, ch & 7));
+                ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk);
                 mma16816(o[2 * dd], pf, b[0], b[1]);
                 mma16816(o[2 * dd + 1], pf, b[2], b[3]);
             }
             if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[s]);
+            if (lane == 0) mbar_arrive(&s_empty[ring_at]);
+            if (++ring_at == ST) {
+                ring_at = 0;
+                ring_phase ^= 1u;
+            }
         }
         // Join the key warps: each leaves its m, l and O, and a thread joins and writes
         // four columns of a row. (The next join comes after the next item's barrier.)
@@ -504,11 +527,14 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int r = p * 8 + (lane >> 2);
-            l[p] += __shfl_xor_sync(~0u, l[p], 1);
-            l[p] += __shfl_xor_sync(~0u, l[p], 2);
+            float l, l1;
+            f2_split(l2[p], l, l1);
+            l += l1;
+            l += __shfl_xor_sync(~0u, l, 1);
+            l += __shfl_xor_sync(~0u, l, 2);
             if ((lane & 3) == 0) {
-                jm[kw * 32 + r] = m[p];
-                jm[kw * 32 + 16 + r] = l[p];
+                jm[kw * 32 + r] = m[p] * a.scale_log2;
+                jm[kw * 32 + 16 + r] = l;
             }
 #pragma unroll
             for (int d = 0; d < DH / 8; ++d)
@@ -564,29 +590,31 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 
 namespace sc {
 
-// A warp joins a row: lane k holds the maximum and sum of part k, then the parts'
-// values are added with Dh / 4 lanes a part, in a fixed order. No load waits for
-// another part's, so the kernel costs a few memory latencies.
+// Dh / 4 lanes join a row (a warp two rows of 64 columns or one of 128): lane k holds the
+// maximum and sum of part k, then every lane adds its four columns of all parts,
+// in a fixed order. No load waits for another part's: the kernel costs three
+// dependent memory latencies, whatever the number of parts.
 template <int DH>
 __global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_ctas) {
     pdl_wait();
     pdl_launch_dependents();
     AttnArgs &a = x.a;
-    constexpr int L = DH / 4, kAtOnce = 32 / L;
-    const int lane = threadIdx.x & 31, c4 = lane % L;
-    const int Hq = a.Hkv * a.G;
-    const int row = (int)((blockIdx.x * (unsigned)blockDim.x + threadIdx.x) >> 5);
-    if (row >= a.N * a.D * Hq) return;
+    constexpr int L = DH / 4;
+    const int c4 = threadIdx.x % L;
+    const int Hq = a.Hkv * a.G, n_rows = a.N * a.D * Hq;
+    const int at = (int)((blockIdx.x * (unsigned)blockDim.x + threadIdx.x) / L);
+    const int row = min(at, n_rows - 1);  // a lane past the last row joins it and writes nothing
     const int token = row / Hq, hq = row % Hq, i = token / a.D, j = token % a.D;
     const int h = hq / a.G, g = hq % a.G;
     const bool prefix = a.shared_keys > 0 && gld(a.leader) >= 0;
     const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
     int slot;
-    if (seq_len(a, i, &slot, false) < 0) return;
+    const bool valid = seq_len(a, i, &slot, false) >= 0;
 
     // The row's parts: prefix_n from prefix_at on, own_n from own_at on.
     const float *prefix_at = nullptr, *own_at = nullptr;
     int prefix_n = 0, own_n = 0, pr = 0, step = 0;
+    bool mine = valid && at < n_rows;
     constexpr int kPSlot = kPR * (DH + 2);
     if (prefix) {
         const int tile = token / x.tpt;
@@ -601,66 +629,79 @@ __global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_cta
     const int r = j * a.G + g, RT = (a.D * a.G + MR - 1) / MR, per = RT * a.Hkv;
     const int oslot = MR * (DH + 2), orow = r % MR;
     if (u_n > u_i) {
-        const int64_t T = (u_n - u_i) / per;
+        const int64_t d = u_n - u_i;
+        const int64_t T = d <= UINT32_MAX ? (uint32_t)d / (uint32_t)per : d / per;
         const int n_cta = (int)min((int64_t)own_ctas, U);
         const int it = r / MR * a.Hkv + h;
         const int64_t u0 = u_i + it * T;
         const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
-        if (c0 == c1 && !prefix) return;  // k_own wrote the row
         own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot;
         own_n = c1 - c0 + 1;
+        if (own_n == 1 && !prefix) {  // k_own wrote the row
+            own_n = 0;
+            mine = false;
+        }
     }
     const int parts = prefix_n + own_n;
-    auto row_of = [&](int p) {  // O of part p's row
-        return p < prefix_n ? prefix_at + (int64_t)p * step + pr * DH
-                            : own_at + (int64_t)(p - prefix_n) * oslot + orow * DH;
-    };
+    int most = parts;  // of the warp's rows: its lanes stay together
+#pragma unroll
+    for (int k = 16; k >= L; k >>= 1) most = max(most, __shfl_xor_sync(~0u, most, k));
     float top = -INFINITY, sum = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     bool bad = false;
-    for (int p0 = 0; p0 < parts; p0 += 32) {
+    for (int p0 = 0; p0 < most; p0 += L) {
         float m = -INFINITY, l = 0.0f;
-        if (p0 + lane < parts) {
-            const int p = p0 + lane;
+        if (p0 + c4 < parts) {
+            const int p = p0 + c4;
             const float *ml = p < prefix_n
                                   ? prefix_at + (int64_t)p * step + kPR * DH + pr
                                   : own_at + (int64_t)(p - prefix_n) * oslot + MR * DH + orow;
             m = gld(ml);
             l = gld(ml + (p < prefix_n ? kPR : MR));
         }
-        bad |= __any_sync(~0u, m != m);
         float now = fmaxf(top, m);
+        int nan = m != m;
 #pragma unroll
-        for (int k = 16; k; k >>= 1) now = fmaxf(now, __shfl_xor_sync(~0u, now, k));
+        for (int k = L / 2; k; k >>= 1) {
+            now = fmaxf(now, __shfl_xor_sync(~0u, now, k));
+            nan |= __shfl_xor_sync(~0u, nan, k);
+        }
+        bad |= nan != 0;
         const float base = now == -INFINITY ? 0.0f : now;
         const float f = ex2(m - base), f0 = ex2(top - base);
         float s = l * f;
 #pragma unroll
-        for (int k = 16; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
+        for (int k = L / 2; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
         sum = sum * f0 + s;
         o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
         top = now;
-        const int here = min(32, parts - p0);
-#pragma unroll 4
-        for (int p = 0; p < here; p += kAtOnce) {
-            const int q = p + lane / L;
-            const float w = __shfl_sync(~0u, f, q & 31);
-            if (q < here) {
-                const float4 v = gld(reinterpret_cast<const float4 *>(row_of(p0 + q)) + c4);
-                o.x = fmaf(w, v.x, o.x);
-                o.y = fmaf(w, v.y, o.y);
-                o.z = fmaf(w, v.z, o.z);
-                o.w = fmaf(w, v.w, o.w);
+        const int here = min(L, parts - p0), rounds = min(L, most - p0);
+        constexpr int kAhead = 8;  // parts loaded before the first is added
+        for (int q0 = 0; q0 < rounds; q0 += kAhead) {
+            float4 v[kAhead];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int p = p0 + q0 + k;
+                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (q0 + k < here)
+                    v[k] = gld(reinterpret_cast<const float4 *>(
+                                   p < prefix_n ? prefix_at + (int64_t)p * step + pr * DH
+                                                : own_at + (int64_t)(p - prefix_n) * oslot +
+                                                      orow * DH) +
+                               c4);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const float w = __shfl_sync(~0u, f, q0 + k, L);
+                if (q0 + k >= here) continue;
+                o.x = fmaf(w, v[k].x, o.x);
+                o.y = fmaf(w, v[k].y, o.y);
+                o.z = fmaf(w, v[k].z, o.z);
+                o.w = fmaf(w, v[k].w, o.w);
             }
         }
     }
-    if constexpr (kAtOnce == 2) {
-        o.x += __shfl_xor_sync(~0u, o.x, 16);
-        o.y += __shfl_xor_sync(~0u, o.y, 16);
-        o.z += __shfl_xor_sync(~0u, o.z, 16);
-        o.w += __shfl_xor_sync(~0u, o.w, 16);
-    }
-    if (bad || lane >= L) return;  // a bad page: the row is not written
+    if (bad || !mine) return;  // a bad page: the row is not written
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
     gst(reinterpret_cast<uint2 *>(a.out + (int64_t)row * DH + c4 * 4),
         make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)));
@@ -848,7 +889,8 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
         e = MR == 16 ? launch_own<128, 1>(a, mk, mv, sm_count, &grid, stream)
                      : launch_own<128, 2>(a, mk, mv, sm_count, &grid, stream);
     if (e != cudaSuccess) return e;
-    const dim3 blocks((unsigned)(((int64_t)s.N * s.D * s.Hq + 7) / 8));  // a warp a row
+    const int lanes = s.Dh / 4;  // of a row
+    const dim3 blocks((unsigned)(((int64_t)s.N * s.D * s.Hq * lanes + 255) / 256));
     return s.Dh == 64 ? launch_pdl(k_merge<64>, blocks, dim3(256), 0, stream, x, MR, grid)
                       : launch_pdl(k_merge<128>, blocks, dim3(256), 0, stream, x, MR, grid);
 }

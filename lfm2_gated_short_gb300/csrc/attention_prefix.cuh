@@ -27,7 +27,6 @@ namespace sc {
 constexpr int kPR = 128;                 // rows of a tile
 constexpr int kPK = 128;                 // keys of a tile
 constexpr int kPfxThreads = 384;         // 2 x 4 softmax warps; producer, QK, PV, an idle warp
-constexpr float kRescaleLog2 = 8.0f;
 
 struct PrefixArgs {
     AttnArgs a;
@@ -143,17 +142,6 @@ __device__ __forceinline__ void fewer_regs() {
 #ifndef SC_BOUNDS_CHECK
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 #endif
-}
-
-__device__ __forceinline__ float max3(float x, float y, float z) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
-    return r;
-}
-__device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
-    f32x2 d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
 }
 
 struct RingPos {
