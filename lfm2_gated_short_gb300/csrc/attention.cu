@@ -64,7 +64,8 @@ struct AttnArgs {
 // slot w + c: along the line each step raises w or c, so slots are distinct.
 
 __host__ __device__ __forceinline__ int64_t share_begin(int64_t c, int64_t U, int64_t n) {
-    return c * U / n;
+    const int64_t x = c * U;
+    return x <= UINT32_MAX ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
 }
 __host__ __device__ __forceinline__ int share_of(int64_t u, int64_t U, int64_t n) {
     const int64_t x = (u + 1) * n - 1;
@@ -93,6 +94,24 @@ __device__ __forceinline__ int own_tiles(const AttnArgs &a, int len) {
     return len > a.shared_keys ? (len - a.shared_keys + kKT - 1) / kKT : 0;
 }
 
+// An item piece as the producer describes it to the consumers: tiles t0 .. t0 + n - 1
+// of T of row tile rt and kv head h of sequence i (len tokens); w: the item's number.
+// n = 0: no more.
+struct OwnItem {
+    int i, len, rt, h, w, t0, n, T;
+};
+
+// Start a 16-byte copy to shared memory; cp_async_arrive arrives on `bar` once, when
+// all that this thread started have landed.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    if (!SC_RD_OK(src, 16)) return;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
 // A producer warp's page ids: the table entries of `nb` boxes (of `box` tokens,
 // nb a divisor of 32) a tile, tile after tile. Lane k holds the page of box b0 + k;
 // the next 32 are in flight, so that a tile waits for no table entry.
@@ -106,10 +125,14 @@ struct PageIds {
         row = table_row;
         shift = 31 - __clz(boxes_of_page);
         last = last_box;
+        begin(b, 0, 0, false);
+    }
+    // Again from box b; with `known`, c and n are what load(b) and load(b + 32) gave.
+    __device__ __forceinline__ void begin(int b, int c, int n, bool known) {
         b0 = b;
         at = 0;
-        cur = load(b0);
-        nxt = load(b0 + 32);
+        cur = known ? c : load(b0);
+        nxt = known ? n : load(b0 + 32);
     }
     __device__ __forceinline__ int load(int b) const {
         return gld(row + (min(b + (int)(threadIdx.x & 31), last) >> shift));
@@ -190,7 +213,7 @@ struct OwnCfg {
     static constexpr uint32_t kQ = MR * 128 * NB;
     static constexpr int kOs = DH + 4;                        // floats of a row to join
     static constexpr uint32_t kJoin = kKeyWarps * MR * (kOs + 2) * 4;  // O, m, l of each key warp
-    static constexpr size_t kSmem = 1024 + kStages * kStage + kQ + kJoin;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + 2 * kQ + kJoin;
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part
 };
 
@@ -202,22 +225,28 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     constexpr int ST = C::kStages, kThreads = C::kThreads;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t s_full[ST], s_empty[ST];
+    __shared__ uint64_t s_qfull[2], s_qempty[2];  // an item's queries and description
+    __shared__ OwnItem s_item[2];
     __shared__ int s_bad[ST];
     __shared__ int64_t s_scan[kThreads / 32];
-    __shared__ int s_seq, s_slot, s_len;
+    __shared__ int s_seq, s_slots[kThreads], s_lens[kThreads];  // of all sequences, if they fit
     __shared__ int64_t s_seq_unit;
     const uint32_t raw_a = smem_addr(raw);
     unsigned char *ring = raw + (((raw_a + 1023u) & ~1023u) - raw_a);
     const uint32_t ring_a = smem_addr(ring);
     unsigned char *qs = ring + ST * C::kStage;
     const uint32_t qs_a = smem_addr(qs);
-    float *join = reinterpret_cast<float *>(qs + C::kQ);
+    float *join = reinterpret_cast<float *>(qs + 2 * C::kQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
             mbar_init(&s_full[s], 1);
             mbar_init(&s_empty[s], C::kWarps);
             s_bad[s] = 0;
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&s_qfull[s], 33);  // every producer lane's copies, and the description
+            mbar_init(&s_qempty[s], C::kWarps);
         }
         mbar_fence_init();
         tma_prefetch_map(&mk);
@@ -234,124 +263,185 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     const int rows = a.D * a.G;
     const int RT = (rows + C::MR - 1) / C::MR;
     const int per = RT * a.Hkv;  // items of a sequence
-    int64_t U = 0, u0 = 0, u1 = 0, mine = 0;
-    int n_cta = 1, slot = 0, len = -1;
-    for (int pass = 0; pass < 2; ++pass) {
-        int64_t base = 0;
-        for (int i0 = 0; i0 < a.N; i0 += kThreads) {
-            const int i = i0 + tid;
-            if (pass == 0 || a.N > kThreads) {  // else this thread's sequence is still here
-                len = i < a.N ? seq_len(a, i, &slot, pass == 0 && blockIdx.x == 0) : -1;
-                mine = (int64_t)per * own_tiles(a, len);
-            }
-            int64_t inc = mine;
+    int64_t U = 0, u0 = 0, u1 = 0;
+    int n_cta = 1;
+    // Units before this thread's sequence of i0 .. i0 + kThreads - 1, the units of that, and
+    // the total with them.
+    auto scan = [&](int i0, int64_t base, int64_t *begin, int64_t *mine, bool report) {
+        const int i = i0 + tid;
+        int slot = 0;
+        const int len = i < a.N ? seq_len(a, i, &slot, report) : -1;
+        *mine = (int64_t)per * own_tiles(a, len);
+        int64_t inc = *mine;
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int64_t up = __shfl_up_sync(~0u, inc, o);
-                if (lane >= o) inc += up;
-            }
-            __syncthreads();
-            if (lane == 31) s_scan[warp] = inc;
-            __syncthreads();
-            int64_t before = base, all = base;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += up;
+        }
+        __syncthreads();  // s_scan of the scan before
+        s_slots[tid] = slot;
+        s_lens[tid] = len;
+        if (lane == 31) s_scan[warp] = inc;
+        __syncthreads();
+        int64_t before = base, all = base;
 #pragma unroll
-            for (int k = 0; k < kThreads / 32; ++k) {
-                if (k < warp) before += s_scan[k];
-                all += s_scan[k];
-            }
-            const int64_t begin = before + inc - mine;
-            if (pass == 1 && i < a.N) {
-                if (u0 >= begin && u0 < begin + mine) {
-                    s_seq = i;
-                    s_slot = slot;
-                    s_len = len;
-                    s_seq_unit = begin;
-                }
-                if (blockIdx.x == 0) gst(a.cum + i, begin);
-            }
-            base = all;
+        for (int k = 0; k < kThreads / 32; ++k) {
+            if (k < warp) before += s_scan[k];
+            all += s_scan[k];
         }
-        if (pass == 0) {
-            U = base;
-            n_cta = (int)min((int64_t)gridDim.x, max(U, (int64_t)1));
-            u0 = share_begin(blockIdx.x, U, n_cta);
-            u1 = share_begin(blockIdx.x + 1, U, n_cta);
-            if (blockIdx.x == 0 && tid == 0) gst(a.cum + a.N, U);
-            if ((int)blockIdx.x >= n_cta && blockIdx.x > 0) return;
+        *begin = before + inc - *mine;
+        return all;
+    };
+    int64_t begin = 0, mine = 0;
+    for (int i0 = 0; i0 < a.N; i0 += kThreads) U = scan(i0, U, &begin, &mine, blockIdx.x == 0);
+    n_cta = (int)min((int64_t)gridDim.x, max(U, (int64_t)1));
+    u0 = share_begin(blockIdx.x, U, n_cta);
+    u1 = share_begin(blockIdx.x + 1, U, n_cta);
+    if (blockIdx.x == 0 && tid == 0) gst(a.cum + a.N, U);
+    if ((int)blockIdx.x >= n_cta && blockIdx.x > 0) return;
+    for (int64_t i0 = 0, base = 0; i0 < a.N; i0 += kThreads) {
+        if (a.N > kThreads) base = scan((int)i0, base, &begin, &mine, false);
+        const int i = (int)i0 + tid;
+        if (i >= a.N) continue;
+        if (u0 >= begin && u0 < begin + mine) {
+            s_seq = i;
+            s_seq_unit = begin;
         }
+        if (blockIdx.x == 0) gst(a.cum + i, begin);
     }
     __syncthreads();
     if (u0 >= u1 || s_seq >= a.N) return;
 
-    // Walk the CTA's units: f(i, slot, len, rt, h, w, first tile, tiles, T) for each
-    // item piece, in order, until it returns false.
-    auto walk = [&](auto &&f) {
-        int64_t left = u1 - u0;
-        int i = s_seq, slot = s_slot, len = s_len;
-        int T = own_tiles(a, len);
-        int it = (int)((u0 - s_seq_unit) / T), t0 = (int)(u0 - s_seq_unit - (int64_t)it * T);
-        int rt = it / a.Hkv, h = it - rt * a.Hkv;
-        while (true) {
-            for (; it < per; ++it) {
-                const int n = (int)min((int64_t)(T - t0), left);
-                if (!f(i, slot, len, rt, h, i * per + it, t0, n, T)) return;
-                left -= n;
-                if (left <= 0) return;
-                t0 = 0;
-                if (++h == a.Hkv) {
-                    h = 0;
-                    ++rt;
-                }
-            }
-            do {  // the next sequence with keys of its own
-                if (++i >= a.N) return;
-                len = seq_len(a, i, &slot, false);
-                T = own_tiles(a, len);
-            } while (T == 0);
-            it = rt = h = 0;
-        }
-    };
-
     if (warp == C::kWarps) {  // producer
+        // It alone walks the CTA's units and reads lengths and tables, a sequence ahead,
+        // and copies each item's queries: under the load of the tile copies a global read
+        // takes thousands of cycles, which no consumer then waits for.
         const int ps = a.pt.page_size;
         const int box = min(ps, kKT), nb = kKT / box;  // keys of a box, boxes of a tile
-        uint32_t g = 0;
-        walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
+        const int first_box = a.shared_keys / box;
+        // Slots and lengths of 32 sequences from `known` on, one a lane.
+        int known = s_seq, slot_l = 0, len_l = -1;
+        auto fetch = [&](int from) {
+            known = from;
+            const int i = from + lane;
+            if (a.N <= kThreads) {
+                len_l = i < a.N ? s_lens[i] : -1;
+                slot_l = i < a.N ? s_slots[i] : 0;
+            } else {
+                len_l = i < a.N ? seq_len(a, i, &slot_l, false) : -1;
+            }
+        };
+        fetch(known);
+        struct Seq {
+            int i, len, T, c, n;  // c, n: this lane's first page ids, as PageIds::begin takes them
             PageIds ids;
-            const int last = (len - 1) / box;
-            ids.start(a.pt.table + (int64_t)slot * a.pt.max_pages, ps / box,
-                      a.shared_keys / box + t0 * nb, last);
-            for (int t = 0; t < n; ++t, ++g) {
-                const uint32_t s = g % ST;
-                if (g >= ST && !mbar_wait_bounded(&s_empty[s], (g / ST - 1) & 1u)) {
+        };
+        // The next sequence from i on with keys of its own (i = N: none).
+        auto find = [&](int i, Seq &s) {
+            s.T = 0;
+            for (; i < a.N; ++i) {
+                if (i - known >= 32) fetch(i);
+                s.len = __shfl_sync(~0u, len_l, i - known);
+                s.T = own_tiles(a, s.len);
+                if (s.T > 0) break;
+            }
+            s.i = i;
+            if (i >= a.N) return;
+            const int slot = __shfl_sync(~0u, slot_l, i - known);
+            s.ids.start(a.pt.table + (int64_t)slot * a.pt.max_pages, ps / box, first_box,
+                        (s.len - 1) / box);
+            s.c = s.ids.cur;
+            s.n = s.ids.nxt;
+        };
+        uint32_t g = 0, items = 0;
+        // Describe an item to the consumers and start its queries; false when a wait gave up.
+        auto announce = [&](const OwnItem &it) {
+            const uint32_t b = items & 1u;
+            if (items >= 2 && !mbar_wait_bounded(&s_qempty[b], (items / 2 - 1) & 1u)) {
+                raise_error(SC_DEV_TIMEOUT);
+                return false;
+            }
+            if (it.n > 0) {
+                const bf16 *q = a.q + (int64_t)it.i * a.D * a.q_stride + it.h * a.G * DH;
+                constexpr int kStep = 256 / DH;  // rows of 32 chunks
+                int r = lane / (DH / 8), rr = it.rt * C::MR + r, j = rr / a.G, gq = rr - j * a.G;
+                const int ch = lane % (DH / 8);
+                const uint32_t col = b * C::kQ + (ch >> 3) * C::MR * 128;
+                for (; r < C::MR; r += kStep, rr += kStep) {
+                    const uint32_t off = col + swz(r, ch & 7);
+                    if (rr < rows)
+                        cp_async16(qs_a + off, q + j * a.q_stride + gq * DH + ch * 8);
+                    else
+                        *reinterpret_cast<uint4 *>(qs + off) = make_uint4(0u, 0u, 0u, 0u);
+                    for (gq += kStep; gq >= a.G; gq -= a.G) ++j;
+                }
+            }
+            cp_async_arrive(&s_qfull[b]);
+            if (lane == 0) s_item[b] = it;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_qfull[b]);
+            ++items;
+            return true;
+        };
+        auto produce = [&](Seq &s, const OwnItem &it) {
+            if (!announce(it)) return false;
+            s.ids.begin(first_box + it.t0 * nb, s.c, s.n, it.t0 == 0);
+            for (int t = 0; t < it.n; ++t, ++g) {
+                const uint32_t st = g % ST;
+                if (g >= ST && !mbar_wait_bounded(&s_empty[st], (g / ST - 1) & 1u)) {
                     raise_error(SC_DEV_TIMEOUT);
                     return false;
                 }
-                const int boxes = min(nb, last + 1 - ids.box());
-                int id = ids.page();
+                const int boxes = min(nb, s.ids.last + 1 - s.ids.box());
+                int id = s.ids.page();
                 bool bad = lane < boxes && (id < 0 || id >= a.pt.n_pages);
                 if (bad) id = 0;
                 bad = __any_sync(~0u, bad);
                 if (lane == 0) {
                     if (bad) raise_error(SC_DEV_BAD_PAGE);
-                    s_bad[s] = bad;
-                    mbar_arrive_expect_tx(&s_full[s], (uint32_t)boxes * box * DH * 4);
+                    s_bad[st] = bad;
+                    mbar_arrive_expect_tx(&s_full[st], (uint32_t)boxes * box * DH * 4);
                 }
                 __syncwarp();
                 if (lane < boxes) {
-                    const int key = id * ps + (ids.box() + lane) * box % ps;
-                    const uint32_t d = ring_a + s * C::kStage + lane * box * 128;
+                    const int key = id * ps + (s.ids.box() + lane) * box % ps;
+                    const uint32_t d = ring_a + st * C::kStage + lane * box * 128;
 #pragma unroll
                     for (int c = 0; c < C::NB; ++c) {
-                        tma_load_3d(d + c * C::kBlk, &mk, &s_full[s], c * 64, h, key);
-                        tma_load_3d(d + (C::NB + c) * C::kBlk, &mv, &s_full[s], c * 64, h, key);
+                        tma_load_3d(d + c * C::kBlk, &mk, &s_full[st], c * 64, it.h, key);
+                        tma_load_3d(d + (C::NB + c) * C::kBlk, &mv, &s_full[st], c * 64, it.h, key);
                     }
                 }
-                ids.next(nb);
+                s.ids.next(nb);
             }
             return true;
-        });
+        };
+        Seq s, after;
+        find(s_seq, s);
+        after.i = -1;  // not looked for yet: the first tiles go first
+        int64_t left = u1 - u0;
+        int it = (int)((u0 - s_seq_unit) / s.T), t0 = (int)(u0 - s_seq_unit - (int64_t)it * s.T);
+        int rt = it / a.Hkv, h = it - rt * a.Hkv;
+        bool ok = true;
+        while (ok && left > 0 && s.i < a.N) {
+            const int n = (int)min((int64_t)(s.T - t0), left);
+            ok = produce(s, OwnItem{s.i, s.len, rt, h, s.i * per + it, t0, n, s.T});
+            left -= n;
+            t0 = 0;
+            if (left > 0 && after.i < 0) find(s.i + 1, after);
+            if (++h == a.Hkv) {
+                h = 0;
+                ++rt;
+            }
+            if (++it == per) {
+                it = rt = h = 0;
+                s = after;
+                after.i = -1;
+            }
+        }
+        if (ok) announce(OwnItem{0, 0, 0, 0, 0, 0, 0, 0});
         // No copy may be in flight when the CTA leaves.
+        asm volatile("cp.async.wait_all;" ::: "memory");
         for (uint32_t c = g > ST ? g - ST : 0; c < g; ++c)
             mbar_wait_bounded(&s_full[c % ST], (c / ST) & 1u);
         return;
@@ -366,21 +456,14 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
     const float rescale = kRescaleLog2 / a.scale_log2;
     // What a thread does with the rows of row tile rt, the same for every item: the
-    // query chunks it loads, the tokens of the two rows it computes, the chunks of
-    // output rows it writes (offset -1: past the item's rows).
-    constexpr int kQn = C::MR * DH / 8 / (32 * C::kWarps);
+    // tokens of the two rows it computes, the chunks of output rows it writes (offset
+    // -1: past the item's rows).
     constexpr int kOn = 16 * DH / 4 / (32 * kKeyWarps);
     const int gt = kw * 32 + lane;  // thread of the row group
-    int rt_now = -1, q_row[kQn], q_off[kQn], row_j[2], o_off[kOn];
+    int rt_now = -1, row_j[2], o_off[kOn];
     auto set_rows = [&](int rt) {
         rt_now = rt;
         const int r0 = rt * C::MR;
-#pragma unroll
-        for (int k = 0; k < kQn; ++k) {
-            const int x = tid + k * 32 * C::kWarps, rr = r0 + x / (DH / 8);
-            q_row[k] = rr < rows ? rr / a.G : -1;
-            q_off[k] = rr % a.G * DH + x % (DH / 8) * 8;
-        }
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int rr = r0 + rg * 16 + p * 8 + (lane >> 2);
@@ -392,24 +475,27 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             o_off[k] = rr < rows ? (rr / a.G * a.Hkv * a.G + rr % a.G) * DH + x % (DH / 4) * 4 : -1;
         }
     };
-    walk([&](int i, int slot, int len, int rt, int h, int w, int t0, int n, int T) {
-        if (rt != rt_now) set_rows(rt);
-#pragma unroll
-        for (int k = 0; k < kQn; ++k) {
-            const int x = tid + k * 32 * C::kWarps, r = x / (DH / 8), ch = x % (DH / 8);
-            uint4 v = make_uint4(0u, 0u, 0u, 0u);
-            if (q_row[k] >= 0)
-                v = ld_plain(a.q + ((int64_t)i * a.D + q_row[k]) * a.q_stride + h * a.G * DH +
-                             q_off[k]);
-            *reinterpret_cast<uint4 *>(qs + (ch >> 3) * C::MR * 128 + swz(r, ch & 7)) = v;
+    for (uint32_t items = 0;; ++items) {
+        const uint32_t qb = items & 1u;
+        const bool ready = !dead && mbar_wait_bounded(&s_qfull[qb], (items / 2) & 1u);
+        // The warps go on together or not at all: none waits at a barrier the others left.
+        if (named_or(1, 32 * C::kWarps, !ready)) {
+            if (!ready && !dead) raise_error(SC_DEV_TIMEOUT);
+            return;
         }
-        named_sync(1, 32 * C::kWarps);
+        const OwnItem item = s_item[qb];
+        const int i = item.i, len = item.len, h = item.h, t0 = item.t0, n = item.n;
+        if (n == 0) return;
+        if (item.rt != rt_now) set_rows(item.rt);
         uint32_t qf[DH / 16][4];
 #pragma unroll
         for (int kk = 0; kk < DH / 16; ++kk) {
             const int ch = kk * 2 + (lane >> 4);
-            ldsm4(qf[kk], qs_a + (ch >> 3) * C::MR * 128 + swz(rg * 16 + (lane & 15), ch & 7));
+            ldsm4(qf[kk], qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
+                              swz(rg * 16 + (lane & 15), ch & 7));
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_qempty[qb]);
         // A row's running maximum m (of the scores before scaling), the score that moves
         // it, and its offset -m scale; the sums of its weights in pairs.
         int see[2];
@@ -468,15 +554,15 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             }
             float top[2];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < 2; ++p)
                 top[p] = fmaxf(max3(sc[0][2 * p], sc[0][2 * p + 1], sc[1][2 * p]), sc[1][2 * p + 1]);
-                top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-                top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
-            }
-            // A row that has seen no key yet keeps m = -inf, offset 0 and sums of zero.
+            // Only when some score passes its row's limit are the row maxima needed. A row that
+            // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
             if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
+                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
+                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
                     if (!(top[p] > limit[p])) continue;
                     const float f = ex2((m[p] - top[p]) * a.scale_log2);
                     m[p] = top[p];
@@ -541,9 +627,9 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                 *reinterpret_cast<float2 *>(jo + (kw * 16 + r) * C::kOs + d * 8 + (lane & 3) * 2) =
                     make_float2(o[d][2 * p], o[d][2 * p + 1]);
         }
-        named_sync(1, 32 * C::kWarps);  // also: every warp has read this item's queries
-        const bool whole = n == T && a.shared_keys == 0;  // nothing to join with
-        float *part = a.own_part + (int64_t)(w + blockIdx.x) * C::kSlot;
+        named_sync(1, 32 * C::kWarps);
+        const bool whole = n == item.T && a.shared_keys == 0;  // nothing to join with
+        float *part = a.own_part + (int64_t)(item.w + blockIdx.x) * C::kSlot;
         bf16 *out = a.out + ((int64_t)i * a.D * a.Hkv + h) * a.G * DH;
 #pragma unroll
         for (int k = 0; k < kOn; ++k) {
@@ -580,8 +666,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                 }
             }
         }
-        return true;
-    });
+    }
 }
 
 }  // namespace sc
@@ -590,52 +675,55 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 
 namespace sc {
 
-// Dh / 4 lanes join a row (a warp two rows of 64 columns or one of 128): lane k holds the
-// maximum and sum of part k, then every lane adds its four columns of all parts,
-// in a fixed order. No load waits for another part's: the kernel costs three
-// dependent memory latencies, whatever the number of parts.
-template <int DH>
-__global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_ctas) {
+// A block joins rows of one token. Dh / 8 lanes hold eight columns of a row each; PG
+// such groups share the row's parts (with few rows there are many parts and lanes
+// to spare). Lane k of the row holds the maximum and sum of part k, then every group
+// adds its parts, in a fixed order. No load waits for another part's.
+constexpr int kMergeThreads = 256;
+template <int DH, int PG>
+__global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, int own_ctas) {
     pdl_wait();
     pdl_launch_dependents();
     AttnArgs &a = x.a;
-    constexpr int L = DH / 4;
-    const int c4 = threadIdx.x % L;
-    const int Hq = a.Hkv * a.G, n_rows = a.N * a.D * Hq;
-    const int at = (int)((blockIdx.x * (unsigned)blockDim.x + threadIdx.x) / L);
-    const int row = min(at, n_rows - 1);  // a lane past the last row joins it and writes nothing
-    const int token = row / Hq, hq = row % Hq, i = token / a.D, j = token % a.D;
-    const int h = hq / a.G, g = hq % a.G;
+    constexpr int L = DH / 8 * PG;
+    const int rl = threadIdx.x % L, c8 = rl % (DH / 8), group = rl / (DH / 8);
+    const int Hq = a.Hkv * a.G;
+    const int token = blockIdx.x, i = token / a.D, j = token - i * a.D;
+    const int at = blockIdx.y * (kMergeThreads / L) + threadIdx.x / L;
+    const int hq = min(at, Hq - 1);  // lanes past the last row join it and write nothing
+    const int h = hq / a.G, g = hq - h * a.G;
     const bool prefix = a.shared_keys > 0 && gld(a.leader) >= 0;
     const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
     int slot;
     const bool valid = seq_len(a, i, &slot, false) >= 0;
 
-    // The row's parts: prefix_n from prefix_at on, own_n from own_at on.
-    const float *prefix_at = nullptr, *own_at = nullptr;
-    int prefix_n = 0, own_n = 0, pr = 0, step = 0;
-    bool mine = valid && at < n_rows;
+    // The row's parts: prefix_n from prefix_at on, own_n from own_at on (its O; m and l
+    // are at +m_off and +l_off).
     constexpr int kPSlot = kPR * (DH + 2);
+    const float *prefix_at = nullptr, *own_at = nullptr;
+    int prefix_n = 0, own_n = 0, prefix_m = 0, own_m = 0, step = 0;
+    bool mine = valid && at < Hq;
     if (prefix) {
-        const int tile = token / x.tpt;
-        pr = token % x.tpt * a.G + g;
+        const int tile = token / x.tpt, r = (token - tile * x.tpt) * a.G + g;
         const int64_t w = (int64_t)(x.split ? tile : tile >> 1) * a.Hkv + h;
         const int c0 = share_of(w * x.T, x.U, x.n_cta);
         const int c1 = share_of(w * x.T + x.T - 1, x.U, x.n_cta);
-        prefix_at = x.part + ((w + c0) * 2 + (x.split ? 0 : tile & 1)) * kPSlot;
+        prefix_at = x.part + ((w + c0) * 2 + (x.split ? 0 : tile & 1)) * kPSlot + r * DH;
+        prefix_m = kPR * DH + r - r * DH;
         step = x.split ? kPSlot : 2 * kPSlot;
         prefix_n = (c1 - c0 + 1) * (x.split ? 2 : 1);
     }
-    const int r = j * a.G + g, RT = (a.D * a.G + MR - 1) / MR, per = RT * a.Hkv;
-    const int oslot = MR * (DH + 2), orow = r % MR;
+    const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * a.Hkv;
+    const int oslot = MR * (DH + 2), rt = r / MR, orow = r - rt * MR;
     if (u_n > u_i) {
         const int64_t d = u_n - u_i;
         const int64_t T = d <= UINT32_MAX ? (uint32_t)d / (uint32_t)per : d / per;
         const int n_cta = (int)min((int64_t)own_ctas, U);
-        const int it = r / MR * a.Hkv + h;
+        const int it = rt * a.Hkv + h;
         const int64_t u0 = u_i + it * T;
         const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
-        own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot;
+        own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot + orow * DH;
+        own_m = MR * DH + orow - orow * DH;
         own_n = c1 - c0 + 1;
         if (own_n == 1 && !prefix) {  // k_own wrote the row
             own_n = 0;
@@ -643,21 +731,21 @@ __global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_cta
         }
     }
     const int parts = prefix_n + own_n;
+    const float *own_from = own_at - (int64_t)prefix_n * oslot;  // part p's, p >= prefix_n, at + p * oslot
     int most = parts;  // of the warp's rows: its lanes stay together
 #pragma unroll
     for (int k = 16; k >= L; k >>= 1) most = max(most, __shfl_xor_sync(~0u, most, k));
-    float top = -INFINITY, sum = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float top = -INFINITY, sum = 0.0f, o[8] = {};
     bool bad = false;
     for (int p0 = 0; p0 < most; p0 += L) {
         float m = -INFINITY, l = 0.0f;
-        if (p0 + c4 < parts) {
-            const int p = p0 + c4;
-            const float *ml = p < prefix_n
-                                  ? prefix_at + (int64_t)p * step + kPR * DH + pr
-                                  : own_at + (int64_t)(p - prefix_n) * oslot + MR * DH + orow;
+        const int p = p0 + rl;
+        if (p < parts) {
+            const bool pre = p < prefix_n;
+            const float *ml = pre ? prefix_at + (int64_t)p * step + prefix_m
+                                  : own_from + (int64_t)p * oslot + own_m;
             m = gld(ml);
-            l = gld(ml + (p < prefix_n ? kPR : MR));
+            l = gld(ml + (pre ? kPR : MR));
         }
         float now = fmaxf(top, m);
         int nan = m != m;
@@ -673,38 +761,49 @@ __global__ void __launch_bounds__(256) k_merge(PrefixArgs x, int MR, int own_cta
 #pragma unroll
         for (int k = L / 2; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
         sum = sum * f0 + s;
-        o.x *= f0, o.y *= f0, o.z *= f0, o.w *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f0;
         top = now;
         const int here = min(L, parts - p0), rounds = min(L, most - p0);
-        constexpr int kAhead = 8;  // parts loaded before the first is added
-        for (int q0 = 0; q0 < rounds; q0 += kAhead) {
-            float4 v[kAhead];
+        constexpr int kAhead = 4;  // parts loaded before the first is added
+        for (int q0 = 0; q0 < rounds; q0 += kAhead * PG) {
+            float4 v[kAhead][2];
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const int p = p0 + q0 + k;
-                v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (q0 + k < here)
-                    v[k] = gld(reinterpret_cast<const float4 *>(
-                                   p < prefix_n ? prefix_at + (int64_t)p * step + pr * DH
-                                                : own_at + (int64_t)(p - prefix_n) * oslot +
-                                                      orow * DH) +
-                               c4);
+                const int q = q0 + k * PG + group;
+                if (q < here) {
+                    const float4 *from = reinterpret_cast<const float4 *>(
+                        p0 + q < prefix_n ? prefix_at + (int64_t)(p0 + q) * step
+                                          : own_from + (int64_t)(p0 + q) * oslot);
+                    v[k][0] = gld(from + c8 * 2);
+                    v[k][1] = gld(from + c8 * 2 + 1);
+                }
             }
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
-                const float w = __shfl_sync(~0u, f, q0 + k, L);
-                if (q0 + k >= here) continue;
-                o.x = fmaf(w, v[k].x, o.x);
-                o.y = fmaf(w, v[k].y, o.y);
-                o.z = fmaf(w, v[k].z, o.z);
-                o.w = fmaf(w, v[k].w, o.w);
+                const int q = q0 + k * PG + group;
+                const float w = __shfl_sync(~0u, f, q, L);
+                if (q >= here) continue;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    o[4 * e] = fmaf(w, v[k][e].x, o[4 * e]);
+                    o[4 * e + 1] = fmaf(w, v[k][e].y, o[4 * e + 1]);
+                    o[4 * e + 2] = fmaf(w, v[k][e].z, o[4 * e + 2]);
+                    o[4 * e + 3] = fmaf(w, v[k][e].w, o[4 * e + 3]);
+                }
             }
         }
     }
+#pragma unroll
+    for (int k = DH / 8; k < L; k <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(~0u, o[e], k);
+    mine = mine && group == 0;
     if (bad || !mine) return;  // a bad page: the row is not written
     const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-    gst(reinterpret_cast<uint2 *>(a.out + (int64_t)row * DH + c4 * 4),
-        make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv)));
+    gst(reinterpret_cast<uint4 *>(a.out + ((int64_t)token * Hq + hq) * DH + c8 * 8),
+        make_uint4(pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv),
+                   pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv)));
 }
 
 // ------------------------------------------------------------ host side
@@ -889,10 +988,14 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
         e = MR == 16 ? launch_own<128, 1>(a, mk, mv, sm_count, &grid, stream)
                      : launch_own<128, 2>(a, mk, mv, sm_count, &grid, stream);
     if (e != cudaSuccess) return e;
-    const int lanes = s.Dh / 4;  // of a row
-    const dim3 blocks((unsigned)(((int64_t)s.N * s.D * s.Hq * lanes + 255) / 256));
-    return s.Dh == 64 ? launch_pdl(k_merge<64>, blocks, dim3(256), 0, stream, x, MR, grid)
-                      : launch_pdl(k_merge<128>, blocks, dim3(256), 0, stream, x, MR, grid);
+    // With few rows all lanes of a warp share one (28 parts of 64 rows: 13 us with 8 lanes a
+    // row, 8 with 32); with many there is work enough (32768 rows: 18 us against 29).
+    const bool few = (int64_t)s.N * s.D * s.Hq <= 4096;
+    const auto merge = s.Dh == 64 ? (few ? k_merge<64, 4> : k_merge<64, 1>)
+                                  : (few ? k_merge<128, 2> : k_merge<128, 1>);
+    const int block_rows = few ? kMergeThreads / 32 : kMergeThreads / (s.Dh / 8);  // of one token
+    const dim3 blocks((unsigned)(s.N * s.D), (unsigned)((s.Hq + block_rows - 1) / block_rows));
+    return launch_pdl(merge, blocks, dim3(kMergeThreads), 0, stream, x, MR, grid);
 }
 
 cudaError_t take_error_attention(cudaStream_t stream, unsigned int *sum) {
