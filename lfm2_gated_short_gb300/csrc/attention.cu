@@ -37,7 +37,6 @@ namespace sc {
 typedef __nv_bfloat16 bf16;
 
 constexpr int kKT = 64;            // keys of a tile
-constexpr int kKeyWarps = 4;       // 16 keys of a tile each
 constexpr int kMaxCtas = 456;      // three CTAs on each of 152 SMs
 constexpr int kMaxPrefixCtas = 152;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -196,24 +195,28 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// RG groups of 16 rows. A CTA's consumer warps are 4 key groups (16 keys of a
-// tile) times RG row groups. Shared memory and registers allow 3 CTAs an SM
-// for 16 rows of 64, 2 for 32 of 64 or 16 of 128, 1 for 32 of 128; either way
-// 128 to 144 KB of tiles are in flight.
+// RG groups of 16 rows times KG key groups: a consumer warp takes 16 rows by 64 / KG keys of
+// a tile. 16 rows are bound by the tiles' bytes, and more, lighter warps start and
+// end an item sooner; 32 rows of 64 columns are bound by the warps' own latency,
+// and 32 keys a warp keep more of their work independent. CTAs of an SM and
+// stages are what shared memory and registers allow.
 template <int DH, int RG>
 struct OwnCfg {
     static constexpr int MR = 16 * RG;
-    static constexpr int kWarps = kKeyWarps * RG;             // consumer warps
+    static constexpr int KG = DH == 64 && RG == 2 ? 2 : 4;    // key groups
+    static constexpr int KB = kKT / 16 / KG;                  // blocks of 16 keys of a warp
+    static constexpr int kWarps = KG * RG;                    // consumer warps
     static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer
     static constexpr int NB = DH / 64;                        // 64-wide column blocks
     static constexpr uint32_t kBlk = kKT * 128;               // one block of a tile, 8 KB
     static constexpr uint32_t kStage = 2 * NB * kBlk;         // K and V of a tile
-    static constexpr int kCtas = DH == 64 ? (RG == 1 ? 3 : 2) : (RG == 1 ? 2 : 1);
-    static constexpr int kStages = DH == 64 ? (RG == 1 ? 3 : 4) : (RG == 1 ? 2 : 4);
+    static constexpr int kCtas = DH == 64 ? 3 : (RG == 1 ? 2 : 1);
+    static constexpr int kStages = DH == 64 ? 3 : (RG == 1 ? 2 : 4);
+    static constexpr int kQBufs = DH == 64 && RG == 2 ? 1 : 2;  // items described ahead
     static constexpr uint32_t kQ = MR * 128 * NB;
     static constexpr int kOs = DH + 4;                        // floats of a row to join
-    static constexpr uint32_t kJoin = kKeyWarps * MR * (kOs + 2) * 4;  // O, m, l of each key warp
-    static constexpr size_t kSmem = 1024 + kStages * kStage + 2 * kQ + kJoin;
+    static constexpr uint32_t kJoin = KG * MR * (kOs + 2) * 4;  // O, m, l of each key group
+    static constexpr size_t kSmem = 1024 + kStages * kStage + kQBufs * kQ + kJoin;
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part
 };
 
@@ -222,11 +225,12 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     k_own(AttnArgs a, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
     using C = OwnCfg<DH, RG>;
-    constexpr int ST = C::kStages, kThreads = C::kThreads;
+    constexpr int ST = C::kStages, kThreads = C::kThreads, KG = C::KG, KB = C::KB;
+    constexpr int QB = C::kQBufs;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t s_full[ST], s_empty[ST];
-    __shared__ uint64_t s_qfull[2], s_qempty[2];  // an item's queries and description
-    __shared__ OwnItem s_item[2];
+    __shared__ uint64_t s_qfull[QB], s_qempty[QB];  // an item's queries and description
+    __shared__ OwnItem s_item[QB];
     __shared__ int s_bad[ST];
     __shared__ int64_t s_scan[kThreads / 32];
     __shared__ int s_seq, s_slots[kThreads], s_lens[kThreads];  // of all sequences, if they fit
@@ -236,7 +240,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     const uint32_t ring_a = smem_addr(ring);
     unsigned char *qs = ring + ST * C::kStage;
     const uint32_t qs_a = smem_addr(qs);
-    float *join = reinterpret_cast<float *>(qs + 2 * C::kQ);
+    float *join = reinterpret_cast<float *>(qs + C::kQBufs * C::kQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -244,7 +248,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             mbar_init(&s_empty[s], C::kWarps);
             s_bad[s] = 0;
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < QB; ++s) {
             mbar_init(&s_qfull[s], 33);  // every producer lane's copies, and the description
             mbar_init(&s_qempty[s], C::kWarps);
         }
@@ -356,8 +360,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         uint32_t g = 0, items = 0;
         // Describe an item to the consumers and start its queries; false when a wait gave up.
         auto announce = [&](const OwnItem &it) {
-            const uint32_t b = items & 1u;
-            if (items >= 2 && !mbar_wait_bounded(&s_qempty[b], (items / 2 - 1) & 1u)) {
+            const uint32_t b = items % QB;
+            if (items >= QB && !mbar_wait_bounded(&s_qempty[b], (items / QB - 1) & 1u)) {
                 raise_error(SC_DEV_TIMEOUT);
                 return false;
             }
@@ -449,16 +453,16 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 
     uint32_t ring_at = 0, ring_phase = 0;
     bool dead = false;
-    const int kw = warp % kKeyWarps, rg = warp / kKeyWarps;  // key and row group
+    const int kw = warp % KG, rg = warp / KG;  // key and row group
     // This lane's ldmatrix address in a K and in a V block: a step of 16 columns flips bits 5, 6.
-    const uint32_t k_lane = swz(kw * 16 + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-    const uint32_t v_lane = swz(kw * 16 + (lane & 15), lane >> 4);
+    const uint32_t k_lane = swz(kw * 16 * KB + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    const uint32_t v_lane = swz(kw * 16 * KB + (lane & 15), lane >> 4);
     const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
     const float rescale = kRescaleLog2 / a.scale_log2;
     // What a thread does with the rows of row tile rt, the same for every item: the
     // tokens of the two rows it computes, the chunks of output rows it writes (offset
     // -1: past the item's rows).
-    constexpr int kOn = 16 * DH / 4 / (32 * kKeyWarps);
+    constexpr int kOn = 16 * DH / 4 / (32 * KG);
     const int gt = kw * 32 + lane;  // thread of the row group
     int rt_now = -1, row_j[2], o_off[kOn];
     auto set_rows = [&](int rt) {
@@ -471,13 +475,13 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         }
 #pragma unroll
         for (int k = 0; k < kOn; ++k) {
-            const int x = gt + k * 32 * kKeyWarps, rr = r0 + rg * 16 + x / (DH / 4);
+            const int x = gt + k * 32 * KG, rr = r0 + rg * 16 + x / (DH / 4);
             o_off[k] = rr < rows ? (rr / a.G * a.Hkv * a.G + rr % a.G) * DH + x % (DH / 4) * 4 : -1;
         }
     };
     for (uint32_t items = 0;; ++items) {
-        const uint32_t qb = items & 1u;
-        const bool ready = !dead && mbar_wait_bounded(&s_qfull[qb], (items / 2) & 1u);
+        const uint32_t qb = items % QB;
+        const bool ready = !dead && mbar_wait_bounded(&s_qfull[qb], (items / QB) & 1u);
         // The warps go on together or not at all: none waits at a barrier the others left.
         if (named_or(1, 32 * C::kWarps, !ready)) {
             if (!ready && !dead) raise_error(SC_DEV_TIMEOUT);
@@ -514,7 +518,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
         bool bad = false;
-        int key0 = a.shared_keys + t0 * kKT + kw * 16;
+        int key0 = a.shared_keys + t0 * kKT + kw * 16 * KB;
         for (int t = 0; t < n; ++t, key0 += kKT) {
             if (!dead && !mbar_wait_bounded(&s_full[ring_at], ring_phase)) {
                 raise_error(SC_DEV_TIMEOUT);
@@ -523,30 +527,35 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             bad |= s_bad[ring_at] != 0;
             const uint32_t stage = ring_a + ring_at * C::kStage;
             const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
-            const bool tail = key0 + 16 > len;
+            const bool tail = key0 + 16 * KB > len;
             if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
                 const int from = max(0, len - key0);
-                for (int x = lane; x < (16 - from) * C::NB * 8; x += 32) {
+                for (int x = lane; x < (16 * KB - from) * C::NB * 8; x += 32) {
                     const int r = from + x / (C::NB * 8), ch = x % (C::NB * 8);
                     *reinterpret_cast<uint4 *>(ring + ring_at * C::kStage +
-                                               (C::NB + (ch >> 3)) * C::kBlk + (kw * 16 + r) * 128 +
+                                               (C::NB + (ch >> 3)) * C::kBlk +
+                                               (kw * 16 * KB + r) * 128 +
                                                (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 __syncwarp();
             }
-            float sc[2][4];
+            float sc[2 * KB][4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sc[0][e] = sc[1][e] = 0.0f;
+            for (int nt = 0; nt < 2 * KB; ++nt)
 #pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-                uint32_t b[4];
-                ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk);
-                mma16816(sc[0], qf[kk], b[0], b[1]);
-                mma16816(sc[1], qf[kk], b[2], b[3]);
-            }
-            if (key0 + 16 > least) {  // some row does not see some of these keys
+                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt)
+            for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    uint32_t b[4];
+                    ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
+                    mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
+                    mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
+                }
+            if (key0 + 16 * KB > least) {  // some row does not see some of these keys
+#pragma unroll
+                for (int nt = 0; nt < 2 * KB; ++nt)
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
                         if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
@@ -554,8 +563,12 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             }
             float top[2];
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
-                top[p] = fmaxf(max3(sc[0][2 * p], sc[0][2 * p + 1], sc[1][2 * p]), sc[1][2 * p + 1]);
+            for (int p = 0; p < 2; ++p) {
+                top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
+#pragma unroll
+                for (int nt = 1; nt < 2 * KB; ++nt)
+                    top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
+            }
             // Only when some score passes its row's limit are the row maxima needed. A row that
             // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
             if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
@@ -576,28 +589,30 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                     }
                 }
             }
-            uint32_t pf[4];
+            uint32_t pf[KB][4];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const f32x2 off2 = f2_make(off[p], off[p]);
 #pragma unroll
-                for (int nt = 0; nt < 2; ++nt) {
+                for (int nt = 0; nt < 2 * KB; ++nt) {
                     float e0, e1;
                     f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
                     e0 = ex2(e0);
                     e1 = ex2(e1);
                     l2[p] = f2_add(l2[p], f2_make(e0, e1));
                     // P enters the second product as bf16: 2^-8 relative a term at most.
-                    pf[nt * 2 + p] = pack_bf16(e0, e1);
+                    pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
                 }
             }
 #pragma unroll
-            for (int dd = 0; dd < DH / 16; ++dd) {
-                uint32_t b[4];
-                ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk);
-                mma16816(o[2 * dd], pf, b[0], b[1]);
-                mma16816(o[2 * dd + 1], pf, b[2], b[3]);
-            }
+            for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                for (int dd = 0; dd < DH / 16; ++dd) {
+                    uint32_t b[4];
+                    ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
+                    mma16816(o[2 * dd], pf[kb], b[0], b[1]);
+                    mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
+                }
             if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[ring_at]);
@@ -608,8 +623,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         }
         // Join the key warps: each leaves its m, l and O, and a thread joins and writes
         // four columns of a row. (The next join comes after the next item's barrier.)
-        float *jo = join + rg * kKeyWarps * 16 * C::kOs;  // [key warp][16][kOs]
-        float *jm = join + kKeyWarps * C::MR * C::kOs + rg * kKeyWarps * 32;  // [key warp][m 16, l 16]
+        float *jo = join + rg * KG * 16 * C::kOs;  // [key group][16][kOs]
+        float *jm = join + KG * C::MR * C::kOs + rg * KG * 32;  // [key group][m 16, l 16]
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             const int r = p * 8 + (lane >> 2);
@@ -633,14 +648,14 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         bf16 *out = a.out + ((int64_t)i * a.D * a.Hkv + h) * a.G * DH;
 #pragma unroll
         for (int k = 0; k < kOn; ++k) {
-            const int x = gt + k * 32 * kKeyWarps, r = x / (DH / 4), c4 = x % (DH / 4);
+            const int x = gt + k * 32 * KG, r = x / (DH / 4), c4 = x % (DH / 4);
             float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-            for (int q = 0; q < kKeyWarps; ++q) top = fmaxf(top, jm[q * 32 + r]);
+            for (int q = 0; q < KG; ++q) top = fmaxf(top, jm[q * 32 + r]);
             const float off = top == -INFINITY ? 0.0f : top;
             float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
-            for (int q = 0; q < kKeyWarps; ++q) {
+            for (int q = 0; q < KG; ++q) {
                 const float f = ex2(jm[q * 32 + r] - off);
                 const float4 u =
                     *reinterpret_cast<float4 *>(jo + (q * 16 + r) * C::kOs + c4 * 4);
