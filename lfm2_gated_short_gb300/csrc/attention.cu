@@ -50,6 +50,7 @@ struct AttnArgs {
     int N, D, G, Hkv, Dh;
     int shared_keys;   // keys whose part k_prefix computes, if a sequence holds them all
     const int *leader; // k_prefix's word on that: < 0 when none does (unused without a prefix)
+    int beside;        // k_own runs beside k_prefix, on the SMs that it leaves
     float scale_log2;  // scale * log2(e)
     bf16 *out;
     int64_t *cum;      // [N + 1] first own tile of each sequence
@@ -258,10 +259,23 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         s_seq = a.N;
     }
     __syncthreads();
-    pdl_wait();
+    // Beside k_prefix: that kernel let this one start only after its own wait, so what this
+    // one reads is there; it waits for k_prefix at its end, since k_merge, which waits
+    // for this one alone, reads what both wrote.
+    if (!a.beside) pdl_wait();
     pdl_launch_dependents();
+    auto leave = [&]() {
+        if (a.beside) pdl_wait();
+    };
 
-    if (a.shared_keys > 0 && gld(a.leader) < 0) a.shared_keys = 0;
+    if (a.shared_keys > 0) {  // as k_prefix finds it: does a sequence hold the whole prefix?
+        bool full = false;
+        for (int i = tid; i < a.N && !full; i += kThreads) {
+            int slot;
+            full = seq_len(a, i, &slot, false) >= a.shared_keys;
+        }
+        if (!__syncthreads_or(full)) a.shared_keys = 0;
+    }
 
     // The units of the call and the sequence that holds this CTA's first one.
     const int rows = a.D * a.G;
@@ -302,7 +316,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     u0 = share_begin(blockIdx.x, U, n_cta);
     u1 = share_begin(blockIdx.x + 1, U, n_cta);
     if (blockIdx.x == 0 && tid == 0) gst(a.cum + a.N, U);
-    if ((int)blockIdx.x >= n_cta && blockIdx.x > 0) return;
+    if ((int)blockIdx.x >= n_cta && blockIdx.x > 0) return leave();
     for (int64_t i0 = 0, base = 0; i0 < a.N; i0 += kThreads) {
         if (a.N > kThreads) base = scan((int)i0, base, &begin, &mine, false);
         const int i = (int)i0 + tid;
@@ -314,7 +328,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         if (blockIdx.x == 0) gst(a.cum + i, begin);
     }
     __syncthreads();
-    if (u0 >= u1 || s_seq >= a.N) return;
+    if (u0 >= u1 || s_seq >= a.N) return leave();
 
     if (warp == C::kWarps) {  // producer
         // It alone walks the CTA's units and reads lengths and tables, a sequence ahead,
@@ -485,11 +499,11 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         // The warps go on together or not at all: none waits at a barrier the others left.
         if (named_or(1, 32 * C::kWarps, !ready)) {
             if (!ready && !dead) raise_error(SC_DEV_TIMEOUT);
-            return;
+            return leave();
         }
         const OwnItem item = s_item[qb];
         const int i = item.i, len = item.len, h = item.h, t0 = item.t0, n = item.n;
-        if (n == 0) return;
+        if (n == 0) return leave();
         if (item.rt != rt_now) set_rows(item.rt);
         uint32_t qf[DH / 16][4];
 #pragma unroll
@@ -904,6 +918,12 @@ static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count) {
     x.U = (int64_t)s.Hkv * (x.split ? 1 : (x.n_tiles + 1) / 2) * x.T;
     const int ctas = sm_count < kMaxPrefixCtas ? sm_count : kMaxPrefixCtas;
     x.n_cta = (int)(x.U < ctas ? x.U : ctas);
+    // A small prefix (at most two units an SM) costs fixed latencies more than work: it takes
+    // a CTA for every four units, and the own parts run on the other SMs meanwhile.
+    // 64 sequences behind 4096 tokens: 50 us one after the other, 42 so; 37 x 3 drafts with
+    // 128-wide heads behind 2976: 38 and 26.
+    x.a.beside = x.U > 0 && x.U <= 2 * ctas && ctas >= 8;
+    if (x.a.beside) x.n_cta = (int)((x.U + 3) / 4);
     return x;
 }
 static size_t prefix_part_floats(const AttnShape &s) {
@@ -930,12 +950,12 @@ static cudaError_t smem_opt_in(F kern, size_t bytes, std::atomic<unsigned long l
 
 template <int DH, int RG>
 static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
-                              int sm_count, int *grid, cudaStream_t stream) {
+                              int sms, int *grid, cudaStream_t stream) {
     using C = OwnCfg<DH, RG>;
     static std::atomic<unsigned long long> done{0};
     const cudaError_t e = smem_opt_in(k_own<DH, RG>, C::kSmem, done);
     if (e != cudaSuccess) return e;
-    *grid = C::kCtas * sm_count < kMaxCtas ? C::kCtas * sm_count : kMaxCtas;
+    *grid = C::kCtas * sms < kMaxCtas ? C::kCtas * sms : kMaxCtas;
     return launch_pdl(k_own<DH, RG>, dim3((unsigned)*grid), dim3(C::kThreads), C::kSmem, stream, a,
                       mk, mv);
 }
@@ -975,33 +995,35 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.own_part = (float *)((char *)workspace + cum_bytes(s));
     x.part = a.own_part + own_part_floats(s);
     CUtensorMap mk, mv;
-    cudaError_t e;
+    const int own_box = pt.page_size < kKT ? pt.page_size : kKT;
+    cudaError_t e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, own_box);
+    if (e != cudaSuccess) return e;
+    e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, own_box);
+    if (e != cudaSuccess) return e;
     if (x.P > 0) {
-        CUtensorMap mq;
+        CUtensorMap mq, pk = mk, pv = mv;
         const int box = pt.page_size < kPK ? pt.page_size : kPK;
-        e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, box);
-        if (e != cudaSuccess) return e;
-        e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, box);
-        if (e != cudaSuccess) return e;
+        if (box != own_box) {
+            e = map_pages(&pk, k_pages, pt, s.Hkv, s.Dh, box);
+            if (e != cudaSuccess) return e;
+            e = map_pages(&pv, v_pages, pt, s.Hkv, s.Dh, box);
+            if (e != cudaSuccess) return e;
+        }
         e = map_queries(&mq, x, s);
         if (e != cudaSuccess) return e;
-        e = s.Dh == 64 ? launch_prefix<64>(x, mq, mk, mv, stream)
-                       : launch_prefix<128>(x, mq, mk, mv, stream);
+        e = s.Dh == 64 ? launch_prefix<64>(x, mq, pk, pv, stream)
+                       : launch_prefix<128>(x, mq, pk, pv, stream);
         if (e != cudaSuccess) return e;
     }
-    const int box = pt.page_size < kKT ? pt.page_size : kKT;
-    e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, box);
-    if (e != cudaSuccess) return e;
-    e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, box);
-    if (e != cudaSuccess) return e;
     const int MR = own_rows(s);
+    const int sms = a.beside ? sm_count - x.n_cta : sm_count;
     int grid = 0;
     if (s.Dh == 64)
-        e = MR == 16 ? launch_own<64, 1>(a, mk, mv, sm_count, &grid, stream)
-                     : launch_own<64, 2>(a, mk, mv, sm_count, &grid, stream);
+        e = MR == 16 ? launch_own<64, 1>(a, mk, mv, sms, &grid, stream)
+                     : launch_own<64, 2>(a, mk, mv, sms, &grid, stream);
     else
-        e = MR == 16 ? launch_own<128, 1>(a, mk, mv, sm_count, &grid, stream)
-                     : launch_own<128, 2>(a, mk, mv, sm_count, &grid, stream);
+        e = MR == 16 ? launch_own<128, 1>(a, mk, mv, sms, &grid, stream)
+                     : launch_own<128, 2>(a, mk, mv, sms, &grid, stream);
     if (e != cudaSuccess) return e;
     // With few rows all lanes of a warp share one (28 parts of 64 rows: 13 us with 8 lanes a
     // row, 8 with 32); with many there is work enough (32768 rows: 18 us against 29).
