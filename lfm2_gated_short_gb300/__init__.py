@@ -467,12 +467,33 @@ def _pools(k_pages, v_pages, n_pages):
             _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype, k_pages.shape))
 
 
-def _workspace(workspace, need, device):
-    if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
-    if workspace.dtype != torch.uint8 or workspace.numel() < need:
-        raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes")
-    return workspace
+# Scratch straight from torch's caching allocator: no tensor object (3 us of host time a
+# call), and the block belongs to the stream that the call runs on, so that it is safe
+# to give back as soon as the call is enqueued.
+_raw_alloc = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+_raw_delete = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_delete", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call_with_workspace(name, fn, workspace, need, device, stream, *args):
+    """``fn(*args, workspace, bytes, stream)``, with the caller's workspace or one of its own."""
+    st = _stream(stream, device)
+    if workspace is not None:
+        if workspace.dtype != torch.uint8 or workspace.numel() < need:
+            raise ValueError(f"workspace must be a uint8 tensor of at least {need} bytes")
+        status = fn(*args, _dev(workspace, "workspace"), workspace.numel(), st)
+    elif _raw_alloc is not None and _raw_delete is not None and device.index == _current_device():
+        p = _raw_alloc(max(need, 16), st)
+        try:
+            status = fn(*args, p, need, st)
+        finally:
+            _raw_delete(p)
+    else:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            ws = torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        status = fn(*args, ws.data_ptr(), need, st)
+    if status:
+        _raise_on(name, status)
 
 
 def page_cache(n_slots: int, max_pages: int, n_pages: int, device="cuda"):
@@ -494,11 +515,11 @@ def pages_resize(refs, table, lens, slot_ids, new_lens, k_pages, v_pages, worksp
     has to be copied, on the pools."""
     n = slot_ids.shape[0]
     ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
-    ws = _workspace(workspace, pages_workspace_bytes(refs.shape[0], n), refs.device)
-    _raise_on("shortconv_pages_resize", lib().shortconv_pages_resize(
+    _call_with_workspace(
+        "shortconv_pages_resize", lib().shortconv_pages_resize, workspace,
+        pages_workspace_bytes(refs.shape[0], n), refs.device, stream,
         *_cache(refs, table, lens), ps, _dev(slot_ids, "slot_ids", torch.int32, (n,)),
-        _dev(new_lens, "new_lens", torch.int32, (n,)), n, L, token_bytes, kp, vp,
-        _dev(ws, "workspace"), ws.numel(), _stream(stream, refs.device)))
+        _dev(new_lens, "new_lens", torch.int32, (n,)), n, L, token_bytes, kp, vp)
 
 
 def pages_fork(refs, table, lens, src_slots, dst_slots, k_pages, v_pages, workspace=None,
@@ -507,11 +528,11 @@ def pages_fork(refs, table, lens, src_slots, dst_slots, k_pages, v_pages, worksp
     filled last page copied. In place."""
     n = src_slots.shape[0]
     ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
-    ws = _workspace(workspace, pages_workspace_bytes(refs.shape[0], n), refs.device)
-    _raise_on("shortconv_pages_fork", lib().shortconv_pages_fork(
+    _call_with_workspace(
+        "shortconv_pages_fork", lib().shortconv_pages_fork, workspace,
+        pages_workspace_bytes(refs.shape[0], n), refs.device, stream,
         *_cache(refs, table, lens), ps, _dev(src_slots, "src_slots", torch.int32, (n,)),
-        _dev(dst_slots, "dst_slots", torch.int32, (n,)), n, L, token_bytes, kp, vp,
-        _dev(ws, "workspace"), ws.numel(), _stream(stream, refs.device)))
+        _dev(dst_slots, "dst_slots", torch.int32, (n,)), n, L, token_bytes, kp, vp)
 
 
 def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=None, stream=None):
@@ -520,11 +541,11 @@ def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=No
     ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
     if n_used is None:
         n_used = torch.empty((1,), dtype=torch.int32, device=refs.device)
-    ws = _workspace(workspace, pages_workspace_bytes(refs.shape[0], 0), refs.device)
-    _raise_on("shortconv_pages_compact", lib().shortconv_pages_compact(
+    _call_with_workspace(
+        "shortconv_pages_compact", lib().shortconv_pages_compact, workspace,
+        pages_workspace_bytes(refs.shape[0], 0), refs.device, stream,
         *_cache(refs, table, lens), ps, L, token_bytes, kp, vp,
-        _dev(n_used, "n_used", torch.int32, (1,)), _dev(ws, "workspace"), ws.numel(),
-        _stream(stream, refs.device)))
+        _dev(n_used, "n_used", torch.int32, (1,)))
     return n_used
 
 
@@ -566,15 +587,14 @@ def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages
     if out is None:
         out = torch.empty((N * D, Hq, Dh), dtype=dt, device=q.device)
     q_p, q_s = _rows(q, "q", dt, (N * D, Hq, Dh))
-    ws = _workspace(workspace, prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages),
-                    q.device)
-    _raise_on("shortconv_prefix_attention", lib().shortconv_prefix_attention(
+    _call_with_workspace(
+        "shortconv_prefix_attention", lib().shortconv_prefix_attention, workspace,
+        prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages), q.device, stream,
         _dcode(q), Hq, Hkv, Dh, q_p, q_s, N, D, _dev(k_pages, "k_pages", dt),
         _dev(v_pages, "v_pages", dt, k_pages.shape), n_pages, ps,
         _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (table.shape[0],)),
         table.shape[0], table.shape[1], _dev(slot_ids, "slot_ids", torch.int32, (N,)),
-        shared_pages, scale, _dev(out, "out", dt, (N * D, Hq, Dh)), _dev(ws, "workspace"),
-        ws.numel(), _stream(stream, q.device)))
+        shared_pages, scale, _dev(out, "out", dt, (N * D, Hq, Dh)))
     return out
 
 
