@@ -104,7 +104,10 @@ struct OwnItem {
 // Start a 16-byte copy to shared memory; cp_async_arrive arrives on `bar` once, when
 // all that this thread started have landed.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
-    if (!SC_RD_OK(src, 16)) return;
+    if (!SC_RD_OK(src, 16)) {  // refused: zeros
+        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+        return;
+    }
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {

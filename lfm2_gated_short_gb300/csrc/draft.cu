@@ -111,7 +111,10 @@ struct Row16 {
         if (mis && lane == 0) copy16(dst + 32 * kPer * 16, at + 32 * kPer * 16);
     }
     static __device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
-        if (!SC_RD_OK(src, 16)) return;
+        if (!SC_RD_OK(src, 16)) {  // refused: zeros
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(dst), "r"(0) : "memory");
+            return;
+        }
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     }
     // The two words that hold this lane's k-th vector of what copy() brought.
