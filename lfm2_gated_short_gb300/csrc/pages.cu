@@ -285,79 +285,89 @@ __global__ void __launch_bounds__(kMetaThreads)
     const bool first = cluster_ctarank() == 0;
     const int64_t cap = (int64_t)pt.max_pages * pt.page_size;
     if (tid == 0) s_copies = 0;
-    // Old and new length of listed sequence i; false (reported once) when either is bad.
-    auto lengths = [&](int i, int *slot, int *old, int *now, bool report) {
-        *slot = gld(slots + i);
-        *now = gld(new_lens + i);
-        *old = slot_len(pt, *slot, report);
-        if (*old >= 0 && (*now < 0 || *now > cap)) {
-            if (report) raise_error(SC_DEV_BAD_LENGTH);
-            return false;
+    // This thread's listed sequence of those from i0 on: slot, old and new length. With at
+    // most kMetaThreads listed it is read once and stays in registers.
+    int slot = 0, old = 0, now = 0;
+    bool ok = false;
+    auto read = [&](int i0, bool report) {
+        const int i = i0 + tid;
+        if (n <= kMetaThreads && !report) return;
+        ok = false;
+        if (i >= n) return;
+        slot = gld(slots + i);
+        now = gld(new_lens + i);
+        old = slot_len(pt, slot, report && first);
+        ok = old >= 0;
+        if (ok && (now < 0 || now > cap)) {
+            if (report && first) raise_error(SC_DEV_BAD_LENGTH);
+            ok = false;
         }
-        return *old >= 0;
     };
-    int slot, old, now;
-    // The sequences from i0 on: released entries, or with `all` the claimed ones too; .w is
+    // The claims of the sequences from i0 on, as this thread's first one (-1 - it where the
+    // sequence gets a copy of its last page), and the number of all so far.
+    auto claims = [&](int want, int *at) {
+        int mine = 0, copy = 0;
+        if (ok) {
+            const int need = pages_of(pt, now), have = pages_of(pt, old);
+            if (now < old && part_of(pt, now) != 0) {
+                const int id = gld(table_row(pt, slot) + need - 1);
+                copy = page_ok(pt, id) && ld_refs(pt.refs + id) > 1;
+            }
+            mine = copy + max(0, need - have);
+        }
+        int here;
+        const int begin = want + block_scan(mine, &here);
+        *at = copy ? -1 - begin : begin;
+        return want + here;
+    };
+    // The sequences as rows: released entries, or with `all` the claimed ones too; .w is
     // the first claim of a growing one, else -1.
-    auto list = [&](int i0, bool all, bool report) {
+    auto list = [&](int i0, bool all, int at) {
         __syncthreads();
         if (tid == 0) rows.n = min(n - i0, kMetaThreads);
-        const int i = i0 + tid;
-        if (i < n) {
-            const bool ok = lengths(i, &slot, &old, &now, report);
+        if (i0 + tid < n) {
             const int need = pages_of(pt, now), have = pages_of(pt, old);
             const bool grows = all && need > have;
             rows.q[tid] = make_int4(slot, ok ? (grows ? have : need) : 0,
                                     ok ? (grows ? need : max(need, have)) : 0,
-                                    ok && grows ? ld_shared_word(w.offset + i) : -1);
+                                    ok && grows ? at : -1);
         }
         __syncthreads();
     };
     for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
-        list(i0, false, first);
+        read(i0, true);
+        list(i0, false, 0);
         count_entries(pt, rows, -1);
     }
     cluster_sync();
+    // Every CTA counts the claims; CTA 0 looks the pages up.
+    int want = 0, at = 0;
+    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+        read(i0, false);
+        want = claims(want, &at);
+        if (n > kMetaThreads && first && i0 + tid < n) gst(w.offset + i0 + tid, at);
+    }
     if (first) {
-        int want = 0;
-        for (int i0 = 0; i0 < n; i0 += kMetaThreads) {  // claims, in listed order
-            const int i = i0 + tid;
-            int claims = 0, copy = 0;
-            if (i < n && lengths(i, &slot, &old, &now, false)) {
-                const int need = pages_of(pt, now), have = pages_of(pt, old);
-                if (now < old && part_of(pt, now) != 0) {
-                    const int id = gld(table_row(pt, slot) + need - 1);
-                    copy = page_ok(pt, id) && ld_refs(pt.refs + id) > 1;
-                }
-                claims = copy + max(0, need - have);
-            }
-            int here;
-            const int at = want + block_scan(claims, &here);
-            if (i < n) gst(w.offset + i, copy ? -1 - at : at);
-            want += here;
-        }
-        const bool enough = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
-        if (tid == 0) gst(w.n_copies, enough ? 1 : 0);  // until the copies are counted
+        const bool found = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
+        if (tid == 0) gst(w.n_copies, found ? 1 : 0);  // until the copies are counted
     }
     cluster_sync();
     const bool enough = ld_shared_word(w.n_copies) != 0;
     for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
-        list(i0, enough, false);
+        read(i0, false);
+        if (n > kMetaThreads && i0 + tid < n) at = ld_shared_word(w.offset + i0 + tid);
+        list(i0, enough, at);
         if (!enough) {  // take the releases back
             count_entries(pt, rows, 1);
             continue;
         }
-        const int i = i0 + tid;
-        if (first && i < n && lengths(i, &slot, &old, &now, false)) {
-            const int at = gld(w.offset + i);
-            if (at < 0) {
-                int32_t *entry = table_row(pt, slot) + pages_of(pt, now) - 1;
-                const int from = gld(entry), to = gld(w.claimed + (-1 - at));
-                add_refs(pt, from, -1);
-                add_refs(pt, to, 1);
-                gst(entry, to);
-                gst(w.copies + atomicAdd(&s_copies, 1), PageCopy{from, to, part_of(pt, now), 0});
-            }
+        if (first && ok && at < 0) {
+            int32_t *entry = table_row(pt, slot) + pages_of(pt, now) - 1;
+            const int from = gld(entry), to = gld(w.claimed + (-1 - at));
+            add_refs(pt, from, -1);
+            add_refs(pt, to, 1);
+            gst(entry, to);
+            gst(w.copies + atomicAdd(&s_copies, 1), PageCopy{from, to, part_of(pt, now), 0});
         }
         for_entries(rows, [&](int r0, int r1, int c) {
             for (int r = r0; r < r1; ++r) {
@@ -373,8 +383,10 @@ __global__ void __launch_bounds__(kMetaThreads)
         });
     }
     cluster_sync();  // every CTA has read the old lengths
-    for (int i = tid; first && enough && i < n; i += kMetaThreads)
-        if (lengths(i, &slot, &old, &now, false)) gst(pt.lens + slot, now);
+    for (int i0 = 0; first && enough && i0 < n; i0 += kMetaThreads) {
+        read(i0, false);
+        if (ok) gst(pt.lens + slot, now);
+    }
     finish_copies(w, s_copies, enough, pt, pools, inline_copy);
 }
 
@@ -389,69 +401,72 @@ __global__ void __launch_bounds__(kMetaThreads)
     const int tid = threadIdx.x;
     const bool first = cluster_ctarank() == 0;
     if (tid == 0) s_copies = 0;
-    auto pair = [&](int i, int *s, int *d, int *ls, int *ld, bool report) {
-        *s = gld(src + i);
-        *d = gld(dst + i);
-        *ls = slot_len(pt, *s, report);
-        *ld = slot_len(pt, *d, report);
-        if (*s == *d && *ls >= 0) {
-            if (report) raise_error(SC_DEV_BAD_SLOT);
-            return false;
-        }
-        return *ls >= 0 && *ld >= 0;
+    // This thread's pair of those from i0 on. With at most kMetaThreads it is read once.
+    int s = 0, d = 0, ls = 0, ld = 0;
+    bool ok = false;
+    auto read = [&](int i0, bool report) {
+        const int i = i0 + tid;
+        if (n <= kMetaThreads && !report) return;
+        ok = false;
+        if (i >= n) return;
+        s = gld(src + i);
+        d = gld(dst + i);
+        ls = slot_len(pt, s, report && first);
+        ld = slot_len(pt, d, report && first);
+        ok = ls >= 0 && ld >= 0 && s != d;
+        if (s == d && ls >= 0 && report && first) raise_error(SC_DEV_BAD_SLOT);
     };
-    int s, d, ls, ld;
-    // The pairs from i0 on: the destination's own entries, or with `share` its whole row
-    // (.w: the source).
-    auto list = [&](int i0, bool share, bool report) {
+    // The pairs as rows: the destination's own entries, or with `share` its whole row (.w:
+    // the source).
+    auto list = [&](int i0, bool share) {
         __syncthreads();
         if (tid == 0) rows.n = min(n - i0, kMetaThreads);
-        const int i = i0 + tid;
-        if (i < n) {
-            const bool ok = pair(i, &s, &d, &ls, &ld, report);
+        if (i0 + tid < n)
             rows.q[tid] = make_int4(d, 0, !ok ? 0 : share ? pt.max_pages : pages_of(pt, ld), s);
-            if (share) {
-                int last = -1;
-                if (ok && part_of(pt, ls)) {
-                    last = ld_shared_word(w.claimed + ld_shared_word(w.offset + i));
-                    if (first) {
-                        const int old = gld(table_row(pt, s) + full_pages(pt, ls));
-                        add_refs(pt, last, 1);
-                        if (page_ok(pt, old))
-                            gst(w.copies + atomicAdd(&s_copies, 1),
-                                PageCopy{old, last, part_of(pt, ls), 0});
-                        else
-                            raise_error(SC_DEV_BAD_PAGE);
-                    }
-                }
-                s_share[tid] = make_int2(full_pages(pt, ls), last);
-            }
-        }
         __syncthreads();
     };
     for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
-        list(i0, false, first);
+        read(i0, true);
+        list(i0, false);
         count_entries(pt, rows, -1);
     }
     cluster_sync();
+    // Every CTA counts the claims; CTA 0 looks the pages up.
+    int want = 0, at = 0;
+    for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
+        read(i0, false);
+        int here;
+        at = want + block_scan(ok && part_of(pt, ls) != 0, &here);
+        if (n > kMetaThreads && first && i0 + tid < n) gst(w.offset + i0 + tid, at);
+        want += here;
+    }
     if (first) {
-        int want = 0;
-        for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
-            const int i = i0 + tid;
-            const int claims =
-                i < n && pair(i, &s, &d, &ls, &ld, false) && part_of(pt, ls) != 0 ? 1 : 0;
-            int here;
-            const int at = want + block_scan(claims, &here);
-            if (i < n) gst(w.offset + i, at);
-            want += here;
-        }
-        const bool enough = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
-        if (tid == 0) gst(w.n_copies, enough ? 1 : 0);  // until the copies are counted
+        const bool found = want <= pt.n_pages && claim_lowest(pt, want, w.claimed);
+        if (tid == 0) gst(w.n_copies, found ? 1 : 0);  // until the copies are counted
     }
     cluster_sync();
     const bool enough = ld_shared_word(w.n_copies) != 0;
     for (int i0 = 0; i0 < n; i0 += kMetaThreads) {
-        list(i0, enough, false);
+        read(i0, false);
+        if (n > kMetaThreads && i0 + tid < n) at = ld_shared_word(w.offset + i0 + tid);
+        __syncthreads();  // s_share of the pairs before
+        if (enough && i0 + tid < n) {
+            int last = -1;
+            if (ok && part_of(pt, ls)) {
+                last = ld_shared_word(w.claimed + at);
+                if (first) {
+                    const int from = gld(table_row(pt, s) + full_pages(pt, ls));
+                    add_refs(pt, last, 1);
+                    if (page_ok(pt, from))
+                        gst(w.copies + atomicAdd(&s_copies, 1),
+                            PageCopy{from, last, part_of(pt, ls), 0});
+                    else
+                        raise_error(SC_DEV_BAD_PAGE);
+                }
+            }
+            s_share[tid] = make_int2(full_pages(pt, ls), last);
+        }
+        list(i0, enough);
         if (!enough) {
             count_entries(pt, rows, 1);
             continue;
@@ -486,8 +501,10 @@ __global__ void __launch_bounds__(kMetaThreads)
         });
     }
     cluster_sync();  // every CTA has read the old lengths
-    for (int i = tid; first && enough && i < n; i += kMetaThreads)
-        if (pair(i, &s, &d, &ls, &ld, false)) gst(pt.lens + d, ls);
+    for (int i0 = 0; first && enough && i0 < n; i0 += kMetaThreads) {
+        read(i0, false);
+        if (ok) gst(pt.lens + d, ls);
+    }
     finish_copies(w, s_copies, enough, pt, pools, inline_copy);
 }
 
