@@ -271,9 +271,12 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         if (a.beside) pdl_wait();
     };
 
+    // This thread's sequence of the first kThreads; all of them, mostly.
+    int my_slot = 0;
+    const int my_len = tid < a.N ? seq_len(a, tid, &my_slot, blockIdx.x == 0) : -1;
     if (a.shared_keys > 0) {  // as k_prefix finds it: does a sequence hold the whole prefix?
-        bool full = false;
-        for (int i = tid; i < a.N && !full; i += kThreads) {
+        bool full = my_len >= a.shared_keys;
+        for (int i = tid + kThreads; i < a.N && !full; i += kThreads) {
             int slot;
             full = seq_len(a, i, &slot, false) >= a.shared_keys;
         }
@@ -290,8 +293,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     // the total with them.
     auto scan = [&](int i0, int64_t base, int64_t *begin, int64_t *mine, bool report) {
         const int i = i0 + tid;
-        int slot = 0;
-        const int len = i < a.N ? seq_len(a, i, &slot, report) : -1;
+        int slot = my_slot, len = my_len;
+        if (i0 > 0) len = i < a.N ? seq_len(a, i, &slot, report) : -1;
         *mine = (int64_t)per * own_tiles(a, len);
         int64_t inc = *mine;
 #pragma unroll
@@ -921,12 +924,14 @@ static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count) {
     x.U = (int64_t)s.Hkv * (x.split ? 1 : (x.n_tiles + 1) / 2) * x.T;
     const int ctas = sm_count < kMaxPrefixCtas ? sm_count : kMaxPrefixCtas;
     x.n_cta = (int)(x.U < ctas ? x.U : ctas);
-    // A small prefix (at most two units an SM) costs fixed latencies more than work: it takes
-    // a CTA for every four units, and the own parts run on the other SMs meanwhile.
-    // 64 sequences behind 4096 tokens: 50 us one after the other, 42 so; 37 x 3 drafts with
-    // 128-wide heads behind 2976: 38 and 26.
-    x.a.beside = x.U > 0 && x.U <= 2 * ctas && ctas >= 8;
-    if (x.a.beside) x.n_cta = (int)((x.U + 3) / 4);
+    // A small prefix costs fixed latencies more than work: it takes a CTA for every eight
+    // units (four of 128-wide heads), up to half the SMs, and the own parts run on the
+    // others meanwhile. 64 sequences behind 4096 tokens: 50 us one after the other, 37 so
+    // (42 with a CTA for every four units); 37 x 3 drafts with 128-wide heads behind
+    // 2976: 38 and 26.
+    const int units = s.Dh == 64 ? 8 : 4;
+    x.a.beside = x.U > 0 && x.U <= (int64_t)units * (ctas / 2);
+    if (x.a.beside) x.n_cta = (int)((x.U + units - 1) / units);
     return x;
 }
 static size_t prefix_part_floats(const AttnShape &s) {
