@@ -448,23 +448,35 @@ def _rows(t, name, dtype, shape):
     return t.data_ptr(), (strides[0] if shape[0] > 1 else width)
 
 
+_I32, _BF16 = torch.int32, torch.bfloat16
+
+
+def _ints(t, name, shape) -> int:
+    """``_dev`` for an int32 array, with one test on the way that calls usually take."""
+    if (type(t) is torch.Tensor and t.is_cuda and t.dtype is _I32 and t.is_contiguous()
+            and t.shape == shape):
+        return t.data_ptr()
+    return _dev(t, name, _I32, shape)
+
+
 def _cache(refs, table, lens):
     n_slots, max_pages = table.shape
-    return (_dev(refs, "refs", torch.int32, (refs.shape[0],)), refs.shape[0],
-            _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (n_slots,)),
-            n_slots, max_pages)
+    n_pages = refs.shape[0]
+    return (_ints(refs, "refs", (n_pages,)), n_pages, _ints(table, "table", (n_slots, max_pages)),
+            _ints(lens, "lens", (n_slots,)), n_slots, max_pages)
 
 
 def _pools(k_pages, v_pages, n_pages):
     """(page_size, L, token_bytes, k, v) of [L, n_pages, page_size, Hkv, Dh] or
     [n_pages, page_size, Hkv, Dh] pools."""
-    shape = tuple(k_pages.shape) if k_pages.dim() == 5 else (1,) + tuple(k_pages.shape)
+    full = k_pages.shape
+    shape = full if len(full) == 5 else (1,) + full
     if len(shape) != 5 or shape[1] != n_pages:
         raise ValueError("k_pages must be [L, n_pages, page_size, Hkv, Dh] or "
                          "[n_pages, page_size, Hkv, Dh]")
     _dcode(k_pages)
     return (shape[2], shape[0], shape[3] * shape[4] * k_pages.element_size(),
-            _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype, k_pages.shape))
+            _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype, full))
 
 
 # Scratch straight from torch's caching allocator: no tensor object (3 us of host time a
@@ -518,8 +530,8 @@ def pages_resize(refs, table, lens, slot_ids, new_lens, k_pages, v_pages, worksp
     _call_with_workspace(
         "shortconv_pages_resize", lib().shortconv_pages_resize, workspace,
         pages_workspace_bytes(refs.shape[0], n), refs.device, stream,
-        *_cache(refs, table, lens), ps, _dev(slot_ids, "slot_ids", torch.int32, (n,)),
-        _dev(new_lens, "new_lens", torch.int32, (n,)), n, L, token_bytes, kp, vp)
+        *_cache(refs, table, lens), ps, _ints(slot_ids, "slot_ids", (n,)),
+        _ints(new_lens, "new_lens", (n,)), n, L, token_bytes, kp, vp)
 
 
 def pages_fork(refs, table, lens, src_slots, dst_slots, k_pages, v_pages, workspace=None,
@@ -531,8 +543,8 @@ def pages_fork(refs, table, lens, src_slots, dst_slots, k_pages, v_pages, worksp
     _call_with_workspace(
         "shortconv_pages_fork", lib().shortconv_pages_fork, workspace,
         pages_workspace_bytes(refs.shape[0], n), refs.device, stream,
-        *_cache(refs, table, lens), ps, _dev(src_slots, "src_slots", torch.int32, (n,)),
-        _dev(dst_slots, "dst_slots", torch.int32, (n,)), n, L, token_bytes, kp, vp)
+        *_cache(refs, table, lens), ps, _ints(src_slots, "src_slots", (n,)),
+        _ints(dst_slots, "dst_slots", (n,)), n, L, token_bytes, kp, vp)
 
 
 def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=None, stream=None):
@@ -545,7 +557,7 @@ def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=No
         "shortconv_pages_compact", lib().shortconv_pages_compact, workspace,
         pages_workspace_bytes(refs.shape[0], 0), refs.device, stream,
         *_cache(refs, table, lens), ps, L, token_bytes, kp, vp,
-        _dev(n_used, "n_used", torch.int32, (1,)))
+        _ints(n_used, "n_used", (1,)))
     return n_used
 
 
@@ -553,18 +565,20 @@ def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None):
     """Write each listed sequence's ``D`` newest tokens, already counted in ``lens``:
     ``k``, ``v`` ``[N*D, Hkv, Dh]`` (rows may be strided) into one layer's pools."""
     N = slot_ids.shape[0]
-    n_pages, ps, Hkv, Dh = k_pages.shape
+    pool = k_pages.shape
+    n_pages, ps, Hkv, Dh = pool
+    n_slots, max_pages = table.shape
     dt = k_pages.dtype
-    _dcode(k_pages)
-    es = k_pages.element_size()
+    es = 2 if dt is _BF16 else 4 if _dcode(k_pages) == SC_F32 else 0
     k_p, k_s = _rows(k, "k", dt, (N * D, Hkv, Dh))
     v_p, v_s = _rows(v, "v", dt, (N * D, Hkv, Dh))
-    _raise_on("shortconv_pages_append", lib().shortconv_pages_append(
+    status = lib().shortconv_pages_append(
         k_p, k_s * es, v_p, v_s * es, N, D, Hkv * Dh * es, _dev(k_pages, "k_pages"),
-        _dev(v_pages, "v_pages", dt, k_pages.shape), n_pages, ps,
-        _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (table.shape[0],)),
-        table.shape[0], table.shape[1], _dev(slot_ids, "slot_ids", torch.int32, (N,)),
-        _stream(stream, k_pages.device)))
+        _dev(v_pages, "v_pages", dt, pool), n_pages, ps,
+        _ints(table, "table", (n_slots, max_pages)), _ints(lens, "lens", (n_slots,)), n_slots,
+        max_pages, _ints(slot_ids, "slot_ids", (N,)), _stream(stream, k_pages.device))
+    if status:
+        _raise_on("shortconv_pages_append", status)
 
 
 @functools.lru_cache(maxsize=1024)
@@ -579,22 +593,27 @@ def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages
     sequence in ``slot_ids[i]``. The first ``shared_pages`` pages are the same for all
     listed sequences and read once. Returns ``out [N*D, Hq, Dh]``."""
     N = slot_ids.shape[0]
-    n_pages, ps, Hkv, Dh = k_pages.shape
+    pool = k_pages.shape
+    n_pages, ps, Hkv, Dh = pool
+    n_slots, max_pages = table.shape
     Hq = q.shape[1]
-    dt = torch.bfloat16
+    rows = (N * D, Hq, Dh)
+    device = q.device
     if scale is None:
         scale = Dh ** -0.5
     if out is None:
-        out = torch.empty((N * D, Hq, Dh), dtype=dt, device=q.device)
-    q_p, q_s = _rows(q, "q", dt, (N * D, Hq, Dh))
+        out = torch.empty(rows, dtype=_BF16, device=device)
+        out_p = out.data_ptr()
+    else:
+        out_p = _dev(out, "out", _BF16, rows)
+    q_p, q_s = _rows(q, "q", _BF16, rows)
     _call_with_workspace(
         "shortconv_prefix_attention", lib().shortconv_prefix_attention, workspace,
-        prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages), q.device, stream,
-        _dcode(q), Hq, Hkv, Dh, q_p, q_s, N, D, _dev(k_pages, "k_pages", dt),
-        _dev(v_pages, "v_pages", dt, k_pages.shape), n_pages, ps,
-        _dev(table, "table", torch.int32), _dev(lens, "lens", torch.int32, (table.shape[0],)),
-        table.shape[0], table.shape[1], _dev(slot_ids, "slot_ids", torch.int32, (N,)),
-        shared_pages, scale, _dev(out, "out", dt, (N * D, Hq, Dh)))
+        prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages), device, stream,
+        SC_BF16, Hq, Hkv, Dh, q_p, q_s, N, D, _dev(k_pages, "k_pages", _BF16),
+        _dev(v_pages, "v_pages", _BF16, pool), n_pages, ps,
+        _ints(table, "table", (n_slots, max_pages)), _ints(lens, "lens", (n_slots,)), n_slots,
+        max_pages, _ints(slot_ids, "slot_ids", (N,)), shared_pages, scale, out_p)
     return out
 
 
@@ -608,35 +627,38 @@ def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, 
     N, D1, V = target.shape
     D = D1 - 1
     dt = target.dtype
-
-    def rows(t, name, n):  # [N, n, V] with every row the same distance apart
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
-        if t.dtype != dt:
-            raise TypeError(f"{name} must be {dt}, got {t.dtype}")
-        if t.shape != (N, n, V):
-            raise ValueError(f"{name} must have shape {(N, n, V)}, got {tuple(t.shape)}")
-        s0, s1, s2 = t.stride()
-        if (V > 1 and s2 != 1) or (n > 1 and N > 1 and s0 != n * s1):
-            raise ValueError(f"{name} must have contiguous, evenly spaced rows")
-        return t.data_ptr(), max(V, s1 if n > 1 else s0)  # of a single row: any step
-
-    code = _dcode(target)
-    tok_p = _dev(tokens, "tokens", torch.int32, (N, D))
-    t_p, t_s = rows(target, "target", D + 1)
-    d_p, d_s = (None, V) if draft is None else rows(draft, "draft", D)
+    code = SC_F32 if dt is torch.float32 else _dcode(target)
+    device = target.device
+    t_p, t_s = _prob_rows(target, "target", dt, (N, D1, V))
+    d_p, d_s = (None, V) if draft is None else _prob_rows(draft, "draft", dt, (N, D, V))
     if accepted is None:
-        accepted = torch.empty((N,), dtype=torch.int32, device=target.device)
+        accepted = torch.empty((N,), dtype=_I32, device=device)
     if out_tokens is None:
-        out_tokens = torch.empty((N, D + 1), dtype=torch.int32, device=target.device)
-    _raise_on("shortconv_draft_accept", lib().shortconv_draft_accept(
-        code, V, N, D, t_p, t_s, d_p, d_s, tok_p,
-        None if n_drafts is None else _dev(n_drafts, "n_drafts", torch.int32, (N,)),
-        _dev(uniforms, "uniforms", torch.float32, (N, D + 1)),
-        _dev(accepted, "accepted", torch.int32, (N,)),
-        _dev(out_tokens, "out_tokens", torch.int32, (N, D + 1)),
-        _stream(stream, target.device)))
+        out_tokens = torch.empty((N, D1), dtype=_I32, device=device)
+    status = lib().shortconv_draft_accept(
+        code, V, N, D, t_p, t_s, d_p, d_s, _ints(tokens, "tokens", (N, D)),
+        None if n_drafts is None else _ints(n_drafts, "n_drafts", (N,)),
+        _dev(uniforms, "uniforms", torch.float32, (N, D1)), _ints(accepted, "accepted", (N,)),
+        _ints(out_tokens, "out_tokens", (N, D1)), _stream(stream, device))
+    if status:
+        _raise_on("shortconv_draft_accept", status)
     return accepted, out_tokens
+
+
+def _prob_rows(t, name, dtype, shape):
+    """Data pointer and row distance of ``[N, n, V]`` probabilities whose rows are
+    contiguous and evenly spaced."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    N, n, V = shape
+    s0, s1, s2 = t.stride()
+    if (V > 1 and s2 != 1) or (n > 1 and N > 1 and s0 != n * s1):
+        raise ValueError(f"{name} must have contiguous, evenly spaced rows")
+    return t.data_ptr(), max(V, s1 if n > 1 else s0)  # of a single row: any step
 
 
 def check_wait_limit(stream=None, device=None) -> None:
