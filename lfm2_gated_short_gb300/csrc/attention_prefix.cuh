@@ -20,6 +20,13 @@
 // Dh = 128 O leaves room for two. O is rescaled only when a row's maximum rose by more
 // than 2^8 since the last time: weights then stay below 2^8, exact enough in
 // the fp32 sums and bf16's exponent range.
+//
+// 1024 rows x 32 heads x 16384 keys of 64: 125 us (1.1 PFLOP/s), tensor cores and
+// exponential unit 48 % busy each. A tile's softmax bounds it: its maxima take 470
+// cycles and its exponentials 850 with both streams at it (1720 a tile and stream in
+// all), the products 512 a tile. Measured slower or the same: exponentials computed while
+// the maximum is still sought and S read again where it rose (141 us), S read twice
+// instead of kept in registers (20 us more), turns at the exponentials (122-124).
 #pragma once
 
 namespace sc {
