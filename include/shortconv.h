@@ -512,13 +512,14 @@ sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v,
  *   out = sum_t exp(scale q.k_t) v_t / sum_t exp(scale q.k_t).
  * A row without keys (p < 0) is zeros. Scores, maxima and sums are held in
  * fp32, the weights enter the second product in bf16, out is rounded once.
- * Nothing past lens is looked at: it may hold NaN.
+ * What a row does not see (past lens, or a later draft) may hold anything, NaN
+ * included.
  *
  * shared_pages: the caller's word that the first shared_pages table entries
  * of all listed sequences are equal (branches forked from one prompt); that
  * part of every row's keys is then read once for the whole batch. 0 is
- * always right. Every listed sequence must hold at least one entry it shares;
- * a row that ends inside the shared part sees its own keys alone.
+ * always right. A sequence whose first new token does not see all of the shared
+ * part (lens - D + 1 < shared_pages * page_size) is computed by itself.
  *
  *   Hq, Hkv, Dh   Hq a multiple of Hkv, Hq / Hkv <= 128; Dh 64 or 128
  *   q             device [N*D, Hq, Dh] bf16, q_stride elements between rows

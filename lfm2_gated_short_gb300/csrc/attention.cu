@@ -53,8 +53,7 @@ struct AttnArgs {
     PageTable pt;
     const int32_t *slots;
     int N, D, G, Hkv, Dh;
-    int shared_keys;   // keys whose part k_prefix computes, if a sequence holds them all
-    const int *leader; // k_prefix's word on that: < 0 when none does (unused without a prefix)
+    int shared_keys;   // keys whose part k_prefix computes (see prefix_keys)
     int beside;        // k_own runs beside k_prefix, on the SMs that it leaves
     float scale_log2;  // scale * log2(e)
     bf16 *out;
@@ -94,9 +93,15 @@ __device__ __forceinline__ int seq_len(const AttnArgs &a, int i, int *slot, bool
     return len;
 }
 
+// Keys of a sequence of len tokens whose part k_prefix computes: the shared ones when every
+// row sees them all, else none (that sequence's part is then its own from key 0 on, and k_prefix
+// needs no mask: a weight of 0 would not silence a NaN in a V row that another row sees).
+__device__ __forceinline__ int prefix_keys(const AttnArgs &a, int len) {
+    return len - a.D + 1 >= a.shared_keys ? a.shared_keys : 0;
+}
 // Key tiles of a sequence's own part.
 __device__ __forceinline__ int own_tiles(const AttnArgs &a, int len) {
-    return len > a.shared_keys ? (len - a.shared_keys + kKT - 1) / kKT : 0;
+    return len > 0 ? (len - prefix_keys(a, len) + kKT - 1) / kKT : 0;
 }
 
 // An item piece as the producer describes it to the consumers: tiles t0 .. t0 + n - 1
@@ -204,6 +209,55 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// Whether some of eight bf16 values is an infinity or NaN.
+__device__ __forceinline__ bool not_finite(const uint4 &v) {
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t w = e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
+        bad |= (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+    }
+    return bad;
+}
+
+// o += P V over a warp's 16 KB keys from key0 on (rows row0 .. of the swizzled V tile at vb),
+// of each row only the keys it sees. P and o are laid out as mma16816's operands.
+template <int DH, int KB>
+__device__ __forceinline__ void product_one_by_one(float (&o)[DH / 8][4],
+                                                   const uint32_t (&pf)[KB][4],
+                                                   const unsigned char *vb, uint32_t block,
+                                                   int row0, int key0, const int (&see)[2]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (int k = 0; k < 16 * KB; ++k) {
+        uint32_t w2[2] = {0, 0};
+#pragma unroll
+        for (int nt = 0; nt < 2 * KB; ++nt)
+            if (nt == k >> 3) {
+                w2[0] = pf[nt / 2][nt % 2 * 2];
+                w2[1] = pf[nt / 2][nt % 2 * 2 + 1];
+            }
+        float w[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const uint32_t x = __shfl_sync(~0u, w2[p], (lane & ~3) | (k & 7) >> 1);
+            w[p] = __uint_as_float(k & 1 ? x & 0xFFFF0000u : x << 16);
+        }
+#pragma unroll
+        for (int d = 0; d < DH / 8; ++d) {
+            const uint32_t v = *reinterpret_cast<const uint32_t *>(
+                vb + (d >> 3) * block + swz(row0 + k, d & 7) + (lane & 3) * 4);
+            const float v0 = __uint_as_float(v << 16), v1 = __uint_as_float(v & 0xFFFF0000u);
+#pragma unroll
+            for (int p = 0; p < 2; ++p)
+                if (key0 + k < see[p]) {
+                    o[d][2 * p] = fmaf(w[p], v0, o[d][2 * p]);
+                    o[d][2 * p + 1] = fmaf(w[p], v1, o[d][2 * p + 1]);
+                }
+        }
+    }
+}
+
 // RG groups of 16 rows times KG key groups: a consumer warp takes 16 rows by 64 / KG keys of
 // a tile. 16 rows are bound by the tiles' bytes, and more, lighter warps start and
 // end an item sooner; 32 rows of 64 columns are bound by the warps' own latency,
@@ -279,14 +333,6 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     // This thread's sequence of the first kThreads; all of them, mostly.
     int my_slot = 0;
     const int my_len = tid < a.N ? seq_len(a, tid, &my_slot, blockIdx.x == 0) : -1;
-    if (a.shared_keys > 0) {  // as k_prefix finds it: does a sequence hold the whole prefix?
-        bool full = my_len >= a.shared_keys;
-        for (int i = tid + kThreads; i < a.N && !full; i += kThreads) {
-            int slot;
-            full = seq_len(a, i, &slot, false) >= a.shared_keys;
-        }
-        if (!__syncthreads_or(full)) a.shared_keys = 0;
-    }
 
     // The units of the call and the sequence that holds this CTA's first one.
     const int rows = a.D * a.G;
@@ -347,7 +393,6 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         // takes thousands of cycles, which no consumer then waits for.
         const int ps = a.pt.page_size;
         const int box = min(ps, kKT), nb = kKT / box;  // keys of a box, boxes of a tile
-        const int first_box = a.shared_keys / box;
         // Slots and lengths of 32 sequences from `known` on, one a lane.
         int known = s_seq, slot_l = 0, len_l = -1;
         auto fetch = [&](int from) {
@@ -362,7 +407,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         };
         fetch(known);
         struct Seq {
-            int i, len, T, c, n;  // c, n: this lane's first page ids, as PageIds::begin takes them
+            int i, len, T, first, c, n;  // first own box; c, n: this lane's first page ids, as
+                                         // PageIds::begin takes them
             PageIds ids;
         };
         // The next sequence from i on with keys of its own (i = N: none).
@@ -377,7 +423,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             s.i = i;
             if (i >= a.N) return;
             const int slot = __shfl_sync(~0u, slot_l, i - known);
-            s.ids.start(a.pt.table + (int64_t)slot * a.pt.max_pages, ps / box, first_box,
+            s.first = prefix_keys(a, s.len) / box;
+            s.ids.start(a.pt.table + (int64_t)slot * a.pt.max_pages, ps / box, s.first,
                         (s.len - 1) / box);
             s.c = s.ids.cur;
             s.n = s.ids.nxt;
@@ -414,7 +461,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         };
         auto produce = [&](Seq &s, const OwnItem &it) {
             if (!announce(it)) return false;
-            s.ids.begin(first_box + it.t0 * nb, s.c, s.n, it.t0 == 0);
+            s.ids.begin(s.first + it.t0 * nb, s.c, s.n, it.t0 == 0);
             for (int t = 0; t < it.n; ++t, ++g) {
                 const uint32_t st = g % ST;
                 if (g >= ST && !mbar_wait_bounded(&s_empty[st], (g / ST - 1) & 1u)) {
@@ -543,7 +590,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
         bool bad = false;
-        int key0 = a.shared_keys + t0 * kKT + kw * 16 * KB;
+        const int from = prefix_keys(a, len);
+        int key0 = from + t0 * kKT + kw * 16 * KB;
         for (int t = 0; t < n; ++t, key0 += kKT) {
             if (!dead && !mbar_wait_bounded(&s_full[ring_at], ring_phase)) {
                 raise_error(SC_DEV_TIMEOUT);
@@ -554,9 +602,9 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
             const bool tail = key0 + 16 * KB > len;
             if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
-                const int from = max(0, len - key0);
-                for (int x = lane; x < (16 * KB - from) * C::NB * 8; x += 32) {
-                    const int r = from + x / (C::NB * 8), ch = x % (C::NB * 8);
+                const int first = max(0, len - key0);
+                for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
+                    const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
                     *reinterpret_cast<uint4 *>(ring + ring_at * C::kStage +
                                                (C::NB + (ch >> 3)) * C::kBlk +
                                                (kw * 16 * KB + r) * 128 +
@@ -629,15 +677,30 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                     pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
                 }
             }
+            // A draft that some row does not see: were its V not finite, a weight of 0 would
+            // not keep it from that row, so the block's product is made one by one.
+            bool plain = false;
+            if (key0 + 16 * KB > least) {
+                const unsigned char *vb = ring + ring_at * C::kStage + C::NB * C::kBlk;
+                const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
+                for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
+                    plain |= not_finite(*reinterpret_cast<const uint4 *>(
+                        vb + (x % (DH / 8) >> 3) * C::kBlk +
+                        swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
+                plain = __any_sync(~0u, plain);
+                if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
+            }
+            if (!plain) {
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+                for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                for (int dd = 0; dd < DH / 16; ++dd) {
-                    uint32_t b[4];
-                    ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
-                    mma16816(o[2 * dd], pf[kb], b[0], b[1]);
-                    mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
-                }
+                    for (int dd = 0; dd < DH / 16; ++dd) {
+                        uint32_t b[4];
+                        ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
+                        mma16816(o[2 * dd], pf[kb], b[0], b[1]);
+                        mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
+                    }
+            }
             if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[ring_at]);
@@ -668,7 +731,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                     make_float2(o[d][2 * p], o[d][2 * p + 1]);
         }
         named_sync(1, 32 * C::kWarps);
-        const bool whole = n == item.T && a.shared_keys == 0;  // nothing to join with
+        const bool whole = n == item.T && from == 0;  // nothing to join with
         float *part = a.own_part + (int64_t)(item.w + blockIdx.x) * C::kSlot;
         bf16 *out = a.out + ((int64_t)i * a.D * a.Hkv + h) * a.G * DH;
 #pragma unroll
@@ -732,10 +795,10 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
     const int at = blockIdx.y * (kMergeThreads / L) + threadIdx.x / L;
     const int hq = min(at, Hq - 1);  // lanes past the last row join it and write nothing
     const int h = hq / a.G, g = hq - h * a.G;
-    const bool prefix = a.shared_keys > 0 && gld(a.leader) >= 0;
     const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
     int slot;
-    const bool valid = seq_len(a, i, &slot, false) >= 0;
+    const int len = seq_len(a, i, &slot, false);
+    const bool valid = len >= 0, prefix = prefix_keys(a, len) > 0;
 
     // The row's parts: prefix_n from prefix_at on, own_n from own_at on (its O; m and l
     // are at +m_off and +l_off).
@@ -913,7 +976,7 @@ static size_t own_part_floats(const AttnShape &s) {
         (size_t)s.N * s.Hkv * (((size_t)s.D * (s.Hq / s.Hkv) + MR - 1) / MR);
     return (items + kMaxCtas) * MR * (s.Dh + 2);
 }
-// [N + 1] first tiles, then k_prefix's leader.
+// [N + 1] first tiles.
 static size_t cum_bytes(const AttnShape &s) { return ((size_t)s.N + 3) / 2 * 16; }
 
 // The prefix's work: everything but the pointers.
@@ -1003,8 +1066,6 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.scale_log2 = scale * kLog2e;
     a.out = (bf16 *)out;
     a.cum = (int64_t *)workspace;
-    x.leader = (int *)(a.cum + s.N + 1);
-    a.leader = x.leader;
     a.own_part = (float *)((char *)workspace + cum_bytes(s));
     x.part = a.own_part + own_part_floats(s);
     CUtensorMap mk, mv;

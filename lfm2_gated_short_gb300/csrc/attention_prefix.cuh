@@ -1,8 +1,8 @@
 // attention_prefix.cuh -- the shared prefix's part of attention.cu, on the
 // tcgen05 tensor cores.
 //
-// Every row of the call sees the prefix's keys, so for one kv head the rows
-// of all sequences (N D G of them) are one query matrix against one K and V:
+// For one kv head the rows of all sequences (N D G of them) are one query matrix against
+// one K and V (rows that do not see all of the prefix are computed along; nothing reads them):
 // tiles of 128 rows by 128 keys, S = Q K^T and O += P V with accumulators in
 // TMEM, P written back to TMEM as the second product's bf16 operand.
 //
@@ -45,7 +45,6 @@ struct PrefixArgs {
     int64_t U;      // units of the call
     int n_cta;
     float *part;    // [2 (items + CTAs)] parts of 128 rows: O [128][Dh], m [128], l [128]
-    int *leader;    // the listed sequence whose table names the prefix, or -1
 };
 
 template <int DH>
@@ -215,18 +214,16 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     const uint32_t tmem = b.tmem;
     pdl_wait();
     pdl_launch_dependents();
-    // The first listed sequence that holds the whole prefix names its pages.
+    // The first listed sequence whose rows all see the whole prefix names its pages.
     for (int i = tid; i < a.N; i += kPfxThreads) {
         int slot;
-        if (seq_len(a, i, &slot, false) >= x.P) {
+        if (prefix_keys(a, seq_len(a, i, &slot, false)) > 0) {
             atomicMin(&b.leader, i);
             break;
         }
     }
     __syncthreads();
     const int leader = b.leader;
-    if (blockIdx.x == 0 && tid == 0) gst(x.leader, leader < a.N ? leader : -1);
-
     const int64_t u0 = share_begin(blockIdx.x, x.U, x.n_cta);
     const int64_t u1 = leader < a.N ? share_begin(blockIdx.x + 1, x.U, x.n_cta) : u0;
     const int per = x.split ? 2 : 1;  // key tiles of a unit
@@ -423,14 +420,6 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             const uint32_t seq0 = seq;
             seq += (uint32_t)n * streams;
             if (tile >= x.n_tiles) return true;  // the second stream has no rows
-            // Keys of the prefix that this thread's row sees.
-            const int64_t token = (int64_t)tile * x.tpt + r / a.G;
-            int limit = 0;
-            if (r < x.tpt * a.G && token < (int64_t)a.N * a.D) {
-                int slot;
-                const int i = (int)(token / a.D), j = (int)(token % a.D);
-                limit = min(x.P, max(0, seq_len(a, i, &slot, false) - a.D + j + 1));
-            }
             float m = -INFINITY, l = 0.0f;
             for (int t = 0; t < n; ++t) {
                 const int key0 = ((t0 + t) * per + (x.split ? s : 0)) * kPK;
@@ -442,10 +431,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                 for (int c = 0; c < kPK / 32; ++c) tmem_ld32(st + c * 32, v + c * 32);
                 tmem_ld_wait();
                 regs_ready(v);
-                if (key0 + kPK > limit) {
+                if (key0 + kPK > x.P) {
 #pragma unroll
                     for (int c = 0; c < kPK; ++c)
-                        if (key0 + c >= limit) v[c] = 0xFF800000u;  // -inf
+                        if (key0 + c >= x.P) v[c] = 0xFF800000u;  // -inf
                 }
                 float top[4];
 #pragma unroll
