@@ -508,6 +508,14 @@ def _call_with_workspace(name, fn, workspace, need, device, stream, *args):
         _raise_on(name, status)
 
 
+def _output(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on, for the same reason."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def page_cache(n_slots: int, max_pages: int, n_pages: int, device="cuda"):
     """``(refs [n_pages], table [n_slots, max_pages], lens [n_slots])`` of an empty cache."""
     i32 = dict(dtype=torch.int32, device=device)
@@ -552,7 +560,7 @@ def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=No
     ``n_used [1]``: no page at or past it is in use."""
     ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
     if n_used is None:
-        n_used = torch.empty((1,), dtype=torch.int32, device=refs.device)
+        n_used = _output((1,), _I32, refs.device, stream)
     _call_with_workspace(
         "shortconv_pages_compact", lib().shortconv_pages_compact, workspace,
         pages_workspace_bytes(refs.shape[0], 0), refs.device, stream,
@@ -602,7 +610,7 @@ def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages
     if scale is None:
         scale = Dh ** -0.5
     if out is None:
-        out = torch.empty(rows, dtype=_BF16, device=device)
+        out = _output(rows, _BF16, device, stream)
         out_p = out.data_ptr()
     else:
         out_p = _dev(out, "out", _BF16, rows)
@@ -632,9 +640,9 @@ def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, 
     t_p, t_s = _prob_rows(target, "target", dt, (N, D1, V))
     d_p, d_s = (None, V) if draft is None else _prob_rows(draft, "draft", dt, (N, D, V))
     if accepted is None:
-        accepted = torch.empty((N,), dtype=_I32, device=device)
+        accepted = _output((N,), _I32, device, stream)
     if out_tokens is None:
-        out_tokens = torch.empty((N, D1), dtype=_I32, device=device)
+        out_tokens = _output((N, D1), _I32, device, stream)
     status = lib().shortconv_draft_accept(
         code, V, N, D, t_p, t_s, d_p, d_s, _ints(tokens, "tokens", (N, D)),
         None if n_drafts is None else _ints(n_drafts, "n_drafts", (N,)),
