@@ -77,15 +77,22 @@ __host__ __device__ __forceinline__ int share_of(int64_t u, int64_t U, int64_t n
     return (int)(x / U);
 }
 
+// Slots, lengths and tables are read in L2: k_own beside k_prefix starts without a wait of
+// its own, which would also drop what its SM's L1 holds of them from before they changed.
+__device__ __forceinline__ int gld_l2(const int32_t *p) {
+    if (!SC_RD_OK(p, 4)) return 0;
+    return __ldcg(p);
+}
+
 // Tokens of sequence i (its D new ones included), or -1 with a bad slot or length.
 __device__ __forceinline__ int seq_len(const AttnArgs &a, int i, int *slot, bool report) {
-    const int s = gld(a.slots + i);
+    const int s = gld_l2(a.slots + i);
     *slot = s;
     if (s < 0 || s >= a.pt.n_slots) {
         if (report) raise_error(SC_DEV_BAD_SLOT);
         return -1;
     }
-    const int len = gld(a.pt.lens + s);
+    const int len = gld_l2(a.pt.lens + s);
     if (len < 0 || len > (int64_t)a.pt.max_pages * a.pt.page_size) {
         if (report) raise_error(SC_DEV_BAD_LENGTH);
         return -1;
@@ -148,7 +155,7 @@ struct PageIds {
         nxt = known ? n : load(b0 + 32);
     }
     __device__ __forceinline__ int load(int b) const {
-        return gld(row + (min(b + (int)(threadIdx.x & 31), last) >> shift));
+        return gld_l2(row + (min(b + (int)(threadIdx.x & 31), last) >> shift));
     }
     // The tile's first box, and lane k's page of its k-th box.
     __device__ __forceinline__ int box() const { return b0 + at; }
