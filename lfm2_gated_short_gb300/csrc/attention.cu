@@ -792,8 +792,6 @@ namespace sc {
 constexpr int kMergeThreads = 256;
 template <int DH, int PG>
 __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, int own_ctas) {
-    pdl_wait();
-    pdl_launch_dependents();
     AttnArgs &a = x.a;
     constexpr int L = DH / 8 * PG;
     const int rl = threadIdx.x % L, c8 = rl % (DH / 8), group = rl / (DH / 8);
@@ -802,7 +800,7 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
     const int at = blockIdx.y * (kMergeThreads / L) + threadIdx.x / L;
     const int hq = min(at, Hq - 1);  // lanes past the last row join it and write nothing
     const int h = hq / a.G, g = hq - h * a.G;
-    const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
+    // Slots and lengths need no wait: k_own let this kernel start when what wrote them was done.
     int slot;
     const int len = seq_len(a, i, &slot, false);
     const bool valid = len >= 0, prefix = prefix_keys(a, len) > 0;
@@ -823,6 +821,9 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
         step = x.split ? kPSlot : 2 * kPSlot;
         prefix_n = (c1 - c0 + 1) * (x.split ? 2 : 1);
     }
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
     const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * a.Hkv;
     const int oslot = MR * (DH + 2), rt = r / MR, orow = r - rt * MR;
     if (u_n > u_i) {
@@ -857,6 +858,25 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
             m = gld(ml);
             l = gld(ml + (pre ? kPR : MR));
         }
+        // Parts are loaded before the factors are known: with few rows, up to 32 (Dh 64) or 16 at
+        // once, since the kernel is then a chain of dependent reads.
+        const int here = min(L, parts - p0), rounds = min(L, most - p0);
+        constexpr int kAhead = PG > 1 ? 8 : 4;
+        float4 v[kAhead][2];
+        auto fetch = [&](int q0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int q = q0 + k * PG + group;
+                if (q < here) {
+                    const float4 *from = reinterpret_cast<const float4 *>(
+                        p0 + q < prefix_n ? prefix_at + (int64_t)(p0 + q) * step
+                                          : own_from + (int64_t)(p0 + q) * oslot);
+                    v[k][0] = gld(from + c8 * 2);
+                    v[k][1] = gld(from + c8 * 2 + 1);
+                }
+            }
+        };
+        fetch(0);
         float now = fmaxf(top, m);
         int nan = m != m;
 #pragma unroll
@@ -874,21 +894,8 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] *= f0;
         top = now;
-        const int here = min(L, parts - p0), rounds = min(L, most - p0);
-        constexpr int kAhead = 4;  // parts loaded before the first is added
         for (int q0 = 0; q0 < rounds; q0 += kAhead * PG) {
-            float4 v[kAhead][2];
-#pragma unroll
-            for (int k = 0; k < kAhead; ++k) {
-                const int q = q0 + k * PG + group;
-                if (q < here) {
-                    const float4 *from = reinterpret_cast<const float4 *>(
-                        p0 + q < prefix_n ? prefix_at + (int64_t)(p0 + q) * step
-                                          : own_from + (int64_t)(p0 + q) * oslot);
-                    v[k][0] = gld(from + c8 * 2);
-                    v[k][1] = gld(from + c8 * 2 + 1);
-                }
-            }
+            if (q0 > 0) fetch(q0);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 const int q = q0 + k * PG + group;
