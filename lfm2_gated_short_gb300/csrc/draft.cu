@@ -211,6 +211,7 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
     __shared__ int s_a, s_n;
     __shared__ u64 s_warp[kDraftWarps];
     __shared__ u64 s_total[2][kMaxDraftCluster];  // every CTA's sum, by pass
+    __shared__ u64 s_found[kMaxDraftCluster];     // and what it found: a, and whether a < n
     pdl_wait();
     pdl_launch_dependents();
     cluster_arrive();  // every CTA of the cluster runs before one stores to another
@@ -253,8 +254,14 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
     __syncthreads();
     const int a = s_a;
     cluster_wait();
-    if (a < 0) {  // bad drafts: nothing accepted, no token (every CTA of the cluster leaves)
-        if (rank == 0) {
+    // No CTA leaves before all know what each found: a store to one that has left faults.
+    if (tid < C)
+        st_cluster_u64(cluster_map(smem_addr(&s_found[rank]), tid),
+                       (u64)(uint32_t)a << 1 | (a < s_n));
+    __syncwarp();
+    if (a < 0) {  // bad drafts
+        cluster_sync();
+        if (rank == 0) {  // nothing accepted, no token
             for (int j = tid; j <= D; j += kDraftThreads) gst(out + j, -1);
             if (tid == 0) gst(accepted + i, 0);
         }
@@ -357,7 +364,12 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
 #pragma unroll
         for (int k = 0; k < kDraftWarps; ++k) here += s_warp[k];
         if (tid < C) st_cluster_u64(cluster_map(smem_addr(&s_total[pass][rank]), tid), here);
+        __syncwarp();
         cluster_sync();
+        // Inputs that change under the call: the CTAs may differ, and all leave here.
+        bool same = true;
+        for (int k = 0; k < C; ++k) same &= s_found[k] == s_found[0];
+        if (!same) return;
         total = before = 0;
         for (int k = 0; k < C; ++k) {
             if (k == rank) before = total;
