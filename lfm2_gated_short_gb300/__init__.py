@@ -629,9 +629,9 @@ def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, 
                  stream=None):
     """Verify drafts against the target: ``target [N, D+1, V]`` and ``draft [N, D, V]``
     (None: certain drafts) are probabilities (float32 or bfloat16; a last dim sliced
-    from wider rows is fine), ``tokens [N, D]`` int32, ``uniforms [N, D+1]`` float32,
-    ``n_drafts [N]`` int32 or None. Returns int32 ``(accepted [N], out_tokens [N, D+1])``:
-    the accepted drafts, the next token, then -1."""
+    from wider rows is fine, broadcast rows are refused), ``tokens [N, D]`` int32,
+    ``uniforms [N, D+1]`` float32, ``n_drafts [N]`` int32 or None. Returns int32
+    ``(accepted [N], out_tokens [N, D+1])``: the accepted drafts, the next token, then -1."""
     N, D1, V = target.shape
     D = D1 - 1
     dt = target.dtype
@@ -655,7 +655,7 @@ def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, 
 
 def _prob_rows(t, name, dtype, shape):
     """Data pointer and row distance of ``[N, n, V]`` probabilities whose rows are
-    contiguous and evenly spaced."""
+    contiguous and evenly spaced, at least V apart (broadcast rows are not)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
     if t.dtype is not dtype:
@@ -664,9 +664,11 @@ def _prob_rows(t, name, dtype, shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     N, n, V = shape
     s0, s1, s2 = t.stride()
-    if (V > 1 and s2 != 1) or (n > 1 and N > 1 and s0 != n * s1):
-        raise ValueError(f"{name} must have contiguous, evenly spaced rows")
-    return t.data_ptr(), max(V, s1 if n > 1 else s0)  # of a single row: any step
+    step = V if N * n <= 1 else s1 if n > 1 else s0  # of a single row: any
+    if (V > 1 and s2 != 1) or (n > 1 and N > 1 and s0 != n * s1) or step < V:
+        raise ValueError(f"{name} must have contiguous, evenly spaced rows that do not overlap "
+                         f"(broadcast ones: .contiguous()), got strides {t.stride()}")
+    return t.data_ptr(), step
 
 
 def check_wait_limit(stream=None, device=None) -> None:
