@@ -539,11 +539,12 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
     const float rescale = kRescaleLog2 / a.scale_log2;
     // What a thread does with the rows of row tile rt, the same for every item: the
-    // tokens of the two rows it computes, the chunks of output rows it writes (offset
-    // -1: past the item's rows).
+    // tokens of the two rows it computes, the output rows it writes chunks of (counted from the
+    // sequence's first row of the kv head, -1 past the item's rows; rows, since the D Hq Dh
+    // elements of one sequence may pass 2^31).
     constexpr int kOn = 16 * DH / 4 / (32 * KG);
     const int gt = kw * 32 + lane;  // thread of the row group
-    int rt_now = -1, row_j[2], o_off[kOn];
+    int rt_now = -1, row_j[2], o_row[kOn];
     auto set_rows = [&](int rt) {
         rt_now = rt;
         const int r0 = rt * C::MR;
@@ -554,8 +555,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         }
 #pragma unroll
         for (int k = 0; k < kOn; ++k) {
-            const int x = gt + k * 32 * KG, rr = r0 + rg * 16 + x / (DH / 4);
-            o_off[k] = rr < rows ? (rr / a.G * a.Hkv * a.G + rr % a.G) * DH + x % (DH / 4) * 4 : -1;
+            const int rr = r0 + rg * 16 + (gt + k * 32 * KG) / (DH / 4);
+            o_row[k] = rr < rows ? rr / a.G * a.Hkv * a.G + rr % a.G : -1;
         }
     };
     for (uint32_t items = 0;; ++items) {
@@ -760,11 +761,11 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                 v.z = fmaf(f, u.z, v.z);
                 v.w = fmaf(f, u.w, v.w);
             }
-            if (o_off[k] < 0) continue;
+            if (o_row[k] < 0) continue;
             if (whole) {
                 if (bad) continue;
                 const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-                gst(reinterpret_cast<uint2 *>(out + o_off[k]),
+                gst(reinterpret_cast<uint2 *>(out + (int64_t)o_row[k] * DH + c4 * 4),
                     make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
             } else {
                 const int row = rg * 16 + r;
