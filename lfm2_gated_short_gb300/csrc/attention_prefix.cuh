@@ -165,6 +165,7 @@ struct PfxBars {
     uint64_t kfull[8], kempty[8], vfull[8], vempty[8];
     uint64_t qfull, qempty;
     uint64_t sfull[3], pready[3], pvdone[3];  // of the S and P buffers
+    uint64_t odone[2];                        // a stream's last product of an item
     uint64_t done;                            // every MMA of the CTA
     uint32_t tmem;
     int leader;
@@ -198,6 +199,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             mbar_init(&b.pready[s], 4);
             mbar_init(&b.pvdone[s], 1);
         }
+        for (int s = 0; s < 2; ++s) mbar_init(&b.odone[s], 1);
         mbar_init(&b.done, 2);
         b.leader = a.N;
         b.bad = 0;
@@ -387,6 +389,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                             mma_bf16_ts(o, p + j * 8, vt + j * (2048 >> 4), idv,
                                         m >= streams || j > 0);
                         mma_commit(&b.pvdone[buf.i]);
+                        if (m >= total - streams) mma_commit(&b.odone[s]);
                         if (s == streams - 1 || x.split) {
                             mma_commit(&b.vempty[ring.i]);
                             ring.next(ST);
@@ -404,7 +407,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
         const int s = warp >> 2, r = tid & 127;  // stream, row = TMEM lane
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21;
         const uint32_t ot = tmem + lane_base + C::kOCol + s * DH;
-        uint32_t seq = 0;  // tiles of earlier items, both streams
+        uint32_t seq = 0;   // tiles of earlier items, both streams
+        uint32_t ends = 0;  // items of this stream that ended
         more_regs<216>();
         bool dead = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -492,8 +496,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&b.pready[buf]);
             }
-            const uint32_t last = seq0 + (uint32_t)(n - 1) * streams + s;
-            wait(&b.pvdone[last % C::kBufs], last / C::kBufs & 1u);
+            // A barrier of the stream's own, which its next item alone completes again. pvdone of the
+            // last tile is not enough: when the next item has one stream, that one's tiles take all
+            // buffers in turn, and pvdone could pass two phases before a late warp sees its parity.
+            wait(&b.odone[s], ends++ & 1u);
             float *part = x.part + ((w + blockIdx.x) * 2 + s) * C::kSlot;
 #pragma unroll
             for (int c = 0; c < DH / 32; ++c) {
