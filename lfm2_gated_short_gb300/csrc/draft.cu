@@ -258,7 +258,6 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
     if (tid < C)
         st_cluster_u64(cluster_map(smem_addr(&s_found[rank]), tid),
                        (u64)(uint32_t)a << 1 | (a < s_n));
-    __syncwarp();
     if (a < 0) {  // bad drafts
         cluster_sync();
         if (rank == 0) {  // nothing accepted, no token
@@ -364,7 +363,6 @@ __global__ void __launch_bounds__(kDraftThreads, 4)
 #pragma unroll
         for (int k = 0; k < kDraftWarps; ++k) here += s_warp[k];
         if (tid < C) st_cluster_u64(cluster_map(smem_addr(&s_total[pass][rank]), tid), here);
-        __syncwarp();
         cluster_sync();
         // Inputs that change under the call: the CTAs may differ, and all leave here.
         bool same = true;

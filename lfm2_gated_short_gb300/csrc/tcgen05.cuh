@@ -105,11 +105,15 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Every thread of every CTA of the cluster arrives, then waits for all.
+// Every thread of every CTA of the cluster arrives, then waits for all. The aligned forms of
+// these and of the named barriers below want the warp's lanes together, which a branch or
+// loop of single lanes before them does not leave by itself.
 __device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void cluster_sync() {
@@ -301,14 +305,16 @@ __device__ __forceinline__ void tmem_regs_ready(uint32_t (&r)[16]) {
                    "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
 }
 
-// Named barrier over `count` threads (ids 1..15; 0 is __syncthreads).
+// Named barrier over `count` threads (ids 1..15; 0 is __syncthreads), whole warps.
 __device__ __forceinline__ void named_sync(int id, int count) {
+    __syncwarp();
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(count) : "memory");
 }
 
 // OR of `pred` over the `count` threads of named barrier `id`.
 __device__ __forceinline__ bool named_or(int id, int count, bool pred) {
     uint32_t out;
+    __syncwarp();
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
