@@ -36,6 +36,7 @@
 #include "shortconv.h"
 #include "tcgen05.cuh"
 #include "tma.cuh"
+#include "work_split.h"
 
 namespace sc {
 
@@ -60,22 +61,6 @@ struct AttnArgs {
     int64_t *cum;      // [N + 1] first own tile of each sequence
     float *own_part;   // [items + CTAs] parts of MR rows: O [MR][Dh], m [MR], l [MR]
 };
-
-// ------------------------------------------------------------ work split
-//
-// The U units (key tiles) of a call lie on a line; CTA c of n takes
-// [c U / n, (c + 1) U / n). The part of item w that CTA c computes goes to
-// slot w + c: along the line each step raises w or c, so slots are distinct.
-
-__host__ __device__ __forceinline__ int64_t share_begin(int64_t c, int64_t U, int64_t n) {
-    const int64_t x = c * U;
-    return x <= UINT32_MAX ? (int64_t)((uint32_t)x / (uint32_t)n) : x / n;
-}
-__host__ __device__ __forceinline__ int share_of(int64_t u, int64_t U, int64_t n) {
-    const int64_t x = (u + 1) * n - 1;
-    if (x <= UINT32_MAX) return (int)((uint32_t)x / (uint32_t)U);  // u < U, n > 0: U is smaller
-    return (int)(x / U);
-}
 
 // Slots, lengths and tables are read in L2: k_own beside k_prefix starts without a wait of
 // its own, which would also drop what its SM's L1 holds of them from before they changed.
