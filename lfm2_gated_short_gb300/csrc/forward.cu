@@ -11,6 +11,7 @@
 // the K-1 values of u before its tile from the B and x rows just above it.
 #include <algorithm>
 #include <atomic>
+#include <condition_variable>
 #include <mutex>
 
 #include "common.cuh"
@@ -653,18 +654,56 @@ cudaError_t launch_rollback(int dtype, int H, int K, int L, int N, int D, const 
 
 // ------------------------------------------------------------ error word
 
-// Every unit's word is ORed into one device word, copied once. Host threads
-// take turns: the sum is shared.
-static __device__ unsigned int g_error_sum;
-static __global__ void k_clear_error_sum() { g_error_sum = 0u; }
+// A call ORs every unit's word into one device word of its own, copied once. Host threads that
+// ask at the same time take different words, so none waits for another's stream.
+constexpr int kErrorCalls = 64;  // at once; a further one waits for one of them
+static __device__ unsigned int g_error_sums[kErrorCalls];
+static __global__ void k_clear_error_sum(unsigned int *sum) { *sum = 0u; }
+
+namespace {
+
+class ErrorSum {
+public:
+    ErrorSum() {
+        std::unique_lock<std::mutex> lock(mu());
+        left().wait(lock, [] { return taken() != ~0ull; });
+        while (taken() >> index & 1) ++index;
+        taken() |= 1ull << index;
+    }
+    ~ErrorSum() {
+        {
+            std::lock_guard<std::mutex> lock(mu());
+            taken() &= ~(1ull << index);
+        }
+        left().notify_one();
+    }
+    ErrorSum(const ErrorSum &) = delete;
+    int index = 0;
+
+private:
+    static std::mutex &mu() {
+        static std::mutex m;
+        return m;
+    }
+    static std::condition_variable &left() {
+        static std::condition_variable c;
+        return c;
+    }
+    static unsigned long long &taken() {
+        static unsigned long long t = 0;
+        return t;
+    }
+};
+
+}  // namespace
 
 cudaError_t read_and_clear_error(cudaStream_t stream, unsigned int *code) {
-    static std::mutex mu;
-    std::lock_guard<std::mutex> lock(mu);
+    const ErrorSum mine;
     unsigned int *sum = nullptr;
-    cudaError_t e = cudaGetSymbolAddress((void **)&sum, g_error_sum);
+    cudaError_t e = cudaGetSymbolAddress((void **)&sum, g_error_sums);
     if (e != cudaSuccess) return e;
-    k_clear_error_sum<<<1, 1, 0, stream>>>();
+    sum += mine.index;
+    k_clear_error_sum<<<1, 1, 0, stream>>>(sum);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     for (auto take : {take_error_here, take_error_backward, take_error_slots, take_error_proj,
