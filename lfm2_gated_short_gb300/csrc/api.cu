@@ -17,8 +17,10 @@ namespace {
 
 bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
-// A pointer describing `bytes` bytes: NULL allowed only when empty.
+// A pointer describing `bytes` bytes: NULL allowed only when empty. No buffer has 2^63 bytes;
+// times() and strided() give SIZE_MAX for a size that does not fit.
 bool ptr_ok(const void *p, size_t bytes, uintptr_t align) {
+    if (bytes > (size_t)INT64_MAX) return false;
     if (bytes == 0) return p == nullptr || aligned(p, align);
     return p != nullptr && aligned(p, align);
 }
@@ -139,6 +141,21 @@ sc_status prefill_impl(sc_dtype dtype, int H, int K, const void *bcx, int64_t T,
                                         (cudaStream_t)stream));
 }
 
+// A product, and the bytes of `rows` rows of `width` bytes `stride` bytes apart.
+size_t times(size_t a, size_t b) {
+    size_t r;
+    return __builtin_mul_overflow(a, b, &r) ? SIZE_MAX : r;
+}
+size_t strided(size_t rows, size_t stride, size_t width) {
+    if (rows == 0) return 0;
+    size_t r;
+    return __builtin_add_overflow(times(rows - 1, stride), width, &r) ? SIZE_MAX : r;
+}
+
+// Query rows that prefix_attention takes: N, D and Hq are positive or zero.
+bool query_rows_ok(int Hq, int N, int D) {
+    return (int64_t)N * D <= INT32_MAX / 2 / Hq;
+}
 
 // The sizes of a page table; token_bytes and L only where pools are given.
 sc_status check_pages(int n_pages, int n_slots, int max_pages, int page_size) {
@@ -177,7 +194,7 @@ sc_status check_page_call(const void *refs, int n_pages, const void *table, cons
     if (L < 0 || (L > 0 && token_bytes <= 0)) return SC_EINVAL;
     if (L > 0 && (token_bytes % 16 != 0 || token_bytes > (1 << 24) || L > (1 << 16)))
         return SC_EUNSUPPORTED;
-    *pool_bytes = L > 0 ? (size_t)L * n_pages * page_size * token_bytes : 0;
+    *pool_bytes = L > 0 ? times((size_t)n_pages * page_size * token_bytes, (size_t)L) : 0;
     if (ws_bytes < need) return SC_EINVAL;
     if (!ptr_ok(refs, (size_t)n_pages * 4, 4) || !ptr_ok(table, (size_t)n_slots * max_pages * 4, 4) ||
         !ptr_ok(lens, (size_t)n_slots * 4, 4) || !ptr_ok(k, *pool_bytes, 16) ||
@@ -655,8 +672,8 @@ sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v,
         return SC_EUNSUPPORTED;
     if ((int64_t)N * D > INT32_MAX / 2) return SC_EINVAL;
     const size_t rows = (size_t)N * D;
-    const size_t n_k = rows ? (rows - 1) * k_stride + token_bytes : 0;
-    const size_t n_v = rows ? (rows - 1) * v_stride + token_bytes : 0;
+    const size_t n_k = strided(rows, k_stride, token_bytes);
+    const size_t n_v = strided(rows, v_stride, token_bytes);
     const size_t n_pool = (size_t)n_pages * page_size * token_bytes;
     const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
     if (!ptr_ok(k, n_k, 16) || !ptr_ok(v, n_v, 16) || !ptr_ok(k_pages, n_pool, 16) ||
@@ -679,7 +696,7 @@ sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v,
 size_t shortconv_prefix_attention_workspace_bytes(int Hq, int Hkv, int Dh, int N, int D,
                                                   int shared_pages) {
     if (Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || (Dh != 64 && Dh != 128) ||
-        N < 0 || D <= 0 || shared_pages < 0 || (int64_t)N * D * Hq > INT32_MAX / 2)
+        N < 0 || D <= 0 || shared_pages < 0 || !query_rows_ok(Hq, N, D))
         return 0;
     return sc::attention_workspace_bytes({Hq, Hkv, Dh, N, D, shared_pages});
 }
@@ -698,12 +715,12 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
         shared_pages > max_pages || q_stride < (int64_t)Hq * Dh || !(scale > 0.0f))
         return SC_EINVAL;
     if (dtype != SC_BF16 || (Dh != 64 && Dh != 128) || Hq / Hkv > 128 || q_stride % 8 != 0 ||
-        q_stride > (1ll << 36) || (int64_t)N * D * Hq > INT32_MAX / 2 ||
+        q_stride > (1ll << 36) || !query_rows_ok(Hq, N, D) ||
         (int64_t)N * D * Hq * ((int64_t)max_pages * page_size / 64 + 1) > (1ll << 40) ||
         Hq > (1 << 16) || !(scale < 1e30f))
         return SC_EUNSUPPORTED;
     const size_t rows = (size_t)N * D;
-    const size_t n_q = rows ? ((rows - 1) * q_stride + (size_t)Hq * Dh) * 2 : 0;
+    const size_t n_q = strided(rows, (size_t)q_stride * 2, (size_t)Hq * Dh * 2);
     const size_t n_out = rows * Hq * Dh * 2;
     const size_t n_pool = (size_t)n_pages * page_size * Hkv * Dh * 2;
     const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
@@ -743,10 +760,11 @@ sc_status shortconv_draft_accept(sc_dtype dtype, int V, int N, int D, const void
         return SC_EUNSUPPORTED;
     if ((int64_t)N * (D + 1ll) > INT32_MAX) return SC_EINVAL;
     const size_t es = elem_size(dtype), nd = (size_t)N * D, nr = (size_t)N * (D + 1);
-    const size_t n_p = nr ? ((nr - 1) * target_stride + V) * es : 0;
-    const size_t n_q = draft && nd ? ((nd - 1) * draft_stride + V) * es : 0;
+    const size_t n_p = strided(nr, target_stride * es, V * es);
+    const size_t n_q = draft ? strided(nd, draft_stride * es, V * es) : 0;
     const size_t n_c = n_drafts ? (size_t)N * 4 : 0;
-    if (!ptr_ok(target, n_p, es) || !opt_ok(draft, es) || !ptr_ok(tokens, nd * 4, 4) ||
+    if (!ptr_ok(target, n_p, es) || (draft && !ptr_ok(draft, n_q, es)) ||
+        !ptr_ok(tokens, nd * 4, 4) ||
         !opt_ok(n_drafts, 4) || !ptr_ok(uniforms, nr * 4, 4) ||
         !ptr_ok(accepted, (size_t)N * 4, 4) || !ptr_ok(out_tokens, nr * 4, 4))
         return SC_EINVAL;
