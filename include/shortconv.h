@@ -522,6 +522,7 @@ sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v,
  * part (lens - D + 1 < shared_pages * page_size) is computed by itself.
  *
  *   Hq, Hkv, Dh   Hq a multiple of Hkv, Hq / Hkv <= 128; Dh 64 or 128
+ *   max_pages     max_pages * page_size <= 2^31 - 256
  *   q             device [N*D, Hq, Dh] bf16, q_stride elements between rows
  *                 (a multiple of 8, at least Hq * Dh)            read
  *   k_pages, v_pages  device [n_pages, page_size, Hkv, Dh] bf16  read

@@ -717,6 +717,7 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
     if (dtype != SC_BF16 || (Dh != 64 && Dh != 128) || Hq / Hkv > 128 || q_stride % 8 != 0 ||
         q_stride > (1ll << 36) || !query_rows_ok(Hq, N, D) ||
         (int64_t)N * D * Hq * ((int64_t)max_pages * page_size / 64 + 1) > (1ll << 40) ||
+        (int64_t)max_pages * page_size > INT32_MAX - 255 ||  // key numbers pass a sequence's end
         Hq > (1 << 16) || !(scale < 1e30f))
         return SC_EUNSUPPORTED;
     const size_t rows = (size_t)N * D;

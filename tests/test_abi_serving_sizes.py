@@ -54,3 +54,13 @@ def test_pool_bytes(L):
 def test_acceptance_bytes(L, N, D, ts, ds):
     # more than 2^30 rows 2^32 elements of 4 bytes apart
     assert L.shortconv_draft_accept(F32, 1000, N, D, A, ts, B, ds, C, D_, E, F, G, None) == EINVAL
+
+
+@pytest.mark.parametrize("ps,max_pages,ok", [(8, 2 ** 28 - 1, False), (8, 2 ** 28 - 31, False),
+                                             (8, 2 ** 28 - 32, True), (32, 2 ** 26 - 1, False),
+                                             (64, 2 ** 25 - 1, False), (256, 2 ** 23 - 1, True)])
+def test_attention_tokens_of_a_sequence(L, ps, max_pages, ok):
+    """Key numbers run up to a tile or two past a sequence's end, in 32 bits: at most 2^31 - 256 tokens."""
+    need = L.shortconv_prefix_attention_workspace_bytes(4, 4, 64, 0, 1, 0)
+    assert L.shortconv_prefix_attention(BF16, 4, 4, 64, A, 256, 0, 1, B, C, 64, ps, D_, E, 1, max_pages, F,
+                                        0, 0.125, G, H, need, None) == (0 if ok else EUNSUPPORTED)
