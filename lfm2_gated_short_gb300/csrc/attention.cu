@@ -27,7 +27,6 @@
 #include <limits.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "common.cuh"
 #include "errors.cuh"
@@ -35,6 +34,7 @@
 #include "launch.h"
 #include "shortconv.h"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 #include "tma.cuh"
 #include "work_split.h"
 
@@ -53,7 +53,7 @@ struct AttnArgs {
     int64_t q_stride;
     PageTable pt;
     const int32_t *slots;
-    int N, D, G, Hkv, Dh;
+    int N, D, G, Hkv;
     int shared_keys;   // keys whose part k_prefix computes (see prefix_keys)
     int beside;        // k_own runs beside k_prefix, on the SMs that it leaves
     float scale_log2;  // scale * log2(e)
@@ -911,25 +911,6 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
 
 // ------------------------------------------------------------ host side
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_tiled() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &r) == cudaSuccess &&
-            r == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
-
 // Pages [n_pages * page_size tokens, Hkv, Dh] in boxes of `keys` tokens of one
 // head, 64 columns, 128-byte swizzle.
 static cudaError_t map_pages(CUtensorMap *m, const void *ptr, const PageTable &pt, int Hkv, int Dh,
@@ -1061,7 +1042,6 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.D = s.D;
     a.G = s.Hq / s.Hkv;
     a.Hkv = s.Hkv;
-    a.Dh = s.Dh;
     a.shared_keys = x.P;
     a.scale_log2 = scale * kLog2e;
     a.out = (bf16 *)out;

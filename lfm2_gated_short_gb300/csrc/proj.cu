@@ -36,7 +36,6 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
-#include <mutex>
 
 #include "common.cuh"
 #include "errors.cuh"
@@ -44,6 +43,7 @@
 #include "launch.h"
 #include "shortconv.h"
 #include "tcgen05.cuh"
+#include "tensor_map.h"
 #include "tma.cuh"
 
 namespace sc {
@@ -1179,25 +1179,6 @@ __global__ void __launch_bounds__(kOutThreads, 1)
 }
 
 // ------------------------------------------------------------ host side
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                                  const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                                  const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-static EncodeTiledFn encode_tiled() {
-    static std::once_flag once;
-    static EncodeTiledFn fn = nullptr;
-    std::call_once(once, [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(p);
-    });
-    return fn;
-}
 
 // A row-major bf16 matrix [outer, inner] copied in {64, box_rows} boxes with
 // the 128-byte swizzle; a load reads rows past the end (or before row 0) as
