@@ -519,7 +519,9 @@ sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v,
  * of all listed sequences are equal (branches forked from one prompt); that
  * part of every row's keys is then read once for the whole batch. 0 is
  * always right. A sequence whose first new token does not see all of the shared
- * part (lens - D + 1 < shared_pages * page_size) is computed by itself.
+ * part (lens - D + 1 < shared_pages * page_size) is computed by itself. Any D is
+ * right, a prompt's length too, but a sequence's own keys are read once for every
+ * 32 rows (D * Hq / Hkv) of a kv head.
  *
  *   Hq, Hkv, Dh   Hq a multiple of Hkv, Hq / Hkv <= 128; Dh 64 or 128
  *   max_pages     max_pages * page_size <= 2^31 - 256

@@ -15,9 +15,10 @@
 // ring of tiles in flight, one TMA box a page, and copies each item's queries.
 // The four consumer warps take a share of a tile's keys and, with 32 rows, of
 // the rows each, and keep their own (m, l, O), joined once an item. Two
-// sequences of 30-40 thousand tokens (143 MB): 27 us, DRAM's rate; 128 x 8 drafts with
-// 100-1200 own tokens (32 rows an item): 55 us, 58 % of DRAM's peak, the rest is
-// the softmax of twice the rows and the start and join of the items.
+// sequences of 30-40 thousand tokens (143 MB): 26 us, 5.4 TB/s, 80 % of the measured copy
+// rate. 128 x 8 drafts with 100-1200 own tokens (32 rows an item, 170 MB): 54 us,
+// 3.1 TB/s; DRAM gives 245 MB for them and is busy 59 % of the time, issue slots 23 %.
+// With D G > 32 the rows go in tiles of 32, and each walks all of the sequence's key tiles.
 //
 // k_merge joins the parts that CTAs left in the workspace, in a fixed order: 4
 // to 6 us of dependent reads with few rows, 17 us for the 32768 rows of 128 x 8 x 32.
@@ -975,9 +976,11 @@ static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count) {
     x.n_cta = (int)(x.U < ctas ? x.U : ctas);
     // A small prefix costs fixed latencies more than work: it takes a CTA for every eight
     // units (four of 128-wide heads), up to half the SMs, and the own parts run on the
-    // others meanwhile. 64 sequences behind 4096 tokens: 50 us one after the other, 37 so
-    // (42 with a CTA for every four units); 37 x 3 drafts with 128-wide heads behind
-    // 2976: 38 and 26.
+    // others meanwhile. 64 sequences of 64-1500 own tokens, us beside and one after the
+    // other: 24.9 and 33.6 with 64 units, 31.7 and 40.2 with 384, 37.1 and 41.6 with 600 (the
+    // rule ends at 608); of 1-30 own tokens 22.8 and 23.7 with 600, 25.5 and 25.4 with 768.
+    // Heads of 128: 46.9 and 58.5 with 64, 58.9 and 66.0 with 256 (the rule ends at 304). Slower
+    // beside: 16 sequences behind 1024 tokens (32 units), 25.9 and 20.3, behind 2048, 23.6 and 21.0.
     const int units = s.Dh == 64 ? 8 : 4;
     x.a.beside = x.U > 0 && x.U <= (int64_t)units * (ctas / 2);
     if (x.a.beside) x.n_cta = (int)((x.U + units - 1) / units);
@@ -1081,7 +1084,10 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     if (e != cudaSuccess) return e;
     // With few rows all lanes of a warp share one: a whole step over two streams of 30-40
     // thousand tokens takes 39 us so, 45 with Dh / 8 lanes a row. With many there is work
-    // enough: 128 x 8 drafts take 193 us with Dh / 8 lanes, 213 with whole warps.
+    // enough: 128 x 8 drafts take 193 us with Dh / 8 lanes, 213 with whole warps. Between, one
+    // token of sequences of 64-1500 tokens, us with whole warps and without: 1024 rows 14.9 and
+    // 15.5, 2048 rows 23.3 both, 4096 rows 52.0 and 49.6, 16384 rows 210 and 201 (heads of 128:
+    // 1024 rows 24.7 and 24.8, 4096 rows 77.9 and 75.2).
     const bool few = (int64_t)s.N * s.D * s.Hq <= 4096;
     const auto merge = s.Dh == 64 ? (few ? k_merge<64, 4> : k_merge<64, 1>)
                                   : (few ? k_merge<128, 2> : k_merge<128, 1>);

@@ -645,9 +645,14 @@ size_t pages_workspace_bytes(int n_pages, int n) {
 }
 
 // The plan of a resize or fork. One CTA is enough for a few thousand table entries; with
-// more, 8 share them. A fork and a resize of 64 sequences of 1025 pages: 49 us with one CTA,
-// 26 with eight; of 2 sequences of 9 pages: 14.0 and 16.6. Copies of up to 128 KB a CTA (were
-// every listed sequence to need one) cost less than a second launch (the latter pair: 14.0 and 15.0).
+// more, 8 share them. Forks of 2 to 64 branches, us with one CTA and with eight: 2100 entries
+// 11.5-12.0 and 11.6-12.9, 4100 entries 12.1-12.7 and 11.3-12.9, 8200 entries 13.4-14.0 and
+// 12.4-12.8, 16400 entries 16.9-17.1 and 13.0-13.4; a fork and a resize of 64 sequences of 1025
+// pages 49 and 26. Copies of up to 128 KB a CTA, were every listed sequence to need one, are
+// made in the same launch. Where few or none are needed, as in a resize, that spares one (a
+// fork and a resize of 2 sequences: 14.0 us, 15.0 with the copy kernel). Where all are: one CTA
+// 9.9 us with 64 KB, 11.0 with 128 and 14.5 with 384 (10.2, 10.4 and 10.5 with the copy kernel),
+// eight CTAs 13.2 with 64 KB each, 13.4 with 128 and 15.1 with 192 (11.9, 12.2 and 11.9).
 struct MetaPlan {
     unsigned ctas;
     int inline_copy;
