@@ -547,6 +547,116 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
                                      size_t workspace_bytes, void *stream);
 
 /*
+ * The cache in 8 bits. The pools hold e4m3 codes, [n_pages, page_size, Hkv, Dh] (Dh a
+ * multiple of 16), and beside each pool lie scales, fp32 [n_pages, page_size / block, Hkv],
+ * 16-byte aligned: a power of two for every block of `block` tokens of a page (a power of
+ * two, 8 to page_size) and kv head; a value is code times scale. Tables, lengths and refs
+ * are the cache's above. Only a scale's exponent is read, held to 2^-64 .. 2^120, so pools and
+ * scales may start out uninitialised. L layers stack pools and scales alike.
+ *
+ * shortconv_pages_append_8bit: shortconv_pages_append into such a pool. A block's scale
+ * becomes the least power of two s with |x| <= 448 s for the new tokens that the block
+ * gets (infinities and NaN do not count) and, where it holds earlier tokens of the sequence,
+ * at least what it was; codes are x / s rounded to nearest, ties to even, infinities become
+ * +-448 and NaN stays NaN. Earlier tokens' codes follow a scale that rises (exactly, but for
+ * values below 2^-14 of the block's new largest possible one). A rollback keeps the scales.
+ *   dtype       of k and v, SC_F32 or SC_BF16
+ *   k, v        device [N*D, Hkv, Dh], rows k_stride, v_stride elements apart (rows start on
+ *               16 bytes)                                                    read
+ *   k_pages, v_pages, k_scales, v_scales                                     written in place
+ *
+ * shortconv_pages_read_8bit: the cache's values as numbers: rows cu_seqlens[i] ..
+ * cu_seqlens[i+1]-1 of k and v are the tokens of slot slot_ids[i] from starts[i] on (starts
+ * NULL: from 0). A slot may be listed more than once. Exact in both dtypes, but for bf16's
+ * range.
+ *   cu_seqlens  device int32 [N+1], 0 = c0 <= c1 <= ... <= cN = T           read
+ *   k, v        device [T, Hkv, Dh] of dtype                                written
+ * Device errors: SC_DEV_BAD_SEQLENS (nothing is written), SC_DEV_BAD_SLOT,
+ * SC_DEV_BAD_LENGTH (more tokens than the sequence has), SC_DEV_BAD_PAGE.
+ *
+ * shortconv_pages_resize_8bit, _fork_8bit, _compact_8bit: the calls above for such pools;
+ * a copied page takes its scales along.
+ *
+ * shortconv_prefix_attention_8bit: shortconv_prefix_attention over such a pool: q and out
+ * bf16, keys and values code times scale. A call with shared_pages unpacks that part once, to
+ * bf16 in the workspace.
+ */
+sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block, const void *k,
+                                      int64_t k_stride, const void *v, int64_t v_stride, int N,
+                                      int D, void *k_pages, void *v_pages, float *k_scales,
+                                      float *v_scales, int n_pages, int page_size,
+                                      const int32_t *table, const int32_t *lens, int n_slots,
+                                      int max_pages, const int32_t *slot_ids, void *stream);
+sc_status shortconv_pages_read_8bit(sc_dtype dtype, int Hkv, int Dh, int block,
+                                    const void *k_pages, const void *v_pages,
+                                    const float *k_scales, const float *v_scales, int n_pages,
+                                    int page_size, const int32_t *table, const int32_t *lens,
+                                    int n_slots, int max_pages, const int32_t *slot_ids,
+                                    const int32_t *cu_seqlens, const int32_t *starts, int N,
+                                    int64_t T, void *k, void *v, void *stream);
+sc_status shortconv_pages_resize_8bit(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                                      int n_slots, int max_pages, int page_size,
+                                      const int32_t *slot_ids, const int32_t *new_lens, int n,
+                                      int L, int Hkv, int Dh, int block, void *k_pages,
+                                      void *v_pages, float *k_scales, float *v_scales,
+                                      void *workspace, size_t workspace_bytes, void *stream);
+sc_status shortconv_pages_fork_8bit(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                                    int n_slots, int max_pages, int page_size,
+                                    const int32_t *src_slots, const int32_t *dst_slots, int n,
+                                    int L, int Hkv, int Dh, int block, void *k_pages,
+                                    void *v_pages, float *k_scales, float *v_scales,
+                                    void *workspace, size_t workspace_bytes, void *stream);
+sc_status shortconv_pages_compact_8bit(int32_t *refs, int n_pages, int32_t *table,
+                                       const int32_t *lens, int n_slots, int max_pages,
+                                       int page_size, int L, int Hkv, int Dh, int block,
+                                       void *k_pages, void *v_pages, float *k_scales,
+                                       float *v_scales, int32_t *n_used, void *workspace,
+                                       size_t workspace_bytes, void *stream);
+size_t shortconv_prefix_attention_8bit_workspace_bytes(int Hq, int Hkv, int Dh, int N, int D,
+                                                       int shared_pages, int page_size);
+sc_status shortconv_prefix_attention_8bit(int Hq, int Hkv, int Dh, int block, const void *q,
+                                          int64_t q_stride, int N, int D, const void *k_pages,
+                                          const void *v_pages, const float *k_scales,
+                                          const float *v_scales, int n_pages, int page_size,
+                                          const int32_t *table, const int32_t *lens, int n_slots,
+                                          int max_pages, const int32_t *slot_ids,
+                                          int shared_pages, float scale, void *out,
+                                          void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * shortconv_rope: rotary positions of queries and keys, and their gradient. Pair i of a
+ * head's first R values, (x_i, x_{i+R/2}) (SC_ROPE_HALF) or (x_{2i}, x_{2i+1})
+ * (SC_ROPE_INTERLEAVED), is turned by t = position * freqs[i] radians and scaled:
+ *   a' = amplitude (a cos t - b sin t),  b' = amplitude (b cos t + a sin t);
+ * the other Dh - R values are copied. With inverse set, the turn is by -t: what takes the
+ * gradients of the outputs to those of the inputs (the same arguments, q and k the
+ * incoming gradients). Angles are exact for every position (an integer number of 2^-64
+ * turns), sums in fp32, each value rounded once.
+ *
+ *   dtype       of q, k and the outputs, SC_F32 or SC_BF16
+ *   R           even, at most 512
+ *   q, k        device [T, Hq, Dh], [T, Hkv, Dh], rows q_stride, k_stride elements apart
+ *               (their elements' alignment is enough; 16 bytes are faster); one of Hq and Hkv
+ *               may be 0, its pointers NULL                                   read
+ *   freqs       device double [R/2], radians a position (finite)              read
+ *   positions   device int32 [T], any sign; or NULL: row i*D + j is at position
+ *               lens[slot_ids[i]] - D + j of the cache, as in shortconv_pages_append (T a
+ *               multiple of D; lens device int32 [n_slots], slot_ids int32 [T / D])  read
+ *   q_out, k_out  as q and k, strides of their own; an output may be its own
+ *               input (same pointer and stride), and rows may lie between another array's
+ *               of the same stride                                            written
+ * Device errors: SC_DEV_BAD_SLOT, SC_DEV_BAD_LENGTH (a position below 0): those rows are
+ * not written.
+ */
+typedef enum { SC_ROPE_HALF = 0, SC_ROPE_INTERLEAVED = 1 } sc_rope_layout;
+sc_status shortconv_rope(sc_dtype dtype, sc_rope_layout layout, int inverse, int Hq, int Hkv,
+                         int Dh, int R, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, int64_t T, const double *freqs, float amplitude,
+                         const int32_t *positions, const int32_t *lens, int n_slots,
+                         const int32_t *slot_ids, int D, void *q_out, int64_t q_out_stride,
+                         void *k_out, int64_t k_out_stride, void *stream);
+
+/*
  * shortconv_draft_accept: verification of drafted tokens against the target's
  * probabilities, from given random numbers (SGLang PR #31041: the accepted
  * length that the rollback of section "实现拆解 2" takes). Sequence i

@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 import threading
 
@@ -30,6 +31,7 @@ DEV_OUT_OF_BOUNDS = 0x20
 
 SC_OK, SC_EINVAL, SC_EUNSUPPORTED, SC_ECUDA, SC_EDEVICE = 0, 1, 2, 3, 4
 SC_F32, SC_BF16 = 0, 1
+SC_ROPE_HALF, SC_ROPE_INTERLEAVED = 0, 1
 DEV_BAD_SLOT, DEV_BAD_SEQLENS, DEV_BAD_ACCEPTED, DEV_TIMEOUT, DEV_NO_SLOT = 0x1, 0x2, 0x4, 0x8, 0x10
 
 DEV_NO_PAGE, DEV_BAD_PAGE, DEV_BAD_LENGTH, DEV_BAD_TOKEN, DEV_BAD_PROBS = (
@@ -100,6 +102,22 @@ def lib() -> ctypes.CDLL:
             L.shortconv_prefix_attention.argtypes = [i32, i32, i32, i32, p, i64, i32, i32, p, p,
                                                      i32, i32, p, p, i32, i32, p, i32,
                                                      ctypes.c_float, p, p, sz, p]
+            L.shortconv_pages_resize_8bit.argtypes = [p, i32, p, p, i32, i32, i32, p, p, i32, i32,
+                                                      i32, i32, i32, p, p, p, p, p, sz, p]
+            L.shortconv_pages_fork_8bit.argtypes = L.shortconv_pages_resize_8bit.argtypes
+            L.shortconv_pages_compact_8bit.argtypes = [p, i32, p, p, i32, i32, i32, i32, i32, i32,
+                                                       i32, p, p, p, p, p, p, sz, p]
+            L.shortconv_pages_append_8bit.argtypes = [i32, i32, i32, i32, p, i64, p, i64, i32, i32,
+                                                      p, p, p, p, i32, i32, p, p, i32, i32, p, p]
+            L.shortconv_pages_read_8bit.argtypes = [i32, i32, i32, i32, p, p, p, p, i32, i32, p, p,
+                                                    i32, i32, p, p, p, i32, i64, p, p, p]
+            L.shortconv_prefix_attention_8bit_workspace_bytes.argtypes = [i32] * 7
+            L.shortconv_prefix_attention_8bit_workspace_bytes.restype = sz
+            L.shortconv_prefix_attention_8bit.argtypes = [i32, i32, i32, i32, p, i64, i32, i32, p,
+                                                          p, p, p, i32, i32, p, p, i32, i32, p,
+                                                          i32, ctypes.c_float, p, p, sz, p]
+            L.shortconv_rope.argtypes = [i32, i32, i32, i32, i32, i32, i32, p, i64, p, i64, i64, p,
+                                         ctypes.c_float, p, p, i32, p, i32, p, i64, p, i64, p]
             L.shortconv_draft_accept.argtypes = [i32, i32, i32, i32, p, i64, p, i64, p, p, p, p, p,
                                                  p]
             L.shortconv_get_error.argtypes = [p, ctypes.POINTER(ctypes.c_int)]
@@ -116,6 +134,8 @@ def lib() -> ctypes.CDLL:
                       "slots_claim",
                       "slots_release", "pool_copy", "pages_resize", "pages_fork",
                       "pages_compact", "pages_append", "prefix_attention", "draft_accept",
+                      "pages_resize_8bit", "pages_fork_8bit", "pages_compact_8bit",
+                      "pages_append_8bit", "pages_read_8bit", "prefix_attention_8bit", "rope",
                       "get_error", "check_wait_limit",
                       "bounds_trim_next", "bounds_take_first_bad"):
                 getattr(L, "shortconv_" + f).restype = i32
@@ -479,6 +499,46 @@ def _pools(k_pages, v_pages, n_pages):
             _dev(k_pages, "k_pages"), _dev(v_pages, "v_pages", k_pages.dtype, full))
 
 
+_E4M3 = torch.float8_e4m3fn
+
+
+def _scales(k_pages, v_pages, k_scales, v_scales):
+    """``(Hkv, Dh, block, k, v, k scales, v scales)`` of e4m3 pools ``[.., n_pages, page_size, Hkv, Dh]``
+    beside float32 scales ``[.., n_pages, page_size / block, Hkv]``."""
+    pool = k_pages.shape
+    if k_scales is None or v_scales is None:
+        raise ValueError("an 8-bit cache has k_scales and v_scales")
+    if len(pool) not in (4, 5) or len(k_scales.shape) != len(pool) - 1:
+        raise ValueError("k_scales must be [.., n_pages, page_size / block, Hkv]")
+    ps, Hkv, Dh = pool[-3:]
+    blocks = k_scales.shape[-2]
+    if blocks < 1 or ps % blocks:
+        raise ValueError(f"{blocks} blocks of scales do not divide a page of {ps} tokens")
+    shape = pool[:-3] + (blocks, Hkv)
+    return (Hkv, Dh, ps // blocks, _dev(k_pages, "k_pages", _E4M3),
+            _dev(v_pages, "v_pages", _E4M3, pool),
+            _dev(k_scales, "k_scales", torch.float32, shape),
+            _dev(v_scales, "v_scales", torch.float32, shape))
+
+
+def _pools8(k_pages, v_pages, k_scales, v_scales, n_pages):
+    """``(page_size, L, Hkv, Dh, block, k, v, k scales, v scales)``, as ``_pools``."""
+    full = k_pages.shape
+    if len(full) not in (4, 5) or full[-4] != n_pages:
+        raise ValueError("k_pages must be [L, n_pages, page_size, Hkv, Dh] or "
+                         "[n_pages, page_size, Hkv, Dh]")
+    return ((full[-3], full[0] if len(full) == 5 else 1)
+            + _scales(k_pages, v_pages, k_scales, v_scales))
+
+
+def _is_8bit(k_pages, k_scales, v_scales):
+    if k_pages.dtype is _E4M3:
+        return True
+    if k_scales is not None or v_scales is not None:
+        raise TypeError(f"scales go with torch.float8_e4m3fn pools, got {k_pages.dtype}")
+    return False
+
+
 # Scratch straight from torch's caching allocator: no tensor object (3 us of host time a
 # call), and the block belongs to the stream that the call runs on, so that it is safe
 # to give back as soon as the call is enqueued.
@@ -529,53 +589,79 @@ def pages_workspace_bytes(n_pages: int, n: int) -> int:
 
 
 def pages_resize(refs, table, lens, slot_ids, new_lens, k_pages, v_pages, workspace=None,
-                 stream=None):
+                 stream=None, k_scales=None, v_scales=None):
     """Give each listed sequence a new length: claims, truncates (a rollback) or frees
     (0) its pages; in place on ``refs``, ``table``, ``lens`` and, where a shared page
     has to be copied, on the pools."""
     n = slot_ids.shape[0]
-    ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
+    name = "shortconv_pages_resize"
+    if _is_8bit(k_pages, k_scales, v_scales):
+        name += "_8bit"
+        ps, *pools = _pools8(k_pages, v_pages, k_scales, v_scales, refs.shape[0])
+    else:
+        ps, *pools = _pools(k_pages, v_pages, refs.shape[0])
     _call_with_workspace(
-        "shortconv_pages_resize", lib().shortconv_pages_resize, workspace,
-        pages_workspace_bytes(refs.shape[0], n), refs.device, stream,
-        *_cache(refs, table, lens), ps, _ints(slot_ids, "slot_ids", (n,)),
-        _ints(new_lens, "new_lens", (n,)), n, L, token_bytes, kp, vp)
+        name, getattr(lib(), name), workspace, pages_workspace_bytes(refs.shape[0], n), refs.device,
+        stream, *_cache(refs, table, lens), ps, _ints(slot_ids, "slot_ids", (n,)),
+        _ints(new_lens, "new_lens", (n,)), n, *pools)
 
 
 def pages_fork(refs, table, lens, src_slots, dst_slots, k_pages, v_pages, workspace=None,
-               stream=None):
+               stream=None, k_scales=None, v_scales=None):
     """``dst_slots[i]`` becomes a branch of ``src_slots[i]``: full pages shared, a partly
     filled last page copied. In place."""
     n = src_slots.shape[0]
-    ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
+    name = "shortconv_pages_fork"
+    if _is_8bit(k_pages, k_scales, v_scales):
+        name += "_8bit"
+        ps, *pools = _pools8(k_pages, v_pages, k_scales, v_scales, refs.shape[0])
+    else:
+        ps, *pools = _pools(k_pages, v_pages, refs.shape[0])
     _call_with_workspace(
-        "shortconv_pages_fork", lib().shortconv_pages_fork, workspace,
-        pages_workspace_bytes(refs.shape[0], n), refs.device, stream,
-        *_cache(refs, table, lens), ps, _ints(src_slots, "src_slots", (n,)),
-        _ints(dst_slots, "dst_slots", (n,)), n, L, token_bytes, kp, vp)
+        name, getattr(lib(), name), workspace, pages_workspace_bytes(refs.shape[0], n), refs.device,
+        stream, *_cache(refs, table, lens), ps, _ints(src_slots, "src_slots", (n,)),
+        _ints(dst_slots, "dst_slots", (n,)), n, *pools)
 
 
-def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=None, stream=None):
+def pages_compact(refs, table, lens, k_pages, v_pages, n_used=None, workspace=None, stream=None,
+                  k_scales=None, v_scales=None):
     """Move the used pages to the front of the pools (in place); returns the int32
     ``n_used [1]``: no page at or past it is in use."""
-    ps, L, token_bytes, kp, vp = _pools(k_pages, v_pages, refs.shape[0])
+    name = "shortconv_pages_compact"
+    if _is_8bit(k_pages, k_scales, v_scales):
+        name += "_8bit"
+        pools = _pools8(k_pages, v_pages, k_scales, v_scales, refs.shape[0])
+    else:
+        pools = _pools(k_pages, v_pages, refs.shape[0])
     if n_used is None:
         n_used = _output((1,), _I32, refs.device, stream)
     _call_with_workspace(
-        "shortconv_pages_compact", lib().shortconv_pages_compact, workspace,
-        pages_workspace_bytes(refs.shape[0], 0), refs.device, stream,
-        *_cache(refs, table, lens), ps, L, token_bytes, kp, vp,
-        _ints(n_used, "n_used", (1,)))
+        name, getattr(lib(), name), workspace, pages_workspace_bytes(refs.shape[0], 0), refs.device,
+        stream, *_cache(refs, table, lens), *pools, _ints(n_used, "n_used", (1,)))
     return n_used
 
 
-def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None):
+def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None, k_scales=None,
+                 v_scales=None):
     """Write each listed sequence's ``D`` newest tokens, already counted in ``lens``:
-    ``k``, ``v`` ``[N*D, Hkv, Dh]`` (rows may be strided) into one layer's pools."""
+    ``k``, ``v`` ``[N*D, Hkv, Dh]`` (rows may be strided) into one layer's pools. Into 8-bit
+    pools they are quantised, block by block of the scales (``page_cache_8bit``)."""
     N = slot_ids.shape[0]
     pool = k_pages.shape
     n_pages, ps, Hkv, Dh = pool
     n_slots, max_pages = table.shape
+    if _is_8bit(k_pages, k_scales, v_scales):
+        dt, rows = k.dtype, (N * D, Hkv, Dh)
+        _, _, block, *pools = _scales(k_pages, v_pages, k_scales, v_scales)
+        k_p, k_s = _rows(k, "k", dt, rows)
+        v_p, v_s = _rows(v, "v", dt, rows)
+        status = lib().shortconv_pages_append_8bit(
+            _dcode(k), Hkv, Dh, block, k_p, k_s, v_p, v_s, N, D, *pools, n_pages, ps,
+            _ints(table, "table", (n_slots, max_pages)), _ints(lens, "lens", (n_slots,)), n_slots,
+            max_pages, _ints(slot_ids, "slot_ids", (N,)), _stream(stream, k_pages.device))
+        if status:
+            _raise_on("shortconv_pages_append_8bit", status)
+        return
     dt = k_pages.dtype
     es = 2 if dt is _BF16 else 4 if _dcode(k_pages) == SC_F32 else 0
     k_p, k_s = _rows(k, "k", dt, (N * D, Hkv, Dh))
@@ -589,17 +675,64 @@ def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None):
         _raise_on("shortconv_pages_append", status)
 
 
+def page_cache_8bit(n_pages: int, page_size: int, Hkv: int, Dh: int, block: int = 16, layers=None,
+                    device="cuda"):
+    """``(k_pages, v_pages, k_scales, v_scales)`` of an 8-bit cache: zeroed e4m3 pools ``[n_pages,
+    page_size, Hkv, Dh]`` and float32 scales ``[n_pages, page_size / block, Hkv]``, a power
+    of two for every ``block`` tokens of a page and kv head; with ``layers``, so many of each."""
+    if block < 1 or page_size % block:
+        raise ValueError(f"blocks of {block} tokens do not divide a page of {page_size}")
+    front = (n_pages,) if layers is None else (layers, n_pages)
+    codes = [torch.zeros(front + (page_size, Hkv, Dh), dtype=torch.uint8, device=device).view(_E4M3)
+             for _ in range(2)]
+    return (*codes, *(torch.ones(front + (page_size // block, Hkv), device=device)
+                      for _ in range(2)))
+
+
+def pages_read(k_pages, v_pages, k_scales, v_scales, table, lens, slot_ids, cu_seqlens, T,
+               starts=None, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """One layer's 8-bit keys and values as numbers: rows ``cu_seqlens[i] .. cu_seqlens[i+1]-1``
+    are the tokens of slot ``slot_ids[i]`` from ``starts[i]`` (None: 0) on. Returns ``k, v
+    [T, Hkv, Dh]``, bfloat16 or float32."""
+    N = slot_ids.shape[0]
+    n_pages, ps, Hkv, Dh = k_pages.shape
+    n_slots, max_pages = table.shape
+    if not _is_8bit(k_pages, k_scales, v_scales):
+        raise TypeError(f"k_pages must be torch.float8_e4m3fn, got {k_pages.dtype}")
+    _, _, block, *pools = _scales(k_pages, v_pages, k_scales, v_scales)
+    rows, device = (T, Hkv, Dh), k_pages.device
+    if k is None:
+        k = _output(rows, dtype, device, stream)
+    if v is None:
+        v = _output(rows, dtype, device, stream)
+    status = lib().shortconv_pages_read_8bit(
+        _dcode(k), Hkv, Dh, block, *pools, n_pages, ps, _ints(table, "table", (n_slots, max_pages)),
+        _ints(lens, "lens", (n_slots,)), n_slots, max_pages, _ints(slot_ids, "slot_ids", (N,)),
+        _ints(cu_seqlens, "cu_seqlens", (N + 1,)),
+        None if starts is None else _ints(starts, "starts", (N,)), N, T, _dev(k, "k", dtype, rows),
+        _dev(v, "v", dtype, rows), _stream(stream, device))
+    if status:
+        _raise_on("shortconv_pages_read_8bit", status)
+    return k, v
+
+
 @functools.lru_cache(maxsize=1024)
 def prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages=0) -> int:
     return int(lib().shortconv_prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages))
 
 
+@functools.lru_cache(maxsize=1024)
+def prefix_attention_8bit_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages, page_size) -> int:
+    return int(lib().shortconv_prefix_attention_8bit_workspace_bytes(Hq, Hkv, Dh, N, D,
+                                                                     shared_pages, page_size))
+
+
 def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages=0, scale=None,
-                     out=None, workspace=None, stream=None):
-    """Attention of a decode (``D`` = 1) or verify step over the paged cache (bf16):
-    row ``i*D + j`` of ``q [N*D, Hq, Dh]`` (rows may be strided) is new token j of the
-    sequence in ``slot_ids[i]``. The first ``shared_pages`` pages are the same for all
-    listed sequences and read once. Returns ``out [N*D, Hq, Dh]``."""
+                     out=None, workspace=None, stream=None, k_scales=None, v_scales=None):
+    """Attention of a decode (``D`` = 1) or verify step over the paged cache (bf16, or 8 bits
+    beside their scales): row ``i*D + j`` of ``q [N*D, Hq, Dh]`` (bf16, rows may be strided) is
+    new token j of the sequence in ``slot_ids[i]``. The first ``shared_pages`` pages are the same
+    for all listed sequences and read once. Returns ``out [N*D, Hq, Dh]``."""
     N = slot_ids.shape[0]
     pool = k_pages.shape
     n_pages, ps, Hkv, Dh = pool
@@ -615,6 +748,15 @@ def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages
     else:
         out_p = _dev(out, "out", _BF16, rows)
     q_p, q_s = _rows(q, "q", _BF16, rows)
+    if _is_8bit(k_pages, k_scales, v_scales):
+        _, _, block, *pools = _scales(k_pages, v_pages, k_scales, v_scales)
+        _call_with_workspace(
+            "shortconv_prefix_attention_8bit", lib().shortconv_prefix_attention_8bit, workspace,
+            prefix_attention_8bit_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages, ps), device,
+            stream, Hq, Hkv, Dh, block, q_p, q_s, N, D, *pools, n_pages, ps,
+            _ints(table, "table", (n_slots, max_pages)), _ints(lens, "lens", (n_slots,)), n_slots,
+            max_pages, _ints(slot_ids, "slot_ids", (N,)), shared_pages, scale, out_p)
+        return out
     _call_with_workspace(
         "shortconv_prefix_attention", lib().shortconv_prefix_attention, workspace,
         prefix_attention_workspace_bytes(Hq, Hkv, Dh, N, D, shared_pages), device, stream,
@@ -623,6 +765,98 @@ def prefix_attention(q, k_pages, v_pages, table, lens, slot_ids, D, shared_pages
         _ints(table, "table", (n_slots, max_pages)), _ints(lens, "lens", (n_slots,)), n_slots,
         max_pages, _ints(slot_ids, "slot_ids", (N,)), shared_pages, scale, out_p)
     return out
+
+
+def rope_frequencies(R, base=10000.0, scaling=None, factor=1.0, original_length=8192, low=1.0,
+                     high=32.0, device="cuda"):
+    """``(freqs, amplitude)`` for ``rope``: ``freqs`` float64 ``[R/2]``, radians a position of pair i,
+    ``base ** (-2i / R)``, and for contexts ``factor`` times as long as trained:
+
+    ``scaling`` None: as it is; ``"linear"``: all of them divided by ``factor``; ``"base"``: the
+    base raised so that the slowest pair alone is divided by ``factor``; ``"parts"``: pairs that turn
+    fewer than ``low`` times in ``original_length`` positions divided by ``factor``, those that turn more
+    than ``high`` times kept, a ramp between, and amplitude ``0.1 ln(factor) + 1``."""
+    if R < 2 or R % 2:
+        raise ValueError(f"R must be even and positive, got {R}")
+    if not (base > 0 and factor > 0 and original_length > 0 and high > low):
+        raise ValueError("base, factor and original_length must be positive, high above low")
+    if scaling == "base" and R > 2:
+        base = base * factor ** (R / (R - 2))
+    elif scaling not in (None, "linear", "base", "parts"):
+        raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
+    f = torch.arange(0, R, 2, dtype=torch.float64)
+    f = torch.exp(f * (-math.log(base) / R))
+    amplitude = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling == "parts":
+        turns = f * (original_length / (2 * math.pi))
+        keep = ((turns - low) / (high - low)).clamp(0.0, 1.0)
+        f = f * (keep + (1 - keep) / factor)
+        amplitude = 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0
+    return f.to(device), amplitude
+
+
+def _rope(name, inverse, q, k, freqs, positions, lens, slot_ids, D, layout, amplitude, q_out, k_out,
+          stream):
+    if layout not in ("half", "interleaved"):
+        raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+    x = q if q is not None else k
+    if x is None:
+        raise ValueError("q or k must be given")
+    T, Dh, dt = x.shape[0], x.shape[2], x.dtype
+    code, device, R = _dcode(x), x.device, 2 * freqs.shape[0]
+    args = []
+    outs = []
+    for label, t, o in (("q", q, q_out), ("k", k, k_out)):
+        if t is None:
+            args += [0, None, 0, None, 0]
+            outs.append(None)
+            continue
+        shape = (T, t.shape[1], Dh)
+        p, s = _rows(t, label, dt, shape)
+        if o is None:
+            o = _output(shape, dt, device, stream)
+        o_p, o_s = _rows(o, label + "_out", dt, shape)
+        args += [t.shape[1], p, s, o_p, o_s]
+        outs.append(o)
+    if positions is not None:
+        if lens is not None or slot_ids is not None:
+            raise ValueError("positions, or lens and slot_ids")
+        where = (_ints(positions, "positions", (T,)), None, 0, None, 0)
+    else:
+        if lens is None or slot_ids is None:
+            raise ValueError("positions, or lens and slot_ids")
+        N, n_slots = slot_ids.shape[0], lens.shape[0]
+        if N * D != T:
+            raise ValueError(f"{T} rows are not {D} of each of {N} sequences")
+        where = (None, _ints(lens, "lens", (n_slots,)), n_slots, _ints(slot_ids, "slot_ids", (N,)), D)
+    hq, q_p, q_s, qo_p, qo_s, hk, k_p, k_s, ko_p, ko_s = args
+    status = lib().shortconv_rope(
+        code, SC_ROPE_HALF if layout == "half" else SC_ROPE_INTERLEAVED, inverse, hq, hk, Dh, R, q_p,
+        q_s, k_p, k_s, T, _dev(freqs, "freqs", torch.float64), amplitude, *where, qo_p, qo_s, ko_p,
+        ko_s, _stream(stream, device))
+    if status:
+        _raise_on(name, status)
+    return tuple(outs)
+
+
+def rope(q, k, freqs, positions=None, lens=None, slot_ids=None, D=1, layout="half", amplitude=1.0,
+         q_out=None, k_out=None, stream=None):
+    """Rotary positions: ``q [T, Hq, Dh]`` and ``k [T, Hkv, Dh]`` (rows may be strided; either may be
+    None) with the first ``2 * len(freqs)`` values of each head turned in pairs, (i, i + R/2) or
+    (2i, 2i + 1) ("interleaved"). ``freqs`` and ``amplitude`` as ``rope_frequencies`` gives them.
+    ``positions`` int32 ``[T]``; or the ``D`` newest tokens of the cache's ``slot_ids`` at ``lens``.
+    ``q_out``, ``k_out`` may be ``q``, ``k`` themselves. Returns ``(q_out, k_out)``."""
+    return _rope("shortconv_rope", 0, q, k, freqs, positions, lens, slot_ids, D, layout, amplitude,
+                 q_out, k_out, stream)
+
+
+def rope_backward(dq, dk, freqs, positions=None, lens=None, slot_ids=None, D=1, layout="half",
+                  amplitude=1.0, dq_out=None, dk_out=None, stream=None):
+    """The gradients of ``rope``'s inputs from those of its outputs, with its other arguments."""
+    return _rope("shortconv_rope", 1, dq, dk, freqs, positions, lens, slot_ids, D, layout, amplitude,
+                 dq_out, dk_out, stream)
 
 
 def draft_accept(target, draft, tokens, uniforms, n_drafts=None, accepted=None, out_tokens=None,

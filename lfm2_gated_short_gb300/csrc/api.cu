@@ -184,11 +184,38 @@ bool disjoint(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
     return true;
 }
 
+// The scales of an 8-bit cache's pools: `page` of them a page and layer (0: no scales).
+struct Scales {
+    float *k, *v;
+    int page;
+};
+
+// Shape of an 8-bit cache, with a page_size that check_pages takes (or will refuse).
+sc_status check_8bit(int Hkv, int Dh, int block, int page_size) {
+    if (Hkv <= 0 || Dh <= 0 || block <= 0) return SC_EINVAL;
+    if (Dh % 16 != 0 || (int64_t)Hkv * Dh > (1 << 24) || block < 8 || (block & (block - 1)) != 0 ||
+        block > page_size)
+        return SC_EUNSUPPORTED;
+    return SC_OK;
+}
+
+// Whether some row of one array (rows of wa bytes, sa apart) meets a row of another, each of
+// them `rows` rows. Arrays of one stride may lie between each other's rows.
+bool rows_meet(const void *a, size_t sa, size_t wa, const void *b, size_t sb, size_t wb,
+               size_t rows) {
+    if (!overlaps(a, strided(wa ? rows : 0, sa, wa), b, strided(wb ? rows : 0, sb, wb)))
+        return false;
+    if (sa != sb || rows < 2) return true;
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    const size_t d = (size_t)((y % sa + sa - x % sa) % sa);  // b's rows behind a's
+    return d < wa || d + wb > sa;
+}
+
 // Arguments that pages_resize, _fork and _compact share; *pool_bytes of one pool.
 sc_status check_page_call(const void *refs, int n_pages, const void *table, const void *lens,
                           int n_slots, int max_pages, int page_size, int L, int64_t token_bytes,
-                          const void *k, const void *v, const void *ws, size_t ws_bytes,
-                          size_t need, size_t *pool_bytes) {
+                          const void *k, const void *v, const Scales &s, const void *ws,
+                          size_t ws_bytes, size_t need, size_t *pool_bytes, size_t *scale_bytes) {
     const sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
     if (st != SC_OK) return st;
     if (L < 0 || (L > 0 && token_bytes <= 0)) return SC_EINVAL;
@@ -200,7 +227,161 @@ sc_status check_page_call(const void *refs, int n_pages, const void *table, cons
         !ptr_ok(lens, (size_t)n_slots * 4, 4) || !ptr_ok(k, *pool_bytes, 16) ||
         !ptr_ok(v, *pool_bytes, 16) || !ptr_ok(ws, need, 16))
         return SC_EINVAL;
+    *scale_bytes = s.page > 0 ? times(times((size_t)n_pages * 4, (size_t)s.page), (size_t)L) : 0;
+    if (s.page > 0 && (!ptr_ok(s.k, *scale_bytes, 16) || !ptr_ok(s.v, *scale_bytes, 16)))
+        return SC_EINVAL;
     return SC_OK;
+}
+
+size_t pages_workspace(int n_pages, int n) {
+    return n_pages <= 0 || n < 0 ? 0 : sc::pages_workspace_bytes(n_pages, n);
+}
+
+sc_status pages_resize(int32_t *refs, int n_pages, int32_t *table, int32_t *lens, int n_slots,
+                       int max_pages, int page_size, const int32_t *slot_ids,
+                       const int32_t *new_lens, int n, int L, int64_t token_bytes, void *k_pages,
+                       void *v_pages, const Scales &s, void *workspace, size_t workspace_bytes,
+                       void *stream) {
+    if (n < 0 || n > n_slots) return SC_EINVAL;
+    const size_t need = pages_workspace(n_pages, n);
+    size_t n_pool = 0, n_sc = 0;
+    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
+                                         L, token_bytes, k_pages, v_pages, s, workspace,
+                                         workspace_bytes, need, &n_pool, &n_sc);
+    if (st != SC_OK) return st;
+    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
+    const size_t n_l = (size_t)n_slots * 4, n_i = (size_t)n * 4;
+    if (!ptr_ok(slot_ids, n_i, 4) || !ptr_ok(new_lens, n_i, 4)) return SC_EINVAL;
+    if (!disjoint({{refs, n_r}, {table, n_t}, {lens, n_l}, {k_pages, n_pool}, {v_pages, n_pool},
+                   {s.k, n_sc}, {s.v, n_sc}, {workspace, need}},
+                  {{slot_ids, n_i}, {new_lens, n_i}}))
+        return SC_EINVAL;
+    if (n == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RW(lens, n_l), RO(slot_ids, n_i),
+                      RO(new_lens, n_i), RW(k_pages, n_pool), RW(v_pages, n_pool),
+                      RW(workspace, need), RW(s.k, n_sc), RW(s.v, n_sc));
+    return from_cuda(sc::launch_pages_resize(
+        {refs, table, lens, n_pages, n_slots, max_pages, page_size}, slot_ids, new_lens, n,
+        {k_pages, v_pages, L, token_bytes, s.k, s.v, s.page}, workspace, sms, (cudaStream_t)stream));
+}
+
+sc_status pages_fork(int32_t *refs, int n_pages, int32_t *table, int32_t *lens, int n_slots,
+                     int max_pages, int page_size, const int32_t *src_slots,
+                     const int32_t *dst_slots, int n, int L, int64_t token_bytes, void *k_pages,
+                     void *v_pages, const Scales &s, void *workspace, size_t workspace_bytes,
+                     void *stream) {
+    if (n < 0 || n > n_slots) return SC_EINVAL;
+    const size_t need = pages_workspace(n_pages, n);
+    size_t n_pool = 0, n_sc = 0;
+    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
+                                         L, token_bytes, k_pages, v_pages, s, workspace,
+                                         workspace_bytes, need, &n_pool, &n_sc);
+    if (st != SC_OK) return st;
+    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
+    const size_t n_l = (size_t)n_slots * 4, n_i = (size_t)n * 4;
+    if (!ptr_ok(src_slots, n_i, 4) || !ptr_ok(dst_slots, n_i, 4)) return SC_EINVAL;
+    if (!disjoint({{refs, n_r}, {table, n_t}, {lens, n_l}, {k_pages, n_pool}, {v_pages, n_pool},
+                   {s.k, n_sc}, {s.v, n_sc}, {workspace, need}},
+                  {{src_slots, n_i}, {dst_slots, n_i}}))
+        return SC_EINVAL;
+    if (n == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RW(lens, n_l), RO(src_slots, n_i),
+                      RO(dst_slots, n_i), RW(k_pages, n_pool), RW(v_pages, n_pool),
+                      RW(workspace, need), RW(s.k, n_sc), RW(s.v, n_sc));
+    return from_cuda(sc::launch_pages_fork(
+        {refs, table, lens, n_pages, n_slots, max_pages, page_size}, src_slots, dst_slots, n,
+        {k_pages, v_pages, L, token_bytes, s.k, s.v, s.page}, workspace, sms, (cudaStream_t)stream));
+}
+
+sc_status pages_compact(int32_t *refs, int n_pages, int32_t *table, const int32_t *lens, int n_slots,
+                        int max_pages, int page_size, int L, int64_t token_bytes, void *k_pages,
+                        void *v_pages, const Scales &s, int32_t *n_used, void *workspace,
+                        size_t workspace_bytes, void *stream) {
+    const size_t need = pages_workspace(n_pages, 0);
+    size_t n_pool = 0, n_sc = 0;
+    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
+                                         L, token_bytes, k_pages, v_pages, s, workspace,
+                                         workspace_bytes, need, &n_pool, &n_sc);
+    if (st != SC_OK) return st;
+    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
+    const size_t n_l = (size_t)n_slots * 4;
+    if (!ptr_ok(n_used, 4, 4)) return SC_EINVAL;
+    if (!disjoint({{refs, n_r}, {table, n_t}, {k_pages, n_pool}, {v_pages, n_pool}, {s.k, n_sc},
+                   {s.v, n_sc}, {n_used, 4}, {workspace, need}},
+                  {{lens, n_l}}))
+        return SC_EINVAL;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RO(lens, n_l), RW(k_pages, n_pool),
+                      RW(v_pages, n_pool), RW(n_used, 4), RW(workspace, need), RW(s.k, n_sc),
+                      RW(s.v, n_sc));
+    return from_cuda(sc::launch_pages_compact(
+        {refs, table, const_cast<int32_t *>(lens), n_pages, n_slots, max_pages, page_size},
+        {k_pages, v_pages, L, token_bytes, s.k, s.v, s.page}, n_used, workspace, sms, (cudaStream_t)stream));
+}
+
+bool attention_sizes_ok(int Hq, int Hkv, int Dh, int N, int D, int shared_pages) {
+    return Hkv > 0 && Hq > 0 && Hq % Hkv == 0 && Hq / Hkv <= 128 && (Dh == 64 || Dh == 128) &&
+           N >= 0 && D > 0 && shared_pages >= 0 && query_rows_ok(Hq, N, D);
+}
+
+// block 0: a bf16 cache without scales.
+sc_status prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, int block, const void *q,
+                           int64_t q_stride, int N, int D, const void *k_pages,
+                           const void *v_pages, const float *k_scales, const float *v_scales,
+                           int n_pages, int page_size, const int32_t *table, const int32_t *lens,
+                           int n_slots, int max_pages, const int32_t *slot_ids, int shared_pages,
+                           float scale, void *out, void *workspace, size_t workspace_bytes,
+                           void *stream) {
+    const sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    if (st != SC_OK) return st;
+    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Dh <= 0 || N < 0 || D <= 0 || shared_pages < 0 ||
+        shared_pages > max_pages || q_stride < (int64_t)Hq * Dh || !(scale > 0.0f))
+        return SC_EINVAL;
+    if (dtype != SC_BF16 || (Dh != 64 && Dh != 128) || Hq / Hkv > 128 || q_stride % 8 != 0 ||
+        q_stride > (1ll << 36) || !query_rows_ok(Hq, N, D) ||
+        (int64_t)N * D * Hq * ((int64_t)max_pages * page_size / 64 + 1) > (1ll << 40) ||
+        (int64_t)max_pages * page_size > INT32_MAX - 255 ||  // key numbers pass a sequence's end
+        Hq > (1 << 16) || !(scale < 1e30f))
+        return SC_EUNSUPPORTED;
+    const size_t rows = (size_t)N * D;
+    const size_t n_q = strided(rows, (size_t)q_stride * 2, (size_t)Hq * Dh * 2);
+    const size_t n_out = rows * Hq * Dh * 2;
+    const size_t n_pool = (size_t)n_pages * page_size * Hkv * Dh * (block ? 1 : 2);
+    const size_t n_sc = block ? times((size_t)n_pages * (page_size / block), (size_t)Hkv * 4) : 0;
+    const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
+    const size_t n_i = (size_t)N * 4;
+    const sc::AttnShape shape = {Hq, Hkv, Dh, N, D, shared_pages};
+    const size_t need = block ? sc::attention8_workspace_bytes(shape, page_size)
+                              : sc::attention_workspace_bytes(shape);
+    if (workspace_bytes < need) return SC_EINVAL;
+    if (!ptr_ok(q, n_q, 16) || !ptr_ok(k_pages, n_pool, 16) || !ptr_ok(v_pages, n_pool, 16) ||
+        !ptr_ok(k_scales, n_sc, 16) || !ptr_ok(v_scales, n_sc, 16) || !ptr_ok(table, n_t, 4) ||
+        !ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4) || !ptr_ok(out, n_out, 16) ||
+        !ptr_ok(workspace, need, 16))
+        return SC_EINVAL;
+    if (!disjoint({{out, n_out}, {workspace, need}},
+                  {{q, n_q}, {k_pages, n_pool}, {v_pages, n_pool}, {k_scales, n_sc},
+                   {v_scales, n_sc}, {table, n_t}, {lens, n_l}, {slot_ids, n_i}}))
+        return SC_EINVAL;
+    if (N == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitAttention, RO(q, n_q), RO(k_pages, n_pool), RO(v_pages, n_pool),
+                      RO(table, n_t), RO(lens, n_l), RO(slot_ids, n_i), RW(out, n_out),
+                      RW(workspace, need), RO(k_scales, n_sc), RO(v_scales, n_sc));
+    int block_log2 = 0;
+    while (block >> (block_log2 + 1)) ++block_log2;
+    const sc::Scales8 scales = {k_scales, v_scales, block_log2};
+    return from_cuda(sc::launch_prefix_attention(
+        shape, q, q_stride, k_pages, v_pages, block ? &scales : nullptr,
+        {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
+         max_pages, page_size},
+        slot_ids, scale, out, workspace, sms, (cudaStream_t)stream));
 }
 
 }  // namespace
@@ -567,8 +748,7 @@ sc_status shortconv_pool_copy(sc_dtype dtype, int H, int K, void *pool, int n_sl
 }
 
 size_t shortconv_pages_workspace_bytes(int n_pages, int n) {
-    if (n_pages <= 0 || n < 0) return 0;
-    return sc::pages_workspace_bytes(n_pages, n);
+    return pages_workspace(n_pages, n);
 }
 
 sc_status shortconv_pages_resize(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
@@ -576,29 +756,9 @@ sc_status shortconv_pages_resize(int32_t *refs, int n_pages, int32_t *table, int
                                  const int32_t *slot_ids, const int32_t *new_lens, int n, int L,
                                  int64_t token_bytes, void *k_pages, void *v_pages,
                                  void *workspace, size_t workspace_bytes, void *stream) {
-    if (n < 0 || n > n_slots) return SC_EINVAL;
-    const size_t need = shortconv_pages_workspace_bytes(n_pages, n);
-    size_t n_pool = 0;
-    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
-                                         L, token_bytes, k_pages, v_pages, workspace,
-                                         workspace_bytes, need, &n_pool);
-    if (st != SC_OK) return st;
-    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
-    const size_t n_l = (size_t)n_slots * 4, n_i = (size_t)n * 4;
-    if (!ptr_ok(slot_ids, n_i, 4) || !ptr_ok(new_lens, n_i, 4)) return SC_EINVAL;
-    if (!disjoint({{refs, n_r}, {table, n_t}, {lens, n_l}, {k_pages, n_pool}, {v_pages, n_pool},
-                   {workspace, need}},
-                  {{slot_ids, n_i}, {new_lens, n_i}}))
-        return SC_EINVAL;
-    if (n == 0) return SC_OK;
-    const int sms = sm_count_of_current_device();
-    if (sms <= 0) return SC_ECUDA;
-    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RW(lens, n_l), RO(slot_ids, n_i),
-                      RO(new_lens, n_i), RW(k_pages, n_pool), RW(v_pages, n_pool),
-                      RW(workspace, need));
-    return from_cuda(sc::launch_pages_resize({refs, table, lens, n_pages, n_slots, max_pages, page_size},
-                                             slot_ids, new_lens, n, {k_pages, v_pages, L, token_bytes},
-                                             workspace, sms, (cudaStream_t)stream));
+    return pages_resize(refs, n_pages, table, lens, n_slots, max_pages, page_size, slot_ids,
+                        new_lens, n, L, token_bytes, k_pages, v_pages, {nullptr, nullptr, 0},
+                        workspace, workspace_bytes, stream);
 }
 
 sc_status shortconv_pages_fork(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
@@ -606,29 +766,9 @@ sc_status shortconv_pages_fork(int32_t *refs, int n_pages, int32_t *table, int32
                                const int32_t *src_slots, const int32_t *dst_slots, int n, int L,
                                int64_t token_bytes, void *k_pages, void *v_pages, void *workspace,
                                size_t workspace_bytes, void *stream) {
-    if (n < 0 || n > n_slots) return SC_EINVAL;
-    const size_t need = shortconv_pages_workspace_bytes(n_pages, n);
-    size_t n_pool = 0;
-    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
-                                         L, token_bytes, k_pages, v_pages, workspace,
-                                         workspace_bytes, need, &n_pool);
-    if (st != SC_OK) return st;
-    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
-    const size_t n_l = (size_t)n_slots * 4, n_i = (size_t)n * 4;
-    if (!ptr_ok(src_slots, n_i, 4) || !ptr_ok(dst_slots, n_i, 4)) return SC_EINVAL;
-    if (!disjoint({{refs, n_r}, {table, n_t}, {lens, n_l}, {k_pages, n_pool}, {v_pages, n_pool},
-                   {workspace, need}},
-                  {{src_slots, n_i}, {dst_slots, n_i}}))
-        return SC_EINVAL;
-    if (n == 0) return SC_OK;
-    const int sms = sm_count_of_current_device();
-    if (sms <= 0) return SC_ECUDA;
-    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RW(lens, n_l), RO(src_slots, n_i),
-                      RO(dst_slots, n_i), RW(k_pages, n_pool), RW(v_pages, n_pool),
-                      RW(workspace, need));
-    return from_cuda(sc::launch_pages_fork({refs, table, lens, n_pages, n_slots, max_pages, page_size},
-                                           src_slots, dst_slots, n, {k_pages, v_pages, L, token_bytes},
-                                           workspace, sms, (cudaStream_t)stream));
+    return pages_fork(refs, n_pages, table, lens, n_slots, max_pages, page_size, src_slots,
+                      dst_slots, n, L, token_bytes, k_pages, v_pages, {nullptr, nullptr, 0},
+                      workspace, workspace_bytes, stream);
 }
 
 sc_status shortconv_pages_compact(int32_t *refs, int n_pages, int32_t *table, const int32_t *lens,
@@ -636,26 +776,51 @@ sc_status shortconv_pages_compact(int32_t *refs, int n_pages, int32_t *table, co
                                   int64_t token_bytes, void *k_pages, void *v_pages,
                                   int32_t *n_used, void *workspace, size_t workspace_bytes,
                                   void *stream) {
-    const size_t need = shortconv_pages_workspace_bytes(n_pages, 0);
-    size_t n_pool = 0;
-    const sc_status st = check_page_call(refs, n_pages, table, lens, n_slots, max_pages, page_size,
-                                         L, token_bytes, k_pages, v_pages, workspace,
-                                         workspace_bytes, need, &n_pool);
+    return pages_compact(refs, n_pages, table, lens, n_slots, max_pages, page_size, L, token_bytes,
+                         k_pages, v_pages, {nullptr, nullptr, 0}, n_used, workspace,
+                         workspace_bytes, stream);
+}
+
+sc_status shortconv_pages_resize_8bit(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                                      int n_slots, int max_pages, int page_size,
+                                      const int32_t *slot_ids, const int32_t *new_lens, int n,
+                                      int L, int Hkv, int Dh, int block, void *k_pages,
+                                      void *v_pages, float *k_scales, float *v_scales,
+                                      void *workspace, size_t workspace_bytes, void *stream) {
+    const sc_status st = check_8bit(Hkv, Dh, block, page_size);
     if (st != SC_OK) return st;
-    const size_t n_r = (size_t)n_pages * 4, n_t = (size_t)n_slots * max_pages * 4;
-    const size_t n_l = (size_t)n_slots * 4;
-    if (!ptr_ok(n_used, 4, 4)) return SC_EINVAL;
-    if (!disjoint({{refs, n_r}, {table, n_t}, {k_pages, n_pool}, {v_pages, n_pool}, {n_used, 4},
-                   {workspace, need}},
-                  {{lens, n_l}}))
-        return SC_EINVAL;
-    const int sms = sm_count_of_current_device();
-    if (sms <= 0) return SC_ECUDA;
-    SC_BOUNDS_INSTALL(kUnitPages, RW(refs, n_r), RW(table, n_t), RO(lens, n_l), RW(k_pages, n_pool),
-                      RW(v_pages, n_pool), RW(n_used, 4), RW(workspace, need));
-    return from_cuda(sc::launch_pages_compact(
-        {refs, table, const_cast<int32_t *>(lens), n_pages, n_slots, max_pages, page_size},
-        {k_pages, v_pages, L, token_bytes}, n_used, workspace, sms, (cudaStream_t)stream));
+    return pages_resize(refs, n_pages, table, lens, n_slots, max_pages, page_size, slot_ids,
+                        new_lens, n, L, (int64_t)Hkv * Dh, k_pages, v_pages,
+                        {k_scales, v_scales, page_size / block * Hkv}, workspace, workspace_bytes,
+                        stream);
+}
+
+sc_status shortconv_pages_fork_8bit(int32_t *refs, int n_pages, int32_t *table, int32_t *lens,
+                                    int n_slots, int max_pages, int page_size,
+                                    const int32_t *src_slots, const int32_t *dst_slots, int n,
+                                    int L, int Hkv, int Dh, int block, void *k_pages,
+                                    void *v_pages, float *k_scales, float *v_scales,
+                                    void *workspace, size_t workspace_bytes, void *stream) {
+    const sc_status st = check_8bit(Hkv, Dh, block, page_size);
+    if (st != SC_OK) return st;
+    return pages_fork(refs, n_pages, table, lens, n_slots, max_pages, page_size, src_slots,
+                      dst_slots, n, L, (int64_t)Hkv * Dh, k_pages, v_pages,
+                      {k_scales, v_scales, page_size / block * Hkv}, workspace, workspace_bytes,
+                      stream);
+}
+
+sc_status shortconv_pages_compact_8bit(int32_t *refs, int n_pages, int32_t *table,
+                                       const int32_t *lens, int n_slots, int max_pages,
+                                       int page_size, int L, int Hkv, int Dh, int block,
+                                       void *k_pages, void *v_pages, float *k_scales,
+                                       float *v_scales, int32_t *n_used, void *workspace,
+                                       size_t workspace_bytes, void *stream) {
+    const sc_status st = check_8bit(Hkv, Dh, block, page_size);
+    if (st != SC_OK) return st;
+    return pages_compact(refs, n_pages, table, lens, n_slots, max_pages, page_size, L,
+                         (int64_t)Hkv * Dh, k_pages, v_pages,
+                         {k_scales, v_scales, page_size / block * Hkv}, n_used, workspace,
+                         workspace_bytes, stream);
 }
 
 sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v, int64_t v_stride,
@@ -689,16 +854,193 @@ sc_status shortconv_pages_append(const void *k, int64_t k_stride, const void *v,
     return from_cuda(sc::launch_pages_append(
         {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
          max_pages, page_size},
-        k, k_stride, v, v_stride, slot_ids, N, D, {k_pages, v_pages, 1, token_bytes},
+        k, k_stride, v, v_stride, slot_ids, N, D, {k_pages, v_pages, 1, token_bytes, nullptr, nullptr, 0},
         (cudaStream_t)stream));
+}
+
+sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block, const void *k,
+                                      int64_t k_stride, const void *v, int64_t v_stride, int N,
+                                      int D, void *k_pages, void *v_pages, float *k_scales,
+                                      float *v_scales, int n_pages, int page_size,
+                                      const int32_t *table, const int32_t *lens, int n_slots,
+                                      int max_pages, const int32_t *slot_ids, void *stream) {
+    if (dtype != SC_BF16 && dtype != SC_F32) return SC_EUNSUPPORTED;
+    sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    if (st == SC_OK) st = check_8bit(Hkv, Dh, block, page_size);
+    if (st != SC_OK) return st;
+    const int64_t width = (int64_t)Hkv * Dh, es = elem_size(dtype);
+    if (N < 0 || D <= 0 || k_stride < width || v_stride < width) return SC_EINVAL;
+    if (k_stride * es % 16 != 0 || v_stride * es % 16 != 0 || k_stride > (1ll << 36) ||
+        v_stride > (1ll << 36))
+        return SC_EUNSUPPORTED;
+    // Blocks of the call, one warp each.
+    const int64_t units = ((int64_t)D + 2 * block - 2) / block * N;
+    if ((int64_t)N * D > INT32_MAX / 2 || units > INT32_MAX / 8 / Hkv) return SC_EINVAL;
+    const size_t rows = (size_t)N * D;
+    const size_t n_k = strided(rows, k_stride * es, width * es);
+    const size_t n_v = strided(rows, v_stride * es, width * es);
+    const size_t n_pool = times((size_t)n_pages * page_size, width);
+    const size_t n_sc = times((size_t)n_pages * (page_size / block), (size_t)Hkv * 4);
+    const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
+    if (!ptr_ok(k, n_k, 16) || !ptr_ok(v, n_v, 16) || !ptr_ok(k_pages, n_pool, 16) ||
+        !ptr_ok(v_pages, n_pool, 16) || !ptr_ok(k_scales, n_sc, 16) ||
+        !ptr_ok(v_scales, n_sc, 16) || !ptr_ok(table, n_t, 4) || !ptr_ok(lens, n_l, 4) ||
+        !ptr_ok(slot_ids, (size_t)N * 4, 4))
+        return SC_EINVAL;
+    if (!disjoint({{k_pages, n_pool}, {v_pages, n_pool}, {k_scales, n_sc}, {v_scales, n_sc}},
+                  {{k, n_k}, {v, n_v}, {table, n_t}, {lens, n_l}, {slot_ids, (size_t)N * 4}}))
+        return SC_EINVAL;
+    if (N == 0) return SC_OK;
+    SC_BOUNDS_INSTALL(kUnitCache8, RO(k, n_k), RO(v, n_v), RW(k_pages, n_pool),
+                      RW(v_pages, n_pool), RW(k_scales, n_sc), RW(v_scales, n_sc), RO(table, n_t),
+                      RO(lens, n_l), RO(slot_ids, (size_t)N * 4));
+    return from_cuda(sc::launch_append8(
+        dtype,
+        {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
+         max_pages, page_size},
+        k, k_stride, v, v_stride, slot_ids, N, D,
+        {k_pages, v_pages, k_scales, v_scales, Hkv, Dh, block}, (cudaStream_t)stream));
+}
+
+sc_status shortconv_pages_read_8bit(sc_dtype dtype, int Hkv, int Dh, int block,
+                                    const void *k_pages, const void *v_pages,
+                                    const float *k_scales, const float *v_scales, int n_pages,
+                                    int page_size, const int32_t *table, const int32_t *lens,
+                                    int n_slots, int max_pages, const int32_t *slot_ids,
+                                    const int32_t *cu_seqlens, const int32_t *starts, int N,
+                                    int64_t T, void *k, void *v, void *stream) {
+    if (dtype != SC_BF16 && dtype != SC_F32) return SC_EUNSUPPORTED;
+    sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    if (st == SC_OK) st = check_8bit(Hkv, Dh, block, page_size);
+    if (st != SC_OK) return st;
+    if (N < 0 || T < 0 || T > INT32_MAX || (N == 0 && T != 0)) return SC_EINVAL;
+    const size_t width = (size_t)Hkv * Dh;
+    const size_t n_out = times((size_t)T, width * elem_size(dtype));
+    const size_t n_pool = times((size_t)n_pages * page_size, width);
+    const size_t n_sc = times((size_t)n_pages * (page_size / block), (size_t)Hkv * 4);
+    const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
+    const size_t n_i = (size_t)N * 4, n_st = starts ? n_i : 0;
+    if (!ptr_ok(k_pages, n_pool, 16) || !ptr_ok(v_pages, n_pool, 16) ||
+        !ptr_ok(k_scales, n_sc, 16) || !ptr_ok(v_scales, n_sc, 16) || !ptr_ok(table, n_t, 4) ||
+        !ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4) ||
+        !ptr_ok(cu_seqlens, n_i + 4, 4) || !opt_ok(starts, 4) || !ptr_ok(k, n_out, 16) ||
+        !ptr_ok(v, n_out, 16))
+        return SC_EINVAL;
+    if (!disjoint({{k, n_out}, {v, n_out}},
+                  {{k_pages, n_pool}, {v_pages, n_pool}, {k_scales, n_sc}, {v_scales, n_sc},
+                   {table, n_t}, {lens, n_l}, {slot_ids, n_i}, {cu_seqlens, n_i + 4},
+                   {starts, n_st}}))
+        return SC_EINVAL;
+    if (N == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitCache8, RO(k_pages, n_pool), RO(v_pages, n_pool), RO(k_scales, n_sc),
+                      RO(v_scales, n_sc), RO(table, n_t), RO(lens, n_l), RO(slot_ids, n_i),
+                      RO(cu_seqlens, n_i + 4), RO(starts, n_st), RW(k, n_out), RW(v, n_out));
+    return from_cuda(sc::launch_read8(
+        dtype,
+        {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
+         max_pages, page_size},
+        slot_ids, cu_seqlens, starts, N, T,
+        {const_cast<void *>(k_pages), const_cast<void *>(v_pages), const_cast<float *>(k_scales),
+         const_cast<float *>(v_scales), Hkv, Dh, block},
+        k, v, sms, (cudaStream_t)stream));
+}
+
+sc_status shortconv_rope(sc_dtype dtype, sc_rope_layout layout, int inverse, int Hq, int Hkv,
+                         int Dh, int R, const void *q, int64_t q_stride, const void *k,
+                         int64_t k_stride, int64_t T, const double *freqs, float amplitude,
+                         const int32_t *positions, const int32_t *lens, int n_slots,
+                         const int32_t *slot_ids, int D, void *q_out, int64_t q_out_stride,
+                         void *k_out, int64_t k_out_stride, void *stream) {
+    if (dtype != SC_BF16 && dtype != SC_F32) return SC_EUNSUPPORTED;
+    if (layout != SC_ROPE_HALF && layout != SC_ROPE_INTERLEAVED) return SC_EINVAL;
+    if (Hq < 0 || Hkv < 0 || Hq + (int64_t)Hkv == 0 || Dh <= 0 || R <= 0 || R > Dh || R % 2 != 0 ||
+        T < 0 || T > INT32_MAX)
+        return SC_EINVAL;
+    if (R > 512 || Dh > (1 << 16) || Hq > (1 << 16) || Hkv > (1 << 16) ||
+        ((int64_t)Hq + Hkv) * Dh > (1 << 24))
+        return SC_EUNSUPPORTED;
+    const size_t es = elem_size(dtype);
+    const int64_t w[2] = {(int64_t)Hq * Dh, (int64_t)Hkv * Dh};
+    const int64_t si[2] = {q_stride, k_stride}, so[2] = {q_out_stride, k_out_stride};
+    const void *in[2] = {q, k};
+    void *out[2] = {q_out, k_out};
+    size_t n_in[2], n_out[2];
+    for (int x = 0; x < 2; ++x) {
+        if (w[x] > 0 && (si[x] < w[x] || so[x] < w[x])) return SC_EINVAL;
+        if (w[x] > 0 && (si[x] > (1ll << 36) || so[x] > (1ll << 36))) return SC_EUNSUPPORTED;
+        n_in[x] = w[x] > 0 ? strided((size_t)T, si[x] * es, w[x] * es) : 0;
+        n_out[x] = w[x] > 0 ? strided((size_t)T, so[x] * es, w[x] * es) : 0;
+        if (!ptr_ok(in[x], n_in[x], es) || !ptr_ok(out[x], n_out[x], es)) return SC_EINVAL;
+    }
+    const bool by_slot = positions == nullptr && T > 0;
+    if (by_slot && (D <= 0 || n_slots <= 0 || T % D != 0)) return SC_EINVAL;
+    const size_t n_f = (size_t)R / 2 * 8, n_p = by_slot ? 0 : (size_t)T * 4;
+    const size_t n_l = by_slot ? (size_t)n_slots * 4 : 0, n_i = by_slot ? (size_t)(T / D) * 4 : 0;
+    if (!ptr_ok(freqs, n_f, 8) || !ptr_ok(positions, n_p, 4) ||
+        (by_slot && (!ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4))))
+        return SC_EINVAL;
+    // An output may be its own input (same pointer and stride); otherwise no row of an
+    // output meets a row of another array, which may lie between them (one projection's q and k).
+    const size_t T_ = (size_t)T;
+    for (int x = 0; x < 2; ++x) {
+        if (n_out[x] == 0) continue;
+        for (int y = 0; y < 2; ++y) {
+            const bool same = x == y && out[x] == in[y] && so[x] == si[y];
+            if (!same && rows_meet(out[x], so[x] * es, w[x] * es, in[y], si[y] * es, w[y] * es, T_))
+                return SC_EINVAL;
+        }
+        if (!disjoint({{out[x], n_out[x]}},
+                      {{freqs, n_f}, {positions, n_p}, {lens, n_l}, {slot_ids, n_i}}))
+            return SC_EINVAL;
+    }
+    if (rows_meet(q_out, so[0] * es, w[0] * es, k_out, so[1] * es, w[1] * es, T_)) return SC_EINVAL;
+    if (T == 0) return SC_OK;
+    const int sms = sm_count_of_current_device();
+    if (sms <= 0) return SC_ECUDA;
+    SC_BOUNDS_INSTALL(kUnitRope, RO(q, n_in[0]), RO(k, n_in[1]), RO(freqs, n_f),
+                      RO(positions, n_p), RO(lens, n_l), RO(slot_ids, n_i), RW(q_out, n_out[0]),
+                      RW(k_out, n_out[1]));
+    sc::RopeArgs a = {};
+    a.q = q;
+    a.k = k;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.freqs = freqs;
+    a.positions = positions;
+    a.lens = lens;
+    a.slots = slot_ids;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.Dh = Dh;
+    a.R = R;
+    a.D = D;
+    a.n_slots = n_slots;
+    a.amplitude = amplitude;
+    a.half_layout = layout == SC_ROPE_HALF;
+    a.inverse = inverse != 0;
+    a.copy = R < Dh && (q_out != q || k_out != k);
+    return from_cuda(sc::launch_rope(dtype, a, sms, (cudaStream_t)stream));
 }
 
 size_t shortconv_prefix_attention_workspace_bytes(int Hq, int Hkv, int Dh, int N, int D,
                                                   int shared_pages) {
-    if (Hkv <= 0 || Hq <= 0 || Hq % Hkv != 0 || Hq / Hkv > 128 || (Dh != 64 && Dh != 128) ||
-        N < 0 || D <= 0 || shared_pages < 0 || !query_rows_ok(Hq, N, D))
-        return 0;
+    if (!attention_sizes_ok(Hq, Hkv, Dh, N, D, shared_pages)) return 0;
     return sc::attention_workspace_bytes({Hq, Hkv, Dh, N, D, shared_pages});
+}
+
+size_t shortconv_prefix_attention_8bit_workspace_bytes(int Hq, int Hkv, int Dh, int N, int D,
+                                                       int shared_pages, int page_size) {
+    if (!attention_sizes_ok(Hq, Hkv, Dh, N, D, shared_pages) || page_size < 8 || page_size > 256 ||
+        (int64_t)shared_pages * page_size > INT32_MAX - 255 || Hkv > (1 << 16))
+        return 0;
+    return sc::attention8_workspace_bytes({Hq, Hkv, Dh, N, D, shared_pages}, page_size);
 }
 
 sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, const void *q,
@@ -709,44 +1051,24 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
                                      float scale, void *out, void *workspace,
                                      size_t workspace_bytes, void *stream) {
     if (dtype != SC_BF16 && dtype != SC_F32) return SC_EUNSUPPORTED;
-    const sc_status st = check_pages(n_pages, n_slots, max_pages, page_size);
+    return prefix_attention(dtype, Hq, Hkv, Dh, 0, q, q_stride, N, D, k_pages, v_pages, nullptr,
+                            nullptr, n_pages, page_size, table, lens, n_slots, max_pages, slot_ids,
+                            shared_pages, scale, out, workspace, workspace_bytes, stream);
+}
+
+sc_status shortconv_prefix_attention_8bit(int Hq, int Hkv, int Dh, int block, const void *q,
+                                          int64_t q_stride, int N, int D, const void *k_pages,
+                                          const void *v_pages, const float *k_scales,
+                                          const float *v_scales, int n_pages, int page_size,
+                                          const int32_t *table, const int32_t *lens, int n_slots,
+                                          int max_pages, const int32_t *slot_ids,
+                                          int shared_pages, float scale, void *out,
+                                          void *workspace, size_t workspace_bytes, void *stream) {
+    const sc_status st = check_8bit(Hkv, Dh, block, page_size);
     if (st != SC_OK) return st;
-    if (Hq <= 0 || Hkv <= 0 || Hq % Hkv != 0 || Dh <= 0 || N < 0 || D <= 0 || shared_pages < 0 ||
-        shared_pages > max_pages || q_stride < (int64_t)Hq * Dh || !(scale > 0.0f))
-        return SC_EINVAL;
-    if (dtype != SC_BF16 || (Dh != 64 && Dh != 128) || Hq / Hkv > 128 || q_stride % 8 != 0 ||
-        q_stride > (1ll << 36) || !query_rows_ok(Hq, N, D) ||
-        (int64_t)N * D * Hq * ((int64_t)max_pages * page_size / 64 + 1) > (1ll << 40) ||
-        (int64_t)max_pages * page_size > INT32_MAX - 255 ||  // key numbers pass a sequence's end
-        Hq > (1 << 16) || !(scale < 1e30f))
-        return SC_EUNSUPPORTED;
-    const size_t rows = (size_t)N * D;
-    const size_t n_q = strided(rows, (size_t)q_stride * 2, (size_t)Hq * Dh * 2);
-    const size_t n_out = rows * Hq * Dh * 2;
-    const size_t n_pool = (size_t)n_pages * page_size * Hkv * Dh * 2;
-    const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
-    const size_t n_i = (size_t)N * 4;
-    const size_t need = sc::attention_workspace_bytes({Hq, Hkv, Dh, N, D, shared_pages});
-    if (workspace_bytes < need) return SC_EINVAL;
-    if (!ptr_ok(q, n_q, 16) || !ptr_ok(k_pages, n_pool, 16) || !ptr_ok(v_pages, n_pool, 16) ||
-        !ptr_ok(table, n_t, 4) || !ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4) ||
-        !ptr_ok(out, n_out, 16) || !ptr_ok(workspace, need, 16))
-        return SC_EINVAL;
-    if (!disjoint({{out, n_out}, {workspace, need}},
-                  {{q, n_q}, {k_pages, n_pool}, {v_pages, n_pool}, {table, n_t}, {lens, n_l},
-                   {slot_ids, n_i}}))
-        return SC_EINVAL;
-    if (N == 0) return SC_OK;
-    const int sms = sm_count_of_current_device();
-    if (sms <= 0) return SC_ECUDA;
-    SC_BOUNDS_INSTALL(kUnitAttention, RO(q, n_q), RO(k_pages, n_pool), RO(v_pages, n_pool),
-                      RO(table, n_t), RO(lens, n_l), RO(slot_ids, n_i), RW(out, n_out),
-                      RW(workspace, need));
-    return from_cuda(sc::launch_prefix_attention(
-        {Hq, Hkv, Dh, N, D, shared_pages}, q, q_stride, k_pages, v_pages,
-        {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
-         max_pages, page_size},
-        slot_ids, scale, out, workspace, sms, (cudaStream_t)stream));
+    return prefix_attention(SC_BF16, Hq, Hkv, Dh, block, q, q_stride, N, D, k_pages, v_pages,
+                            k_scales, v_scales, n_pages, page_size, table, lens, n_slots, max_pages,
+                            slot_ids, shared_pages, scale, out, workspace, workspace_bytes, stream);
 }
 
 sc_status shortconv_draft_accept(sc_dtype dtype, int V, int N, int D, const void *target,

@@ -30,6 +30,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "e4m3.cuh"
 #include "errors.cuh"
 #include "kernels.h"
 #include "launch.h"
@@ -43,7 +44,6 @@ namespace sc {
 
 typedef __nv_bfloat16 bf16;
 
-constexpr int kKT = 64;            // keys of a tile
 constexpr int kMaxCtas = 456;      // three CTAs on each of 152 SMs
 constexpr int kMaxPrefixCtas = 152;
 constexpr float kLog2e = 1.4426950408889634f;
@@ -61,6 +61,7 @@ struct AttnArgs {
     bf16 *out;
     int64_t *cum;      // [N + 1] first own tile of each sequence
     float *own_part;   // [items + CTAs] parts of MR rows: O [MR][Dh], m [MR], l [MR]
+    Scales8 s8;        // of an 8-bit cache
 };
 
 // Slots, lengths and tables are read in L2: k_own beside k_prefix starts without a wait of
@@ -92,9 +93,10 @@ __device__ __forceinline__ int seq_len(const AttnArgs &a, int i, int *slot, bool
 __device__ __forceinline__ int prefix_keys(const AttnArgs &a, int len) {
     return len - a.D + 1 >= a.shared_keys ? a.shared_keys : 0;
 }
-// Key tiles of a sequence's own part.
+// Tiles of KT keys of a sequence's own part.
+template <int KT>
 __device__ __forceinline__ int own_tiles(const AttnArgs &a, int len) {
-    return len > 0 ? (len - prefix_keys(a, len) + kKT - 1) / kKT : 0;
+    return len > 0 ? (len - prefix_keys(a, len) + KT - 1) / KT : 0;
 }
 
 // An item piece as the producer describes it to the consumers: tiles t0 .. t0 + n - 1
@@ -251,20 +253,21 @@ __device__ __forceinline__ void product_one_by_one(float (&o)[DH / 8][4],
     }
 }
 
-// RG groups of 16 rows times KG key groups: a consumer warp takes 16 rows by 64 / KG keys of
+// RG groups of 16 rows times KG key groups: a consumer warp takes 16 rows by KT / KG keys of
 // a tile. 16 rows are bound by the tiles' bytes, and more, lighter warps start and
 // end an item sooner; 32 rows of 64 columns are bound by the warps' own latency,
 // and 32 keys a warp keep more of their work independent. CTAs of an SM and
 // stages are what shared memory and registers allow.
-template <int DH, int RG>
+template <int DH, int RG, bool Q8>
 struct OwnCfg {
     static constexpr int MR = 16 * RG;
+    static constexpr int KT = 64;                             // keys of a tile
     static constexpr int KG = DH == 64 && RG == 2 ? 2 : 4;    // key groups
-    static constexpr int KB = kKT / 16 / KG;                  // blocks of 16 keys of a warp
+    static constexpr int KB = KT / 16 / KG;                   // blocks of 16 keys of a warp
     static constexpr int kWarps = KG * RG;                    // consumer warps
     static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer
     static constexpr int NB = DH / 64;                        // 64-wide column blocks
-    static constexpr uint32_t kBlk = kKT * 128;               // one block of a tile, 8 KB
+    static constexpr uint32_t kBlk = KT * 128;                // one block of a tile, 8 KB
     static constexpr uint32_t kStage = 2 * NB * kBlk;         // K and V of a tile
     static constexpr int kCtas = DH == 64 ? 3 : (RG == 1 ? 2 : 1);
     static constexpr int kStages = DH == 64 ? 3 : (RG == 1 ? 2 : 4);
@@ -276,18 +279,47 @@ struct OwnCfg {
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part
 };
 
+// The 8-bit cache's tiles have half the bytes a key: twice the keys a tile.
 template <int DH, int RG>
-__global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCtas)
+struct OwnCfg<DH, RG, true> {
+    static constexpr int MR = 16 * RG;
+    static constexpr int KT = DH == 64 ? 128 : 64;
+    static constexpr int KG = 4;
+    static constexpr int KB = KT / 16 / KG;
+    static constexpr int kWarps = KG * RG;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int NB = DH / 64;                        // 64-wide column blocks of Q
+    static constexpr uint32_t kV = KT * DH;                   // the tile's V behind its K
+    static constexpr uint32_t kStage = 2 * kV;                // 16 KB
+    static constexpr int kCtas = DH == 64 ? 4 - RG : 3 - RG;
+    static constexpr int kStages = 3;
+    static constexpr int kQBufs = 2;
+    static constexpr uint32_t kQ = MR * 128 * NB;
+    static constexpr int kOs = DH + 4;
+    static constexpr uint32_t kJoin = KG * MR * (kOs + 2) * 4;
+    static constexpr size_t kSmem = 1024 + kStages * kStage + kQBufs * kQ + kJoin;
+    static constexpr int kSlot = MR * (DH + 2);
+};
+
+}  // namespace sc
+
+#include "attention_8bit.cuh"
+
+namespace sc {
+
+template <int DH, int RG, bool Q8>
+__global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q8>::kCtas)
     k_own(AttnArgs a, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
-    using C = OwnCfg<DH, RG>;
-    constexpr int ST = C::kStages, kThreads = C::kThreads, KG = C::KG, KB = C::KB;
+    using C = OwnCfg<DH, RG, Q8>;
+    constexpr int ST = C::kStages, kThreads = C::kThreads, KG = C::KG, KB = C::KB, kKT = C::KT;
     constexpr int QB = C::kQBufs;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t s_full[ST], s_empty[ST];
     __shared__ uint64_t s_qfull[QB], s_qempty[QB];  // an item's queries and description
     __shared__ OwnItem s_item[QB];
     __shared__ int s_bad[ST];
+    __shared__ TileScales8<Q8 ? kKT / 8 : 1> s_scale[Q8 ? ST : 1];  // of the 8-bit cache's tiles
     __shared__ int64_t s_scan[kThreads / 32];
     __shared__ int s_seq, s_slots[kThreads], s_lens[kThreads];  // of all sequences, if they fit
     __shared__ int64_t s_seq_unit;
@@ -300,7 +332,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
-            mbar_init(&s_full[s], 1);
+            mbar_init(&s_full[s], Q8 ? 33 : 1);  // the scales' copies, by all lanes
             mbar_init(&s_empty[s], C::kWarps);
             s_bad[s] = 0;
         }
@@ -339,7 +371,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         const int i = i0 + tid;
         int slot = my_slot, len = my_len;
         if (i0 > 0) len = i < a.N ? seq_len(a, i, &slot, report) : -1;
-        *mine = (int64_t)per * own_tiles(a, len);
+        *mine = (int64_t)per * own_tiles<kKT>(a, len);
         int64_t inc = *mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -410,7 +442,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             for (; i < a.N; ++i) {
                 if (i - known >= 32) fetch(i);
                 s.len = __shfl_sync(~0u, len_l, i - known);
-                s.T = own_tiles(a, s.len);
+                s.T = own_tiles<kKT>(a, s.len);
                 if (s.T > 0) break;
             }
             s.i = i;
@@ -469,16 +501,30 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                 if (lane == 0) {
                     if (bad) raise_error(SC_DEV_BAD_PAGE);
                     s_bad[st] = bad;
-                    mbar_arrive_expect_tx(&s_full[st], (uint32_t)boxes * box * DH * 4);
                 }
+                if constexpr (Q8) {
+                    copy_tile_scales(a, s_scale[st], id, s.ids.box() * box, box, boxes, it.h);
+                    cp_async_arrive(&s_full[st]);
+                }
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive_expect_tx(&s_full[st],
+                                          (uint32_t)boxes * box * DH * (Q8 ? 2 : 4));
                 __syncwarp();
                 if (lane < boxes) {
                     const int key = id * ps + (s.ids.box() + lane) * box % ps;
-                    const uint32_t d = ring_a + st * C::kStage + lane * box * 128;
+                    if constexpr (Q8) {
+                        const uint32_t d = ring_a + st * C::kStage + lane * box * DH;
+                        tma_load_3d(d, &mk, &s_full[st], 0, it.h, key);
+                        tma_load_3d(d + C::kV, &mv, &s_full[st], 0, it.h, key);
+                    } else {
+                        const uint32_t d = ring_a + st * C::kStage + lane * box * 128;
 #pragma unroll
-                    for (int c = 0; c < C::NB; ++c) {
-                        tma_load_3d(d + c * C::kBlk, &mk, &s_full[st], c * 64, it.h, key);
-                        tma_load_3d(d + (C::NB + c) * C::kBlk, &mv, &s_full[st], c * 64, it.h, key);
+                        for (int c = 0; c < C::NB; ++c) {
+                            tma_load_3d(d + c * C::kBlk, &mk, &s_full[st], c * 64, it.h, key);
+                            tma_load_3d(d + (C::NB + c) * C::kBlk, &mv, &s_full[st], c * 64, it.h,
+                                        key);
+                        }
                     }
                 }
                 s.ids.next(nb);
@@ -520,8 +566,9 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
     bool dead = false;
     const int kw = warp % KG, rg = warp / KG;  // key and row group
     // This lane's ldmatrix address in a K and in a V block: a step of 16 columns flips bits 5, 6.
-    const uint32_t k_lane = swz(kw * 16 * KB + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-    const uint32_t v_lane = swz(kw * 16 * KB + (lane & 15), lane >> 4);
+    [[maybe_unused]] const uint32_t k_lane =
+        swz(kw * 16 * KB + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    [[maybe_unused]] const uint32_t v_lane = swz(kw * 16 * KB + (lane & 15), lane >> 4);
     const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
     const float rescale = kRescaleLog2 / a.scale_log2;
     // What a thread does with the rows of row tile rt, the same for every item: the
@@ -558,11 +605,16 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
         if (n == 0) return leave();
         if (item.rt != rt_now) set_rows(item.rt);
         uint32_t qf[DH / 16][4];
+        [[maybe_unused]] float unit[2];  // of a row's scores, where Q is held to f16's range
+        if constexpr (Q8) {
+            load_queries8<DH>(qf, unit, qs + qb * C::kQ, C::MR * 128, rg * 16, a.scale_log2);
+        } else {
 #pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk) {
-            const int ch = kk * 2 + (lane >> 4);
-            ldsm4(qf[kk], qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
-                              swz(rg * 16 + (lane & 15), ch & 7));
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                const int ch = kk * 2 + (lane >> 4);
+                ldsm4(qf[kk], qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
+                                  swz(rg * 16 + (lane & 15), ch & 7));
+            }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_qempty[qb]);
@@ -592,110 +644,115 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
                 dead = true;  // no more waits: the rest runs through on what is there
             }
             bad |= s_bad[ring_at] != 0;
-            const uint32_t stage = ring_a + ring_at * C::kStage;
-            const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
-            const bool tail = key0 + 16 * KB > len;
-            if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
-                const int first = max(0, len - key0);
-                for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
-                    const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
-                    *reinterpret_cast<uint4 *>(ring + ring_at * C::kStage +
-                                               (C::NB + (ch >> 3)) * C::kBlk +
-                                               (kw * 16 * KB + r) * 128 +
-                                               (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+            if constexpr (Q8) {
+                tile8<DH, KB>(ring + ring_at * C::kStage, C::kV, s_scale[ring_at], kw, key0, len,
+                              least, see, qf, unit, m, limit, l2, o);
+            } else {
+                const uint32_t stage = ring_a + ring_at * C::kStage;
+                const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
+                const bool tail = key0 + 16 * KB > len;
+                if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
+                    const int first = max(0, len - key0);
+                    for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
+                        const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
+                        *reinterpret_cast<uint4 *>(ring + ring_at * C::kStage +
+                                                   (C::NB + (ch >> 3)) * C::kBlk +
+                                                   (kw * 16 * KB + r) * 128 +
+                                                   (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
-            }
-            float sc[2 * KB][4];
-#pragma unroll
-            for (int nt = 0; nt < 2 * KB; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk)
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) {
-                    uint32_t b[4];
-                    ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
-                    mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
-                    mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
-                }
-            if (key0 + 16 * KB > least) {  // some row does not see some of these keys
+                float sc[2 * KB][4];
 #pragma unroll
                 for (int nt = 0; nt < 2 * KB; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
-                            sc[nt][e] = -INFINITY;
-            }
-            float top[2];
+                    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
+                for (int kk = 0; kk < DH / 16; ++kk)
 #pragma unroll
-                for (int nt = 1; nt < 2 * KB; ++nt)
-                    top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
-            }
-            // Only when some score passes its row's limit are the row maxima needed. A row that
-            // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
-            if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+                    for (int kb = 0; kb < KB; ++kb) {
+                        uint32_t b[4];
+                        ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
+                        mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
+                        mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
+                    }
+                if (key0 + 16 * KB > least) {  // some row does not see some of these keys
+#pragma unroll
+                    for (int nt = 0; nt < 2 * KB; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
+                                sc[nt][e] = -INFINITY;
+                }
+                float top[2];
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
-                    if (!(top[p] > limit[p])) continue;
-                    const float f = ex2((m[p] - top[p]) * a.scale_log2);
-                    m[p] = top[p];
-                    limit[p] = top[p] + rescale;
-                    off[p] = -top[p] * a.scale_log2;
-                    l2[p] = f2_mul(l2[p], f2_make(f, f));
+                    top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
 #pragma unroll
-                    for (int d = 0; d < DH / 8; ++d) {
-                        o[d][2 * p] *= f;
-                        o[d][2 * p + 1] *= f;
+                    for (int nt = 1; nt < 2 * KB; ++nt)
+                        top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
+                }
+                // Only when some score passes its row's limit are the row maxima needed. A row that
+                // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
+                if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
+                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
+                        if (!(top[p] > limit[p])) continue;
+                        const float f = ex2((m[p] - top[p]) * a.scale_log2);
+                        m[p] = top[p];
+                        limit[p] = top[p] + rescale;
+                        off[p] = -top[p] * a.scale_log2;
+                        l2[p] = f2_mul(l2[p], f2_make(f, f));
+#pragma unroll
+                        for (int d = 0; d < DH / 8; ++d) {
+                            o[d][2 * p] *= f;
+                            o[d][2 * p + 1] *= f;
+                        }
                     }
                 }
-            }
-            uint32_t pf[KB][4];
+                uint32_t pf[KB][4];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const f32x2 off2 = f2_make(off[p], off[p]);
+                for (int p = 0; p < 2; ++p) {
+                    const f32x2 off2 = f2_make(off[p], off[p]);
 #pragma unroll
-                for (int nt = 0; nt < 2 * KB; ++nt) {
-                    float e0, e1;
-                    f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
-                    e0 = ex2(e0);
-                    e1 = ex2(e1);
-                    l2[p] = f2_add(l2[p], f2_make(e0, e1));
-                    // P enters the second product as bf16: 2^-8 relative a term at most.
-                    pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
-                }
-            }
-            // A draft that some row does not see: were its V not finite, a weight of 0 would
-            // not keep it from that row, so the block's product is made one by one.
-            bool plain = false;
-            if (key0 + 16 * KB > least) {
-                const unsigned char *vb = ring + ring_at * C::kStage + C::NB * C::kBlk;
-                const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
-                for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
-                    plain |= not_finite(*reinterpret_cast<const uint4 *>(
-                        vb + (x % (DH / 8) >> 3) * C::kBlk +
-                        swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
-                plain = __any_sync(~0u, plain);
-                if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
-            }
-            if (!plain) {
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                    for (int dd = 0; dd < DH / 16; ++dd) {
-                        uint32_t b[4];
-                        ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
-                        mma16816(o[2 * dd], pf[kb], b[0], b[1]);
-                        mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
+                    for (int nt = 0; nt < 2 * KB; ++nt) {
+                        float e0, e1;
+                        f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        l2[p] = f2_add(l2[p], f2_make(e0, e1));
+                        // P enters the second product as bf16: 2^-8 relative a term at most.
+                        pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
                     }
+                }
+                // A draft that some row does not see: were its V not finite, a weight of 0 would
+                // not keep it from that row, so the block's product is made one by one.
+                bool plain = false;
+                if (key0 + 16 * KB > least) {
+                    const unsigned char *vb = ring + ring_at * C::kStage + C::NB * C::kBlk;
+                    const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
+                    for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
+                        plain |= not_finite(*reinterpret_cast<const uint4 *>(
+                            vb + (x % (DH / 8) >> 3) * C::kBlk +
+                            swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
+                    plain = __any_sync(~0u, plain);
+                    if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
+                }
+                if (!plain) {
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int dd = 0; dd < DH / 16; ++dd) {
+                            uint32_t b[4];
+                            ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
+                            mma16816(o[2 * dd], pf[kb], b[0], b[1]);
+                            mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
+                        }
+                }
+                if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             }
-            if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_empty[ring_at]);
             if (++ring_at == ST) {
@@ -716,13 +773,24 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG>::kThreads, OwnCfg<DH, RG>::kCta
             l += __shfl_xor_sync(~0u, l, 1);
             l += __shfl_xor_sync(~0u, l, 2);
             if ((lane & 3) == 0) {
-                jm[kw * 32 + r] = m[p] * a.scale_log2;
+                jm[kw * 32 + r] = Q8 ? m[p] : m[p] * a.scale_log2;
                 jm[kw * 32 + 16 + r] = l;
             }
+            float *row = jo + (kw * 16 + r) * C::kOs;
+            if constexpr (Q8) {  // this thread's columns are DH / 4 in a row (see tile8)
 #pragma unroll
-            for (int d = 0; d < DH / 8; ++d)
-                *reinterpret_cast<float2 *>(jo + (kw * 16 + r) * C::kOs + d * 8 + (lane & 3) * 2) =
-                    make_float2(o[d][2 * p], o[d][2 * p + 1]);
+                for (int d = 0; d < DH / 4; d += 4) {
+                    constexpr int W = DH / 8;
+                    const int e = 2 * p + d / W;
+                    *reinterpret_cast<float4 *>(row + (lane & 3) * 2 * W + d) =
+                        make_float4(o[d % W][e], o[d % W + 1][e], o[d % W + 2][e], o[d % W + 3][e]);
+                }
+            } else {
+#pragma unroll
+                for (int d = 0; d < DH / 8; ++d)
+                    *reinterpret_cast<float2 *>(row + d * 8 + (lane & 3) * 2) =
+                        make_float2(o[d][2 * p], o[d][2 * p + 1]);
+            }
         }
         named_sync(1, 32 * C::kWarps);
         const bool whole = n == item.T && from == 0;  // nothing to join with
@@ -913,20 +981,22 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
 // ------------------------------------------------------------ host side
 
 // Pages [n_pages * page_size tokens, Hkv, Dh] in boxes of `keys` tokens of one
-// head, 64 columns, 128-byte swizzle.
+// head: 64 columns of bf16, 128-byte swizzle, or all columns of an 8-bit cache, swizzled
+// within their 64 or 128 bytes.
 static cudaError_t map_pages(CUtensorMap *m, const void *ptr, const PageTable &pt, int Hkv, int Dh,
-                             int keys) {
+                             int keys, bool q8) {
     EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)Dh, (cuuint64_t)Hkv,
                                 (cuuint64_t)pt.n_pages * pt.page_size};
-    const cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, (cuuint64_t)Hkv * Dh * 2};
-    const cuuint32_t box[3] = {64, 1, (cuuint32_t)keys};
-    const cuuint32_t es[3] = {1, 1, 1};
-    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
-                          strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t es = q8 ? 1 : 2, strides[2] = {Dh * es, (cuuint64_t)Hkv * Dh * es};
+    const cuuint32_t box[3] = {(cuuint32_t)(q8 ? Dh : 64), 1, (cuuint32_t)keys};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    const CUresult r =
+        fn(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+           const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           q8 && Dh == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1008,15 +1078,15 @@ static cudaError_t smem_opt_in(F kern, size_t bytes, std::atomic<unsigned long l
     return e;
 }
 
-template <int DH, int RG>
+template <int DH, int RG, bool Q8>
 static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                               int sms, int *grid, cudaStream_t stream) {
-    using C = OwnCfg<DH, RG>;
+    using C = OwnCfg<DH, RG, Q8>;
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = smem_opt_in(k_own<DH, RG>, C::kSmem, done);
+    const cudaError_t e = smem_opt_in(k_own<DH, RG, Q8>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     *grid = C::kCtas * sms < kMaxCtas ? C::kCtas * sms : kMaxCtas;
-    return launch_pdl(k_own<DH, RG>, dim3((unsigned)*grid), dim3(C::kThreads), C::kSmem, stream, a,
+    return launch_pdl(k_own<DH, RG, Q8>, dim3((unsigned)*grid), dim3(C::kThreads), C::kSmem, stream, a,
                       mk, mv);
 }
 
@@ -1031,10 +1101,15 @@ static cudaError_t launch_prefix(const PrefixArgs &x, const CUtensorMap &mq, con
                       mq, mk, mv);
 }
 
+size_t attention8_workspace_bytes(const AttnShape &s, int page_size) {
+    return attention_workspace_bytes(s) + 2 * unpacked_bytes(s, page_size);
+}
+
 cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
-                                    const void *k_pages, const void *v_pages, const PageTable &pt,
-                                    const int32_t *slots, float scale, void *out,
-                                    void *workspace, int sm_count, cudaStream_t stream) {
+                                    const void *k_pages, const void *v_pages,
+                                    const Scales8 *scales, const PageTable &pt,
+                                    const int32_t *slots, float scale, void *out, void *workspace,
+                                    int sm_count, cudaStream_t stream) {
     PrefixArgs x = prefix_plan(s, pt.page_size, sm_count);
     AttnArgs &a = x.a;
     a.q = (const bf16 *)q;
@@ -1051,19 +1126,34 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.cum = (int64_t *)workspace;
     a.own_part = (float *)((char *)workspace + cum_bytes(s));
     x.part = a.own_part + own_part_floats(s);
+    const bool q8 = scales != nullptr;
+    if (q8) a.s8 = *scales;
+    const int kt = q8 ? (s.Dh == 64 ? OwnCfg<64, 1, true>::KT : OwnCfg<128, 1, true>::KT)
+                      : OwnCfg<64, 1, false>::KT;
+    const int own_box = pt.page_size < kt ? pt.page_size : kt;
     CUtensorMap mk, mv;
-    const int own_box = pt.page_size < kKT ? pt.page_size : kKT;
-    cudaError_t e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, own_box);
+    cudaError_t e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, own_box, q8);
     if (e != cudaSuccess) return e;
-    e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, own_box);
+    e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, own_box, q8);
     if (e != cudaSuccess) return e;
     if (x.P > 0) {
         CUtensorMap mq, pk = mk, pv = mv;
         const int box = pt.page_size < kPK ? pt.page_size : kPK;
-        if (box != own_box) {
-            e = map_pages(&pk, k_pages, pt, s.Hkv, s.Dh, box);
+        PageTable from = pt;
+        if (q8) {  // the prefix as bf16 pages in the workspace
+            bf16 *k16 = (bf16 *)((char *)workspace + attention_workspace_bytes(s));
+            bf16 *v16 = k16 + unpacked_bytes(s, pt.page_size) / 2;
+            e = launch_unpack(a, s, k_pages, v_pages, k16, v16, sm_count, stream);
             if (e != cudaSuccess) return e;
-            e = map_pages(&pv, v_pages, pt, s.Hkv, s.Dh, box);
+            x.packed = 1;
+            from.n_pages = s.shared_pages;
+            k_pages = k16;
+            v_pages = v16;
+        }
+        if (q8 || box != own_box) {
+            e = map_pages(&pk, k_pages, from, s.Hkv, s.Dh, box, false);
+            if (e != cudaSuccess) return e;
+            e = map_pages(&pv, v_pages, from, s.Hkv, s.Dh, box, false);
             if (e != cudaSuccess) return e;
         }
         e = map_queries(&mq, x, s);
@@ -1075,12 +1165,11 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     const int MR = own_rows(s);
     const int sms = a.beside ? sm_count - x.n_cta : sm_count;
     int grid = 0;
-    if (s.Dh == 64)
-        e = MR == 16 ? launch_own<64, 1>(a, mk, mv, sms, &grid, stream)
-                     : launch_own<64, 2>(a, mk, mv, sms, &grid, stream);
-    else
-        e = MR == 16 ? launch_own<128, 1>(a, mk, mv, sms, &grid, stream)
-                     : launch_own<128, 2>(a, mk, mv, sms, &grid, stream);
+    const auto own = q8 ? (s.Dh == 64 ? (MR == 16 ? launch_own<64, 1, true> : launch_own<64, 2, true>)
+                                      : (MR == 16 ? launch_own<128, 1, true> : launch_own<128, 2, true>))
+                        : (s.Dh == 64 ? (MR == 16 ? launch_own<64, 1, false> : launch_own<64, 2, false>)
+                                      : (MR == 16 ? launch_own<128, 1, false> : launch_own<128, 2, false>));
+    e = own(a, mk, mv, sms, &grid, stream);
     if (e != cudaSuccess) return e;
     // With few rows all lanes of a warp share one: a whole step over two streams of 30-40
     // thousand tokens takes 39 us so, 45 with Dh / 8 lanes a row. With many there is work

@@ -45,6 +45,7 @@ struct PrefixArgs {
     int T;          // units of an item: key tiles, or pairs of them with split
     int64_t U;      // units of the call
     int n_cta;
+    int packed;     // 1: K and V are the prefix alone, in order (an 8-bit cache's, unpacked)
     float *part;    // [2 (items + CTAs)] parts of 128 rows: O [128][Dh], m [128], l [128]
 };
 
@@ -285,7 +286,8 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             }
             __syncwarp();
             if (lane < boxes) {
-                const int key = id * ps + (ids.box() + lane) * box % ps;
+                const int at = (ids.box() + lane) * box;
+                const int key = x.packed ? at : id * ps + at % ps;
 #pragma unroll
                 for (int c = 0; c < C::NB; ++c)
                     tma_load_3d(dst + c * C::kBlk + lane * box * 128, m, &full[s], c * 64, h, key);

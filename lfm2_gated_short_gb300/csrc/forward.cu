@@ -707,7 +707,8 @@ cudaError_t read_and_clear_error(cudaStream_t stream, unsigned int *code) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     for (auto take : {take_error_here, take_error_backward, take_error_slots, take_error_proj,
-                      take_error_pages, take_error_draft, take_error_attention}) {
+                      take_error_pages, take_error_draft, take_error_attention,
+                      take_error_cache8, take_error_rope}) {
         e = take(stream, sum);
         if (e != cudaSuccess) return e;
     }
@@ -727,12 +728,14 @@ cudaError_t bounds_install(int unit, const BoundsRegion *r, int n, cudaStream_t 
         case kUnitSlots: return bounds_install_slots(r, n, s);
         case kUnitPages: return bounds_install_pages(r, n, s);
         case kUnitDraft: return bounds_install_draft(r, n, s);
+        case kUnitCache8: return bounds_install_cache8(r, n, s);
+        case kUnitRope: return bounds_install_rope(r, n, s);
         default: return bounds_install_attention(r, n, s);
     }
 }
 
 cudaError_t bounds_take_first_bad(cudaStream_t s, unsigned long long *addr) {
-    unsigned long long a[7] = {0, 0, 0, 0, 0, 0, 0};
+    unsigned long long a[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
     cudaError_t e = bounds_take_first_bad_here(s, &a[0]);
     if (e == cudaSuccess) e = bounds_take_backward(s, &a[1]);
     if (e == cudaSuccess) e = bounds_take_proj(s, &a[2]);
@@ -740,9 +743,11 @@ cudaError_t bounds_take_first_bad(cudaStream_t s, unsigned long long *addr) {
     if (e == cudaSuccess) e = bounds_take_pages(s, &a[4]);
     if (e == cudaSuccess) e = bounds_take_draft(s, &a[5]);
     if (e == cudaSuccess) e = bounds_take_attention(s, &a[6]);
+    if (e == cudaSuccess) e = bounds_take_cache8(s, &a[7]);
+    if (e == cudaSuccess) e = bounds_take_rope(s, &a[8]);
     if (e != cudaSuccess) return e;
     *addr = 0;
-    for (int i = 0; i < 7 && *addr == 0; ++i) *addr = a[i] & ~1ull;  // bit 0 marks "set"
+    for (int i = 0; i < 9 && *addr == 0; ++i) *addr = a[i] & ~1ull;  // bit 0 marks "set"
     return cudaSuccess;
 }
 #endif

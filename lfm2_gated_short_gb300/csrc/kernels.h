@@ -107,6 +107,8 @@ struct PagePools {
     void *k, *v;
     int L;
     int64_t token_bytes;
+    float *k_scales, *v_scales;  // of an 8-bit cache: page_scales a page and layer
+    int page_scales;             // 0: none
 };
 size_t pages_workspace_bytes(int n_pages, int n);
 cudaError_t launch_pages_resize(const PageTable &pt, const int32_t *slots, const int32_t *new_lens,
@@ -122,6 +124,36 @@ cudaError_t launch_pages_append(const PageTable &pt, const void *k, int64_t k_st
                                 int D, const PagePools &pools, cudaStream_t stream);
 cudaError_t take_error_pages(cudaStream_t stream, unsigned int *sum);
 
+// The 8-bit cache (cache8.cu): pools of e4m3 codes, [n_pages, page_size, Hkv, Dh], and scales,
+// [n_pages, page_size / block, Hkv].
+struct Cache8 {
+    void *k, *v;
+    float *k_scales, *v_scales;
+    int Hkv, Dh, block;
+};
+cudaError_t launch_append8(int dtype, const PageTable &pt, const void *k, int64_t k_stride,
+                           const void *v, int64_t v_stride, const int32_t *slots, int N, int D,
+                           const Cache8 &c, cudaStream_t stream);
+cudaError_t launch_read8(int dtype, const PageTable &pt, const int32_t *slots, const int32_t *cu,
+                         const int32_t *starts, int N, int64_t rows, const Cache8 &c, void *k,
+                         void *v, int sm_count, cudaStream_t stream);
+cudaError_t take_error_cache8(cudaStream_t stream, unsigned int *sum);
+
+// Rotary positions (rope.cu). Strides in elements; positions, or D newest tokens of slots.
+struct RopeArgs {
+    const void *q, *k;
+    void *q_out, *k_out;
+    int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+    const double *freqs;
+    const int32_t *positions, *lens, *slots;
+    int64_t T;
+    int Hq, Hkv, Dh, R, D, n_slots;
+    float amplitude;
+    int half_layout, inverse, copy;  // copy: the values behind R, from in to out
+};
+cudaError_t launch_rope(int dtype, const RopeArgs &a, int sm_count, cudaStream_t stream);
+cudaError_t take_error_rope(cudaStream_t stream, unsigned int *sum);
+
 // Draft acceptance (draft.cu). draft NULL: the drafts were certain.
 cudaError_t launch_draft_accept(int dtype, int V, int N, int D, const void *target,
                                 int64_t target_stride, const void *draft, int64_t draft_stride,
@@ -130,15 +162,22 @@ cudaError_t launch_draft_accept(int dtype, int V, int N, int D, const void *targ
                                 int sm_count, cudaStream_t stream);
 cudaError_t take_error_draft(cudaStream_t stream, unsigned int *sum);
 
-// Attention over the paged cache (attention.cu), bf16.
+// Attention over the paged cache (attention.cu), bf16, or e4m3 codes with scales of 2^block_log2
+// tokens and a head (NULL: bf16).
 struct AttnShape {
     int Hq, Hkv, Dh, N, D, shared_pages;
 };
+struct Scales8 {
+    const float *k, *v;
+    int block_log2;
+};
 size_t attention_workspace_bytes(const AttnShape &s);
+size_t attention8_workspace_bytes(const AttnShape &s, int page_size);
 cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
-                                    const void *k_pages, const void *v_pages, const PageTable &pt,
-                                    const int32_t *slots, float scale, void *out,
-                                    void *workspace, int sm_count, cudaStream_t stream);
+                                    const void *k_pages, const void *v_pages,
+                                    const Scales8 *scales, const PageTable &pt,
+                                    const int32_t *slots, float scale, void *out, void *workspace,
+                                    int sm_count, cudaStream_t stream);
 cudaError_t take_error_attention(cudaStream_t stream, unsigned int *sum);
 
 // Read and clear the device error word of the current device (synchronous
@@ -163,7 +202,9 @@ enum BoundsUnit {
     kUnitSlots = 3,
     kUnitPages = 4,
     kUnitDraft = 5,
-    kUnitAttention = 6
+    kUnitAttention = 6,
+    kUnitCache8 = 7,
+    kUnitRope = 8
 };
 cudaError_t bounds_install(int unit, const BoundsRegion *r, int n, cudaStream_t stream);
 // The first address any unit refused since the last call (0 when none), cleared.
@@ -174,12 +215,16 @@ cudaError_t bounds_install_slots(const BoundsRegion *r, int n, cudaStream_t stre
 cudaError_t bounds_install_pages(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_draft(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_attention(const BoundsRegion *r, int n, cudaStream_t stream);
+cudaError_t bounds_install_cache8(const BoundsRegion *r, int n, cudaStream_t stream);
+cudaError_t bounds_install_rope(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_take_backward(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_proj(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_slots(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_pages(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_draft(cudaStream_t stream, unsigned long long *addr);
 cudaError_t bounds_take_attention(cudaStream_t stream, unsigned long long *addr);
+cudaError_t bounds_take_cache8(cudaStream_t stream, unsigned long long *addr);
+cudaError_t bounds_take_rope(cudaStream_t stream, unsigned long long *addr);
 #endif
 
 }  // namespace sc

@@ -253,6 +253,17 @@ __device__ __forceinline__ void copy_pages(const PageWork &w, int n, const PageT
         for (int k = 0; k < kWords; ++k)
             if (i0 + 32 * k < q) st_plain(to + i0 + 32 * k, v[k]);
     }
+    // A page's scales go whole: those of blocks without a copied token are nobody's.
+    if (pools.page_scales == 0) return;
+    for (int64_t u = worker; u < (int64_t)n * 2 * pools.L; u += workers) {
+        const uint32_t ci = (uint32_t)(u / (2 * pools.L)), lp = (uint32_t)(u - (int64_t)ci * 2 * pools.L);
+        const int4 c = ld_shared_word(reinterpret_cast<const int4 *>(w.copies + ci));
+        float *base = (lp & 1 ? pools.v_scales : pools.k_scales) +
+                      (int64_t)(lp >> 1) * pt.n_pages * pools.page_scales;
+        const float *from = base + (int64_t)c.x * pools.page_scales;
+        float *to = base + (int64_t)c.y * pools.page_scales;
+        for (int i = lane; i < pools.page_scales; i += 32) gst(to + i, gld(from + i));
+    }
 }
 
 // The end of a resize or fork: the number of copies for the copy kernel, or the copies

@@ -1,0 +1,221 @@
+// rope.cu -- rotary positions: pairs of a head's first R values turned by position times
+// frequency, and the gradient, the same turn backwards.
+//
+//   a' = A (a cos t - b sin t),  b' = A (b cos t + a sin t),  t = p f_i
+// Pair i is (x_i, x_{i + R/2}) or (x_{2i}, x_{2i+1}).
+//
+// The angle is counted in turns as a 64-bit fraction: F_i = f_i / 2 pi mod 1 in units of
+// 2^-64, and p F_i mod 2^64 is exact for every position, so that a far position's angle
+// is as good as a near one's (an fp32 product of 10^6 radians is off by up to 0.03). Sines and
+// cosines come from the fraction's distance to the nearest quarter turn.
+//
+// A tile is a few tokens: its sines and cosines are computed once, for all heads, into
+// shared memory; the rest streams the heads through registers, bound by their bytes.
+#include <cuda_bf16.h>
+
+#include "common.cuh"
+#include "errors.cuh"
+#include "kernels.h"
+#include "launch.h"
+#include "shortconv.h"
+
+namespace sc {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTokens = 8;     // of a tile, at most
+
+// Turns a position of f radians a position, mod 1, in units of 2^-64: f = m 2^(e - 1075)
+// times floor(2^64 / 2 pi), whose relative error is below 2^-61.
+__device__ __forceinline__ uint64_t turns_of(double f) {
+    const uint64_t b = (uint64_t)__double_as_longlong(f);
+    const int e = (int)(b >> 52) & 0x7FF;
+    if (e == 0 || e == 0x7FF) return 0;
+    const uint64_t m = (b & 0xFFFFFFFFFFFFFull) | 1ull << 52;
+    constexpr uint64_t kInv2Pi = 0x28BE60DB9391054Aull;
+    const uint64_t lo = m * kInv2Pi, hi = __umul64hi(m, kInv2Pi);
+    const int s = 1075 - e;  // the product's shift to the right
+    uint64_t t;
+    if (s <= 0)
+        t = s > -64 ? lo << -s : 0;
+    else if (s < 64)
+        t = hi << (64 - s) | lo >> s;
+    else
+        t = s < 128 ? hi >> (s - 64) : 0;
+    return (int64_t)b < 0 ? 0 - t : t;
+}
+
+// (cos, sin) of a 64-bit fraction of a turn.
+__device__ __forceinline__ float2 cos_sin(uint64_t turns) {
+    const uint64_t q = (turns + (1ull << 61)) >> 62;  // nearest quarter
+    const int64_t rest = (int64_t)(turns - (q << 62));  // within an eighth of a turn
+    float s, c;
+    sincospif((float)rest * 0x1p-63f, &s, &c);
+    const float x = q & 1 ? s : c, y = q & 1 ? c : s;
+    return make_float2(((q + 1) & 2) ? -x : x, (q & 2) ? -y : y);
+}
+
+// VP values as fp32, read and written as one access where VP fills 16 bytes (or 4).
+template <typename T, int VP>
+struct Part {
+    float f[VP];
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VP * sizeof(T) == 16) {
+            const uint4 q = ld_plain(p);
+            if constexpr (sizeof(T) == 2) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w;
+                    f[2 * e] = bf16_lo(w);
+                    f[2 * e + 1] = bf16_hi(w);
+                }
+            } else {
+                f[0] = __uint_as_float(q.x);
+                f[1] = __uint_as_float(q.y);
+                f[2] = __uint_as_float(q.z);
+                f[3] = __uint_as_float(q.w);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < VP; ++e) f[e] = (float)gld(p + e);
+        }
+    }
+    __device__ __forceinline__ void store(T *p) const {
+        if constexpr (VP * sizeof(T) == 16) {
+            uint4 q;
+            if constexpr (sizeof(T) == 2)
+                q = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                               pack_bf16(f[6], f[7]));
+            else
+                q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                               __float_as_uint(f[3]));
+            st_plain(p, q);
+        } else {
+#pragma unroll
+            for (int e = 0; e < VP; ++e) gst(p + e, (T)f[e]);
+        }
+    }
+};
+
+// Position of row t, or INT64_MIN for a row that is left alone.
+__device__ __forceinline__ int64_t position_of(const RopeArgs &a, int64_t t, bool report) {
+    if (a.positions != nullptr) return gld(a.positions + t);
+    const int64_t i = t / a.D;
+    const int j = (int)(t - i * a.D), slot = gld(a.slots + i);
+    if (slot < 0 || slot >= a.n_slots) {
+        if (report) raise_error(SC_DEV_BAD_SLOT);
+        return INT64_MIN;
+    }
+    const int64_t p = (int64_t)gld(a.lens + slot) - a.D + j;
+    if (p < 0) {
+        if (report) raise_error(SC_DEV_BAD_LENGTH);
+        return INT64_MIN;
+    }
+    return p;
+}
+
+template <typename T, int VP, bool HALF>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, int tokens) {
+    extern __shared__ float s_turn[];  // [tokens][cos of the pairs, sin of the pairs]
+    __shared__ bool s_live[kRopeTokens];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int half = a.R / 2;
+    const int64_t t0 = (int64_t)blockIdx.x * tokens;
+    const int here = (int)min((int64_t)tokens, a.T - t0);
+    for (int x = threadIdx.x; x < here * half; x += kRopeThreads) {
+        const int t = x / half, i = x - t * half;
+        const int64_t p = position_of(a, t0 + t, i == 0);
+        if (i == 0) s_live[t] = p != INT64_MIN;
+        float2 cs = cos_sin((uint64_t)p * turns_of(gld(a.freqs + i)));
+        s_turn[t * a.R + i] = cs.x * a.amplitude;
+        s_turn[t * a.R + half + i] = (a.inverse ? -cs.y : cs.y) * a.amplitude;
+    }
+    __syncthreads();
+    // Items: VP pairs of a head, then VP of the values behind them.
+    const int turned = half / VP, per = turned + (a.copy ? (a.Dh - a.R) / VP : 0);
+    const int heads = a.Hq + a.Hkv;
+    for (int x = threadIdx.x; x < here * heads * per; x += kRopeThreads) {
+        const int t = x / (heads * per), y = x - t * heads * per, hd = y / per, c = y - hd * per;
+        if (!s_live[t]) continue;
+        const bool is_k = hd >= a.Hq;
+        const int64_t row = t0 + t, at = (int64_t)(is_k ? hd - a.Hq : hd) * a.Dh;
+        const T *from = (const T *)(is_k ? a.k : a.q) + row * (is_k ? a.k_stride : a.q_stride) + at;
+        T *to = (T *)(is_k ? a.k_out : a.q_out) +
+                row * (is_k ? a.k_out_stride : a.q_out_stride) + at;
+        Part<T, VP> u, w;
+        if (c >= turned) {
+            const int o = a.R + (c - turned) * VP;
+            u.load(from + o);
+            u.store(to + o);
+            continue;
+        }
+        const float *cs = s_turn + t * a.R + c * VP, *sn = cs + half;
+        const int first = HALF ? c * VP : 2 * c * VP, second = HALF ? first + half : first + VP;
+        u.load(from + first);
+        w.load(from + second);
+        Part<T, VP> ru, rw;
+#pragma unroll
+        for (int e = 0; e < VP; ++e) {
+            if constexpr (HALF) {
+                ru.f[e] = u.f[e] * cs[e] - w.f[e] * sn[e];
+                rw.f[e] = w.f[e] * cs[e] + u.f[e] * sn[e];
+            } else {
+                const float x0 = 2 * e < VP ? u.f[(2 * e) % VP] : w.f[(2 * e) % VP];
+                const float x1 = 2 * e + 1 < VP ? u.f[(2 * e + 1) % VP] : w.f[(2 * e + 1) % VP];
+                const float y0 = x0 * cs[e] - x1 * sn[e], y1 = x1 * cs[e] + x0 * sn[e];
+                if (2 * e < VP) ru.f[(2 * e) % VP] = y0;
+                else rw.f[(2 * e) % VP] = y0;
+                if (2 * e + 1 < VP) ru.f[(2 * e + 1) % VP] = y1;
+                else rw.f[(2 * e + 1) % VP] = y1;
+            }
+        }
+        ru.store(to + first);
+        rw.store(to + second);
+    }
+}
+
+// ------------------------------------------------------------ host side
+
+template <typename T, int VP>
+static cudaError_t launch_rope_vp(const RopeArgs &a, int tokens, cudaStream_t stream) {
+    const dim3 grid((unsigned)((a.T + tokens - 1) / tokens));
+    const size_t smem = (size_t)tokens * a.R * 4;
+    return a.half_layout
+               ? launch_pdl(k_rope<T, VP, true>, grid, dim3(kRopeThreads), smem, stream, a, tokens)
+               : launch_pdl(k_rope<T, VP, false>, grid, dim3(kRopeThreads), smem, stream, a, tokens);
+}
+
+template <typename T>
+static cudaError_t launch_rope_t(const RopeArgs &a, int tokens, cudaStream_t stream) {
+    // 16-byte accesses where every row, head and half starts on 16 bytes.
+    constexpr int kFull = 16 / (int)sizeof(T);
+    auto fits = [](const void *p, int64_t stride) {
+        return ((uintptr_t)p & 15) == 0 && stride % kFull == 0;
+    };
+    const bool full = a.R / 2 % kFull == 0 && a.Dh % kFull == 0 && fits(a.q, a.q_stride) &&
+                      fits(a.q_out, a.q_out_stride) && fits(a.k, a.k_stride) &&
+                      fits(a.k_out, a.k_out_stride);
+    return full ? launch_rope_vp<T, kFull>(a, tokens, stream) : launch_rope_vp<T, 1>(a, tokens, stream);
+}
+
+cudaError_t launch_rope(int dtype, const RopeArgs &a, int sm_count, cudaStream_t stream) {
+    int tokens = kRopeTokens;
+    while (tokens > 1 && a.T < (int64_t)tokens * 4 * sm_count) tokens >>= 1;
+    return dtype == SC_BF16 ? launch_rope_t<__nv_bfloat16>(a, tokens, stream)
+                            : launch_rope_t<float>(a, tokens, stream);
+}
+
+cudaError_t take_error_rope(cudaStream_t stream, unsigned int *sum) {
+    return take_error_here(stream, sum);
+}
+
+#ifdef SC_BOUNDS_CHECK
+cudaError_t bounds_install_rope(const BoundsRegion *r, int n, cudaStream_t stream) {
+    return bounds_install_here(r, n, stream);
+}
+cudaError_t bounds_take_rope(cudaStream_t stream, unsigned long long *addr) {
+    return bounds_take_first_bad_here(stream, addr);
+}
+#endif
+
+}  // namespace sc
