@@ -26,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include <limits.h>
+#include <stdlib.h>
 
 #include <atomic>
 
@@ -258,12 +259,15 @@ __device__ __forceinline__ void product_one_by_one(float (&o)[DH / 8][4],
 // end an item sooner; 32 rows of 64 columns are bound by the warps' own latency,
 // and 32 keys a warp keep more of their work independent. CTAs of an SM and
 // stages are what shared memory and registers allow.
-template <int DH, int RG, bool Q8>
+template <int DH, int MR_, int HG>
 struct OwnCfg {
-    static constexpr int MR = 16 * RG;
+    struct Scales {};
+    static constexpr int kDh = DH;
+    static constexpr int MR = MR_, RG = MR / 16;              // rows, and row groups
     static constexpr int KT = 64;                             // keys of a tile
     static constexpr int KG = DH == 64 && RG == 2 ? 2 : 4;    // key groups
     static constexpr int KB = KT / 16 / KG;                   // blocks of 16 keys of a warp
+    static constexpr int kHeads = 1;                          // kv heads of an item
     static constexpr int kWarps = KG * RG;                    // consumer warps
     static constexpr int kThreads = 32 * (kWarps + 1);        // and the producer
     static constexpr int NB = DH / 64;                        // 64-wide column blocks
@@ -272,33 +276,23 @@ struct OwnCfg {
     static constexpr int kCtas = DH == 64 ? 3 : (RG == 1 ? 2 : 1);
     static constexpr int kStages = DH == 64 ? 3 : (RG == 1 ? 2 : 4);
     static constexpr int kQBufs = DH == 64 && RG == 2 ? 1 : 2;  // items described ahead
-    static constexpr uint32_t kQ = MR * 128 * NB;
+    static constexpr uint32_t kQ = MR * 128 * NB;             // queries of a head
     static constexpr int kOs = DH + 4;                        // floats of a row to join
     static constexpr uint32_t kJoin = KG * MR * (kOs + 2) * 4;  // O, m, l of each key group
     static constexpr size_t kSmem = 1024 + kStages * kStage + kQBufs * kQ + kJoin;
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part
 };
 
-// The 8-bit cache's tiles have half the bytes a key: twice the keys a tile.
-template <int DH, int RG>
-struct OwnCfg<DH, RG, true> {
-    static constexpr int MR = 16 * RG;
-    static constexpr int KT = DH == 64 ? 128 : 64;
-    static constexpr int KG = 4;
-    static constexpr int KB = KT / 16 / KG;
-    static constexpr int kWarps = KG * RG;
-    static constexpr int kThreads = 32 * (kWarps + 1);
-    static constexpr int NB = DH / 64;                        // 64-wide column blocks of Q
-    static constexpr uint32_t kV = KT * DH;                   // the tile's V behind its K
-    static constexpr uint32_t kStage = 2 * kV;                // 16 KB
-    static constexpr int kCtas = DH == 64 ? 4 - RG : 3 - RG;
-    static constexpr int kStages = 3;
-    static constexpr int kQBufs = 2;
-    static constexpr uint32_t kQ = MR * 128 * NB;
-    static constexpr int kOs = DH + 4;
-    static constexpr uint32_t kJoin = KG * MR * (kOs + 2) * 4;
-    static constexpr size_t kSmem = 1024 + kStages * kStage + kQBufs * kQ + kJoin;
-    static constexpr int kSlot = MR * (DH + 2);
+// What the producer and the consumers of a CTA share.
+template <typename C>
+struct OwnSmem {
+    unsigned char *ring;  // kStages tiles
+    uint32_t ring_a, qs_a;
+    float *join;
+    uint64_t *full, *empty, *qfull, *qempty;
+    OwnItem *item;
+    int *bad;
+    typename C::Scales *scales;  // of an 8-bit cache's tiles
 };
 
 }  // namespace sc
@@ -307,19 +301,277 @@ struct OwnCfg<DH, RG, true> {
 
 namespace sc {
 
-template <int DH, int RG, bool Q8>
-__global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q8>::kCtas)
+// A consumer warp's part over a bf16 cache.
+template <typename C>
+__device__ __forceinline__ void consume16(const AttnArgs &a, int rows, int per,
+                                          const OwnSmem<C> &s) {
+    constexpr int DH = C::kDh, ST = C::kStages, KG = C::KG, KB = C::KB, kKT = C::KT, QB = C::kQBufs;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint32_t ring_at = 0, ring_phase = 0;
+    bool dead = false;
+    const int kw = warp % KG, rg = warp / KG;  // key and row group
+    // This lane's ldmatrix address in a K and in a V block: a step of 16 columns flips bits 5, 6.
+    const uint32_t k_lane = swz(kw * 16 * KB + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    const uint32_t v_lane = swz(kw * 16 * KB + (lane & 15), lane >> 4);
+    const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
+    const float rescale = kRescaleLog2 / a.scale_log2;
+    // What a thread does with the rows of row tile rt, the same for every item: the
+    // tokens of the two rows it computes, the output rows it writes chunks of (counted from the
+    // sequence's first row of the kv head, -1 past the item's rows; rows, since the D Hq Dh
+    // elements of one sequence may pass 2^31).
+    constexpr int kOn = 16 * DH / 4 / (32 * KG);
+    const int gt = kw * 32 + lane;  // thread of the row group
+    int rt_now = -1, row_j[2], o_row[kOn];
+    auto set_rows = [&](int rt) {
+        rt_now = rt;
+        const int r0 = rt * C::MR;
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int rr = r0 + rg * 16 + p * 8 + (lane >> 2);
+            row_j[p] = rr < rows ? rr / a.G : INT_MIN / 2;
+        }
+#pragma unroll
+        for (int k = 0; k < kOn; ++k) {
+            const int rr = r0 + rg * 16 + (gt + k * 32 * KG) / (DH / 4);
+            o_row[k] = rr < rows ? rr / a.G * a.Hkv * a.G + rr % a.G : -1;
+        }
+    };
+    for (uint32_t items = 0;; ++items) {
+        const uint32_t qb = items % QB;
+        const bool ready = !dead && mbar_wait_bounded(&s.qfull[qb], (items / QB) & 1u);
+        // The warps go on together or not at all: none waits at a barrier the others left.
+        if (named_or(1, 32 * C::kWarps, !ready)) {
+            if (!ready && !dead) raise_error(SC_DEV_TIMEOUT);
+            return;
+        }
+        const OwnItem item = s.item[qb];
+        const int i = item.i, len = item.len, h = item.h, t0 = item.t0, n = item.n;
+        if (n == 0) return;
+        if (item.rt != rt_now) set_rows(item.rt);
+        uint32_t qf[DH / 16][4];
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk) {
+                const int ch = kk * 2 + (lane >> 4);
+                ldsm4(qf[kk], s.qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
+                                  swz(rg * 16 + (lane & 15), ch & 7));
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.qempty[qb]);
+        // A row's running maximum m (of the scores before scaling), the score that moves
+        // it, and its offset -m scale; the sums of its weights in pairs.
+        int see[2];
+        float m[2], limit[2], off[2], o[DH / 8][4];
+        f32x2 l2[2];
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            see[p] = len - a.D + 1 + row_j[p];  // below zero for a row past the item's
+            m[p] = limit[p] = -INFINITY;
+            off[p] = 0.0f;
+            l2[p] = f2_make(0.0f, 0.0f);
+        }
+        const int least = len - a.D + 1;  // keys that every row of the sequence sees
+#pragma unroll
+        for (int d = 0; d < DH / 8; ++d)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
+        bool bad = false;
+        const int from = prefix_keys(a, len);
+        int key0 = from + t0 * kKT + kw * 16 * KB;
+        for (int t = 0; t < n; ++t, key0 += kKT) {
+            if (!dead && !mbar_wait_bounded(&s.full[ring_at], ring_phase)) {
+                raise_error(SC_DEV_TIMEOUT);
+                dead = true;  // no more waits: the rest runs through on what is there
+            }
+            bad |= s.bad[ring_at] != 0;
+                const uint32_t stage = s.ring_a + ring_at * C::kStage;
+                const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
+                const bool tail = key0 + 16 * KB > len;
+                if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
+                    const int first = max(0, len - key0);
+                    for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
+                        const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
+                        *reinterpret_cast<uint4 *>(s.ring + ring_at * C::kStage +
+                                                   (C::NB + (ch >> 3)) * C::kBlk +
+                                                   (kw * 16 * KB + r) * 128 +
+                                                   (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    __syncwarp();
+                }
+                float sc[2 * KB][4];
+#pragma unroll
+                for (int nt = 0; nt < 2 * KB; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb) {
+                        uint32_t b[4];
+                        ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
+                        mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
+                        mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
+                    }
+                if (key0 + 16 * KB > least) {  // some row does not see some of these keys
+#pragma unroll
+                    for (int nt = 0; nt < 2 * KB; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
+                                sc[nt][e] = -INFINITY;
+                }
+                float top[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
+#pragma unroll
+                    for (int nt = 1; nt < 2 * KB; ++nt)
+                        top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
+                }
+                // Only when some score passes its row's limit are the row maxima needed. A row that
+                // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
+                if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
+                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
+                        if (!(top[p] > limit[p])) continue;
+                        const float f = ex2((m[p] - top[p]) * a.scale_log2);
+                        m[p] = top[p];
+                        limit[p] = top[p] + rescale;
+                        off[p] = -top[p] * a.scale_log2;
+                        l2[p] = f2_mul(l2[p], f2_make(f, f));
+#pragma unroll
+                        for (int d = 0; d < DH / 8; ++d) {
+                            o[d][2 * p] *= f;
+                            o[d][2 * p + 1] *= f;
+                        }
+                    }
+                }
+                uint32_t pf[KB][4];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const f32x2 off2 = f2_make(off[p], off[p]);
+#pragma unroll
+                    for (int nt = 0; nt < 2 * KB; ++nt) {
+                        float e0, e1;
+                        f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
+                        e0 = ex2(e0);
+                        e1 = ex2(e1);
+                        l2[p] = f2_add(l2[p], f2_make(e0, e1));
+                        // P enters the second product as bf16: 2^-8 relative a term at most.
+                        pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
+                    }
+                }
+                // A draft that some row does not see: were its V not finite, a weight of 0 would
+                // not keep it from that row, so the block's product is made one by one.
+                bool plain = false;
+                if (key0 + 16 * KB > least) {
+                    const unsigned char *vb = s.ring + ring_at * C::kStage + C::NB * C::kBlk;
+                    const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
+                    for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
+                        plain |= not_finite(*reinterpret_cast<const uint4 *>(
+                            vb + (x % (DH / 8) >> 3) * C::kBlk +
+                            swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
+                    plain = __any_sync(~0u, plain);
+                    if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
+                }
+                if (!plain) {
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                        for (int dd = 0; dd < DH / 16; ++dd) {
+                            uint32_t b[4];
+                            ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
+                            mma16816(o[2 * dd], pf[kb], b[0], b[1]);
+                            mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
+                        }
+                }
+                if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.empty[ring_at]);
+            if (++ring_at == ST) {
+                ring_at = 0;
+                ring_phase ^= 1u;
+            }
+        }
+        // Join the key warps: each leaves its m, l and O, and a thread joins and writes
+        // four columns of a row. (The next join comes after the next item's barrier.)
+        float *jo = s.join + rg * KG * 16 * C::kOs;  // [key group][16][kOs]
+        float *jm = s.join + KG * C::MR * C::kOs + rg * KG * 32;  // [key group][m 16, l 16]
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+            const int r = p * 8 + (lane >> 2);
+            float l, l1;
+            f2_split(l2[p], l, l1);
+            l += l1;
+            l += __shfl_xor_sync(~0u, l, 1);
+            l += __shfl_xor_sync(~0u, l, 2);
+            if ((lane & 3) == 0) {
+                jm[kw * 32 + r] = m[p] * a.scale_log2;
+                jm[kw * 32 + 16 + r] = l;
+            }
+#pragma unroll
+            for (int d = 0; d < DH / 8; ++d)
+                *reinterpret_cast<float2 *>(jo + (kw * 16 + r) * C::kOs + d * 8 + (lane & 3) * 2) =
+                    make_float2(o[d][2 * p], o[d][2 * p + 1]);
+        }
+        named_sync(1, 32 * C::kWarps);
+        const bool whole = n == item.T && from == 0;  // nothing to join with
+        float *part = a.own_part + (int64_t)(item.w + blockIdx.x) * C::kSlot;
+        bf16 *out = a.out + ((int64_t)i * a.D * a.Hkv + h) * a.G * DH;
+#pragma unroll
+        for (int k = 0; k < kOn; ++k) {
+            const int x = gt + k * 32 * KG, r = x / (DH / 4), c4 = x % (DH / 4);
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+            for (int q = 0; q < KG; ++q) top = fmaxf(top, jm[q * 32 + r]);
+            const float off = top == -INFINITY ? 0.0f : top;
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < KG; ++q) {
+                const float f = ex2(jm[q * 32 + r] - off);
+                const float4 u =
+                    *reinterpret_cast<float4 *>(jo + (q * 16 + r) * C::kOs + c4 * 4);
+                sum = fmaf(f, jm[q * 32 + 16 + r], sum);
+                v.x = fmaf(f, u.x, v.x);
+                v.y = fmaf(f, u.y, v.y);
+                v.z = fmaf(f, u.z, v.z);
+                v.w = fmaf(f, u.w, v.w);
+            }
+            if (o_row[k] < 0) continue;
+            if (whole) {
+                if (bad) continue;
+                const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+                gst(reinterpret_cast<uint2 *>(out + (int64_t)o_row[k] * DH + c4 * 4),
+                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
+            } else {
+                const int row = rg * 16 + r;
+                gst(reinterpret_cast<float4 *>(part + row * DH + c4 * 4), v);
+                if (c4 == 0) {
+                    // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
+                    gst(part + C::MR * DH + row, bad ? __int_as_float(0x7FC00000) : top);
+                    gst(part + C::MR * DH + C::MR + row, sum);
+                }
+            }
+        }
+    }
+}
+
+// HG: 0 for a bf16 cache, else the kv heads of an item over an 8-bit one.
+template <int DH, int MR, int HG>
+__global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, HG>::kCtas)
     k_own(AttnArgs a, const __grid_constant__ CUtensorMap mk,
           const __grid_constant__ CUtensorMap mv) {
-    using C = OwnCfg<DH, RG, Q8>;
-    constexpr int ST = C::kStages, kThreads = C::kThreads, KG = C::KG, KB = C::KB, kKT = C::KT;
+    using C = OwnCfg<DH, MR, HG>;
+    constexpr bool Q8 = HG > 0;
+    constexpr int ST = C::kStages, kThreads = C::kThreads, kKT = C::KT;
     constexpr int QB = C::kQBufs;
     extern __shared__ unsigned char raw[];
     __shared__ uint64_t s_full[ST], s_empty[ST];
     __shared__ uint64_t s_qfull[QB], s_qempty[QB];  // an item's queries and description
     __shared__ OwnItem s_item[QB];
     __shared__ int s_bad[ST];
-    __shared__ TileScales8<Q8 ? kKT / 8 : 1> s_scale[Q8 ? ST : 1];  // of the 8-bit cache's tiles
+    __shared__ typename C::Scales s_scale[ST];  // of an 8-bit cache's tiles
     __shared__ int64_t s_scan[kThreads / 32];
     __shared__ int s_seq, s_slots[kThreads], s_lens[kThreads];  // of all sequences, if they fit
     __shared__ int64_t s_seq_unit;
@@ -328,7 +580,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
     const uint32_t ring_a = smem_addr(ring);
     unsigned char *qs = ring + ST * C::kStage;
     const uint32_t qs_a = smem_addr(qs);
-    float *join = reinterpret_cast<float *>(qs + C::kQBufs * C::kQ);
+    float *join = reinterpret_cast<float *>(qs + C::kQBufs * C::kHeads * C::kQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -362,7 +614,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
     // The units of the call and the sequence that holds this CTA's first one.
     const int rows = a.D * a.G;
     const int RT = (rows + C::MR - 1) / C::MR;
-    const int per = RT * a.Hkv;  // items of a sequence
+    const int heads = a.Hkv / C::kHeads;  // items of a row tile
+    const int per = RT * heads;           // items of a sequence
     int64_t U = 0, u0 = 0, u1 = 0;
     int n_cta = 1;
     // Units before this thread's sequence of i0 .. i0 + kThreads - 1, the units of that, and
@@ -467,13 +720,17 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
                 constexpr int kStep = 256 / DH;  // rows of 32 chunks
                 int r = lane / (DH / 8), rr = it.rt * C::MR + r, j = rr / a.G, gq = rr - j * a.G;
                 const int ch = lane % (DH / 8);
-                const uint32_t col = b * C::kQ + (ch >> 3) * C::MR * 128;
+                const uint32_t col = b * C::kHeads * C::kQ + (ch >> 3) * C::MR * 128;
                 for (; r < C::MR; r += kStep, rr += kStep) {
-                    const uint32_t off = col + swz(r, ch & 7);
-                    if (rr < rows)
-                        cp_async16(qs_a + off, q + j * a.q_stride + gq * DH + ch * 8);
-                    else
-                        *reinterpret_cast<uint4 *>(qs + off) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int hh = 0; hh < C::kHeads; ++hh) {
+                        const uint32_t off = col + hh * C::kQ + swz(r, ch & 7);
+                        if (rr < rows)
+                            cp_async16(qs_a + off,
+                                       q + j * a.q_stride + (hh * a.G + gq) * DH + ch * 8);
+                        else
+                            *reinterpret_cast<uint4 *>(qs + off) = make_uint4(0u, 0u, 0u, 0u);
+                    }
                     for (gq += kStep; gq >= a.G; gq -= a.G) ++j;
                 }
             }
@@ -509,14 +766,18 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive_expect_tx(&s_full[st],
-                                          (uint32_t)boxes * box * DH * (Q8 ? 2 : 4));
+                                          (uint32_t)boxes * box * DH * (Q8 ? 2 * HG : 4));
                 __syncwarp();
                 if (lane < boxes) {
                     const int key = id * ps + (s.ids.box() + lane) * box % ps;
                     if constexpr (Q8) {
-                        const uint32_t d = ring_a + st * C::kStage + lane * box * DH;
-                        tma_load_3d(d, &mk, &s_full[st], 0, it.h, key);
-                        tma_load_3d(d + C::kV, &mv, &s_full[st], 0, it.h, key);
+                        const uint32_t d = ring_a + st * C::kStage + lane * box * C::kRow;
+#pragma unroll
+                        for (int c = 0; c < C::NC; ++c) {
+                            const int x = it.h * DH + c * 128;
+                            tma_load_2d(d + c * C::kBlk, &mk, &s_full[st], x, key);
+                            tma_load_2d(d + C::kV + c * C::kBlk, &mv, &s_full[st], x, key);
+                        }
                     } else {
                         const uint32_t d = ring_a + st * C::kStage + lane * box * 128;
 #pragma unroll
@@ -536,7 +797,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
         after.i = -1;  // not looked for yet: the first tiles go first
         int64_t left = u1 - u0;
         int it = (int)((u0 - s_seq_unit) / s.T), t0 = (int)(u0 - s_seq_unit - (int64_t)it * s.T);
-        int rt = it / a.Hkv, h = it - rt * a.Hkv;
+        int rt = it / heads, h = (it - rt * heads) * C::kHeads;
         bool ok = true;
         while (ok && left > 0 && s.i < a.N) {
             const int n = (int)min((int64_t)(s.T - t0), left);
@@ -544,7 +805,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
             left -= n;
             t0 = 0;
             if (left > 0 && after.i < 0) find(s.i + 1, after);
-            if (++h == a.Hkv) {
+            if ((h += C::kHeads) == a.Hkv) {
                 h = 0;
                 ++rt;
             }
@@ -562,276 +823,13 @@ __global__ void __launch_bounds__(OwnCfg<DH, RG, Q8>::kThreads, OwnCfg<DH, RG, Q
         return;
     }
 
-    uint32_t ring_at = 0, ring_phase = 0;
-    bool dead = false;
-    const int kw = warp % KG, rg = warp / KG;  // key and row group
-    // This lane's ldmatrix address in a K and in a V block: a step of 16 columns flips bits 5, 6.
-    [[maybe_unused]] const uint32_t k_lane =
-        swz(kw * 16 * KB + (lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-    [[maybe_unused]] const uint32_t v_lane = swz(kw * 16 * KB + (lane & 15), lane >> 4);
-    const f32x2 scale2 = f2_make(a.scale_log2, a.scale_log2);
-    const float rescale = kRescaleLog2 / a.scale_log2;
-    // What a thread does with the rows of row tile rt, the same for every item: the
-    // tokens of the two rows it computes, the output rows it writes chunks of (counted from the
-    // sequence's first row of the kv head, -1 past the item's rows; rows, since the D Hq Dh
-    // elements of one sequence may pass 2^31).
-    constexpr int kOn = 16 * DH / 4 / (32 * KG);
-    const int gt = kw * 32 + lane;  // thread of the row group
-    int rt_now = -1, row_j[2], o_row[kOn];
-    auto set_rows = [&](int rt) {
-        rt_now = rt;
-        const int r0 = rt * C::MR;
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int rr = r0 + rg * 16 + p * 8 + (lane >> 2);
-            row_j[p] = rr < rows ? rr / a.G : INT_MIN / 2;
-        }
-#pragma unroll
-        for (int k = 0; k < kOn; ++k) {
-            const int rr = r0 + rg * 16 + (gt + k * 32 * KG) / (DH / 4);
-            o_row[k] = rr < rows ? rr / a.G * a.Hkv * a.G + rr % a.G : -1;
-        }
-    };
-    for (uint32_t items = 0;; ++items) {
-        const uint32_t qb = items % QB;
-        const bool ready = !dead && mbar_wait_bounded(&s_qfull[qb], (items / QB) & 1u);
-        // The warps go on together or not at all: none waits at a barrier the others left.
-        if (named_or(1, 32 * C::kWarps, !ready)) {
-            if (!ready && !dead) raise_error(SC_DEV_TIMEOUT);
-            return leave();
-        }
-        const OwnItem item = s_item[qb];
-        const int i = item.i, len = item.len, h = item.h, t0 = item.t0, n = item.n;
-        if (n == 0) return leave();
-        if (item.rt != rt_now) set_rows(item.rt);
-        uint32_t qf[DH / 16][4];
-        [[maybe_unused]] float unit[2];  // of a row's scores, where Q is held to f16's range
-        if constexpr (Q8) {
-            load_queries8<DH>(qf, unit, qs + qb * C::kQ, C::MR * 128, rg * 16, a.scale_log2);
-        } else {
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-                const int ch = kk * 2 + (lane >> 4);
-                ldsm4(qf[kk], qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
-                                  swz(rg * 16 + (lane & 15), ch & 7));
-            }
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_qempty[qb]);
-        // A row's running maximum m (of the scores before scaling), the score that moves
-        // it, and its offset -m scale; the sums of its weights in pairs.
-        int see[2];
-        float m[2], limit[2], off[2], o[DH / 8][4];
-        f32x2 l2[2];
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            see[p] = len - a.D + 1 + row_j[p];  // below zero for a row past the item's
-            m[p] = limit[p] = -INFINITY;
-            off[p] = 0.0f;
-            l2[p] = f2_make(0.0f, 0.0f);
-        }
-        const int least = len - a.D + 1;  // keys that every row of the sequence sees
-#pragma unroll
-        for (int d = 0; d < DH / 8; ++d)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[d][e] = 0.0f;
-        bool bad = false;
-        const int from = prefix_keys(a, len);
-        int key0 = from + t0 * kKT + kw * 16 * KB;
-        for (int t = 0; t < n; ++t, key0 += kKT) {
-            if (!dead && !mbar_wait_bounded(&s_full[ring_at], ring_phase)) {
-                raise_error(SC_DEV_TIMEOUT);
-                dead = true;  // no more waits: the rest runs through on what is there
-            }
-            bad |= s_bad[ring_at] != 0;
-            if constexpr (Q8) {
-                tile8<DH, KB>(ring + ring_at * C::kStage, C::kV, s_scale[ring_at], kw, key0, len,
-                              least, see, qf, unit, m, limit, l2, o);
-            } else {
-                const uint32_t stage = ring_a + ring_at * C::kStage;
-                const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
-                const bool tail = key0 + 16 * KB > len;
-                if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
-                    const int first = max(0, len - key0);
-                    for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
-                        const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
-                        *reinterpret_cast<uint4 *>(ring + ring_at * C::kStage +
-                                                   (C::NB + (ch >> 3)) * C::kBlk +
-                                                   (kw * 16 * KB + r) * 128 +
-                                                   (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    __syncwarp();
-                }
-                float sc[2 * KB][4];
-#pragma unroll
-                for (int nt = 0; nt < 2 * KB; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
-#pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk)
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
-                        uint32_t b[4];
-                        ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
-                        mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
-                        mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
-                    }
-                if (key0 + 16 * KB > least) {  // some row does not see some of these keys
-#pragma unroll
-                    for (int nt = 0; nt < 2 * KB; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
-                                sc[nt][e] = -INFINITY;
-                }
-                float top[2];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
-#pragma unroll
-                    for (int nt = 1; nt < 2 * KB; ++nt)
-                        top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
-                }
-                // Only when some score passes its row's limit are the row maxima needed. A row that
-                // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
-                if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
-                        if (!(top[p] > limit[p])) continue;
-                        const float f = ex2((m[p] - top[p]) * a.scale_log2);
-                        m[p] = top[p];
-                        limit[p] = top[p] + rescale;
-                        off[p] = -top[p] * a.scale_log2;
-                        l2[p] = f2_mul(l2[p], f2_make(f, f));
-#pragma unroll
-                        for (int d = 0; d < DH / 8; ++d) {
-                            o[d][2 * p] *= f;
-                            o[d][2 * p + 1] *= f;
-                        }
-                    }
-                }
-                uint32_t pf[KB][4];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const f32x2 off2 = f2_make(off[p], off[p]);
-#pragma unroll
-                    for (int nt = 0; nt < 2 * KB; ++nt) {
-                        float e0, e1;
-                        f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        l2[p] = f2_add(l2[p], f2_make(e0, e1));
-                        // P enters the second product as bf16: 2^-8 relative a term at most.
-                        pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
-                    }
-                }
-                // A draft that some row does not see: were its V not finite, a weight of 0 would
-                // not keep it from that row, so the block's product is made one by one.
-                bool plain = false;
-                if (key0 + 16 * KB > least) {
-                    const unsigned char *vb = ring + ring_at * C::kStage + C::NB * C::kBlk;
-                    const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
-                    for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
-                        plain |= not_finite(*reinterpret_cast<const uint4 *>(
-                            vb + (x % (DH / 8) >> 3) * C::kBlk +
-                            swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
-                    plain = __any_sync(~0u, plain);
-                    if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
-                }
-                if (!plain) {
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int dd = 0; dd < DH / 16; ++dd) {
-                            uint32_t b[4];
-                            ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
-                            mma16816(o[2 * dd], pf[kb], b[0], b[1]);
-                            mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
-                        }
-                }
-                if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_empty[ring_at]);
-            if (++ring_at == ST) {
-                ring_at = 0;
-                ring_phase ^= 1u;
-            }
-        }
-        // Join the key warps: each leaves its m, l and O, and a thread joins and writes
-        // four columns of a row. (The next join comes after the next item's barrier.)
-        float *jo = join + rg * KG * 16 * C::kOs;  // [key group][16][kOs]
-        float *jm = join + KG * C::MR * C::kOs + rg * KG * 32;  // [key group][m 16, l 16]
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const int r = p * 8 + (lane >> 2);
-            float l, l1;
-            f2_split(l2[p], l, l1);
-            l += l1;
-            l += __shfl_xor_sync(~0u, l, 1);
-            l += __shfl_xor_sync(~0u, l, 2);
-            if ((lane & 3) == 0) {
-                jm[kw * 32 + r] = Q8 ? m[p] : m[p] * a.scale_log2;
-                jm[kw * 32 + 16 + r] = l;
-            }
-            float *row = jo + (kw * 16 + r) * C::kOs;
-            if constexpr (Q8) {  // this thread's columns are DH / 4 in a row (see tile8)
-#pragma unroll
-                for (int d = 0; d < DH / 4; d += 4) {
-                    constexpr int W = DH / 8;
-                    const int e = 2 * p + d / W;
-                    *reinterpret_cast<float4 *>(row + (lane & 3) * 2 * W + d) =
-                        make_float4(o[d % W][e], o[d % W + 1][e], o[d % W + 2][e], o[d % W + 3][e]);
-                }
-            } else {
-#pragma unroll
-                for (int d = 0; d < DH / 8; ++d)
-                    *reinterpret_cast<float2 *>(row + d * 8 + (lane & 3) * 2) =
-                        make_float2(o[d][2 * p], o[d][2 * p + 1]);
-            }
-        }
-        named_sync(1, 32 * C::kWarps);
-        const bool whole = n == item.T && from == 0;  // nothing to join with
-        float *part = a.own_part + (int64_t)(item.w + blockIdx.x) * C::kSlot;
-        bf16 *out = a.out + ((int64_t)i * a.D * a.Hkv + h) * a.G * DH;
-#pragma unroll
-        for (int k = 0; k < kOn; ++k) {
-            const int x = gt + k * 32 * KG, r = x / (DH / 4), c4 = x % (DH / 4);
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll
-            for (int q = 0; q < KG; ++q) top = fmaxf(top, jm[q * 32 + r]);
-            const float off = top == -INFINITY ? 0.0f : top;
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-            for (int q = 0; q < KG; ++q) {
-                const float f = ex2(jm[q * 32 + r] - off);
-                const float4 u =
-                    *reinterpret_cast<float4 *>(jo + (q * 16 + r) * C::kOs + c4 * 4);
-                sum = fmaf(f, jm[q * 32 + 16 + r], sum);
-                v.x = fmaf(f, u.x, v.x);
-                v.y = fmaf(f, u.y, v.y);
-                v.z = fmaf(f, u.z, v.z);
-                v.w = fmaf(f, u.w, v.w);
-            }
-            if (o_row[k] < 0) continue;
-            if (whole) {
-                if (bad) continue;
-                const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
-                gst(reinterpret_cast<uint2 *>(out + (int64_t)o_row[k] * DH + c4 * 4),
-                    make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
-            } else {
-                const int row = rg * 16 + r;
-                gst(reinterpret_cast<float4 *>(part + row * DH + c4 * 4), v);
-                if (c4 == 0) {
-                    // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
-                    gst(part + C::MR * DH + row, bad ? __int_as_float(0x7FC00000) : top);
-                    gst(part + C::MR * DH + C::MR + row, sum);
-                }
-            }
-        }
-    }
+    const OwnSmem<C> s = {ring,   ring_a,  qs_a,   join, s_full, s_empty,
+                          s_qfull, s_qempty, s_item, s_bad, s_scale};
+    if constexpr (HG > 0)
+        consume8<C>(a, rows, s);
+    else
+        consume16<C>(a, rows, per, s);
+    leave();
 }
 
 }  // namespace sc
@@ -846,7 +844,8 @@ namespace sc {
 // adds its parts, in a fixed order. No load waits for another part's.
 constexpr int kMergeThreads = 256;
 template <int DH, int PG>
-__global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, int own_ctas) {
+__global__ void __launch_bounds__(kMergeThreads)
+    k_merge(PrefixArgs x, int MR, int own_ctas, int own_heads) {
     AttnArgs &a = x.a;
     constexpr int L = DH / 8 * PG;
     const int rl = threadIdx.x % L, c8 = rl % (DH / 8), group = rl / (DH / 8);
@@ -879,16 +878,18 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
     pdl_wait();
     pdl_launch_dependents();
     const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
-    const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * a.Hkv;
-    const int oslot = MR * (DH + 2), rt = r / MR, orow = r - rt * MR;
+    // k_own's items are of own_heads kv heads, a part's slots one for each.
+    const int groups = a.Hkv / own_heads, hi = h / own_heads, hh = h - hi * own_heads;
+    const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * groups;
+    const int slot_n = MR * (DH + 2), oslot = slot_n * own_heads, rt = r / MR, orow = r - rt * MR;
     if (u_n > u_i) {
         const int64_t d = u_n - u_i;
         const int64_t T = d <= UINT32_MAX ? (uint32_t)d / (uint32_t)per : d / per;
         const int n_cta = (int)min((int64_t)own_ctas, U);
-        const int it = rt * a.Hkv + h;
+        const int it = rt * groups + hi;
         const int64_t u0 = u_i + it * T;
         const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
-        own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot + orow * DH;
+        own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot + hh * slot_n + orow * DH;
         own_m = MR * DH + orow - orow * DH;
         own_n = c1 - c0 + 1;
         if (own_n == 1 && !prefix) {  // k_own wrote the row
@@ -981,22 +982,39 @@ __global__ void __launch_bounds__(kMergeThreads) k_merge(PrefixArgs x, int MR, i
 // ------------------------------------------------------------ host side
 
 // Pages [n_pages * page_size tokens, Hkv, Dh] in boxes of `keys` tokens of one
-// head: 64 columns of bf16, 128-byte swizzle, or all columns of an 8-bit cache, swizzled
-// within their 64 or 128 bytes.
+// head, 64 columns, 128-byte swizzle.
 static cudaError_t map_pages(CUtensorMap *m, const void *ptr, const PageTable &pt, int Hkv, int Dh,
-                             int keys, bool q8) {
+                             int keys) {
     EncodeTiledFn fn = encode_tiled();
     if (fn == nullptr) return cudaErrorNotSupported;
     const cuuint64_t dims[3] = {(cuuint64_t)Dh, (cuuint64_t)Hkv,
                                 (cuuint64_t)pt.n_pages * pt.page_size};
-    const cuuint64_t es = q8 ? 1 : 2, strides[2] = {Dh * es, (cuuint64_t)Hkv * Dh * es};
-    const cuuint32_t box[3] = {(cuuint32_t)(q8 ? Dh : 64), 1, (cuuint32_t)keys};
-    const cuuint32_t steps[3] = {1, 1, 1};
+    const cuuint64_t strides[2] = {(cuuint64_t)Dh * 2, (cuuint64_t)Hkv * Dh * 2};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)keys};
+    const cuuint32_t es[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr), dims,
+                          strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// An 8-bit cache's pages [n_pages * page_size tokens, Hkv * Dh] in boxes of `keys` tokens by
+// 128 bytes (two heads of 64, one of 128), 128-byte swizzle; by 64 where an item is one head of 64.
+static cudaError_t map_codes(CUtensorMap *m, const void *ptr, const PageTable &pt, int Hkv, int Dh,
+                             int keys, int heads) {
+    EncodeTiledFn fn = encode_tiled();
+    if (fn == nullptr) return cudaErrorNotSupported;
+    const bool narrow = heads * Dh == 64;
+    const cuuint64_t dims[2] = {(cuuint64_t)Hkv * Dh, (cuuint64_t)pt.n_pages * pt.page_size};
+    const cuuint64_t strides[1] = {(cuuint64_t)Hkv * Dh};
+    const cuuint32_t box[2] = {narrow ? 64u : 128u, (cuuint32_t)keys};
+    const cuuint32_t es[2] = {1, 1};
     const CUresult r =
-        fn(m, q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-           const_cast<void *>(ptr), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           q8 && Dh == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+        fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, es,
+           CU_TENSOR_MAP_INTERLEAVE_NONE,
+           narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+           (CUtensorMapL2promotion)(getenv("PROMO") ? atoi(getenv("PROMO")) : 2), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1019,14 +1037,24 @@ static cudaError_t map_queries(CUtensorMap *m, const PrefixArgs &x, const AttnSh
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Rows of an item: 16 hold up to 16 rows of a sequence and kv head, else 32.
-static int own_rows(const AttnShape &s) { return s.D * (s.Hq / s.Hkv) <= 16 ? 16 : 32; }
+// Rows of an item: 16 hold up to 16 rows of a sequence and kv head (over an 8-bit cache 8 hold
+// 8), else 32.
+static int own_rows(const AttnShape &s, bool q8) {
+    const int rows = s.D * (s.Hq / s.Hkv);
+    return q8 && rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
+}
+// kv heads of an item over an 8-bit cache: a token's codes of one head are 64 or 128 bytes,
+// which DRAM gives best together with its neighbours'.
+static int own_heads(const AttnShape &s, bool q8) {
+    if (!q8) return 1;
+    return s.Hkv % 4 == 0 && own_rows(s, true) < 32 ? 4 : s.Hkv % 2 == 0 ? 2 : 1;
+}
 
-static size_t own_part_floats(const AttnShape &s) {
-    const int MR = own_rows(s);
+static size_t own_part_floats(const AttnShape &s, bool q8) {
+    const int MR = own_rows(s, q8);
     const size_t items =
         (size_t)s.N * s.Hkv * (((size_t)s.D * (s.Hq / s.Hkv) + MR - 1) / MR);
-    return (items + kMaxCtas) * MR * (s.Dh + 2);
+    return (items + (size_t)kMaxCtas * own_heads(s, q8)) * MR * (s.Dh + 2);
 }
 // [N + 1] first tiles.
 static size_t cum_bytes(const AttnShape &s) { return ((size_t)s.N + 3) / 2 * 16; }
@@ -1063,8 +1091,12 @@ static size_t prefix_part_floats(const AttnShape &s) {
     return 2 * (items + kMaxPrefixCtas) * kPR * (s.Dh + 2);
 }
 
-size_t attention_workspace_bytes(const AttnShape &s) {
-    return cum_bytes(s) + (own_part_floats(s) + prefix_part_floats(s)) * 4;
+static size_t workspace_bytes(const AttnShape &s, bool q8) {
+    return cum_bytes(s) + (own_part_floats(s, q8) + prefix_part_floats(s)) * 4;
+}
+size_t attention_workspace_bytes(const AttnShape &s) { return workspace_bytes(s, false); }
+size_t attention8_workspace_bytes(const AttnShape &s, int page_size) {
+    return workspace_bytes(s, true) + 2 * unpacked_bytes(s, page_size);
 }
 
 template <typename F>
@@ -1078,16 +1110,29 @@ static cudaError_t smem_opt_in(F kern, size_t bytes, std::atomic<unsigned long l
     return e;
 }
 
-template <int DH, int RG, bool Q8>
+template <int DH, int MR, int HG>
 static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CUtensorMap &mv,
                               int sms, int *grid, cudaStream_t stream) {
-    using C = OwnCfg<DH, RG, Q8>;
+    using C = OwnCfg<DH, MR, HG>;
     static std::atomic<unsigned long long> done{0};
-    const cudaError_t e = smem_opt_in(k_own<DH, RG, Q8>, C::kSmem, done);
+    const cudaError_t e = smem_opt_in(k_own<DH, MR, HG>, C::kSmem, done);
     if (e != cudaSuccess) return e;
     *grid = C::kCtas * sms < kMaxCtas ? C::kCtas * sms : kMaxCtas;
-    return launch_pdl(k_own<DH, RG, Q8>, dim3((unsigned)*grid), dim3(C::kThreads), C::kSmem, stream, a,
-                      mk, mv);
+    return launch_pdl(k_own<DH, MR, HG>, dim3((unsigned)*grid), dim3(C::kThreads), C::kSmem, stream,
+                      a, mk, mv);
+}
+
+typedef cudaError_t (*LaunchOwn)(const AttnArgs &, const CUtensorMap &, const CUtensorMap &, int,
+                                 int *, cudaStream_t);
+template <int MR, int HG>
+static LaunchOwn own_of(int Dh) {
+    return Dh == 64 ? launch_own<64, MR, HG> : launch_own<128, MR, HG>;
+}
+template <int MR>
+static LaunchOwn own8_of(int Dh, int heads) {
+    if constexpr (MR < 32)
+        if (heads == 4) return own_of<MR, 4>(Dh);
+    return heads == 2 ? own_of<MR, 2>(Dh) : own_of<MR, 1>(Dh);
 }
 
 template <int DH>
@@ -1099,10 +1144,6 @@ static cudaError_t launch_prefix(const PrefixArgs &x, const CUtensorMap &mq, con
     if (e != cudaSuccess) return e;
     return launch_pdl(k_prefix<DH>, dim3((unsigned)x.n_cta), dim3(kPfxThreads), C::kSmem, stream, x,
                       mq, mk, mv);
-}
-
-size_t attention8_workspace_bytes(const AttnShape &s, int page_size) {
-    return attention_workspace_bytes(s) + 2 * unpacked_bytes(s, page_size);
 }
 
 cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
@@ -1125,23 +1166,25 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.out = (bf16 *)out;
     a.cum = (int64_t *)workspace;
     a.own_part = (float *)((char *)workspace + cum_bytes(s));
-    x.part = a.own_part + own_part_floats(s);
     const bool q8 = scales != nullptr;
+    const int heads = own_heads(s, q8), MR = own_rows(s, q8);
+    x.part = a.own_part + own_part_floats(s, q8);
     if (q8) a.s8 = *scales;
-    const int kt = q8 ? (s.Dh == 64 ? OwnCfg<64, 1, true>::KT : OwnCfg<128, 1, true>::KT)
-                      : OwnCfg<64, 1, false>::KT;
-    const int own_box = pt.page_size < kt ? pt.page_size : kt;
+    const int own_keys = !q8 ? OwnCfg<64, 16, 0>::KT : 128 / (heads * (MR == 32 ? 2 : 1));  // of a tile
+    const int own_box = pt.page_size < own_keys ? pt.page_size : own_keys;
     CUtensorMap mk, mv;
-    cudaError_t e = map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, own_box, q8);
+    cudaError_t e = q8 ? map_codes(&mk, k_pages, pt, s.Hkv, s.Dh, own_box, heads)
+                       : map_pages(&mk, k_pages, pt, s.Hkv, s.Dh, own_box);
     if (e != cudaSuccess) return e;
-    e = map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, own_box, q8);
+    e = q8 ? map_codes(&mv, v_pages, pt, s.Hkv, s.Dh, own_box, heads)
+           : map_pages(&mv, v_pages, pt, s.Hkv, s.Dh, own_box);
     if (e != cudaSuccess) return e;
     if (x.P > 0) {
         CUtensorMap mq, pk = mk, pv = mv;
         const int box = pt.page_size < kPK ? pt.page_size : kPK;
         PageTable from = pt;
         if (q8) {  // the prefix as bf16 pages in the workspace
-            bf16 *k16 = (bf16 *)((char *)workspace + attention_workspace_bytes(s));
+            bf16 *k16 = (bf16 *)((char *)workspace + workspace_bytes(s, true));
             bf16 *v16 = k16 + unpacked_bytes(s, pt.page_size) / 2;
             e = launch_unpack(a, s, k_pages, v_pages, k16, v16, sm_count, stream);
             if (e != cudaSuccess) return e;
@@ -1151,9 +1194,9 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
             v_pages = v16;
         }
         if (q8 || box != own_box) {
-            e = map_pages(&pk, k_pages, from, s.Hkv, s.Dh, box, false);
+            e = map_pages(&pk, k_pages, from, s.Hkv, s.Dh, box);
             if (e != cudaSuccess) return e;
-            e = map_pages(&pv, v_pages, from, s.Hkv, s.Dh, box, false);
+            e = map_pages(&pv, v_pages, from, s.Hkv, s.Dh, box);
             if (e != cudaSuccess) return e;
         }
         e = map_queries(&mq, x, s);
@@ -1162,13 +1205,12 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
                        : launch_prefix<128>(x, mq, pk, pv, stream);
         if (e != cudaSuccess) return e;
     }
-    const int MR = own_rows(s);
     const int sms = a.beside ? sm_count - x.n_cta : sm_count;
     int grid = 0;
-    const auto own = q8 ? (s.Dh == 64 ? (MR == 16 ? launch_own<64, 1, true> : launch_own<64, 2, true>)
-                                      : (MR == 16 ? launch_own<128, 1, true> : launch_own<128, 2, true>))
-                        : (s.Dh == 64 ? (MR == 16 ? launch_own<64, 1, false> : launch_own<64, 2, false>)
-                                      : (MR == 16 ? launch_own<128, 1, false> : launch_own<128, 2, false>));
+    const LaunchOwn own = !q8       ? (MR == 16 ? own_of<16, 0>(s.Dh) : own_of<32, 0>(s.Dh))
+                          : MR == 8  ? own8_of<8>(s.Dh, heads)
+                          : MR == 16 ? own8_of<16>(s.Dh, heads)
+                                     : own8_of<32>(s.Dh, heads);
     e = own(a, mk, mv, sms, &grid, stream);
     if (e != cudaSuccess) return e;
     // With few rows all lanes of a warp share one: a whole step over two streams of 30-40
@@ -1182,7 +1224,8 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
                                   : (few ? k_merge<128, 2> : k_merge<128, 1>);
     const int block_rows = few ? kMergeThreads / 32 : kMergeThreads / (s.Dh / 8);  // of one token
     const dim3 blocks((unsigned)(s.N * s.D), (unsigned)((s.Hq + block_rows - 1) / block_rows));
-    return launch_pdl(merge, blocks, dim3(kMergeThreads), 0, stream, x, MR, grid);
+    return launch_pdl(merge, blocks, dim3(kMergeThreads), 0, stream, x, MR, grid,
+                      heads);
 }
 
 cudaError_t take_error_attention(cudaStream_t stream, unsigned int *sum) {

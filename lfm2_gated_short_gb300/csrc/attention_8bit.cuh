@@ -2,14 +2,16 @@
 // unpacking of a shared prefix.
 //
 // A key is ks k', a value vs v' (codes k', v' of e4m3, powers of two ks, vs of the block and
-// head). The codes go to the tensor cores as f16, which holds them exactly, one conversion a pair;
-// Q goes there as f16 too, times a power of two that takes its row's largest to 2^14
-// (11 bits of f16 hold bf16's 8). The scales stay out of the products: with s_t a row's score in
-// units of log2,
+// head). The codes go to the tensor cores as f16, which holds them exactly; Q goes there as f16 too,
+// times a power of two that takes its row's largest to 2^14 (11 bits of f16 hold bf16's 8). The
+// scales stay out of the products: with s_t a row's score in units of log2,
 //   out = sum_t 2^(s_t + log2 vs_t - m) v'_t / sum_t 2^(s_t + log2 vs_t - m) / vs_t,
 // so that the weights that meet v' are at most 1 (2^8 with the lazy maximum), whatever the
 // sizes of the blocks' values, and are rounded to f16's 11 bits. m is the running
 // maximum of s_t + log2 vs_t.
+//
+// (The register MMA of e4m3 itself is made of conversions of both operands and f16 MMAs on this
+// GPU: it measured 146 us where this takes TODO.)
 #pragma once
 
 namespace sc {
@@ -49,11 +51,6 @@ __device__ __forceinline__ void copy_tile_scales(const AttnArgs &a, TileScales8<
     s.at[which][g] = at;
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 // d += a b for a 16 x 8 x 16 f16 product, fp32 accumulators.
 __device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
                                              uint32_t b1) {
@@ -63,237 +60,525 @@ __device__ __forceinline__ void mma16816_f16(float (&d)[4], const uint32_t (&a)[
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+// Two 16 x 16 matrices of bytes, transposed: lane 4 g + c gets rows 4 c .. 4 c + 3 of column g
+// (r[0]) and of column g + 8 (r[1]) of the first, and the same of the second.
+__device__ __forceinline__ void ldsm2_t8(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
 __device__ __forceinline__ uint32_t word_of(const uint4 &v, int e) {
     return e == 0 ? v.x : e == 1 ? v.y : e == 2 ? v.z : v.w;
 }
-
-// A tile row of DH bytes has its 16-byte chunks swizzled as a TMA box of 64-byte (DH 64) or
-// 128-byte rows lays them out.
-template <int DH>
-__device__ __forceinline__ uint32_t swz8(int row, int chunk) {
-    return (uint32_t)(row * DH + ((chunk ^ (DH == 64 ? row >> 1 & 3 : row & 7)) << 4));
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// An 8 x 8 matrix of 16-bit values, transposed: lane 4 g + c holds row g's columns 2 c, 2 c + 1.
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
 }
 
-// The column order of the first product is free as long as Q and K agree: lane c of a row's four
-// takes the columns 16 c .. 16 c + 15 (of each 64), four a step, which K's row holds as
-// one 16-byte chunk. unit[p]: what a product of row p stands for, times scale_log2.
-template <int DH>
-__device__ __forceinline__ void load_queries8(uint32_t (&qf)[DH / 16][4], float (&unit)[2],
-                                              const unsigned char *q, uint32_t block, int row0,
-                                              float scale_log2) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-#pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        uint4 v[DH / 32];
-        uint32_t most = 0;
-#pragma unroll
-        for (int b = 0; b < DH / 32; ++b) {
-            v[b] = *reinterpret_cast<const uint4 *>(q + (b >> 1) * block +
-                                                    swz(row0 + 8 * p + g, 2 * c + (b & 1)));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t w = word_of(v[b], e);
-                most = max(most, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
-            }
-        }
-        most = max(most, __shfl_xor_sync(~0u, most, 1));
-        most = max(most, __shfl_xor_sync(~0u, most, 2));
-        const uint32_t e = max(most >> 7, 32u);  // the largest's exponent, biased by 127
-        const float to = __uint_as_float((268 - e) << 23);  // 2^(14 - (e - 127))
-        unit[p] = __uint_as_float((e - 14) << 23) * scale_log2;
-#pragma unroll
-        for (int b = 0; b < DH / 32; ++b)
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const uint32_t two = word_of(v[b], w);
-                qf[b * 2 + w / 2][w % 2 * 2 + p] = pack_f16(bf16_lo(two) * to, bf16_hi(two) * to);
-            }
+// An item is MR rows of a sequence for HG kv heads at once. A consumer warp takes WR rows of one
+// head by 32 keys of a tile. Both products have the keys' matrix first (16 keys, or 16 columns of
+// V, by 8 rows of queries), so that 8 rows fill a product and a code is converted once for all rows.
+template <int DH, int MR_, int HG>
+struct Own8Cfg {
+    static constexpr int kDh = DH;
+    static constexpr int MR = MR_;
+    static constexpr int RG = MR == 32 ? 2 : 1;               // row groups
+    static constexpr int WR = MR / RG;
+    static constexpr int NT = WR / 8;                         // row tiles of a warp
+    static constexpr int kHeads = HG;
+    static constexpr int KG = 4 / (HG * RG);                  // key groups
+    static constexpr int KT = 32 * KG;                        // keys of a tile
+    static constexpr int kWarps = 4;
+    static constexpr int kThreads = 32 * (kWarps + 1);
+    static constexpr int kRow = HG * DH == 64 ? 64 : 128;     // bytes of a key in a column block
+    static constexpr int NC = HG * DH / kRow;                 // column blocks
+    static constexpr uint32_t kBlk = KT * kRow;
+    static constexpr uint32_t kV = NC * kBlk;                 // the tile's V behind its K
+    static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows or Dh 128 8 to 32
+    static constexpr int kCtas = DH == 64 ? 3 : 2;
+    static constexpr int kQBufs = KG == 1 && DH == 64 ? 2 : 1;  // items described ahead
+    static constexpr int NB = DH / 64;                        // 64-wide column blocks of Q
+    static constexpr uint32_t kQ = MR * 128 * NB;             // queries of a head
+    static constexpr int kOs = DH + 4;                        // floats of a row to join
+    static constexpr uint32_t kJoin = KG > 1 ? kWarps * WR * (kOs + 2) * 4 : 0;
+    // Tiles in flight: what the CTAs of an SM leave of its 228 KB beside 4.5 KB each of static and
+    // reserved shared memory.
+    static constexpr size_t kRest = 1024 + kQBufs * HG * kQ + kJoin;
+    static constexpr int kFit = (int)((228 * 1024 / kCtas - 4608 - kRest) / kStage);
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static_assert(kStages >= 2, "shared memory of an SM");
+    static constexpr size_t kSmem = kRest + kStages * kStage;
+    static constexpr int kSlot = MR * (DH + 2);               // floats of a part and head
+    typedef TileScales8<KT / 8> Scales;
+};
+template <int DH, int MR>
+struct OwnCfg<DH, MR, 1> : Own8Cfg<DH, MR, 1> {};
+template <int DH, int MR>
+struct OwnCfg<DH, MR, 2> : Own8Cfg<DH, MR, 2> {};
+template <int DH, int MR>
+struct OwnCfg<DH, MR, 4> : Own8Cfg<DH, MR, 4> {};
+
+// Where this lane, 4 g + c, finds a tile's codes, as byte offsets from the tile's K (or V).
+// Rows of 128 bytes have their 16-byte chunks XOR-swizzled by the row's low 3 bits, rows of 64 by its
+// bits 1 and 2.
+//
+// The order of 16 keys in both products is free as long as they agree: key_of() gives the key
+// of place i. Places g and g + 8, whose scores a lane holds, are then in one group of 8 keys,
+// the four places 2 c, 2 c + 1, 2 c + 8, 2 c + 9 of a lane's second operand are one word of
+// ldsm2_t8, and neither product's reads meet in a bank (in rows of 128 bytes).
+template <typename C>
+struct Lane8 {
+    int g, c, half;      // half: of its column block, where that holds two heads
+    uint32_t base;       // of this warp's head and its first key
+    uint32_t k_at[2];    // chunk c of the keys at places g, g + 8; the next 64 columns: XOR 64
+    uint32_t v_at;       // for ldsm2_t8, columns 0 .. 15; the next 16: XOR 16
+    int key;             // at place g; at place g + 8: 2 more
+    __device__ __forceinline__ Lane8(int hh, int row0) {
+        const int lane = threadIdx.x & 31;
+        g = lane >> 2;
+        c = lane & 3;
+        constexpr bool kTwo = C::kRow == 128 && C::kDh == 64;
+        half = kTwo ? hh & 1 : 0;
+        base = (kTwo ? hh >> 1 : C::kRow == 128 ? hh : 0) * C::kBlk + row0 * C::kRow;
+        key = key_of(g);
+        k_at[0] = at(key, c);
+        k_at[1] = at(key + 2, c);
+        const int i = lane & 15;  // word i / 4, byte i % 4
+        v_at = at((lane & 16) + key_of(2 * (i >> 2) + (i & 1) + 4 * (i & 2)), 0);
     }
-}
+    static __device__ __forceinline__ int key_of(int i) {
+        return (i >> 2 & 1) * 8 + (i & 1) * 4 + (i >> 3) * 2 + (i >> 1 & 1);
+    }
+    // Chunk `chunk` of this warp's head at its key `row`.
+    __device__ __forceinline__ uint32_t at(int row, int chunk) const {
+        const int x = C::kRow == 64 ? row >> 1 & 3 : row & 7;
+        return base + row * C::kRow + (uint32_t)((half * 4 + chunk) ^ x) * 16;
+    }
+};
 
-// o += P V over a warp's 16 KB keys, of each row only the keys it sees; as tile8 lays P and o out.
-template <int DH, int KB>
-__device__ __forceinline__ void product_one_by_one8(float (&o)[DH / 8][4],
-                                                    const uint32_t (&pf)[KB][4],
-                                                    const unsigned char *v, int row0, int key0,
-                                                    const int (&see)[2]) {
-    const int lane = threadIdx.x & 31, c = lane & 3;
-    constexpr int W = DH / 8;
-#pragma unroll 1
-    for (int k = 0; k < 16 * KB; ++k) {
-        uint32_t w2[2] = {0, 0};
+// A warp's rows of an item: the lane's are rows 8 n + 2 c and the next, as pairs.
+template <typename C>
+struct Rows8 {
+    // Row 8 n + g as the first product's second operand. The column order of that product is free
+    // too: lane c takes the columns 16 c .. 16 c + 15 (of each 64), four a step, which K's row
+    // holds as one chunk.
+    uint32_t qf[C::NT][C::kDh / 16][2];
+    f32x2 unit[C::NT];  // what a product stands for, times scale log2(e)
+    f32x2 off[C::NT];   // -m, or 0 where no key was seen
+    f32x2 l[C::NT];
+    float m[C::NT][2];
+    int see[C::NT][2];  // keys that a row sees
+    float o[C::NT][C::kDh / 16][4];  // columns 16 j + g and 16 j + 8 + g, of both rows each
+
+    __device__ __forceinline__ void load(uint32_t q, float scale_log2) {
+        const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+        constexpr int DH = C::kDh;
 #pragma unroll
-        for (int nt = 0; nt < 2 * KB; ++nt)
-            if (nt == k >> 3) {
-                w2[0] = pf[nt / 2][nt % 2 * 2];
-                w2[1] = pf[nt / 2][nt % 2 * 2 + 1];
-            }
-        float w[2];
+        for (int n = 0; n < C::NT; ++n) {
+            uint4 v[DH / 32];
+            uint32_t most = 0;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const uint32_t x = __shfl_sync(~0u, w2[p], (lane & ~3) | (k & 7) >> 1);
-            w[p] = k & 1 ? f16_hi(x) : f16_lo(x);
-        }
+            for (int b = 0; b < DH / 32; ++b) {
+                v[b] = lds16(q + (b >> 1) * C::MR * 128 + swz(8 * n + g, 2 * c + (b & 1)));
 #pragma unroll
-        for (int b = 0; b < 2 * W / 16; ++b) {  // this lane's 2 W columns
-            const uint4 q = *reinterpret_cast<const uint4 *>(
-                v + swz8<DH>(row0 + k, c * (2 * W / 16) + b));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = e4m3x2_f16x2(word_of(q, e)), hi = e4m3x2_f16x2_hi(word_of(q, e));
-                const float x[4] = {f16_lo(lo), f16_hi(lo), f16_lo(hi), f16_hi(hi)};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int col = b * 16 + e * 4 + u;
-#pragma unroll
-                    for (int p = 0; p < 2; ++p)
-                        if (key0 + k < see[p]) {
-                            float &to = o[col % W][2 * p + col / W];
-                            to = fmaf(w[p], x[u], to);
-                        }
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t w = word_of(v[b], e);
+                    most = max(most, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
                 }
             }
+            most = max(most, __shfl_xor_sync(~0u, most, 1));
+            most = max(most, __shfl_xor_sync(~0u, most, 2));
+            const uint32_t e = max(most >> 7, 32u);  // the largest's exponent, biased by 127
+            const float to = __uint_as_float((268 - e) << 23);  // 2^(14 - (e - 127))
+            const float u = __uint_as_float((e - 14) << 23) * scale_log2;
+            unit[n] = f2_make(__shfl_sync(~0u, u, 8 * c), __shfl_sync(~0u, u, 8 * c + 4));
+#pragma unroll
+            for (int b = 0; b < DH / 32; ++b)
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t two = word_of(v[b], w);
+                    qf[n][b * 2 + w / 2][w % 2] = pack_f16(bf16_lo(two) * to, bf16_hi(two) * to);
+                }
         }
+    }
+};
+
+// o += P V over a warp's 32 keys, of each row only the keys it sees; e[n][2 h + x]: the weights of
+// the key at place g + 8 x of 16, half h.
+template <typename C>
+__device__ __forceinline__ void product_one_by_one8(Rows8<C> &r, const f32x2 (&e)[C::NT][4],
+                                                    uint32_t v, const Lane8<C> &at, int key0) {
+#pragma unroll 1
+    for (int k = 0; k < 32; ++k) {
+        const int g = (k >> 3 & 1) * 4 + (k & 1) * 2 + (k >> 2 & 1);  // of the lanes that hold key k
+        const int x = (k >> 4) * 2 + (k >> 1 & 1);
+        float w[C::NT][2];
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n) {
+            f32x2 mine = e[n][0];
+#pragma unroll
+            for (int i = 1; i < 4; ++i)
+                if (i == x) mine = e[n][i];
+            f2_split(mine, w[n][0], w[n][1]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) w[n][p] = __shfl_sync(~0u, w[n][p], 4 * g + at.c);
+        }
+#pragma unroll
+        for (int j = 0; j < C::kDh / 16; ++j)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t code;
+                asm volatile("ld.shared.u8 %0, [%1];"
+                             : "=r"(code)
+                             : "r"(v + at.at(k, j) + 8 * h + at.g)
+                             : "memory");
+                const float y = f16_lo(e4m3x2_f16x2(code));
+#pragma unroll
+                for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+                    for (int p = 0; p < 2; ++p)
+                        if (key0 + k < r.see[n][p])
+                            r.o[n][j][2 * h + p] = fmaf(w[n][p], y, r.o[n][j][2 * h + p]);
+            }
     }
 }
 
-// One tile's part of a warp: 16 rows by 16 KB keys from tile row 16 KB kw (key key0) on. The order
-// of the output's columns is free too: lane g of the second product's eight takes the DH / 8
-// columns from g DH / 8 on, which V's row holds together, step d the d-th of them; o[d][2p + e] is
-// then row p's column (2 c + e) DH / 8 + d.
-template <int DH, int KB, int G>
-__device__ __forceinline__ void tile8(const unsigned char *k, uint32_t v_off,
-                                      const TileScales8<G> &scales, int kw, int key0, int len,
-                                      int least, const int (&see)[2],
-                                      const uint32_t (&qf)[DH / 16][4], const float (&unit)[2],
-                                      float (&m)[2], float (&limit)[2], f32x2 (&l2)[2],
-                                      float (&o)[DH / 8][4]) {
-    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
-    const int row0 = kw * 16 * KB;
-    const unsigned char *v = k + v_off;
-    float s[2 * KB][4], inverse[2 * KB];
+// One tile's part of a warp: its rows by 32 keys (from key key0 on).
+template <typename C>
+__device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C> &at, int hh,
+                                      int group0, int key0, int len, int least, Rows8<C> &r) {
+    constexpr int DH = C::kDh, NT = C::NT, kG = C::KT / 8;
+    const int lane = threadIdx.x & 31;
+    const uint32_t v = k + C::kV;
+    f32x2 s[NT][4];  // s[n][2 h + x]: key at place g + 8 x of 16, half h
 #pragma unroll
-    for (int nt = 0; nt < 2 * KB; ++nt) {
+    for (int h = 0; h < 2; ++h) {
+        float d[NT][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[nt][e] = 0.0f;
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[n][e] = 0.0f;
 #pragma unroll
         for (int b = 0; b < DH / 64; ++b) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(
-                k + (row0 + nt * 8) * DH + swz8<DH>(g, c + 4 * b));
+            const uint4 w0 = lds16(k + (at.k_at[0] ^ b * 64) + h * 16 * C::kRow);
+            const uint4 w1 = lds16(k + (at.k_at[1] ^ b * 64) + h * 16 * C::kRow);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                mma16816_f16(s[nt], qf[b * 4 + e], e4m3x2_f16x2(word_of(w, e)),
-                             e4m3x2_f16x2_hi(word_of(w, e)));
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a[4] = {
+                    e4m3x2_f16x2(word_of(w0, j)), e4m3x2_f16x2(word_of(w1, j)),
+                    e4m3x2_f16x2_hi(word_of(w0, j)), e4m3x2_f16x2_hi(word_of(w1, j))};
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma16816_f16(d[n], a, r.qf[n][4 * b + j][0], r.qf[n][4 * b + j][1]);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            s[n][2 * h] = f2_make(d[n][0], d[n][1]);
+            s[n][2 * h + 1] = f2_make(d[n][2], d[n][3]);
         }
     }
-    float top[2] = {-INFINITY, -INFINITY};
+    const bool some = key0 + 32 > least;  // some row does not see some of these keys
+    float top[NT][2], inverse[2];
 #pragma unroll
-    for (int nt = 0; nt < 2 * KB; ++nt) {
-        const int group = 2 * KB * kw + nt;
-        const uint32_t kb = scale_bits(
-            reinterpret_cast<const uint32_t *>(&scales.four[0][group])[scales.at[0][group]]);
-        const uint32_t vb = scale_bits(
-            reinterpret_cast<const uint32_t *>(&scales.four[1][group])[scales.at[1][group]]);
+    for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {  // the lane's keys of each 16 share their scales
+        const int group = group0 + 2 * h + (at.g >> 2);
+        uint32_t four = scales + group * 16 + hh * 4, four_v = four + 16 * kG;
+        if constexpr (C::kHeads != 4) {  // TileScales8: four[2][kG], then at[2][kG]
+            const uint32_t which = scales + 32 * kG + group * 4;
+            four += lds4(which) * 4;
+            four_v += lds4(which + 4 * kG) * 4;
+        }
+        const float kb = __uint_as_float(scale_bits(lds4(four)));
+        const uint32_t vb = scale_bits(lds4(four_v));
         const float add = (float)((int)(vb >> 23) - 127);
-        inverse[nt] = __uint_as_float(inverse_bits(vb));
+        inverse[h] = __uint_as_float(inverse_bits(vb));
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            const float by = unit[p] * __uint_as_float(kb);
-            f2_split(f2_fma(f2_make(s[nt][2 * p], s[nt][2 * p + 1]), f2_make(by, by),
-                            f2_make(add, add)),
-                     s[nt][2 * p], s[nt][2 * p + 1]);
-            if (key0 + 16 * KB > least) {  // some row does not see some of these keys
+        for (int n = 0; n < NT; ++n) {
+            const f32x2 unit = f2_mul(r.unit[n], f2_make(kb, kb));
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                    if (key0 + nt * 8 + c * 2 + e >= see[p]) s[nt][2 * p + e] = -INFINITY;
+            for (int x = 0; x < 2; ++x) {
+                float y[2];
+                f2_split(f2_fma(s[n][2 * h + x], unit, f2_make(add, add)), y[0], y[1]);
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    if (some && key0 + 16 * h + at.key + 2 * x >= r.see[n][p]) y[p] = -INFINITY;
+                    top[n][p] = fmaxf(top[n][p], y[p]);
+                }
+                s[n][2 * h + x] = f2_make(y[0], y[1]);
             }
-            top[p] = max3(top[p], s[nt][2 * p], s[nt][2 * p + 1]);
         }
     }
-    // Only when some score passes its row's limit are the row maxima needed. A row that
+    // Only when some score passes its row's maximum by 2^8 are the row maxima needed. A row that
     // has seen no key yet keeps m = -inf and sums of zero.
-    if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+    bool rise = false;
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
-            top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-            top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
-            if (!(top[p] > limit[p])) continue;
-            const float f = ex2(m[p] - top[p]);
-            m[p] = top[p];
-            limit[p] = top[p] + kRescaleLog2;
-            l2[p] = f2_mul(l2[p], f2_make(f, f));
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int d = 0; d < DH / 8; ++d) {
-                o[d][2 * p] *= f;
-                o[d][2 * p + 1] *= f;
+        for (int p = 0; p < 2; ++p) rise |= top[n][p] > r.m[n][p] + kRescaleLog2;
+    if (__any_sync(~0u, rise)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float t = top[n][p];
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, x));
+                const bool up = t > r.m[n][p] + kRescaleLog2;
+                f[p] = up ? ex2(r.m[n][p] - t) : 1.0f;
+                if (up) r.m[n][p] = t;
             }
+            r.off[n] = f2_make(r.m[n][0] == -INFINITY ? 0.0f : -r.m[n][0],
+                               r.m[n][1] == -INFINITY ? 0.0f : -r.m[n][1]);
+            r.l[n] = f2_mul(r.l[n], f2_make(f[0], f[1]));
+#pragma unroll
+            for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r.o[n][j][e] *= f[e & 1];
         }
     }
-    uint32_t pf[KB][4];
+    uint32_t pf[NT][4];  // the weights as the second product's second operand
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-        const float off = m[p] == -INFINITY ? 0.0f : -m[p];
-        const f32x2 off2 = f2_make(off, off);
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int nt = 0; nt < 2 * KB; ++nt) {
+        for (int x = 0; x < 4; ++x) {
             float e0, e1;
-            f2_split(f2_add(f2_make(s[nt][2 * p], s[nt][2 * p + 1]), off2), e0, e1);
+            f2_split(f2_add(s[n][x], r.off[n]), e0, e1);
             e0 = ex2(e0);
             e1 = ex2(e1);
-            l2[p] = f2_fma(f2_make(e0, e1), f2_make(inverse[nt], inverse[nt]), l2[p]);
-            pf[nt / 2][nt % 2 * 2 + p] = pack_f16(e0, e1);  // 2^-11 relative a term at most
+            s[n][x] = f2_make(e0, e1);
+            r.l[n] = f2_fma(s[n][x], f2_make(inverse[x >> 1], inverse[x >> 1]), r.l[n]);
+            pf[n][x] = transposed(pack_f16(e0, e1));  // 2^-11 relative at most
         }
-    }
-    // A draft that some row does not see: were its V NaN, a weight of 0 would not keep it
-    // from that row, so the block's product is made one by one.
-    if (key0 + 16 * KB > least) {
+    uint32_t live[2] = {~0u, ~0u};  // the lane's keys inside the sequence, a byte each
+    if (some) {
+        // A draft that some row does not see: were its V NaN, a weight of 0 would not keep it
+        // from that row, so the product is made one by one.
         bool nan = false;
-        const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
-        for (int x = lane; x < (hi - lo) * (DH / 16); x += 32) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(
-                v + (row0 + lo + x / (DH / 16)) * DH + x % (DH / 16) * 16);
+        const int from = max(least - key0, 0), to = min(len - key0, 32);
+        for (int x = lane; x < (to - from) * (DH / 16); x += 32) {
+            const uint4 w = lds16(v + at.at(from + x / (DH / 16), x % (DH / 16)));
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 nan |= (((word_of(w, e) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
         }
         if (__any_sync(~0u, nan)) {
-            product_one_by_one8<DH, KB>(o, pf, v, row0, key0, see);
+            product_one_by_one8<C>(r, s, v, at, key0);
             return;
         }
+        // Codes past the sequence may be NaN, which a weight of 0 would not silence.
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            live[h] = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (key0 + 16 * h + at.key_of(2 * at.c + (i & 1) + 4 * (i & 2)) < len)
+                    live[h] |= 0xFFu << 8 * i;
+        }
     }
-    constexpr int VW = DH / 32;  // words of DH / 8 codes
 #pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        uint32_t w[4][VW];  // of the keys 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int r = 2 * c + (x & 1) + (x & 2) * 4;
-            if constexpr (DH == 64) {
-                const uint2 u = *reinterpret_cast<const uint2 *>(
-                    v + (row0 + kb * 16) * DH + swz8<DH>(r, g >> 1) + (g & 1) * 8);
-                w[x][0] = u.x;
-                w[x][1] = u.y;
-            } else {
-                const uint4 u = *reinterpret_cast<const uint4 *>(
-                    v + (row0 + kb * 16) * DH + swz8<DH>(r, g));
-#pragma unroll
-                for (int e = 0; e < VW; ++e) w[x][e] = word_of(u, e);
-            }
-            // Codes past the sequence may be NaN, which a weight of 0 would not silence.
-            if (key0 + 16 * KB > len && key0 + kb * 16 + r >= len)
-#pragma unroll
-                for (int e = 0; e < VW; ++e) w[x][e] = 0;
+    for (int j = 0; j < DH / 16; ++j) {
+        uint32_t w[4];
+        ldsm2_t8(w, v + (at.v_at ^ j * 16));
+        if (some) {
+            w[0] &= live[0];
+            w[1] &= live[0];
+            w[2] &= live[1];
+            w[3] &= live[1];
         }
 #pragma unroll
-        for (int e = 0; e < VW; ++e) {
-            const uint32_t a0 = __byte_perm(w[0][e], w[1][e], 0x5140);
-            const uint32_t a1 = __byte_perm(w[0][e], w[1][e], 0x7362);
-            const uint32_t b0 = __byte_perm(w[2][e], w[3][e], 0x5140);
-            const uint32_t b1 = __byte_perm(w[2][e], w[3][e], 0x7362);
-            mma16816_f16(o[4 * e], pf[kb], e4m3x2_f16x2(a0), e4m3x2_f16x2(b0));
-            mma16816_f16(o[4 * e + 1], pf[kb], e4m3x2_f16x2_hi(a0), e4m3x2_f16x2_hi(b0));
-            mma16816_f16(o[4 * e + 2], pf[kb], e4m3x2_f16x2(a1), e4m3x2_f16x2(b1));
-            mma16816_f16(o[4 * e + 3], pf[kb], e4m3x2_f16x2_hi(a1), e4m3x2_f16x2_hi(b1));
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {e4m3x2_f16x2(w[2 * h]), e4m3x2_f16x2(w[2 * h + 1]),
+                                   e4m3x2_f16x2_hi(w[2 * h]), e4m3x2_f16x2_hi(w[2 * h + 1])};
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+                mma16816_f16(r.o[n][j], a, pf[n][2 * h], pf[n][2 * h + 1]);
+        }
+    }
+}
+
+// A consumer warp's part of k_own over an 8-bit cache.
+template <typename C>
+__device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnSmem<C> &s) {
+    constexpr int DH = C::kDh, ST = C::kStages, QB = C::kQBufs, KG = C::KG, WR = C::WR, NT = C::NT;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kw = warp % KG, rg = warp / KG % C::RG, hh = warp / (KG * C::RG);
+    const Lane8<C> at(hh, kw * 32);
+    uint32_t ring_at = 0, ring_phase = 0;
+    bool dead = false;
+    for (uint32_t items = 0;; ++items) {
+        const uint32_t qb = items % QB;
+        const bool ready = !dead && mbar_wait_bounded(&s.qfull[qb], (items / QB) & 1u);
+        // Where key groups join, the warps go on together or not at all: none waits at a
+        // barrier the others left.
+        if (KG > 1 ? named_or(1, 32 * C::kWarps, !ready) : !ready) {
+            if (!ready && !dead) raise_error(SC_DEV_TIMEOUT);
+            return;
+        }
+        const OwnItem item = s.item[qb];
+        if (item.n == 0) return;
+        const int len = item.len, least = len - a.D + 1;  // keys that every row sees
+        const int row0 = item.rt * C::MR + rg * WR;       // of the sequence's rows of a head
+        Rows8<C> r;
+        r.load(s.qs_a + (qb * C::kHeads + hh) * C::kQ + rg * WR * 128, a.scale_log2);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const int rr = row0 + n * 8 + 2 * at.c + p;
+                r.see[n][p] = rr < rows ? least + rr / a.G : INT_MIN / 2;
+                r.m[n][p] = -INFINITY;
+            }
+            r.l[n] = r.off[n] = f2_make(0.0f, 0.0f);
+#pragma unroll
+            for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r.o[n][j][e] = 0.0f;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.qempty[qb]);
+        bool bad = false;
+        const int from = prefix_keys(a, len);
+        int key0 = from + item.t0 * C::KT + kw * 32;
+        for (int t = 0; t < item.n; ++t, key0 += C::KT) {
+            if (!dead && !mbar_wait_bounded(&s.full[ring_at], ring_phase)) {
+                raise_error(SC_DEV_TIMEOUT);
+                dead = true;  // no more waits: the rest runs through on what is there
+            }
+            bad |= s.bad[ring_at] != 0;
+            tile8<C>(s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh, kw * 4,
+                     key0, len, least, r);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s.empty[ring_at]);
+            if (++ring_at == ST) {
+                ring_at = 0;
+                ring_phase ^= 1u;
+            }
+        }
+        const bool whole = item.n == item.T && from == 0;  // nothing to join with
+        float *part = a.own_part + ((int64_t)(item.w + blockIdx.x) * C::kHeads + hh) * C::kSlot;
+        bf16 *out = a.out + ((int64_t)item.i * a.D * a.Hkv + item.h + hh) * a.G * DH;
+        auto out_row = [&](int rr) {
+            return out + ((int64_t)(rr / a.G) * a.Hkv * a.G + rr % a.G) * DH;
+        };
+        // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
+        auto put_part = [&](int row, int col, float x) {
+            gst(part + (rg * WR + row) * DH + col, x);
+        };
+        auto put_sums = [&](int row, float m, float l) {
+            gst(part + C::MR * DH + rg * WR + row, bad ? __int_as_float(0x7FC00000) : m);
+            gst(part + C::MR * DH + C::MR + rg * WR + row, l);
+        };
+        auto inverse_of = [](float l) { return l > 0.0f ? 1.0f / l : l == 0.0f ? 0.0f : l; };
+        [[maybe_unused]] float *jm = s.join + C::kWarps * WR * C::kOs;  // [warp][m, l]
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float l[2], inv[2];
+            f2_split(r.l[n], l[0], l[1]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) l[p] += __shfl_xor_sync(~0u, l[p], x);
+                inv[p] = inverse_of(l[p]);
+            }
+            const int row = n * 8 + 2 * at.c;  // and the next
+            if (KG > 1 || !whole) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    if (KG == 1 && row0 + row + p >= rows) continue;
+#pragma unroll
+                    for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int col = 16 * j + 8 * h + at.g;
+                            const float x = r.o[n][j][2 * h + p];
+                            if constexpr (KG > 1)
+                                s.join[(warp * WR + row + p) * C::kOs + col] = x;
+                            else
+                                put_part(row + p, col, x);
+                        }
+                    if (at.g != 0) continue;
+                    if constexpr (KG > 1) {
+                        jm[warp * 2 * WR + row + p] = r.m[n][p];
+                        jm[(warp * 2 + 1) * WR + row + p] = l[p];
+                    } else {
+                        put_sums(row + p, r.m[n][p], l[p]);
+                    }
+                }
+            } else {
+                // Pairs of rows become pairs of columns: lane 4 g + c has row g's.
+                const int rr = row0 + n * 8 + at.g;
+#pragma unroll
+                for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t two =
+                            transposed(pack_bf16(r.o[n][j][2 * h] * inv[0],
+                                                 r.o[n][j][2 * h + 1] * inv[1]));
+                        if (rr < rows && !bad)
+                            gst(reinterpret_cast<uint32_t *>(out_row(rr) + 16 * j + 8 * h +
+                                                             2 * at.c),
+                                two);
+                    }
+            }
+        }
+        if constexpr (KG > 1) {
+            // The key groups of a head and row group join: a thread four columns of a row.
+            // (The next join comes after the next item's barrier.)
+            named_sync(1, 32 * C::kWarps);
+            const int w0 = warp - kw;
+            for (int x = kw * 32 + lane; x < WR * DH / 4; x += 32 * KG) {
+                const int row = x / (DH / 4), col = x % (DH / 4) * 4, rr = row0 + row;
+                float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+                for (int q = 0; q < KG; ++q) top = fmaxf(top, jm[(w0 + q) * 2 * WR + row]);
+                const float off = top == -INFINITY ? 0.0f : top;
+                float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int q = 0; q < KG; ++q) {
+                    const float f = ex2(jm[(w0 + q) * 2 * WR + row] - off);
+                    const float4 u = *reinterpret_cast<float4 *>(
+                        s.join + ((w0 + q) * WR + row) * C::kOs + col);
+                    sum = fmaf(f, jm[((w0 + q) * 2 + 1) * WR + row], sum);
+                    v.x = fmaf(f, u.x, v.x);
+                    v.y = fmaf(f, u.y, v.y);
+                    v.z = fmaf(f, u.z, v.z);
+                    v.w = fmaf(f, u.w, v.w);
+                }
+                if (rr >= rows) continue;
+                if (!whole) {
+                    gst(reinterpret_cast<float4 *>(part + (rg * WR + row) * DH + col), v);
+                    if (col == 0) put_sums(row, top, sum);
+                } else if (!bad) {
+                    const float inv = inverse_of(sum);
+                    gst(reinterpret_cast<uint2 *>(out_row(rr) + col),
+                        make_uint2(pack_bf16(v.x * inv, v.y * inv), pack_bf16(v.z * inv, v.w * inv)));
+                }
+            }
         }
     }
 }
