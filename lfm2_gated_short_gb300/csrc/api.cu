@@ -193,10 +193,16 @@ struct Scales {
 // Shape of an 8-bit cache, with a page_size that check_pages takes (or will refuse).
 sc_status check_8bit(int Hkv, int Dh, int block, int page_size) {
     if (Hkv <= 0 || Dh <= 0 || block <= 0) return SC_EINVAL;
-    if (Dh % 16 != 0 || (int64_t)Hkv * Dh > (1 << 24) || block < 8 || (block & (block - 1)) != 0 ||
+    if (Dh % 16 != 0 || Dh > 1024 || (int64_t)Hkv * Dh > (1 << 24) || block < 8 || (block & (block - 1)) != 0 ||
         block > page_size)
         return SC_EUNSUPPORTED;
     return SC_OK;
+}
+
+int log2_of(int x) {
+    int n = 0;
+    while (x >> (n + 1)) ++n;
+    return n;
 }
 
 // Whether some row of one array (rows of wa bytes, sa apart) meets a row of another, each of
@@ -374,9 +380,7 @@ sc_status prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, int block, c
     SC_BOUNDS_INSTALL(kUnitAttention, RO(q, n_q), RO(k_pages, n_pool), RO(v_pages, n_pool),
                       RO(table, n_t), RO(lens, n_l), RO(slot_ids, n_i), RW(out, n_out),
                       RW(workspace, need), RO(k_scales, n_sc), RO(v_scales, n_sc));
-    int block_log2 = 0;
-    while (block >> (block_log2 + 1)) ++block_log2;
-    const sc::Scales8 scales = {k_scales, v_scales, block_log2};
+    const sc::Scales8 scales = {k_scales, v_scales, log2_of(block)};
     return from_cuda(sc::launch_prefix_attention(
         shape, q, q_stride, k_pages, v_pages, block ? &scales : nullptr,
         {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
@@ -899,7 +903,7 @@ sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block
         {nullptr, const_cast<int32_t *>(table), const_cast<int32_t *>(lens), n_pages, n_slots,
          max_pages, page_size},
         k, k_stride, v, v_stride, slot_ids, N, D,
-        {k_pages, v_pages, k_scales, v_scales, Hkv, Dh, block}, (cudaStream_t)stream));
+        {k_pages, v_pages, k_scales, v_scales, Hkv, Dh, log2_of(block)}, (cudaStream_t)stream));
 }
 
 sc_status shortconv_pages_read_8bit(sc_dtype dtype, int Hkv, int Dh, int block,
@@ -943,7 +947,7 @@ sc_status shortconv_pages_read_8bit(sc_dtype dtype, int Hkv, int Dh, int block,
          max_pages, page_size},
         slot_ids, cu_seqlens, starts, N, T,
         {const_cast<void *>(k_pages), const_cast<void *>(v_pages), const_cast<float *>(k_scales),
-         const_cast<float *>(v_scales), Hkv, Dh, block},
+         const_cast<float *>(v_scales), Hkv, Dh, log2_of(block)},
         k, v, sms, (cudaStream_t)stream));
 }
 

@@ -6,6 +6,8 @@
 // those tokens' codes to it.
 #include <cuda_bf16.h>
 
+#include <limits.h>
+
 #include "common.cuh"
 #include "e4m3.cuh"
 #include "errors.cuh"
@@ -17,7 +19,6 @@ namespace sc {
 
 constexpr int kAppendThreads = 256;
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 32;  // rows of a tile
 
 __device__ __forceinline__ int slot_length(const PageTable &pt, int slot, bool report) {
     if (slot < 0 || slot >= pt.n_slots) {
@@ -32,7 +33,7 @@ __device__ __forceinline__ int slot_length(const PageTable &pt, int slot, bool r
     return len;
 }
 
-// Eight values of a row as fp32.
+// Eight values of a row.
 template <typename T>
 struct Eight {
     Row<T> r;
@@ -40,11 +41,23 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < Dt<T>::Q; ++i) r.q[i] = ld_plain(reinterpret_cast<const uint4 *>(p) + i);
     }
-    // The largest magnitude's fp32 bits; infinities and NaN do not count.
-    __device__ __forceinline__ uint32_t most() const {
+    // The largest magnitude's bits, of bf16 in both halves of a word: infinities and NaN lie above
+    // all finite ones.
+    __device__ __forceinline__ uint32_t most(uint32_t m) const {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(r.q);
+#pragma unroll
+        for (int e = 0; e < 4 * Dt<T>::Q; ++e) {
+            if constexpr (sizeof(T) == 2)
+                asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7FFF7FFFu));
+            else
+                m = max(m, w[e] & 0x7FFFFFFFu);
+        }
+        return m;
+    }
+    // The same without them, as fp32 bits.
+    __device__ __forceinline__ uint32_t most_finite(uint32_t m) const {
         float f[kCh];
         Dt<T>::unpack(r.q, f);
-        uint32_t m = 0;
 #pragma unroll
         for (int e = 0; e < kCh; ++e) {
             const uint32_t b = __float_as_uint(f[e]) & 0x7FFFFFFFu;
@@ -58,7 +71,26 @@ struct Eight {
         uint32_t w[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = f32_e4m3x2(f[2 * e] * inverse, f[2 * e + 1] * inverse);
-        return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
+        return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+    }
+};
+
+// A lane's places among a block's rows of `per` eights: lane, lane + 32, ...
+struct Places {
+    int per, row, col, drow, dcol;
+    __device__ __forceinline__ Places(int per_, int lane) : per(per_) {
+        row = lane / per;
+        col = lane - row * per;
+        drow = 32 / per;
+        dcol = 32 - drow * per;
+    }
+    __device__ __forceinline__ void next() {
+        row += drow;
+        col += dcol;
+        if (col >= per) {
+            col -= per;
+            ++row;
+        }
     }
 };
 
@@ -72,169 +104,227 @@ __global__ void __launch_bounds__(kAppendThreads)
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int64_t unit = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (unit >= (int64_t)N * nb * 2 * c.Hkv) return;
-    const int h = (int)(unit % c.Hkv);
-    const int64_t rest = unit / c.Hkv;
+    // The call's units are below 2^28.
+    const uint32_t unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
+    const uint32_t rest = unit / (uint32_t)c.Hkv, pair = rest >> 1;
+    const int h = (int)(unit - rest * c.Hkv), i = (int)(pair / (uint32_t)nb);
+    const int b = (int)(pair - (uint32_t)i * nb);
     const bool is_v = rest & 1;
-    const int b = (int)((rest >> 1) % nb), i = (int)((rest >> 1) / nb);
+    if (i >= N) return;
     const int slot = gld(slots + i);
     const int len = slot_length(pt, slot, lane == 0);
     if (len < 0) return;
     const int first = len - D;  // position of the first new token
     if (first < 0 && lane == 0) raise_error(SC_DEV_BAD_LENGTH);
-    const int from = max(first, 0), B = c.block, ps = pt.page_size;
-    const int64_t b0 = (int64_t)(from / B + b) * B;
+    const int lb = c.block_log2, lp = __ffs(pt.page_size) - 1, from = max(first, 0);
+    const int64_t b0 = ((int64_t)(from >> lb) + b) << lb;
     if (b0 >= len) return;
-    const int lo = max((int)b0, from), hi = (int)min(b0 + B, (int64_t)len);
-    const int id = gld(pt.table + (int64_t)slot * pt.max_pages + (int)b0 / ps);
+    const int lo = max((int)b0, from), hi = (int)min(b0 + (1 << lb), (int64_t)len);
+    const int id = gld(pt.table + (int64_t)slot * pt.max_pages + ((int)b0 >> lp));
     if (id < 0 || id >= pt.n_pages) {
         if (lane == 0) raise_error(SC_DEV_BAD_PAGE);
         return;
     }
-    const int r0 = (int)b0 % ps;
+    const int r0 = (int)b0 & (pt.page_size - 1);
     const int64_t width = (int64_t)c.Hkv * c.Dh;
     unsigned char *codes = (unsigned char *)(is_v ? c.v : c.k) +
-                           ((int64_t)id * ps + r0) * width + h * c.Dh;  // of the block's first token
+                           (((int64_t)id << lp) + r0) * width + h * c.Dh;  // of the block's first token
     uint32_t *scale = reinterpret_cast<uint32_t *>(is_v ? c.v_scales : c.k_scales) +
-                      ((int64_t)id * (ps / B) + r0 / B) * c.Hkv + h;
+                      (((int64_t)id << (lp - lb)) + (r0 >> lb)) * c.Hkv + h;
     const int64_t stride = is_v ? v_stride : k_stride;
     const T *x = (is_v ? v : k) + ((int64_t)i * D + (lo - first)) * stride + h * c.Dh;
-    const int per = c.Dh / 8, n = (hi - lo) * per;  // eights of a row, and of the new rows
-    constexpr int kKeep = 4;                        // a lane's first eights stay in registers
+    const int n = hi - lo;  // new rows
+    constexpr int kKeep = sizeof(T) == 2 ? 8 : 4;  // a lane's first eights stay in registers
     Eight<T> keep[kKeep];
-    uint32_t most = 0;
+    Places at(c.Dh / 8, lane);
 #pragma unroll
-    for (int q = 0; q < kKeep; ++q) {
-        const int e = lane + 32 * q;
-        if (e < n) keep[q].load(x + (int64_t)(e / per) * stride + e % per * 8);
-    }
+    for (int q = 0; q < kKeep; ++q, at.next())
+        if (at.row < n) keep[q].load(x + at.row * stride + at.col * 8);
+    // Every eight of the block, the kept ones first: f(eight, row, column).
+    auto each = [&](auto &&f) {
+        Places p(c.Dh / 8, lane);
+#pragma unroll
+        for (int q = 0; q < kKeep; ++q, p.next())
+            if (p.row < n) f(keep[q], p.row, p.col);
+        for (; p.row < n; p.next()) {
+            Eight<T> u;
+            u.load(x + p.row * stride + p.col * 8);
+            f(u, p.row, p.col);
+        }
+    };
     const uint32_t was = lo > b0 ? scale_bits(gld(scale)) : 0u;
-#pragma unroll
-    for (int q = 0; q < kKeep; ++q)
-        if (lane + 32 * q < n) most = max(most, keep[q].most());
-    for (int e = lane + 32 * kKeep; e < n; e += 32) {
-        Eight<T> u;
-        u.load(x + (int64_t)(e / per) * stride + e % per * 8);
-        most = max(most, u.most());
+    uint32_t most = 0;
+    each([&](const Eight<T> &u, int, int) { most = u.most(most); });
+    if (sizeof(T) == 2) most = max(most & 0xFFFF0000u, most << 16);
+    most = __reduce_max_sync(~0u, most);
+    if (most >= 0x7F800000u) {
+        most = 0;
+        each([&](const Eight<T> &u, int, int) { most = u.most_finite(most); });
+        most = __reduce_max_sync(~0u, most);
     }
-    const uint32_t need = scale_for(__reduce_max_sync(~0u, most));
-    const uint32_t now = max(need, was);
+    const uint32_t now = max(scale_for(most), was);
     if (lane == 0) gst(scale, now);
     const float inverse = __uint_as_float(inverse_bits(now));
     unsigned char *to = codes + (lo - b0) * width;
-#pragma unroll
-    for (int q = 0; q < kKeep; ++q) {
-        const int e = lane + 32 * q;
-        if (e < n)
-            gst(reinterpret_cast<uint2 *>(to + (e / per) * width + e % per * 8),
-                keep[q].codes(inverse));
-    }
-    for (int e = lane + 32 * kKeep; e < n; e += 32) {
-        Eight<T> u;
-        u.load(x + (int64_t)(e / per) * stride + e % per * 8);
-        gst(reinterpret_cast<uint2 *>(to + (e / per) * width + e % per * 8), u.codes(inverse));
-    }
+    each([&](const Eight<T> &u, int row, int col) {
+        gst(reinterpret_cast<uint2 *>(to + row * width + col * 8), u.codes(inverse));
+    });
     if (lo == b0 || now == was) return;
     const float step = __uint_as_float(was) * inverse;  // 2^-184 at least: exact or zero
-    for (int e = lane; e < (int)(lo - b0) * per; e += 32) {
-        uint2 *p = reinterpret_cast<uint2 *>(codes + (e / per) * width + e % per * 8);
-        const uint2 w = gld(p);
+    for (Places p(c.Dh / 8, lane); p.row < (int)(lo - b0); p.next()) {
+        uint2 *q = reinterpret_cast<uint2 *>(codes + p.row * width + p.col * 8);
+        const uint2 w = gld(q);
         uint32_t out[2];
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-            const uint32_t two = q ? w.y : w.x;
-            const uint32_t a = e4m3x2_f16x2(two), z = e4m3x2_f16x2_hi(two);
-            out[q] = f32_e4m3x2(f16_lo(a) * step, f16_hi(a) * step) |
+        for (int e = 0; e < 2; ++e) {
+            const uint32_t four = e ? w.y : w.x;
+            const uint32_t a = e4m3x2_f16x2(four), z = e4m3x2_f16x2_hi(four);
+            out[e] = f32_e4m3x2(f16_lo(a) * step, f16_hi(a) * step) |
                      f32_e4m3x2(f16_lo(z) * step, f16_hi(z) * step) << 16;
         }
-        gst(p, make_uint2(out[0], out[1]));
+        gst(q, make_uint2(out[0], out[1]));
     }
 }
 
-// Rows cu[i] .. cu[i + 1] - 1 are sequence i's tokens from starts[i] on. A tile's rows find
-// their pages first, then all threads stream 16 codes at a time.
+// A word of codes is what becomes 16 bytes of values: 8 codes in bf16, 4 in fp32.
 template <typename T>
-__global__ void __launch_bounds__(kReadThreads)
+struct Codes;
+template <>
+struct Codes<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    typedef uint2 Word;
+    static __device__ __forceinline__ uint4 values(uint2 w, uint32_t scale) {
+        // The scale is a power of two: multiplying after the conversion is exact too.
+        const uint32_t s = scale >> 16 | (scale & 0xFFFF0000u);
+        uint32_t out[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t four = e < 2 ? w.x : w.y;
+            const uint32_t h = e & 1 ? e4m3x2_f16x2_hi(four) : e4m3x2_f16x2(four);
+            out[e] = bf2_mul(pack_bf16(f16_lo(h), f16_hi(h)), s);
+        }
+        return make_uint4(out[0], out[1], out[2], out[3]);
+    }
+};
+template <>
+struct Codes<float> {
+    static constexpr int kN = 4;
+    typedef uint32_t Word;
+    static __device__ __forceinline__ uint4 values(uint32_t w, uint32_t scale) {
+        const float s = __uint_as_float(scale);
+        const uint32_t a = e4m3x2_f16x2(w), z = e4m3x2_f16x2_hi(w);
+        return make_uint4(__float_as_uint(f16_lo(a) * s), __float_as_uint(f16_hi(a) * s),
+                          __float_as_uint(f16_lo(z) * s), __float_as_uint(f16_hi(z) * s));
+    }
+};
+
+// Rows cu[i] .. cu[i + 1] - 1 are sequence i's tokens from starts[i] on. A warp takes R rows of
+// both pools at a time, lane r finds row r's place, and the next rows' places are looked
+// for (a chain of dependent reads) while these rows' codes are on their way.
+template <typename T>
+__global__ void __launch_bounds__(kReadThreads, 4)
     k_read8(PageTable pt, const int32_t *__restrict__ slots, const int32_t *__restrict__ cu,
-            const int32_t *__restrict__ starts, int N, int64_t rows, Cache8 c, T *__restrict__ k,
-            T *__restrict__ v) {
-    __shared__ int64_t s_row[kReadRows];    // row of the pools, or -1
-    __shared__ int64_t s_block[kReadRows];  // its block
-    __shared__ int s_bad;
+            const int32_t *__restrict__ starts, int N, int rows, int R, uint32_t head_magic,
+            Cache8 c, T *__restrict__ k, T *__restrict__ v) {
+    typedef typename Codes<T>::Word Word;
+    constexpr int kN = Codes<T>::kN;
     pdl_wait();
     pdl_launch_dependents();
-    const int tid = threadIdx.x;
-    if (tid == 0) s_bad = 0;
-    __syncthreads();
+    const int tid = threadIdx.x, lane = tid & 31;
+    bool bad = false;
     for (int i = tid; i <= N; i += kReadThreads) {
         const int at = gld(cu + i), before = i > 0 ? gld(cu + i - 1) : 0;
-        if (at < before || (i == 0 && at != 0) || (i == N && at != rows)) s_bad = 1;
+        bad |= at < before || (i == 0 && at != 0) || (i == N && at != rows);
     }
-    __syncthreads();
-    if (s_bad) {
+    if (__syncthreads_or(bad)) {
         if (tid == 0 && blockIdx.x == 0) raise_error(SC_DEV_BAD_SEQLENS);
         return;
     }
-    const int per = c.Hkv * c.Dh / 16, ps = pt.page_size, blocks = ps / c.block;
-    for (int64_t r0 = (int64_t)blockIdx.x * kReadRows; r0 < rows;
-         r0 += (int64_t)gridDim.x * kReadRows) {
-        const int here = (int)min((int64_t)kReadRows, rows - r0);
-        __syncthreads();
-        if (tid < here) {
-            const int r = (int)r0 + tid;
-            int i = 0, top = N;  // the last i with cu[i] <= r
+    const int per = c.Hkv * c.Dh / kN;  // words of a row
+    const int lb = c.block_log2, lp = __ffs(pt.page_size) - 1;
+    const int ends = lane < N ? gld(cu + lane + 1) : INT_MAX;  // of the first 32 sequences
+    // Lane r: the row of the pools of row r0 + r, -1 for one that is left alone.
+    auto find = [&](int64_t r0) {
+        int i = 0;
+        if (N <= 32) {
+            for (int r = 0; r < R; ++r) {
+                const int before = __popc(__ballot_sync(~0u, ends <= r0 + r));
+                if (r == lane) i = before;
+            }
+        }
+        if (lane >= R || r0 + lane >= rows) return -1;
+        const int r = (int)r0 + lane;
+        if (N > 32) {
+            int top = N;  // the last i with cu[i] <= r
             while (top - i > 1) {
                 const int mid = (i + top) >> 1;
                 if (gld(cu + mid) <= r) i = mid;
                 else top = mid;
             }
-            const int slot = gld(slots + i), begin = gld(cu + i), end = gld(cu + i + 1);
-            const int len = slot_length(pt, slot, true);
-            const int start = starts != nullptr ? gld(starts + i) : 0;
-            int64_t at = -1, block = 0;
-            if (len >= 0 && (start < 0 || (int64_t)start + end - begin > len)) {
-                raise_error(SC_DEV_BAD_LENGTH);
-            } else if (len >= 0) {
-                const int pos = start + (r - begin);
-                const int id = gld(pt.table + (int64_t)slot * pt.max_pages + pos / ps);
-                if (id < 0 || id >= pt.n_pages) {
-                    raise_error(SC_DEV_BAD_PAGE);
-                } else {
-                    at = (int64_t)id * ps + pos % ps;
-                    block = (int64_t)id * blocks + pos % ps / c.block;
-                }
-            }
-            s_row[tid] = at;
-            s_block[tid] = block;
         }
-        __syncthreads();
-        for (int x = tid; x < here * 2 * per; x += kReadThreads) {
-            const int r = x / (2 * per), y = x - r * 2 * per;
-            const bool is_v = y >= per;
-            const int q = is_v ? y - per : y, h = q * 16 / c.Dh;
-            const int64_t at = s_row[r];
-            if (at < 0) continue;
-            const uint4 w = ld_plain((const uint4 *)(is_v ? c.v : c.k) + at * per + q);
-            const float s = __uint_as_float(scale_bits(
-                gld(reinterpret_cast<const uint32_t *>(is_v ? c.v_scales : c.k_scales) +
-                    s_block[r] * c.Hkv + h)));
-            T *to = (is_v ? v : k) + ((r0 + r) * per + q) * 16;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float f[kCh];
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const uint32_t four = e ? (u ? w.w : w.z) : (u ? w.y : w.x);
-                    const uint32_t a = e4m3x2_f16x2(four), z = e4m3x2_f16x2_hi(four);
-                    f[4 * u] = f16_lo(a) * s;
-                    f[4 * u + 1] = f16_hi(a) * s;
-                    f[4 * u + 2] = f16_lo(z) * s;
-                    f[4 * u + 3] = f16_hi(z) * s;
-                }
-                store_row<T>(to + e * kCh, f);
-            }
+        const int slot = gld(slots + i), begin = gld(cu + i), end = gld(cu + i + 1);
+        const int start = starts != nullptr ? gld(starts + i) : 0;
+        const int len = slot_length(pt, slot, true);
+        if (len < 0) return -1;
+        if (start < 0 || (int64_t)start + end - begin > len) {
+            raise_error(SC_DEV_BAD_LENGTH);
+            return -1;
         }
+        const int pos = start + (r - begin);
+        const int id = gld(pt.table + (int64_t)slot * pt.max_pages + (pos >> lp));
+        if (id < 0 || id >= pt.n_pages) {
+            raise_error(SC_DEV_BAD_PAGE);
+            return -1;
+        }
+        return (id << lp) + (pos & (pt.page_size - 1));  // n_pages * page_size < 2^31
+    };
+    const int64_t step = (int64_t)gridDim.x * (kReadThreads / 32) * R;
+    int64_t r0 = ((int64_t)blockIdx.x * (kReadThreads / 32) + (tid >> 5)) * R;
+    int here = find(r0);
+    constexpr int kAhead = 4;  // words of a lane in flight
+    // Word w of a unit: row r, word x of its K or V, of head h. With several rows a unit is
+    // one round of the loop below, and a lane's words are the same in each.
+    struct Word4 {
+        int r, x, h;
+        bool v, live;
+    };
+    auto word = [&](int w) {
+        Word4 u;
+        u.r = R == 1 ? 0 : w / (2 * per);
+        const int y = w - u.r * 2 * per;
+        u.live = y < 2 * per && u.r < R;
+        u.v = y >= per;
+        u.x = u.v ? y - per : y;
+        u.h = __umulhi((uint32_t)u.x, head_magic);
+        return u;
+    };
+    Word4 fixed[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) fixed[q] = word(32 * q + lane);
+    for (; r0 < rows; r0 += step) {
+        int next = -1;
+        for (int w0 = 0; w0 < 2 * R * per; w0 += 32 * kAhead) {
+            Word code[kAhead];
+            uint32_t scale[kAhead];
+            T *to[kAhead];
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q) {
+                const Word4 u = w0 == 0 ? fixed[q] : word(w0 + 32 * q + lane);
+                const int row = __shfl_sync(~0u, here, u.r & 31);
+                to[q] = nullptr;
+                if (!u.live || row < 0) continue;
+                code[q] = gld((const Word *)(u.v ? c.v : c.k) + (int64_t)row * per + u.x);
+                scale[q] = gld(reinterpret_cast<const uint32_t *>(u.v ? c.v_scales : c.k_scales) +
+                               (int64_t)(row >> lb) * c.Hkv + u.h);
+                to[q] = (u.v ? v : k) + ((r0 + u.r) * per + u.x) * kN;
+            }
+            if (w0 == 0) next = find(r0 + step);
+#pragma unroll
+            for (int q = 0; q < kAhead; ++q)
+                if (to[q] != nullptr)
+                    st_stream(to[q], Codes<T>::values(code[q], scale_bits(scale[q])));
+        }
+        here = next;
     }
 }
 
@@ -244,7 +334,7 @@ template <typename T>
 static cudaError_t append8(const PageTable &pt, const void *k, int64_t k_stride, const void *v,
                            int64_t v_stride, const int32_t *slots, int N, int D, const Cache8 &c,
                            cudaStream_t stream) {
-    const int nb = (int)(((int64_t)D + 2 * c.block - 2) / c.block);  // blocks that D tokens meet at most
+    const int nb = (int)(((int64_t)D + 2 * (1 << c.block_log2) - 2) >> c.block_log2);  // blocks that D tokens meet at most
     const int64_t threads = (int64_t)N * nb * 2 * c.Hkv * 32;
     return launch_pdl(k_append8<T>, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)),
                       dim3(kAppendThreads), 0, stream, pt, (const T *)k, k_stride, (const T *)v,
@@ -259,16 +349,28 @@ cudaError_t launch_append8(int dtype, const PageTable &pt, const void *k, int64_
                : append8<float>(pt, k, k_stride, v, v_stride, slots, N, D, c, stream);
 }
 
+template <typename T>
+static cudaError_t read8(const PageTable &pt, const int32_t *slots, const int32_t *cu,
+                         const int32_t *starts, int N, int rows, const Cache8 &c, void *k, void *v,
+                         int sm_count, cudaStream_t stream) {
+    // A warp's rows: up to 128 words at once, four a lane.
+    const int per = c.Hkv * c.Dh / Codes<T>::kN, of_head = c.Dh / Codes<T>::kN;
+    const int R = per >= 64 ? 1 : 64 / per;
+    const uint32_t magic = (uint32_t)((1ull << 32) / of_head) + 1;  // words below 2^22, Dh <= 1024
+    const int64_t warps = (rows + R - 1) / R, blocks = (warps * 32 + kReadThreads - 1) / kReadThreads;
+    const int64_t most = 4ll * sm_count;
+    return launch_pdl(k_read8<T>, dim3((unsigned)(blocks < 1 ? 1 : blocks < most ? blocks : most)),
+                      dim3(kReadThreads), 0, stream, pt, slots, cu, starts, N, rows, R, magic, c,
+                      (T *)k, (T *)v);
+}
+
 cudaError_t launch_read8(int dtype, const PageTable &pt, const int32_t *slots, const int32_t *cu,
                          const int32_t *starts, int N, int64_t rows, const Cache8 &c, void *k,
                          void *v, int sm_count, cudaStream_t stream) {
-    const int64_t tiles = (rows + kReadRows - 1) / kReadRows, most = 8ll * sm_count;
-    const dim3 grid((unsigned)(tiles < 1 ? 1 : tiles < most ? tiles : most));
-    if (dtype == SC_BF16)
-        return launch_pdl(k_read8<__nv_bfloat16>, grid, dim3(kReadThreads), 0, stream, pt, slots,
-                          cu, starts, N, rows, c, (__nv_bfloat16 *)k, (__nv_bfloat16 *)v);
-    return launch_pdl(k_read8<float>, grid, dim3(kReadThreads), 0, stream, pt, slots, cu, starts, N,
-                      rows, c, (float *)k, (float *)v);
+    return dtype == SC_BF16 ? read8<__nv_bfloat16>(pt, slots, cu, starts, N, (int)rows, c, k, v,
+                                                   sm_count, stream)
+                            : read8<float>(pt, slots, cu, starts, N, (int)rows, c, k, v, sm_count,
+                                           stream);
 }
 
 cudaError_t take_error_cache8(cudaStream_t stream, unsigned int *sum) {

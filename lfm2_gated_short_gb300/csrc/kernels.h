@@ -125,11 +125,11 @@ cudaError_t launch_pages_append(const PageTable &pt, const void *k, int64_t k_st
 cudaError_t take_error_pages(cudaStream_t stream, unsigned int *sum);
 
 // The 8-bit cache (cache8.cu): pools of e4m3 codes, [n_pages, page_size, Hkv, Dh], and scales,
-// [n_pages, page_size / block, Hkv].
+// [n_pages, page_size / 2^block_log2, Hkv].
 struct Cache8 {
     void *k, *v;
     float *k_scales, *v_scales;
-    int Hkv, Dh, block;
+    int Hkv, Dh, block_log2;
 };
 cudaError_t launch_append8(int dtype, const PageTable &pt, const void *k, int64_t k_stride,
                            const void *v, int64_t v_stride, const int32_t *slots, int N, int D,

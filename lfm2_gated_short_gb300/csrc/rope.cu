@@ -54,44 +54,40 @@ __device__ __forceinline__ float2 cos_sin(uint64_t turns) {
     return make_float2(((q + 1) & 2) ? -x : x, (q & 2) ? -y : y);
 }
 
-// VP values as fp32, read and written as one access where VP fills 16 bytes (or 4).
+// VP values as they are stored, one access where VP fills 16 bytes.
 template <typename T, int VP>
 struct Part {
-    float f[VP];
+    static constexpr bool kFull = VP * sizeof(T) == 16;
+    static constexpr int kWords = kFull ? 4 : 1;
+    uint32_t w[kWords];
     __device__ __forceinline__ void load(const T *p) {
-        if constexpr (VP * sizeof(T) == 16) {
+        if constexpr (kFull) {
             const uint4 q = ld_plain(p);
-            if constexpr (sizeof(T) == 2) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const uint32_t w = e == 0 ? q.x : e == 1 ? q.y : e == 2 ? q.z : q.w;
-                    f[2 * e] = bf16_lo(w);
-                    f[2 * e + 1] = bf16_hi(w);
-                }
-            } else {
-                f[0] = __uint_as_float(q.x);
-                f[1] = __uint_as_float(q.y);
-                f[2] = __uint_as_float(q.z);
-                f[3] = __uint_as_float(q.w);
-            }
+            w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
         } else {
-#pragma unroll
-            for (int e = 0; e < VP; ++e) f[e] = (float)gld(p + e);
+            static_assert(VP == 1, "one value or 16 bytes");
+            w[0] = __float_as_uint((float)gld(p));
         }
     }
     __device__ __forceinline__ void store(T *p) const {
-        if constexpr (VP * sizeof(T) == 16) {
-            uint4 q;
-            if constexpr (sizeof(T) == 2)
-                q = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
-                               pack_bf16(f[6], f[7]));
-            else
-                q = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
-                               __float_as_uint(f[3]));
-            st_plain(p, q);
+        if constexpr (kFull)
+            st_plain(p, make_uint4(w[0], w[1], w[2], w[3]));
+        else
+            gst(p, (T)__uint_as_float(w[0]));
+    }
+    __device__ __forceinline__ void get(float (&f)[VP]) const {
+#pragma unroll
+        for (int e = 0; e < VP; ++e)
+            f[e] = kFull && sizeof(T) == 2 ? (e & 1 ? bf16_hi(w[e / 2]) : bf16_lo(w[e / 2]))
+                                           : __uint_as_float(w[e < kWords ? e : 0]);
+    }
+    __device__ __forceinline__ void set(const float (&f)[VP]) {
+        if constexpr (kFull && sizeof(T) == 2) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_bf16(f[2 * e], f[2 * e + 1]);
         } else {
 #pragma unroll
-            for (int e = 0; e < VP; ++e) gst(p + e, (T)f[e]);
+            for (int e = 0; e < VP; ++e) w[e] = __float_as_uint(f[e]);
         }
     }
 };
@@ -131,46 +127,74 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, int tokens) {
         s_turn[t * a.R + half + i] = (a.inverse ? -cs.y : cs.y) * a.amplitude;
     }
     __syncthreads();
-    // Items: VP pairs of a head, then VP of the values behind them.
-    const int turned = half / VP, per = turned + (a.copy ? (a.Dh - a.R) / VP : 0);
-    const int heads = a.Hq + a.Hkv;
-    for (int x = threadIdx.x; x < here * heads * per; x += kRopeThreads) {
-        const int t = x / (heads * per), y = x - t * heads * per, hd = y / per, c = y - hd * per;
-        if (!s_live[t]) continue;
-        const bool is_k = hd >= a.Hq;
-        const int64_t row = t0 + t, at = (int64_t)(is_k ? hd - a.Hq : hd) * a.Dh;
-        const T *from = (const T *)(is_k ? a.k : a.q) + row * (is_k ? a.k_stride : a.q_stride) + at;
-        T *to = (T *)(is_k ? a.k_out : a.q_out) +
-                row * (is_k ? a.k_out_stride : a.q_out_stride) + at;
-        Part<T, VP> u, w;
-        if (c >= turned) {
-            const int o = a.R + (c - turned) * VP;
-            u.load(from + o);
-            u.store(to + o);
-            continue;
-        }
-        const float *cs = s_turn + t * a.R + c * VP, *sn = cs + half;
-        const int first = HALF ? c * VP : 2 * c * VP, second = HALF ? first + half : first + VP;
-        u.load(from + first);
-        w.load(from + second);
-        Part<T, VP> ru, rw;
+    // Items: VP pairs of a head, then 2 VP of the values behind them (VP of them last, where
+    // they are no whole number). A thread takes every 256th, kAhead of them in flight.
+    const int turned = half / VP, rest = (a.Dh - a.R) / VP;
+    const int per = turned + (a.copy ? (rest + 1) / 2 : 0), heads = a.Hq + a.Hkv;
+    const int dh = kRopeThreads / per, dc = kRopeThreads - dh * per;  // the step to a thread's next
+    int hd = threadIdx.x / per, c = threadIdx.x - hd * per, t = hd / heads;
+    hd -= t * heads;
+    constexpr int kAhead = VP * sizeof(T) == 16 ? 4 : 1;
+    while (t < here) {
+        Part<T, VP> u[kAhead], w[kAhead];
+        T *to[kAhead];
+        int at[kAhead][3];  // first, second (-1: none), place of its sines (-1: copied)
 #pragma unroll
-        for (int e = 0; e < VP; ++e) {
-            if constexpr (HALF) {
-                ru.f[e] = u.f[e] * cs[e] - w.f[e] * sn[e];
-                rw.f[e] = w.f[e] * cs[e] + u.f[e] * sn[e];
-            } else {
-                const float x0 = 2 * e < VP ? u.f[(2 * e) % VP] : w.f[(2 * e) % VP];
-                const float x1 = 2 * e + 1 < VP ? u.f[(2 * e + 1) % VP] : w.f[(2 * e + 1) % VP];
-                const float y0 = x0 * cs[e] - x1 * sn[e], y1 = x1 * cs[e] + x0 * sn[e];
-                if (2 * e < VP) ru.f[(2 * e) % VP] = y0;
-                else rw.f[(2 * e) % VP] = y0;
-                if (2 * e + 1 < VP) ru.f[(2 * e + 1) % VP] = y1;
-                else rw.f[(2 * e + 1) % VP] = y1;
+        for (int n = 0; n < kAhead; ++n) {
+            to[n] = nullptr;
+            if (t < here && s_live[t]) {
+                const bool is_k = hd >= a.Hq;
+                const int64_t row = t0 + t, head = (int64_t)(is_k ? hd - a.Hq : hd) * a.Dh;
+                const T *from =
+                    (const T *)(is_k ? a.k : a.q) + row * (is_k ? a.k_stride : a.q_stride) + head;
+                to[n] = (T *)(is_k ? a.k_out : a.q_out) +
+                        row * (is_k ? a.k_out_stride : a.q_out_stride) + head;
+                if (c < turned) {
+                    at[n][0] = HALF ? c * VP : 2 * c * VP;
+                    at[n][1] = at[n][0] + (HALF ? half : VP);
+                    at[n][2] = t * a.R + c * VP;
+                } else {
+                    at[n][0] = a.R + 2 * (c - turned) * VP;
+                    at[n][1] = at[n][0] + VP < a.Dh ? at[n][0] + VP : -1;
+                    at[n][2] = -1;
+                }
+                u[n].load(from + at[n][0]);
+                if (at[n][1] >= 0) w[n].load(from + at[n][1]);
+            }
+            hd += dh;
+            c += dc;
+            if (c >= per) {
+                c -= per;
+                ++hd;
+            }
+            while (hd >= heads) {
+                hd -= heads;
+                ++t;
             }
         }
-        ru.store(to + first);
-        rw.store(to + second);
+#pragma unroll
+        for (int n = 0; n < kAhead; ++n) {
+            if (to[n] == nullptr) continue;
+            if (at[n][2] >= 0) {
+                const float *cs = s_turn + at[n][2], *sn = cs + half;
+                float x[VP], y[VP];
+                u[n].get(x);
+                w[n].get(y);
+#pragma unroll
+                for (int e = 0; e < VP; ++e) {
+                    // Pair e is (x_e, y_e), or values 2 e and 2 e + 1 of x and y together.
+                    float &p = HALF || VP == 1 ? x[e] : (2 * e < VP ? x : y)[2 * e % VP];
+                    float &q = HALF || VP == 1 ? y[e] : (2 * e + 1 < VP ? x : y)[(2 * e + 1) % VP];
+                    const float p0 = p, q0 = q;
+                    p = p0 * cs[e] - q0 * sn[e];
+                    q = q0 * cs[e] + p0 * sn[e];
+                }
+                u[n].set(x);
+                w[n].set(y);
+            }
+            u[n].store(to[n] + at[n][0]);
+            if (at[n][1] >= 0) w[n].store(to[n] + at[n][1]);
+        }
     }
 }
 
