@@ -452,6 +452,12 @@ def pool_copy(pool, src_slots, dst_slots, stream=None):
 def _rows(t, name, dtype, shape):
     """Data pointer and row stride (elements) of a CUDA tensor whose rows (the
     dims after the first) are contiguous and may lie further apart."""
+    if len(shape) == 3 and type(t) is torch.Tensor and t.is_cuda and t.dtype is dtype and t.shape == shape:
+        # one test on the way that calls usually take
+        n, _, width = shape
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and s1 == width and n > 1:
+            return t.data_ptr(), s0
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -508,6 +514,15 @@ def _scales(k_pages, v_pages, k_scales, v_scales):
     pool = k_pages.shape
     if k_scales is None or v_scales is None:
         raise ValueError("an 8-bit cache has k_scales and v_scales")
+    blocked = k_scales.shape
+    if (len(pool) == 4 and len(blocked) == 3 and v_pages.shape == pool and v_scales.shape == blocked
+            and blocked[0] == pool[0] and blocked[2] == pool[2] and blocked[1] and not pool[1] % blocked[1]
+            and k_pages.dtype is _E4M3 and v_pages.dtype is _E4M3 and k_scales.dtype is torch.float32
+            and v_scales.dtype is torch.float32 and k_pages.is_cuda and v_pages.is_cuda
+            and k_scales.is_cuda and v_scales.is_cuda and k_pages.is_contiguous()
+            and v_pages.is_contiguous() and k_scales.is_contiguous() and v_scales.is_contiguous()):
+        return (pool[2], pool[3], pool[1] // blocked[1], k_pages.data_ptr(), v_pages.data_ptr(),
+                k_scales.data_ptr(), v_scales.data_ptr())
     if len(pool) not in (4, 5) or len(k_scales.shape) != len(pool) - 1:
         raise ValueError("k_scales must be [.., n_pages, page_size / block, Hkv]")
     ps, Hkv, Dh = pool[-3:]
@@ -799,46 +814,69 @@ def rope_frequencies(R, base=10000.0, scaling=None, factor=1.0, original_length=
 
 def _rope(name, inverse, q, k, freqs, positions, lens, slot_ids, D, layout, amplitude, q_out, k_out,
           stream):
-    if layout not in ("half", "interleaved"):
+    if layout == "half":
+        order = SC_ROPE_HALF
+    elif layout == "interleaved":
+        order = SC_ROPE_INTERLEAVED
+    else:
         raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
     x = q if q is not None else k
     if x is None:
         raise ValueError("q or k must be given")
-    T, Dh, dt = x.shape[0], x.shape[2], x.dtype
-    code, device, R = _dcode(x), x.device, 2 * freqs.shape[0]
-    args = []
-    outs = []
-    for label, t, o in (("q", q, q_out), ("k", k, k_out)):
-        if t is None:
-            args += [0, None, 0, None, 0]
-            outs.append(None)
-            continue
-        shape = (T, t.shape[1], Dh)
-        p, s = _rows(t, label, dt, shape)
-        if o is None:
-            o = _output(shape, dt, device, stream)
-        o_p, o_s = _rows(o, label + "_out", dt, shape)
-        args += [t.shape[1], p, s, o_p, o_s]
-        outs.append(o)
+    T, _, Dh = x.shape
+    dt, device = x.dtype, x.device
+    code = SC_BF16 if dt is _BF16 else _dcode(x)
+    Hq = Hkv = q_s = k_s = qo_s = ko_s = 0
+    q_p = k_p = qo_p = ko_p = None
+    if q is not None:
+        shape = q.shape
+        Hq = shape[1]
+        q_p, q_s = _rows(q, "q", dt, (T, Hq, Dh))
+        if q_out is None:
+            q_out = _output(shape, dt, device, stream)
+            qo_p, qo_s = q_out.data_ptr(), Hq * Dh
+        elif q_out is q:
+            qo_p, qo_s = q_p, q_s
+        else:
+            qo_p, qo_s = _rows(q_out, "q_out", dt, (T, Hq, Dh))
+    else:
+        q_out = None
+    if k is not None:
+        shape = k.shape
+        Hkv = shape[1]
+        k_p, k_s = _rows(k, "k", dt, (T, Hkv, Dh))
+        if k_out is None:
+            k_out = _output(shape, dt, device, stream)
+            ko_p, ko_s = k_out.data_ptr(), Hkv * Dh
+        elif k_out is k:
+            ko_p, ko_s = k_p, k_s
+        else:
+            ko_p, ko_s = _rows(k_out, "k_out", dt, (T, Hkv, Dh))
+    else:
+        k_out = None
+    half, = freqs.shape
+    f_p = _dev(freqs, "freqs", torch.float64)
+    p_p = l_p = s_p = None
+    n_slots = 0
     if positions is not None:
         if lens is not None or slot_ids is not None:
             raise ValueError("positions, or lens and slot_ids")
-        where = (_ints(positions, "positions", (T,)), None, 0, None, 0)
+        p_p = _ints(positions, "positions", (T,))
     else:
         if lens is None or slot_ids is None:
             raise ValueError("positions, or lens and slot_ids")
-        N, n_slots = slot_ids.shape[0], lens.shape[0]
+        N, = slot_ids.shape
+        n_slots, = lens.shape
         if N * D != T:
             raise ValueError(f"{T} rows are not {D} of each of {N} sequences")
-        where = (None, _ints(lens, "lens", (n_slots,)), n_slots, _ints(slot_ids, "slot_ids", (N,)), D)
-    hq, q_p, q_s, qo_p, qo_s, hk, k_p, k_s, ko_p, ko_s = args
-    status = lib().shortconv_rope(
-        code, SC_ROPE_HALF if layout == "half" else SC_ROPE_INTERLEAVED, inverse, hq, hk, Dh, R, q_p,
-        q_s, k_p, k_s, T, _dev(freqs, "freqs", torch.float64), amplitude, *where, qo_p, qo_s, ko_p,
-        ko_s, _stream(stream, device))
+        l_p = _ints(lens, "lens", (n_slots,))
+        s_p = _ints(slot_ids, "slot_ids", (N,))
+    status = lib().shortconv_rope(code, order, inverse, Hq, Hkv, Dh, 2 * half, q_p, q_s, k_p, k_s, T, f_p,
+                                  amplitude, p_p, l_p, n_slots, s_p, D, qo_p, qo_s, ko_p, ko_s,
+                                  _stream(stream, device))
     if status:
         _raise_on(name, status)
-    return tuple(outs)
+    return q_out, k_out
 
 
 def rope(q, k, freqs, positions=None, lens=None, slot_ids=None, D=1, layout="half", amplitude=1.0,

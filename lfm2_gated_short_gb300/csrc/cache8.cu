@@ -218,9 +218,9 @@ struct Codes<float> {
     }
 };
 
-// Rows cu[i] .. cu[i + 1] - 1 are sequence i's tokens from starts[i] on. A warp takes R rows of
-// both pools at a time, lane r finds row r's place, and the next rows' places are looked
-// for (a chain of dependent reads) while these rows' codes are on their way.
+// Rows cu[i] .. cu[i + 1] - 1 are sequence i's tokens from starts[i] on. A warp takes units of R
+// rows of both pools; its lanes find the places of its next 32 rows (a chain of dependent
+// reads) at once.
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads, 4)
     k_read8(PageTable pt, const int32_t *__restrict__ slots, const int32_t *__restrict__ cu,
@@ -242,25 +242,16 @@ __global__ void __launch_bounds__(kReadThreads, 4)
     }
     const int per = c.Hkv * c.Dh / kN;  // words of a row
     const int lb = c.block_log2, lp = __ffs(pt.page_size) - 1;
-    const int ends = lane < N ? gld(cu + lane + 1) : INT_MAX;  // of the first 32 sequences
-    // Lane r: the row of the pools of row r0 + r, -1 for one that is left alone.
-    auto find = [&](int64_t r0) {
-        int i = 0;
-        if (N <= 32) {
-            for (int r = 0; r < R; ++r) {
-                const int before = __popc(__ballot_sync(~0u, ends <= r0 + r));
-                if (r == lane) i = before;
-            }
-        }
-        if (lane >= R || r0 + lane >= rows) return -1;
-        const int r = (int)r0 + lane;
-        if (N > 32) {
-            int top = N;  // the last i with cu[i] <= r
-            while (top - i > 1) {
-                const int mid = (i + top) >> 1;
-                if (gld(cu + mid) <= r) i = mid;
-                else top = mid;
-            }
+    const int64_t step = (int64_t)gridDim.x * (kReadThreads / 32) * R;
+    // The row of the pools of row r, -1 for one that is left alone.
+    auto find = [&](int64_t r64) {
+        if (r64 >= rows) return -1;
+        const int r = (int)r64;
+        int i = 0, top = N;  // the last i with cu[i] <= r
+        while (top - i > 1) {
+            const int mid = (i + top) >> 1;
+            if (gld(cu + mid) <= r) i = mid;
+            else top = mid;
         }
         const int slot = gld(slots + i), begin = gld(cu + i), end = gld(cu + i + 1);
         const int start = starts != nullptr ? gld(starts + i) : 0;
@@ -278,53 +269,70 @@ __global__ void __launch_bounds__(kReadThreads, 4)
         }
         return (id << lp) + (pos & (pt.page_size - 1));  // n_pages * page_size < 2^31
     };
-    const int64_t step = (int64_t)gridDim.x * (kReadThreads / 32) * R;
+    // A unit's words of each pool go by in rounds of 64, two a lane; several rows make one round.
+    const int ahead = 32 / R;  // units whose places the lanes hold: lane u R + r unit u's row r
+    const int rounds = (R * per + 63) / 64;
+    int w_row[2], w_x[2];  // the lane's words in round 0
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        const int w = 32 * q + lane;
+        w_row[q] = R == 1 ? 0 : w / per;
+        w_x[q] = w - w_row[q] * per;
+    }
     int64_t r0 = ((int64_t)blockIdx.x * (kReadThreads / 32) + (tid >> 5)) * R;
-    int here = find(r0);
-    constexpr int kAhead = 4;  // words of a lane in flight
-    // Word w of a unit: row r, word x of its K or V, of head h. With several rows a unit is
-    // one round of the loop below, and a lane's words are the same in each.
-    struct Word4 {
-        int r, x, h;
-        bool v, live;
+    int place = -1, unit = ahead, round = 0;
+    struct Batch {
+        Word k[2], v[2];
+        uint32_t ks[2], vs[2];
+        int64_t to[2];  // word of the outputs, -1: none
     };
-    auto word = [&](int w) {
-        Word4 u;
-        u.r = R == 1 ? 0 : w / (2 * per);
-        const int y = w - u.r * 2 * per;
-        u.live = y < 2 * per && u.r < R;
-        u.v = y >= per;
-        u.x = u.v ? y - per : y;
-        u.h = __umulhi((uint32_t)u.x, head_magic);
-        return u;
-    };
-    Word4 fixed[kAhead];
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) fixed[q] = word(32 * q + lane);
-    for (; r0 < rows; r0 += step) {
-        int next = -1;
-        for (int w0 = 0; w0 < 2 * R * per; w0 += 32 * kAhead) {
-            Word code[kAhead];
-            uint32_t scale[kAhead];
-            T *to[kAhead];
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q) {
-                const Word4 u = w0 == 0 ? fixed[q] : word(w0 + 32 * q + lane);
-                const int row = __shfl_sync(~0u, here, u.r & 31);
-                to[q] = nullptr;
-                if (!u.live || row < 0) continue;
-                code[q] = gld((const Word *)(u.v ? c.v : c.k) + (int64_t)row * per + u.x);
-                scale[q] = gld(reinterpret_cast<const uint32_t *>(u.v ? c.v_scales : c.k_scales) +
-                               (int64_t)(row >> lb) * c.Hkv + u.h);
-                to[q] = (u.v ? v : k) + ((r0 + u.r) * per + u.x) * kN;
-            }
-            if (w0 == 0) next = find(r0 + step);
-#pragma unroll
-            for (int q = 0; q < kAhead; ++q)
-                if (to[q] != nullptr)
-                    st_stream(to[q], Codes<T>::values(code[q], scale_bits(scale[q])));
+    auto load = [&](Batch &b) {
+        if (round == 0 && unit == ahead) {
+            unit = 0;
+            place = lane < ahead * R ? find(r0 + lane / R * step + lane % R) : -1;
         }
-        here = next;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            const int x = w_x[q] + 64 * round;
+            const int row = __shfl_sync(~0u, place, unit * R + w_row[q] & 31);
+            b.to[q] = -1;
+            if (x >= per || w_row[q] >= R || row < 0) continue;
+            const int64_t at = (int64_t)row * per + x;
+            const int64_t scale =
+                (int64_t)(row >> lb) * c.Hkv + __umulhi((uint32_t)x, head_magic);
+            b.k[q] = gld((const Word *)c.k + at);
+            b.v[q] = gld((const Word *)c.v + at);
+            b.ks[q] = gld(reinterpret_cast<const uint32_t *>(c.k_scales) + scale);
+            b.vs[q] = gld(reinterpret_cast<const uint32_t *>(c.v_scales) + scale);
+            b.to[q] = (r0 + w_row[q]) * per + x;
+        }
+        if (++round == rounds) {
+            round = 0;
+            ++unit;
+            r0 += step;
+        }
+    };
+    auto put = [&](const Batch &b) {
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            if (b.to[q] < 0) continue;
+            st_stream(k + b.to[q] * kN, Codes<T>::values(b.k[q], scale_bits(b.ks[q])));
+            st_stream(v + b.to[q] * kN, Codes<T>::values(b.v[q], scale_bits(b.vs[q])));
+        }
+    };
+    // One batch is on its way while the one before becomes values.
+    Batch even, odd;
+    if (r0 >= rows) return;
+    load(even);
+    while (true) {
+        const bool more = r0 < rows;
+        if (more) load(odd);
+        put(even);
+        if (!more) return;
+        const bool more2 = r0 < rows;
+        if (more2) load(even);
+        put(odd);
+        if (!more2) return;
     }
 }
 
@@ -355,7 +363,7 @@ static cudaError_t read8(const PageTable &pt, const int32_t *slots, const int32_
                          int sm_count, cudaStream_t stream) {
     // A warp's rows: up to 128 words at once, four a lane.
     const int per = c.Hkv * c.Dh / Codes<T>::kN, of_head = c.Dh / Codes<T>::kN;
-    const int R = per >= 64 ? 1 : 64 / per;
+    const int R = per >= 64 ? 1 : 64 / per < 32 ? 64 / per : 32;
     const uint32_t magic = (uint32_t)((1ull << 32) / of_head) + 1;  // words below 2^22, Dh <= 1024
     const int64_t warps = (rows + R - 1) / R, blocks = (warps * 32 + kReadThreads - 1) / kReadThreads;
     const int64_t most = 4ll * sm_count;

@@ -110,7 +110,7 @@ __device__ __forceinline__ int64_t position_of(const RopeArgs &a, int64_t t, boo
 }
 
 template <typename T, int VP, bool HALF>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, int tokens) {
+__global__ void __launch_bounds__(kRopeThreads, 5) k_rope(RopeArgs a, int tokens) {
     extern __shared__ float s_turn[];  // [tokens][cos of the pairs, sin of the pairs]
     __shared__ bool s_live[kRopeTokens];
     pdl_wait();
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(RopeArgs a, int tokens) {
     const int dh = kRopeThreads / per, dc = kRopeThreads - dh * per;  // the step to a thread's next
     int hd = threadIdx.x / per, c = threadIdx.x - hd * per, t = hd / heads;
     hd -= t * heads;
-    constexpr int kAhead = VP * sizeof(T) == 16 ? 4 : 1;
+    constexpr int kAhead = VP * sizeof(T) == 16 ? 2 : 1;
     while (t < here) {
         Part<T, VP> u[kAhead], w[kAhead];
         T *to[kAhead];
@@ -223,8 +223,15 @@ static cudaError_t launch_rope_t(const RopeArgs &a, int tokens, cudaStream_t str
 }
 
 cudaError_t launch_rope(int dtype, const RopeArgs &a, int sm_count, cudaStream_t stream) {
+    // A tile of up to 44 KB: less pays its sines and its start too often, more leaves the GPU's
+    // last wave half empty. us forward and backward, of 40 bf16 heads of 64 (5 KB a token) and 16
+    // fp32 heads of 128, half turned (8 KB), with 4 and 8 tokens a tile: 16384 tokens of the
+    // first 61.3 and 56.8; 9000 tokens of both 36.2 and 35.0, 49.1 and 53.7; 30000 tokens 105 and 96,
+    // 146 and 150. With few tokens, four tiles an SM.
+    const int64_t row = (int64_t)(a.Hq + a.Hkv) * a.Dh * (dtype == SC_BF16 ? 2 : 4);
     int tokens = kRopeTokens;
-    while (tokens > 1 && a.T < (int64_t)tokens * 4 * sm_count) tokens >>= 1;
+    while (tokens > 1 && (tokens * row > (44 << 10) || a.T < (int64_t)tokens * 4 * sm_count))
+        tokens >>= 1;
     return dtype == SC_BF16 ? launch_rope_t<__nv_bfloat16>(a, tokens, stream)
                             : launch_rope_t<float>(a, tokens, stream);
 }
