@@ -586,7 +586,8 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
 // The shared prefix as bf16 [keys, Hkv, Dh], for k_prefix: every key is read by many row tiles, so
 // it is unpacked once, and stays in L2. Exact: a code has 4 bits, a scale none.
 constexpr int kUnpackThreads = 256;
-static __global__ void __launch_bounds__(kUnpackThreads)
+constexpr int kUnpackWords = 2;  // of each pool, of a lane at once
+static __global__ void __launch_bounds__(kUnpackThreads, 4)
     k_unpack(AttnArgs a, const unsigned char *__restrict__ k, const unsigned char *__restrict__ v,
              int Dh, bf16 *__restrict__ k16, bf16 *__restrict__ v16) {
     __shared__ int s_leader;
@@ -608,31 +609,55 @@ static __global__ void __launch_bounds__(kUnpackThreads)
     int slot;
     seq_len(a, s_leader, &slot, false);
     const int32_t *row = a.pt.table + (int64_t)slot * a.pt.max_pages;
-    const int per = a.Hkv * Dh / 16, ps = a.pt.page_size, bl = a.s8.block_log2;
-    const int64_t n = (int64_t)a.shared_keys * 2 * per;
-    for (int64_t x = (int64_t)blockIdx.x * kUnpackThreads + tid; x < n;
-         x += (int64_t)gridDim.x * kUnpackThreads) {
-        const int t = (int)(x / (2 * per)), y = (int)(x - (int64_t)t * 2 * per);
-        const bool is_v = y >= per;
-        const int q = is_v ? y - per : y, at = t & (ps - 1);
-        const int id = gld_l2(row + t / ps);
-        if (id < 0 || id >= a.pt.n_pages) continue;  // k_prefix reports it
-        const uint4 w = ld_plain((is_v ? v : k) + (((int64_t)id * ps + at) * per + q) * 16);
-        const float *scales = is_v ? a.s8.v : a.s8.k;
-        const float s = __uint_as_float(scale_bits(__float_as_uint(
-            gld(scales + ((int64_t)id * (ps >> bl) + (at >> bl)) * a.Hkv + q * 16 / Dh))));
-        bf16 *to = (is_v ? v16 : k16) + ((int64_t)t * per + q) * 16;
+    // A warp takes a key at a time, eight codes of K and of V a lane; the next key's are on their way.
+    const int per = a.Hkv * Dh / 8, lp = __ffs(a.pt.page_size) - 1, bl = a.s8.block_log2;
+    const int warps = gridDim.x * (kUnpackThreads / 32);
+    for (int w0 = 0; w0 < per; w0 += 32 * kUnpackWords) {
+        struct Batch {
+            uint2 k[kUnpackWords], v[kUnpackWords];
+            uint32_t ks[kUnpackWords], vs[kUnpackWords];
+        };
+        int head[kUnpackWords];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            uint32_t out[4];
+        for (int q = 0; q < kUnpackWords; ++q) head[q] = (w0 + 32 * q + (tid & 31)) * 8 / Dh;
+        auto load = [&](Batch &b, int t) {
+            const int id = gld_l2(row + (t >> lp));
+            // A bad page is k_prefix's to report; its part counts for nothing.
+            const int page = id < 0 || id >= a.pt.n_pages ? 0 : id;
+            const int64_t at = ((int64_t)page << lp) + (t & (a.pt.page_size - 1));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t four = word_of(w, 2 * half + e);
-                const uint32_t lo = e4m3x2_f16x2(four), hi = e4m3x2_f16x2_hi(four);
-                out[2 * e] = pack_bf16(f16_lo(lo) * s, f16_hi(lo) * s);
-                out[2 * e + 1] = pack_bf16(f16_lo(hi) * s, f16_hi(hi) * s);
+            for (int q = 0; q < kUnpackWords; ++q) {
+                const int x = w0 + 32 * q + (tid & 31);
+                if (x >= per) continue;
+                b.k[q] = gld(reinterpret_cast<const uint2 *>(k) + at * per + x);
+                b.v[q] = gld(reinterpret_cast<const uint2 *>(v) + at * per + x);
+                const int64_t s = (at >> bl) * a.Hkv + head[q];
+                b.ks[q] = gld(reinterpret_cast<const uint32_t *>(a.s8.k) + s);
+                b.vs[q] = gld(reinterpret_cast<const uint32_t *>(a.s8.v) + s);
             }
-            st_plain(to + 8 * half, make_uint4(out[0], out[1], out[2], out[3]));
+        };
+        auto put = [&](const Batch &b, int t) {
+#pragma unroll
+            for (int q = 0; q < kUnpackWords; ++q) {
+                const int x = w0 + 32 * q + (tid & 31);
+                if (x >= per) continue;
+                const int64_t to = ((int64_t)t * per + x) * 8;
+                st_plain(k16 + to, e4m3_bf16x8(b.k[q], scale_bits(b.ks[q])));
+                st_plain(v16 + to, e4m3_bf16x8(b.v[q], scale_bits(b.vs[q])));
+            }
+        };
+        Batch even, odd;
+        int t = blockIdx.x * (kUnpackThreads / 32) + (tid >> 5);
+        if (t < a.shared_keys) load(even, t);
+        while (t < a.shared_keys) {
+            const int next = t + warps;
+            if (next < a.shared_keys) load(odd, next);
+            put(even, t);
+            t = next;
+            if (t >= a.shared_keys) break;
+            if (t + warps < a.shared_keys) load(even, t + warps);
+            put(odd, t);
+            t += warps;
         }
     }
 }
@@ -644,8 +669,8 @@ static size_t unpacked_bytes(const AttnShape &s, int page_size) {
 
 static cudaError_t launch_unpack(const AttnArgs &a, const AttnShape &s, const void *k, const void *v,
                                  bf16 *k16, bf16 *v16, int sm_count, cudaStream_t stream) {
-    const int64_t n = (int64_t)a.shared_keys * 2 * (s.Hkv * s.Dh / 16);
-    const int64_t blocks = (n + kUnpackThreads - 1) / kUnpackThreads, most = 8ll * sm_count;
+    const int blocks = (a.shared_keys + kUnpackThreads / 32 - 1) / (kUnpackThreads / 32);
+    const int most = 4 * sm_count;
     return launch_pdl(k_unpack, dim3((unsigned)(blocks < most ? blocks : most)),
                       dim3(kUnpackThreads), 0, stream, a, (const unsigned char *)k,
                       (const unsigned char *)v, s.Dh, k16, v16);

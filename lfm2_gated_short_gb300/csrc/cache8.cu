@@ -194,16 +194,7 @@ struct Codes<__nv_bfloat16> {
     static constexpr int kN = 8;
     typedef uint2 Word;
     static __device__ __forceinline__ uint4 values(uint2 w, uint32_t scale) {
-        // The scale is a power of two: multiplying after the conversion is exact too.
-        const uint32_t s = scale >> 16 | (scale & 0xFFFF0000u);
-        uint32_t out[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t four = e < 2 ? w.x : w.y;
-            const uint32_t h = e & 1 ? e4m3x2_f16x2_hi(four) : e4m3x2_f16x2(four);
-            out[e] = bf2_mul(pack_bf16(f16_lo(h), f16_hi(h)), s);
-        }
-        return make_uint4(out[0], out[1], out[2], out[3]);
+        return e4m3_bf16x8(w, scale);
     }
 };
 template <>

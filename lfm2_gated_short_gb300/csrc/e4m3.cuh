@@ -10,6 +10,8 @@
 
 #include <stdint.h>
 
+#include "common.cuh"
+
 namespace sc {
 
 constexpr int kMinScaleExp = -64, kMaxScaleExp = 120;
@@ -69,6 +71,20 @@ __device__ __forceinline__ uint32_t scale_bits(uint32_t word) {
     return min(max(e, (uint32_t)(127 + kMinScaleExp) << 23), (uint32_t)(127 + kMaxScaleExp) << 23);
 }
 __device__ __forceinline__ uint32_t inverse_bits(uint32_t scale) { return 0x7F000000u - scale; }
+
+// Eight codes times their scale as bf16. The scale is a power of two, so that multiplying after
+// the rounding to bf16 is exact too.
+__device__ __forceinline__ uint4 e4m3_bf16x8(uint2 w, uint32_t scale) {
+    const uint32_t s = scale >> 16 | (scale & 0xFFFF0000u);
+    uint32_t out[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t four = e < 2 ? w.x : w.y;
+        const uint32_t h = e & 1 ? e4m3x2_f16x2_hi(four) : e4m3x2_f16x2(four);
+        out[e] = bf2_mul(pack_bf16(f16_lo(h), f16_hi(h)), s);
+    }
+    return make_uint4(out[0], out[1], out[2], out[3]);
+}
 
 // The least scale with which a value of these fp32 bits (finite, not negative) fits: 448 is
 // 1.75 x 2^8.
