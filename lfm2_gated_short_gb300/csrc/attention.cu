@@ -72,6 +72,11 @@ __device__ __forceinline__ int gld_l2(const int32_t *p) {
     return __ldcg(p);
 }
 
+__device__ __forceinline__ uint4 gld_l2(const uint4 *p) {
+    if (!SC_RD_OK(p, 16)) return make_uint4(0u, 0u, 0u, 0u);
+    return __ldcg(p);
+}
+
 // Tokens of sequence i (its D new ones included), or -1 with a bad slot or length.
 __device__ __forceinline__ int seq_len(const AttnArgs &a, int i, int *slot, bool report) {
     const int s = gld_l2(a.slots + i);
@@ -580,7 +585,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
     const uint32_t ring_a = smem_addr(ring);
     unsigned char *qs = ring + ST * C::kStage;
     const uint32_t qs_a = smem_addr(qs);
-    float *join = reinterpret_cast<float *>(qs + C::kQBufs * C::kHeads * C::kQ);
+    float *join = reinterpret_cast<float *>(qs + C::kQBufs * C::kQ);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     if (tid == 0) {
         for (int s = 0; s < ST; ++s) {
@@ -589,7 +594,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
             s_bad[s] = 0;
         }
         for (int s = 0; s < QB; ++s) {
-            mbar_init(&s_qfull[s], 33);  // every producer lane's copies, and the description
+            mbar_init(&s_qfull[s], Q8 ? 1 : 33);  // the description, and every lane's copies
             mbar_init(&s_qempty[s], C::kWarps);
         }
         mbar_fence_init();
@@ -715,26 +720,22 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
                 raise_error(SC_DEV_TIMEOUT);
                 return false;
             }
-            if (it.n > 0) {
+            if (!Q8 && it.n > 0) {
                 const bf16 *q = a.q + (int64_t)it.i * a.D * a.q_stride + it.h * a.G * DH;
                 constexpr int kStep = 256 / DH;  // rows of 32 chunks
                 int r = lane / (DH / 8), rr = it.rt * C::MR + r, j = rr / a.G, gq = rr - j * a.G;
                 const int ch = lane % (DH / 8);
-                const uint32_t col = b * C::kHeads * C::kQ + (ch >> 3) * C::MR * 128;
+                const uint32_t col = b * C::kQ + (ch >> 3) * C::MR * 128;
                 for (; r < C::MR; r += kStep, rr += kStep) {
-#pragma unroll
-                    for (int hh = 0; hh < C::kHeads; ++hh) {
-                        const uint32_t off = col + hh * C::kQ + swz(r, ch & 7);
-                        if (rr < rows)
-                            cp_async16(qs_a + off,
-                                       q + j * a.q_stride + (hh * a.G + gq) * DH + ch * 8);
-                        else
-                            *reinterpret_cast<uint4 *>(qs + off) = make_uint4(0u, 0u, 0u, 0u);
-                    }
+                    const uint32_t off = col + swz(r, ch & 7);
+                    if (rr < rows)
+                        cp_async16(qs_a + off, q + j * a.q_stride + gq * DH + ch * 8);
+                    else
+                        *reinterpret_cast<uint4 *>(qs + off) = make_uint4(0u, 0u, 0u, 0u);
                     for (gq += kStep; gq >= a.G; gq -= a.G) ++j;
                 }
             }
-            cp_async_arrive(&s_qfull[b]);
+            if (!Q8) cp_async_arrive(&s_qfull[b]);
             if (lane == 0) s_item[b] = it;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_qfull[b]);

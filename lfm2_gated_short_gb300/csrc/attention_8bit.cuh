@@ -117,14 +117,13 @@ struct Own8Cfg {
     static constexpr uint32_t kV = NC * kBlk;                 // the tile's V behind its K
     static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows or Dh 128 8 to 32
     static constexpr int kCtas = DH == 64 ? 3 : 2;
-    static constexpr int kQBufs = KG == 1 && DH == 64 ? 2 : 1;  // items described ahead
-    static constexpr int NB = DH / 64;                        // 64-wide column blocks of Q
-    static constexpr uint32_t kQ = MR * 128 * NB;             // queries of a head
+    static constexpr int kQBufs = 2;                          // items described ahead
+    static constexpr uint32_t kQ = 0;                         // the consumers read their queries
     static constexpr int kOs = DH + 4;                        // floats of a row to join
     static constexpr uint32_t kJoin = KG > 1 ? kWarps * WR * (kOs + 2) * 4 : 0;
     // Tiles in flight: what the CTAs of an SM leave of its 228 KB beside 4.5 KB each of static and
     // reserved shared memory.
-    static constexpr size_t kRest = 1024 + kQBufs * HG * kQ + kJoin;
+    static constexpr size_t kRest = 1024 + kJoin;
     static constexpr int kFit = (int)((228 * 1024 / kCtas - 4608 - kRest) / kStage);
     static constexpr int kStages = kFit < 6 ? kFit : 6;
     static_assert(kStages >= 2, "shared memory of an SM");
@@ -191,27 +190,38 @@ struct Rows8 {
     int see[C::NT][2];  // keys that a row sees
     float o[C::NT][C::kDh / 16][4];  // columns 16 j + g and 16 j + 8 + g, of both rows each
 
-    __device__ __forceinline__ void load(uint32_t q, float scale_log2) {
+    // The rows from row0 on of the `rows` of sequence i under kv head h.
+    __device__ __forceinline__ void load(const AttnArgs &a, int i, int h, int row0, int rows) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
         constexpr int DH = C::kDh;
+        uint4 all[C::NT][DH / 32];
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) {
-            uint4 v[DH / 32];
+            const int rr = row0 + 8 * n + g, j = rr / a.G;
+            const bf16 *q = a.q + ((int64_t)i * a.D + j) * a.q_stride +
+                            (int64_t)(h * a.G + rr - j * a.G) * DH + 16 * c;
+#pragma unroll
+            for (int b = 0; b < DH / 32; ++b)
+                all[n][b] = rr < rows ? gld_l2(reinterpret_cast<const uint4 *>(
+                                            q + (b >> 1) * 64 + (b & 1) * 8))
+                                      : make_uint4(0u, 0u, 0u, 0u);
+        }
+#pragma unroll
+        for (int n = 0; n < C::NT; ++n) {
+            uint4(&v)[DH / 32] = all[n];
             uint32_t most = 0;
 #pragma unroll
-            for (int b = 0; b < DH / 32; ++b) {
-                v[b] = lds16(q + (b >> 1) * C::MR * 128 + swz(8 * n + g, 2 * c + (b & 1)));
+            for (int b = 0; b < DH / 32; ++b)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const uint32_t w = word_of(v[b], e);
                     most = max(most, max(w & 0x7FFFu, w >> 16 & 0x7FFFu));
                 }
-            }
             most = max(most, __shfl_xor_sync(~0u, most, 1));
             most = max(most, __shfl_xor_sync(~0u, most, 2));
             const uint32_t e = max(most >> 7, 32u);  // the largest's exponent, biased by 127
             const float to = __uint_as_float((268 - e) << 23);  // 2^(14 - (e - 127))
-            const float u = __uint_as_float((e - 14) << 23) * scale_log2;
+            const float u = __uint_as_float((e - 14) << 23) * a.scale_log2;
             unit[n] = f2_make(__shfl_sync(~0u, u, 8 * c), __shfl_sync(~0u, u, 8 * c + 4));
 #pragma unroll
             for (int b = 0; b < DH / 32; ++b)
@@ -444,7 +454,9 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         const int len = item.len, least = len - a.D + 1;  // keys that every row sees
         const int row0 = item.rt * C::MR + rg * WR;       // of the sequence's rows of a head
         Rows8<C> r;
-        r.load(s.qs_a + (qb * C::kHeads + hh) * C::kQ + rg * WR * 128, a.scale_log2);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.qempty[qb]);
+        r.load(a, item.i, item.h + hh, row0, rows);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -459,8 +471,6 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
 #pragma unroll
                 for (int e = 0; e < 4; ++e) r.o[n][j][e] = 0.0f;
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.qempty[qb]);
         bool bad = false;
         const int from = prefix_keys(a, len);
         int key0 = from + item.t0 * C::KT + kw * 32;
