@@ -26,7 +26,6 @@
 #include <cuda_bf16.h>
 
 #include <limits.h>
-#include <stdlib.h>
 
 #include <atomic>
 
@@ -839,6 +838,67 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
 
 namespace sc {
 
+// The parts of a row, prefix_n from prefix_at on, own_n from own_at on, each its O; m and l
+// are at +prefix_m (+kPR) and +own_m (+MR).
+struct RowParts {
+    const float *prefix_at, *own_at;
+    int prefix_n, own_n, prefix_m, own_m, prefix_step, own_step;
+    bool written;  // k_own wrote the row
+};
+// Before the wait: what does not depend on k_own. k_own's items are of own_heads kv heads, a
+// part's slots one for each.
+template <int DH>
+struct PartFinder {
+    RowParts p = {};
+    int i, j, h, g, own_heads;
+    bool valid, prefix;
+    __device__ __forceinline__ PartFinder(const PrefixArgs &x, int token, int hq, int own_heads_)
+        : own_heads(own_heads_) {
+        const AttnArgs &a = x.a;
+        i = token / a.D;
+        j = token - i * a.D;
+        h = hq / a.G;
+        g = hq - h * a.G;
+        // Slots and lengths need no wait: k_own let this kernel start when what wrote them was done.
+        int slot;
+        const int len = seq_len(a, i, &slot, false);
+        valid = len >= 0;
+        prefix = prefix_keys(a, len) > 0;
+        constexpr int kPSlot = kPR * (DH + 2);
+        if (prefix) {
+            const int tile = token / x.tpt, r = (token - tile * x.tpt) * a.G + g;
+            const int64_t w = (int64_t)(x.split ? tile : tile >> 1) * a.Hkv + h;
+            const int c0 = share_of(w * x.T, x.U, x.n_cta);
+            const int c1 = share_of(w * x.T + x.T - 1, x.U, x.n_cta);
+            p.prefix_at = x.part + ((w + c0) * 2 + (x.split ? 0 : tile & 1)) * kPSlot + r * DH;
+            p.prefix_m = kPR * DH + r - r * DH;
+            p.prefix_step = x.split ? kPSlot : 2 * kPSlot;
+            p.prefix_n = (c1 - c0 + 1) * (x.split ? 2 : 1);
+        }
+    }
+    __device__ __forceinline__ void find_own(const AttnArgs &a, int MR, int own_ctas) {
+        const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
+        const int groups = a.Hkv / own_heads, hi = h / own_heads, hh = h - hi * own_heads;
+        const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * groups;
+        const int slot_n = MR * (DH + 2), rt = r / MR, orow = r - rt * MR;
+        p.own_step = slot_n * own_heads;
+        if (u_n <= u_i) return;
+        const int64_t d = u_n - u_i;
+        const int64_t T = d <= UINT32_MAX ? (uint32_t)d / (uint32_t)per : d / per;
+        const int n_cta = (int)min((int64_t)own_ctas, U);
+        const int it = rt * groups + hi;
+        const int64_t u0 = u_i + it * T;
+        const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
+        p.own_at = a.own_part + ((int64_t)i * per + it + c0) * p.own_step + hh * slot_n + orow * DH;
+        p.own_m = MR * DH + orow - orow * DH;
+        p.own_n = c1 - c0 + 1;
+        if (p.own_n == 1 && !prefix) {
+            p.own_n = 0;
+            p.written = true;
+        }
+    }
+};
+
 // A block joins rows of one token. Dh / 8 lanes hold eight columns of a row each; PG
 // such groups share the row's parts (with few rows there are many parts and lanes
 // to spare). Lane k of the row holds the maximum and sum of part k, then every group
@@ -851,53 +911,17 @@ __global__ void __launch_bounds__(kMergeThreads)
     constexpr int L = DH / 8 * PG;
     const int rl = threadIdx.x % L, c8 = rl % (DH / 8), group = rl / (DH / 8);
     const int Hq = a.Hkv * a.G;
-    const int token = blockIdx.x, i = token / a.D, j = token - i * a.D;
+    const int token = blockIdx.x;
     const int at = blockIdx.y * (kMergeThreads / L) + threadIdx.x / L;
     const int hq = min(at, Hq - 1);  // lanes past the last row join it and write nothing
-    const int h = hq / a.G, g = hq - h * a.G;
-    // Slots and lengths need no wait: k_own let this kernel start when what wrote them was done.
-    int slot;
-    const int len = seq_len(a, i, &slot, false);
-    const bool valid = len >= 0, prefix = prefix_keys(a, len) > 0;
-
-    // The row's parts: prefix_n from prefix_at on, own_n from own_at on (its O; m and l
-    // are at +m_off and +l_off).
-    constexpr int kPSlot = kPR * (DH + 2);
-    const float *prefix_at = nullptr, *own_at = nullptr;
-    int prefix_n = 0, own_n = 0, prefix_m = 0, own_m = 0, step = 0;
-    bool mine = valid && at < Hq;
-    if (prefix) {
-        const int tile = token / x.tpt, r = (token - tile * x.tpt) * a.G + g;
-        const int64_t w = (int64_t)(x.split ? tile : tile >> 1) * a.Hkv + h;
-        const int c0 = share_of(w * x.T, x.U, x.n_cta);
-        const int c1 = share_of(w * x.T + x.T - 1, x.U, x.n_cta);
-        prefix_at = x.part + ((w + c0) * 2 + (x.split ? 0 : tile & 1)) * kPSlot + r * DH;
-        prefix_m = kPR * DH + r - r * DH;
-        step = x.split ? kPSlot : 2 * kPSlot;
-        prefix_n = (c1 - c0 + 1) * (x.split ? 2 : 1);
-    }
+    PartFinder<DH> find(x, token, hq, own_heads);
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
-    // k_own's items are of own_heads kv heads, a part's slots one for each.
-    const int groups = a.Hkv / own_heads, hi = h / own_heads, hh = h - hi * own_heads;
-    const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * groups;
-    const int slot_n = MR * (DH + 2), oslot = slot_n * own_heads, rt = r / MR, orow = r - rt * MR;
-    if (u_n > u_i) {
-        const int64_t d = u_n - u_i;
-        const int64_t T = d <= UINT32_MAX ? (uint32_t)d / (uint32_t)per : d / per;
-        const int n_cta = (int)min((int64_t)own_ctas, U);
-        const int it = rt * groups + hi;
-        const int64_t u0 = u_i + it * T;
-        const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
-        own_at = a.own_part + ((int64_t)i * per + it + c0) * oslot + hh * slot_n + orow * DH;
-        own_m = MR * DH + orow - orow * DH;
-        own_n = c1 - c0 + 1;
-        if (own_n == 1 && !prefix) {  // k_own wrote the row
-            own_n = 0;
-            mine = false;
-        }
-    }
+    find.find_own(a, MR, own_ctas);
+    bool mine = find.valid && at < Hq && !find.p.written;
+    const float *prefix_at = find.p.prefix_at, *own_at = find.p.own_at;
+    const int prefix_n = find.p.prefix_n, own_n = find.p.own_n, prefix_m = find.p.prefix_m;
+    const int own_m = find.p.own_m, step = find.p.prefix_step, oslot = find.p.own_step;
     const int parts = prefix_n + own_n;
     const float *own_from = own_at - (int64_t)prefix_n * oslot;  // part p's, p >= prefix_n, at + p * oslot
     int most = parts;  // of the warp's rows: its lanes stay together
@@ -980,6 +1004,123 @@ __global__ void __launch_bounds__(kMergeThreads)
                    pack_bf16(o[4] * inv, o[5] * inv), pack_bf16(o[6] * inv, o[7] * inv)));
 }
 
+// One row a block, for rows of many parts: its warps take the parts in turns of 32 (Dh 64) or
+// 16 and are joined through shared memory, in a fixed order.
+template <int DH>
+__global__ void __launch_bounds__(kMergeThreads)
+    k_merge_wide(PrefixArgs x, int MR, int own_ctas, int own_heads) {
+    const AttnArgs &a = x.a;
+    constexpr int kWarps = kMergeThreads / 32, C = DH / 8, PG = 32 / C;  // part groups of a warp
+    __shared__ float s_o[kWarps][DH], s_m[kWarps], s_l[kWarps];
+    __shared__ int s_bad[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane % C, group = lane / C;
+    const int token = blockIdx.x, hq = blockIdx.y;
+    PartFinder<DH> find(x, token, hq, own_heads);
+    pdl_wait();
+    pdl_launch_dependents();
+    find.find_own(a, MR, own_ctas);
+    const RowParts &p = find.p;
+    const int parts = p.prefix_n + p.own_n;
+    auto part_at = [&](int q) {
+        return q < p.prefix_n ? p.prefix_at + (int64_t)q * p.prefix_step
+                              : p.own_at + (int64_t)(q - p.prefix_n) * p.own_step;
+    };
+    // A warp's parts: 4 PG of every kWarps times as many, a group's four loaded at once.
+    constexpr int kAhead = 4, kTurn = kAhead * PG;
+    float top = -INFINITY, sum = 0.0f, o[8] = {};
+    bool bad = false;
+    for (int q0 = warp * kTurn; q0 < parts; q0 += kWarps * kTurn) {
+        float4 v[kAhead][2];
+        float m[kAhead], l[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int q = q0 + k * PG + group;
+            m[k] = -INFINITY;
+            l[k] = 0.0f;
+            v[k][0] = v[k][1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (q >= parts) continue;
+            const float *from = part_at(q);
+            const bool pre = q < p.prefix_n;
+            m[k] = gld(from + (pre ? p.prefix_m : p.own_m));
+            l[k] = gld(from + (pre ? p.prefix_m + kPR : p.own_m + MR));
+            v[k][0] = gld(reinterpret_cast<const float4 *>(from) + c8 * 2);
+            v[k][1] = gld(reinterpret_cast<const float4 *>(from) + c8 * 2 + 1);
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            bad |= m[k] != m[k];
+            now = fmaxf(now, m[k]);
+        }
+        const float base = now == -INFINITY ? 0.0f : now, f0 = ex2(top - base);
+        sum *= f0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] *= f0;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const float f = ex2(m[k] - base);
+            sum = fmaf(f, l[k], sum);
+            o[0] = fmaf(f, v[k][0].x, o[0]);
+            o[1] = fmaf(f, v[k][0].y, o[1]);
+            o[2] = fmaf(f, v[k][0].z, o[2]);
+            o[3] = fmaf(f, v[k][0].w, o[3]);
+            o[4] = fmaf(f, v[k][1].x, o[4]);
+            o[5] = fmaf(f, v[k][1].y, o[5]);
+            o[6] = fmaf(f, v[k][1].z, o[6]);
+            o[7] = fmaf(f, v[k][1].w, o[7]);
+        }
+        top = now;
+    }
+    // The warp's groups, then the warps.
+    float all = top;
+#pragma unroll
+    for (int k = C; k < 32; k <<= 1) all = fmaxf(all, __shfl_xor_sync(~0u, all, k));
+    const float f = all == -INFINITY ? 0.0f : ex2(top - all);
+    sum *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) o[e] *= f;
+#pragma unroll
+    for (int k = C; k < 32; k <<= 1) {
+        sum += __shfl_xor_sync(~0u, sum, k);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o[e] += __shfl_xor_sync(~0u, o[e], k);
+    }
+    bad = __any_sync(~0u, bad);
+    if (group == 0) {
+        *reinterpret_cast<float4 *>(&s_o[warp][c8 * 8]) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4 *>(&s_o[warp][c8 * 8 + 4]) = make_float4(o[4], o[5], o[6], o[7]);
+    }
+    if (lane == 0) {
+        s_m[warp] = all;
+        s_l[warp] = sum;
+        s_bad[warp] = bad;
+    }
+    __syncthreads();
+    const int col = threadIdx.x * 2;
+    if (col >= DH || !find.valid || p.written) return;
+    top = -INFINITY;
+    bad = false;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        top = fmaxf(top, s_m[w]);
+        bad |= s_bad[w] != 0;
+    }
+    if (bad) return;  // a bad page: the row is not written
+    const float base = top == -INFINITY ? 0.0f : top;
+    float x0 = 0.0f, x1 = 0.0f;
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        const float g = ex2(s_m[w] - base);
+        sum = fmaf(g, s_l[w], sum);
+        x0 = fmaf(g, s_o[w][col], x0);
+        x1 = fmaf(g, s_o[w][col + 1], x1);
+    }
+    const float inv = sum > 0.0f ? 1.0f / sum : sum == 0.0f ? 0.0f : sum;
+    gst(reinterpret_cast<uint32_t *>(a.out + ((int64_t)token * a.Hkv * a.G + hq) * DH + col),
+        pack_bf16(x0 * inv, x1 * inv));
+}
+
 // ------------------------------------------------------------ host side
 
 // Pages [n_pages * page_size tokens, Hkv, Dh] in boxes of `keys` tokens of one
@@ -1015,7 +1156,10 @@ static cudaError_t map_codes(CUtensorMap *m, const void *ptr, const PageTable &p
         fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(ptr), dims, strides, box, es,
            CU_TENSOR_MAP_INTERLEAVE_NONE,
            narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
-           (CUtensorMapL2promotion)(getenv("PROMO") ? atoi(getenv("PROMO")) : 2), CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+           // With an item a head, 64 bytes of each token's 512, DRAM gave 920 MB for 404 where L2
+           // fetched 256 bytes at a time (168 us; 109 with 64).
+           narrow ? CU_TENSOR_MAP_L2_PROMOTION_L2_64B : CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1061,7 +1205,7 @@ static size_t own_part_floats(const AttnShape &s, bool q8) {
 static size_t cum_bytes(const AttnShape &s) { return ((size_t)s.N + 3) / 2 * 16; }
 
 // The prefix's work: everything but the pointers.
-static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count) {
+static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count, bool q8) {
     PrefixArgs x = {};
     const int G = s.Hq / s.Hkv;
     x.P = s.shared_pages * page_size;
@@ -1080,14 +1224,17 @@ static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count) {
     // rule ends at 608); of 1-30 own tokens 22.8 and 23.7 with 600, 25.5 and 25.4 with 768.
     // Heads of 128: 46.9 and 58.5 with 64, 58.9 and 66.0 with 256 (the rule ends at 304). Slower
     // beside: 16 sequences behind 1024 tokens (32 units), 25.9 and 20.3, behind 2048, 23.6 and 21.0.
-    const int units = s.Dh == 64 ? 8 : 4;
+    // Over an 8-bit cache the own parts leave k_prefix more: four units of 64-wide heads too, where
+    // it then has half the SMs at most. 37 x 3 drafts of 14 heads behind 2976 tokens, us with four and
+    // with eight: 21.2 and 25.0; 64 sequences behind 512 tokens 25.4 and 27.4, behind 2048 26.4 and 27.1.
+    const int units = s.Dh == 64 && !(q8 && x.U <= 4 * (ctas / 2)) ? 8 : 4;
     x.a.beside = x.U > 0 && x.U <= (int64_t)units * (ctas / 2);
     if (x.a.beside) x.n_cta = (int)((x.U + units - 1) / units);
     return x;
 }
 static size_t prefix_part_floats(const AttnShape &s) {
     if (s.shared_pages == 0) return 0;
-    const PrefixArgs x = prefix_plan(s, 1, kMaxPrefixCtas);
+    const PrefixArgs x = prefix_plan(s, 1, kMaxPrefixCtas, false);
     const size_t items = (size_t)s.Hkv * (x.split ? 1 : (x.n_tiles + 1) / 2);
     return 2 * (items + kMaxPrefixCtas) * kPR * (s.Dh + 2);
 }
@@ -1152,7 +1299,8 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
                                     const Scales8 *scales, const PageTable &pt,
                                     const int32_t *slots, float scale, void *out, void *workspace,
                                     int sm_count, cudaStream_t stream) {
-    PrefixArgs x = prefix_plan(s, pt.page_size, sm_count);
+    const bool q8 = scales != nullptr;
+    PrefixArgs x = prefix_plan(s, pt.page_size, sm_count, q8);
     AttnArgs &a = x.a;
     a.q = (const bf16 *)q;
     a.q_stride = q_stride;
@@ -1167,7 +1315,6 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     a.out = (bf16 *)out;
     a.cum = (int64_t *)workspace;
     a.own_part = (float *)((char *)workspace + cum_bytes(s));
-    const bool q8 = scales != nullptr;
     const int heads = own_heads(s, q8), MR = own_rows(s, q8);
     x.part = a.own_part + own_part_floats(s, q8);
     if (q8) a.s8 = *scales;
@@ -1221,6 +1368,14 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     // 15.5, 2048 rows 23.3 both, 4096 rows 52.0 and 49.6, 16384 rows 210 and 201 (heads of 128:
     // 1024 rows 24.7 and 24.8, 4096 rows 77.9 and 75.2).
     const bool few = (int64_t)s.N * s.D * s.Hq <= 4096;
+    // Over an 8-bit cache a CTA takes four kv heads at once, so that few rows have many parts each: a
+    // block a row. One token of sequences of 4000 and of 500, us with a block a row and with
+    // a warp: 32 rows 10.0 and 16.5, 7.8 and 8.2; 128 rows 11.6 and 13.8, 8.2 and 9.6; 256 rows 13.9
+    // and 15.2, 8.8 and 10.2; 512 rows 22.4 and 20.4, 13.3 and 11.5.
+    if (q8 && (int64_t)s.N * s.D * s.Hq <= 2 * sm_count)
+        return launch_pdl(s.Dh == 64 ? k_merge_wide<64> : k_merge_wide<128>,
+                          dim3((unsigned)(s.N * s.D), (unsigned)s.Hq), dim3(kMergeThreads), 0,
+                          stream, x, MR, grid, heads);
     const auto merge = s.Dh == 64 ? (few ? k_merge<64, 4> : k_merge<64, 1>)
                                   : (few ? k_merge<128, 2> : k_merge<128, 1>);
     const int block_rows = few ? kMergeThreads / 32 : kMergeThreads / (s.Dh / 8);  // of one token

@@ -10,8 +10,8 @@
 // sizes of the blocks' values, and are rounded to f16's 11 bits. m is the running
 // maximum of s_t + log2 vs_t.
 //
-// (The register MMA of e4m3 itself is made of conversions of both operands and f16 MMAs on this
-// GPU: it measured 146 us where this takes TODO.)
+// (The register MMA of e4m3 itself is made of conversions of both operands and further MMAs on this
+// GPU: 56 million warp instructions for 128 sequences of 200-6000 tokens, this takes 33.)
 #pragma once
 
 namespace sc {
@@ -542,6 +542,8 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
             } else {
                 // Pairs of rows become pairs of columns: lane 4 g + c has row g's.
                 const int rr = row0 + n * 8 + at.g;
+                const bool mine = rr < rows && !bad;
+                bf16 *to = out_row(min(rr, rows - 1)) + 2 * at.c;
 #pragma unroll
                 for (int j = 0; j < DH / 16; ++j)
 #pragma unroll
@@ -549,10 +551,7 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
                         const uint32_t two =
                             transposed(pack_bf16(r.o[n][j][2 * h] * inv[0],
                                                  r.o[n][j][2 * h + 1] * inv[1]));
-                        if (rr < rows && !bad)
-                            gst(reinterpret_cast<uint32_t *>(out_row(rr) + 16 * j + 8 * h +
-                                                             2 * at.c),
-                                two);
+                        if (mine) gst(reinterpret_cast<uint32_t *>(to + 16 * j + 8 * h), two);
                     }
             }
         }
