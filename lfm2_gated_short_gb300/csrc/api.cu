@@ -234,7 +234,7 @@ sc_status check_page_call(const void *refs, int n_pages, const void *table, cons
         !ptr_ok(v, *pool_bytes, 16) || !ptr_ok(ws, need, 16))
         return SC_EINVAL;
     *scale_bytes = s.page > 0 ? times(times((size_t)n_pages * 4, (size_t)s.page), (size_t)L) : 0;
-    if (s.page > 0 && (!ptr_ok(s.k, *scale_bytes, 16) || !ptr_ok(s.v, *scale_bytes, 16)))
+    if (s.page > 0 && (!ptr_ok(s.k, *scale_bytes, 4) || !ptr_ok(s.v, *scale_bytes, 4)))
         return SC_EINVAL;
     return SC_OK;
 }
@@ -366,7 +366,7 @@ sc_status prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, int block, c
                               : sc::attention_workspace_bytes(shape);
     if (workspace_bytes < need) return SC_EINVAL;
     if (!ptr_ok(q, n_q, 16) || !ptr_ok(k_pages, n_pool, 16) || !ptr_ok(v_pages, n_pool, 16) ||
-        !ptr_ok(k_scales, n_sc, 16) || !ptr_ok(v_scales, n_sc, 16) || !ptr_ok(table, n_t, 4) ||
+        !ptr_ok(k_scales, n_sc, 4) || !ptr_ok(v_scales, n_sc, 4) || !ptr_ok(table, n_t, 4) ||
         !ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4) || !ptr_ok(out, n_out, 16) ||
         !ptr_ok(workspace, need, 16))
         return SC_EINVAL;
@@ -887,8 +887,8 @@ sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block
     const size_t n_sc = times((size_t)n_pages * (page_size / block), (size_t)Hkv * 4);
     const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
     if (!ptr_ok(k, n_k, 16) || !ptr_ok(v, n_v, 16) || !ptr_ok(k_pages, n_pool, 16) ||
-        !ptr_ok(v_pages, n_pool, 16) || !ptr_ok(k_scales, n_sc, 16) ||
-        !ptr_ok(v_scales, n_sc, 16) || !ptr_ok(table, n_t, 4) || !ptr_ok(lens, n_l, 4) ||
+        !ptr_ok(v_pages, n_pool, 16) || !ptr_ok(k_scales, n_sc, 4) ||
+        !ptr_ok(v_scales, n_sc, 4) || !ptr_ok(table, n_t, 4) || !ptr_ok(lens, n_l, 4) ||
         !ptr_ok(slot_ids, (size_t)N * 4, 4))
         return SC_EINVAL;
     if (!disjoint({{k_pages, n_pool}, {v_pages, n_pool}, {k_scales, n_sc}, {v_scales, n_sc}},
@@ -925,7 +925,7 @@ sc_status shortconv_pages_read_8bit(sc_dtype dtype, int Hkv, int Dh, int block,
     const size_t n_t = (size_t)n_slots * max_pages * 4, n_l = (size_t)n_slots * 4;
     const size_t n_i = (size_t)N * 4, n_st = starts ? n_i : 0;
     if (!ptr_ok(k_pages, n_pool, 16) || !ptr_ok(v_pages, n_pool, 16) ||
-        !ptr_ok(k_scales, n_sc, 16) || !ptr_ok(v_scales, n_sc, 16) || !ptr_ok(table, n_t, 4) ||
+        !ptr_ok(k_scales, n_sc, 4) || !ptr_ok(v_scales, n_sc, 4) || !ptr_ok(table, n_t, 4) ||
         !ptr_ok(lens, n_l, 4) || !ptr_ok(slot_ids, n_i, 4) ||
         !ptr_ok(cu_seqlens, n_i + 4, 4) || !opt_ok(starts, 4) || !ptr_ok(k, n_out, 16) ||
         !ptr_ok(v, n_out, 16))

@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
                     s_bad[st] = bad;
                 }
                 if constexpr (Q8) {
-                    copy_tile_scales(a, s_scale[st], id, s.ids.box() * box, box, boxes, it.h);
+                    copy_tile_scales<HG>(a, s_scale[st], id, s.ids.box() * box, box, boxes, it.h);
                     cp_async_arrive(&s_full[st]);
                 }
                 __syncwarp();

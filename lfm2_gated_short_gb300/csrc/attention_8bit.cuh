@@ -26,8 +26,9 @@ struct TileScales8 {
 
 // The producer warp's part: lane k starts group k's copy. `id`: lane b's page of box b (of
 // `box` keys, `boxes` of them there) of the tile that begins at key `key0` of the sequence. Copies
-// go to L2 (.cg), as the other reads of a kernel that may start beside another.
-template <int G>
+// go to L2 (.cg), as the other reads of a kernel that may start beside another. Arrays that do not
+// start on 16 bytes (a layer's of stacked ones) are read word by word.
+template <int HG, int G>
 __device__ __forceinline__ void copy_tile_scales(const AttnArgs &a, TileScales8<G> &s, int id,
                                                  int key0, int box, int boxes, int h) {
     const int lane = threadIdx.x & 31, which = lane / G & 1, g = lane % G;
@@ -39,11 +40,18 @@ __device__ __forceinline__ void copy_tile_scales(const AttnArgs &a, TileScales8<
         const int64_t total = (int64_t)a.pt.n_pages * per_page * a.Hkv;
         const int64_t i =
             ((int64_t)page * per_page + (((key0 + g * 8) & (a.pt.page_size - 1)) >> bl)) * a.Hkv + h;
+        const float *all = which ? a.s8.v : a.s8.k;
         const int64_t first = i & ~(int64_t)3;
         const uint32_t bytes = (uint32_t)min((int64_t)16, (total - first) * 4);
-        const float *from = (which ? a.s8.v : a.s8.k) + first;
+        const float *from = all + first;
         at = (int)(i - first);
-        if (SC_RD_OK(from, bytes))
+        if ((reinterpret_cast<uintptr_t>(all) & 15) != 0) {
+            at = 0;
+#pragma unroll
+            for (int e = 0; e < HG; ++e)
+                reinterpret_cast<int *>(&s.four[which][g])[e] =
+                    gld_l2(reinterpret_cast<const int32_t *>(all + i + e));
+        } else if (SC_RD_OK(from, bytes))
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                              smem_addr(&s.four[which][g])),
                          "l"(from), "r"(bytes));

@@ -131,7 +131,9 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_rope(RopeArgs a, int tokens
     // they are no whole number). A thread takes every 256th, kAhead of them in flight.
     const int turned = half / VP, rest = (a.Dh - a.R) / VP;
     const int per = turned + (a.copy ? (rest + 1) / 2 : 0), heads = a.Hq + a.Hkv;
-    const int dh = kRopeThreads / per, dc = kRopeThreads - dh * per;  // the step to a thread's next
+    // The step to a thread's next item: dt tokens, dh heads, dc places.
+    const int dhs = kRopeThreads / per, dc = kRopeThreads - dhs * per, dt = dhs / heads;
+    const int dh = dhs - dt * heads;
     int hd = threadIdx.x / per, c = threadIdx.x - hd * per, t = hd / heads;
     hd -= t * heads;
     constexpr int kAhead = VP * sizeof(T) == 16 ? 2 : 1;
@@ -161,13 +163,14 @@ __global__ void __launch_bounds__(kRopeThreads, 5) k_rope(RopeArgs a, int tokens
                 u[n].load(from + at[n][0]);
                 if (at[n][1] >= 0) w[n].load(from + at[n][1]);
             }
+            t += dt;
             hd += dh;
             c += dc;
             if (c >= per) {
                 c -= per;
                 ++hd;
             }
-            while (hd >= heads) {
+            if (hd >= heads) {
                 hd -= heads;
                 ++t;
             }

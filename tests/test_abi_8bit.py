@@ -33,7 +33,7 @@ SHAPES = [(dict(Hkv=0), EINVAL), (dict(Dh=0), EINVAL), (dict(Dh=24), EUNSUPPORTE
 @pytest.mark.parametrize("kw,status", SHAPES + [
     (dict(dt=7), EUNSUPPORTED), (dict(N=-1), EINVAL), (dict(D=0), EINVAL), (dict(ks=64), EINVAL),
     (dict(vs=129), EUNSUPPORTED), (dict(dt=F32, vs=130), EUNSUPPORTED), (dict(k=A + 8), EINVAL),
-    (dict(v=0), EINVAL), (dict(kp=0), EINVAL), (dict(vp=D_ + 4), EINVAL), (dict(kc=E + 4), EINVAL),
+    (dict(v=0), EINVAL), (dict(kp=0), EINVAL), (dict(vp=D_ + 4), EINVAL), (dict(kc=E + 2), EINVAL),
     (dict(vc=0), EINVAL), (dict(table=0), EINVAL), (dict(lens=H + 1), EINVAL), (dict(slots=0), EINVAL),
     (dict(vp=C), EINVAL), (dict(kc=C + 64), EINVAL), (dict(vc=E), EINVAL), (dict(k=C), EINVAL),
     (dict(table=F), EINVAL), (dict(N=1 << 20, D=1 << 12), EINVAL),
@@ -77,7 +77,7 @@ def resize(L, fn="resize", refs=A, n_pages=64, table=B, lens=C, n_slots=8, max_p
 @pytest.mark.parametrize("fn", ["resize", "fork"])
 @pytest.mark.parametrize("kw,status", [
     (dict(block=32), EUNSUPPORTED), (dict(Dh=8), EUNSUPPORTED), (dict(Hkv=0), EINVAL), (dict(kc=0), EINVAL),
-    (dict(vc=J + 8), EINVAL), (dict(kc=F + 64), EINVAL), (dict(vc=I), EINVAL), (dict(new=I), EINVAL),
+    (dict(vc=J + 1), EINVAL), (dict(kc=F + 64), EINVAL), (dict(vc=I), EINVAL), (dict(new=I), EINVAL),
     (dict(layers=-1), EINVAL), (dict(wsb=-1), EINVAL), (dict(ps=512), EUNSUPPORTED), (dict(n=9), EINVAL)])
 def test_resize_and_fork_refuse(L, fn, kw, status):
     assert resize(L, fn=fn, **kw) == status
@@ -110,7 +110,7 @@ def attention(L, Hq=4, Hkv=2, Dh=64, block=16, q=A, qs=256, N=3, D=2, kp=B, vp=C
     (dict(Hq=5), EINVAL), (dict(Dh=32), EUNSUPPORTED), (dict(Hq=512), EINVAL), (dict(qs=255), EINVAL),
     (dict(qs=260), EUNSUPPORTED), (dict(N=-1), EINVAL), (dict(D=0), EINVAL), (dict(shared=17), EINVAL),
     (dict(scale=0.0), EINVAL), (dict(scale=float("nan")), EINVAL), (dict(scale=1e31), EUNSUPPORTED),
-    (dict(kc=0), EINVAL), (dict(vc=E + 4), EINVAL), (dict(out=D_), EINVAL), (dict(ws=E), EINVAL),
+    (dict(kc=0), EINVAL), (dict(vc=E + 2), EINVAL), (dict(out=D_), EINVAL), (dict(ws=E), EINVAL),
     (dict(out=A), EINVAL), (dict(q=0), EINVAL), (dict(kp=B + 8), EINVAL), (dict(wsb=-1), EINVAL)])
 def test_attention_refuses(L, kw, status):
     assert attention(L, **kw) == status
