@@ -1272,15 +1272,18 @@ static cudaError_t launch_own(const AttnArgs &a, const CUtensorMap &mk, const CU
 
 typedef cudaError_t (*LaunchOwn)(const AttnArgs &, const CUtensorMap &, const CUtensorMap &, int,
                                  int *, cudaStream_t);
-template <int MR, int HG>
-static LaunchOwn own_of(int Dh) {
-    return Dh == 64 ? launch_own<64, MR, HG> : launch_own<128, MR, HG>;
-}
-template <int MR>
-static LaunchOwn own8_of(int Dh, int heads) {
+template <int DH, int MR>
+static LaunchOwn own8_of(int heads) {
     if constexpr (MR < 32)
-        if (heads == 4) return own_of<MR, 4>(Dh);
-    return heads == 2 ? own_of<MR, 2>(Dh) : own_of<MR, 1>(Dh);
+        if (heads == 4) return launch_own<DH, MR, 4>;
+    return heads == 2 ? launch_own<DH, MR, 2> : launch_own<DH, MR, 1>;
+}
+template <int DH>
+static LaunchOwn own_of(bool q8, int MR, int heads) {
+    if (!q8) return MR == 16 ? launch_own<DH, 16, 0> : launch_own<DH, 32, 0>;
+    return MR == 8    ? own8_of<DH, 8>(heads)
+           : MR == 16 ? own8_of<DH, 16>(heads)
+                      : own8_of<DH, 32>(heads);
 }
 
 template <int DH>
@@ -1318,7 +1321,8 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     const int heads = own_heads(s, q8), MR = own_rows(s, q8);
     x.part = a.own_part + own_part_floats(s, q8);
     if (q8) a.s8 = *scales;
-    const int own_keys = !q8 ? OwnCfg<64, 16, 0>::KT : 128 / (heads * (MR == 32 ? 2 : 1));  // of a tile
+    const int own_keys =  // of a tile
+        !q8 ? OwnCfg<64, 16, 0>::KT : (s.Dh == 64 ? 128 : 64) / (heads * (MR == 32 ? 2 : 1));
     const int own_box = pt.page_size < own_keys ? pt.page_size : own_keys;
     CUtensorMap mk, mv;
     cudaError_t e = q8 ? map_codes(&mk, k_pages, pt, s.Hkv, s.Dh, own_box, heads)
@@ -1355,10 +1359,7 @@ cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q
     }
     const int sms = a.beside ? sm_count - x.n_cta : sm_count;
     int grid = 0;
-    const LaunchOwn own = !q8       ? (MR == 16 ? own_of<16, 0>(s.Dh) : own_of<32, 0>(s.Dh))
-                          : MR == 8  ? own8_of<8>(s.Dh, heads)
-                          : MR == 16 ? own8_of<16>(s.Dh, heads)
-                                     : own8_of<32>(s.Dh, heads);
+    const LaunchOwn own = s.Dh == 64 ? own_of<64>(q8, MR, heads) : own_of<128>(q8, MR, heads);
     e = own(a, mk, mv, sms, &grid, stream);
     if (e != cudaSuccess) return e;
     // With few rows all lanes of a warp share one: a whole step over two streams of 30-40

@@ -105,8 +105,11 @@ __device__ __forceinline__ uint32_t lds4(uint32_t addr) {
 }
 
 // An item is MR rows of a sequence for HG kv heads at once. A consumer warp takes WR rows of one
-// head by 32 keys of a tile. Both products have the keys' matrix first (16 keys, or 16 columns of
-// V, by 8 rows of queries), so that 8 rows fill a product and a code is converted once for all rows.
+// head by 32 keys of a tile, or 16 with heads of 128: a row's sums are twice as many registers there,
+// and tiles of half the bytes leave twice as many on their way (72 sequences of 5 drafts by 7 heads:
+// 12.1 us, with 32 keys 13.8; 64 sequences of 8 by 7: 18.8 for 20.7; short single tokens even).
+// Both products have the keys' matrix first (16 keys, or 16 columns of V, by 8 rows of queries), so
+// that 8 rows fill a product and a code is converted once for all rows.
 template <int DH, int MR_, int HG>
 struct Own8Cfg {
     static constexpr int kDh = DH;
@@ -116,15 +119,16 @@ struct Own8Cfg {
     static constexpr int NT = WR / 8;                         // row tiles of a warp
     static constexpr int kHeads = HG;
     static constexpr int KG = 4 / (HG * RG);                  // key groups
-    static constexpr int KT = 32 * KG;                        // keys of a tile
+    static constexpr int KH = DH == 64 ? 2 : 1;               // halves of 16 keys of a warp
+    static constexpr int KT = 16 * KH * KG;                   // keys of a tile
     static constexpr int kWarps = 4;
     static constexpr int kThreads = 32 * (kWarps + 1);
     static constexpr int kRow = HG * DH == 64 ? 64 : 128;     // bytes of a key in a column block
     static constexpr int NC = HG * DH / kRow;                 // column blocks
     static constexpr uint32_t kBlk = KT * kRow;
     static constexpr uint32_t kV = NC * kBlk;                 // the tile's V behind its K
-    static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows or Dh 128 8 to 32
-    static constexpr int kCtas = DH == 64 ? 3 : 2;
+    static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows 8
+    static constexpr int kCtas = DH == 64 || MR == 8 ? 3 : 2;
     static constexpr int kQBufs = 2;                          // items described ahead
     static constexpr uint32_t kQ = 0;                         // the consumers read their queries
     static constexpr int kOs = DH + 4;                        // floats of a row to join
@@ -133,7 +137,7 @@ struct Own8Cfg {
     // reserved shared memory.
     static constexpr size_t kRest = 1024 + kJoin;
     static constexpr int kFit = (int)((228 * 1024 / kCtas - 4608 - kRest) / kStage);
-    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr int kStages = kFit < 8 ? kFit : 8;
     static_assert(kStages >= 2, "shared memory of an SM");
     static constexpr size_t kSmem = kRest + kStages * kStage;
     static constexpr int kSlot = MR * (DH + 2);               // floats of a part and head
@@ -159,7 +163,7 @@ struct Lane8 {
     int g, c, half;      // half: of its column block, where that holds two heads
     uint32_t base;       // of this warp's head and its first key
     uint32_t k_at[2];    // chunk c of the keys at places g, g + 8; the next 64 columns: XOR 64
-    uint32_t v_at;       // for ldsm2_t8, columns 0 .. 15; the next 16: XOR 16
+    uint32_t v_at;       // for ldsm2_t8: both halves' keys, or 32 columns of 16 keys; the next: XOR
     int key;             // at place g; at place g + 8: 2 more
     __device__ __forceinline__ Lane8(int hh, int row0) {
         const int lane = threadIdx.x & 31;
@@ -172,7 +176,8 @@ struct Lane8 {
         k_at[0] = at(key, c);
         k_at[1] = at(key + 2, c);
         const int i = lane & 15;  // word i / 4, byte i % 4
-        v_at = at((lane & 16) + key_of(2 * (i >> 2) + (i & 1) + 4 * (i & 2)), 0);
+        const int i_key = key_of(2 * (i >> 2) + (i & 1) + 4 * (i & 2));
+        v_at = C::KH == 2 ? at((lane & 16) + i_key, 0) : at(i_key, lane >> 4);
     }
     static __device__ __forceinline__ int key_of(int i) {
         return (i >> 2 & 1) * 8 + (i & 1) * 4 + (i >> 3) * 2 + (i >> 1 & 1);
@@ -242,13 +247,14 @@ struct Rows8 {
     }
 };
 
-// o += P V over a warp's 32 keys, of each row only the keys it sees; e[n][2 h + x]: the weights of
+// o += P V over a warp's keys, of each row only the keys it sees; e[n][2 h + x]: the weights of
 // the key at place g + 8 x of 16, half h.
 template <typename C>
-__device__ __forceinline__ void product_one_by_one8(Rows8<C> &r, const f32x2 (&e)[C::NT][4],
-                                                    uint32_t v, const Lane8<C> &at, int key0) {
+__device__ __forceinline__ void product_one_by_one8(Rows8<C> &r,
+                                                    const f32x2 (&e)[C::NT][2 * C::KH], uint32_t v,
+                                                    const Lane8<C> &at, int key0) {
 #pragma unroll 1
-    for (int k = 0; k < 32; ++k) {
+    for (int k = 0; k < 16 * C::KH; ++k) {
         const int g = (k >> 3 & 1) * 4 + (k & 1) * 2 + (k >> 2 & 1);  // of the lanes that hold key k
         const int x = (k >> 4) * 2 + (k >> 1 & 1);
         float w[C::NT][2];
@@ -256,7 +262,7 @@ __device__ __forceinline__ void product_one_by_one8(Rows8<C> &r, const f32x2 (&e
         for (int n = 0; n < C::NT; ++n) {
             f32x2 mine = e[n][0];
 #pragma unroll
-            for (int i = 1; i < 4; ++i)
+            for (int i = 1; i < 2 * C::KH; ++i)
                 if (i == x) mine = e[n][i];
             f2_split(mine, w[n][0], w[n][1]);
 #pragma unroll
@@ -282,16 +288,16 @@ __device__ __forceinline__ void product_one_by_one8(Rows8<C> &r, const f32x2 (&e
     }
 }
 
-// One tile's part of a warp: its rows by 32 keys (from key key0 on).
+// One tile's part of a warp: its rows by its keys (from key key0 on).
 template <typename C>
 __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C> &at, int hh,
                                       int group0, int key0, int len, int least, Rows8<C> &r) {
-    constexpr int DH = C::kDh, NT = C::NT, kG = C::KT / 8;
+    constexpr int DH = C::kDh, NT = C::NT, KH = C::KH, kKeys = 16 * KH, kG = C::KT / 8;
     const int lane = threadIdx.x & 31;
     const uint32_t v = k + C::kV;
-    f32x2 s[NT][4];  // s[n][2 h + x]: key at place g + 8 x of 16, half h
+    f32x2 s[NT][2 * KH];  // s[n][2 h + x]: key at place g + 8 x of 16, half h
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < KH; ++h) {
         float d[NT][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -317,12 +323,12 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
             s[n][2 * h + 1] = f2_make(d[n][2], d[n][3]);
         }
     }
-    const bool some = key0 + 32 > least;  // some row does not see some of these keys
-    float top[NT][2], inverse[2];
+    const bool some = key0 + kKeys > least;  // some row does not see some of these keys
+    float top[NT][2], inverse[KH];
 #pragma unroll
     for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {  // the lane's keys of each 16 share their scales
+    for (int h = 0; h < KH; ++h) {  // the lane's keys of each 16 share their scales
         const int group = group0 + 2 * h + (at.g >> 2);
         uint32_t four = scales + group * 16 + hh * 4, four_v = four + 16 * kG;
         if constexpr (C::kHeads != 4) {  // TileScales8: four[2][kG], then at[2][kG]
@@ -379,11 +385,11 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
                 for (int e = 0; e < 4; ++e) r.o[n][j][e] *= f[e & 1];
         }
     }
-    uint32_t pf[NT][4];  // the weights as the second product's second operand
+    uint32_t pf[NT][2 * KH];  // the weights as the second product's second operand
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
+        for (int x = 0; x < 2 * KH; ++x) {
             float e0, e1;
             f2_split(f2_add(s[n][x], r.off[n]), e0, e1);
             e0 = ex2(e0);
@@ -392,12 +398,12 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
             r.l[n] = f2_fma(s[n][x], f2_make(inverse[x >> 1], inverse[x >> 1]), r.l[n]);
             pf[n][x] = transposed(pack_f16(e0, e1));  // 2^-11 relative at most
         }
-    uint32_t live[2] = {~0u, ~0u};  // the lane's keys inside the sequence, a byte each
+    uint32_t live[KH] = {};  // the lane's keys inside the sequence, a byte each
     if (some) {
         // A draft that some row does not see: were its V NaN, a weight of 0 would not keep it
         // from that row, so the product is made one by one.
         bool nan = false;
-        const int from = max(least - key0, 0), to = min(len - key0, 32);
+        const int from = max(least - key0, 0), to = min(len - key0, kKeys);
         for (int x = lane; x < (to - from) * (DH / 16); x += 32) {
             const uint4 w = lds16(v + at.at(from + x / (DH / 16), x % (DH / 16)));
 #pragma unroll
@@ -410,28 +416,28 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
         }
         // Codes past the sequence may be NaN, which a weight of 0 would not silence.
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            live[h] = 0;
+        for (int h = 0; h < KH; ++h) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (key0 + 16 * h + at.key_of(2 * at.c + (i & 1) + 4 * (i & 2)) < len)
                     live[h] |= 0xFFu << 8 * i;
         }
     }
+    // The 16 x 16 blocks of V, two at a time: both halves of 16 columns, or 32 columns.
 #pragma unroll
-    for (int j = 0; j < DH / 16; ++j) {
+    for (int u = 0; u < KH * DH / 32; ++u) {
         uint32_t w[4];
-        ldsm2_t8(w, v + (at.v_at ^ j * 16));
-        if (some) {
-            w[0] &= live[0];
-            w[1] &= live[0];
-            w[2] &= live[1];
-            w[3] &= live[1];
-        }
+        ldsm2_t8(w, v + (at.v_at ^ u * (KH == 2 ? 16 : 32)));
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const uint32_t a[4] = {e4m3x2_f16x2(w[2 * h]), e4m3x2_f16x2(w[2 * h + 1]),
-                                   e4m3x2_f16x2_hi(w[2 * h]), e4m3x2_f16x2_hi(w[2 * h + 1])};
+        for (int x = 0; x < 2; ++x) {
+            const int h = KH == 2 ? x : 0, j = KH == 2 ? u : 2 * u + x;
+            uint32_t w0 = w[2 * x], w1 = w[2 * x + 1];
+            if (some) {
+                w0 &= live[h];
+                w1 &= live[h];
+            }
+            const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2_hi(w0),
+                                   e4m3x2_f16x2_hi(w1)};
 #pragma unroll
             for (int n = 0; n < NT; ++n)
                 mma16816_f16(r.o[n][j], a, pf[n][2 * h], pf[n][2 * h + 1]);
@@ -445,7 +451,7 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
     constexpr int DH = C::kDh, ST = C::kStages, QB = C::kQBufs, KG = C::KG, WR = C::WR, NT = C::NT;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int kw = warp % KG, rg = warp / KG % C::RG, hh = warp / (KG * C::RG);
-    const Lane8<C> at(hh, kw * 32);
+    const Lane8<C> at(hh, kw * 16 * C::KH);
     uint32_t ring_at = 0, ring_phase = 0;
     bool dead = false;
     for (uint32_t items = 0;; ++items) {
@@ -481,15 +487,15 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         }
         bool bad = false;
         const int from = prefix_keys(a, len);
-        int key0 = from + item.t0 * C::KT + kw * 32;
+        int key0 = from + item.t0 * C::KT + kw * 16 * C::KH;
         for (int t = 0; t < item.n; ++t, key0 += C::KT) {
             if (!dead && !mbar_wait_bounded(&s.full[ring_at], ring_phase)) {
                 raise_error(SC_DEV_TIMEOUT);
                 dead = true;  // no more waits: the rest runs through on what is there
             }
             bad |= s.bad[ring_at] != 0;
-            tile8<C>(s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh, kw * 4,
-                     key0, len, least, r);
+            tile8<C>(s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh,
+                     kw * 2 * C::KH, key0, len, least, r);
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[ring_at]);
             if (++ring_at == ST) {
