@@ -579,8 +579,8 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
  * a copied page takes its scales along.
  *
  * shortconv_prefix_attention_8bit: shortconv_prefix_attention over such a pool: q and out
- * bf16, keys and values code times scale. A call with shared_pages unpacks that part once, to
- * bf16 in the workspace.
+ * bf16, keys and values code times scale. A call with many shared pages unpacks them once, to
+ * bf16 in the workspace; one with few reads them with each sequence's own.
  */
 sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block, const void *k,
                                       int64_t k_stride, const void *v, int64_t v_stride, int N,

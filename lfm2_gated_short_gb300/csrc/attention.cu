@@ -1242,8 +1242,21 @@ static size_t prefix_part_floats(const AttnShape &s) {
 static size_t workspace_bytes(const AttnShape &s, bool q8) {
     return cum_bytes(s) + (own_part_floats(s, q8) + prefix_part_floats(s)) * 4;
 }
+// Over an 8-bit cache a shared prefix is unpacked and has a kernel of its own, two launches more.
+// Where its codes, read again for every row tile of every sequence (from L2), are few, k_own takes
+// them with the rest. Us unpacked and with the rest, of 9 to 140 sequences: 0.5 MB in all 25 to 29
+// and 8 to 10; 8 MB 20 to 46 and 10 to 16 (rows of 8), 23 to 37 and 15 to 21 (more rows); 33 MB 19
+// to 36 and 13 to 19, and 25 to 48 and 19 to 40 (one in four up to 3 % slower); 50 MB 21 to 32 and
+// 16 to 22, and 23 to 35 and 24 to 35; 67 MB 20 to 38 and 19 to 24, and 29 to 48 and 26 to 51.
+static AttnShape planned8(AttnShape s, int page_size) {
+    const int64_t row_tiles = ((int64_t)s.D * (s.Hq / s.Hkv) + 31) / 32;
+    const double again = (double)s.N * (double)row_tiles * s.shared_pages * page_size * s.Hkv * s.Dh * 2;
+    if (again <= (own_rows(s, true) == 8 ? 48 : 32) * 1048576.0) s.shared_pages = 0;
+    return s;
+}
 size_t attention_workspace_bytes(const AttnShape &s) { return workspace_bytes(s, false); }
-size_t attention8_workspace_bytes(const AttnShape &s, int page_size) {
+size_t attention8_workspace_bytes(const AttnShape &given, int page_size) {
+    const AttnShape s = planned8(given, page_size);
     return workspace_bytes(s, true) + 2 * unpacked_bytes(s, page_size);
 }
 
@@ -1297,12 +1310,13 @@ static cudaError_t launch_prefix(const PrefixArgs &x, const CUtensorMap &mq, con
                       mq, mk, mv);
 }
 
-cudaError_t launch_prefix_attention(const AttnShape &s, const void *q, int64_t q_stride,
+cudaError_t launch_prefix_attention(const AttnShape &given, const void *q, int64_t q_stride,
                                     const void *k_pages, const void *v_pages,
                                     const Scales8 *scales, const PageTable &pt,
                                     const int32_t *slots, float scale, void *out, void *workspace,
                                     int sm_count, cudaStream_t stream) {
     const bool q8 = scales != nullptr;
+    const AttnShape s = q8 ? planned8(given, pt.page_size) : given;
     PrefixArgs x = prefix_plan(s, pt.page_size, sm_count, q8);
     AttnArgs &a = x.a;
     a.q = (const bf16 *)q;

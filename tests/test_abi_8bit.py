@@ -120,9 +120,14 @@ def test_attention_workspace(L):
     f = L.shortconv_prefix_attention_8bit_workspace_bytes
     plain = L.shortconv_prefix_attention_workspace_bytes
     assert f(8, 2, 64, 3, 1, 0, 16) > 0
-    unpacked = 2 * 4 * 16 * 2 * 64 * 2
-    prefix = plain(8, 2, 64, 3, 1, 4) - plain(8, 2, 64, 3, 1, 0)
-    assert f(8, 2, 64, 3, 1, 4, 16) == f(8, 2, 64, 3, 1, 0, 16) + prefix + unpacked
+    unpacked = 2 * 5000 * 16 * 2 * 64 * 2
+    prefix = plain(8, 2, 64, 3, 1, 5000) - plain(8, 2, 64, 3, 1, 0)
+    assert f(8, 2, 64, 3, 1, 5000, 16) == f(8, 2, 64, 3, 1, 0, 16) + prefix + unpacked
+    assert f(8, 2, 64, 3, 1, 4, 16) == f(8, 2, 64, 3, 1, 0, 16)  # few: read with the rest
+    last = 0  # more shared pages never need less
+    for shared in (0, 1, 64, 512, 2048, 4096, 4097, 8192, 65536):
+        assert last <= f(8, 2, 64, 3, 1, shared, 16)
+        last = f(8, 2, 64, 3, 1, shared, 16)
     for bad in ((8, 3, 64, 3, 1, 0, 16), (8, 2, 96, 3, 1, 0, 16), (8, 2, 64, -1, 1, 0, 16),
                 (8, 2, 64, 3, 0, 0, 16), (8, 2, 64, 3, 1, -1, 16), (8, 2, 64, 3, 1, 1, 4),
                 (8, 2, 64, 3, 1, 1 << 30, 16)):

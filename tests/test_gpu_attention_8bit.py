@@ -84,6 +84,96 @@ def test_long_shared_prefix(Dh, ps, N, D, G):
     check(build([4096 + D + 3 * i for i in range(N)], shared=n, ps=ps, D=D, G=G, Hkv=1, Dh=Dh, seed=5))
 
 
+# A prefix that many rows share is unpacked once; the workspace then has room for it.
+
+def unpacked(lens, shared, **kw):
+    c = build(lens, shared=shared, **kw)
+    ps, Hkv, Dh = c["k"].shape[1:]
+    need = [sc.prefix_attention_8bit_workspace_bytes(c["q"].shape[1], Hkv, Dh, len(lens), c["D"], n, ps)
+            for n in (0, shared)]
+    assert need[1] - need[0] >= 4 * shared * ps * Hkv * Dh
+    return c
+
+
+@pytest.mark.parametrize("Dh,Hkv,G,D,N,shared,ps,B", [
+    (64, 2, 64, 4, 10, 105, 16, 16), (64, 1, 128, 3, 9, 153, 16, 8), (128, 1, 5, 9, 23, 23, 256, 128),
+    (64, 8, 4, 1, 47, 17, 64, 8), (128, 3, 7, 2, 60, 101, 8, 8), (64, 4, 8, 8, 35, 69, 32, 32),
+    (128, 5, 1, 1, 90, 27, 32, 16)])
+def test_unpacked_prefix(Dh, Hkv, G, D, N, shared, ps, B):
+    """Own parts of D tokens, to several tiles; ends on and around page and tile borders."""
+    r = np.random.default_rng(G)
+    own = [D, D + 1, ps, ps + 1, 64 + D, 129, *r.integers(D, 300, N)][:N]
+    check(unpacked([shared * ps + max(n, D) for n in own], shared, Dh=Dh, Hkv=Hkv, G=G, D=D, ps=ps, B=B,
+                   seed=N))
+
+
+def test_rows_that_end_inside_an_unpacked_prefix():
+    c = unpacked([105 * 16 + 20] * 11, 105, G=64, D=4, seed=31)
+    for i, n in enumerate((105 * 16 + 3, 105 * 16, 900, 3, 0)):  # the first that sees all is the sixth
+        c["lens"][c["slots"][i]] = n
+    check(c)
+
+
+def test_an_unpacked_prefix_with_bad_data():
+    c = unpacked([105 * 16 + 20] * 11, 105, G=64, D=4, seed=32)
+    ref, mag = reference(c, 0.125)
+    d = on_device(c)
+    for bad_page in (-1, len(c["k"]), 2 ** 31 - 1):
+        slots, lens, table = c["slots"].copy(), c["lens"].copy(), c["table"].copy()
+        slots[0], lens[slots[1]] = -5, -1
+        table[slots[3], 105] = bad_page
+        out = torch.full(d["q"].shape, 7.0, dtype=torch.bfloat16, device="cuda")
+        args = dict(shared_pages=105, k_scales=d["ks"], v_scales=d["vs"], out=out)
+        sc.prefix_attention(d["q"], d["k"], d["v"], i32(table), i32(lens), i32(slots), 4, **args)
+        assert sc.get_error() == sc.DEV_BAD_SLOT | sc.DEV_BAD_LENGTH | sc.DEV_BAD_PAGE
+        got = out.double().cpu().numpy().reshape(11, 4, 128, 64)
+        skipped = [0, 1, 3]
+        assert (got[skipped] == 7.0).all()
+        err = np.abs(got.reshape(ref.shape) - ref)
+        ok = err <= 1.5 * EPS * mag + 1.01 * EPS * np.abs(ref) + 2.0 ** -40
+        assert np.delete(ok.reshape(got.shape), skipped, 0).all()
+        table[slots[2], 50] = bad_page  # in the prefix as the first good sequence has it: no row
+        out.fill_(7.0)
+        sc.prefix_attention(d["q"], d["k"], d["v"], i32(table), i32(lens), i32(slots), 4, **args)
+        assert sc.get_error() & sc.DEV_BAD_PAGE
+        assert (out == 7.0).all()
+
+
+def test_an_unpacked_prefix_on_streams_and_in_graphs():
+    cases = [unpacked([105 * 16 + 20 + 31 * i for i in range(11)], 105, G=64, D=4, seed=33 + i)
+             for i in range(2)]
+    dev = [on_device(c) for c in cases]
+
+    def run(d, out=None):
+        return sc.prefix_attention(d["q"], d["k"], d["v"], d["table"], d["lens"], d["slots"], 4,
+                                   shared_pages=105, k_scales=d["ks"], v_scales=d["vs"], out=out)
+    want = [run(d).clone() for d in dev]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in dev]
+    outs = [torch.zeros_like(w) for w in want]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for d, s, o in zip(dev, streams, outs):
+            with torch.cuda.stream(s):
+                run(d, o)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
+    graph, x = torch.cuda.CUDAGraph(), {n: t.clone() for n, t in dev[0].items()}
+    with torch.cuda.graph(graph):
+        got = run(x)
+    for d, w in zip(dev[::-1], want[::-1]):
+        for n in ("q", "table", "lens", "slots"):
+            x[n].copy_(d[n])
+        for n in ("k", "v"):
+            x[n].view(torch.uint8).copy_(d[n].view(torch.uint8))
+        x["ks"].copy_(d["ks"])
+        x["vs"].copy_(d["vs"])
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, w)
+    assert sc.get_error() == 0
+
+
 @pytest.mark.parametrize("Dh", [64, 128])
 def test_long_sequences_are_split(Dh):
     check(build([9000, 4001], Hkv=1, G=4, Dh=Dh, ps=64, B=32, seed=6))

@@ -124,7 +124,8 @@ def attention(c, trim=None):
 @pytest.mark.parametrize("shared,D,G,Hkv,Dh,B", [(0, 1, 1, 1, 64, 8), (0, 3, 7, 2, 64, 16),
                                                  (0, 2, 5, 2, 128, 8), (3, 1, 3, 4, 64, 16),
                                                  (9, 5, 7, 1, 128, 16), (5, 8, 4, 2, 64, 8),
-                                                 (4, 1, 128, 1, 64, 16), (0, 4, 4, 4, 128, 8)])
+                                                 (4, 1, 128, 1, 64, 16), (0, 4, 4, 4, 128, 8),
+                                                 (105, 8, 64, 2, 64, 16)])
 def test_attention(shared, D, G, Hkv, Dh, B):
     c = build([shared * 16 + n for n in (9, 33, 200, 16, 70)], shared=shared, B=B, D=D, G=G, Hkv=Hkv,
               Dh=Dh, seed=G)
