@@ -12,6 +12,13 @@
 //
 // (The register MMA of e4m3 itself is made of conversions of both operands and further MMAs on this
 // GPU: 56 million warp instructions for 128 sequences of 200-6000 tokens, this takes 33.)
+//
+// What bounds it: the codes' bytes with up to 8 rows (128 sequences of 200-6000 tokens by 8 x 4 heads:
+// 404 MB from DRAM, the same that are needed, in 71 us; issue slots 43 %); with 16 and 32 rows the
+// conversions and the softmax in the issue slots (128 of 500-1500 tokens: 34 us a call with 4 rows, 41
+// with 16, 65 with 32, whose k_own issues in half of its cycles, waiting for its own results). Not better: four
+// row tiles a warp instead of two row groups (k_own 46 to 80 us, spills); eight-row groups with heads of
+// 128 (74 to 84); 256-byte L2 promotion with an item a head (920 MB read for 404).
 #pragma once
 
 namespace sc {
@@ -128,7 +135,7 @@ struct Own8Cfg {
     static constexpr uint32_t kBlk = KT * kRow;
     static constexpr uint32_t kV = NC * kBlk;                 // the tile's V behind its K
     static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows 8
-    static constexpr int kCtas = DH == 64 || MR == 8 ? 3 : 2;
+    static constexpr int kCtas = DH == 64 || MR == 8 ? 3 : 2;  // by registers: 128 a thread, or 168
     static constexpr int kQBufs = 2;                          // items described ahead
     static constexpr uint32_t kQ = 0;                         // the consumers read their queries
     static constexpr int kOs = DH + 4;                        // floats of a row to join
@@ -607,7 +614,10 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
 }
 
 // The shared prefix as bf16 [keys, Hkv, Dh], for k_prefix: every key is read by many row tiles, so
-// it is unpacked once, and stays in L2. Exact: a code has 4 bits, a scale none.
+// it is unpacked once, and stays in L2. Exact: a code has 4 bits, a scale none. 16384 tokens of 8 x 64
+// (50 MB read and written): 12 us; 2976 of 2 x 128: 5.5, a chain of dependent reads. Converting in k_prefix
+// instead, by four warps more between the copies and the products, took a step of 128 x 8 drafts behind
+// 16384 tokens from 188 to 315 us, and 37 x 3 behind 2976 from 28.6 to 35: each row tile converts again.
 constexpr int kUnpackThreads = 256;
 constexpr int kUnpackWords = 2;  // of each pool, of a lane at once
 static __global__ void __launch_bounds__(kUnpackThreads, 4)

@@ -95,7 +95,13 @@ struct Places {
 };
 
 // A warp takes one block of K or V: it finds the new tokens' largest magnitude, moves the
-// earlier codes where the scale rises, and writes the new ones.
+// earlier codes where the scale rises, and writes the new ones. The block's values stay in registers
+// between the two passes over them, so that they are read once.
+// 16391 bf16 tokens of 8 x 64 in blocks of 32 (50 MB read and written): 12.9 us in a graph, 3.9 TB/s of
+// the 6.75 that a copy reaches; 24 warps an SM (80 registers) are 2.25 times filled, half the issue
+// slots go, and each wave loads, works and stores as one. Not better: addresses stepped instead of
+// multiplied (17 % fewer instructions, 16.7 us), and with that 32 warps an SM (spills, 17.3 cold for
+// 15.5). One token a sequence is latency: 3.0 us for 64 of them.
 template <typename T>
 __global__ void __launch_bounds__(kAppendThreads)
     k_append8(PageTable pt, const T *__restrict__ k, int64_t k_stride, const T *__restrict__ v,
@@ -104,7 +110,7 @@ __global__ void __launch_bounds__(kAppendThreads)
     pdl_wait();
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    // The call's units are below 2^28.
+    // The call's units are below 2^29.
     const uint32_t unit = blockIdx.x * (kAppendThreads / 32) + (threadIdx.x >> 5);
     const uint32_t rest = unit / (uint32_t)c.Hkv, pair = rest >> 1;
     const int h = (int)(unit - rest * c.Hkv), i = (int)(pair / (uint32_t)nb);
@@ -211,7 +217,9 @@ struct Codes<float> {
 
 // Rows cu[i] .. cu[i + 1] - 1 are sequence i's tokens from starts[i] on. A warp takes units of R
 // rows of both pools; its lanes find the places of its next 32 rows (a chain of dependent
-// reads) at once.
+// reads) at once. Bound by DRAM: 16 sequences of 2001-9000 tokens of 8 x 64 from somewhere inside on, to
+// bf16 (203 MB read and written): 35.4 us, 5.7 TB/s of 6.75. With the places found one row after the
+// other it was 49.6.
 template <typename T>
 __global__ void __launch_bounds__(kReadThreads, 4)
     k_read8(PageTable pt, const int32_t *__restrict__ slots, const int32_t *__restrict__ cu,
@@ -333,7 +341,8 @@ template <typename T>
 static cudaError_t append8(const PageTable &pt, const void *k, int64_t k_stride, const void *v,
                            int64_t v_stride, const int32_t *slots, int N, int D, const Cache8 &c,
                            cudaStream_t stream) {
-    const int nb = (int)(((int64_t)D + 2 * (1 << c.block_log2) - 2) >> c.block_log2);  // blocks that D tokens meet at most
+    // Blocks that D tokens meet at most.
+    const int nb = (int)(((int64_t)D + 2 * (1 << c.block_log2) - 2) >> c.block_log2);
     const int64_t threads = (int64_t)N * nb * 2 * c.Hkv * 32;
     return launch_pdl(k_append8<T>, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)),
                       dim3(kAppendThreads), 0, stream, pt, (const T *)k, k_stride, (const T *)v,

@@ -10,7 +10,10 @@
 // cosines come from the fraction's distance to the nearest quarter turn.
 //
 // A tile is a few tokens: its sines and cosines are computed once, for all heads, into
-// shared memory; the rest streams the heads through registers, bound by their bytes.
+// shared memory; the rest streams the heads through registers, bound by their bytes: 16384 tokens of
+// 32 + 8 bf16 heads of 64, forward and backward (336 MB), 56.7 us, 5.9 TB/s of the 6.75 that a copy
+// reaches; 5001 of 14 + 2 fp32 heads of 128 at far positions, half turned (164 MB), 30.5 us, 5.4 TB/s. A
+// step's few tokens are latency, 2.8 us.
 #include <cuda_bf16.h>
 
 #include "common.cuh"

@@ -264,3 +264,18 @@ def test_same_bits_every_time():
     a = attend(c)
     for _ in range(3):
         assert torch.equal(a, attend(c))
+
+
+@pytest.mark.parametrize("Dh,G,D", [(64, 4, 1), (64, 8, 2), (64, 8, 4), (128, 5, 3)])
+def test_queries_that_are_not_finite_stay_in_their_rows(Dh, G, D):
+    c = build([300, 45, 1, 0], Hkv=4, G=G, D=D, Dh=Dh, seed=20)
+    clean = attend(c)
+    rows = [(0, 1), (D, 0), (D, 2)]
+    for (t, h), x in zip(rows, (float("nan"), float("inf"), -float("inf"))):
+        c["q"][t, h, 3] = x
+    got = attend(c)
+    assert sc.get_error() == 0
+    for t, h in rows:
+        assert torch.isnan(got[t, h]).all()
+        got[t, h] = clean[t, h]
+    assert torch.equal(got, clean)
