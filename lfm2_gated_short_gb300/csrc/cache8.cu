@@ -17,7 +17,8 @@
 
 namespace sc {
 
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 128;
+constexpr int kAppendCtas = 7;  // of an SM; with 6, 7, 8, 9: 13.2, 11.0, 11.9, 13.6 us (spills) of the prompt below
 constexpr int kReadThreads = 256;
 
 __device__ __forceinline__ int slot_length(const PageTable &pt, int slot, bool report) {
@@ -41,16 +42,20 @@ struct Eight {
 #pragma unroll
         for (int i = 0; i < Dt<T>::Q; ++i) r.q[i] = ld_plain(reinterpret_cast<const uint4 *>(p) + i);
     }
-    // The largest magnitude's bits, of bf16 in both halves of a word: infinities and NaN lie above
-    // all finite ones.
+    // The largest magnitude's bits, of bf16 in both halves of a word, without NaN (that maximum
+    // gives the other operand).
     __device__ __forceinline__ uint32_t most(uint32_t m) const {
         const uint32_t *w = reinterpret_cast<const uint32_t *>(r.q);
 #pragma unroll
         for (int e = 0; e < 4 * Dt<T>::Q; ++e) {
             if constexpr (sizeof(T) == 2)
-                asm("max.u16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e] & 0x7FFF7FFFu));
+                asm("{\n\t.reg .b32 a;\n\t"
+                    "abs.bf16x2 a, %1;\n\t"
+                    "max.bf16x2 %0, %0, a;\n\t}"
+                    : "+r"(m)
+                    : "r"(w[e]));
             else
-                m = max(m, w[e] & 0x7FFFFFFFu);
+                m = __float_as_uint(fmaxf(__uint_as_float(m), fabsf(__uint_as_float(w[e]))));
         }
         return m;
     }
@@ -65,17 +70,29 @@ struct Eight {
         }
         return m;
     }
+    // `inverse`: of the scale, a power of two, so that a bf16 product is exact too (or so small that
+    // its code is 0).
     __device__ __forceinline__ uint2 codes(float inverse) const {
-        float f[kCh];
-        Dt<T>::unpack(r.q, f);
         uint32_t w[4];
+        const uint32_t both = __float_as_uint(inverse) | __float_as_uint(inverse) >> 16;
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(r.q);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = f32_e4m3x2(f[2 * e] * inverse, f[2 * e + 1] * inverse);
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (sizeof(T) == 2) {
+                const uint32_t x = bf2_mul(u[e], both);
+                w[e] = f32_e4m3x2(bf16_lo(x), bf16_hi(x));
+            } else {
+                w[e] = f32_e4m3x2(__uint_as_float(u[2 * e]) * inverse,
+                                  __uint_as_float(u[2 * e + 1]) * inverse);
+            }
+        }
         return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
     }
 };
 
-// A lane's places among a block's rows of `per` eights: lane, lane + 32, ...
+// A lane's places among a block's rows of `per` eights: lane, lane + 32, ... EVEN: `per` divides
+// 32, so that a lane keeps its column.
+template <bool EVEN>
 struct Places {
     int per, row, col, drow, dcol;
     __device__ __forceinline__ Places(int per_, int lane) : per(per_) {
@@ -86,6 +103,7 @@ struct Places {
     }
     __device__ __forceinline__ void next() {
         row += drow;
+        if (EVEN) return;
         col += dcol;
         if (col >= per) {
             col -= per;
@@ -97,13 +115,12 @@ struct Places {
 // A warp takes one block of K or V: it finds the new tokens' largest magnitude, moves the
 // earlier codes where the scale rises, and writes the new ones. The block's values stay in registers
 // between the two passes over them, so that they are read once.
-// 16391 bf16 tokens of 8 x 64 in blocks of 32 (50 MB read and written): 12.9 us in a graph, 3.9 TB/s of
-// the 6.75 that a copy reaches; 24 warps an SM (80 registers) are 2.25 times filled, half the issue
-// slots go, and each wave loads, works and stores as one. Not better: addresses stepped instead of
-// multiplied (17 % fewer instructions, 16.7 us), and with that 32 warps an SM (spills, 17.3 cold for
-// 15.5). One token a sequence is latency: 3.0 us for 64 of them.
-template <typename T>
-__global__ void __launch_bounds__(kAppendThreads)
+// 16391 bf16 tokens of 8 x 64 in blocks of 32 (50 MB read and written): 11.0 us in a graph, 4.6 TB/s of
+// the 6.75 that a copy reaches; of 8 x 128 in blocks of 16, 18.1 us, 5.6 TB/s. A wave of 28 warps an
+// SM loads, works and stores as one, and the last of two is not full. CTAs of 256 threads give 12.9 and
+// 22 (24 warps an SM). One token a sequence is latency: 2.7 us for 64 of them.
+template <typename T, bool EVEN>
+__global__ void __launch_bounds__(kAppendThreads, kAppendCtas)
     k_append8(PageTable pt, const T *__restrict__ k, int64_t k_stride, const T *__restrict__ v,
               int64_t v_stride, const int32_t *__restrict__ slots, int N, int D, int nb,
               Cache8 c) {
@@ -127,6 +144,23 @@ __global__ void __launch_bounds__(kAppendThreads)
     if (b0 >= len) return;
     const int lo = max((int)b0, from), hi = (int)min(b0 + (1 << lb), (int64_t)len);
     const int id = gld(pt.table + (int64_t)slot * pt.max_pages + ((int)b0 >> lp));
+    const int64_t stride = is_v ? v_stride : k_stride;
+    const T *x = (is_v ? v : k) + ((int64_t)i * D + (lo - first)) * stride + h * c.Dh;
+    const int n = hi - lo;  // new rows
+    constexpr int kKeep = sizeof(T) == 2 ? 8 : 4;  // a lane's first eights stay in registers
+    Eight<T> keep[kKeep];
+    const Places<EVEN> begin(c.Dh / 8, lane);
+    // Places past the new rows repeat the last one's values, which changes no maximum: the kept
+    // ones need no branches, four at a time.
+    const bool many = n * begin.per > 128;
+    {
+        Places<EVEN> p = begin;
+#pragma unroll
+        for (int q = 0; q < kKeep; ++q, p.next()) {
+            if (q == 4 && !many) break;
+            keep[q].load(x + min(p.row, n - 1) * stride + p.col * 8);
+        }
+    }
     if (id < 0 || id >= pt.n_pages) {
         if (lane == 0) raise_error(SC_DEV_BAD_PAGE);
         return;
@@ -137,21 +171,14 @@ __global__ void __launch_bounds__(kAppendThreads)
                            (((int64_t)id << lp) + r0) * width + h * c.Dh;  // of the block's first token
     uint32_t *scale = reinterpret_cast<uint32_t *>(is_v ? c.v_scales : c.k_scales) +
                       (((int64_t)id << (lp - lb)) + (r0 >> lb)) * c.Hkv + h;
-    const int64_t stride = is_v ? v_stride : k_stride;
-    const T *x = (is_v ? v : k) + ((int64_t)i * D + (lo - first)) * stride + h * c.Dh;
-    const int n = hi - lo;  // new rows
-    constexpr int kKeep = sizeof(T) == 2 ? 8 : 4;  // a lane's first eights stay in registers
-    Eight<T> keep[kKeep];
-    Places at(c.Dh / 8, lane);
-#pragma unroll
-    for (int q = 0; q < kKeep; ++q, at.next())
-        if (at.row < n) keep[q].load(x + at.row * stride + at.col * 8);
     // Every eight of the block, the kept ones first: f(eight, row, column).
     auto each = [&](auto &&f) {
-        Places p(c.Dh / 8, lane);
+        Places<EVEN> p = begin;
 #pragma unroll
-        for (int q = 0; q < kKeep; ++q, p.next())
-            if (p.row < n) f(keep[q], p.row, p.col);
+        for (int q = 0; q < kKeep; ++q, p.next()) {
+            if (q == 4 && !many) return;
+            f(keep[q], p.row, p.col);
+        }
         for (; p.row < n; p.next()) {
             Eight<T> u;
             u.load(x + p.row * stride + p.col * 8);
@@ -173,11 +200,12 @@ __global__ void __launch_bounds__(kAppendThreads)
     const float inverse = __uint_as_float(inverse_bits(now));
     unsigned char *to = codes + (lo - b0) * width;
     each([&](const Eight<T> &u, int row, int col) {
-        gst(reinterpret_cast<uint2 *>(to + row * width + col * 8), u.codes(inverse));
+        const uint2 w = u.codes(inverse);
+        if (row < n) gst(reinterpret_cast<uint2 *>(to + row * width + col * 8), w);
     });
     if (lo == b0 || now == was) return;
     const float step = __uint_as_float(was) * inverse;  // 2^-184 at least: exact or zero
-    for (Places p(c.Dh / 8, lane); p.row < (int)(lo - b0); p.next()) {
+    for (Places<EVEN> p = begin; p.row < (int)(lo - b0); p.next()) {
         uint2 *q = reinterpret_cast<uint2 *>(codes + p.row * width + p.col * 8);
         const uint2 w = gld(q);
         uint32_t out[2];
@@ -344,7 +372,8 @@ static cudaError_t append8(const PageTable &pt, const void *k, int64_t k_stride,
     // Blocks that D tokens meet at most.
     const int nb = (int)(((int64_t)D + 2 * (1 << c.block_log2) - 2) >> c.block_log2);
     const int64_t threads = (int64_t)N * nb * 2 * c.Hkv * 32;
-    return launch_pdl(k_append8<T>, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)),
+    const auto kernel = 256 % c.Dh == 0 ? k_append8<T, true> : k_append8<T, false>;
+    return launch_pdl(kernel, dim3((unsigned)((threads + kAppendThreads - 1) / kAppendThreads)),
                       dim3(kAppendThreads), 0, stream, pt, (const T *)k, k_stride, (const T *)v,
                       v_stride, slots, N, D, nb, c);
 }
