@@ -193,8 +193,8 @@ struct Scales {
 // Shape of an 8-bit cache, with a page_size that check_pages takes (or will refuse).
 sc_status check_8bit(int Hkv, int Dh, int block, int page_size) {
     if (Hkv <= 0 || Dh <= 0 || block <= 0) return SC_EINVAL;
-    if (Dh % 16 != 0 || Dh > 1024 || (int64_t)Hkv * Dh > (1 << 24) || block < 8 || (block & (block - 1)) != 0 ||
-        block > page_size)
+    if (Dh % 16 != 0 || Dh > 1024 || (int64_t)Hkv * Dh > (1 << 24) || block < 8 ||
+        (block & (block - 1)) != 0 || block > page_size)
         return SC_EUNSUPPORTED;
     return SC_OK;
 }

@@ -1230,10 +1230,16 @@ static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count, b
     // rule ends at 608); of 1-30 own tokens 22.8 and 23.7 with 600, 25.5 and 25.4 with 768.
     // Heads of 128: 46.9 and 58.5 with 64, 58.9 and 66.0 with 256 (the rule ends at 304). Slower
     // beside: 16 sequences behind 1024 tokens (32 units), 25.9 and 20.3, behind 2048, 23.6 and 21.0.
-    // Over an 8-bit cache the own parts leave k_prefix more: four units of 64-wide heads too, where
-    // it then has half the SMs at most. 37 x 3 drafts of 14 heads behind 2976 tokens, us with four and
-    // with eight: 21.2 and 25.0; 64 sequences behind 512 tokens 25.4 and 27.4, behind 2048 26.4 and 27.1.
-    const int units = s.Dh == 64 && !(q8 && x.U <= 4 * (ctas / 2)) ? 8 : 4;
+    // Over an 8-bit cache the own parts leave k_prefix more: a quarter of the units a CTA, and twice
+    // as many where that would take more than half the SMs. 64 sequences behind 1024 tokens (64 units),
+    // us with 1, 2, 4, 8 a CTA: 19.8, 18.3, 20.0, 23.8; behind 2048 (128) 27.0, 19.9, 20.7, 25.0; behind
+    // 4096 (256) 29.1, 29.0, 22.6, 26.2. Heads of 128: 100 sequences behind 3200 (50) 23.1, 29.5, 31.0,
+    // 39.4; 16 of 40 heads (96 units) 34.6, 25.8, 30.5, 44.4; 37 x 3 drafts of 14 behind 2976 (192)
+    // 38.1, 38.1, 28.6, 36.1.
+    int units = s.Dh == 64 ? 8 : 4;
+    if (q8)
+        for (int n = units / 4; n < units; n *= 2)
+            if (x.U <= (int64_t)n * (ctas / 2)) units = n;
     x.a.beside = x.U > 0 && x.U <= (int64_t)units * (ctas / 2);
     if (x.a.beside) x.n_cta = (int)((x.U + units - 1) / units);
     return x;

@@ -18,7 +18,8 @@
 namespace sc {
 
 constexpr int kAppendThreads = 128;
-constexpr int kAppendCtas = 7;  // of an SM; with 6, 7, 8, 9: 13.2, 11.0, 11.9, 13.6 us (spills) of the prompt below
+// CTAs of an SM: with 6, 7, 8 and 9 (which spills) k_append8's prompt below takes 13.2, 11.0, 11.9, 13.6 us.
+constexpr int kAppendCtas = 7;
 constexpr int kReadThreads = 256;
 
 __device__ __forceinline__ int slot_length(const PageTable &pt, int slot, bool report) {
