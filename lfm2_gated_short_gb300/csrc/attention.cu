@@ -357,11 +357,11 @@ __device__ __forceinline__ void consume16(const AttnArgs &a, int rows, int per,
         if (item.rt != rt_now) set_rows(item.rt);
         uint32_t qf[DH / 16][4];
 #pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk) {
-                const int ch = kk * 2 + (lane >> 4);
-                ldsm4(qf[kk], s.qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
-                                  swz(rg * 16 + (lane & 15), ch & 7));
-            }
+        for (int kk = 0; kk < DH / 16; ++kk) {
+            const int ch = kk * 2 + (lane >> 4);
+            ldsm4(qf[kk], s.qs_a + qb * C::kQ + (ch >> 3) * C::MR * 128 +
+                              swz(rg * 16 + (lane & 15), ch & 7));
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.qempty[qb]);
         // A row's running maximum m (of the scores before scaling), the score that moves
@@ -390,110 +390,110 @@ __device__ __forceinline__ void consume16(const AttnArgs &a, int rows, int per,
                 dead = true;  // no more waits: the rest runs through on what is there
             }
             bad |= s.bad[ring_at] != 0;
-                const uint32_t stage = s.ring_a + ring_at * C::kStage;
-                const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
-                const bool tail = key0 + 16 * KB > len;
-                if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
-                    const int first = max(0, len - key0);
-                    for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
-                        const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
-                        *reinterpret_cast<uint4 *>(s.ring + ring_at * C::kStage +
-                                                   (C::NB + (ch >> 3)) * C::kBlk +
-                                                   (kw * 16 * KB + r) * 128 +
-                                                   (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    __syncwarp();
+            const uint32_t stage = s.ring_a + ring_at * C::kStage;
+            const uint32_t kt = stage + k_lane, vt = stage + C::NB * C::kBlk + v_lane;
+            const bool tail = key0 + 16 * KB > len;
+            if (tail) {  // V rows past the sequence hold anything: 0 x NaN must not reach the sum
+                const int first = max(0, len - key0);
+                for (int x = lane; x < (16 * KB - first) * C::NB * 8; x += 32) {
+                    const int r = first + x / (C::NB * 8), ch = x % (C::NB * 8);
+                    *reinterpret_cast<uint4 *>(s.ring + ring_at * C::kStage +
+                                               (C::NB + (ch >> 3)) * C::kBlk +
+                                               (kw * 16 * KB + r) * 128 +
+                                               (ch & 7) * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
-                float sc[2 * KB][4];
+                __syncwarp();
+            }
+            float sc[2 * KB][4];
+#pragma unroll
+            for (int nt = 0; nt < 2 * KB; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk)
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb) {
+                    uint32_t b[4];
+                    ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
+                    mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
+                    mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
+                }
+            if (key0 + 16 * KB > least) {  // some row does not see some of these keys
 #pragma unroll
                 for (int nt = 0; nt < 2 * KB; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[nt][e] = 0.0f;
+                    for (int e = 0; e < 4; ++e)
+                        if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
+                            sc[nt][e] = -INFINITY;
+            }
+            float top[2];
 #pragma unroll
-                for (int kk = 0; kk < DH / 16; ++kk)
+            for (int p = 0; p < 2; ++p) {
+                top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
 #pragma unroll
-                    for (int kb = 0; kb < KB; ++kb) {
+                for (int nt = 1; nt < 2 * KB; ++nt)
+                    top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
+            }
+            // Only when some score passes its row's limit are the row maxima needed. A row that
+            // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
+            if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
+                    top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
+                    if (!(top[p] > limit[p])) continue;
+                    const float f = ex2((m[p] - top[p]) * a.scale_log2);
+                    m[p] = top[p];
+                    limit[p] = top[p] + rescale;
+                    off[p] = -top[p] * a.scale_log2;
+                    l2[p] = f2_mul(l2[p], f2_make(f, f));
+#pragma unroll
+                    for (int d = 0; d < DH / 8; ++d) {
+                        o[d][2 * p] *= f;
+                        o[d][2 * p + 1] *= f;
+                    }
+                }
+            }
+            uint32_t pf[KB][4];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const f32x2 off2 = f2_make(off[p], off[p]);
+#pragma unroll
+                for (int nt = 0; nt < 2 * KB; ++nt) {
+                    float e0, e1;
+                    f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
+                    e0 = ex2(e0);
+                    e1 = ex2(e1);
+                    l2[p] = f2_add(l2[p], f2_make(e0, e1));
+                    // P enters the second product as bf16: 2^-8 relative a term at most.
+                    pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
+                }
+            }
+            // A draft that some row does not see: were its V not finite, a weight of 0 would
+            // not keep it from that row, so the block's product is made one by one.
+            bool plain = false;
+            if (key0 + 16 * KB > least) {
+                const unsigned char *vb = s.ring + ring_at * C::kStage + C::NB * C::kBlk;
+                const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
+                for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
+                    plain |= not_finite(*reinterpret_cast<const uint4 *>(
+                        vb + (x % (DH / 8) >> 3) * C::kBlk +
+                        swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
+                plain = __any_sync(~0u, plain);
+                if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
+            }
+            if (!plain) {
+#pragma unroll
+                for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+                    for (int dd = 0; dd < DH / 16; ++dd) {
                         uint32_t b[4];
-                        ldsm4(b, (kt ^ ((kk & 3) << 5)) + (kk >> 2) * C::kBlk + kb * 2048);
-                        mma16816(sc[2 * kb], qf[kk], b[0], b[1]);
-                        mma16816(sc[2 * kb + 1], qf[kk], b[2], b[3]);
+                        ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
+                        mma16816(o[2 * dd], pf[kb], b[0], b[1]);
+                        mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
                     }
-                if (key0 + 16 * KB > least) {  // some row does not see some of these keys
-#pragma unroll
-                    for (int nt = 0; nt < 2 * KB; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (key0 + nt * 8 + (lane & 3) * 2 + (e & 1) >= see[e >> 1])
-                                sc[nt][e] = -INFINITY;
-                }
-                float top[2];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    top[p] = fmaxf(sc[0][2 * p], sc[0][2 * p + 1]);
-#pragma unroll
-                    for (int nt = 1; nt < 2 * KB; ++nt)
-                        top[p] = max3(top[p], sc[nt][2 * p], sc[nt][2 * p + 1]);
-                }
-                // Only when some score passes its row's limit are the row maxima needed. A row that
-                // has seen no key yet keeps m = -inf, offset 0 and sums of zero.
-                if (__any_sync(~0u, top[0] > limit[0] || top[1] > limit[1])) {
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) {
-                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 1));
-                        top[p] = fmaxf(top[p], __shfl_xor_sync(~0u, top[p], 2));
-                        if (!(top[p] > limit[p])) continue;
-                        const float f = ex2((m[p] - top[p]) * a.scale_log2);
-                        m[p] = top[p];
-                        limit[p] = top[p] + rescale;
-                        off[p] = -top[p] * a.scale_log2;
-                        l2[p] = f2_mul(l2[p], f2_make(f, f));
-#pragma unroll
-                        for (int d = 0; d < DH / 8; ++d) {
-                            o[d][2 * p] *= f;
-                            o[d][2 * p + 1] *= f;
-                        }
-                    }
-                }
-                uint32_t pf[KB][4];
-#pragma unroll
-                for (int p = 0; p < 2; ++p) {
-                    const f32x2 off2 = f2_make(off[p], off[p]);
-#pragma unroll
-                    for (int nt = 0; nt < 2 * KB; ++nt) {
-                        float e0, e1;
-                        f2_split(f2_fma(f2_make(sc[nt][2 * p], sc[nt][2 * p + 1]), scale2, off2), e0, e1);
-                        e0 = ex2(e0);
-                        e1 = ex2(e1);
-                        l2[p] = f2_add(l2[p], f2_make(e0, e1));
-                        // P enters the second product as bf16: 2^-8 relative a term at most.
-                        pf[nt / 2][nt % 2 * 2 + p] = pack_bf16(e0, e1);
-                    }
-                }
-                // A draft that some row does not see: were its V not finite, a weight of 0 would
-                // not keep it from that row, so the block's product is made one by one.
-                bool plain = false;
-                if (key0 + 16 * KB > least) {
-                    const unsigned char *vb = s.ring + ring_at * C::kStage + C::NB * C::kBlk;
-                    const int lo = max(least - key0, 0), hi = min(len - key0, 16 * KB);
-                    for (int x = lane; x < (hi - lo) * DH / 8; x += 32)
-                        plain |= not_finite(*reinterpret_cast<const uint4 *>(
-                            vb + (x % (DH / 8) >> 3) * C::kBlk +
-                            swz(kw * 16 * KB + lo + x / (DH / 8), x & 7)));
-                    plain = __any_sync(~0u, plain);
-                    if (plain) product_one_by_one<DH, KB>(o, pf, vb, C::kBlk, kw * 16 * KB, key0, see);
-                }
-                if (!plain) {
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-                        for (int dd = 0; dd < DH / 16; ++dd) {
-                            uint32_t b[4];
-                            ldsm4_t(b, (vt ^ ((dd & 3) << 5)) + (dd >> 2) * C::kBlk + kb * 2048);
-                            mma16816(o[2 * dd], pf[kb], b[0], b[1]);
-                            mma16816(o[2 * dd + 1], pf[kb], b[2], b[3]);
-                        }
-                }
-                if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
+            }
+            if (tail) fence_proxy_async_smem();  // the zeroed rows before the next copy there
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[ring_at]);
             if (++ring_at == ST) {
@@ -853,15 +853,13 @@ struct RowParts {
 template <int DH>
 struct PartFinder {
     RowParts p = {};
-    int i, j, h, g, own_heads;
+    int i, per, it, at;  // sequence, its items, the row's item, the row's place in a part
     bool valid, prefix;
-    __device__ __forceinline__ PartFinder(const PrefixArgs &x, int token, int hq, int own_heads_)
-        : own_heads(own_heads_) {
+    __device__ __forceinline__ PartFinder(const PrefixArgs &x, int token, int hq, int MR,
+                                          int own_heads) {
         const AttnArgs &a = x.a;
         i = token / a.D;
-        j = token - i * a.D;
-        h = hq / a.G;
-        g = hq - h * a.G;
+        const int j = token - i * a.D, h = hq / a.G, g = hq - h * a.G;
         // Slots and lengths need no wait: k_own let this kernel start when what wrote them was done.
         int slot;
         const int len = seq_len(a, i, &slot, false);
@@ -878,22 +876,25 @@ struct PartFinder {
             p.prefix_step = x.split ? kPSlot : 2 * kPSlot;
             p.prefix_n = (c1 - c0 + 1) * (x.split ? 2 : 1);
         }
-    }
-    __device__ __forceinline__ void find_own(const AttnArgs &a, int MR, int own_ctas) {
-        const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
-        const int groups = a.Hkv / own_heads, hi = h / own_heads, hh = h - hi * own_heads;
-        const int r = j * a.G + g, per = (a.D * a.G + MR - 1) / MR * groups;
-        const int slot_n = MR * (DH + 2), rt = r / MR, orow = r - rt * MR;
+        const int log_h = __ffs(own_heads) - 1, log_m = __ffs(MR) - 1;  // powers of two
+        const int groups = a.Hkv >> log_h, hi = h >> log_h, hh = h & (own_heads - 1);
+        const int r = j * a.G + g, rt = r >> log_m, orow = r & (MR - 1);
+        const int slot_n = MR * (DH + 2);
+        per = ((a.D * a.G + MR - 1) >> log_m) * groups;
+        it = rt * groups + hi;
+        at = hh * slot_n + orow * DH;
         p.own_step = slot_n * own_heads;
+        p.own_m = MR * DH + orow - orow * DH;
+    }
+    __device__ __forceinline__ void find_own(const AttnArgs &a, int own_ctas) {
+        const int64_t U = gld(a.cum + a.N), u_i = gld(a.cum + i), u_n = gld(a.cum + i + 1);
         if (u_n <= u_i) return;
         const int64_t d = u_n - u_i;
         const int64_t T = d <= UINT32_MAX ? (uint32_t)d / (uint32_t)per : d / per;
         const int n_cta = (int)min((int64_t)own_ctas, U);
-        const int it = rt * groups + hi;
         const int64_t u0 = u_i + it * T;
         const int c0 = share_of(u0, U, n_cta), c1 = share_of(u0 + T - 1, U, n_cta);
-        p.own_at = a.own_part + ((int64_t)i * per + it + c0) * p.own_step + hh * slot_n + orow * DH;
-        p.own_m = MR * DH + orow - orow * DH;
+        p.own_at = a.own_part + ((int64_t)i * per + it + c0) * p.own_step + at;
         p.own_n = c1 - c0 + 1;
         if (p.own_n == 1 && !prefix) {
             p.own_n = 0;
@@ -917,10 +918,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     const int token = blockIdx.x;
     const int at = blockIdx.y * (kMergeThreads / L) + threadIdx.x / L;
     const int hq = min(at, Hq - 1);  // lanes past the last row join it and write nothing
-    PartFinder<DH> find(x, token, hq, own_heads);
+    PartFinder<DH> find(x, token, hq, MR, own_heads);
     pdl_wait();
     pdl_launch_dependents();
-    find.find_own(a, MR, own_ctas);
+    find.find_own(a, own_ctas);
     bool mine = find.valid && at < Hq && !find.p.written;
     const float *prefix_at = find.p.prefix_at, *own_at = find.p.own_at;
     const int prefix_n = find.p.prefix_n, own_n = find.p.own_n, prefix_m = find.p.prefix_m;
@@ -1018,10 +1019,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     __shared__ int s_bad[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c8 = lane % C, group = lane / C;
     const int token = blockIdx.x, hq = blockIdx.y;
-    PartFinder<DH> find(x, token, hq, own_heads);
+    PartFinder<DH> find(x, token, hq, MR, own_heads);
     pdl_wait();
     pdl_launch_dependents();
-    find.find_own(a, MR, own_ctas);
+    find.find_own(a, own_ctas);
     const RowParts &p = find.p;
     const int parts = p.prefix_n + p.own_n;
     auto part_at = [&](int q) {
