@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
         s_seq = a.N;
     }
     __syncthreads();
-    // Beside k_prefix: that kernel let this one start only after its own wait, so what this
-    // one reads is there; it waits for k_prefix at its end, since k_merge, which waits
+    // Beside k_prefix: that kernel let this one start only after its own wait (or k_unpack's), so what
+    // this one reads is there; it waits for k_prefix at its end, since k_merge, which waits
     // for this one alone, reads what both wrote.
     if (!a.beside) pdl_wait();
     pdl_launch_dependents();

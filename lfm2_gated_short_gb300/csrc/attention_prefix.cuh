@@ -216,7 +216,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = b.tmem;
-    pdl_wait();
+    // k_unpack let this kernel start after its own wait, so that all but what it writes is there:
+    // k_own may start beside it too, and it is waited for as late as can be.
+    if (!x.packed) pdl_wait();
     pdl_launch_dependents();
     // The first listed sequence whose rows all see the whole prefix names its pages.
     for (int i = tid; i < a.N; i += kPfxThreads) {
@@ -226,6 +228,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
             break;
         }
     }
+    if (x.packed) pdl_wait();
     __syncthreads();
     const int leader = b.leader;
     const int64_t u0 = share_begin(blockIdx.x, x.U, x.n_cta);
