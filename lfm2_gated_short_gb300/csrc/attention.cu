@@ -1233,10 +1233,10 @@ static PrefixArgs prefix_plan(const AttnShape &s, int page_size, int sm_count, b
     // beside: 16 sequences behind 1024 tokens (32 units), 25.9 and 20.3, behind 2048, 23.6 and 21.0.
     // Over an 8-bit cache the own parts leave k_prefix more: a quarter of the units a CTA, and twice
     // as many where that would take more than half the SMs. 64 sequences behind 1024 tokens (64 units),
-    // us with 1, 2, 4, 8 a CTA: 19.8, 18.3, 20.0, 23.8; behind 2048 (128) 27.0, 19.9, 20.7, 25.0; behind
-    // 4096 (256) 29.1, 29.0, 22.6, 26.2. Heads of 128: 100 sequences behind 3200 (50) 23.1, 29.5, 31.0,
-    // 39.4; 16 of 40 heads (96 units) 34.6, 25.8, 30.5, 44.4; 37 x 3 drafts of 14 behind 2976 (192)
-    // 38.1, 38.1, 28.6, 36.1.
+    // us with 1, 2, 4, 8 a CTA: 18.1, 17.3, 19.2, 23.1; behind 2048 (128) 26.8, 18.9, 20.2, 24.1; behind
+    // 4096 (256) 28.4, 28.5, 22.0, 25.9; x 4 drafts behind 512 (128) 33.1, 23.6, 21.6, 28.5. Heads of 128:
+    // 100 sequences behind 3200 (50) 23.1, 29.3, 30.8, 39.2; 16 of 40 heads (96 units) 35.1, 26.1, 30.0,
+    // 44.5; 37 x 3 drafts of 14 behind 2976 (192) 37.2, 37.2, 28.3, 35.7.
     int units = s.Dh == 64 ? 8 : 4;
     if (q8)
         for (int n = units / 4; n < units; n *= 2)
@@ -1257,10 +1257,10 @@ static size_t workspace_bytes(const AttnShape &s, bool q8) {
 }
 // Over an 8-bit cache a shared prefix is unpacked and has a kernel of its own, two launches more.
 // Where its codes, read again for every row tile of every sequence (from L2), are few, k_own takes
-// them with the rest. Us unpacked and with the rest, of 9 to 140 sequences: 0.5 MB in all 25 to 29
-// and 8 to 10; 8 MB 20 to 46 and 10 to 16 (rows of 8), 23 to 37 and 15 to 21 (more rows); 33 MB 19
-// to 36 and 13 to 19, and 25 to 48 and 19 to 40 (one in four up to 3 % slower); 50 MB 21 to 32 and
-// 16 to 22, and 23 to 35 and 24 to 35; 67 MB 20 to 38 and 19 to 24, and 29 to 48 and 26 to 51.
+// them with the rest. Us unpacked and with the rest, of 9 to 140 sequences, 0.5 MB in all: 13 to 23 and
+// 8 to 13; 8 MB: up to 8 rows 15 to 20 and 10 to 16, more rows 19 to 24 and 14 to 21; 33 MB: 17 to 24 and
+// 14 to 21, 22 to 47 and 18 to 39 (one in five up to 8 % slower); 50 MB: 18 to 30 and 16 to 26 (one in
+// four up to 6 % slower), 24 to 43 and 21 to 45; 67 MB: 18 to 32 and 18 to 28, 29 to 48 and 23 to 50.
 static AttnShape planned8(AttnShape s, int page_size) {
     const int64_t row_tiles = ((int64_t)s.D * (s.Hq / s.Hkv) + 31) / 32;
     const double again = (double)s.N * (double)row_tiles * s.shared_pages * page_size * s.Hkv * s.Dh * 2;
