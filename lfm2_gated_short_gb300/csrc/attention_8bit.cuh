@@ -135,7 +135,9 @@ struct Own8Cfg {
     static constexpr uint32_t kBlk = KT * kRow;
     static constexpr uint32_t kV = NC * kBlk;                 // the tile's V behind its K
     static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows 8
-    static constexpr int kCtas = DH == 64 || MR == 8 ? 3 : 2;  // by registers: 128 a thread, or 168
+    // By registers: 128 a thread, or 168. Heads of 64, us with 2, 3 and 4: 128 sequences of 200-6000
+    // tokens 97, 79, 80; 8 drafts of 128 of 500-1500 67, 65, 94; 512 of 20-60 28.8, 29.9, 33.2.
+    static constexpr int kCtas = DH == 64 || MR == 8 ? 3 : 2;
     static constexpr int kQBufs = 2;                          // items described ahead
     static constexpr uint32_t kQ = 0;                         // the consumers read their queries
     static constexpr int kOs = DH + 4;                        // floats of a row to join
