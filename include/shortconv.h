@@ -548,12 +548,12 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
 
 /*
  * The cache in 8 bits. The pools hold e4m3 codes, [n_pages, page_size, Hkv, Dh] (Dh a
- * multiple of 16, at most 1024), and beside each pool lie scales, fp32 [n_pages, page_size / block, Hkv]
- * (4-byte aligned; attention is a little faster with 16): a power of two for every block of
- * `block` tokens of a page (a power of two, 8 to page_size) and kv head; a value is code times
- * scale. Tables, lengths and refs
- * are the cache's above. Only a scale's exponent is read, held to 2^-64 .. 2^120, so pools and
- * scales may start out uninitialised. L layers stack pools and scales alike.
+ * multiple of 16, at most 1024), and beside each pool lie scales, fp32 [n_pages,
+ * page_size / block, Hkv] (4-byte aligned; attention is a little faster with 16): a power of two
+ * for every block of `block` tokens of a page (a power of two, 8 to page_size) and kv head; a
+ * value is code times scale. Tables, lengths and refs are the cache's above. Only a scale's
+ * exponent is read, held to 2^-64 .. 2^120, so pools and scales may start out uninitialised. L
+ * layers stack pools and scales alike.
  *
  * shortconv_pages_append_8bit: shortconv_pages_append into such a pool. A block's scale
  * becomes the least power of two s with |x| <= 448 s for the new tokens that the block
