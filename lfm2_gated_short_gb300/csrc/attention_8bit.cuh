@@ -13,12 +13,13 @@
 // (The register MMA of e4m3 itself is made of conversions of both operands and further MMAs on this
 // GPU: 56 million warp instructions for 128 sequences of 200-6000 tokens, this takes 33.)
 //
-// What bounds it: the codes' bytes with up to 8 rows (128 sequences of 200-6000 tokens by 8 x 4 heads:
-// 404 MB from DRAM, the same that are needed, in 71 us; issue slots 43 %); with 16 and 32 rows the
-// conversions and the softmax in the issue slots (128 of 500-1500 tokens: 34 us a call with 4 rows, 41
-// with 16, 65 with 32, whose k_own issues in half of its cycles, waiting for its own results). Not
-// better: four row tiles a warp instead of two row groups (k_own 46 to 80 us, spills); eight-row groups with heads of
-// 128 (74 to 84); 256-byte L2 promotion with an item a head (920 MB read for 404).
+// What bounds it: the codes' bytes with up to 8 rows (128 sequences of 200-6000 tokens by 8 x 4
+// heads: 404 MB from DRAM, the same that are needed, in 71 us; issue slots 43 %); with 16 and 32
+// rows the conversions and the softmax in the issue slots (128 of 500-1500 tokens: 34 us a call
+// with 4 rows, 41 with 16, 65 with 32, whose k_own issues in half of its cycles, waiting for its
+// own results). Not better: four row tiles a warp instead of two row groups (k_own 46 to 80 us,
+// spills); eight-row groups with heads of 128 (74 to 84); 256-byte L2 promotion with an item a head
+// (920 MB read for 404).
 #pragma once
 
 namespace sc {
