@@ -742,12 +742,18 @@ const char *shortconv_status_string(sc_status status);
  * SC_EINVAL for a region number outside [0, 16); SC_EUNSUPPORTED in the
  * standard build.
  *
+ * shortconv_bounds_starve_next: the next shortconv_prefix_attention or
+ * _8bit call copies no tile of the sequences' own keys, so that its waits
+ * for them run out (about 2 s) as behind a copy that never lands:
+ * SC_DEV_TIMEOUT. SC_EUNSUPPORTED in the standard build.
+ *
  * shortconv_bounds_take_first_bad: synchronize `stream` and return in
  * *addr the first device address refused since the last take (0 if none),
  * clearing it. SC_EUNSUPPORTED in the standard build.
  */
 int shortconv_bounds_checked(void);
 sc_status shortconv_bounds_trim_next(int region, uint64_t bytes);
+sc_status shortconv_bounds_starve_next(void);
 sc_status shortconv_bounds_take_first_bad(void *stream, uint64_t *addr);
 
 #ifdef __cplusplus

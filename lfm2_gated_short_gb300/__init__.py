@@ -125,6 +125,7 @@ def lib() -> ctypes.CDLL:
             L.shortconv_bounds_checked.argtypes = []
             L.shortconv_bounds_checked.restype = i32
             L.shortconv_bounds_trim_next.argtypes = [i32, ctypes.c_uint64]
+            L.shortconv_bounds_starve_next.argtypes = []
             L.shortconv_bounds_take_first_bad.argtypes = [p, ctypes.POINTER(ctypes.c_uint64)]
             L.shortconv_status_string.argtypes = [i32]
             L.shortconv_status_string.restype = ctypes.c_char_p
@@ -137,7 +138,7 @@ def lib() -> ctypes.CDLL:
                       "pages_resize_8bit", "pages_fork_8bit", "pages_compact_8bit",
                       "pages_append_8bit", "pages_read_8bit", "prefix_attention_8bit", "rope",
                       "get_error", "check_wait_limit",
-                      "bounds_trim_next", "bounds_take_first_bad"):
+                      "bounds_trim_next", "bounds_starve_next", "bounds_take_first_bad"):
                 getattr(L, "shortconv_" + f).restype = i32
             _lib = L
     return _lib
@@ -971,6 +972,11 @@ def bounds_checked() -> bool:
 def bounds_trim_next(region: int, nbytes: int) -> None:
     """Bounds-checked build: shorten buffer ``region`` of the next call's record."""
     _raise_on("shortconv_bounds_trim_next", lib().shortconv_bounds_trim_next(region, nbytes))
+
+
+def bounds_starve_next() -> None:
+    """Bounds-checked build: the next attention call's waits for its own keys run out."""
+    _raise_on("shortconv_bounds_starve_next", lib().shortconv_bounds_starve_next())
 
 
 def bounds_take_first_bad(stream=None, device=None) -> int:

@@ -1145,6 +1145,15 @@ sc_status shortconv_bounds_trim_next(int region, uint64_t bytes) {
 #endif
 }
 
+sc_status shortconv_bounds_starve_next(void) {
+#ifdef SC_BOUNDS_CHECK
+    sc::bounds_starve_next_attention();
+    return SC_OK;
+#else
+    return SC_EUNSUPPORTED;
+#endif
+}
+
 sc_status shortconv_bounds_take_first_bad(void *stream, uint64_t *addr) {
 #ifdef SC_BOUNDS_CHECK
     if (addr == nullptr) return SC_EINVAL;

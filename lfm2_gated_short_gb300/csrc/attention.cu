@@ -65,6 +65,9 @@ struct AttnArgs {
     int64_t *cum;      // [N + 1] first own tile of each sequence
     float *own_part;   // [items + CTAs] parts of MR rows: O [MR][Dh], m [MR], l [MR]
     Scales8 s8;        // of an 8-bit cache
+#ifdef SC_BOUNDS_CHECK
+    bool starve;       // no tile is copied: k_own's waits run out
+#endif
 };
 
 // Slots, lengths and tables are read in L2: k_own beside k_prefix starts without a wait of
@@ -746,6 +749,9 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
         };
         auto produce = [&](Seq &s, const OwnItem &it) {
             if (!announce(it)) return false;
+#ifdef SC_BOUNDS_CHECK
+            if (a.starve) return false;
+#endif
             s.ids.begin(s.first + it.t0 * nb, s.c, s.n, it.t0 == 0);
             for (int t = 0; t < it.n; ++t, ++g) {
                 const uint32_t st = g % ST;
@@ -1323,6 +1329,11 @@ static cudaError_t launch_prefix(const PrefixArgs &x, const CUtensorMap &mq, con
                       mq, mk, mv);
 }
 
+#ifdef SC_BOUNDS_CHECK
+static std::atomic<bool> g_starve_next{false};
+void bounds_starve_next_attention() { g_starve_next = true; }
+#endif
+
 cudaError_t launch_prefix_attention(const AttnShape &given, const void *q, int64_t q_stride,
                                     const void *k_pages, const void *v_pages,
                                     const Scales8 *scales, const PageTable &pt,
@@ -1348,6 +1359,9 @@ cudaError_t launch_prefix_attention(const AttnShape &given, const void *q, int64
     const int heads = own_heads(s, q8), MR = own_rows(s, q8);
     x.part = a.own_part + own_part_floats(s, q8);
     if (q8) a.s8 = *scales;
+#ifdef SC_BOUNDS_CHECK
+    a.starve = g_starve_next.exchange(false);
+#endif
     const int own_keys =  // of a tile
         !q8 ? OwnCfg<64, 16, 0>::KT : (s.Dh == 64 ? 128 : 64) / (heads * (MR == 32 ? 2 : 1));
     const int own_box = pt.page_size < own_keys ? pt.page_size : own_keys;

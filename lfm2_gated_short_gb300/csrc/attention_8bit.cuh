@@ -499,13 +499,17 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         const int from = prefix_keys(a, len);
         int key0 = from + item.t0 * C::KT + kw * 16 * C::KH;
         for (int t = 0; t < item.n; ++t, key0 += C::KT) {
+            // A wait that gave up is the last one: no more tiles, since what describes one (its scales'
+            // places are offsets) may be anything, and no rows written.
             if (!dead && !mbar_wait_bounded(&s.full[ring_at], ring_phase)) {
                 raise_error(SC_DEV_TIMEOUT);
-                dead = true;  // no more waits: the rest runs through on what is there
+                dead = bad = true;
             }
-            bad |= s.bad[ring_at] != 0;
-            tile8<C>(s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh,
-                     kw * 2 * C::KH, key0, len, least, r);
+            if (!dead) {
+                bad |= s.bad[ring_at] != 0;
+                tile8<C>(s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh,
+                         kw * 2 * C::KH, key0, len, least, r);
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[ring_at]);
             if (++ring_at == ST) {
@@ -519,7 +523,7 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         auto out_row = [&](int rr) {
             return out + ((int64_t)(rr / a.G) * a.Hkv * a.G + rr % a.G) * DH;
         };
-        // A NaN maximum marks a part with a bad page: k_merge leaves its rows alone.
+        // A NaN maximum marks a part with a bad page or a lost tile: k_merge leaves its rows alone.
         auto put_part = [&](int row, int col, float x) {
             gst(part + (rg * WR + row) * DH + col, x);
         };
@@ -582,7 +586,7 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         if constexpr (KG > 1) {
             // The key groups of a head and row group join: a thread four columns of a row.
             // (The next join comes after the next item's barrier.)
-            named_sync(1, 32 * C::kWarps);
+            bad = named_or(1, 32 * C::kWarps, bad);
             const int w0 = warp - kw;
             for (int x = kw * 32 + lane; x < WR * DH / 4; x += 32 * KG) {
                 const int row = x / (DH / 4), col = x % (DH / 4) * 4, rr = row0 + row;

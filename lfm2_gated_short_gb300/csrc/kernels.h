@@ -214,6 +214,7 @@ cudaError_t bounds_install_proj(const BoundsRegion *r, int n, cudaStream_t strea
 cudaError_t bounds_install_slots(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_pages(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_draft(const BoundsRegion *r, int n, cudaStream_t stream);
+void bounds_starve_next_attention();
 cudaError_t bounds_install_attention(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_cache8(const BoundsRegion *r, int n, cudaStream_t stream);
 cudaError_t bounds_install_rope(const BoundsRegion *r, int n, cudaStream_t stream);
