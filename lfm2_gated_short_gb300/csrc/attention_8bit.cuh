@@ -6,9 +6,12 @@
 // times a power of two that takes its row's largest to 2^14 (11 bits of f16 hold bf16's 8). The
 // scales stay out of the products: with s_t a row's score in units of log2,
 //   out = sum_t 2^(s_t + log2 vs_t - m) v'_t / sum_t 2^(s_t + log2 vs_t - m) / vs_t,
-// so that the weights that meet v' are at most 1 (2^8 with the lazy maximum), whatever the
-// sizes of the blocks' values, and are rounded to f16's 11 bits. m is the running
-// maximum of s_t + log2 vs_t.
+// so that the weights that meet v' lie below the row's largest, whatever the sizes of the
+// blocks' values. m is the running maximum of s_t + log2 vs_t. Weights go to the second product as
+// f16, at most 2^15: rounded by 2^-11 of themselves down to 2^-27 of the row's largest, by 2^-8, as bf16
+// would be, down to 2^-30. Smaller ones lose what is too little to see, 2^-10 of a channel's
+// sum w |v| in all, or, where the keys of much weight hold zeros in a channel, so that such weights are
+// all it has, go into further products scaled up (small_weights8).
 //
 // (The register MMA of e4m3 itself is made of conversions of both operands and further MMAs on this
 // GPU: 56 million warp instructions for 128 sequences of 200-6000 tokens, this takes 33.)
@@ -23,6 +26,14 @@
 #pragma once
 
 namespace sc {
+
+// A row's maximum moves when a score passes it by kRescale8 (in log2), and weighs 2^kTop8: weights
+// are at most 2^15. Those below kLeast, which f16 rounds by more than 2^-8, are looked after in tile8.
+// A maximum that lags by 2^8, as in a bf16 cache, leaves less room below: 128 sequences of 500-1500 tokens
+// by 8 drafts of 8 x 4 heads 69.4 us, by 2^4 68.4, 2^2 68.3; single tokens even.
+constexpr float kRescale8 = 2.0f, kTop8 = 15.0f - kRescale8;
+constexpr float kLeastLog2 = -17.0f, kLeast = 0x1p-17f;
+constexpr float kUnseen8 = 0x1p127f;  // the offset of a row without a key
 
 // The scales of a tile's G groups of 8 keys, K's and V's: the aligned 16 bytes of the
 // scale array that hold each, and which of the four it is.
@@ -207,16 +218,28 @@ struct Rows8 {
     // holds as one chunk.
     uint32_t qf[C::NT][C::kDh / 16][2];
     f32x2 unit[C::NT];  // what a product stands for, times scale log2(e)
-    f32x2 off[C::NT];   // -m, or 0 where no key was seen
+    f32x2 off[C::NT];   // o and l are in units of 2^-off: kTop8 - m, kUnseen8 before any key
     f32x2 l[C::NT];
-    float m[C::NT][2];
-    int see[C::NT][2];  // keys that a row sees
+    int row0;           // of the sequence's rows of a head
+    int sees[2];        // of one row tile, the keys that its rows see
     float o[C::NT][C::kDh / 16][4];  // columns 16 j + g and 16 j + 8 + g, of both rows each
+
+    // Keys that row 8 n + 2 c + p sees: `least` and one a token before its own; below zero for a row
+    // past the item's. Two row tiles are short of registers, and few tiles of keys ask.
+    __device__ __forceinline__ int see(const AttnArgs &a, int least, int n, int p) const {
+        if (C::NT == 1) return sees[p];
+        return find_see(a, least, n, p);
+    }
+    __device__ __forceinline__ int find_see(const AttnArgs &a, int least, int n, int p) const {
+        const int rr = row0 + n * 8 + 2 * (threadIdx.x & 3) + p;
+        return rr < a.D * a.G ? least + rr / a.G : INT_MIN / 2;
+    }
 
     // The rows from row0 on of the `rows` of sequence i under kv head h.
     __device__ __forceinline__ void load(const AttnArgs &a, int i, int h, int row0, int rows) {
         const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
         constexpr int DH = C::kDh;
+        this->row0 = row0;
         uint4 all[C::NT][DH / 32];
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) {
@@ -257,12 +280,17 @@ struct Rows8 {
     }
 };
 
-// o += P V over a warp's keys, of each row only the keys it sees; e[n][2 h + x]: the weights of
-// the key at place g + 8 x of 16, half h.
+// o += P V over a warp's keys, of each row only the keys it sees; z[n][2 h + x]: the weights' logarithms
+// of the key at place g + 8 x of 16, half h.
 template <typename C>
-__device__ __forceinline__ void product_one_by_one8(Rows8<C> &r,
-                                                    const f32x2 (&e)[C::NT][2 * C::KH], uint32_t v,
+__device__ __forceinline__ void product_one_by_one8(const AttnArgs &a, int least, Rows8<C> &r,
+                                                    const f32x2 (&z)[C::NT][2 * C::KH], uint32_t v,
                                                     const Lane8<C> &at, int key0) {
+    int see[C::NT][2];
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n)
+#pragma unroll
+        for (int p = 0; p < 2; ++p) see[n][p] = r.see(a, least, n, p);
 #pragma unroll 1
     for (int k = 0; k < 16 * C::KH; ++k) {
         const int g = (k >> 3 & 1) * 4 + (k & 1) * 2 + (k >> 2 & 1);  // of the lanes that hold key k
@@ -270,13 +298,13 @@ __device__ __forceinline__ void product_one_by_one8(Rows8<C> &r,
         float w[C::NT][2];
 #pragma unroll
         for (int n = 0; n < C::NT; ++n) {
-            f32x2 mine = e[n][0];
+            f32x2 mine = z[n][0];
 #pragma unroll
             for (int i = 1; i < 2 * C::KH; ++i)
-                if (i == x) mine = e[n][i];
+                if (i == x) mine = z[n][i];
             f2_split(mine, w[n][0], w[n][1]);
 #pragma unroll
-            for (int p = 0; p < 2; ++p) w[n][p] = __shfl_sync(~0u, w[n][p], 4 * g + at.c);
+            for (int p = 0; p < 2; ++p) w[n][p] = ex2(__shfl_sync(~0u, w[n][p], 4 * g + at.c));
         }
 #pragma unroll
         for (int j = 0; j < C::kDh / 16; ++j)
@@ -292,16 +320,120 @@ __device__ __forceinline__ void product_one_by_one8(Rows8<C> &r,
                 for (int n = 0; n < C::NT; ++n)
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
-                        if (key0 + k < r.see[n][p])
+                        if (key0 + k < see[n][p])
                             r.o[n][j][2 * h + p] = fmaf(w[n][p], y, r.o[n][j][2 * h + p]);
             }
     }
 }
 
-// One tile's part of a warp: its rows by its keys (from key key0 on).
+// f(j, h, a) for the 16 x 16 blocks of a warp's V: columns 16 j of its 16 keys h, as a product's first
+// operand. They come two at a time: both halves of 16 columns, or 32 columns. `live`: with some, the
+// lane's keys inside the sequence, a byte each (codes past it may be NaN, which a weight of 0 would not
+// silence).
+template <typename C, typename F>
+__device__ __forceinline__ void each_v_block8(uint32_t v_at, bool some, const uint32_t (&live)[C::KH],
+                                              F &&f) {
+    constexpr int KH = C::KH;
+#pragma unroll
+    for (int u = 0; u < KH * C::kDh / 32; ++u) {
+        uint32_t w[4];
+        ldsm2_t8(w, v_at ^ u * (KH == 2 ? 16 : 32));
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int h = KH == 2 ? x : 0, j = KH == 2 ? u : 2 * u + x;
+            uint32_t w0 = w[2 * x], w1 = w[2 * x + 1];
+            if (some) {
+                w0 &= live[h];
+                w1 &= live[h];
+            }
+            const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2_hi(w0),
+                                   e4m3x2_f16x2_hi(w1)};
+            f(j, h, a);
+        }
+    }
+}
+
+// What rounding to f16 took from the weights below kLeast, times V: each pass takes a row's largest rest
+// and those within 2^-28 of it, times a power of two that takes it to 2^14, and the sums back. A row
+// that has none, or none left, gets zeros, so that no row depends on another. Down to 2^-112, 2^-125
+// of the row's largest weight. With two row tiles it is a call, which keeps the registers that it
+// takes out of the tile's usual way.
 template <typename C>
-__device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C> &at, int hh,
-                                      int group0, int key0, int len, int least, Rows8<C> &r) {
+struct Small8 {
+    float o[C::NT][C::kDh / 16][4];
+    f32x2 z[C::NT][2 * C::KH];  // the weights' logarithms, of the key at place g + 8 x of half h: 2 h + x
+    uint32_t live[C::KH];
+};
+template <typename C>
+__device__ __forceinline__ void small_weights8(Small8<C> &r, uint32_t v_at, bool some) {
+    constexpr int KH = C::KH;
+#pragma unroll
+    for (int n = 0; n < C::NT; ++n) {  // one after the other, which takes fewer registers
+        float rest[2 * KH][2];
+#pragma unroll
+        for (int x = 0; x < 2 * KH; ++x) {
+            float e[2];
+            f2_split(r.z[n][x], e[0], e[1]);
+            e[0] = ex2(e[0]);
+            e[1] = ex2(e[1]);
+            const uint32_t two = pack_f16(e[0], e[1]);
+            rest[x][0] = e[0] < kLeast ? e[0] - f16_lo(two) : 0.0f;
+            rest[x][1] = e[1] < kLeast ? e[1] - f16_hi(two) : 0.0f;
+        }
+#pragma unroll 1
+        for (int pass = 0; pass < 4; ++pass) {  // 4 x 28 powers of two
+            float up[2], down[2];
+            bool any = false;
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                float t = 0.0f;
+#pragma unroll
+                for (int x = 0; x < 2 * KH; ++x) t = fmaxf(t, fabsf(rest[x][p]));
+#pragma unroll
+                for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, x));
+                const uint32_t e = __float_as_uint(t) & 0x7F800000u;  // of 2^-112 .. 2^-17
+                const bool has = t >= 0x1p-112f;
+                any |= has;
+                up[p] = has ? __uint_as_float((254u + 14u << 23) - e) : 0.0f;
+                down[p] = has ? __uint_as_float(e - (14u << 23)) : 0.0f;
+            }
+            if (!__any_sync(~0u, any)) break;
+            uint32_t pf[2 * KH];
+#pragma unroll
+            for (int x = 0; x < 2 * KH; ++x) {
+                float e[2];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const float w = rest[x][p] * up[p];
+                    const bool take = fabsf(w) >= 0x1p-14f;
+                    e[p] = take ? w : 0.0f;
+                    if (take) rest[x][p] = 0.0f;
+                }
+                pf[x] = transposed(pack_f16(e[0], e[1]));
+            }
+            float d[4];
+            each_v_block8<C>(v_at, some, r.live, [&](int j, int h, const uint32_t(&a)[4]) {
+                if (h == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
+                mma16816_f16(d, a, pf[2 * h], pf[2 * h + 1]);
+                if (h < KH - 1) return;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r.o[n][j][e] = fmaf(d[e], down[e & 1], r.o[n][j][e]);
+            });
+        }
+    }
+}
+
+template <typename C>
+__device__ __noinline__ void small_weights8_call(Small8<C> &r, uint32_t v_at, bool some) {
+    small_weights8<C>(r, v_at, some);
+}
+
+// One tile's part of a warp: its rows by its keys (from key key0 on), behind the `walked` that it has
+// seen of the item.
+template <typename C>
+__device__ __forceinline__ void tile8(const AttnArgs &args, uint32_t k, uint32_t scales,
+                                      const Lane8<C> &at, int hh, int group0, int key0, int len,
+                                      int least, int walked, Rows8<C> &r) {
     constexpr int DH = C::kDh, NT = C::NT, KH = C::KH, kKeys = 16 * KH, kG = C::KT / 8;
     const int lane = threadIdx.x & 31;
     const uint32_t v = k + C::kV;
@@ -353,41 +485,59 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const f32x2 unit = f2_mul(r.unit[n], f2_make(kb, kb));
+            float y[2][2];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
+                s[n][2 * h + x] = f2_fma(s[n][2 * h + x], unit, f2_make(add, add));
+                f2_split(s[n][2 * h + x], y[x][0], y[x][1]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) top[n][p] = max3(top[n][p], y[0][p], y[1][p]);
+        }
+    }
+    if (some) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int see[2] = {r.see(args, least, n, 0), r.see(args, least, n, 1)};
+            top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+            for (int x = 0; x < 2 * KH; ++x) {
                 float y[2];
-                f2_split(f2_fma(s[n][2 * h + x], unit, f2_make(add, add)), y[0], y[1]);
+                f2_split(s[n][x], y[0], y[1]);
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    if (some && key0 + 16 * h + at.key + 2 * x >= r.see[n][p]) y[p] = -INFINITY;
+                    if (key0 + 16 * (x >> 1) + at.key + 2 * (x & 1) >= see[p]) y[p] = -INFINITY;
                     top[n][p] = fmaxf(top[n][p], y[p]);
                 }
-                s[n][2 * h + x] = f2_make(y[0], y[1]);
+                s[n][x] = f2_make(y[0], y[1]);
             }
         }
     }
-    // Only when some score passes its row's maximum by 2^8 are the row maxima needed. A row that
-    // has seen no key yet keeps m = -inf and sums of zero.
+    // Only when some score passes its row's maximum by kRescale8 are the row maxima needed. A row that
+    // has seen no key yet keeps its offset and sums of zero.
     bool rise = false;
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+    for (int n = 0; n < NT; ++n) {
+        float off[2];
+        f2_split(r.off[n], off[0], off[1]);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) rise |= top[n][p] > r.m[n][p] + kRescaleLog2;
+        for (int p = 0; p < 2; ++p) rise |= top[n][p] + off[p] > kTop8 + kRescale8;
+    }
     if (__any_sync(~0u, rise)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float f[2];
+            float f[2], off[2];
+            f2_split(r.off[n], off[0], off[1]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 float t = top[n][p];
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, x));
-                const bool up = t > r.m[n][p] + kRescaleLog2;
-                f[p] = up ? ex2(r.m[n][p] - t) : 1.0f;
-                if (up) r.m[n][p] = t;
+                const float was = off[p];
+                if (t + was > kTop8 + kRescale8) off[p] = kTop8 - t;
+                f[p] = ex2(off[p] - was);
             }
-            r.off[n] = f2_make(r.m[n][0] == -INFINITY ? 0.0f : -r.m[n][0],
-                               r.m[n][1] == -INFINITY ? 0.0f : -r.m[n][1]);
+            r.off[n] = f2_make(off[0], off[1]);
             r.l[n] = f2_mul(r.l[n], f2_make(f[0], f[1]));
 #pragma unroll
             for (int j = 0; j < DH / 16; ++j)
@@ -396,18 +546,34 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
         }
     }
     uint32_t pf[NT][2 * KH];  // the weights as the second product's second operand
+    float low = INFINITY;     // the least weight's logarithm
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 2 * KH; ++x) {
+            s[n][x] = f2_add(s[n][x], r.off[n]);
             float e0, e1;
-            f2_split(f2_add(s[n][x], r.off[n]), e0, e1);
+            f2_split(s[n][x], e0, e1);
+            low = min3(low, e0, e1);
             e0 = ex2(e0);
             e1 = ex2(e1);
-            s[n][x] = f2_make(e0, e1);
-            r.l[n] = f2_fma(s[n][x], f2_make(inverse[x >> 1], inverse[x >> 1]), r.l[n]);
-            pf[n][x] = transposed(pack_f16(e0, e1));  // 2^-11 relative at most
+            r.l[n] = f2_fma(f2_make(e0, e1), f2_make(inverse[x >> 1], inverse[x >> 1]), r.l[n]);
+            pf[n][x] = transposed(pack_f16(e0, e1));
         }
+    if (some) {  // of those that there are
+        low = INFINITY;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 2 * KH; ++x) {
+                float z[2];
+                f2_split(s[n][x], z[0], z[1]);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    if (z[p] > -INFINITY) low = fminf(low, z[p]);
+            }
+    }
+    const bool small = __any_sync(~0u, low < kLeastLog2);  // some weight is
     uint32_t live[KH] = {};  // the lane's keys inside the sequence, a byte each
     if (some) {
         // A draft that some row does not see: were its V NaN, a weight of 0 would not keep it
@@ -421,10 +587,9 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
                 nan |= (((word_of(w, e) & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0;
         }
         if (__any_sync(~0u, nan)) {
-            product_one_by_one8<C>(r, s, v, at, key0);
+            product_one_by_one8<C>(args, least, r, s, v, at, key0);
             return;
         }
-        // Codes past the sequence may be NaN, which a weight of 0 would not silence.
 #pragma unroll
         for (int h = 0; h < KH; ++h) {
 #pragma unroll
@@ -433,25 +598,62 @@ __device__ __forceinline__ void tile8(uint32_t k, uint32_t scales, const Lane8<C
                     live[h] |= 0xFFu << 8 * i;
         }
     }
-    // The 16 x 16 blocks of V, two at a time: both halves of 16 columns, or 32 columns.
+    each_v_block8<C>(v + at.v_at, some, live, [&](int j, int h, const uint32_t(&a)[4]) {
 #pragma unroll
-    for (int u = 0; u < KH * DH / 32; ++u) {
-        uint32_t w[4];
-        ldsm2_t8(w, v + (at.v_at ^ u * (KH == 2 ? 16 : 32)));
+        for (int n = 0; n < NT; ++n) mma16816_f16(r.o[n][j], a, pf[n][2 * h], pf[n][2 * h + 1]);
+    });
+    if (!small) return;
+    // f16 takes 2^-25 of a small weight at most, and a code is 448 at most: a row in which every sum is
+    // past that of all keys so far times 2^10 loses, in all, 2^-10 of sum w |v| at most, channel by
+    // channel. The others take what was lost.
+    const float enough = (float)(walked + kKeys) * 0x1p-6f;
+    float least_o[NT][2], least_all = INFINITY;
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const int h = KH == 2 ? x : 0, j = KH == 2 ? u : 2 * u + x;
-            uint32_t w0 = w[2 * x], w1 = w[2 * x + 1];
-            if (some) {
-                w0 &= live[h];
-                w1 &= live[h];
-            }
-            const uint32_t a[4] = {e4m3x2_f16x2(w0), e4m3x2_f16x2(w1), e4m3x2_f16x2_hi(w0),
-                                   e4m3x2_f16x2_hi(w1)};
+    for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                mma16816_f16(r.o[n][j], a, pf[n][2 * h], pf[n][2 * h + 1]);
+        for (int p = 0; p < 2; ++p) {
+            least_o[n][p] = INFINITY;
+#pragma unroll
+            for (int j = 0; j < DH / 16; ++j)
+                least_o[n][p] = min3(least_o[n][p], fabsf(r.o[n][j][p]), fabsf(r.o[n][j][2 + p]));
         }
+        least_all = min3(least_all, least_o[n][0], least_o[n][1]);
+    }
+    if (__any_sync(~0u, least_all < enough)) {
+        Small8<C> x;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            bool take[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {  // some lane's, of the row's
+                float t = least_o[n][p];
+#pragma unroll
+                for (int y = 4; y < 32; y <<= 1) t = fminf(t, __shfl_xor_sync(~0u, t, y));
+                take[p] = t < enough;
+            }
+#pragma unroll
+            for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x.o[n][j][e] = r.o[n][j][e];
+#pragma unroll
+            for (int e = 0; e < 2 * KH; ++e) {
+                float z[2];
+                f2_split(s[n][e], z[0], z[1]);
+                x.z[n][e] = f2_make(take[0] ? z[0] : 0.0f, take[1] ? z[1] : 0.0f);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < KH; ++h) x.live[h] = live[h];
+        if constexpr (NT > 1)
+            small_weights8_call<C>(x, v + at.v_at, some);
+        else
+            small_weights8<C>(x, v + at.v_at, some);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < DH / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r.o[n][j][e] = x.o[n][j][e];
     }
 }
 
@@ -481,15 +683,13 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.qempty[qb]);
         r.load(a, item.i, item.h + hh, row0, rows);
+        if (NT == 1)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) r.sees[p] = r.find_see(a, least, 0, p);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const int rr = row0 + n * 8 + 2 * at.c + p;
-                r.see[n][p] = rr < rows ? least + rr / a.G : INT_MIN / 2;
-                r.m[n][p] = -INFINITY;
-            }
-            r.l[n] = r.off[n] = f2_make(0.0f, 0.0f);
+            r.l[n] = f2_make(0.0f, 0.0f);
+            r.off[n] = f2_make(kUnseen8, kUnseen8);
 #pragma unroll
             for (int j = 0; j < DH / 16; ++j)
 #pragma unroll
@@ -507,8 +707,8 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
             }
             if (!dead) {
                 bad |= s.bad[ring_at] != 0;
-                tile8<C>(s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh,
-                         kw * 2 * C::KH, key0, len, least, r);
+                tile8<C>(a, s.ring_a + ring_at * C::kStage, smem_addr(&s.scales[ring_at]), at, hh,
+                         kw * 2 * C::KH, key0, len, least, t * 16 * C::KH, r);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s.empty[ring_at]);
@@ -535,13 +735,15 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
         [[maybe_unused]] float *jm = s.join + C::kWarps * WR * C::kOs;  // [warp][m, l]
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float l[2], inv[2];
+            float l[2], m[2], inv[2];
             f2_split(r.l[n], l[0], l[1]);
+            f2_split(r.off[n], m[0], m[1]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
 #pragma unroll
                 for (int x = 4; x < 32; x <<= 1) l[p] += __shfl_xor_sync(~0u, l[p], x);
                 inv[p] = inverse_of(l[p]);
+                m[p] = m[p] == kUnseen8 ? -INFINITY : -m[p];
             }
             const int row = n * 8 + 2 * at.c;  // and the next
             if (KG > 1 || !whole) {
@@ -561,10 +763,10 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
                         }
                     if (at.g != 0) continue;
                     if constexpr (KG > 1) {
-                        jm[warp * 2 * WR + row + p] = r.m[n][p];
+                        jm[warp * 2 * WR + row + p] = m[p];
                         jm[(warp * 2 + 1) * WR + row + p] = l[p];
                     } else {
-                        put_sums(row + p, r.m[n][p], l[p]);
+                        put_sums(row + p, m[p], l[p]);
                     }
                 }
             } else {
