@@ -220,6 +220,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// sum + x 2^e, with f = ex2(e), which may be below fp32's numbers: over an 8-bit cache a part's sum is in
+// units of its largest weight times V scale, of 2^-64 to 2^120.
+__device__ __forceinline__ float add_times_2_to(float sum, float x, float e, float f) {
+    if (e >= -126.0f) return fmaf(f, x, sum);
+    const float half = ex2(0.5f * e);
+    return fmaf(x * half, half, sum);
+}
+
 // Whether some of eight bf16 values is an infinity or NaN.
 __device__ __forceinline__ bool not_finite(const uint4 &v) {
     bool bad = false;
@@ -983,10 +991,10 @@ __global__ void __launch_bounds__(kMergeThreads)
         bad |= nan != 0;
         const float base = now == -INFINITY ? 0.0f : now;
         const float f = ex2(m - base), f0 = ex2(top - base);
-        float s = l * f;
+        float s = add_times_2_to(0.0f, l, m - base, f);
 #pragma unroll
         for (int k = L / 2; k; k >>= 1) s += __shfl_xor_sync(~0u, s, k);
-        sum = sum * f0 + s;
+        sum = add_times_2_to(s, sum, top - base, f0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] *= f0;
         top = now;
@@ -1068,13 +1076,13 @@ __global__ void __launch_bounds__(kMergeThreads)
             now = fmaxf(now, m[k]);
         }
         const float base = now == -INFINITY ? 0.0f : now, f0 = ex2(top - base);
-        sum *= f0;
+        sum = add_times_2_to(0.0f, sum, top - base, f0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) o[e] *= f0;
 #pragma unroll
         for (int k = 0; k < kAhead; ++k) {
             const float f = ex2(m[k] - base);
-            sum = fmaf(f, l[k], sum);
+            sum = add_times_2_to(sum, l[k], m[k] - base, f);
             o[0] = fmaf(f, v[k][0].x, o[0]);
             o[1] = fmaf(f, v[k][0].y, o[1]);
             o[2] = fmaf(f, v[k][0].z, o[2]);
@@ -1091,7 +1099,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
     for (int k = C; k < 32; k <<= 1) all = fmaxf(all, __shfl_xor_sync(~0u, all, k));
     const float f = all == -INFINITY ? 0.0f : ex2(top - all);
-    sum *= f;
+    sum = all == -INFINITY ? 0.0f : add_times_2_to(0.0f, sum, top - all, f);
 #pragma unroll
     for (int e = 0; e < 8; ++e) o[e] *= f;
 #pragma unroll
@@ -1127,7 +1135,7 @@ __global__ void __launch_bounds__(kMergeThreads)
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         const float g = ex2(s_m[w] - base);
-        sum = fmaf(g, s_l[w], sum);
+        sum = add_times_2_to(sum, s_l[w], s_m[w] - base, g);
         x0 = fmaf(g, s_o[w][col], x0);
         x1 = fmaf(g, s_o[w][col + 1], x1);
     }

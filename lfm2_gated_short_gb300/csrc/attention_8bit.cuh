@@ -526,7 +526,7 @@ __device__ __forceinline__ void tile8(const AttnArgs &args, uint32_t k, uint32_t
     if (__any_sync(~0u, rise)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float f[2], off[2];
+            float f[2], h[2], off[2];
             f2_split(r.off[n], off[0], off[1]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
@@ -536,9 +536,10 @@ __device__ __forceinline__ void tile8(const AttnArgs &args, uint32_t k, uint32_t
                 const float was = off[p];
                 if (t + was > kTop8 + kRescale8) off[p] = kTop8 - t;
                 f[p] = ex2(off[p] - was);
+                h[p] = ex2(0.5f * (off[p] - was));  // f may be below fp32's numbers where l counts
             }
             r.off[n] = f2_make(off[0], off[1]);
-            r.l[n] = f2_mul(r.l[n], f2_make(f[0], f[1]));
+            r.l[n] = f2_mul(f2_mul(r.l[n], f2_make(h[0], h[1])), f2_make(h[0], h[1]));
 #pragma unroll
             for (int j = 0; j < DH / 16; ++j)
 #pragma unroll
@@ -574,6 +575,25 @@ __device__ __forceinline__ void tile8(const AttnArgs &args, uint32_t k, uint32_t
             }
     }
     const bool small = __any_sync(~0u, low < kLeastLog2);  // some weight is
+    if (small && __any_sync(~0u, low < -126.0f)) {
+        // A weight that 32 bits do not hold, beside a V scale so much larger, counts in the sum all the
+        // same: 2^z / vs.
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float l[2];
+            f2_split(r.l[n], l[0], l[1]);
+#pragma unroll
+            for (int x = 0; x < 2 * KH; ++x) {
+                const float over_vs = (float)((int)(__float_as_uint(inverse[x >> 1]) >> 23) - 127);
+                float z[2];
+                f2_split(s[n][x], z[0], z[1]);
+#pragma unroll
+                for (int p = 0; p < 2; ++p)
+                    if (ex2(z[p]) == 0.0f) l[p] = fmaf(ex2(z[p] + over_vs + 32.0f), 0x1p-32f, l[p]);
+            }
+            r.l[n] = f2_make(l[0], l[1]);
+        }
+    }
     uint32_t live[KH] = {};  // the lane's keys inside the sequence, a byte each
     if (some) {
         // A draft that some row does not see: were its V NaN, a weight of 0 would not keep it
@@ -799,10 +819,10 @@ __device__ __forceinline__ void consume8(const AttnArgs &a, int rows, const OwnS
                 float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int q = 0; q < KG; ++q) {
-                    const float f = ex2(jm[(w0 + q) * 2 * WR + row] - off);
+                    const float m = jm[(w0 + q) * 2 * WR + row] - off, f = ex2(m);
                     const float4 u = *reinterpret_cast<float4 *>(
                         s.join + ((w0 + q) * WR + row) * C::kOs + col);
-                    sum = fmaf(f, jm[((w0 + q) * 2 + 1) * WR + row], sum);
+                    sum = add_times_2_to(sum, jm[((w0 + q) * 2 + 1) * WR + row], m, f);
                     v.x = fmaf(f, u.x, v.x);
                     v.y = fmaf(f, u.y, v.y);
                     v.z = fmaf(f, u.z, v.z);
