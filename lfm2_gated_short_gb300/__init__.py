@@ -789,16 +789,19 @@ def rope_frequencies(R, base=10000.0, scaling=None, factor=1.0, original_length=
     ``base ** (-2i / R)``, and for contexts ``factor`` times as long as trained:
 
     ``scaling`` None: as it is; ``"linear"``: all of them divided by ``factor``; ``"base"``: the
-    base raised so that the slowest pair alone is divided by ``factor``; ``"parts"``: pairs that turn
+    base raised, which slows every pair but the first, the slowest by ``factor`` (``R`` 4 or more: of one
+    pair it slows none); ``"parts"``: pairs that turn
     fewer than ``low`` times in ``original_length`` positions divided by ``factor``, those that turn more
     than ``high`` times kept, a ramp between, and amplitude ``0.1 ln(factor) + 1``."""
     if R < 2 or R % 2:
         raise ValueError(f"R must be even and positive, got {R}")
     if not (base > 0 and factor > 0 and original_length > 0 and high > low):
         raise ValueError("base, factor and original_length must be positive, high above low")
-    if scaling == "base" and R > 2:
+    if scaling == "base":
+        if R == 2:
+            raise ValueError("scaling 'base' needs R of 4 or more: the first pair keeps its frequency")
         base = base * factor ** (R / (R - 2))
-    elif scaling not in (None, "linear", "base", "parts"):
+    elif scaling not in (None, "linear", "parts"):
         raise ValueError(f"scaling must be None, 'linear', 'base' or 'parts', got {scaling!r}")
     f = torch.arange(0, R, 2, dtype=torch.float64)
     f = torch.exp(f * (-math.log(base) / R))

@@ -83,3 +83,17 @@ def test_frequencies():
                dict(R=8, base=-1.0)):
         with pytest.raises(ValueError):
             sc.rope_frequencies(device="cpu", **kw)
+
+
+def test_a_raised_base_slows_every_pair_but_the_first():
+    for R in (4, 6, 64):
+        f, _ = sc.rope_frequencies(R, base=1e4, device="cpu")
+        raised, a = sc.rope_frequencies(R, base=1e4, scaling="base", factor=4.0, device="cpu")
+        ratio = (f / raised).numpy()
+        assert a == 1.0 and ratio[0] == 1.0 and np.isclose(ratio[-1], 4.0, rtol=1e-12)
+        assert (np.diff(ratio) > 0).all()
+    for factor in (1.0, 4.0):  # the first pair is the only one
+        with pytest.raises(ValueError):
+            sc.rope_frequencies(2, scaling="base", factor=factor, device="cpu")
+    for scaling in (None, "linear", "parts"):
+        assert sc.rope_frequencies(2, scaling=scaling, factor=4.0, device="cpu")[0].shape == (1,)
