@@ -14,6 +14,7 @@
 #include "kernels.h"
 #include "launch.h"
 #include "shortconv.h"
+#include "work_split.h"
 
 namespace sc {
 
@@ -391,11 +392,11 @@ template <typename T>
 static cudaError_t read8(const PageTable &pt, const int32_t *slots, const int32_t *cu,
                          const int32_t *starts, int N, int rows, const Cache8 &c, void *k, void *v,
                          int sm_count, cudaStream_t stream) {
-    // A warp's rows: up to 128 words at once, four a lane.
+    // A warp's rows: up to 64 words of each pool at once, two a lane.
     const int per = c.Hkv * c.Dh / Codes<T>::kN, of_head = c.Dh / Codes<T>::kN;
     const int R = per >= 64 ? 1 : 64 / per < 32 ? 64 / per : 32;
     const uint32_t magic = (uint32_t)((1ull << 32) / of_head) + 1;  // words below 2^22, Dh <= 1024
-    const int64_t warps = (rows + R - 1) / R, blocks = (warps * 32 + kReadThreads - 1) / kReadThreads;
+    const int64_t blocks = row_groups(row_groups(rows, R), kReadThreads / 32);
     const int64_t most = 4ll * sm_count;
     return launch_pdl(k_read8<T>, dim3((unsigned)(blocks < 1 ? 1 : blocks < most ? blocks : most)),
                       dim3(kReadThreads), 0, stream, pt, slots, cu, starts, N, rows, R, magic, c,

@@ -27,4 +27,7 @@ SC_HOST_DEVICE int share_of(int64_t u, int64_t U, int64_t n) {
     return (int)(x / U);
 }
 
+// Groups of R rows that hold `rows` of them; rows + R may pass 2^31.
+SC_HOST_DEVICE int64_t row_groups(int64_t rows, int64_t R) { return (rows + R - 1) / R; }
+
 }  // namespace sc
