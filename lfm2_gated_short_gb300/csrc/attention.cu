@@ -326,8 +326,7 @@ namespace sc {
 
 // A consumer warp's part over a bf16 cache.
 template <typename C>
-__device__ __forceinline__ void consume16(const AttnArgs &a, int rows, int per,
-                                          const OwnSmem<C> &s) {
+__device__ __forceinline__ void consume16(const AttnArgs &a, int rows, const OwnSmem<C> &s) {
     constexpr int DH = C::kDh, ST = C::kStages, KG = C::KG, KB = C::KB, kKT = C::KT, QB = C::kQBufs;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint32_t ring_at = 0, ring_phase = 0;
@@ -850,7 +849,7 @@ __global__ void __launch_bounds__(OwnCfg<DH, MR, HG>::kThreads, OwnCfg<DH, MR, H
     if constexpr (HG > 0)
         consume8<C>(a, rows, s);
     else
-        consume16<C>(a, rows, per, s);
+        consume16<C>(a, rows, s);
     leave();
 }
 
