@@ -580,7 +580,9 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
  *
  * shortconv_prefix_attention_8bit: shortconv_prefix_attention over such a pool: q and out
  * bf16, keys and values code times scale. A call with many shared pages unpacks them once, to
- * bf16 in the workspace; one with few reads them with each sequence's own.
+ * bf16 in the workspace; one with few reads them with each sequence's own. A weight times its
+ * block's V scale counts down to 2^-124 of its row's largest, in the sum whatever it is. A tile
+ * whose waits ran out (SC_DEV_TIMEOUT) leaves its rows unwritten.
  */
 sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block, const void *k,
                                       int64_t k_stride, const void *v, int64_t v_stride, int N,
@@ -631,8 +633,8 @@ sc_status shortconv_prefix_attention_8bit(int Hq, int Hkv, int Dh, int block, co
  *   a' = amplitude (a cos t - b sin t),  b' = amplitude (b cos t + a sin t);
  * the other Dh - R values are copied. With inverse set, the turn is by -t: what takes the
  * gradients of the outputs to those of the inputs (the same arguments, q and k the
- * incoming gradients). Angles are exact for every position (an integer number of 2^-64
- * turns), sums in fp32, each value rounded once.
+ * incoming gradients). A frequency is held as a fraction of a turn within 2^-64 of one or 2^-61 of
+ * itself; its product with any position is exact. Sums are in fp32, each value rounded once.
  *
  *   dtype       of q, k and the outputs, SC_F32 or SC_BF16
  *   R           even, at most 512

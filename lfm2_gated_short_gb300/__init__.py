@@ -661,7 +661,9 @@ def pages_append(k, v, k_pages, v_pages, table, lens, slot_ids, D, stream=None, 
                  v_scales=None):
     """Write each listed sequence's ``D`` newest tokens, already counted in ``lens``:
     ``k``, ``v`` ``[N*D, Hkv, Dh]`` (rows may be strided) into one layer's pools. Into 8-bit
-    pools they are quantised, block by block of the scales (``page_cache_8bit``)."""
+    pools they are quantised, block by block of the scales (``page_cache_8bit``): a new token of larger
+    values than its block's earlier ones moves their codes to a larger scale, which a rollback of that
+    token does not undo."""
     N = slot_ids.shape[0]
     pool = k_pages.shape
     n_pages, ps, Hkv, Dh = pool
@@ -789,10 +791,10 @@ def rope_frequencies(R, base=10000.0, scaling=None, factor=1.0, original_length=
     ``base ** (-2i / R)``, and for contexts ``factor`` times as long as trained:
 
     ``scaling`` None: as it is; ``"linear"``: all of them divided by ``factor``; ``"base"``: the
-    base raised, which slows every pair but the first, the slowest by ``factor`` (``R`` 4 or more: of one
-    pair it slows none); ``"parts"``: pairs that turn
-    fewer than ``low`` times in ``original_length`` positions divided by ``factor``, those that turn more
-    than ``high`` times kept, a ramp between, and amplitude ``0.1 ln(factor) + 1``."""
+    base raised, which slows every pair but the first, the slowest by ``factor`` (``R`` 4 or more);
+    ``"parts"``: pairs that turn fewer than ``low`` times in ``original_length`` positions divided by
+    ``factor``, those that turn more than ``high`` times kept, a ramp between, and amplitude
+    ``0.1 ln(factor) + 1``."""
     if R < 2 or R % 2:
         raise ValueError(f"R must be even and positive, got {R}")
     if not (base > 0 and factor > 0 and original_length > 0 and high > low):
@@ -892,7 +894,8 @@ def rope(q, k, freqs, positions=None, lens=None, slot_ids=None, D=1, layout="hal
     None) with the first ``2 * len(freqs)`` values of each head turned in pairs, (i, i + R/2) or
     (2i, 2i + 1) ("interleaved"). ``freqs`` and ``amplitude`` as ``rope_frequencies`` gives them.
     ``positions`` int32 ``[T]``; or the ``D`` newest tokens of the cache's ``slot_ids`` at ``lens``.
-    ``q_out``, ``k_out`` may be ``q``, ``k`` themselves. Returns ``(q_out, k_out)``."""
+    ``q_out``, ``k_out`` may be ``q``, ``k`` themselves. Returns ``(q_out, k_out)``, without autograd
+    history: ``rope_backward`` gives the gradients."""
     return _rope("shortconv_rope", 0, q, k, freqs, positions, lens, slot_ids, D, layout, amplitude,
                  q_out, k_out, stream)
 

@@ -20,8 +20,8 @@
 // 3.1 TB/s; DRAM gives 245 MB for them and is busy 59 % of the time, issue slots 23 %.
 // With D G > 32 the rows go in tiles of 32, and each walks all of the sequence's key tiles.
 // Over an 8-bit cache an item is 8, 16 or 32 rows of up to four kv heads (attention_8bit.cuh): the long
-// pair (72 MB) 21.7 us with its join, 128 sequences of 200-6000 tokens by 8 x 4 heads (404 MB) 71 us, 5.7
-// TB/s, 84 % of the copy rate.
+// pair (72 MB) 22.2 us with its join, 128 sequences of 200-6000 tokens by 8 x 4 heads (404 MB) 72 us, 5.6
+// TB/s, 83 % of the copy rate.
 //
 // k_merge joins the parts that CTAs left in the workspace, in a fixed order: 4
 // to 6 us of dependent reads with few rows, 17 us for the 32768 rows of 128 x 8 x 32.
@@ -1206,15 +1206,15 @@ static cudaError_t map_queries(CUtensorMap *m, const PrefixArgs &x, const AttnSh
 
 // Rows of an item: 16 hold up to 16 rows of a sequence and kv head (over an 8-bit cache 8 hold
 // 8), else 32. Up to 8 rows over an 8-bit cache, us with items of 8, 16 and 32: 128 sequences of 200-6000
-// tokens by 8 x 4 heads of 64 79.6, 87.1, 154; 512 of 20-60 29.8, 34.2, 47.2; 4 of 20-400 7.8, 8.7,
-// 9.1; 128 of 500-1500 by heads of 128 55, 69, 109.
+// tokens by 8 x 4 heads of 64 81.3, 89.5, 157; 512 of 20-60 30.8, 35.1, 49.0; 4 of 20-400 8.1, 8.9,
+// 9.0; 128 of 500-1500 by heads of 128 55, 69, 110.
 static int own_rows(const AttnShape &s, bool q8) {
     const int rows = s.D * (s.Hq / s.Hkv);
     return q8 && rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
 }
 // kv heads of an item over an 8-bit cache: a token's codes of one head are 64 or 128 bytes,
-// which DRAM gives best together with its neighbours'. The same calls with 4, 2 and 1: 79.6, 83.4, 97.6;
-// 29.8, 31.4, 40.9; 7.8, 7.7, 7.9; 55.2, 57.3, 59.4. (32 rows take two warps a head, so two heads.)
+// which DRAM gives best together with its neighbours'. The same calls with 4, 2 and 1: 81.3, 83.7, 95.8;
+// 30.8, 32.7, 42.7; 8.1, 8.1, 8.2; 55.5, 58.0, 60.5. (32 rows take two warps a head, so two heads.)
 static int own_heads(const AttnShape &s, bool q8) {
     if (!q8) return 1;
     return s.Hkv % 4 == 0 && own_rows(s, true) < 32 ? 4 : s.Hkv % 2 == 0 ? 2 : 1;

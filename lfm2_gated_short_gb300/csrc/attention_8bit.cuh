@@ -17,10 +17,10 @@
 // GPU: 56 million warp instructions for 128 sequences of 200-6000 tokens, this takes 33.)
 //
 // What bounds it: the codes' bytes with up to 8 rows (128 sequences of 200-6000 tokens by 8 x 4
-// heads: 404 MB from DRAM, the same that are needed, in 71 us; issue slots 43 %); with 16 and 32
-// rows the conversions and the softmax in the issue slots (128 of 500-1500 tokens: 34 us a call
-// with 4 rows, 41 with 16, 65 with 32, whose k_own issues in half of its cycles, waiting for its
-// own results). Not better: four row tiles a warp instead of two row groups (k_own 46 to 80 us,
+// heads: 404 MB from DRAM, the same that are needed, in 72 us; issue slots 42 %; 128 of 500-1500 by heads
+// of 128: 259 MB in 50 us, 5.2 TB/s); with 16 and 32 rows the
+// conversions and the softmax in the issue slots (128 of 500-1500 tokens: 34 us a call with 4 rows, 41
+// with 16, 67 with 32, whose k_own issues in half of its cycles, waiting for its own results). Not better: four row tiles a warp instead of two row groups (k_own 46 to 80 us,
 // spills); eight-row groups with heads of 128 (74 to 84); 256-byte L2 promotion with an item a head
 // (920 MB read for 404).
 #pragma once
@@ -28,9 +28,9 @@
 namespace sc {
 
 // A row's maximum moves when a score passes it by kRescale8 (in log2), and weighs 2^kTop8: weights
-// are at most 2^15. Those below kLeast, which f16 rounds by more than 2^-8, are looked after in tile8.
-// A maximum that lags by 2^8, as in a bf16 cache, leaves less room below: 128 sequences of 500-1500 tokens
-// by 8 drafts of 8 x 4 heads 69.4 us, by 2^4 68.4, 2^2 68.3; single tokens even.
+// are at most 2^15. Those below kLeast, which f16 rounds by more than 2^-8, are looked after in tile8: the
+// less a maximum lags, the fewer they are. 128 sequences of 500-1500 tokens by 8 drafts of 8 x 4 heads, us
+// with a lag of 2^8, 2^4 and 2^2: 67.8, 66.7, 67.2; with queries three times as large 101, 79, 76.
 constexpr float kRescale8 = 2.0f, kTop8 = 15.0f - kRescale8;
 constexpr float kLeastLog2 = -17.0f, kLeast = 0x1p-17f;
 constexpr float kUnseen8 = 0x1p127f;  // the offset of a row without a key
@@ -148,7 +148,7 @@ struct Own8Cfg {
     static constexpr uint32_t kV = NC * kBlk;                 // the tile's V behind its K
     static constexpr uint32_t kStage = 2 * kV;                // 16 KB, with 32 rows 8
     // By registers: 128 a thread, or 168. Heads of 64, us with 2, 3 and 4: 128 sequences of 200-6000
-    // tokens 97, 79, 80; 8 drafts of 128 of 500-1500 67, 65, 94; 512 of 20-60 28.8, 29.9, 33.2.
+    // tokens 99, 81, 92; 8 drafts of 128 of 500-1500 72, 67, 106; 512 of 20-60 29.2, 30.8, 33.1.
     static constexpr int kCtas = DH == 64 || MR == 8 ? 3 : 2;
     static constexpr int kQBufs = 2;                          // items described ahead
     static constexpr uint32_t kQ = 0;                         // the consumers read their queries
@@ -356,8 +356,10 @@ __device__ __forceinline__ void each_v_block8(uint32_t v_at, bool some, const ui
 // What rounding to f16 took from the weights below kLeast, times V: each pass takes a row's largest rest
 // and those within 2^-28 of it, times a power of two that takes it to 2^14, and the sums back. A row
 // that has none, or none left, gets zeros, so that no row depends on another. Down to 2^-112, 2^-125
-// of the row's largest weight. With two row tiles it is a call, which keeps the registers that it
-// takes out of the tile's usual way.
+// of the row's largest weight. With two row tiles of 128 it is a call, which keeps the registers that it
+// takes out of the tile's usual way: 72 sequences of 5 drafts by 2 x 7 heads 28.1 us, 29.7 without. Of 64
+// it is not: 128 of 500-1500 tokens by 8 drafts 67 both, and 72.3 us for 75.5 where it has work (queries
+// three times as large).
 template <typename C>
 struct Small8 {
     float o[C::NT][C::kDh / 16][4];
@@ -664,7 +666,7 @@ __device__ __forceinline__ void tile8(const AttnArgs &args, uint32_t k, uint32_t
         }
 #pragma unroll
         for (int h = 0; h < KH; ++h) x.live[h] = live[h];
-        if constexpr (NT > 1)
+        if constexpr (NT > 1 && DH == 128)
             small_weights8_call<C>(x, v + at.v_at, some);
         else
             small_weights8<C>(x, v + at.v_at, some);

@@ -4,8 +4,8 @@
 // A scale is a power of two in fp32; its exponent alone is read, held to 2^-64 .. 2^120, so that
 // scales, their inverses and sums of weights times either stay finite whatever the bits
 // are. Powers of two: code times scale is exact in bf16 and fp32, a scale that rises moves
-// only the exponents of earlier codes (no bit is lost but below 2^-15 of the block's largest),
-// and a quotient by it needs no division. A scale of 32 bits a block costs 0.4 % of 16 x 64 codes.
+// only the exponents of earlier codes (no bit is lost but below 2^-14 of the largest value that the
+// new scale can hold), and a quotient by it needs no division. A scale of 32 bits a block costs 0.4 % of 16 x 64 codes.
 #pragma once
 
 #include <stdint.h>

@@ -81,6 +81,22 @@ def test_frequencies_of_any_size():
     assert np.isfinite(got.cpu().numpy()).all()
 
 
+def test_large_frequencies_at_near_positions():
+    """Thousands of turns and more a position: a frequency is held within 2^-61 of itself."""
+    f = np.array([2.0 ** 20 + 0.3, 2.0 ** 30 + 0.25, 2.0 ** 40 + 0.5, 2.0 ** 52 + 1.0])
+    p = [0, 1, -1, 2, 17, -1000]
+    x = np.random.default_rng(1).standard_normal((6, 2, 8)).astype(np.float32)
+    got, _ = sc.rope(torch.from_numpy(x).cuda(), None, torch.from_numpy(f).cuda(), positions=i32(p))
+    ref = cache8.turned(x.astype(np.float64), p, f, "half")
+    err = np.abs(got.double().cpu().numpy() - ref)
+    lim = bound(x.astype(np.float64), f, "half", 1.0, ref, torch.float32)
+    for i in range(4):
+        angle = np.abs(p) * f[i] * 2.0 ** -61 + 2 * np.pi * np.abs(p) * 2.0 ** -64
+        extra = angle[:, None] * (np.abs(x[..., i]) + np.abs(x[..., i + 4]))
+        for j in (i, i + 4):
+            assert (err[..., j] <= lim[..., j] + extra).all(), (i, err[..., j], extra)
+
+
 def test_positions_of_cache_slots():
     D, lens, slots = 3, np.array([5, 3, 900, 70000]), [3, 0, 2]
     q = torch.randn((9, 4, 64)).cuda()
