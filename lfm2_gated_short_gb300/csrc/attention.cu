@@ -1275,10 +1275,10 @@ static size_t workspace_bytes(const AttnShape &s, bool q8) {
 }
 // Over an 8-bit cache a shared prefix is unpacked and has a kernel of its own, two launches more.
 // Where its codes, read again for every row tile of every sequence (from L2), are few, k_own takes
-// them with the rest. Us unpacked and with the rest, of 9 to 140 sequences, 0.5 MB in all: 13 to 23 and
-// 8 to 13; 8 MB: up to 8 rows 15 to 20 and 10 to 16, more rows 19 to 24 and 14 to 21; 33 MB: 17 to 24 and
-// 14 to 21, 22 to 47 and 18 to 39 (one in five up to 8 % slower); 50 MB: 18 to 30 and 16 to 26 (one in
-// four up to 6 % slower), 24 to 43 and 21 to 45; 67 MB: 18 to 32 and 18 to 28, 29 to 48 and 23 to 50.
+// them with the rest. Us unpacked and with the rest, of 9 to 140 sequences, 0.5 MB in all: 14 to 22 and
+// 8 to 14; 8 MB: up to 8 rows 15 to 24 and 10 to 21, more rows 18 to 78 and 14 to 56; 33 MB: 17 to 24 and
+// 14 to 23, 21 to 78 and 18 to 57 (one in seven up to 6 % slower); 50 MB: 18 to 30 and 16 to 26 (one in
+// four up to 10 % slower), 24 to 79 and 21 to 63 (one in three, 14 %); 67 MB: half of them up to 24 %.
 static AttnShape planned8(AttnShape s, int page_size) {
     const int64_t row_tiles = ((int64_t)s.D * (s.Hq / s.Hkv) + 31) / 32;
     const double again = (double)s.N * (double)row_tiles * s.shared_pages * page_size * s.Hkv * s.Dh * 2;
