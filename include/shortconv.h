@@ -581,8 +581,8 @@ sc_status shortconv_prefix_attention(sc_dtype dtype, int Hq, int Hkv, int Dh, co
  * shortconv_prefix_attention_8bit: shortconv_prefix_attention over such a pool: q and out
  * bf16, keys and values code times scale. A call with many shared pages unpacks them once, to
  * bf16 in the workspace; one with few reads them with each sequence's own. A weight times its
- * block's V scale counts down to 2^-124 of its row's largest, in the sum whatever it is. A tile
- * whose waits ran out (SC_DEV_TIMEOUT) leaves its rows unwritten.
+ * block's V scale counts down to 2^-124 of its row's largest, in the sum whatever it is. After a
+ * wait that ran out (SC_DEV_TIMEOUT) no more tiles are read, and rows are missing from out.
  */
 sc_status shortconv_pages_append_8bit(sc_dtype dtype, int Hkv, int Dh, int block, const void *k,
                                       int64_t k_stride, const void *v, int64_t v_stride, int N,

@@ -60,7 +60,8 @@ def peaked(lens, gap, up, alike, D=1, **kw):
     c["k"][..., 0] = 0
     c["k"][:, first::16, :, 0] = code(gap)
     c["ks"][:] = 1.0
-    c["k"][..., 1:] = np.where(live_k[..., 1:], code(np.clip(r.standard_normal(c["k"][..., 1:].shape), -4, 4)), 0)
+    rest = np.clip(r.standard_normal(c["k"][..., 1:].shape), -4, 4)
+    c["k"][..., 1:] = np.where(live_k[..., 1:], code(rest), 0)
     v = c["v"]
     v[:, big] = np.where(np.arange(Dh) == 5, code(448.0), 0)
     v[:, ~big, :, 5] = 0
